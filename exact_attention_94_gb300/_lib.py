@@ -19,6 +19,14 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _S = ctypes.c_size_t
+_L = ctypes.c_longlong
+
+
+class RopePlanStruct(ctypes.Structure):
+    """fa_rope_plan of fa.h."""
+    _fields_ = [("n_axes", _I), ("neighbours", _I), ("axis", ctypes.c_byte * 64), ("inv_freq", ctypes.c_double * 64)]
+
+
 SIGNATURES = {
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
@@ -53,6 +61,12 @@ SIGNATURES = {
     "fa_decode_num_splits": (_I, [_I, _I, _I, _I]),
     "fa_decode_splitkv": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _F, _P]),
     "fa_decode_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _F, _P]),
+    "fa_page_plan": (_I, [_P] * 11 + [_I] * 5 + [_P]),
+    "fa_rope_axes": (_I, [_P] * 5 + [ctypes.POINTER(RopePlanStruct)] + [_I] * 4 + [_L] * 4 + [_I, _P]),
+    "fa_kv8_append": (_I, [_P] * 9 + [_I] * 5 + [_L] * 2 + [_P]),
+    "fa_decode_kv8": (_I, [_P] * 9 + [_I] * 11 + [_P, _F, _P]),
+    "fa_decode_kv8_num_splits": (_I, [_I] * 7),
+    "fa_decode_kv8_workspace_bytes": (_S, [_I] * 5),
     "fa_device_error": (_I, [ctypes.POINTER(ctypes.c_uint)]),
     "fa_selftest_wait_timeout": (_I, [ctypes.c_double, _P]),
     "fa_selftest_exp2": (_I, [_P, _P, _I, _I, _P]),

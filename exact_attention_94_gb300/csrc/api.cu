@@ -195,6 +195,7 @@ fa_status fa_device_error(unsigned int* code) {
   if (v != 0) {
     const unsigned zero = 0;
     cudaMemcpyToSymbol(g_fa_error, &zero, sizeof(zero));
+    if (v == FA_DEVERR_OUT_OF_PAGES) return FA_ERR_OUT_OF_PAGES;
     return v >= FA_DEVERR_BAD_PAGE ? FA_ERR_INVALID_ARG : FA_ERR_TIMEOUT;
   }
   return FA_OK;
@@ -726,6 +727,206 @@ fa_status fa_decode_gqa(const void* q, const void* k_cache, const void* v_cache,
                         int Hkv, int L, int d, int num_splits, void* workspace, float scale, fa_stream_t stream) {
   return decode_common(q, k_cache, v_cache, nullptr, nullptr, 0, 0, 0, o, lse, B, Hq, Hkv, L, d, num_splits,
                        workspace, scale, stream);
+}
+
+// ---------------------------------------------------------------- serving steps
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+fa_status fa_page_plan(const int* ctx_lens, const int* new_lens, const int* free_pages, const int* free_count,
+                       int* block_table, int* seq_lens, int* cu_new, int* page, int* slot, int* position,
+                       int* free_count_out, int B, int max_tokens, int page_size, int num_pages, int max_blocks,
+                       fa_stream_t stream) {
+  if (B < 1 || B > 16384 || max_tokens < 0 || page_size < 1 || num_pages < 1 || max_blocks < 1)
+    return FA_ERR_INVALID_ARG;
+  if (!ctx_lens || !new_lens || !free_pages || !free_count || !block_table || !seq_lens || !cu_new || !free_count_out)
+    return FA_ERR_INVALID_ARG;
+  if (max_tokens > 0 && (!page || !slot || !position)) return FA_ERR_INVALID_ARG;
+  const void* ptrs[] = {ctx_lens, new_lens, free_pages, free_count, block_table, seq_lens,
+                        cu_new,   page,     slot,       position,   free_count_out};
+  for (const void* ptr : ptrs)
+    if (!aligned4(ptr)) return FA_ERR_MISALIGNED;
+  if (!ensure_init()) return FA_ERR_LAUNCH;
+  PlanParams p{};
+  p.ctx_lens = ctx_lens;
+  p.new_lens = new_lens;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu_new = cu_new;
+  p.page = page;
+  p.slot = slot;
+  p.position = position;
+  p.free_count_out = free_count_out;
+  p.B = B;
+  p.max_tokens = max_tokens;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.max_blocks = max_blocks;
+  p.err = g_err_ptr;
+  return launch_page_plan(p, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+fa_status fa_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                       const fa_rope_plan* plan, int T, int Hq, int Hkv, int d, long long q_stride,
+                       long long k_stride, long long q_out_stride, long long k_out_stride, int inverse,
+                       fa_stream_t stream) {
+  if (T < 0 || Hq < 0 || Hkv < 0 || Hq + (long long)Hkv < 1 || Hq + (long long)Hkv > 65535 || !plan)
+    return FA_ERR_INVALID_ARG;
+  if (inverse != 0 && inverse != 1) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (plan->n_axes < 1 || plan->n_axes > 4 || (plan->neighbours != 0 && plan->neighbours != 1))
+    return FA_ERR_INVALID_ARG;
+  RopeParams p{};
+  for (int i = 0; i < d / 2; ++i) {
+    const int a = plan->axis[i];
+    const double f = plan->inv_freq[i];
+    if (a < -1 || a >= plan->n_axes || !std::isfinite(f)) return FA_ERR_INVALID_ARG;
+    p.axis[i] = (signed char)a;
+    // the fraction of a turn in 2^-64, rounded; a negative frequency's wraps like the product with it
+    const double turns = f / 6.283185307179586477;
+    const double scaled = std::nearbyint(std::ldexp(turns - std::floor(turns), 64));
+    p.turn[i] = scaled >= 18446744073709551616.0 ? 0 : (uint64_t)scaled;
+  }
+  if (T == 0) return FA_OK;
+  if (!positions || (Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out))) return FA_ERR_INVALID_ARG;
+  if (!aligned4(positions)) return FA_ERR_MISALIGNED;
+  if (Hq > 0) {
+    if (q_stride < (long long)Hq * d || q_out_stride < (long long)Hq * d) return FA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(q_out) || q_stride % 8 != 0 || q_out_stride % 8 != 0) return FA_ERR_MISALIGNED;
+    if (q == q_out && q_stride != q_out_stride) return FA_ERR_INVALID_ARG;
+  }
+  if (Hkv > 0) {
+    if (k_stride < (long long)Hkv * d || k_out_stride < (long long)Hkv * d) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(k_out) || k_stride % 8 != 0 || k_out_stride % 8 != 0) return FA_ERR_MISALIGNED;
+    if (k == k_out && k_stride != k_out_stride) return FA_ERR_INVALID_ARG;
+  }
+  p.q = q;
+  p.k = k;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.positions = positions;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.inverse = inverse;
+  return launch_rope(p, d, plan->neighbours != 0, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, void* v_codes, float* k_scale,
+                        float* v_scale, const int* page, const int* slot, const int* copy_src, int n, int Hkv, int d,
+                        int page_size, int num_pages, long long k_stride, long long v_stride, fa_stream_t stream) {
+  if (n < 0 || Hkv < 1 || Hkv > 65535 || num_pages < 1 || page_size < 16 || page_size % 16 != 0)
+    return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (n == 0) return FA_OK;
+  if (!k_new || !v_new || !k_codes || !v_codes || !k_scale || !v_scale || !page || !slot) return FA_ERR_INVALID_ARG;
+  if (k_stride < (long long)Hkv * d || v_stride < (long long)Hkv * d) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_codes) || !aligned16(v_codes) || k_stride % 8 != 0 ||
+      v_stride % 8 != 0)
+    return FA_ERR_MISALIGNED;
+  if (!aligned4(k_scale) || !aligned4(v_scale) || !aligned4(page) || !aligned4(slot) || !aligned4(copy_src))
+    return FA_ERR_MISALIGNED;
+  if (!ensure_init()) return FA_ERR_LAUNCH;
+  Kv8AppendParams p{};
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.k_codes = k_codes;
+  p.v_codes = v_codes;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.page = page;
+  p.slot = slot;
+  p.copy_src = copy_src;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.n = n;
+  p.Hkv = Hkv;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.err = g_err_ptr;
+  return launch_kv8_append(p, d, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+// Keys that the queries of a request see at most.
+static int kv8_span(int Nq, int max_seq_len, int window_left) {
+  if (window_left < 0 || (long long)window_left + Nq >= max_seq_len) return max_seq_len;
+  return window_left + Nq;
+}
+
+size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int d, int num_splits) {
+  if (B < 1 || Nq < 1 || Hq < 1 || d < 1 || num_splits < 1) return 0;
+  const size_t rows = (size_t)B * Nq * Hq * num_splits;
+  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float));
+}
+
+int fa_decode_kv8_num_splits(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left, int d) {
+  (void)d;
+  if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || max_seq_len < 1) return 1;
+  return kv8_auto_splits(B, Nq, Hkv, Hq / Hkv, kv8_span(Nq, max_seq_len, window_left));
+}
+
+fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                        const float* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse, int B,
+                        int Nq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_blocks, int max_seq_len,
+                        int window_left, int num_splits, void* workspace, float scale, fa_stream_t stream) {
+  if (B < 1 || B > 65535 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (long long)Nq * Hq > 65535)
+    return FA_ERR_INVALID_ARG;
+  if (num_pages < 1 || max_blocks < 1 || max_seq_len < 0 || num_splits < 0 || num_splits > 65535 || window_left < -1)
+    return FA_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size % 16 != 0 || (long long)max_blocks * page_size < max_seq_len)
+    return FA_ERR_INVALID_ARG;
+  if ((long long)num_pages * Hkv > 0x7fffffffll || max_seq_len > (1 << 30)) return FA_ERR_INVALID_ARG;
+  if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !block_table || !seq_lens || !o || !lse || !workspace)
+    return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (!scale_ok(scale)) return FA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k_codes, v_codes, o, workspace};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return FA_ERR_MISALIGNED;
+  if (!aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse))
+    return FA_ERR_MISALIGNED;
+  if (!ensure_init()) return FA_ERR_LAUNCH;
+  Kv8DecodeParams p{};
+  if (window_left >= max_seq_len) window_left = -1;  // a window past every key is no window
+  const int span = kv8_span(Nq, max_seq_len, window_left);
+  p.splits = num_splits > 0 ? num_splits : fa_decode_kv8_num_splits(B, Nq, Hq, Hkv, max_seq_len, window_left, d);
+  // whole tiles; a window's first tile may begin up to a tile before its first key
+  const long long tiles = ((long long)span + kKv8Tile - 1) / kKv8Tile + (window_left >= 0 ? 1 : 0);
+  p.chunk = (int)((tiles + p.splits - 1) / p.splits) * kKv8Tile;
+  if (p.chunk < kKv8Tile) p.chunk = kKv8Tile;
+  const size_t rows = (size_t)B * Nq * Hq * p.splits;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.q = q;
+  p.k_codes = static_cast<const uint8_t*>(k_codes);
+  p.v_codes = static_cast<const uint8_t*>(v_codes);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.o = o;
+  p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_lse = reinterpret_cast<float*>(ws + align256(rows * d * sizeof(float)));
+  p.B = B;
+  p.Nq = Nq;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.group = Hq / Hkv;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.max_blocks = max_blocks;
+  p.max_len = max_seq_len;
+  p.win_left = window_left;
+  p.scale_log2 = scale * kLog2e;
+  p.err = g_err_ptr;
+  p.timeout_ns = g_opt.timeout_ns;
+  return launch_decode_kv8(p, d, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -157,6 +157,88 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, void* k_pa
                                 const int* slot, const int* copy_src, int n, int Hkv, int d, int page_size,
                                 int num_pages, unsigned* err, cudaStream_t stream);
 
+// Planning a step (see fa_page_plan in fa.h).
+struct PlanParams {
+  const int* ctx_lens;       // [B]
+  const int* new_lens;       // [B]
+  const int* free_pages;     // [num_pages]
+  const int* free_count;     // [1]
+  int* block_table;          // [B, max_blocks]
+  int* seq_lens;             // [B], may be ctx_lens
+  int* cu_new;               // [B + 1]
+  int* page;                 // [max_tokens] x 3
+  int* slot;
+  int* position;
+  int* free_count_out;       // [1], may be free_count
+  int B;
+  int max_tokens;
+  int page_size;
+  int num_pages;
+  int max_blocks;
+  unsigned* err;
+};
+cudaError_t launch_page_plan(const PlanParams& p, cudaStream_t stream);
+
+// Rotary positions (see fa_rope_axes in fa.h).
+struct RopeParams {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const int* positions;      // [n_axes, T]
+  long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements between rows
+  int T, Hq, Hkv;
+  int inverse;
+  int heads_per_thread;      // set by the launch
+  int chunks;                //   thread chunks of a token's Hq + Hkv heads
+  signed char axis[64];      // axis of pair p, -1: not rotated
+  uint64_t turn[64];         // its frequency: fraction of a turn per position, in 2^-64
+};
+cudaError_t launch_rope(RopeParams& p, int D, bool neighbours, cudaStream_t stream);
+
+// 8-bit paged cache, write side (see fa_kv8_append in fa.h).
+struct Kv8AppendParams {
+  const void* k_new;
+  const void* v_new;
+  void* k_codes;
+  void* v_codes;
+  float* k_scale;
+  float* v_scale;
+  const int* page;           // [n]
+  const int* slot;           // [n]
+  const int* copy_src;       // [n] or nullptr
+  long long k_stride, v_stride;
+  int n, Hkv, page_size, num_pages;
+  int rows_per_warp;         // set by the launch
+  unsigned* err;
+};
+cudaError_t launch_kv8_append(Kv8AppendParams& p, int D, cudaStream_t stream);
+
+// Attention over the 8-bit paged cache (see fa_decode_kv8 in fa.h).
+constexpr int kKv8Tile = 128;  // keys per tile; chunks are multiples of it
+struct Kv8DecodeParams {
+  const void* q;             // [B, Nq, Hq, d] bf16
+  const uint8_t* k_codes;    // [num_pages, Hkv, page_size, d]
+  const uint8_t* v_codes;
+  const float* k_scale;      // [num_pages, Hkv]
+  const float* v_scale;
+  const int* block_table;    // [B, max_blocks]
+  const int* seq_lens;       // [B]
+  void* o;
+  float* lse;
+  float* part_o;             // [B, Nq, Hq, splits, d] fp32, each normalised
+  float* part_lse;           // [B, Nq, Hq, splits] log2 of each chunk's softmax mass
+  int B, Nq, Hq, Hkv, group;
+  int page_size, num_pages, max_blocks, max_len;
+  int win_left;              // -1: no window
+  int splits, chunk;         // keys per split
+  float scale_log2;
+  unsigned* err;
+  unsigned long long timeout_ns;
+};
+int kv8_auto_splits(int B, int Nq, int Hkv, int group, int span);
+cudaError_t launch_decode_kv8(const Kv8DecodeParams& p, int D, cudaStream_t stream);
+
 int decode_stages(int G, int D);
 size_t decode_smem_bytes(int G, int D);
 cudaError_t launch_decode(const DecodeParams& p, int D, void* o, float* lse, cudaStream_t stream);

@@ -15,6 +15,7 @@ enum : unsigned {
   FA_DEVERR_TIMEOUT_BASE = 0x1000u,  // + site id
   FA_DEVERR_BAD_PAGE = 0x2000u,      // a block-table entry outside the page pool
   FA_DEVERR_BAD_SEQLEN = 0x2001u,    // a sequence length outside [0, max_seq_len]
+  FA_DEVERR_OUT_OF_PAGES = 0x2002u,  // a plan needs more pages than the free stack has
   FA_DEVERR_BOUNDS_BASE = 0x3000u,   // + site id: an index outside its buffer (bounds-checked builds only)
 };
 

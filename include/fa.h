@@ -428,11 +428,158 @@ fa_status fa_decode_paged_window(const void* q, const void* k_pages, const void*
                                  int num_splits, void* workspace, float scale, fa_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------- serving steps
+ * One step of a server that keeps its keys and values in pages of 8-bit codes:
+ * fa_page_plan says where the step's tokens go, fa_rope_axes rotates their
+ * queries and keys, fa_kv8_append writes their keys and values, and
+ * fa_decode_kv8 attends.  ("efficient-attention/flash-2-3", sections "Paged KV
+ * caches, a preview of serving" and "FP8, and the outlier problem".)
+ */
+
+/*
+ * Plans a step on the GPU: what fa_pool_reserve_append does on the host for
+ * one token a sequence, for any number of tokens a request and without the
+ * host knowing the lengths.  Request b has ctx_lens[b] tokens in the pages of
+ * its block-table row and gets new_lens[b] more (0 allowed).  It needs
+ *     ceil((ctx + new) / page_size) - ceil(ctx / page_size)
+ * new pages; they come off the top of the free stack, for request 0 first and
+ * in block order within a request: the j-th page taken by the step is
+ * free_pages[free_count - 1 - j].
+ *   ctx_lens, new_lens : int32 [B], device
+ *   free_pages  : int32 [num_pages], device; entries 0 .. *free_count - 1 are
+ *                 free pages (the stack is only read: popping is free_count_out)
+ *   free_count  : int32 [1], device
+ *   block_table : int32 [B, max_blocks], device; the new pages' entries are
+ *                 written, all others left as they are
+ *   seq_lens    : int32 [B], written: ctx + new.  May be ctx_lens itself
+ *   cu_new      : int32 [B + 1], written: exclusive sums of new_lens (the packed
+ *                 batch's offsets)
+ *   page, slot, position : int32 [max_tokens], written: row cu_new[b] + i is
+ *                 token ctx_lens[b] + i of request b, which goes to slot[row] of
+ *                 page[row] and stands at position[row].  Rows past the last
+ *                 token get page = slot = -1 and position = 0 (fa_kv8_append
+ *                 skips them)
+ *   free_count_out : int32 [1], written: pages left.  May be free_count itself
+ * Other arguments do not overlap.  All or nothing: a negative length, a request
+ * past max_blocks pages, more tokens than max_tokens or a free count outside
+ * [0, num_pages] (code 0x2001, FA_ERR_INVALID_ARG), or more pages needed than
+ * are free (code 0x2002, FA_ERR_OUT_OF_PAGES), is reported by fa_device_error;
+ * then cu_new is 0, every row is padding, seq_lens = ctx_lens, the free count
+ * stays and the table is untouched.  A page number outside [0, num_pages), on
+ * the stack or in the table, is reported (code 0x2000); the rows that it would
+ * serve get page = slot = -1 and no table entry is written from it.
+ * 1 <= B <= 16384, max_tokens >= 0; int32 arrays 4-byte aligned.
+ */
+fa_status fa_page_plan(const int* ctx_lens, const int* new_lens, const int* free_pages, const int* free_count,
+                       int* block_table, int* seq_lens, int* cu_new, int* page, int* slot, int* position,
+                       int* free_count_out, int B, int max_tokens, int page_size, int num_pages, int max_blocks,
+                       fa_stream_t stream);
+
+/*
+ * Rotary positions with several axes (time, height and width of image and
+ * video patches; one axis is the usual rotary).  Pair p of a head, 0 <= p <
+ * d / 2, belongs to axis axis[p] and turns by the angle
+ *     a = positions[axis[p]][t] * inv_freq[p]:
+ *     (x1, x2) -> (x1 cos a - x2 sin a, x1 sin a + x2 cos a),
+ * where pair p is elements (p, p + d / 2) of the head, or (2p, 2p + 1) with
+ * neighbours = 1.  A pair of axis -1 is copied (partial rotary).  The plan is
+ * HOST memory, read during the call.
+ */
+typedef struct {
+  int n_axes;            /* 1 .. 4 */
+  int neighbours;        /* 0: pairs (p, p + d/2); 1: pairs (2p, 2p + 1) */
+  signed char axis[64];  /* axis of pair p, -1 .. n_axes - 1; the first d/2 count */
+  double inv_freq[64];   /* radians per position of pair p, finite */
+} fa_rope_plan;
+
+/*
+ * Rotates q and k (or either alone: the other NULL, with 0 heads).
+ *   q, q_out : T rows of Hq heads of d bf16, rows q_stride, q_out_stride
+ *              elements apart (multiples of 8, at least Hq * d; slices of a
+ *              fused projection need no copy).  q_out may be q with the same
+ *              stride; otherwise outputs overlap no input
+ *   k, k_out : the same with Hkv heads
+ *   positions: int32 [n_axes, T], device, any sign
+ *   inverse  : 0 or 1 = rotate by -a: the gradient of the call with 0 (dq, dk
+ *              from the gradients of q_out, k_out)
+ * The angle is reduced to one turn in 64-bit fixed point before its sine and
+ * cosine are taken in fp32, so far positions lose nothing; the result is
+ * rounded once, to bf16.  T >= 0.
+ */
+fa_status fa_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                       const fa_rope_plan* plan, int T, int Hq, int Hkv, int d, long long q_stride,
+                       long long k_stride, long long q_out_stride, long long k_out_stride, int inverse,
+                       fa_stream_t stream);
+
+/*
+ * 8-bit paged cache.  Codes are e4m3, one scale per page and K/V head:
+ *   k_codes, v_codes : uint8 [num_pages, Hkv, page_size, d], device
+ *   k_scale, v_scale : fp32 [num_pages, Hkv], device; a value is code * scale
+ * A scale is a power of two, the smallest with |x| <= 448 scale for every
+ * (finite) x the page has held since its slot 0 was written, 0 if all were 0.
+ * e4m3 is a floating format, so a power of two costs its values no precision
+ * and a growing scale moves older codes almost always exactly.
+ *
+ * Appends n tokens.  Rows of one page are consecutive, with consecutive slots
+ * (fa_page_plan and fa_pool_reserve_append give them so): a run.  A run that
+ * starts at slot 0 starts its page anew; any other run finds slots 0 .. first -
+ * 1 filled, takes the larger of the page's scale and its own, and re-encodes
+ * the older codes, code * old / new rounded to e4m3, if the scale grows.
+ * Codes are rounded to nearest even; a NaN or an infinity is stored as NaN and
+ * counts in no scale.  Slots behind the run are left as they are.
+ *   k_new, v_new : n rows of Hkv heads of d bf16, rows k_stride, v_stride
+ *                  elements apart (multiples of 8, at least Hkv * d)
+ *   page, slot   : int32 [n], device.  page = -1: padding, the row is skipped
+ *   copy_src     : int32 [n], device, or NULL: for a run's first row, the page
+ *                  whose slots 0 .. first - 1 (and scale) are copied in place of
+ *                  the page's own, -1 for none
+ * A page has at most one run a call.  A copy_src may be a page that another
+ * run of the call writes in place (the copy-on-write of fa_pool_*): it is read
+ * first; but not one that another run copies into.  A page, slot or copy_src
+ * outside the cache is skipped and reported by fa_device_error (code 0x2000).
+ * page_size a multiple of 16, d = 64 or 128.
+ */
+fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, void* v_codes, float* k_scale,
+                        float* v_scale, const int* page, const int* slot, const int* copy_src, int n, int Hkv, int d,
+                        int page_size, int num_pages, long long k_stride, long long v_stride, fa_stream_t stream);
+
+/*
+ * Attention of a few query tokens per request over the 8-bit paged cache
+ * (split-KV, as fa_decode_paged_window).  Query i of the Nq of request b sits
+ * at key position seq_lens[b] - Nq + i and sees the keys up to its own
+ * position, from position - window_left on (window_left = -1: from 0).  One
+ * token is plain decoding; more are drafts to verify, whose keys the cache
+ * holds already.  A query that sees no key gets O = 0 and lse = -inf.
+ *   q            : [B, Nq, Hq, d] bf16;   o the same, written
+ *   lse          : [B, Hq, Nq] fp32, written
+ *   codes, scales: as above; Hkv divides Hq
+ *   block_table  : int32 [B, max_blocks], seq_lens : int32 [B], device
+ *   max_seq_len  : <= max_blocks * page_size and <= 2^30; sizes the splits
+ *   num_splits   : 0 = choose (fa_decode_kv8_num_splits); else 1 .. 65535
+ *   workspace    : fa_decode_kv8_workspace_bytes(B, Nq, Hq, d, splits) bytes, 16-byte
+ *                  aligned, contents on entry do not matter; calls whose work
+ *                  overlaps on the GPU need one each
+ * What a page holds behind a request's last key is never used, whatever it
+ * is.  Table entries outside the pool and lengths outside [0, max_seq_len] are
+ * handled and reported as in fa_decode_paged.  page_size a multiple of 16, d = 64
+ * or 128, Nq >= 1.
+ */
+fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                        const float* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse, int B,
+                        int Nq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_blocks, int max_seq_len,
+                        int window_left, int num_splits, void* workspace, float scale, fa_stream_t stream);
+
+/* Splits fa_decode_kv8 uses when it is given num_splits = 0 (window_left as there). */
+int fa_decode_kv8_num_splits(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left, int d);
+size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int d, int num_splits);
+
+/*
  * Synchronises the device, then returns FA_OK if no kernel of this library
  * recorded an error since the last call, FA_ERR_TIMEOUT if a bounded wait ran
  * out (code 0x1000 + wait site), FA_ERR_INVALID_ARG if a kernel met a bad
  * device-side argument (0x2000: block-table entry outside the page pool,
- * 0x2001: sequence length out of range).  The recorded code goes to *code
+ * 0x2001: sequence length out of range), FA_ERR_OUT_OF_PAGES if a plan found too
+ * few free pages (0x2002).  The recorded code goes to *code
  * when code is not NULL.  Clears the recorded code.
  */
 fa_status fa_device_error(unsigned int* code);
