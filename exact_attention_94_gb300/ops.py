@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -605,3 +605,280 @@ def decode_paged_window(q, k_pages, v_pages, block_table, seq_lens, max_seq_len:
                                       int(max_seq_len), int(window_left), splits, _ptr(ws), scale, _stream(stream))
     _lib.check(st, "fa_decode_paged_window")
     return o, l
+
+
+# ---------------------------------------------------------------- serving steps: planning, rotary, 8-bit cache
+#
+# A decode step launches a few kernels of some microseconds each, so these
+# wrappers spend as little host time as their checks allow: addresses go to
+# ctypes as plain integers, and the current stream comes as its raw handle.
+
+def _on_call_stream(fn):
+    """Runs a wrapper with the device of its tensors and the call's stream
+    current: outputs and workspaces then come from that stream's own memory,
+    so one call's cannot be handed to a call on another stream while it runs.
+    ``stream`` reaches the wrapper as the raw handle."""
+    @functools.wraps(fn)
+    def wrapper(*args, stream=None, **kwargs):
+        dev = None
+        for a in (*args, *kwargs.values()) if kwargs else args:
+            if isinstance(a, torch.Tensor) and a.is_cuda:
+                i = a.get_device()
+                if dev is None:
+                    dev = i
+                elif i != dev:
+                    raise ValueError("all CUDA tensors of a call must be on one device")
+        if stream is not None:
+            if dev is not None and stream.device.index != dev:
+                raise ValueError("stream must be on the device of the tensors")
+            with torch.cuda.stream(stream):
+                return fn(*args, stream=stream.cuda_stream, **kwargs)
+        if dev is None:
+            return fn(*args, stream=0, **kwargs)  # refused below: nothing is on a GPU
+        if dev == torch.cuda.current_device():
+            return fn(*args, stream=torch.cuda.current_stream(dev).cuda_stream, **kwargs)
+        with torch.cuda.device(dev):
+            return fn(*args, stream=torch.cuda.current_stream(dev).cuda_stream, **kwargs)
+    return wrapper
+
+
+def _check_i32(name, t, shape):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _check_rows(name, t, shape=None):
+    """A bf16 [..., H, d] tensor whose heads lie side by side and whose rows lie
+    one stride apart (a slice of a fused projection, say).  Returns that stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dim() < 3:
+        raise ValueError(f"{name} must be [..., H, d]")
+    size = t.shape
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
+    H, d = size[-2], size[-1]
+    if t.is_contiguous():
+        return H * d
+    step = t.stride()
+    rows = [(n, s) for n, s in zip(size[:-2], step[:-2]) if n != 1]
+    ok = (d <= 1 or step[-1] == 1) and (H <= 1 or step[-2] == d)
+    ok = ok and all(rows[i][1] == rows[i + 1][0] * rows[i + 1][1] for i in range(len(rows) - 1))
+    ok = ok and (not rows or rows[-1][1] >= H * d)
+    if not ok:
+        raise ValueError(f"{name} must have contiguous heads and evenly spaced rows")
+    return rows[-1][1] if rows else H * d
+
+
+class PagePlan(NamedTuple):
+    """What page_plan returns; int32 device tensors."""
+    seq_lens: torch.Tensor    # [B] tokens of each request after the step
+    cu_new: torch.Tensor      # [B + 1] packed offsets of the step's tokens
+    page: torch.Tensor        # [max_tokens] where each row's token goes; -1 past the last
+    slot: torch.Tensor        # [max_tokens]
+    position: torch.Tensor    # [max_tokens] its position in its request; 0 past the last
+    free_count: torch.Tensor  # [1] pages left
+
+
+@_on_call_stream
+def page_plan(ctx_lens, new_lens, free_pages, free_count, block_table, page_size: int, max_tokens: int, out=None, *,
+              stream=None) -> PagePlan:
+    """Plans a step on the GPU.  ctx_lens, new_lens int32 [B]: tokens each
+    request holds and gets; free_pages int32 [num_pages] and free_count int32
+    [1]: the stack of free pages; block_table int32 [B, max_blocks], whose new
+    entries are written.  max_tokens: rows of the outputs, at least the step's
+    tokens.  ``out``: a PagePlan to write into; its seq_lens may be ctx_lens and
+    its free_count the given one, which advances them in place."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    B, max_blocks = block_table.shape
+    n = int(max_tokens)
+    if n < 0:
+        raise ValueError("max_tokens must not be negative")
+    _check_i32("ctx_lens", ctx_lens, (B,))
+    _check_i32("new_lens", new_lens, (B,))
+    num_pages = free_pages.numel()
+    _check_i32("free_pages", free_pages, (num_pages,))
+    _check_i32("free_count", free_count, (1,))
+    _check_i32("block_table", block_table, (B, max_blocks))
+    sizes = (B, B + 1, n, n, n, 1)
+    if out is None:  # one buffer, cut up; the rows' three arrays first
+        buf = torch.empty(3 * n + 2 * B + 2, dtype=torch.int32, device=block_table.device)
+        page, slot, position, seq, cu, left = buf.split((n, n, n, B, B + 1, 1))
+        out = PagePlan(seq, cu, page, slot, position, left)
+    else:
+        for name, t, s in zip(PagePlan._fields, out, sizes):
+            _check_i32(f"out.{name}", t, (s,))
+            if t.device != block_table.device:
+                raise ValueError("all CUDA tensors of a call must be on one device")
+    st = lib().fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+                            block_table.data_ptr(), *[t.data_ptr() for t in out], B, n, int(page_size), num_pages,
+                            max_blocks, stream)
+    _lib.check(st, "fa_page_plan")
+    return out
+
+
+class RopePlan:
+    """Which axis each pair of a head turns with, and how fast; kept by the
+    caller.  ``axis``: d / 2 integers, -1 for a pair that is copied; ``inv_freq``:
+    d / 2 numbers, radians per position; ``neighbours``: pairs (2p, 2p + 1)
+    instead of (p, p + d / 2)."""
+
+    def __init__(self, d: int, axis, inv_freq, neighbours: bool = False):
+        axis, inv_freq = [int(a) for a in axis], [float(f) for f in inv_freq]
+        if d not in (64, 128):
+            raise _lib.FaError(_lib.FA_ERR_UNSUPPORTED, "RopePlan")
+        if len(axis) != d // 2 or len(inv_freq) != d // 2:
+            raise ValueError(f"axis and inv_freq must have {d // 2} entries")
+        if any(not -1 <= a < 4 for a in axis) or not all(math.isfinite(f) for f in inv_freq):
+            raise ValueError("axis entries must be -1 .. 3 and inv_freq finite")
+        self.d, self.n_axes = d, max(1, max(axis) + 1)
+        self.struct = _lib.RopePlanStruct(self.n_axes, int(bool(neighbours)))
+        self.struct.axis[:d // 2] = axis
+        self.struct.inv_freq[:d // 2] = inv_freq
+        self._ref = ctypes.byref(self.struct)
+
+
+def rope_plan(d: int, sections, theta: float = 10000.0, per_axis: bool = False, neighbours: bool = False) -> RopePlan:
+    """The usual plans.  ``sections``: pairs of each axis, in order; what they
+    leave of the d / 2 pairs is copied.  Frequencies are theta^(-p / (d / 2)) of
+    pair p (one ladder over the head, shared by the axes), or, per_axis, a
+    ladder for each axis: theta^(-j / n) of pair j of its n."""
+    sections = [int(n) for n in sections]
+    if not sections or len(sections) > 4 or min(sections) < 0 or sum(sections) > d // 2:
+        raise ValueError("sections must be 1 to 4 counts of pairs, d / 2 of them at most")
+    axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    if per_axis:
+        freq = [theta ** (-j / n) for n in sections for j in range(n)]
+    else:
+        freq = [theta ** (-p / (d // 2)) for p in range(len(axis))]
+    rest = d // 2 - len(axis)
+    return RopePlan(d, axis + [-1] * rest, freq + [0.0] * rest, neighbours)
+
+
+def _rope_side(name, t, o, plan):
+    """(rows, heads, address, address, stride, stride, output) of q or k."""
+    stride = _check_rows(name, t)
+    if t.shape[-1] != plan.d:
+        raise ValueError(f"{name} has head dim {t.shape[-1]}, the plan {plan.d}")
+    H = t.shape[-2]
+    if o is None:
+        o, out_stride = torch.empty(t.shape, dtype=t.dtype, device=t.device), H * plan.d
+    else:
+        out_stride = _check_rows(f"out {name}", o, t.shape)
+        if o.device != t.device:
+            raise ValueError("all CUDA tensors of a call must be on one device")
+    return t.numel() // max(1, H * plan.d), H, t.data_ptr(), o.data_ptr(), stride, out_stride, o
+
+
+def _rope(q, k, positions, plan, inverse, out, stream):
+    if not isinstance(plan, RopePlan):
+        raise TypeError("plan must be a RopePlan")
+    if q is None and k is None:
+        raise ValueError("q or k must be given")
+    oq, ok = out if out is not None else (None, None)
+    none = (None, 0, None, None, 0, 0, None)
+    nq, Hq, pq, poq, qs, qos, oq = _rope_side("q", q, oq, plan) if q is not None else none
+    nk, Hkv, pk, pok, ks, kos, ok = _rope_side("k", k, ok, plan) if k is not None else none
+    if nq is not None and nk is not None and nq != nk:
+        raise ValueError("q and k must have the same rows")
+    rows = nq if nq is not None else nk
+    _check_i32("positions", positions, (plan.n_axes, rows))
+    st = lib().fa_rope_axes(pq, pk, poq, pok, positions.data_ptr(), plan._ref, rows, Hq, Hkv, plan.d, qs, ks, qos, kos,
+                            inverse, stream)
+    _lib.check(st, "fa_rope_axes")
+    return oq, ok
+
+
+@_on_call_stream
+def rope_axes(q, k, positions, plan: RopePlan, out=None, *, stream=None):
+    """Rotates q [..., Hq, d] and k [..., Hkv, d] (either may be None) by their
+    rows' positions, int32 [plan.n_axes, rows].  Rows may lie a stride apart.
+    Returns (q, k) rotated, in ``out`` = (q_out, k_out) when given (q_out may be q)."""
+    return _rope(q, k, positions, plan, 0, out, stream)
+
+
+@_on_call_stream
+def rope_axes_bwd(dq, dk, positions, plan: RopePlan, out=None, *, stream=None):
+    """Gradients of rope_axes: (dq, dk) with respect to what it was given, from
+    those with respect to what it returned."""
+    return _rope(dq, dk, positions, plan, 1, out, stream)
+
+
+def _check_kv8(k_codes, v_codes, k_scale, v_scale):
+    for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.dim() != 4:
+            raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_size, d]")
+    size = k_codes.shape
+    if v_codes.shape != size:
+        raise ValueError("k_codes and v_codes must have one shape")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or \
+                t.shape != size[:2]:
+            raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor [num_pages, Hkv]")
+    return size
+
+
+@_on_call_stream
+def kv8_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, page, slot, copy_src=None, *, stream=None) -> None:
+    """Quantises tokens ([n, Hkv, d] bf16, rows may lie a stride apart) into the
+    8-bit cache: codes uint8 [num_pages, Hkv, page_size, d] and scales fp32
+    [num_pages, Hkv], updated.  page, slot (and copy_src) int32 [n] as from
+    page_plan or PagePool.reserve_append; page -1 skips a row."""
+    num_pages, Hkv, P, d = _check_kv8(k_codes, v_codes, k_scale, v_scale)
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
+        raise ValueError("k_new must be [n, Hkv, d]")
+    n = k_new.shape[0]
+    ks, vs = _check_rows("k_new", k_new, (n, Hkv, d)), _check_rows("v_new", v_new, (n, Hkv, d))
+    _check_i32("page", page, (n,))
+    _check_i32("slot", slot, (n,))
+    if copy_src is not None:
+        _check_i32("copy_src", copy_src, (n,))
+    st = lib().fa_kv8_append(k_new.data_ptr(), v_new.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
+                             k_scale.data_ptr(), v_scale.data_ptr(), page.data_ptr(), slot.data_ptr(),
+                             None if copy_src is None else copy_src.data_ptr(), n, Hkv, d, P, num_pages, ks, vs, stream)
+    _lib.check(st, "fa_kv8_append")
+
+
+@_on_call_stream
+def decode_kv8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, max_seq_len: int, window_left: int = -1,
+               num_splits: int = 0, scale: Optional[float] = None, workspace=None, *, stream=None):
+    """Attention of q [B, Nq, Hq, d] over the 8-bit paged cache; query i of a
+    request stands at seq_lens - Nq + i.  block_table int32 [B, max_blocks] and
+    seq_lens int32 [B] on the device.  Returns (o [B, Nq, Hq, d], lse [B, Hq, Nq])."""
+    _check_bf16("q", q)
+    num_pages, Hkv, P, d = _check_kv8(k_codes, v_codes, k_scale, v_scale)
+    if q.dim() != 4 or q.shape[3] != d:
+        raise ValueError(f"q must be [B, Nq, Hq, {d}]")
+    B, Nq, Hq, _ = q.shape
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    max_blocks = block_table.shape[1]
+    _check_i32("block_table", block_table, (B, max_blocks))
+    _check_i32("seq_lens", seq_lens, (B,))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    L, wl, splits, so = int(max_seq_len), int(window_left), int(num_splits), lib()
+    if splits == 0:
+        splits = so.fa_decode_kv8_num_splits(B, Nq, Hq, Hkv, L, wl, d)
+    nbytes = so.fa_decode_kv8_workspace_bytes(B, Nq, Hq, d, max(splits, 1))
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    elif workspace.numel() * workspace.element_size() < nbytes or not workspace.is_contiguous():
+        raise ValueError("workspace too small")
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+    st = so.fa_decode_kv8(q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                          block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d,
+                          P, num_pages, max_blocks, L, wl, splits, workspace.data_ptr(), scale, stream)
+    _lib.check(st, "fa_decode_kv8")
+    return o, lse
