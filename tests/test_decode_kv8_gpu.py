@@ -1,0 +1,212 @@
+"""fa_decode_kv8 against the reference attention over the dequantised cache.
+
+Tolerances, with A = sum_j P_j |v_j| (element by element):
+  O   : half a bf16 step of the result, 2^-8 |O|, plus 2^-11 A for what comes
+        before it.  The products are exact in the tensor cores' inputs but for
+        P, held to 2^-12 of itself or better; scores and sums are fp32: with
+        |s| <= 2^6 a score is off by a few 2^-24 * 2^6 = 2^-18, its exponential
+        by as much of itself.
+  lse : 2^-13 absolute: the score error above, the fp32 logarithm and sum.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from exact_attention_94_gb300 import _lib, ops
+from oracle import serving
+
+pytestmark = pytest.mark.gpu
+
+
+def make(lens, Nq, Hq, Hkv, d, P, seed=0, amp=1.0, garbage=True):
+    """A cache of quantised normal values; slots that no request holds, and whole
+    spare pages, are NaN codes with NaN scales; tables are padded with nonsense."""
+    g = torch.Generator().manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    blocks = [-(-n // P) for n in lens]
+    pages, mb = sum(blocks) + 2, max(1, max(blocks)) + 1
+    order = rng.permutation(pages)
+    table = rng.integers(-10, 10 ** 6, (len(lens), mb))
+    out, at = {}, 0
+    held = np.zeros((pages, P), bool)
+    for b, n in enumerate(lens):
+        table[b, :blocks[b]] = order[at:at + blocks[b]]
+        at += blocks[b]
+        for j in range(n):
+            held[table[b, j // P], j % P] = True
+    for name in ("k", "v"):
+        x = torch.randn((pages, Hkv, P, d), generator=g).numpy() * (amp * 2.0 ** rng.integers(-3, 3, (pages, Hkv, 1, 1)))
+        codes, scales = np.empty(x.shape, np.uint8), np.empty((pages, Hkv), np.float32)
+        for p in range(pages):
+            for h in range(Hkv):
+                scales[p, h] = serving.pow2_scale(np.abs(x[p, h]).max()) if held[p].any() or not garbage else np.nan
+                codes[p, h] = serving._encode(x[p, h] / scales[p, h])
+        if garbage:
+            codes[~np.broadcast_to(held[:, None, :], codes.shape[:3])] = 0x7F
+        out[name] = (codes, scales)
+    q = (torch.randn((len(lens), Nq, Hq, d), generator=g)).to(torch.bfloat16)
+    return q, out["k"], out["v"], table, np.array(lens)
+
+
+def cu(a, dt):
+    return torch.tensor(np.ascontiguousarray(a), dtype=dt).cuda()
+
+
+def dev(case):
+    q, (kc, ks), (vc, vs), table, lens = case
+    return (q.cuda(), cu(kc, torch.uint8), cu(vc, torch.uint8), cu(ks, torch.float32), cu(vs, torch.float32),
+            cu(table, torch.int32), cu(lens, torch.int32))
+
+
+def assert_close(o, lse, ref):
+    o_ref, l_ref, a = ref
+    o, lse = synth.to_f64(o), lse.cpu().numpy()
+    assert np.all(np.isfinite(o))
+    err = np.abs(o - o_ref)
+    tol = 2.0 ** -8 * np.abs(o_ref) + 2.0 ** -11 * a
+    assert np.all(err <= tol), float((err - tol).max())
+    none = np.isneginf(l_ref)
+    assert np.array_equal(none, np.isneginf(lse))
+    assert np.all(np.abs(lse[~none] - l_ref[~none]) <= 2.0 ** -13)
+    assert np.all(o[np.moveaxis(none, 1, 2)] == 0)
+
+
+def check(case, window=-1, splits=0, L=None, scale=None):
+    q, (kc, ks), (vc, vs), table, lens = case
+    sc = 1 / math.sqrt(q.shape[3]) if scale is None else scale
+    L = int(lens.max()) if L is None else L
+    o, lse = ops.decode_kv8(*dev(case), L, window_left=window, num_splits=splits, scale=scale)
+    assert ops.device_error() == 0
+    assert_close(o, lse, serving.decode_kv8(synth.to_f64(q), kc, vc, ks, vs, table, lens, window, sc))
+    return o, lse
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("P", [16, 48, 64, 128, 256])
+def test_lengths_around_every_border(d, P):
+    lens = [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300]
+    check(make(lens, 1, 4, 2, d, P, seed=P + d))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (8, 1), (7, 1), (12, 4), (16, 1), (40, 2), (33, 1), (64, 1)])
+def test_head_groups(d, Hq, Hkv):
+    check(make([200, 1, 130], 1, Hq, Hkv, d, 16, seed=Hq))
+
+
+@pytest.mark.parametrize("Nq", [2, 3, 4, 8, 17])
+@pytest.mark.parametrize("Hq,Hkv,d", [(2, 2, 64), (8, 2, 128), (10, 2, 128), (8, 1, 64)])
+def test_drafts(Nq, Hq, Hkv, d):
+    """Rows of one request end at different keys; the first rows of short requests see none."""
+    check(make([1, 3, 130, 257, 0], Nq, Hq, Hkv, d, 32, seed=Nq))
+
+
+@pytest.mark.parametrize("window", [0, 1, 15, 100, 127, 128, 129, 1000])
+@pytest.mark.parametrize("Nq", [1, 4])
+@pytest.mark.parametrize("d", [64, 128])
+def test_windows(window, Nq, d):
+    check(make([1, 2, 128, 129, 300, 511, 0], Nq, 4, 2, d, 16, seed=window), window=window)
+    check(make([300, 700], Nq, 4, 1, d, 64, seed=window), window=window, splits=3)
+
+
+@pytest.mark.parametrize("splits", [1, 2, 3, 5, 7, 64])
+def test_splits_agree(splits):
+    """More chunks than tiles, chunks that are empty for the short requests, a capacity far above the lengths."""
+    case = make([1, 640, 0, 129], 1, 8, 2, 128, 16, seed=3)
+    check(case, splits=splits)
+    check(case, splits=splits, L=656)
+
+
+def test_large_and_small_values():
+    check(make([300, 40], 1, 4, 2, 128, 16, seed=1, amp=2.0 ** 40), scale=2.0 ** -45)
+    check(make([300, 40], 1, 4, 2, 128, 16, seed=1, amp=2.0 ** -40), scale=2.0 ** 35)
+    q, k, v, table, lens = make([300, 40], 1, 4, 2, 64, 16, seed=2)
+    q = q * torch.logspace(-25, 20, 64, base=2.0).to(torch.bfloat16)      # queries of a wide range
+    check((q, k, v, table, lens), scale=2.0 ** -22)
+    check(make([300, 40], 1, 4, 2, 64, 16, seed=2), scale=30.0 / 8)       # peaked: scores of a hundred and more
+
+
+def test_pages_of_zeros_and_one_loud_page():
+    q, (kc, ks), (vc, vs), table, lens = make([200], 1, 4, 2, 128, 16, seed=5)
+    kc[table[0, 3]], ks[table[0, 3]] = 0, 0.0      # a page whose keys and values were all zero: scale 0
+    vc[table[0, 3]], vs[table[0, 3]] = 0, 0.0
+    vs[table[0, 7]] *= 2.0 ** 30
+    check((q, (kc, ks), (vc, vs), table, lens))
+    vc[table[0, :13]], vs[table[0, :13]] = 0, 0.0  # no values at all
+    o, lse = check((q, (kc, ks), (vc, vs), table, lens))
+    assert torch.all(o == 0) and torch.isfinite(lse).all()
+
+
+def test_equal_keys_average_the_values():
+    """With q = 0 every weight is 1 / n and lse = log n, whatever the keys."""
+    for n in (1, 100, 1000):
+        q, k, v, table, lens = make([n], 1, 2, 1, 64, 16, seed=n)
+        o, lse = check((q * 0, k, v, table, lens))
+        assert np.all(np.abs(lse.cpu().numpy() - math.log(n)) <= 2.0 ** -13)
+
+
+def test_bad_tables_and_lengths_are_reported():
+    q, k, v, table, lens = make([100, 50], 1, 4, 2, 64, 16, seed=6, garbage=False)
+    a = dev((q, k, v, table, lens))
+    for bad in (-1, k[0].shape[0], 2 ** 31 - 1):
+        t = a[5].clone()
+        t[0, 2] = bad
+        ops.decode_kv8(*a[:5], t, a[6], 100)
+        assert ops.device_error() == 0x2000
+    for n in (-5, 101, 2 ** 31 - 1):
+        s = a[6].clone()
+        s[1] = n
+        o, lse = ops.decode_kv8(*a[:5], a[5].clamp(0, k[0].shape[0] - 1), s, 100)
+        assert ops.device_error() == 0x2001
+        if n < 0:
+            assert torch.all(o[1] == 0) and torch.all(lse[1] == -math.inf)
+
+
+def test_a_captured_call_follows_the_lengths():
+    case = make([700, 300], 1, 8, 2, 128, 16, seed=7)
+    a = dev(case)
+    ws = torch.empty(_lib.load().fa_decode_kv8_workspace_bytes(2, 1, 8, 128, 64), dtype=torch.uint8, device="cuda")
+    ops.decode_kv8(*a, 700, workspace=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = ops.decode_kv8(*a, 700, workspace=ws)
+    ws.fill_(0xFF)
+    for lens in ([700, 300], [1, 0], [512, 129]):
+        a[6].copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        q, (kc, ks), (vc, vs), table, _ = case
+        assert_close(o, lse, serving.decode_kv8(synth.to_f64(q), kc, vc, ks, vs, table, lens, -1, 128 ** -0.5))
+    assert ops.device_error() == 0
+
+
+def test_two_calls_at_once_and_another_stream():
+    one, two = make([700], 1, 8, 2, 128, 16, seed=8), make([650, 3], 1, 4, 2, 64, 32, seed=9)
+    a, b = dev(one), dev(two)
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        got.append((ops.decode_kv8(*a, 700, stream=s), ops.decode_kv8(*b, 650, stream=t)))
+    s.synchronize(), t.synchronize()
+    for x, case in ((0, one), (1, two)):
+        q, (kc, ks), (vc, vs), table, lens = case
+        ref = serving.decode_kv8(synth.to_f64(q), kc, vc, ks, vs, table, lens, -1, q.shape[3] ** -0.5)
+        for pair in got:
+            assert_close(*pair[x], ref)
+
+
+def test_refusals():
+    a = list(dev(make([20], 1, 4, 2, 64, 16)))
+    with pytest.raises(ValueError):
+        ops.decode_kv8(a[0][..., :32], *a[1:], 20)
+    with pytest.raises(ValueError):
+        ops.decode_kv8(*a, 20, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(_lib.FaError):
+        ops.decode_kv8(*a, 10 ** 6)                       # more keys than the table has blocks for
+    with pytest.raises(_lib.FaError):
+        ops.decode_kv8(a[0][:, :, :3].contiguous(), *a[1:], 20)
+    with pytest.raises(ValueError):
+        ops.decode_kv8(a[0].repeat(1, 1, 1, 2)[..., ::2], *a[1:], 20)
