@@ -126,6 +126,18 @@ bool make_tmap_u8(CUtensorMap* m, const void* ptr, const uint64_t dims_in[4], co
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_codes(CUtensorMap* m, const void* ptr, int D, int page_size, long long page_heads, int box_rows) {
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page_size, (cuuint64_t)page_heads};
+  cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)page_size * D};
+  cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace fa
 
 using namespace fa;
@@ -926,7 +938,13 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   p.scale_log2 = scale * kLog2e;
   p.err = g_err_ptr;
   p.timeout_ns = g_opt.timeout_ns;
-  return launch_decode_kv8(p, d, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  p.box_rows = 16;
+  while (p.box_rows < kKv8Tile && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+  CUtensorMap tk, tv;
+  if (!make_tmap_codes(&tk, k_codes, d, page_size, (long long)num_pages * Hkv, p.box_rows) ||
+      !make_tmap_codes(&tv, v_codes, d, page_size, (long long)num_pages * Hkv, p.box_rows))
+    return FA_ERR_INVALID_ARG;
+  return launch_decode_kv8(tk, tv, p, d, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

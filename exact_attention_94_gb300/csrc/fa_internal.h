@@ -232,12 +232,17 @@ struct Kv8DecodeParams {
   int page_size, num_pages, max_blocks, max_len;
   int win_left;              // -1: no window
   int splits, chunk;         // keys per split
+  int box_rows;              // keys per TMA box: 16 .. 128, divides the page and the tile
+  int row_tiles;             // CTAs' worth of query rows per K/V head, set by the launch
   float scale_log2;
   unsigned* err;
   unsigned long long timeout_ns;
 };
 int kv8_auto_splits(int B, int Nq, int Hkv, int group, int span);
-cudaError_t launch_decode_kv8(const Kv8DecodeParams& p, int D, cudaStream_t stream);
+// 3-D uint8 tensor map of the codes, [heads of pages][page_size][D], swizzled at the row's length.
+bool make_tmap_codes(CUtensorMap* m, const void* ptr, int D, int page_size, long long page_heads, int box_rows);
+cudaError_t launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int D,
+                              cudaStream_t stream);
 
 int decode_stages(int G, int D);
 size_t decode_smem_bytes(int G, int D);

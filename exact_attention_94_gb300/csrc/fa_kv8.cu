@@ -17,23 +17,14 @@
 #include "fa_internal.h"
 #include "ptx.cuh"
 
-#include <cuda_fp16.h>
-
 namespace fa {
 
 namespace {
 
 constexpr int kAppendWarps = 8;
 
-// Two e4m3 codes (low byte first) -> two fp32 values, exact.
-__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
-  const float2 a = e4m3x2_to_f32(w & 0xffffu), b = e4m3x2_to_f32(w >> 16);
+  const float2 a = unpack_e4m3x2(w & 0xffffu), b = unpack_e4m3x2(w >> 16);
   return pack_e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
 }
 
