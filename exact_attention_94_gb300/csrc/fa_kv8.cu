@@ -22,6 +22,8 @@ namespace fa {
 namespace {
 
 constexpr int kAppendWarps = 8;
+constexpr long long kAppendMany = 152 * 64;  // warps that the SMs hold at once
+constexpr int kHeld = 16;  // vectors of a run that a lane holds in registers
 
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
   const float2 a = unpack_e4m3x2(w & 0xffffu), b = unpack_e4m3x2(w >> 16);
@@ -117,13 +119,36 @@ __global__ void __launch_bounds__(32 * kAppendWarps) fa_kv8_append_kernel(const 
       len += more < 0 ? 32 : more;
       if (more >= 0) break;
     }
-    // ---- largest finite magnitude (as bf16 bits: they order like the values)
+    // ---- largest finite magnitude (as bf16 bits: they order like the values).
+    // A run of up to kHeld * RPI rows stays in registers; a longer one is read
+    // again for its codes.
+    const __nv_bfloat16* rows_at = x + row * xs + seg * 8;
+    uint4 held[kHeld];
     uint32_t mx = 0;
-    for (int i = sub; i < len; i += RPI) {
-      const uint4 u = *reinterpret_cast<const uint4*>(x + (row + i) * xs + seg * 8);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    auto load = [&](int i0) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) mx = __vmaxu2(mx, finite_or_zero(w[q] & 0x7fff7fffu));
+      for (int c = 0; c < kHeld; ++c) {
+        const int i = i0 + sub + c * RPI;
+        held[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < len) held[c] = *reinterpret_cast<const uint4*>(rows_at + i * xs);
+      }
+    };
+    for (int i0 = 0; i0 < len; i0 += kHeld * RPI) {
+      load(i0);
+#pragma unroll
+      for (int c = 0; c < kHeld; ++c) {
+        if (i0 + c * RPI >= len) break;
+        const uint32_t w[4] = {held[c].x, held[c].y, held[c].z, held[c].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) top = __vmaxu2(top, w[q] & 0x7fff7fffu);
+        if (__vcmpgeu2(top, 0x7f807f80u) != 0) {  // an infinity or a NaN among them
+          top = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) top = __vmaxu2(top, finite_or_zero(w[q] & 0x7fff7fffu));
+        }
+        mx = __vmaxu2(mx, top);
+      }
     }
     const float own = pow2_scale(__reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16)));
     const size_t at = (size_t)page * p.Hkv + head;
@@ -145,16 +170,24 @@ __global__ void __launch_bounds__(32 * kAppendWarps) fa_kv8_append_kernel(const 
       }
     }
     // ---- new codes
-    for (int i = sub; i < len; i += RPI) {
-      const uint4 u = *reinterpret_cast<const uint4*>(x + (row + i) * xs + seg * 8);
-      *reinterpret_cast<uint2*>(dst + (size_t)(first + i) * D) = encode8(u, inv);
+    dst += (size_t)first * D;
+    for (int i0 = 0; i0 < len; i0 += kHeld * RPI) {
+      if (len > kHeld * RPI) load(i0);
+#pragma unroll
+      for (int c = 0; c < kHeld; ++c) {
+        const int i = i0 + sub + c * RPI;
+        if (i < len) *reinterpret_cast<uint2*>(dst + (size_t)i * D) = encode8(held[c], inv);
+      }
     }
   }
 }
 
 template <int D>
 static cudaError_t launch_kv8_append_t(Kv8AppendParams& p, cudaStream_t stream) {
-  p.rows_per_warp = 1;
+  // A warp looks at one row where there are few (its run's work starts at once,
+  // and warps whose row begins no run cost nothing but their launch), at 16
+  // where the launch itself would cost more than the runs.
+  p.rows_per_warp = (long long)p.n * 2 * p.Hkv > kAppendMany ? 16 : 1;
   const long long units = ((long long)p.n + p.rows_per_warp - 1) / p.rows_per_warp * 2 * p.Hkv;
   const long long blocks = (units + kAppendWarps - 1) / kAppendWarps;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;

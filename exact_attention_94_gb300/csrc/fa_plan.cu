@@ -27,6 +27,7 @@ namespace fa {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanRows = 4;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
 __device__ __forceinline__ int div_up(int a, int b) { return (int)(((long long)a + b - 1) / b); }
@@ -119,45 +120,69 @@ __global__ void __launch_bounds__(kPlanThreads) fa_page_plan_kernel(const PlanPa
     }
   }
 
-  // ---- rows
+  // ---- rows, kPlanRows of a thread at a time: their searches and page loads overlap
   const int total = s_cu[p.B];
-  for (long long r = (long long)rank * kPlanThreads + tid; r < p.max_tokens; r += (long long)ranks * kPlanThreads) {
-    const int row = (int)r;
-    int page = -1, slot = -1, pos = 0;
-    if (row < total) {
-      int lo = 0, hi = p.B - 1;  // the last request whose first row is at most this one
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_cu[mid] <= row)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      const int ctx = s_ctx[lo];
-      pos = ctx + row - s_cu[lo];
-      const int blk = pos / p.page_size, held = div_up(ctx, p.page_size);
-      slot = pos - blk * p.page_size;
-      int* entry = p.block_table + (size_t)lo * p.max_blocks + blk;
-      page = blk < held ? *entry : p.free_pages[free_n - 1 - (s_base[lo] + blk - held)];
-      if (page < 0 || page >= p.num_pages) {
-        atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
-        page = slot = -1;
-      } else if (slot == 0) {
-        *entry = page;  // the first token of a new page
+  const long long step = (long long)ranks * kPlanThreads;
+  for (long long r0 = (long long)rank * kPlanThreads + tid; r0 < p.max_tokens; r0 += step * kPlanRows) {
+    int page[kPlanRows], slot[kPlanRows], pos[kPlanRows], lo[kPlanRows], hi[kPlanRows];
+    int* entry[kPlanRows];
+#pragma unroll
+    for (int x = 0; x < kPlanRows; ++x) lo[x] = 0, hi[x] = p.B - 1;
+    for (int n = p.B; n > 1; n = (n + 1) >> 1) {  // the last request whose first row is at most this one
+#pragma unroll
+      for (int x = 0; x < kPlanRows; ++x) {
+        const int mid = (lo[x] + hi[x] + 1) >> 1;
+        const bool up = s_cu[mid] <= r0 + x * step;
+        lo[x] = up ? mid : lo[x];
+        hi[x] = up ? hi[x] : max(lo[x], mid - 1);
       }
     }
-    p.page[row] = page;
-    p.slot[row] = slot;
-    p.position[row] = pos;
+#pragma unroll
+    for (int x = 0; x < kPlanRows; ++x) {
+      page[x] = slot[x] = -1;
+      pos[x] = 0;
+      entry[x] = nullptr;
+      if (r0 + x * step < total) {
+        const int ctx = s_ctx[lo[x]];
+        pos[x] = ctx + (int)(r0 + x * step) - s_cu[lo[x]];
+        const int blk = pos[x] / p.page_size, held = div_up(ctx, p.page_size);
+        slot[x] = pos[x] - blk * p.page_size;
+        entry[x] = p.block_table + (size_t)lo[x] * p.max_blocks + blk;
+        page[x] = *(blk < held ? entry[x] : p.free_pages + (free_n - 1 - (s_base[lo[x]] + blk - held)));
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kPlanRows; ++x) {
+      const long long row = r0 + x * step;
+      if (row >= p.max_tokens) break;
+      if (entry[x] != nullptr) {
+        if (page[x] < 0 || page[x] >= p.num_pages) {
+          atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
+          page[x] = slot[x] = -1;
+        } else if (slot[x] == 0) {
+          *entry[x] = page[x];  // the first token of a new page
+        }
+      }
+      p.page[row] = page[x];
+      p.slot[row] = slot[x];
+      p.position[row] = pos[x];
+    }
   }
 }
 
 cudaError_t launch_page_plan(const PlanParams& p, cudaStream_t stream) {
   const size_t smem = (3 * (size_t)p.B + 1) * sizeof(int);
-  cudaError_t e = cudaFuncSetAttribute(fa_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(fa_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.max_tokens <= 4 * kPlanThreads) {
+    fa_page_plan_kernel<<<1, kPlanThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.max_tokens > 4 * kPlanThreads ? 8 : 1);
+  cfg.gridDim = dim3(8);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

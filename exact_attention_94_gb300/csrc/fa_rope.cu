@@ -20,6 +20,7 @@ namespace fa {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr long long kRopeFull = 152 * 1024;  // threads that keep the SMs busy
 
 __device__ __forceinline__ float2 bf2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -27,7 +28,7 @@ __device__ __forceinline__ float2 bf2(uint32_t w) {
 
 }  // namespace
 
-template <int D, bool NB>
+template <int D, bool NB, int BATCH>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int TPT = D / 16;  // threads per token and head: 8 pairs each
   const long long item = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) / TPT;
@@ -56,52 +57,79 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
   }
   // element offsets of the thread's two vectors within a head
   const int o0 = NB ? 16 * j : 8 * j, o1 = NB ? 16 * j + 8 : 8 * j + D / 2;
-  for (int h = h0; h < h1; ++h) {
-    const bool isq = h < p.Hq;
-    const int hh = isq ? h : h - p.Hq;
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(isq ? p.q : p.k) +
-                               t * (isq ? p.q_stride : p.k_stride) + (size_t)hh * D;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(isq ? p.q_out : p.k_out) +
-                         t * (isq ? p.q_out_stride : p.k_out_stride) + (size_t)hh * D;
-    const uint4 u = *reinterpret_cast<const uint4*>(src + o0), v = *reinterpret_cast<const uint4*>(src + o1);
-    const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
-    uint32_t ra[4], rb[4];
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride;
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride;
+  __nv_bfloat16* qo = static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride;
+  __nv_bfloat16* ko = static_cast<__nv_bfloat16*>(p.k_out) + t * p.k_out_stride;
+  // the loads of BATCH heads first, then their stores: outputs may be the
+  // inputs, so the compiler could not move a load past a store by itself
+  for (int h = h0; h < h1; h += BATCH) {
+    uint4 u[BATCH], v[BATCH];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (NB) {  // word i of a is pair 8j + i, word i of b pair 8j + 4 + i
-        const float2 x = bf2(a[i]), y = bf2(b[i]);
-        ra[i] = pack_bf16x2(x.x * co[i] - x.y * si[i], x.x * si[i] + x.y * co[i]);
-        rb[i] = pack_bf16x2(y.x * co[4 + i] - y.y * si[4 + i], y.x * si[4 + i] + y.y * co[4 + i]);
-        if (!(turned >> i & 1)) ra[i] = a[i];
-        if (!(turned >> (4 + i) & 1)) rb[i] = b[i];
-      } else {  // words i hold the two halves of pairs 8j + 2i and 8j + 2i + 1
-        const float2 x = bf2(a[i]), y = bf2(b[i]);
-        ra[i] = pack_bf16x2(x.x * co[2 * i] - y.x * si[2 * i], x.y * co[2 * i + 1] - y.y * si[2 * i + 1]);
-        rb[i] = pack_bf16x2(x.x * si[2 * i] + y.x * co[2 * i], x.y * si[2 * i + 1] + y.y * co[2 * i + 1]);
-        // a pair that does not turn is copied: 0 times an infinity would not be
-        const uint32_t keep = ((turned >> (2 * i) & 1) ? 0u : 0xffffu) | ((turned >> (2 * i + 1) & 1) ? 0u : 0xffff0000u);
-        ra[i] = (ra[i] & ~keep) | (a[i] & keep);
-        rb[i] = (rb[i] & ~keep) | (b[i] & keep);
+    for (int x = 0; x < BATCH; ++x) {
+      if (h + x < h1) {
+        const __nv_bfloat16* src = h + x < p.Hq ? q + (size_t)(h + x) * D : k + (size_t)(h + x - p.Hq) * D;
+        u[x] = *reinterpret_cast<const uint4*>(src + o0);
+        v[x] = *reinterpret_cast<const uint4*>(src + o1);
       }
     }
-    *reinterpret_cast<uint4*>(dst + o0) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
-    *reinterpret_cast<uint4*>(dst + o1) = make_uint4(rb[0], rb[1], rb[2], rb[3]);
+#pragma unroll
+    for (int x = 0; x < BATCH; ++x) {
+      if (h + x >= h1) break;
+      const uint32_t a[4] = {u[x].x, u[x].y, u[x].z, u[x].w}, b[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+      uint32_t ra[4], rb[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = bf2(a[i]), z = bf2(b[i]);
+        if constexpr (NB) {  // word i of a is pair 8j + i, word i of b pair 8j + 4 + i
+          ra[i] = pack_bf16x2(y.x * co[i] - y.y * si[i], y.x * si[i] + y.y * co[i]);
+          rb[i] = pack_bf16x2(z.x * co[4 + i] - z.y * si[4 + i], z.x * si[4 + i] + z.y * co[4 + i]);
+        } else {  // words i hold the two halves of pairs 8j + 2i and 8j + 2i + 1
+          ra[i] = pack_bf16x2(y.x * co[2 * i] - z.x * si[2 * i], y.y * co[2 * i + 1] - z.y * si[2 * i + 1]);
+          rb[i] = pack_bf16x2(y.x * si[2 * i] + z.x * co[2 * i], y.y * si[2 * i + 1] + z.y * co[2 * i + 1]);
+        }
+      }
+      if (turned != 0xffu) {  // pairs that do not turn are copied: 0 times an infinity would not be
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (NB) {
+            if (!(turned >> i & 1)) ra[i] = a[i];
+            if (!(turned >> (4 + i) & 1)) rb[i] = b[i];
+          } else {
+            const uint32_t keep =
+                ((turned >> (2 * i) & 1) ? 0u : 0xffffu) | ((turned >> (2 * i + 1) & 1) ? 0u : 0xffff0000u);
+            ra[i] = (ra[i] & ~keep) | (a[i] & keep);
+            rb[i] = (rb[i] & ~keep) | (b[i] & keep);
+          }
+        }
+      }
+      __nv_bfloat16* dst = h + x < p.Hq ? qo + (size_t)(h + x) * D : ko + (size_t)(h + x - p.Hq) * D;
+      *reinterpret_cast<uint4*>(dst + o0) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
+      *reinterpret_cast<uint4*>(dst + o1) = make_uint4(rb[0], rb[1], rb[2], rb[3]);
+    }
   }
 }
 
-cudaError_t launch_rope(RopeParams& p, int D, bool neighbours, cudaStream_t stream) {
-  p.heads_per_thread = 1;
-  p.chunks = p.Hq + p.Hkv;
-  const long long threads = (long long)p.T * p.chunks * (D / 16);
-  const long long blocks = (threads + kRopeThreads - 1) / kRopeThreads;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)blocks);
-  if (D == 64)
-    neighbours ? fa_rope_kernel<64, true><<<grid, kRopeThreads, 0, stream>>>(p)
-               : fa_rope_kernel<64, false><<<grid, kRopeThreads, 0, stream>>>(p);
+template <int D, bool NB>
+static void launch_rope_t(const RopeParams& p, unsigned blocks, cudaStream_t stream) {
+  if (p.heads_per_thread == 1)
+    fa_rope_kernel<D, NB, 1><<<blocks, kRopeThreads, 0, stream>>>(p);
   else
-    neighbours ? fa_rope_kernel<128, true><<<grid, kRopeThreads, 0, stream>>>(p)
-               : fa_rope_kernel<128, false><<<grid, kRopeThreads, 0, stream>>>(p);
+    fa_rope_kernel<D, NB, 4><<<blocks, kRopeThreads, 0, stream>>>(p);
+}
+
+cudaError_t launch_rope(RopeParams& p, int D, bool neighbours, cudaStream_t stream) {
+  const int H = p.Hq + p.Hkv, tpt = D / 16;
+  const long long one = (long long)p.T * H * tpt;  // threads with a head each
+  p.chunks = one >= 8 * kRopeFull ? (H + 7) / 8 : H;
+  p.heads_per_thread = (H + p.chunks - 1) / p.chunks;
+  p.chunks = (H + p.heads_per_thread - 1) / p.heads_per_thread;
+  const long long blocks = ((long long)p.T * p.chunks * tpt + kRopeThreads - 1) / kRopeThreads;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (D == 64)
+    neighbours ? launch_rope_t<64, true>(p, (unsigned)blocks, stream) : launch_rope_t<64, false>(p, (unsigned)blocks, stream);
+  else
+    neighbours ? launch_rope_t<128, true>(p, (unsigned)blocks, stream) : launch_rope_t<128, false>(p, (unsigned)blocks, stream);
   return cudaGetLastError();
 }
 
