@@ -871,25 +871,24 @@ static int kv8_span(int Nq, int max_seq_len, int window_left) {
   return window_left + Nq;
 }
 
-size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int d, int num_splits) {
-  if (B < 1 || Nq < 1 || Hq < 1 || d < 1 || num_splits < 1) return 0;
-  const size_t rows = (size_t)B * Nq * Hq * num_splits;
-  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float));
+size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_shares) {
+  if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || d < 1 || num_shares < 1) return 0;
+  const size_t rows = 2 * (size_t)num_shares * kv8_row_tile(Nq * (Hq / Hkv));
+  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float)) + ((size_t)B + 1) * sizeof(long long);
 }
 
-int fa_decode_kv8_num_splits(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left, int d) {
-  (void)d;
+int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left) {
   if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || max_seq_len < 1) return 1;
-  return kv8_auto_splits(B, Nq, Hkv, Hq / Hkv, kv8_span(Nq, max_seq_len, window_left));
+  return kv8_auto_shares(B, Nq, Hkv, Hq / Hkv, kv8_span(Nq, max_seq_len, window_left));
 }
 
 fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
                         const float* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse, int B,
                         int Nq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_blocks, int max_seq_len,
-                        int window_left, int num_splits, void* workspace, float scale, fa_stream_t stream) {
+                        int window_left, int num_shares, void* workspace, float scale, fa_stream_t stream) {
   if (B < 1 || B > 65535 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (long long)Nq * Hq > 65535)
     return FA_ERR_INVALID_ARG;
-  if (num_pages < 1 || max_blocks < 1 || max_seq_len < 0 || num_splits < 0 || num_splits > 65535 || window_left < -1)
+  if (num_pages < 1 || max_blocks < 1 || max_seq_len < 0 || num_shares < 0 || num_shares > 65535 || window_left < -1)
     return FA_ERR_INVALID_ARG;
   if (page_size < 16 || page_size % 16 != 0 || (long long)max_blocks * page_size < max_seq_len)
     return FA_ERR_INVALID_ARG;
@@ -906,13 +905,9 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   if (!ensure_init()) return FA_ERR_LAUNCH;
   Kv8DecodeParams p{};
   if (window_left >= max_seq_len) window_left = -1;  // a window past every key is no window
-  const int span = kv8_span(Nq, max_seq_len, window_left);
-  p.splits = num_splits > 0 ? num_splits : fa_decode_kv8_num_splits(B, Nq, Hq, Hkv, max_seq_len, window_left, d);
-  // whole tiles; a window's first tile may begin up to a tile before its first key
-  const long long tiles = ((long long)span + kKv8Tile - 1) / kKv8Tile + (window_left >= 0 ? 1 : 0);
-  p.chunk = (int)((tiles + p.splits - 1) / p.splits) * kKv8Tile;
-  if (p.chunk < kKv8Tile) p.chunk = kKv8Tile;
-  const size_t rows = (size_t)B * Nq * Hq * p.splits;
+  if (num_shares == 0) num_shares = fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, max_seq_len, window_left);
+  const size_t rows = 2 * (size_t)num_shares * kv8_row_tile(Nq * (Hq / Hkv));
+  const size_t o_bytes = align256(rows * d * sizeof(float)), l_bytes = align256(rows * sizeof(float));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = q;
   p.k_codes = static_cast<const uint8_t*>(k_codes);
@@ -924,7 +919,8 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   p.o = o;
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws);
-  p.part_lse = reinterpret_cast<float*>(ws + align256(rows * d * sizeof(float)));
+  p.part_lse = reinterpret_cast<float*>(ws + o_bytes);
+  p.first_tile = reinterpret_cast<long long*>(ws + o_bytes + l_bytes);
   p.B = B;
   p.Nq = Nq;
   p.Hq = Hq;
@@ -944,7 +940,7 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   if (!make_tmap_codes(&tk, k_codes, d, page_size, (long long)num_pages * Hkv, p.box_rows) ||
       !make_tmap_codes(&tv, v_codes, d, page_size, (long long)num_pages * Hkv, p.box_rows))
     return FA_ERR_INVALID_ARG;
-  return launch_decode_kv8(tk, tv, p, d, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  return launch_decode_kv8(tk, tv, p, d, num_shares, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -215,7 +215,7 @@ struct Kv8AppendParams {
 cudaError_t launch_kv8_append(Kv8AppendParams& p, int D, cudaStream_t stream);
 
 // Attention over the 8-bit paged cache (see fa_decode_kv8 in fa.h).
-constexpr int kKv8Tile = 128;  // keys per tile; chunks are multiples of it
+constexpr int kKv8Tile = 128;  // keys per tile
 struct Kv8DecodeParams {
   const void* q;             // [B, Nq, Hq, d] bf16
   const uint8_t* k_codes;    // [num_pages, Hkv, page_size, d]
@@ -226,22 +226,23 @@ struct Kv8DecodeParams {
   const int* seq_lens;       // [B]
   void* o;
   float* lse;
-  float* part_o;             // [B, Nq, Hq, splits, d] fp32, each normalised
-  float* part_lse;           // [B, Nq, Hq, splits] log2 of each chunk's softmax mass
+  float* part_o;             // [2 * shares, RT, d] fp32: the pieces a share's borders cut, each normalised
+  float* part_lse;           // [2 * shares, RT] log2 of each piece's softmax mass
+  long long* first_tile;     // [B + 1] tiles before each request, written by the kernel for the merge
   int B, Nq, Hq, Hkv, group;
   int page_size, num_pages, max_blocks, max_len;
   int win_left;              // -1: no window
-  int splits, chunk;         // keys per split
   int box_rows;              // keys per TMA box: 16 .. 128, divides the page and the tile
-  int row_tiles;             // CTAs' worth of query rows per K/V head, set by the launch
+  int row_tiles;             // tiles of query rows per K/V head, set by the launch
   float scale_log2;
   unsigned* err;
   unsigned long long timeout_ns;
 };
-int kv8_auto_splits(int B, int Nq, int Hkv, int group, int span);
+int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span);
+int kv8_row_tile(int rows);  // query rows of a CTA for `rows` rows per K/V head
 // 3-D uint8 tensor map of the codes, [heads of pages][page_size][D], swizzled at the row's length.
 bool make_tmap_codes(CUtensorMap* m, const void* ptr, int D, int page_size, long long page_heads, int box_rows);
-cudaError_t launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int D,
+cudaError_t launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int D, int shares,
                               cudaStream_t stream);
 
 int decode_stages(int G, int D);

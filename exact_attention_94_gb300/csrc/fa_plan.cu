@@ -30,7 +30,11 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanRows = 4;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
-__device__ __forceinline__ int div_up(int a, int b) { return (int)(((long long)a + b - 1) / b); }
+// a / b rounded up, for a >= 0, b > 0, without a 64-bit division
+__device__ __forceinline__ int div_up(int a, int b) {
+  const unsigned q = (unsigned)a / (unsigned)b;
+  return (int)(q + (q * (unsigned)b != (unsigned)a ? 1u : 0u));
+}
 
 __device__ __forceinline__ long long warp_incl_sum(long long v, int lane) {
 #pragma unroll
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_page_plan_kernel(const PlanPa
       if (r0 + x * step < total) {
         const int ctx = s_ctx[lo[x]];
         pos[x] = ctx + (int)(r0 + x * step) - s_cu[lo[x]];
-        const int blk = pos[x] / p.page_size, held = div_up(ctx, p.page_size);
+        const int blk = (int)((unsigned)pos[x] / (unsigned)p.page_size), held = div_up(ctx, p.page_size);
         slot[x] = pos[x] - blk * p.page_size;
         entry[x] = p.block_table + (size_t)lo[x] * p.max_blocks + blk;
         page[x] = *(blk < held ? entry[x] : p.free_pages + (free_n - 1 - (s_base[lo[x]] + blk - held)));

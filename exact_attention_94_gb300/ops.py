@@ -852,7 +852,7 @@ def kv8_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, page, slot, cop
 
 @_on_call_stream
 def decode_kv8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, max_seq_len: int, window_left: int = -1,
-               num_splits: int = 0, scale: Optional[float] = None, workspace=None, *, stream=None):
+               num_shares: int = 0, scale: Optional[float] = None, workspace=None, *, stream=None):
     """Attention of q [B, Nq, Hq, d] over the 8-bit paged cache; query i of a
     request stands at seq_lens - Nq + i.  block_table int32 [B, max_blocks] and
     seq_lens int32 [B] on the device.  Returns (o [B, Nq, Hq, d], lse [B, Hq, Nq])."""
@@ -867,10 +867,10 @@ def decode_kv8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, max
     _check_i32("block_table", block_table, (B, max_blocks))
     _check_i32("seq_lens", seq_lens, (B,))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    L, wl, splits, so = int(max_seq_len), int(window_left), int(num_splits), lib()
-    if splits == 0:
-        splits = so.fa_decode_kv8_num_splits(B, Nq, Hq, Hkv, L, wl, d)
-    nbytes = so.fa_decode_kv8_workspace_bytes(B, Nq, Hq, d, max(splits, 1))
+    L, wl, shares, so = int(max_seq_len), int(window_left), int(num_shares), lib()
+    if shares == 0:
+        shares = so.fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, L, wl)
+    nbytes = so.fa_decode_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, max(shares, 1))
     if workspace is None:
         workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
     elif workspace.numel() * workspace.element_size() < nbytes or not workspace.is_contiguous():
@@ -879,6 +879,6 @@ def decode_kv8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, max
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
     st = so.fa_decode_kv8(q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                           block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d,
-                          P, num_pages, max_blocks, L, wl, splits, workspace.data_ptr(), scale, stream)
+                          P, num_pages, max_blocks, L, wl, shares, workspace.data_ptr(), scale, stream)
     _lib.check(st, "fa_decode_kv8")
     return o, lse

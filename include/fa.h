@@ -545,7 +545,8 @@ fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, voi
 
 /*
  * Attention of a few query tokens per request over the 8-bit paged cache
- * (split-KV, as fa_decode_paged_window).  Query i of the Nq of request b sits
+ * (split-KV, as fa_decode_paged_window, but with the requests' keys dealt in
+ * equal shares, whatever their lengths).  Query i of the Nq of request b sits
  * at key position seq_lens[b] - Nq + i and sees the keys up to its own
  * position, from position - window_left on (window_left = -1: from 0).  One
  * token is plain decoding; more are drafts to verify, whose keys the cache
@@ -554,11 +555,12 @@ fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, voi
  *   lse          : [B, Hq, Nq] fp32, written
  *   codes, scales: as above; Hkv divides Hq
  *   block_table  : int32 [B, max_blocks], seq_lens : int32 [B], device
- *   max_seq_len  : <= max_blocks * page_size and <= 2^30; sizes the splits
- *   num_splits   : 0 = choose (fa_decode_kv8_num_splits); else 1 .. 65535
- *   workspace    : fa_decode_kv8_workspace_bytes(B, Nq, Hq, d, splits) bytes, 16-byte
- *                  aligned, contents on entry do not matter; calls whose work
- *                  overlaps on the GPU need one each
+ *   max_seq_len  : <= max_blocks * page_size and <= 2^30
+ *   num_shares   : shares (CTAs) that the work is dealt to, 1 .. 65535; 0 =
+ *                  choose (fa_decode_kv8_num_shares)
+ *   workspace    : fa_decode_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, shares) bytes,
+ *                  16-byte aligned, contents on entry do not matter; calls
+ *                  whose work overlaps on the GPU need one each
  * What a page holds behind a request's last key is never used, whatever it
  * is.  Table entries outside the pool and lengths outside [0, max_seq_len] are
  * handled and reported as in fa_decode_paged.  page_size a multiple of 16, d = 64
@@ -567,11 +569,11 @@ fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, voi
 fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
                         const float* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse, int B,
                         int Nq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_blocks, int max_seq_len,
-                        int window_left, int num_splits, void* workspace, float scale, fa_stream_t stream);
+                        int window_left, int num_shares, void* workspace, float scale, fa_stream_t stream);
 
-/* Splits fa_decode_kv8 uses when it is given num_splits = 0 (window_left as there). */
-int fa_decode_kv8_num_splits(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left, int d);
-size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int d, int num_splits);
+/* Shares fa_decode_kv8 uses when it is given num_shares = 0 (window_left as there). */
+int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left);
+size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_shares);
 
 /*
  * Synchronises the device, then returns FA_OK if no kernel of this library

@@ -74,11 +74,11 @@ def assert_close(o, lse, ref):
     assert np.all(o[np.moveaxis(none, 1, 2)] == 0)
 
 
-def check(case, window=-1, splits=0, L=None, scale=None):
+def check(case, window=-1, shares=0, L=None, scale=None):
     q, (kc, ks), (vc, vs), table, lens = case
     sc = 1 / math.sqrt(q.shape[3]) if scale is None else scale
     L = int(lens.max()) if L is None else L
-    o, lse = ops.decode_kv8(*dev(case), L, window_left=window, num_splits=splits, scale=scale)
+    o, lse = ops.decode_kv8(*dev(case), L, window_left=window, num_shares=shares, scale=scale)
     assert ops.device_error() == 0
     assert_close(o, lse, serving.decode_kv8(synth.to_f64(q), kc, vc, ks, vs, table, lens, window, sc))
     return o, lse
@@ -109,15 +109,32 @@ def test_drafts(Nq, Hq, Hkv, d):
 @pytest.mark.parametrize("d", [64, 128])
 def test_windows(window, Nq, d):
     check(make([1, 2, 128, 129, 300, 511, 0], Nq, 4, 2, d, 16, seed=window), window=window)
-    check(make([300, 700], Nq, 4, 1, d, 64, seed=window), window=window, splits=3)
+    check(make([300, 700], Nq, 4, 1, d, 64, seed=window), window=window, shares=3)
 
 
-@pytest.mark.parametrize("splits", [1, 2, 3, 5, 7, 64])
-def test_splits_agree(splits):
-    """More chunks than tiles, chunks that are empty for the short requests, a capacity far above the lengths."""
-    case = make([1, 640, 0, 129], 1, 8, 2, 128, 16, seed=3)
-    check(case, splits=splits)
-    check(case, splits=splits, L=656)
+@pytest.mark.parametrize("shares", [1, 2, 3, 5, 7, 16, 64])
+@pytest.mark.parametrize("Nq", [1, 9])
+def test_any_number_of_shares(shares, Nq):
+    """Shares of several requests, requests of several shares, more shares than tiles; a capacity above the lengths.
+    (Nq = 9: the 36 query rows of a K/V head take two tiles.)"""
+    case = make([1, 640, 0, 129, 0], Nq, 8, 2, 128, 16, seed=3)
+    check(case, shares=shares)
+    check(case, shares=shares, L=656)
+
+
+def test_rising_scores():
+    """Keys whose scores grow tile by tile: the reference moves again and again, in every way that it can."""
+    for up in (0.5, 2.0, 40.0):
+        q, (kc, ks), (vc, vs), table, lens = make([1000], 1, 8, 2, 128, 16, seed=4)
+        q = torch.ones_like(q)
+        for j in range(63):
+            kc[table[0, j]] = serving._encode(np.full((2, 16, 128), 1.0))
+            ks[table[0, j]] = 2.0 ** -6 * (j // 8 * up + (j % 3) * 0.25)
+        check((q, (kc, ks), (vc, vs), table, lens), shares=1)
+        vs[table[0, :63]] = 2.0 ** np.arange(-31, 32)[:, None]          # and the value scales with them
+        check((q, (kc, ks), (vc, vs), table, lens), shares=1)
+        vs[table[0, :63]] = 2.0 ** np.arange(31, -32, -1)[:, None]
+        check((q, (kc, ks), (vc, vs), table, lens), shares=2)
 
 
 def test_large_and_small_values():
@@ -168,7 +185,7 @@ def test_bad_tables_and_lengths_are_reported():
 def test_a_captured_call_follows_the_lengths():
     case = make([700, 300], 1, 8, 2, 128, 16, seed=7)
     a = dev(case)
-    ws = torch.empty(_lib.load().fa_decode_kv8_workspace_bytes(2, 1, 8, 128, 64), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(_lib.load().fa_decode_kv8_workspace_bytes(2, 1, 8, 2, 128, 304), dtype=torch.uint8, device="cuda")
     ops.decode_kv8(*a, 700, workspace=ws)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
