@@ -15,14 +15,15 @@
 // own:  q = 2^k (q1 + q2 / 16) exactly (a bf16 has 8 significant bits, an e4m3
 // 4) for what is within 2^13 of the row's largest, and to 2^-22 of the largest
 // below;  p = p1 + p2 / 16 + p3 / 256 to 2^-12 of itself, or, far below the
-// largest, to 2^-22 of that.  Page scales are one factor per key: k_scale
+// largest, to 2^-24 of that.  Page scales are one factor per key: k_scale
 // joins the score, v_scale the probability.
 //
-// O stays in TMEM over the tiles.  It is made against a reference score per
-// row and a reference value scale, at which a probability is 16: the reference
-// moves only when one would pass e4m3's 448 (2^4.8 times the largest at the
+// O stays in TMEM over the tiles.  It is made against a reference per row, in
+// log2 units of probability times value scale, at which p = 64: the reference
+// moves only when a p would pass e4m3's 448 (2^2.8 times the largest at the
 // reference's making), and O is rescaled then.  A tile costs a vote of the four
-// softmax warps on that, and no exchange of maxima.
+// softmax warps on that, and no exchange of maxima.  The row sums share the
+// reference; fp32 holds them over the whole range of value scales.
 //
 // Work: the tiles of 128 keys of all (request, K/V head, row tile) units in
 // one list, dealt in equal shares to the CTAs (two per SM), which balances
@@ -48,8 +49,9 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 192;
-constexpr float kAtRef = 16.f;       // a probability at the reference
-constexpr float kHeadroom = 4.8f;    // log2(448 / 16), rounded down
+constexpr float kAtRef = 64.f;       // p at the reference
+constexpr float kHeadroom = 2.8f;    // log2(448 / 64), rounded down
+constexpr float kLeastScale = -100.f;  // log2 of a value scale, from below: a page of zeros counts as one of 2^-100
 constexpr float kNoRef = -3.0e38f;   // reference of a row that has seen no key
 
 template <int D, int RT>
@@ -62,8 +64,8 @@ struct Layout {
   static constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;  // TMEM columns, two CTAs' 512 at most
   static constexpr uint32_t kPOff = kSlots * kSlot;
   static constexpr uint32_t kQOff = kPOff + kNP * 128u;
-  static constexpr uint32_t kScOff = kQOff + kNS * (uint32_t)D;              // per V slot: 8 key scales, 8 value scales, their largest
-  static constexpr uint32_t kScBytes = 80;
+  static constexpr uint32_t kScOff = kQOff + kNS * (uint32_t)D;              // per V slot: 8 key scales, 8 value scales
+  static constexpr uint32_t kScBytes = 64;
   static constexpr uint32_t kMaxOff = kScOff + kSlots / 2 * kScBytes;        // [4][RT] warps' maxima, [4][RT] sums
   static constexpr uint32_t kRowOff = kMaxOff + 2 * 4 * RT * 4;                  // two of: [RT] query scales, [RT] positions
   static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // [2][4] votes, scan, start
@@ -296,14 +298,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (use > 0) ok = mbar_wait(EMPTY(slot), (use - 1) & 1, w, 51);
           if (!__all_sync(0xffffffffu, ok)) break;
           if (v == 1) {
-            float mv = vs;
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
             if ((lane >> 3) == i) {
               float* sc = reinterpret_cast<float*>(sb + L::kScOff + (slot >> 1) * L::kScBytes);
               sc[lane & 7] = ks;
               sc[8 + (lane & 7)] = vs;
-              if ((lane & 7) == 0) sc[16] = mv;
             }
             __syncwarp();
           }
@@ -456,7 +454,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int rows = rows_of(pc);
       ok = __all_sync(0xffffffffu, mbar_wait(QB, piece & 1, w, 56));
       float ref[RT], l[RT];
-      float vref = 0.f, to_ref = 0.f;  // value scale at the reference; kAtRef over it
 #pragma unroll
       for (int r = 0; r < RT; ++r) ref[r] = kNoRef, l[r] = 0.f;
 
@@ -468,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!ok) break;
         tc_fence_after();
         const float* sc = reinterpret_cast<const float*>(sb + L::kScOff + (vslot >> 1) * L::kScBytes);
-        const float ks = sc[chunk], vs = sc[8 + chunk], mv = sc[16];
+        const float ks = sc[chunk], vs = sc[8 + chunk], lvs = fmaxf(__log2f(vs), kLeastScale);
         const int j0 = pc.beg + t * kKv8Tile, j = j0 + key;
         // some row does not see some key of the tile
         const bool partial = j0 + kKv8Tile > pc.len - p.Nq + 1 || (p.win_left >= 0 && j0 < pc.len - 1 - p.win_left);
@@ -507,27 +504,25 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         };
         scores(false);
-        // ---- does any probability pass what e4m3 holds, or the value scale leave zero?
+        // ---- does any p pass what e4m3 holds?
         float top = s[0];
 #pragma unroll
         for (int r = 1; r < RT; ++r) top = fmaxf(top, s[r]);
-        const float limit = fminf(kHeadroom - __log2f(vs * to_ref * (1.f / kAtRef)), 60.f);
-        const bool move = __any_sync(0xffffffffu, top > limit) || (vref == 0.f && mv > 0.f);
+        const bool move = __any_sync(0xffffffffu, top > kHeadroom - lvs);
         if (lane == 0) s_vote[(it & 1) * 4 + warp] = move;
         ok = exchange();
         if (!ok) break;
         const int4 votes = *reinterpret_cast<const int4*>(s_vote + (it & 1) * 4);
         const bool moved = (votes.x | votes.y | votes.z | votes.w) != 0;
-        if (moved) {  // ---- new references: the largest scores up to here
+        if (moved) {  // ---- new references: the largest up to here
           scores(true);
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
-            const float x = warp_max(s[r]);
+            const float x = warp_max(s[r] + lvs);
             if (lane == 0) s_max[warp * RT + r] = x;
           }
           ok = exchange();
           if (!ok) break;
-          const float v_new = fmaxf(vref, mv), v_ratio = v_new > 0.f ? vref / v_new : 0.f;
           float al[RT];
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
@@ -537,10 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             s[r] -= now;
             l[r] *= al[r];
             ref[r] = now;
-            al[r] *= v_ratio;
           }
-          vref = v_new;
-          to_ref = vref > 0.f ? kAtRef / vref : 0.f;
           if (t > pc.t0) {  // O stands at the old ones
             ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 62));
             if (!ok) break;
@@ -562,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 57));
           if (!ok) break;
         }
-        const float vn = vs * to_ref;
+        const float vn = vs * kAtRef;
 #pragma unroll
         for (int r = 0; r < RT; r += 2) {
           const float p0 = ex2_sfu(s[r]), p1 = ex2_sfu(s[r + 1]);
@@ -622,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const float sum = s_sum[r] + s_sum[RT + r] + s_sum[2 * RT + r] + s_sum[3 * RT + r];
             const float y = fmaf(fmaf(__uint_as_float(o3[x]), 0.0625f, __uint_as_float(o2[x])), 0.0625f, __uint_as_float(o1[x]));
             // sum = 0: the row sees none of these keys (a NaN passes through both)
-            const float val = sum == 0.f ? 0.f : y * (vref * (1.f / kAtRef)) / sum;
+            const float val = sum == 0.f ? 0.f : y * (1.f / kAtRef) / sum;
             const float lse2 = sum == 0.f ? -INFINITY : ref[r] + __log2f(sum);
             if (whole) {
               int i, h;

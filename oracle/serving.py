@@ -135,13 +135,14 @@ def kv8_values(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
 
 
 def decode_kv8(q: np.ndarray, codes_k, codes_v, scales_k, scales_v, table, lens, window_left: int, scale: float):
-    """q [B, Nq, Hq, d] -> (o, lse [B, Hq, Nq], a): float64; a = sum_j P_j |v_j|, the
-    size that errors of P are measured against."""
+    """q [B, Nq, Hq, d] -> (o, lse [B, Hq, Nq], a, f): float64; a = sum_j P_j |v_j|, the
+    size that relative errors of P are measured against, and
+    f = max_j (P_j vs_j) sum_j |v8_j|, that of errors of P vs relative to its largest."""
     q = np.asarray(q, np.float64)
     B, Nq, Hq, d = q.shape
     Hkv, P = codes_k.shape[1], codes_k.shape[2]
     g = Hq // Hkv
-    o, a = np.zeros(q.shape), np.zeros(q.shape)
+    o, a, f = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
     lse = np.full((B, Hq, Nq), NEG_INF)
     for b in range(B):
         n = int(lens[b])
@@ -149,6 +150,8 @@ def decode_kv8(q: np.ndarray, codes_k, codes_v, scales_k, scales_v, table, lens,
             at = [(int(table[b, j // P]), j % P) for j in range(n)]
             k = np.array([e4m3_decode(codes_k[p, h, t]) * float(scales_k[p, h]) for p, t in at]).reshape(n, d)
             v = np.array([e4m3_decode(codes_v[p, h, t]) * float(scales_v[p, h]) for p, t in at]).reshape(n, d)
+            vs = np.array([float(scales_v[p, h]) for p, t in at])
+            v8 = np.array([np.abs(e4m3_decode(codes_v[p, h, t])) for p, t in at]).reshape(n, d)
             for i in range(Nq):
                 pos = n - Nq + i
                 lo = max(0, pos - window_left) if window_left >= 0 else 0
@@ -162,4 +165,5 @@ def decode_kv8(q: np.ndarray, codes_k, codes_v, scales_k, scales_v, table, lens,
                     w /= w.sum()
                     o[b, i, hq] = w @ v[lo:pos + 1]
                     a[b, i, hq] = w @ np.abs(v[lo:pos + 1])
-    return o, lse, a
+                    f[b, i, hq] = (w * vs[lo:pos + 1]).max() * v8[lo:pos + 1].sum(0)
+    return o, lse, a, f

@@ -1,11 +1,18 @@
 """fa_decode_kv8 against the reference attention over the dequantised cache.
 
-Tolerances, with A = sum_j P_j |v_j| (element by element):
-  O   : half a bf16 step of the result, 2^-8 |O|, plus 2^-11 A for what comes
-        before it.  The products are exact in the tensor cores' inputs but for
-        P, held to 2^-12 of itself or better; scores and sums are fp32: with
-        |s| <= 2^6 a score is off by a few 2^-24 * 2^6 = 2^-18, its exponential
-        by as much of itself.
+Tolerances, with A = sum_j P_j |v_j| and F = max_j (P_j vs_j) sum_j |v8_j|
+(element by element; v8 the codes' values, vs their scales):
+  O   : half a bf16 step of the result, 2^-8 |O|, plus 2^-11 A + 2^-24 F for
+        what comes before it.  The products are exact in the tensor cores'
+        inputs but for P vs, which is held as the sum of three e4m3 numbers 16
+        times apart, at a scale where a row's largest is 64 or more.  Each part
+        leaves half a step of itself, 2^-4, to the next: 2^-12 of P vs, as long
+        as the last part is in e4m3's normal range.  Below it the last part's
+        step is 2^-9, half of it over 256 is 2^-18, and against the largest's
+        64, 2^-24 of max_j (P_j vs_j), for each key's |v8|: that is 2^-24 F (it
+        shows where the row's loudest key is nearly zero in one channel, so that
+        A is small there).  Scores and sums are fp32: with |s| <= 2^6 a score is
+        off by a few 2^-24 * 2^6 = 2^-18, its exponential by as much of itself.
   lse : 2^-13 absolute: the score error above, the fp32 logarithm and sum.
 """
 import math
@@ -62,11 +69,11 @@ def dev(case):
 
 
 def assert_close(o, lse, ref):
-    o_ref, l_ref, a = ref
+    o_ref, l_ref, a, f = ref
     o, lse = synth.to_f64(o), lse.cpu().numpy()
     assert np.all(np.isfinite(o))
     err = np.abs(o - o_ref)
-    tol = 2.0 ** -8 * np.abs(o_ref) + 2.0 ** -11 * a
+    tol = 2.0 ** -8 * np.abs(o_ref) + 2.0 ** -11 * a + 2.0 ** -24 * f
     assert np.all(err <= tol), float((err - tol).max())
     none = np.isneginf(l_ref)
     assert np.array_equal(none, np.isneginf(lse))
@@ -155,6 +162,20 @@ def test_pages_of_zeros_and_one_loud_page():
     vc[table[0, :13]], vs[table[0, :13]] = 0, 0.0  # no values at all
     o, lse = check((q, (kc, ks), (vc, vs), table, lens))
     assert torch.all(o == 0) and torch.isfinite(lse).all()
+
+
+def test_a_loud_page_that_hardly_counts():
+    """Values 2^40 times the others' in a page whose keys score 2^-60 of theirs: the quiet pages' average, to the
+    same precision."""
+    q, (kc, ks), (vc, vs), table, lens = make([400], 1, 4, 2, 128, 16, seed=6)
+    q = torch.ones_like(q)
+    for j in (0, 9, 24):
+        kc[table[0, j]] = serving._encode(np.full((2, 16, 128), -1.0))
+        ks[table[0, j]] = 0.75 * 128 ** -0.5 * 8      # scores of -68: e^-68 = 2^-98
+        vs[table[0, j]] *= 2.0 ** 40
+    check((q, (kc, ks), (vc, vs), table, lens), shares=2)
+    o, _ = check((q, (kc, ks), (vc, vs), table, lens), shares=5)
+    assert float(o.float().abs().max()) < 100
 
 
 def test_equal_keys_average_the_values():

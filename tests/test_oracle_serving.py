@@ -108,16 +108,16 @@ def test_attention_equals_the_plain_one():
     scales = (2.0 ** rng.integers(-12, -6, (2, 4, Hkv))).astype(np.float32)
     table = np.array([[3, 1, 0]])
     q = rng.standard_normal((1, 1, Hkv * g, d))
-    o, lse, a = serving.decode_kv8(q, codes[0], codes[1], scales[0], scales[1], table, [n], -1, 0.3)
+    o, lse, a, f = serving.decode_kv8(q, codes[0], codes[1], scales[0], scales[1], table, [n], -1, 0.3)
     k, v = (serving.kv8_values(codes[i], scales[i])[table[0]].transpose(0, 2, 1, 3).reshape(1, -1, Hkv, d)[:, :n]
             for i in (0, 1))
     o2, lse2 = oracle.gqa_decode_forward(q, k, v, 0.3)
-    assert np.allclose(o, o2) and np.allclose(lse[:, :, 0], lse2) and np.all(a >= np.abs(o) - 1e-12)
+    assert np.allclose(o, o2) and np.allclose(lse[:, :, 0], lse2) and np.all(a >= np.abs(o) - 1e-12) and np.all(f >= a / n)
     # four queries, a window: the masked oracle's bottom-right alignment
     q = rng.standard_normal((1, 4, Hkv * g, d))
-    o, lse, _ = serving.decode_kv8(q, codes[0], codes[1], scales[0], scales[1], table, [n], 5, 0.3)
+    o, lse, _, _ = serving.decode_kv8(q, codes[0], codes[1], scales[0], scales[1], table, [n], 5, 0.3)
     o2, lse2 = oracle.masked_forward(q, k, v, 0.3, 5, 0)
     assert np.allclose(o, o2) and np.allclose(lse, lse2)
     # more queries than keys: the first see nothing
-    o, lse, _ = serving.decode_kv8(q, codes[0], codes[1], scales[0], scales[1], table, [2], -1, 0.3)
+    o, lse, _, _ = serving.decode_kv8(q, codes[0], codes[1], scales[0], scales[1], table, [2], -1, 0.3)
     assert np.all(o[0, :2] == 0) and np.all(lse[0, :, :2] == -np.inf) and np.all(np.isfinite(lse[0, :, 2:]))
