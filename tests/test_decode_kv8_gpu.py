@@ -165,13 +165,13 @@ def test_pages_of_zeros_and_one_loud_page():
 
 
 def test_a_loud_page_that_hardly_counts():
-    """Values 2^40 times the others' in a page whose keys score 2^-60 of theirs: the quiet pages' average, to the
+    """Values 2^40 times the others' in pages whose keys weigh 2^-98 of theirs: the quiet pages' average, to the
     same precision."""
     q, (kc, ks), (vc, vs), table, lens = make([400], 1, 4, 2, 128, 16, seed=6)
     q = torch.ones_like(q)
     for j in (0, 9, 24):
         kc[table[0, j]] = serving._encode(np.full((2, 16, 128), -1.0))
-        ks[table[0, j]] = 0.75 * 128 ** -0.5 * 8      # scores of -68: e^-68 = 2^-98
+        ks[table[0, j]] = 68 * 128 ** -0.5            # scores of -68: e^-68 = 2^-98
         vs[table[0, j]] *= 2.0 ** 40
     check((q, (kc, ks), (vc, vs), table, lens), shares=2)
     o, _ = check((q, (kc, ks), (vc, vs), table, lens), shares=5)
