@@ -57,7 +57,10 @@ constexpr float kNoRef = -3.0e38f;   // reference of a row that has seen no key
 template <int D, int RT>
 struct Layout {
   static constexpr uint32_t kSlot = 128u * D;                                // a tile of K or V
-  static constexpr int kSlots = (RT == 32 ? 4 : 6) * (128 / D);              // ring: K0 V0 K1 V1 ...
+  // CTAs per SM.  A tile costs a CTA about 1.1 us whatever its bytes, so the
+  // half-size tiles of d = 64 want three at once where registers allow it.
+  static constexpr int kCtas = D == 64 && RT <= 8 ? 3 : 2;
+  static constexpr int kSlots = D == 64 ? (kCtas == 3 ? 8 : RT == 32 ? 8 : 12) : RT == 32 ? 4 : 6;  // ring: K0 V0 K1 V1 ...
   static constexpr int kNS = 2 * RT < 16 ? 16 : 2 * RT;                      // columns of S
   static constexpr int kNP = (3 * RT + 15) / 16 * 16;                        // columns of P and O
   static constexpr uint32_t kUsed = 2 * kNS + kNP;
@@ -66,8 +69,8 @@ struct Layout {
   static constexpr uint32_t kQOff = kPOff + kNP * 128u;
   static constexpr uint32_t kScOff = kQOff + kNS * (uint32_t)D;              // per V slot: 8 key scales, 8 value scales
   static constexpr uint32_t kScBytes = 64;
-  static constexpr uint32_t kMaxOff = kScOff + kSlots / 2 * kScBytes;        // [4][RT] warps' maxima, [4][RT] sums
-  static constexpr uint32_t kRowOff = kMaxOff + 2 * 4 * RT * 4;                  // two of: [RT] query scales, [RT] positions
+  static constexpr uint32_t kMaxOff = kScOff + kSlots / 2 * kScBytes;        // [4][RT] each: warps' maxima, sums, references, factors
+  static constexpr uint32_t kRowOff = kMaxOff + (16 + 8) * RT * 4;           // (and [4][RT] output rows, 8 bytes each) two of: [RT] query scales, [RT] positions
   static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // [2][4] votes, scan, start
   static constexpr uint32_t kBarOff = kMiscOff + 128;
   static constexpr uint32_t kBytes = kBarOff + 8 * (2 * kSlots + 6) + 16 + 1024;
@@ -94,9 +97,14 @@ __device__ __forceinline__ int kv8_tiles(const Kv8DecodeParams& p, int len) {
   return (len - kv8_begin(p, len) + kKv8Tile - 1) / kKv8Tile;
 }
 
+// a / b for a >= 0, b > 0, in 32 bits where both fit (a 64-bit division takes some hundred instructions)
+__host__ __device__ __forceinline__ long long quick_div(long long a, long long b) {
+  return (((unsigned long long)a | (unsigned long long)b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // First tile of a CTA's share.
 __host__ __device__ __forceinline__ long long share_begin(long long total, int shares, int k) {
-  const long long each = total / shares, more = total - each * shares;  // the first `more` shares have one tile more
+  const long long each = quick_div(total, shares), more = total - each * shares;  // the first `more` shares have one tile more
   return each * k + (k < more ? k : more);
 }
 
@@ -120,7 +128,7 @@ struct Walk {
       tiles = kv8_tiles(p, len);
     }
     s.b = b;
-    s.u = (int)(off / tiles);
+    s.u = (int)quick_div(off, tiles);
     s.t0 = (int)(off - (long long)s.u * tiles);
     s.t1 = (int)(left < tiles - s.t0 ? s.t0 + left : tiles);
     s.tiles = tiles;
@@ -146,6 +154,37 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r) {
   }
 }
 
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t* r) {
+  if constexpr (N >= 8) {
+    tmem_st8(addr, r);
+    if constexpr (N > 8) tmem_store<N - 8>(addr + 8, r + 8);
+  } else if constexpr (N > 0) {
+    static_assert(N == 4, "columns in fours");
+    tmem_st4(addr, r);
+  }
+}
+
+// Sums v[r] of the warp's lanes for every r: lane r * (32 / RT) gets the total
+// of row r.  Halves the rows while it adds (31 shuffles for 32 rows, not 160).
+template <int RT>
+__device__ __forceinline__ float warp_row_sums(float (&v)[RT], int lane) {
+  int o = 16;
+#pragma unroll
+  for (int n = RT / 2; n > 0; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? v[i] : v[i + n];
+      v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (int b = 16 / RT; b > 0; b >>= 1) x += __shfl_xor_sync(0xffffffffu, x, b);
+  return x;
+}
+
 __device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -153,7 +192,7 @@ __device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
 }  // namespace
 
 template <int D, int RT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     fa_decode_kv8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ Kv8DecodeParams p) {
   using L = Layout<D, RT>;
@@ -241,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (to > from) walk = {to - from, s_start[1], (int)s_start[0], (int)(s_start[2] >> 32), (int)(s_start[2] & 0xffffffffll)};
   Piece pc;
   bool ok = true;
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge may be set up; it waits for this grid's end
 
   if (warp == 4) {
     // ============================================================ producer
@@ -368,6 +408,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ============================================================ softmax
     float* s_max = reinterpret_cast<float*>(sb + L::kMaxOff);
     float* s_sum = s_max + 4 * RT;
+    float* my_ref = s_max + (8 + warp) * RT;   // this warp's copies: the rows' references,
+    float* my_al = s_max + (12 + warp) * RT;   //   and what a moved one multiplies sums by
     const uint32_t lane_sel = (uint32_t)warp << 21;  // TMEM lane 32 * warp
     const int key = warp * 32 + lane;                // key of the tile
     const uint32_t p_at = base + L::kPOff + (key & 15);  // this thread's byte in P's 128-byte rows
@@ -376,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     // row r of a piece: its row of q and o, its query token
     auto q_row = [&](const Piece& s, int r, int& i, int& h) {
       const int x = s.u % p.row_tiles * RT + r;
-      i = x / p.group;
-      h = s.u / p.row_tiles * p.group + x - i * p.group;
+      i = p.Nq == 1 ? 0 : (int)((unsigned)x / (unsigned)p.group);
+      h = (int)((unsigned)s.u / (unsigned)p.row_tiles) * p.group + x - i * p.group;
       return ((size_t)s.b * p.Nq + i) * p.Hq + h;
     };
     // ---- Q: a warp per row, split into two e4m3 parts at the row's power of two
@@ -385,53 +427,61 @@ __global__ void __launch_bounds__(kThreads, 2)
       float* s_qsc = reinterpret_cast<float*>(sb + L::kRowOff + (piece & 1) * 2 * RT * 4);
       int* s_pos = reinterpret_cast<int*>(s_qsc + RT);
       const int rows = rows_of(s);
-      constexpr int E = D / 32;
-      for (int r = warp; r < RT; r += 4) {
-        float q[E];
-        float mx = 0.f;
-        bool odd = false;  // an infinity or a NaN in the row
+      constexpr int LPR = D / 8, RPW = 32 / LPR;                // lanes per row, rows per warp and pass
+      constexpr int PASSES = (RT + 4 * RPW - 1) / (4 * RPW);
+      const int sub = lane / LPR, seg = lane % LPR;
+      uint4 q[PASSES];
+      int pos[PASSES];
+#pragma unroll
+      for (int x = 0; x < PASSES; ++x) {
+        const int r = (x * 4 + warp) * RPW + sub;
+        q[x] = make_uint4(0u, 0u, 0u, 0u);
         int i = 0, h;
+        if (r < rows) q[x] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + q_row(s, r, i, h) * D + seg * 8);
+        pos[x] = s.len - p.Nq + i;
+      }
 #pragma unroll
-        for (int e = 0; e < E; ++e) q[e] = 0.f;
-        if (r < rows) {
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + q_row(s, r, i, h) * D + lane * E;
+      for (int x = 0; x < PASSES; ++x) {
+        const int r = (x * 4 + warp) * RPW + sub;
+        const uint32_t wd[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
+        float f[8], mx = 0.f;
 #pragma unroll
-          for (int e = 0; e < E; ++e) q[e] = __bfloat162float(src[e]);
+        for (int e = 0; e < 8; ++e) {
+          f[e] = __uint_as_float(e & 1 ? wd[e / 2] & 0xffff0000u : wd[e / 2] << 16);
+          mx = fmaxf(mx, fabsf(f[e]));
         }
+        bool odd = false;  // an infinity or a NaN in the row
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          odd |= !(fabsf(q[e]) <= 3.4e38f);
-          mx = fmaxf(mx, fabsf(q[e]));
-        }
-        mx = fminf(warp_max(mx), 3.39e38f);
-        odd = __any_sync(0xffffffffu, odd);
+        for (int e = 0; e < 8; ++e) odd |= !(fabsf(f[e]) <= 3.4e38f);
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = fminf(mx, 3.39e38f);
+        odd = (__ballot_sync(0xffffffffu, odd) >> (sub * LPR) & ((1u << LPR) - 1u)) != 0;
         // 2^k with mx / 2^k in [128, 256)
         const int ex = max((int)(__float_as_uint(mx) >> 23) - 7, 1);  // biased exponent of 2^k
         const float inv = mx > 0.f ? __uint_as_float((uint32_t)(254 - ex) << 23) : 1.f;
         const float sc = mx > 0.f ? __uint_as_float((uint32_t)ex << 23) : 1.f;
-        uint32_t c1[E / 2], c2[E / 2];
+        uint32_t c1[4], c2[4];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float x = odd ? __uint_as_float(0x7fffffffu) : q[e] * inv, y = odd ? __uint_as_float(0x7fffffffu) : q[e + 1] * inv;
-          c1[e / 2] = pack_e4m3x2(x, y);
-          const float2 f = unpack_e4m3x2(c1[e / 2]);
-          c2[e / 2] = pack_e4m3x2((x - f.x) * 16.f, (y - f.y) * 16.f);
+        for (int e = 0; e < 4; ++e) {
+          const float y = odd ? __uint_as_float(0x7fffffffu) : f[2 * e] * inv;
+          const float z = odd ? __uint_as_float(0x7fffffffu) : f[2 * e + 1] * inv;
+          c1[e] = pack_e4m3x2(y, z);
+          const float2 g = unpack_e4m3x2(c1[e]);
+          c2[e] = pack_e4m3x2((y - g.x) * 16.f, (z - g.y) * 16.f);
         }
+        if (r < RT) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const int col = part * RT + r;
-          if constexpr (D == 128) {
-            const uint32_t v = part ? (c2[0] | c2[1] << 16) : (c1[0] | c1[1] << 16);
-            *reinterpret_cast<uint32_t*>(sb + L::kQOff + col * 128 + (((lane >> 2) ^ (col & 7)) << 4) + (lane & 3) * 4) = v;
-          } else {
-            const uint32_t v = part ? c2[0] : c1[0];
-            *reinterpret_cast<uint16_t*>(sb + L::kQOff + col * 64 + (((lane >> 3) ^ ((col >> 1) & 3)) << 4) + (lane & 7) * 2) =
-                (uint16_t)v;
+          for (int part = 0; part < 2; ++part) {
+            const int col = part * RT + r;
+            const uint32_t* c = part ? c2 : c1;
+            const uint32_t at = D == 128 ? col * 128 + (((seg >> 1) ^ (col & 7)) << 4) : col * 64 + (((seg >> 1) ^ ((col >> 1) & 3)) << 4);
+            *reinterpret_cast<uint2*>(sb + L::kQOff + at + (seg & 1) * 8) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
           }
-        }
-        if (lane == 0) {
-          s_qsc[r] = sc * p.scale_log2;
-          s_pos[r] = s.len - p.Nq + i;
+          if (seg == 0) {
+            s_qsc[r] = sc * p.scale_log2;
+            s_pos[r] = pos[x];
+          }
         }
       }
       fence_proxy_async_smem();
@@ -453,9 +503,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int* s_pos = reinterpret_cast<const int*>(s_qsc + RT);
       const int rows = rows_of(pc);
       ok = __all_sync(0xffffffffu, mbar_wait(QB, piece & 1, w, 56));
-      float ref[RT], l[RT];
+      float l[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) ref[r] = kNoRef, l[r] = 0.f;
+      for (int r = 0; r < RT; ++r) l[r] = 0.f;
+      __syncwarp();
+      if (lane < RT) my_ref[lane] = kNoRef;
+      __syncwarp();
 
       for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
         const int vslot = (2 * it + 1) % NSL;
@@ -479,9 +532,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int e = 0; e < D / 16; ++e) row[e] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        // scores less the references (or, on the slow path, less nothing), in log2 units
+        auto sees = [&](int r) { return j <= s_pos[r] && (p.win_left < 0 || j >= s_pos[r] - p.win_left); };
         float s[RT];
-        auto scores = [&](bool plain) {
+        for (bool settled = false;;) {
+          // ---- scores less the references, in log2 units
           constexpr int H = RT > 16 ? 16 : RT;  // rows per load
 #pragma unroll
           for (int h = 0; h < RT; h += H) {
@@ -492,63 +546,75 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int r = 0; r < H; ++r) {
               const float x = fmaf(__uint_as_float(s2[r]), 0.0625f, __uint_as_float(s1[r]));
-              s[h + r] = fmaf(x, ks * s_qsc[h + r], plain ? 0.f : -ref[h + r]);
+              s[h + r] = fmaf(x, ks * s_qsc[h + r], -my_ref[h + r]);
             }
           }
           if (partial) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              const int pos = s_pos[r];
-              if (!(j <= pos && (p.win_left < 0 || j >= pos - p.win_left))) s[r] = -INFINITY;
-            }
+            for (int r = 0; r < RT; ++r) s[r] = sees(r) ? s[r] : -INFINITY;
           }
-        };
-        scores(false);
-        // ---- does any p pass what e4m3 holds?
-        float top = s[0];
+          if (settled) break;
+          // ---- does any p pass what e4m3 holds?
+          float top = s[0];
 #pragma unroll
-        for (int r = 1; r < RT; ++r) top = fmaxf(top, s[r]);
-        const bool move = __any_sync(0xffffffffu, top > kHeadroom - lvs);
-        if (lane == 0) s_vote[(it & 1) * 4 + warp] = move;
-        ok = exchange();
-        if (!ok) break;
-        const int4 votes = *reinterpret_cast<const int4*>(s_vote + (it & 1) * 4);
-        const bool moved = (votes.x | votes.y | votes.z | votes.w) != 0;
-        if (moved) {  // ---- new references: the largest up to here
-          scores(true);
+          for (int r = 1; r < RT; ++r) top = fmaxf(top, s[r]);
+          const bool move = __any_sync(0xffffffffu, top > kHeadroom - lvs);
+          if (lane == 0) s_vote[(it & 1) * 4 + warp] = move;
+          ok = exchange();
+          if (!ok) break;
+          const int4 votes = *reinterpret_cast<const int4*>(s_vote + (it & 1) * 4);
+          if ((votes.x | votes.y | votes.z | votes.w) == 0) break;
+          // ---- new references: the largest up to here (rolled loops: rare, and the code is long already)
+          constexpr int G = RT > 8 ? 8 : RT;  // rows at a time
+#pragma unroll 1
+          for (int r = 0; r < RT; r += G) {
+            uint32_t s1[G], s2[G];
+            tmem_load<G>(tS + (it & 1) * L::kNS + lane_sel + r, s1);
+            tmem_load<G>(tS + (it & 1) * L::kNS + lane_sel + RT + r, s2);
+            tmem_ld_wait();
+            float x[G];
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const float x = warp_max(s[r] + lvs);
-            if (lane == 0) s_max[warp * RT + r] = x;
+            for (int e = 0; e < G; ++e) {
+              x[e] = fmaf(__uint_as_float(s2[e]), 0.0625f, __uint_as_float(s1[e])) * (ks * s_qsc[r + e]) + lvs;
+              if (partial && !sees(r + e)) x[e] = -INFINITY;
+              x[e] = warp_max(x[e]);
+            }
+            if (lane == 0) {
+#pragma unroll
+              for (int e = 0; e < G; e += 4)
+                *reinterpret_cast<float4*>(s_max + warp * RT + r + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            }
           }
           ok = exchange();
           if (!ok) break;
-          float al[RT];
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const float x = fmaxf(fmaxf(s_max[r], s_max[RT + r]), fmaxf(s_max[2 * RT + r], s_max[3 * RT + r]));
-            const float now = fmaxf(ref[r], x);  // (a row that sees no key yet has -inf here and keeps its reference)
-            al[r] = ex2_sfu(ref[r] - now);
-            s[r] -= now;
-            l[r] *= al[r];
-            ref[r] = now;
+          if (lane < RT) {
+            const float x = fmaxf(fmaxf(s_max[lane], s_max[RT + lane]), fmaxf(s_max[2 * RT + lane], s_max[3 * RT + lane]));
+            const float old = my_ref[lane], now = fmaxf(old, x);  // (a row that sees no key yet has -inf in x)
+            my_ref[lane] = now;
+            my_al[lane] = ex2_sfu(old - now);
           }
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < RT; ++r) l[r] *= my_al[r];
           if (t > pc.t0) {  // O stands at the old ones
             ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 62));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int h = 0; h < 3 * RT; h += 4) {
-              uint32_t o[4];
-              tmem_ld4(tO + lane_sel + h, o);
+            constexpr int H = RT > 16 ? 16 : RT;  // columns at a time
+#pragma unroll 1
+            for (int h = 0; h < 3 * RT; h += H) {
+              uint32_t o[H];
+              tmem_load<H>(tO + lane_sel + h, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al[(h + e) % RT]);
-              tmem_st4(tO + lane_sel + h, o);
+              for (int e = 0; e < H; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * my_al[h % RT + e]);
+              tmem_store<H>(tO + lane_sel + h, o);
             }
             tmem_st_wait();
           }
+          settled = true;
         }
+        if (!ok) break;
         // ---- probabilities; P's buffer is free when the product before has read it
         if (t > pc.t0) {
           ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 57));
@@ -585,12 +651,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       have = walk.next(p, units, pc);
       if (have) load_q(pc, piece + 1);
       // ---- each row's sum over the 128 key lanes
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-        if (lane == 0) s_sum[warp * RT + r] = l[r];
-      }
+      const float row_sum = warp_row_sums<RT>(l, lane);
+      if (lane % (32 / RT) == 0) s_sum[warp * RT + lane / (32 / RT)] = row_sum;
       ok = exchange();
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 61));
       if (!ok) break;
@@ -599,9 +661,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int e = D == 128 ? key : warp * 16 + lane;
       const bool has = D == 128 || lane < 16;
       const bool whole = done.t0 == 0 && done.t1 == done.tiles;
-      const size_t part = 2 * (size_t)k + (piece > 0 ? 1 : 0);  // a share's first piece, or its last
-#pragma unroll
-      for (int r4 = 0; r4 < RT; r4 += 4) {
+      // lane r works out row r for its warp: where it goes, what its sums are divided by; the row's lse
+      long long* my_at = reinterpret_cast<long long*>(s_max + 16 * RT) + warp * RT;
+      if (lane < rows) {
+        const float sum = s_sum[lane] + s_sum[RT + lane] + s_sum[2 * RT + lane] + s_sum[3 * RT + lane];
+        // sum = 0: the row sees none of these keys (a NaN passes through)
+        const float lse2 = sum == 0.f ? -INFINITY : my_ref[lane] + __log2f(sum);
+        my_al[lane] = sum == 0.f ? 0.f : 1.f / (sum * kAtRef);
+        if (whole) {
+          int i, h;
+          my_at[lane] = (long long)q_row(done, lane, i, h) * D;
+          if (warp == 0) p.lse[((size_t)done.b * p.Hq + h) * p.Nq + i] = lse2 * 0.69314718055994531f;
+        } else {
+          const size_t part = 2 * (size_t)k + (piece > 0 ? 1 : 0);  // a share's first piece, or its last
+          my_at[lane] = (long long)(part * RT + lane) * D;
+          if (warp == 0) p.part_lse[part * RT + lane] = lse2;
+        }
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int r4 = 0; r4 < rows; r4 += 4) {
         uint32_t o1[4], o2[4], o3[4];
         tmem_ld4(tO + lane_sel + r4, o1);
         tmem_ld4(tO + lane_sel + RT + r4, o2);
@@ -609,22 +688,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_ld_wait();
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int r = r4 + x;
-          if (r < rows) {
-            const float sum = s_sum[r] + s_sum[RT + r] + s_sum[2 * RT + r] + s_sum[3 * RT + r];
+          if (r4 + x < rows && has) {
             const float y = fmaf(fmaf(__uint_as_float(o3[x]), 0.0625f, __uint_as_float(o2[x])), 0.0625f, __uint_as_float(o1[x]));
-            // sum = 0: the row sees none of these keys (a NaN passes through both)
-            const float val = sum == 0.f ? 0.f : y * (1.f / kAtRef) / sum;
-            const float lse2 = sum == 0.f ? -INFINITY : ref[r] + __log2f(sum);
-            if (whole) {
-              int i, h;
-              const size_t row = q_row(done, r, i, h);
-              if (has) static_cast<__nv_bfloat16*>(p.o)[row * D + e] = __float2bfloat16_rn(val);
-              if (key == 0) p.lse[((size_t)done.b * p.Hq + h) * p.Nq + i] = lse2 * 0.69314718055994531f;
-            } else {
-              if (has) p.part_o[(part * RT + r) * D + e] = val;
-              if (key == 0) p.part_lse[part * RT + r] = lse2;
-            }
+            const float f = my_al[r4 + x];
+            const float val = f == 0.f ? 0.f : y * f;  // (0 * NaN would not be 0)
+            if (whole)
+              static_cast<__nv_bfloat16*>(p.o)[my_at[r4 + x] + e] = __float2bfloat16_rn(val);
+            else
+              p.part_o[my_at[r4 + x] + e] = val;
           }
         }
       }
@@ -653,21 +724,22 @@ template <int D>
 __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_constant__ Kv8DecodeParams p, int RT,
                                                                   int shares) {
   constexpr int E = D / 32;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = lane_id();
-  if (row >= (long long)p.B * p.Nq * p.Hq) return;
-  const int h = (int)(row % p.Hq);
-  const long long bi = row / p.Hq;
-  const int i = (int)(bi % p.Nq), b = (int)(bi / p.Nq);
-  const int hk = h / p.group, x = i * p.group + h - hk * p.group;  // row of the K/V head
+  if (at >= (long long)p.B * p.Nq * p.Hq) return;
+  const unsigned per = (unsigned)(p.Nq * p.Hq);  // (at most 65535)
+  const int b = (int)(at / per), x0 = (int)(at - (long long)b * per);
+  const int i = (int)((unsigned)x0 / (unsigned)p.Hq), h = x0 - i * p.Hq;
+  const int hk = (int)((unsigned)h / (unsigned)p.group), x = i * p.group + h - hk * p.group;  // row of the K/V head
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done
   const int units = p.Hkv * p.row_tiles, u = hk * p.row_tiles + x / RT, r = x % RT;
   const long long total = p.first_tile[p.B], first = p.first_tile[b];
-  const long long tiles = (p.first_tile[b + 1] - first) / units, u0 = first + u * tiles, u1 = u0 + tiles;
+  const long long tiles = quick_div(p.first_tile[b + 1] - first, units), u0 = first + u * tiles, u1 = u0 + tiles;
   int ka = 0, kb = -1;
   if (tiles > 0) {
-    const long long each = total / shares, more = total - each * shares;
+    const long long each = quick_div(total, shares), more = total - each * shares;
     auto share_of = [&](long long t) {
-      return (int)(t < more * (each + 1) ? t / (each + 1) : more + (t - more * (each + 1)) / each);
+      return (int)(t < more * (each + 1) ? quick_div(t, each + 1) : more + quick_div(t - more * (each + 1), each));
     };
     ka = share_of(u0);
     kb = share_of(u1 - 1);
@@ -681,16 +753,16 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int k = ka; k <= kb; ++k) {
-    const long long at = slot_of(k);
-    const float lc = p.part_lse[at];
+    const long long sl = slot_of(k);
+    const float lc = p.part_lse[sl];
     const float wc = lc == -INFINITY ? 0.f : ex2_sfu(lc - m);
     wsum += wc;
-    const float* src = p.part_o + at * D + lane * E;
+    const float* src = p.part_o + sl * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = fmaf(wc, src[e], acc[e]);
   }
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D + lane * E);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   if (lane == 0)
@@ -700,12 +772,13 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
 // Query rows of one CTA.
 int kv8_row_tile(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
-int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span) {
+int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span, int D) {
   int dev = 0, n_sm = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   const int rows = Nq * group, rt = kv8_row_tile(rows);
+  const int ctas = n_sm * (D == 64 && rt <= 8 ? Layout<64, 8>::kCtas : Layout<128, 8>::kCtas);
   const long long tiles = (long long)B * Hkv * ((rows + rt - 1) / rt) * (((long long)span + kKv8Tile - 1) / kKv8Tile);
-  return (int)(tiles < 1 ? 1 : tiles < 2 * n_sm ? tiles : 2 * n_sm);  // two CTAs per SM
+  return (int)(tiles < 1 ? 1 : tiles < ctas ? tiles : ctas);
 }
 
 template <int D, int RT>
@@ -713,16 +786,25 @@ static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8
                                cudaStream_t stream) {
   auto kern = fa_decode_kv8_kernel<D, RT>;
   constexpr uint32_t smem = Layout<D, RT>::kBytes;
-  static_assert(smem <= 113 * 1024, "two CTAs per SM");
+  static_assert((smem + 1024) * Layout<D, RT>::kCtas <= 228 * 1024, "CTAs per SM");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   p.row_tiles = (p.Nq * p.group + RT - 1) / RT;
   kern<<<shares, kThreads, smem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // the merge's launch overlaps the main kernel (programmatic dependent launch); its blocks wait for the grid's end
   const long long rows = (long long)p.B * p.Nq * p.Hq;
-  fa_decode_kv8_merge_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p, RT, shares);
-  return cudaGetLastError();
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_decode_kv8_merge_kernel<D>, static_cast<const Kv8DecodeParams&>(p), (int)RT, shares);
 }
 
 template <int D>

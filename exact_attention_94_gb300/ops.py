@@ -869,7 +869,7 @@ def decode_kv8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, max
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     L, wl, shares, so = int(max_seq_len), int(window_left), int(num_shares), lib()
     if shares == 0:
-        shares = so.fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, L, wl)
+        shares = so.fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, d, L, wl)
     nbytes = so.fa_decode_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, max(shares, 1))
     if workspace is None:
         workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
