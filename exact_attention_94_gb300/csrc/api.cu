@@ -920,7 +920,7 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_lse = reinterpret_cast<float*>(ws + o_bytes);
-  p.first_tile = reinterpret_cast<long long*>(ws + o_bytes + l_bytes);
+  p.first_slot = reinterpret_cast<long long*>(ws + o_bytes + l_bytes);
   p.B = B;
   p.Nq = Nq;
   p.Hq = Hq;
@@ -940,7 +940,7 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   if (!make_tmap_codes(&tk, k_codes, d, page_size, (long long)num_pages * Hkv, p.box_rows) ||
       !make_tmap_codes(&tv, v_codes, d, page_size, (long long)num_pages * Hkv, p.box_rows))
     return FA_ERR_INVALID_ARG;
-  return launch_decode_kv8(tk, tv, p, d, num_shares, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  return launch_decode_kv8(tk, tv, p, d, num_shares, kv8_span(Nq, max_seq_len, window_left), (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

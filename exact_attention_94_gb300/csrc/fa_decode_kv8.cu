@@ -27,7 +27,8 @@
 //
 // Work: the tiles of 128 keys of all (request, K/V head, row tile) units in
 // one list, dealt in equal shares to the CTAs (two per SM), which balances
-// requests of any lengths.  A unit inside one share is finished there; one that
+// requests of any lengths; a unit counts some tiles more than it has, for its
+// start and end.  A unit inside one share is finished there; one that
 // a share's border cuts leaves normalised partials, which a second kernel
 // merges: lse = log sum_c e^(lse_c), O = sum_c e^(lse_c - lse) O_c.
 //
@@ -52,6 +53,7 @@ constexpr int kThreads = 192;
 constexpr float kAtRef = 64.f;       // p at the reference
 constexpr float kHeadroom = 2.8f;    // log2(448 / 64), rounded down
 constexpr float kLeastScale = -100.f;  // log2 of a value scale, from below: a page of zeros counts as one of 2^-100
+constexpr int kLead(int RT) { return 4 + RT / 16; }  // what a unit's start and end cost, in tiles
 constexpr float kNoRef = -3.0e38f;   // reference of a row that has seen no key
 
 template <int D, int RT>
@@ -102,10 +104,16 @@ __host__ __device__ __forceinline__ long long quick_div(long long a, long long b
   return (((unsigned long long)a | (unsigned long long)b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
-// First tile of a CTA's share.
+// First slot of a CTA's share of the whole weight.
 __host__ __device__ __forceinline__ long long share_begin(long long total, int shares, int k) {
-  const long long each = quick_div(total, shares), more = total - each * shares;  // the first `more` shares have one tile more
+  const long long each = quick_div(total, shares), more = total - each * shares;  // the first `more` shares have one slot more
   return each * k + (k < more ? k : more);
+}
+
+// A unit weighs its tiles and p.lead more, what its start and end cost a CTA in
+// tiles; slot p.lead + t of its weight is tile t.
+__device__ __forceinline__ long long kv8_weight(const Kv8DecodeParams& p, int tiles) {
+  return tiles > 0 ? tiles + p.lead : 0;
 }
 
 // A piece of a share: tiles t0 .. t1 - 1 of unit u (K/V head and row tile) of request b.
@@ -115,28 +123,33 @@ struct Piece {
 
 // Walks a CTA's share piece by piece; every role walks for itself.
 struct Walk {
-  long long left;  // tiles of the share still to come
-  long long off;   // next tile within the request's units
+  long long left;  // weight of the share still to come
+  long long off;   // next slot within the weight of the request's units
   int b, tiles, len;
 
   __device__ __forceinline__ bool next(const Kv8DecodeParams& p, int units, Piece& s) {
-    if (left <= 0) return false;
-    while (off >= (long long)tiles * units) {  // the request's units are done (or it has no keys)
-      off = 0;
-      ++b;
-      len = kv8_len(p, b);
-      tiles = kv8_tiles(p, len);
+    while (left > 0) {
+      const int each = tiles + p.lead;
+      if (tiles == 0 || off >= (long long)each * units) {  // the request's units are done (or it has no keys)
+        off = 0;
+        ++b;
+        len = kv8_len(p, b);
+        tiles = kv8_tiles(p, len);
+        continue;
+      }
+      s.b = b;
+      s.u = (int)quick_div(off, each);
+      const int w0 = (int)(off - (long long)s.u * each), w1 = (int)(left < each - w0 ? w0 + left : each);
+      off += w1 - w0;
+      left -= w1 - w0;
+      s.t0 = max(w0 - p.lead, 0);
+      s.t1 = max(w1 - p.lead, 0);
+      s.tiles = tiles;
+      s.len = len;
+      s.beg = kv8_begin(p, len);
+      if (s.t0 < s.t1) return true;
     }
-    s.b = b;
-    s.u = (int)quick_div(off, tiles);
-    s.t0 = (int)(off - (long long)s.u * tiles);
-    s.t1 = (int)(left < tiles - s.t0 ? s.t0 + left : tiles);
-    s.tiles = tiles;
-    s.len = len;
-    s.beg = kv8_begin(p, len);
-    off += s.t1 - s.t0;
-    left -= s.t1 - s.t0;
-    return true;
+    return false;
   }
 };
 
@@ -230,10 +243,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  // ---- the share: tiles of all requests, thread t adding up requests t*n .. t*n + n - 1
+  // ---- the share: the weight of all requests, thread t adding up requests t*n .. t*n + n - 1
   long long mine = 0, before;
   const int n = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, (int)threadIdx.x * n), b1 = min(p.B, b0 + n);
-  for (int b = b0; b < b1; ++b) mine += (long long)kv8_tiles(p, kv8_len(p, b)) * units;
+  for (int b = b0; b < b1; ++b) mine += kv8_weight(p, kv8_tiles(p, kv8_len(p, b))) * units;
   before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -255,22 +268,22 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     long long at = before;
     for (int b = b0; b < b1; ++b) {
       const int len = kv8_len(p, b), tiles = kv8_tiles(p, len);
-      if (from < at + (long long)tiles * units) {
+      if (from < at + kv8_weight(p, tiles) * units) {
         s_start[0] = b;
         s_start[1] = from - at;
         s_start[2] = (long long)tiles << 32 | (unsigned)len;
         break;
       }
-      at += (long long)tiles * units;
+      at += kv8_weight(p, tiles) * units;
     }
   }
-  if (k == 0) {  // for the merge: the requests' first tiles
+  if (k == 0) {  // for the merge: where the requests' weights begin
     long long at = before;
     for (int b = b0; b < b1; ++b) {
-      p.first_tile[b] = at;
-      at += (long long)kv8_tiles(p, kv8_len(p, b)) * units;
+      p.first_slot[b] = at;
+      at += kv8_weight(p, kv8_tiles(p, kv8_len(p, b))) * units;
     }
-    if (threadIdx.x == 0) p.first_tile[p.B] = total;
+    if (threadIdx.x == 0) p.first_slot[p.B] = total;
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
@@ -733,16 +746,16 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
   const int hk = (int)((unsigned)h / (unsigned)p.group), x = i * p.group + h - hk * p.group;  // row of the K/V head
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done
   const int units = p.Hkv * p.row_tiles, u = hk * p.row_tiles + x / RT, r = x % RT;
-  const long long total = p.first_tile[p.B], first = p.first_tile[b];
-  const long long tiles = quick_div(p.first_tile[b + 1] - first, units), u0 = first + u * tiles, u1 = u0 + tiles;
+  const long long total = p.first_slot[p.B], first = p.first_slot[b];
+  const long long weight = quick_div(p.first_slot[b + 1] - first, units), u0 = first + u * weight;
   int ka = 0, kb = -1;
-  if (tiles > 0) {
+  if (weight > 0) {
     const long long each = quick_div(total, shares), more = total - each * shares;
     auto share_of = [&](long long t) {
       return (int)(t < more * (each + 1) ? quick_div(t, each + 1) : more + quick_div(t - more * (each + 1), each));
     };
-    ka = share_of(u0);
-    kb = share_of(u1 - 1);
+    ka = share_of(u0 + p.lead);
+    kb = share_of(u0 + weight - 1);
     if (ka == kb) return;
   }
   auto slot_of = [&](int k) { return (2 * (long long)k + (share_begin(total, shares, k) < u0 ? 1 : 0)) * RT + r; };
@@ -772,17 +785,25 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
 // Query rows of one CTA.
 int kv8_row_tile(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
-int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span, int D) {
+// CTAs that run at once, and the most tiles a call can have.
+static int kv8_ctas(int Nq, int group, int D) {
   int dev = 0, n_sm = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  return n_sm * (D == 64 && kv8_row_tile(Nq * group) <= 8 ? Layout<64, 8>::kCtas : Layout<128, 8>::kCtas);
+}
+static long long kv8_most_tiles(int B, int Nq, int Hkv, int group, int span) {
   const int rows = Nq * group, rt = kv8_row_tile(rows);
-  const int ctas = n_sm * (D == 64 && rt <= 8 ? Layout<64, 8>::kCtas : Layout<128, 8>::kCtas);
-  const long long tiles = (long long)B * Hkv * ((rows + rt - 1) / rt) * (((long long)span + kKv8Tile - 1) / kKv8Tile);
+  return (long long)B * Hkv * ((rows + rt - 1) / rt) * (((long long)span + kKv8Tile - 1) / kKv8Tile);
+}
+
+int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span, int D) {
+  const long long tiles = kv8_most_tiles(B, Nq, Hkv, group, span);
+  const int ctas = kv8_ctas(Nq, group, D);
   return (int)(tiles < 1 ? 1 : tiles < ctas ? tiles : ctas);
 }
 
 template <int D, int RT>
-static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int shares,
+static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int shares, int span,
                                cudaStream_t stream) {
   auto kern = fa_decode_kv8_kernel<D, RT>;
   constexpr uint32_t smem = Layout<D, RT>::kBytes;
@@ -790,6 +811,8 @@ static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   p.row_tiles = (p.Nq * p.group + RT - 1) / RT;
+  // Where a share is a tile or less, nothing is gained by making room for starts.
+  p.lead = kv8_most_tiles(p.B, p.Nq, p.Hkv, p.group, span) > kv8_ctas(p.Nq, p.group, D) ? kLead(RT) : 0;
   kern<<<shares, kThreads, smem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -808,20 +831,20 @@ static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8
 }
 
 template <int D>
-static cudaError_t launch_decode_kv8_t(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int shares,
+static cudaError_t launch_decode_kv8_t(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int shares, int span,
                                        cudaStream_t stream) {
   switch (kv8_row_tile(p.Nq * p.group)) {
-    case 4: return launch_main<D, 4>(tk, tv, p, shares, stream);
-    case 8: return launch_main<D, 8>(tk, tv, p, shares, stream);
-    case 16: return launch_main<D, 16>(tk, tv, p, shares, stream);
-    default: return launch_main<D, 32>(tk, tv, p, shares, stream);
+    case 4: return launch_main<D, 4>(tk, tv, p, shares, span, stream);
+    case 8: return launch_main<D, 8>(tk, tv, p, shares, span, stream);
+    case 16: return launch_main<D, 16>(tk, tv, p, shares, span, stream);
+    default: return launch_main<D, 32>(tk, tv, p, shares, span, stream);
   }
 }
 
-cudaError_t launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int D, int shares,
+cudaError_t launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int D, int shares, int span,
                               cudaStream_t stream) {
-  if (D == 64) return launch_decode_kv8_t<64>(tk, tv, p, shares, stream);
-  if (D == 128) return launch_decode_kv8_t<128>(tk, tv, p, shares, stream);
+  if (D == 64) return launch_decode_kv8_t<64>(tk, tv, p, shares, span, stream);
+  if (D == 128) return launch_decode_kv8_t<128>(tk, tv, p, shares, span, stream);
   return cudaErrorInvalidValue;
 }
 

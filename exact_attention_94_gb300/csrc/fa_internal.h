@@ -228,11 +228,12 @@ struct Kv8DecodeParams {
   float* lse;
   float* part_o;             // [2 * shares, RT, d] fp32: the pieces a share's borders cut, each normalised
   float* part_lse;           // [2 * shares, RT] log2 of each piece's softmax mass
-  long long* first_tile;     // [B + 1] tiles before each request, written by the kernel for the merge
+  long long* first_slot;     // [B + 1] weight of the work before each request, written by the kernel for the merge
   int B, Nq, Hq, Hkv, group;
   int page_size, num_pages, max_blocks, max_len;
   int win_left;              // -1: no window
   int box_rows;              // keys per TMA box: 16 .. 128, divides the page and the tile
+  int lead;                  // tiles that a unit counts for its start and end, set by the launch
   int row_tiles;             // tiles of query rows per K/V head, set by the launch
   float scale_log2;
   unsigned* err;
@@ -242,7 +243,7 @@ int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span, int D);
 int kv8_row_tile(int rows);  // query rows of a CTA for `rows` rows per K/V head
 // 3-D uint8 tensor map of the codes, [heads of pages][page_size][D], swizzled at the row's length.
 bool make_tmap_codes(CUtensorMap* m, const void* ptr, int D, int page_size, long long page_heads, int box_rows);
-cudaError_t launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int D, int shares,
+cudaError_t launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int D, int shares, int span,
                               cudaStream_t stream);
 
 int decode_stages(int G, int D);
