@@ -74,7 +74,8 @@ struct Layout {
   static constexpr uint32_t kMaxOff = kScOff + kSlots / 2 * kScBytes;        // [4][RT] each: warps' maxima, sums, references, factors
   static constexpr uint32_t kRowOff = kMaxOff + (16 + 8) * RT * 4;           // (and [4][RT] output rows, 8 bytes each) two of: [RT] query scales, [RT] positions
   static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // [2][4] votes, scan, start
-  static constexpr uint32_t kBarOff = kMiscOff + 128;
+  static constexpr uint32_t kWalkOff = kMiscOff + 128;                       // [6] the warps' walks
+  static constexpr uint32_t kBarOff = kWalkOff + 6 * 32;
   static constexpr uint32_t kBytes = kBarOff + 8 * (2 * kSlots + 6) + 16 + 1024;
   static_assert(kUsed <= 256, "TMEM columns");
 };
@@ -121,37 +122,44 @@ struct Piece {
   int b, u, t0, t1, tiles, len, beg;
 };
 
-// Walks a CTA's share piece by piece; every role walks for itself.
+// Walks a CTA's share piece by piece.  Every warp walks for itself; its state
+// lies in shared memory, so that it holds no registers over the tiles.
 struct Walk {
   long long left;  // weight of the share still to come
   long long off;   // next slot within the weight of the request's units
   int b, tiles, len;
 
-  __device__ __forceinline__ bool next(const Kv8DecodeParams& p, int units, Piece& s) {
-    while (left > 0) {
-      const int each = tiles + p.lead;
-      if (tiles == 0 || off >= (long long)each * units) {  // the request's units are done (or it has no keys)
-        off = 0;
-        ++b;
-        len = kv8_len(p, b);
-        tiles = kv8_tiles(p, len);
-        continue;
-      }
-      s.b = b;
-      s.u = (int)quick_div(off, each);
-      const int w0 = (int)(off - (long long)s.u * each), w1 = (int)(left < each - w0 ? w0 + left : each);
-      off += w1 - w0;
-      left -= w1 - w0;
-      s.t0 = max(w0 - p.lead, 0);
-      s.t1 = max(w1 - p.lead, 0);
-      s.tiles = tiles;
-      s.len = len;
-      s.beg = kv8_begin(p, len);
-      if (s.t0 < s.t1) return true;
-    }
-    return false;
-  }
 };
+
+__device__ __forceinline__ bool next_piece(Walk* walk, const Kv8DecodeParams& p, int units, Piece& s) {
+  Walk w = *walk;
+  bool found = false;
+  while (w.left > 0 && !found) {
+    const int each = w.tiles + p.lead;
+    if (w.tiles == 0 || w.off >= (long long)each * units) {  // the request's units are done (or it has no keys)
+      w.off = 0;
+      ++w.b;
+      w.len = kv8_len(p, w.b);
+      w.tiles = kv8_tiles(p, w.len);
+      continue;
+    }
+    s.b = w.b;
+    s.u = (int)quick_div(w.off, each);
+    const int w0 = (int)(w.off - (long long)s.u * each), w1 = (int)(w.left < each - w0 ? w0 + w.left : each);
+    w.off += w1 - w0;
+    w.left -= w1 - w0;
+    s.t0 = max(w0 - p.lead, 0);
+    s.t1 = max(w1 - p.lead, 0);
+    s.tiles = w.tiles;
+    s.len = w.len;
+    s.beg = kv8_begin(p, w.len);
+    found = s.t0 < s.t1;
+  }
+  __syncwarp();
+  if (lane_id() == 0) *walk = w;
+  __syncwarp();
+  return found;
+}
 
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r) {
@@ -289,8 +297,12 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS = tmem, tO = tmem + 2 * L::kNS;
   const WaitCtx w{abort_flag, p.timeout_ns, p.err};
-  Walk walk{to - from, 0, 0, 0, 0};
-  if (to > from) walk = {to - from, s_start[1], (int)s_start[0], (int)(s_start[2] >> 32), (int)(s_start[2] & 0xffffffffll)};
+  Walk* walk = reinterpret_cast<Walk*>(sb + L::kWalkOff) + warp;
+  if (lane == 0) {
+    *walk = {to - from, 0, 0, 0, 0};
+    if (to > from) *walk = {to - from, s_start[1], (int)s_start[0], (int)(s_start[2] >> 32), (int)(s_start[2] & 0xffffffffll)};
+  }
+  __syncwarp();
   Piece pc;
   bool ok = true;
   asm volatile("griddepcontrol.launch_dependents;");  // the merge may be set up; it waits for this grid's end
@@ -305,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     }
     const int bpb = p.box_rows / 16;  // 16-key groups per TMA box
     int it = 0;                       // tiles of the share so far
-    while (ok && walk.next(p, units, pc)) {
+    while (ok && next_piece(walk, p, units, pc)) {
       const int hk = pc.u / p.row_tiles;
       const int g_first = (pc.beg + pc.t0 * kKv8Tile) / 16, g_end = min((pc.len + 15) / 16, g_first + (pc.t1 - pc.t0) * 8);
       const int* table = p.block_table + (size_t)pc.b * p.max_blocks;
@@ -397,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     };
     int it = 0, piece = 0;
     bool was_first = false;  // whether tile it - 1 was its piece's first
-    while (ok && walk.next(p, units, pc)) {
+    while (ok && next_piece(walk, p, units, pc)) {
       ok = __all_sync(0xffffffffu, mbar_wait(QB, piece & 1, w, 52));
       ++piece;
       for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
@@ -509,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       if (lane == 0) mbar_arrive(XB);
       return __all_sync(0xffffffffu, mbar_wait(XB, xphase++ & 1, w, 60));
     };
-    bool have = walk.next(p, units, pc);
+    bool have = next_piece(walk, p, units, pc);
     if (have) load_q(pc, 0);
     while (have) {
       const float* s_qsc = reinterpret_cast<const float*>(sb + L::kRowOff + (piece & 1) * 2 * RT * 4);
@@ -661,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       if (!ok) break;
       // ---- the next piece's Q, while this one's last products run (its scores are all read)
       const Piece done = pc;
-      have = walk.next(p, units, pc);
+      have = next_piece(walk, p, units, pc);
       if (have) load_q(pc, piece + 1);
       // ---- each row's sum over the 128 key lanes
       const float row_sum = warp_row_sums<RT>(l, lane);
