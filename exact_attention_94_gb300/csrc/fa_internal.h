@@ -175,9 +175,10 @@ struct PlanParams {
   int page_size;
   int num_pages;
   int max_blocks;
+  int totals_later;          // set by the launch: seq_lens and free_count_out come from a second kernel
   unsigned* err;
 };
-cudaError_t launch_page_plan(const PlanParams& p, cudaStream_t stream);
+cudaError_t launch_page_plan(PlanParams& p, cudaStream_t stream);
 
 // Rotary positions (see fa_rope_axes in fa.h).
 struct RopeParams {

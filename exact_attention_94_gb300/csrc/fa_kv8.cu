@@ -21,7 +21,7 @@ namespace fa {
 
 namespace {
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4;
 constexpr long long kAppendMany = 152 * 64;  // warps that the SMs hold at once
 constexpr int kHeld = 16;  // vectors of a run that a lane holds in registers
 
@@ -46,7 +46,9 @@ __device__ __forceinline__ float pow2_scale(uint32_t amax_bits) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Eight bf16 values times inv -> eight codes; an infinity becomes NaN.
+// Eight bf16 values times inv -> eight codes.  The conversion keeps a NaN; an
+// infinity, which it would saturate, has to be made one first (ODD).
+template <bool ODD>
 __device__ __forceinline__ uint2 encode8(const uint4& u, float inv) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   float f[8];
@@ -56,7 +58,7 @@ __device__ __forceinline__ uint2 encode8(const uint4& u, float inv) {
     f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = isinf(f[i]) ? __uint_as_float(0x7fffffffu) : f[i] * inv;
+  for (int i = 0; i < 8; ++i) f[i] = ODD && isinf(f[i]) ? __uint_as_float(0x7fffffffu) : f[i] * inv;
   return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
@@ -138,19 +140,22 @@ __global__ void __launch_bounds__(32 * kAppendWarps) fa_kv8_append_kernel(const 
 #pragma unroll
       for (int c = 0; c < kHeld; ++c) {
         if (i0 + c * RPI >= len) break;
-        const uint32_t w[4] = {held[c].x, held[c].y, held[c].z, held[c].w};
-        uint32_t top = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) top = __vmaxu2(top, w[q] & 0x7fff7fffu);
-        if (__vcmpgeu2(top, 0x7f807f80u) != 0) {  // an infinity or a NaN among them
-          top = 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) top = __vmaxu2(top, finite_or_zero(w[q] & 0x7fff7fffu));
-        }
-        mx = __vmaxu2(mx, top);
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(held[c].x & 0x7fff7fffu, held[c].y & 0x7fff7fffu),
+                                   __vmaxu2(held[c].z & 0x7fff7fffu, held[c].w & 0x7fff7fffu)));
       }
     }
-    const float own = pow2_scale(__reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16)));
+    uint32_t amax = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+    const bool odd = amax >= 0x7f80u;  // an infinity or a NaN in the run: again, without them
+    if (odd) {
+      mx = 0;
+      for (int i = sub; i < len; i += RPI) {
+        const uint4 u = *reinterpret_cast<const uint4*>(rows_at + i * xs);
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(finite_or_zero(u.x & 0x7fff7fffu), finite_or_zero(u.y & 0x7fff7fffu)),
+                                   __vmaxu2(finite_or_zero(u.z & 0x7fff7fffu), finite_or_zero(u.w & 0x7fff7fffu))));
+      }
+      amax = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+    }
+    const float own = pow2_scale(amax);
     const size_t at = (size_t)page * p.Hkv + head;
     const size_t from = (size_t)(src >= 0 ? src : page) * p.Hkv + head;
     const float old = first > 0 ? scales[from] : 0.f;
@@ -171,12 +176,18 @@ __global__ void __launch_bounds__(32 * kAppendWarps) fa_kv8_append_kernel(const 
     }
     // ---- new codes
     dst += (size_t)first * D;
+    if (odd) {
+      for (int i = sub; i < len; i += RPI)
+        *reinterpret_cast<uint2*>(dst + (size_t)i * D) = encode8<true>(*reinterpret_cast<const uint4*>(rows_at + i * xs), inv);
+      continue;
+    }
     for (int i0 = 0; i0 < len; i0 += kHeld * RPI) {
       if (len > kHeld * RPI) load(i0);
 #pragma unroll
       for (int c = 0; c < kHeld; ++c) {
         const int i = i0 + sub + c * RPI;
-        if (i < len) *reinterpret_cast<uint2*>(dst + (size_t)i * D) = encode8(held[c], inv);
+        if (i0 + c * RPI >= len) break;
+        if (i < len) *reinterpret_cast<uint2*>(dst + (size_t)i * D) = encode8<false>(held[c], inv);
       }
     }
   }

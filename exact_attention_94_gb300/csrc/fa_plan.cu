@@ -11,24 +11,18 @@
 //     is the table's for a block held before, else
 //     free[count - 1 - (base_b + block - ceil(c_b / P))].
 // The step is bound by latency: a few thousand integers in, 12 bytes out per
-// row.  So one launch does all of it.  Every CTA scans all requests for itself
-// (the sums stay in its shared memory; nothing passes between CTAs through
-// device memory) and serves every k-th block of 1024 rows.  The CTAs form one
-// thread-block cluster, whose barrier separates the last read of ctx_lens and
-// free_count from the first write of seq_lens and free_count_out, so both may
-// be updated in place.
+// row.  Every CTA scans all requests for itself (the sums stay in its shared
+// memory; nothing passes between CTAs) and serves its part of the rows.  One
+// CTA does a step of few rows, in one launch.  Where there are many, the CTAs
+// that read ctx_lens and free_count have no order among themselves, so seq_lens
+// and free_count_out, which may be the same arrays, are then written by a
+// second launch of one CTA, from cu_new and what the first has left of the count.
 #include "fa_internal.h"
 #include "ptx.cuh"
-
-#include <cooperative_groups.h>
 
 namespace fa {
 
 namespace {
-
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanRows = 4;
-constexpr int kPlanWarps = kPlanThreads / 32;
 
 // a / b rounded up, for a >= 0, b > 0, without a 64-bit division
 __device__ __forceinline__ int div_up(int a, int b) {
@@ -47,23 +41,24 @@ __device__ __forceinline__ long long warp_incl_sum(long long v, int lane) {
 
 }  // namespace
 
-__global__ void __launch_bounds__(kPlanThreads) fa_page_plan_kernel(const PlanParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) fa_page_plan_kernel(const PlanParams p) {
+  constexpr int WARPS = THREADS / 32;
   extern __shared__ int s_mem[];
   int* s_cu = s_mem;                // [B + 1] first row of each request
   int* s_ctx = s_cu + p.B + 1;      // [B] tokens held before
   int* s_base = s_ctx + p.B;        // [B] stack position of its first new page, counted from the top
-  __shared__ long long s_tok[kPlanWarps], s_need[kPlanWarps];
+  __shared__ long long s_tok[WARPS], s_need[WARPS];
   __shared__ int s_free;
 
   const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
-  const auto cluster = cooperative_groups::this_cluster();
-  const int rank = (int)blockIdx.x, ranks = (int)gridDim.x;
 
   // ---- sums over the requests: thread t takes requests t*k .. t*k + k - 1
-  const int k = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int k = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(p.B, tid * k), b1 = min(p.B, b0 + k);
   long long tok = 0, need = 0;
   bool bad = false;
+  if (tid == 0) s_free = *p.free_count;
   for (int b = b0; b < b1; ++b) {
     int c = p.ctx_lens[b], n = p.new_lens[b];
     s_ctx[b] = c;
@@ -76,7 +71,6 @@ __global__ void __launch_bounds__(kPlanThreads) fa_page_plan_kernel(const PlanPa
     tok += n;
     need += div_up(c + n, p.page_size) - div_up(c, p.page_size);
   }
-  if (tid == 0) s_free = *p.free_count;
   const long long tok_in = warp_incl_sum(tok, lane), need_in = warp_incl_sum(need, lane);
   if (lane == 31) {
     s_tok[warp] = tok_in;
@@ -85,7 +79,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_page_plan_kernel(const PlanPa
   const bool any_bad = __syncthreads_or(bad);
   long long tok0 = tok_in - tok, need0 = need_in - need, tok_all = 0, need_all = 0;
 #pragma unroll
-  for (int w = 0; w < kPlanWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) {
       tok0 += s_tok[w];
       need0 += s_need[w];
@@ -107,96 +101,95 @@ __global__ void __launch_bounds__(kPlanThreads) fa_page_plan_kernel(const PlanPa
     }
   }
   if (tid == 0) s_cu[p.B] = ok ? (int)tok_all : 0;
-  // every CTA has read the lengths and the count: they may be overwritten now
-  if (ranks > 1)
-    cluster.sync();
-  else
-    __syncthreads();
+  __syncthreads();
 
-  if (rank == 0) {
-    for (int b = tid; b <= p.B; b += kPlanThreads) {
+  if (blockIdx.x == 0) {
+    for (int b = tid; b <= p.B; b += THREADS) {
       p.cu_new[b] = ok ? s_cu[b] : 0;
-      if (b < p.B) p.seq_lens[b] = s_ctx[b] + (ok ? s_cu[b + 1] - s_cu[b] : 0);
+      if (b < p.B && !p.totals_later) p.seq_lens[b] = s_ctx[b] + (ok ? s_cu[b + 1] - s_cu[b] : 0);
     }
     if (tid == 0) {
-      *p.free_count_out = ok ? free_n - (int)need_all : free_n;
+      if (!p.totals_later) *p.free_count_out = ok ? free_n - (int)need_all : free_n;
       if (!ok) atomicCAS(p.err, 0u, code);
     }
   }
 
-  // ---- rows, kPlanRows of a thread at a time: their searches and page loads overlap
+  // ---- rows
   const int total = s_cu[p.B];
-  const long long step = (long long)ranks * kPlanThreads;
-  for (long long r0 = (long long)rank * kPlanThreads + tid; r0 < p.max_tokens; r0 += step * kPlanRows) {
-    int page[kPlanRows], slot[kPlanRows], pos[kPlanRows], lo[kPlanRows], hi[kPlanRows];
-    int* entry[kPlanRows];
-#pragma unroll
-    for (int x = 0; x < kPlanRows; ++x) lo[x] = 0, hi[x] = p.B - 1;
-    for (int n = p.B; n > 1; n = (n + 1) >> 1) {  // the last request whose first row is at most this one
-#pragma unroll
-      for (int x = 0; x < kPlanRows; ++x) {
-        const int mid = (lo[x] + hi[x] + 1) >> 1;
-        const bool up = s_cu[mid] <= r0 + x * step;
-        lo[x] = up ? mid : lo[x];
-        hi[x] = up ? hi[x] : max(lo[x], mid - 1);
+  for (long long row = (long long)blockIdx.x * THREADS + tid; row < p.max_tokens; row += (long long)gridDim.x * THREADS) {
+    int page = -1, slot = -1, pos = 0;
+    if (row < total) {
+      int lo = 0, hi = p.B - 1;  // the last request whose first row is at most this one
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_cu[mid] <= row)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int ctx = s_ctx[lo];
+      pos = ctx + (int)row - s_cu[lo];
+      const int blk = (int)((unsigned)pos / (unsigned)p.page_size), held = div_up(ctx, p.page_size);
+      slot = pos - blk * p.page_size;
+      int* entry = p.block_table + (size_t)lo * p.max_blocks + blk;
+      page = blk < held ? *entry : p.free_pages[free_n - 1 - (s_base[lo] + blk - held)];
+      if (page < 0 || page >= p.num_pages) {
+        atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
+        page = slot = -1;
+      } else if (slot == 0) {
+        *entry = page;  // the first token of a new page
       }
     }
-#pragma unroll
-    for (int x = 0; x < kPlanRows; ++x) {
-      page[x] = slot[x] = -1;
-      pos[x] = 0;
-      entry[x] = nullptr;
-      if (r0 + x * step < total) {
-        const int ctx = s_ctx[lo[x]];
-        pos[x] = ctx + (int)(r0 + x * step) - s_cu[lo[x]];
-        const int blk = (int)((unsigned)pos[x] / (unsigned)p.page_size), held = div_up(ctx, p.page_size);
-        slot[x] = pos[x] - blk * p.page_size;
-        entry[x] = p.block_table + (size_t)lo[x] * p.max_blocks + blk;
-        page[x] = *(blk < held ? entry[x] : p.free_pages + (free_n - 1 - (s_base[lo[x]] + blk - held)));
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < kPlanRows; ++x) {
-      const long long row = r0 + x * step;
-      if (row >= p.max_tokens) break;
-      if (entry[x] != nullptr) {
-        if (page[x] < 0 || page[x] >= p.num_pages) {
-          atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
-          page[x] = slot[x] = -1;
-        } else if (slot[x] == 0) {
-          *entry[x] = page[x];  // the first token of a new page
-        }
-      }
-      p.page[row] = page[x];
-      p.slot[row] = slot[x];
-      p.position[row] = pos[x];
-    }
+    p.page[row] = page;
+    p.slot[row] = slot;
+    p.position[row] = pos;
   }
 }
 
-cudaError_t launch_page_plan(const PlanParams& p, cudaStream_t stream) {
+// The lengths and the free count after a step whose rows many CTAs have written.
+__global__ void __launch_bounds__(1024) fa_page_plan_totals_kernel(const PlanParams p) {
+  long long need = 0;
+  for (int b = threadIdx.x; b < p.B; b += 1024) {
+    const int c = p.ctx_lens[b], n = p.cu_new[b + 1] - p.cu_new[b];  // (a refused step: n = 0, any c)
+    p.seq_lens[b] = c + n;
+    if (n > 0) need += div_up(c + n, p.page_size) - div_up(c, p.page_size);
+  }
+  __shared__ long long s_need[32];
+  const long long in_warp = warp_incl_sum(need, lane_id());
+  if (lane_id() == 31) s_need[threadIdx.x >> 5] = in_warp;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    long long all = 0;
+    for (int w = 0; w < 32; ++w) all += s_need[w];
+    *p.free_count_out = *p.free_count - (int)all;
+  }
+}
+
+template <int THREADS>
+static cudaError_t launch_page_plan_t(const PlanParams& p, int ctas, cudaStream_t stream) {
   const size_t smem = (3 * (size_t)p.B + 1) * sizeof(int);
   if (smem > 48 * 1024) {
     const cudaError_t e =
-        cudaFuncSetAttribute(fa_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(fa_page_plan_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  if (p.max_tokens <= 4 * kPlanThreads) {
-    fa_page_plan_kernel<<<1, kPlanThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+  fa_page_plan_kernel<THREADS><<<ctas, THREADS, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_page_plan(PlanParams& p, cudaStream_t stream) {
+  // One CTA for few rows; a small one starts and synchronises sooner.
+  if (p.max_tokens <= 4096) {
+    p.totals_later = 0;
+    return p.max_tokens <= 1024 && p.B <= 1024 ? launch_page_plan_t<256>(p, 1, stream)
+                                               : launch_page_plan_t<1024>(p, 1, stream);
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(8);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim.x = cfg.gridDim.x;
-  a.val.clusterDim.y = a.val.clusterDim.z = 1;
-  cfg.attrs = &a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_page_plan_kernel, p);
+  p.totals_later = p.seq_lens == p.ctx_lens || p.free_count_out == p.free_count;
+  const int ctas = (p.max_tokens + 1023) / 1024;
+  const cudaError_t e = launch_page_plan_t<1024>(p, ctas < 304 ? ctas : 304, stream);
+  if (e != cudaSuccess || !p.totals_later) return e;
+  fa_page_plan_totals_kernel<<<1, 1024, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace fa

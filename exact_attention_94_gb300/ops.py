@@ -610,70 +610,91 @@ def decode_paged_window(q, k_pages, v_pages, block_table, seq_lens, max_seq_len:
 # ---------------------------------------------------------------- serving steps: planning, rotary, 8-bit cache
 #
 # A decode step launches a few kernels of some microseconds each, so these
-# wrappers spend as little host time as their checks allow: addresses go to
-# ctypes as plain integers, and the current stream comes as its raw handle.
+# wrappers spend as little host time as their checks allow: one expression per
+# tensor that holds for a good one, messages worked out only for a bad one,
+# addresses passed as plain integers, the stream as its raw handle.
 
 def _on_call_stream(fn):
-    """Runs a wrapper with the device of its tensors and the call's stream
-    current: outputs and workspaces then come from that stream's own memory,
-    so one call's cannot be handed to a call on another stream while it runs.
-    ``stream`` reaches the wrapper as the raw handle."""
+    """Runs a wrapper with the device of its first CUDA tensor and the call's
+    stream current: outputs and workspaces then come from that stream's own
+    memory, so one call's cannot be handed to a call on another stream while it
+    runs.  The wrapper gets the device's index and the stream's raw handle, and
+    checks that every tensor is on that device."""
     @functools.wraps(fn)
     def wrapper(*args, stream=None, **kwargs):
-        dev = None
-        for a in (*args, *kwargs.values()) if kwargs else args:
-            if isinstance(a, torch.Tensor) and a.is_cuda:
-                i = a.get_device()
-                if dev is None:
-                    dev = i
-                elif i != dev:
-                    raise ValueError("all CUDA tensors of a call must be on one device")
+        dev = -1
+        for a in args:
+            if isinstance(a, torch.Tensor):
+                dev = a.get_device()
+                if dev >= 0:
+                    break
+        if dev < 0:
+            for a in kwargs.values():
+                if isinstance(a, torch.Tensor) and a.is_cuda:
+                    dev = a.get_device()
+                    break
+            else:
+                return fn(*args, dev=-2, raw=0, **kwargs)  # nothing is on a GPU: refused by the checks
         if stream is not None:
-            if dev is not None and stream.device.index != dev:
+            if stream.device.index != dev:
                 raise ValueError("stream must be on the device of the tensors")
             with torch.cuda.stream(stream):
-                return fn(*args, stream=stream.cuda_stream, **kwargs)
-        if dev is None:
-            return fn(*args, stream=0, **kwargs)  # refused below: nothing is on a GPU
+                return fn(*args, dev=dev, raw=stream.cuda_stream, **kwargs)
         if dev == torch.cuda.current_device():
-            return fn(*args, stream=torch.cuda.current_stream(dev).cuda_stream, **kwargs)
+            return fn(*args, dev=dev, raw=torch._C._cuda_getCurrentRawStream(dev), **kwargs)
         with torch.cuda.device(dev):
-            return fn(*args, stream=torch.cuda.current_stream(dev).cuda_stream, **kwargs)
+            return fn(*args, dev=dev, raw=torch._C._cuda_getCurrentRawStream(dev), **kwargs)
     return wrapper
 
 
-def _check_i32(name, t, shape):
+def _refuse(name, t, dtype, dev, shape):
+    """Says what is wrong with a tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _check_rows(name, t, shape=None):
-    """A bf16 [..., H, d] tensor whose heads lie side by side and whose rows lie
-    one stride apart (a slice of a fused projection, say).  Returns that stride."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.dtype != dtype:
+        raise (TypeError if dtype == torch.bfloat16 else ValueError)(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.dim() < 3:
+    if t.get_device() != dev:
+        raise ValueError("all CUDA tensors of a call must be on one device")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _check(name, t, dtype, dev, shape):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous()):
+        _refuse(name, t, dtype, dev, shape)
+
+
+def _check_dims(name, t, dtype, dev, dims, what):
+    """As _check for a tensor that sets the call's sizes: its dimensions."""
+    if isinstance(t, torch.Tensor) and t.dim() != dims:
+        raise ValueError(f"{name} must be {what}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        _refuse(name, t, dtype, dev, None)
+    return t.shape
+
+
+def _check_rows(name, t, dev, shape=None):
+    """A bf16 [..., H, d] tensor whose heads lie side by side and whose rows lie
+    one stride apart (a slice of a fused projection, say).  Returns that stride."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev
+            and (shape is None or t.shape == shape)):
+        _refuse(name, t, torch.bfloat16, dev, shape)
+    size, step = t.shape, t.stride()
+    if len(size) < 3:
         raise ValueError(f"{name} must be [..., H, d]")
-    size = t.shape
-    if shape is not None and size != shape:
-        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
     H, d = size[-2], size[-1]
+    if len(size) == 3 and step[2] == 1 and step[1] == d and step[0] >= H * d:
+        return step[0]
     if t.is_contiguous():
         return H * d
-    step = t.stride()
     rows = [(n, s) for n, s in zip(size[:-2], step[:-2]) if n != 1]
     ok = (d <= 1 or step[-1] == 1) and (H <= 1 or step[-2] == d)
     ok = ok and all(rows[i][1] == rows[i + 1][0] * rows[i + 1][1] for i in range(len(rows) - 1))
-    ok = ok and (not rows or rows[-1][1] >= H * d)
-    if not ok:
+    if not ok or (rows and rows[-1][1] < H * d):
         raise ValueError(f"{name} must have contiguous heads and evenly spaced rows")
     return rows[-1][1] if rows else H * d
 
@@ -690,39 +711,34 @@ class PagePlan(NamedTuple):
 
 @_on_call_stream
 def page_plan(ctx_lens, new_lens, free_pages, free_count, block_table, page_size: int, max_tokens: int, out=None, *,
-              stream=None) -> PagePlan:
+              dev, raw) -> PagePlan:
     """Plans a step on the GPU.  ctx_lens, new_lens int32 [B]: tokens each
     request holds and gets; free_pages int32 [num_pages] and free_count int32
     [1]: the stack of free pages; block_table int32 [B, max_blocks], whose new
     entries are written.  max_tokens: rows of the outputs, at least the step's
     tokens.  ``out``: a PagePlan to write into; its seq_lens may be ctx_lens and
     its free_count the given one, which advances them in place."""
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    B, max_blocks = block_table.shape
+    i32 = torch.int32
+    B, max_blocks = _check_dims("block_table", block_table, i32, dev, 2, "[B, max_blocks]")
+    (num_pages,) = _check_dims("free_pages", free_pages, i32, dev, 1, "[num_pages]")
+    _check("ctx_lens", ctx_lens, i32, dev, (B,))
+    _check("new_lens", new_lens, i32, dev, (B,))
+    _check("free_count", free_count, i32, dev, (1,))
     n = int(max_tokens)
     if n < 0:
         raise ValueError("max_tokens must not be negative")
-    _check_i32("ctx_lens", ctx_lens, (B,))
-    _check_i32("new_lens", new_lens, (B,))
-    num_pages = free_pages.numel()
-    _check_i32("free_pages", free_pages, (num_pages,))
-    _check_i32("free_count", free_count, (1,))
-    _check_i32("block_table", block_table, (B, max_blocks))
-    sizes = (B, B + 1, n, n, n, 1)
-    if out is None:  # one buffer, cut up; the rows' three arrays first
-        buf = torch.empty(3 * n + 2 * B + 2, dtype=torch.int32, device=block_table.device)
-        page, slot, position, seq, cu, left = buf.split((n, n, n, B, B + 1, 1))
+    if out is None:  # one buffer, cut up
+        buf = torch.empty(3 * n + 2 * B + 2, dtype=i32, device=block_table.device)
+        page, slot, position, seq, cu, left = buf.split_with_sizes((n, n, n, B, B + 1, 1))
         out = PagePlan(seq, cu, page, slot, position, left)
     else:
-        for name, t, s in zip(PagePlan._fields, out, sizes):
-            _check_i32(f"out.{name}", t, (s,))
-            if t.device != block_table.device:
-                raise ValueError("all CUDA tensors of a call must be on one device")
+        for name, t, size in zip(PagePlan._fields, out, (B, B + 1, n, n, n, 1)):
+            _check(f"out.{name}", t, i32, dev, (size,))
     st = lib().fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
                             block_table.data_ptr(), *[t.data_ptr() for t in out], B, n, int(page_size), num_pages,
-                            max_blocks, stream)
-    _lib.check(st, "fa_page_plan")
+                            max_blocks, raw)
+    if st:
+        _lib.check(st, "fa_page_plan")
     return out
 
 
@@ -764,121 +780,120 @@ def rope_plan(d: int, sections, theta: float = 10000.0, per_axis: bool = False, 
     return RopePlan(d, axis + [-1] * rest, freq + [0.0] * rest, neighbours)
 
 
-def _rope_side(name, t, o, plan):
+def _rope_side(name, t, o, plan, dev):
     """(rows, heads, address, address, stride, stride, output) of q or k."""
-    stride = _check_rows(name, t)
-    if t.shape[-1] != plan.d:
-        raise ValueError(f"{name} has head dim {t.shape[-1]}, the plan {plan.d}")
-    H = t.shape[-2]
+    stride = _check_rows(name, t, dev)
+    size = t.shape
+    H, d = size[-2], size[-1]
+    if d != plan.d:
+        raise ValueError(f"{name} has head dim {d}, the plan {plan.d}")
     if o is None:
-        o, out_stride = torch.empty(t.shape, dtype=t.dtype, device=t.device), H * plan.d
+        o, out_stride = torch.empty(size, dtype=torch.bfloat16, device=t.device), H * d
     else:
-        out_stride = _check_rows(f"out {name}", o, t.shape)
-        if o.device != t.device:
-            raise ValueError("all CUDA tensors of a call must be on one device")
-    return t.numel() // max(1, H * plan.d), H, t.data_ptr(), o.data_ptr(), stride, out_stride, o
+        out_stride = _check_rows(f"out {name}", o, dev, size)
+    return t.numel() // max(1, H * d), H, t.data_ptr(), o.data_ptr(), stride, out_stride, o
 
 
-def _rope(q, k, positions, plan, inverse, out, stream):
+def _rope(q, k, positions, plan, inverse, out, dev, raw):
     if not isinstance(plan, RopePlan):
         raise TypeError("plan must be a RopePlan")
     if q is None and k is None:
         raise ValueError("q or k must be given")
     oq, ok = out if out is not None else (None, None)
     none = (None, 0, None, None, 0, 0, None)
-    nq, Hq, pq, poq, qs, qos, oq = _rope_side("q", q, oq, plan) if q is not None else none
-    nk, Hkv, pk, pok, ks, kos, ok = _rope_side("k", k, ok, plan) if k is not None else none
+    nq, Hq, pq, poq, qs, qos, oq = _rope_side("q", q, oq, plan, dev) if q is not None else none
+    nk, Hkv, pk, pok, ks, kos, ok = _rope_side("k", k, ok, plan, dev) if k is not None else none
     if nq is not None and nk is not None and nq != nk:
         raise ValueError("q and k must have the same rows")
     rows = nq if nq is not None else nk
-    _check_i32("positions", positions, (plan.n_axes, rows))
+    _check("positions", positions, torch.int32, dev, (plan.n_axes, rows))
     st = lib().fa_rope_axes(pq, pk, poq, pok, positions.data_ptr(), plan._ref, rows, Hq, Hkv, plan.d, qs, ks, qos, kos,
-                            inverse, stream)
-    _lib.check(st, "fa_rope_axes")
+                            inverse, raw)
+    if st:
+        _lib.check(st, "fa_rope_axes")
     return oq, ok
 
 
 @_on_call_stream
-def rope_axes(q, k, positions, plan: RopePlan, out=None, *, stream=None):
+def rope_axes(q, k, positions, plan: RopePlan, out=None, *, dev, raw):
     """Rotates q [..., Hq, d] and k [..., Hkv, d] (either may be None) by their
     rows' positions, int32 [plan.n_axes, rows].  Rows may lie a stride apart.
     Returns (q, k) rotated, in ``out`` = (q_out, k_out) when given (q_out may be q)."""
-    return _rope(q, k, positions, plan, 0, out, stream)
+    return _rope(q, k, positions, plan, 0, out, dev, raw)
 
 
 @_on_call_stream
-def rope_axes_bwd(dq, dk, positions, plan: RopePlan, out=None, *, stream=None):
+def rope_axes_bwd(dq, dk, positions, plan: RopePlan, out=None, *, dev, raw):
     """Gradients of rope_axes: (dq, dk) with respect to what it was given, from
     those with respect to what it returned."""
-    return _rope(dq, dk, positions, plan, 1, out, stream)
+    return _rope(dq, dk, positions, plan, 1, out, dev, raw)
 
 
-def _check_kv8(k_codes, v_codes, k_scale, v_scale):
-    for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.dim() != 4:
-            raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_size, d]")
-    size = k_codes.shape
-    if v_codes.shape != size:
-        raise ValueError("k_codes and v_codes must have one shape")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or \
-                t.shape != size[:2]:
-            raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor [num_pages, Hkv]")
+def _check_kv8(k_codes, v_codes, k_scale, v_scale, dev):
+    size = _check_dims("k_codes", k_codes, torch.uint8, dev, 4, "[num_pages, Hkv, page_size, d]")
+    _check("v_codes", v_codes, torch.uint8, dev, size)
+    _check("k_scale", k_scale, torch.float32, dev, size[:2])
+    _check("v_scale", v_scale, torch.float32, dev, size[:2])
     return size
 
 
 @_on_call_stream
-def kv8_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, page, slot, copy_src=None, *, stream=None) -> None:
+def kv8_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, page, slot, copy_src=None, *, dev, raw) -> None:
     """Quantises tokens ([n, Hkv, d] bf16, rows may lie a stride apart) into the
     8-bit cache: codes uint8 [num_pages, Hkv, page_size, d] and scales fp32
     [num_pages, Hkv], updated.  page, slot (and copy_src) int32 [n] as from
     page_plan or PagePool.reserve_append; page -1 skips a row."""
-    num_pages, Hkv, P, d = _check_kv8(k_codes, v_codes, k_scale, v_scale)
-    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
-        raise ValueError("k_new must be [n, Hkv, d]")
-    n = k_new.shape[0]
-    ks, vs = _check_rows("k_new", k_new, (n, Hkv, d)), _check_rows("v_new", v_new, (n, Hkv, d))
-    _check_i32("page", page, (n,))
-    _check_i32("slot", slot, (n,))
+    num_pages, Hkv, P, d = _check_kv8(k_codes, v_codes, k_scale, v_scale, dev)
+    (n,) = _check_dims("page", page, torch.int32, dev, 1, "[n]")
+    _check("slot", slot, torch.int32, dev, (n,))
+    ks, vs = _check_rows("k_new", k_new, dev, (n, Hkv, d)), _check_rows("v_new", v_new, dev, (n, Hkv, d))
     if copy_src is not None:
-        _check_i32("copy_src", copy_src, (n,))
+        _check("copy_src", copy_src, torch.int32, dev, (n,))
+        copy_src = copy_src.data_ptr()
     st = lib().fa_kv8_append(k_new.data_ptr(), v_new.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
-                             k_scale.data_ptr(), v_scale.data_ptr(), page.data_ptr(), slot.data_ptr(),
-                             None if copy_src is None else copy_src.data_ptr(), n, Hkv, d, P, num_pages, ks, vs, stream)
-    _lib.check(st, "fa_kv8_append")
+                             k_scale.data_ptr(), v_scale.data_ptr(), page.data_ptr(), slot.data_ptr(), copy_src, n, Hkv,
+                             d, P, num_pages, ks, vs, raw)
+    if st:
+        _lib.check(st, "fa_kv8_append")
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv8_shares(dev, B, Nq, Hq, Hkv, d, L, window_left, shares):
+    """(shares, workspace bytes) of a call: they depend on its sizes and the device alone."""
+    if shares == 0:
+        shares = lib().fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, d, L, window_left)
+    return shares, max(16, lib().fa_decode_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, max(shares, 1)))
 
 
 @_on_call_stream
 def decode_kv8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, max_seq_len: int, window_left: int = -1,
-               num_shares: int = 0, scale: Optional[float] = None, workspace=None, *, stream=None):
+               num_shares: int = 0, scale: Optional[float] = None, workspace=None, *, dev, raw):
     """Attention of q [B, Nq, Hq, d] over the 8-bit paged cache; query i of a
     request stands at seq_lens - Nq + i.  block_table int32 [B, max_blocks] and
     seq_lens int32 [B] on the device.  Returns (o [B, Nq, Hq, d], lse [B, Hq, Nq])."""
-    _check_bf16("q", q)
-    num_pages, Hkv, P, d = _check_kv8(k_codes, v_codes, k_scale, v_scale)
-    if q.dim() != 4 or q.shape[3] != d:
+    num_pages, Hkv, P, d = _check_kv8(k_codes, v_codes, k_scale, v_scale, dev)
+    B, Nq, Hq, dq = _check_dims("q", q, torch.bfloat16, dev, 4, f"[B, Nq, Hq, {d}]")
+    if dq != d:
         raise ValueError(f"q must be [B, Nq, Hq, {d}]")
-    B, Nq, Hq, _ = q.shape
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    max_blocks = block_table.shape[1]
-    _check_i32("block_table", block_table, (B, max_blocks))
-    _check_i32("seq_lens", seq_lens, (B,))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    L, wl, shares, so = int(max_seq_len), int(window_left), int(num_shares), lib()
-    if shares == 0:
-        shares = so.fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, d, L, wl)
-    nbytes = so.fa_decode_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, max(shares, 1))
+    rows, max_blocks = _check_dims("block_table", block_table, torch.int32, dev, 2, "[B, max_blocks]")
+    if rows != B:
+        raise ValueError(f"block_table has {rows} rows for {B} requests")
+    _check("seq_lens", seq_lens, torch.int32, dev, (B,))
+    L, wl = int(max_seq_len), int(window_left)
+    shares, nbytes = _kv8_shares(dev, B, Nq, Hq, Hkv, d, L, wl, int(num_shares))
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-    elif workspace.numel() * workspace.element_size() < nbytes or not workspace.is_contiguous():
-        raise ValueError("workspace too small")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    else:
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the device of q")
+        if workspace.numel() * workspace.element_size() < nbytes:
+            raise ValueError("workspace too small")
     o = torch.empty_like(q)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
-    st = so.fa_decode_kv8(q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                          block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d,
-                          P, num_pages, max_blocks, L, wl, shares, workspace.data_ptr(), scale, stream)
-    _lib.check(st, "fa_decode_kv8")
+    st = lib().fa_decode_kv8(q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
+                             v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+                             lse.data_ptr(), B, Nq, Hq, Hkv, d, P, num_pages, max_blocks, L, wl, shares,
+                             workspace.data_ptr(), 1.0 / math.sqrt(d) if scale is None else float(scale), raw)
+    if st:
+        _lib.check(st, "fa_decode_kv8")
     return o, lse
