@@ -210,7 +210,7 @@ struct Kv8AppendParams {
   const int* copy_src;       // [n] or nullptr
   long long k_stride, v_stride;
   int n, Hkv, page_size, num_pages;
-  int rows_per_warp;         // set by the launch
+  int split;                 // warps that share 32 rows' runs, set by the launch
   unsigned* err;
 };
 cudaError_t launch_kv8_append(Kv8AppendParams& p, int D, cudaStream_t stream);

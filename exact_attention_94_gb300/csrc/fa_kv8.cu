@@ -22,8 +22,8 @@ namespace fa {
 namespace {
 
 constexpr int kAppendWarps = 4;
-constexpr long long kAppendMany = 152 * 64;  // warps that the SMs hold at once
-constexpr int kHeld = 16;  // vectors of a run that a lane holds in registers
+constexpr int kAppendBlocks = 7;  // CTAs per SM
+constexpr int kHeld = 8;  // vectors of a run that a lane holds in registers
 
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
   const float2 a = unpack_e4m3x2(w & 0xffffu), b = unpack_e4m3x2(w >> 16);
@@ -68,18 +68,20 @@ __device__ __forceinline__ uint2 encode8(const uint4& u, float inv) {
 // copies, 1 and 2 are two launches: an in-place run may rescale the very page
 // that another run copies from, and the copy has to read it first.
 template <int D>
-__global__ void __launch_bounds__(32 * kAppendWarps) fa_kv8_append_kernel(const Kv8AppendParams p, int pass) {
+__global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) fa_kv8_append_kernel(const Kv8AppendParams p, int pass) {
   constexpr int LPR = D / 8;     // lanes per row, 8 elements each
   constexpr int RPI = 32 / LPR;  // rows per iteration
   const int lane = lane_id();
   const long long unit = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-  const long long tile = unit / (2 * p.Hkv);
-  const int which = (int)(unit - tile * 2 * p.Hkv);
+  const long long part = unit / (2 * p.Hkv);
+  const int which = (int)(unit - part * 2 * p.Hkv);
+  const long long tile = part / p.split;
+  const int turn = (int)(part - tile * p.split);  // this warp's runs of the tile: every split-th one from here
   const int head = which % p.Hkv;
   const bool is_v = which >= p.Hkv;
-  const long long r0 = tile * p.rows_per_warp;
+  const long long r0 = tile * 32;
   if (r0 >= p.n) return;
-  const int rows = (int)min((long long)p.rows_per_warp, p.n - r0);
+  const int rows = (int)min(32ll, p.n - r0);
 
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(is_v ? p.v_new : p.k_new) + (size_t)head * D;
   const long long xs = is_v ? p.v_stride : p.k_stride;
@@ -98,6 +100,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) fa_kv8_append_kernel(const 
     if (lead && i > 0 && sl > 0 && sl < p.page_size) lead = !(p.page[i - 1] == pg && p.slot[i - 1] == sl - 1);
   }
   uint32_t todo = __ballot_sync(0xffffffffu, lead);
+  const int rank = __popc(todo & ((1u << lane) - 1u));
+  todo = __ballot_sync(0xffffffffu, lead && (unsigned)rank % (unsigned)p.split == (unsigned)turn);
   while (todo != 0) {
     const int l = __ffs(todo) - 1;
     todo &= todo - 1;
@@ -156,14 +160,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps) fa_kv8_append_kernel(const 
       amax = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
     }
     const float own = pow2_scale(amax);
-    const size_t at = (size_t)page * p.Hkv + head;
+    const size_t to = (size_t)page * p.Hkv + head;
     const size_t from = (size_t)(src >= 0 ? src : page) * p.Hkv + head;
     const float old = first > 0 ? scales[from] : 0.f;
     const float scale = fmaxf(old, own);
     const float inv = scale > 0.f ? 1.f / scale : 0.f;
     __syncwarp();
-    if (lane == 0) scales[at] = scale;
-    uint8_t* dst = codes + at * p.page_size * D + seg * 8;
+    if (lane == 0) scales[to] = scale;
+    uint8_t* dst = codes + to * p.page_size * D + seg * 8;
     // ---- older codes of the page
     if (first > 0 && (src >= 0 || scale != old)) {
       const uint8_t* old_codes = codes + from * p.page_size * D + seg * 8;
@@ -195,12 +199,13 @@ __global__ void __launch_bounds__(32 * kAppendWarps) fa_kv8_append_kernel(const 
 
 template <int D>
 static cudaError_t launch_kv8_append_t(Kv8AppendParams& p, cudaStream_t stream) {
-  // A warp looks at one row where there are few (its run's work starts at once,
-  // and warps whose row begins no run cost nothing but their launch), at 16
-  // where the launch itself would cost more than the runs.
-  p.rows_per_warp = (long long)p.n * 2 * p.Hkv > kAppendMany ? 16 : 1;
-  const long long units = ((long long)p.n + p.rows_per_warp - 1) / p.rows_per_warp * 2 * p.Hkv;
-  const long long blocks = (units + kAppendWarps - 1) / kAppendWarps;
+  // A warp looks at 32 rows and takes every split-th run that begins there: all
+  // of them where there are many rows (prompts: a run or two), fewer where the
+  // rows alone would leave SMs idle (a step of single tokens: 32 runs).
+  const long long tiles = ((long long)p.n + 31) / 32 * 2 * p.Hkv;
+  const long long split = 152ll * kAppendBlocks * kAppendWarps / tiles;
+  p.split = (int)(split < 1 ? 1 : split > 32 ? 32 : split);
+  const long long blocks = (tiles * p.split + kAppendWarps - 1) / kAppendWarps;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   for (int pass = p.copy_src != nullptr ? 1 : 0; pass <= (p.copy_src != nullptr ? 2 : 0); ++pass) {
     fa_kv8_append_kernel<D><<<(unsigned)blocks, 32 * kAppendWarps, 0, stream>>>(p, pass);

@@ -29,7 +29,7 @@ __device__ __forceinline__ float2 bf2(uint32_t w) {
 }  // namespace
 
 template <int D, bool NB, int BATCH>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int TPT = D / 16;  // threads per token and head: 8 pairs each
   const long long item = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) / TPT;
   const int j = threadIdx.x % TPT;
