@@ -65,7 +65,7 @@ SIGNATURES = {
     "fa_rope_axes": (_I, [_P] * 5 + [ctypes.POINTER(RopePlanStruct)] + [_I] * 4 + [_L] * 4 + [_I, _P]),
     "fa_kv8_append": (_I, [_P] * 9 + [_I] * 5 + [_L] * 2 + [_P]),
     "fa_decode_kv8": (_I, [_P] * 9 + [_I] * 11 + [_P, _F, _P]),
-    "fa_decode_kv8_num_shares": (_I, [_I] * 7),
+    "fa_decode_kv8_num_shares": (_I, [_I] * 6),
     "fa_decode_kv8_workspace_bytes": (_S, [_I] * 6),
     "fa_device_error": (_I, [ctypes.POINTER(ctypes.c_uint)]),
     "fa_selftest_wait_timeout": (_I, [ctypes.c_double, _P]),

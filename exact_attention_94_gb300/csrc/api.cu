@@ -877,9 +877,9 @@ size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int 
   return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float)) + ((size_t)B + 1) * sizeof(long long);
 }
 
-int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int d, int max_seq_len, int window_left) {
+int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left) {
   if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || max_seq_len < 1) return 1;
-  return kv8_auto_shares(B, Nq, Hkv, Hq / Hkv, kv8_span(Nq, max_seq_len, window_left), d);
+  return kv8_auto_shares(B, Nq, Hkv, Hq / Hkv, kv8_span(Nq, max_seq_len, window_left));
 }
 
 fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
@@ -905,7 +905,7 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   if (!ensure_init()) return FA_ERR_LAUNCH;
   Kv8DecodeParams p{};
   if (window_left >= max_seq_len) window_left = -1;  // a window past every key is no window
-  if (num_shares == 0) num_shares = fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, d, max_seq_len, window_left);
+  if (num_shares == 0) num_shares = fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, max_seq_len, window_left);
   const size_t rows = 2 * (size_t)num_shares * kv8_row_tile(Nq * (Hq / Hkv));
   const size_t o_bytes = align256(rows * d * sizeof(float)), l_bytes = align256(rows * sizeof(float));
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -56,13 +56,14 @@ constexpr float kLeastScale = -100.f;  // log2 of a value scale, from below: a p
 constexpr int kLead(int RT) { return 4 + RT / 16; }  // what a unit's start and end cost, in tiles
 constexpr float kNoRef = -3.0e38f;   // reference of a row that has seen no key
 
+// CTAs per SM: three where their registers allow it.
+constexpr int kv8_ctas_per_sm(int RT) { return RT <= 8 ? 3 : 2; }
+
 template <int D, int RT>
 struct Layout {
   static constexpr uint32_t kSlot = 128u * D;                                // a tile of K or V
-  // CTAs per SM.  A tile costs a CTA about 1.1 us whatever its bytes, so the
-  // half-size tiles of d = 64 want three at once where registers allow it.
-  static constexpr int kCtas = D == 64 && RT <= 8 ? 3 : 2;
-  static constexpr int kSlots = D == 64 ? (kCtas == 3 ? 8 : RT == 32 ? 8 : 12) : RT == 32 ? 4 : 6;  // ring: K0 V0 K1 V1 ...
+  static constexpr int kCtas = kv8_ctas_per_sm(RT);
+  static constexpr int kSlots = D == 64 ? (kCtas == 3 ? 8 : RT == 32 ? 8 : 12) : RT == 32 || kCtas == 3 ? 4 : 6;  // ring: K0 V0 K1 V1 ...
   static constexpr int kNS = 2 * RT < 16 ? 16 : 2 * RT;                      // columns of S
   static constexpr int kNP = (3 * RT + 15) / 16 * 16;                        // columns of P and O
   static constexpr uint32_t kUsed = 2 * kNS + kNP;
@@ -771,20 +772,34 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
     if (ka == kb) return;
   }
   auto slot_of = [&](int k) { return (2 * (long long)k + (share_begin(total, shares, k) < u0 ? 1 : 0)) * RT + r; };
-  float m = -INFINITY;
-  for (int k = ka + lane; k <= kb; k += 32) m = fmaxf(m, p.part_lse[slot_of(k)]);
-  m = warp_max(m);
-  float acc[E], wsum = 0.f;
+  // four shares at a time, their loads together, against a running maximum
+  float acc[E], wsum = 0.f, m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int k = ka; k <= kb; ++k) {
-    const long long sl = slot_of(k);
-    const float lc = p.part_lse[sl];
-    const float wc = lc == -INFINITY ? 0.f : ex2_sfu(lc - m);
-    wsum += wc;
-    const float* src = p.part_o + sl * D + lane * E;
+  for (int k0 = ka; k0 <= kb; k0 += 4) {
+    float lc[4], v[4][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(wc, src[e], acc[e]);
+    for (int x = 0; x < 4; ++x) {
+      const bool on = k0 + x <= kb;
+      const long long sl = slot_of(on ? k0 + x : kb);
+      lc[x] = on ? p.part_lse[sl] : -INFINITY;
+      const float* src = p.part_o + sl * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[x][e] = src[e];
+    }
+    const float mn = fmaxf(fmaxf(fmaxf(lc[0], lc[1]), fmaxf(lc[2], lc[3])), m), ref = mn == -INFINITY ? 0.f : mn;
+    const float al = ex2_sfu(m - ref);
+    m = mn;
+    wsum *= al;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= al;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float wc = ex2_sfu(lc[x] - ref);
+      wsum += wc;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(wc, v[x][e], acc[e]);
+    }
   }
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at * D + lane * E);
@@ -798,19 +813,19 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
 int kv8_row_tile(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 // CTAs that run at once, and the most tiles a call can have.
-static int kv8_ctas(int Nq, int group, int D) {
+static int kv8_ctas(int Nq, int group) {
   int dev = 0, n_sm = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-  return n_sm * (D == 64 && kv8_row_tile(Nq * group) <= 8 ? Layout<64, 8>::kCtas : Layout<128, 8>::kCtas);
+  return n_sm * kv8_ctas_per_sm(kv8_row_tile(Nq * group));
 }
 static long long kv8_most_tiles(int B, int Nq, int Hkv, int group, int span) {
   const int rows = Nq * group, rt = kv8_row_tile(rows);
   return (long long)B * Hkv * ((rows + rt - 1) / rt) * (((long long)span + kKv8Tile - 1) / kKv8Tile);
 }
 
-int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span, int D) {
+int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span) {
   const long long tiles = kv8_most_tiles(B, Nq, Hkv, group, span);
-  const int ctas = kv8_ctas(Nq, group, D);
+  const int ctas = kv8_ctas(Nq, group);
   return (int)(tiles < 1 ? 1 : tiles < ctas ? tiles : ctas);
 }
 
@@ -824,7 +839,7 @@ static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8
   if (e != cudaSuccess) return e;
   p.row_tiles = (p.Nq * p.group + RT - 1) / RT;
   // Where a share is a tile or less, nothing is gained by making room for starts.
-  p.lead = kv8_most_tiles(p.B, p.Nq, p.Hkv, p.group, span) > kv8_ctas(p.Nq, p.group, D) ? kLead(RT) : 0;
+  p.lead = kv8_most_tiles(p.B, p.Nq, p.Hkv, p.group, span) > kv8_ctas(p.Nq, p.group) ? kLead(RT) : 0;
   kern<<<shares, kThreads, smem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -861,7 +861,7 @@ def kv8_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, page, slot, cop
 def _kv8_shares(dev, B, Nq, Hq, Hkv, d, L, window_left, shares):
     """(shares, workspace bytes) of a call: they depend on its sizes and the device alone."""
     if shares == 0:
-        shares = lib().fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, d, L, window_left)
+        shares = lib().fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, L, window_left)
     return shares, max(16, lib().fa_decode_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, max(shares, 1)))
 
 

@@ -572,7 +572,7 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
                         int window_left, int num_shares, void* workspace, float scale, fa_stream_t stream);
 
 /* Shares fa_decode_kv8 uses when it is given num_shares = 0 (window_left as there). */
-int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int d, int max_seq_len, int window_left);
+int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left);
 size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_shares);
 
 /*

@@ -206,7 +206,7 @@ def test_bad_tables_and_lengths_are_reported():
 def test_a_captured_call_follows_the_lengths():
     case = make([700, 300], 1, 8, 2, 128, 16, seed=7)
     a = dev(case)
-    ws = torch.empty(_lib.load().fa_decode_kv8_workspace_bytes(2, 1, 8, 2, 128, 304), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(_lib.load().fa_decode_kv8_workspace_bytes(2, 1, 8, 2, 128, 456), dtype=torch.uint8, device="cuda")
     ops.decode_kv8(*a, 700, workspace=ws)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
