@@ -63,21 +63,27 @@ template <int D, int RT>
 struct Layout {
   static constexpr uint32_t kSlot = 128u * D;                                // a tile of K or V
   static constexpr int kCtas = kv8_ctas_per_sm(RT);
-  static constexpr int kSlots = D == 64 ? (kCtas == 3 ? 8 : RT == 32 ? 8 : 12) : RT == 32 || kCtas == 3 ? 4 : 6;  // ring: K0 V0 K1 V1 ...
+  static constexpr int kSlots = D == 64 ? 8 : 4;  // ring: K0 V0 K1 V1 ...
   static constexpr int kNS = 2 * RT < 16 ? 16 : 2 * RT;                      // columns of S
   static constexpr int kNP = (3 * RT + 15) / 16 * 16;                        // columns of P and O
   static constexpr uint32_t kUsed = 2 * kNS + kNP;
   static constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;  // TMEM columns, two CTAs' 512 at most
   static constexpr uint32_t kPOff = kSlots * kSlot;
-  static constexpr uint32_t kQOff = kPOff + kNP * 128u;
+  // (P's rows past 3 RT, whole eights of them, are no rows of its own: the product's columns there are not read)
+  static constexpr uint32_t kQOff = kPOff + (3 * RT + 7) / 8 * 1024u;
   static constexpr uint32_t kScOff = kQOff + kNS * (uint32_t)D;              // per V slot: 8 key scales, 8 value scales
   static constexpr uint32_t kScBytes = 64;
   static constexpr uint32_t kMaxOff = kScOff + kSlots / 2 * kScBytes;        // [4][RT] each: warps' maxima, sums, references, factors
   static constexpr uint32_t kRowOff = kMaxOff + (16 + 8) * RT * 4;           // (and [4][RT] output rows, 8 bytes each) two of: [RT] query scales, [RT] positions
   static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // [2][4] votes, scan, start
-  static constexpr uint32_t kWalkOff = kMiscOff + 128;                       // [6] the warps' walks
-  static constexpr uint32_t kBarOff = kWalkOff + 6 * 32;
-  static constexpr uint32_t kBytes = kBarOff + 8 * (2 * kSlots + 6) + 16 + 1024;
+  // pieces announced ahead of their tiles, with their rows of Q as they lie in memory
+  static constexpr int kPieces = RT == 8 && D == 128 ? 1 : RT <= 8 ? 4 : 2;  // as many as the CTAs leave room for
+  static constexpr uint32_t kPieceOff = kMiscOff + 128;                      // [kPieces] and the producer's [4], 32 bytes each
+  static constexpr uint32_t kStageOff = (kPieceOff + (kPieces + 4) * 32 + 127) / 128 * 128;
+  static constexpr uint32_t kStage = RT * D * 2u;
+  static constexpr uint32_t kBarOff = kStageOff + kPieces * kStage;
+  static constexpr int kBars = 2 * kSlots + 6 + 2 * kPieces;
+  static constexpr uint32_t kBytes = kBarOff + 8 * kBars + 16 + 1024;
   static_assert(kUsed <= 256, "TMEM columns");
 };
 
@@ -118,49 +124,42 @@ __device__ __forceinline__ long long kv8_weight(const Kv8DecodeParams& p, int ti
   return tiles > 0 ? tiles + p.lead : 0;
 }
 
-// A piece of a share: tiles t0 .. t1 - 1 of unit u (K/V head and row tile) of request b.
+// A piece of a share: tiles t0 .. t1 - 1 of unit u (K/V head and row tile) of
+// request b; t0 = t1 marks the share's end.
 struct Piece {
-  int b, u, t0, t1, tiles, len, beg;
+  int b, u, t0, t1, tiles, len, beg, pad;
 };
 
-// Walks a CTA's share piece by piece.  Every warp walks for itself; its state
-// lies in shared memory, so that it holds no registers over the tiles.
+// The producer's walk over the share, piece by piece.
 struct Walk {
   long long left;  // weight of the share still to come
   long long off;   // next slot within the weight of the request's units
   int b, tiles, len;
+  int len_next;    // length of request b + 1, read long before it is needed
 
-};
-
-__device__ __forceinline__ bool next_piece(Walk* walk, const Kv8DecodeParams& p, int units, Piece& s) {
-  Walk w = *walk;
-  bool found = false;
-  while (w.left > 0 && !found) {
-    const int each = w.tiles + p.lead;
-    if (w.tiles == 0 || w.off >= (long long)each * units) {  // the request's units are done (or it has no keys)
-      w.off = 0;
-      ++w.b;
-      w.len = kv8_len(p, w.b);
-      w.tiles = kv8_tiles(p, w.len);
-      continue;
+  __device__ __forceinline__ Piece next(const Kv8DecodeParams& p, int units) {
+    Piece s{};
+    while (left > 0) {
+      const int each = tiles + p.lead;
+      if (tiles == 0 || off >= (long long)each * units) {  // the request's units are done (or it has no keys)
+        off = 0;
+        ++b;
+        len = len_next;
+        tiles = kv8_tiles(p, len);
+        len_next = b + 1 < p.B ? kv8_len(p, b + 1) : 0;
+        continue;
+      }
+      const int u = (int)quick_div(off, each);
+      const int w0 = (int)(off - (long long)u * each), w1 = (int)(left < each - w0 ? w0 + left : each);
+      off += w1 - w0;
+      left -= w1 - w0;
+      s = {b, u, max(w0 - p.lead, 0), max(w1 - p.lead, 0), tiles, len, kv8_begin(p, len), 0};
+      if (s.t0 < s.t1) return s;
     }
-    s.b = w.b;
-    s.u = (int)quick_div(w.off, each);
-    const int w0 = (int)(w.off - (long long)s.u * each), w1 = (int)(w.left < each - w0 ? w0 + w.left : each);
-    w.off += w1 - w0;
-    w.left -= w1 - w0;
-    s.t0 = max(w0 - p.lead, 0);
-    s.t1 = max(w1 - p.lead, 0);
-    s.tiles = w.tiles;
-    s.len = w.len;
-    s.beg = kv8_begin(p, w.len);
-    found = s.t0 < s.t1;
+    s.t0 = s.t1 = 0;
+    return s;
   }
-  __syncwarp();
-  if (lane_id() == 0) *walk = w;
-  __syncwarp();
-  return found;
-}
+};
 
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r) {
@@ -230,14 +229,17 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
   auto EMPTY = [&](int s) { return bars + 8u * (uint32_t)(NSL + s); };
   const uint32_t SF = bars + 16u * NSL;  // S ready [2]; then P ready, O ready, the warps' exchange, Q ready
   const uint32_t PF = SF + 16, OF = SF + 24, XB = SF + 32, QB = SF + 40;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::kBarOff + 16 * NSL + 48);
-  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sb + L::kBarOff + 16 * NSL + 52);
+  auto HERE = [&](int s) { return SF + 48 + 8u * (uint32_t)s; };                  // piece announced
+  auto TAKEN = [&](int s) { return SF + 48 + 8u * (uint32_t)(L::kPieces + s); };  // and taken by its five readers
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::kBarOff + 8 * L::kBars);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sb + L::kBarOff + 8 * L::kBars + 4);
+  Piece* s_piece = reinterpret_cast<Piece*>(sb + L::kPieceOff);
   int* s_vote = reinterpret_cast<int*>(sb + L::kMiscOff);                       // [2][4]
   long long* s_scan = reinterpret_cast<long long*>(sb + L::kMiscOff + 32);      // [6] warps' sums
   volatile long long* s_start = reinterpret_cast<volatile long long*>(sb + L::kMiscOff + 80);  // b, off, tiles and len
 
   if (warp == 5) {
-    tmem_alloc(base + L::kBarOff + 16 * NSL + 52, L::kCols);
+    tmem_alloc(base + L::kBarOff + 8 * L::kBars + 4, L::kCols);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -249,6 +251,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     mbar_init(OF, 1);
     mbar_init(XB, 4);
     mbar_init(QB, 4);
+    for (int s = 0; s < L::kPieces; ++s) {
+      mbar_init(HERE(s), 1);
+      mbar_init(TAKEN(s), 5);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -298,94 +304,134 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS = tmem, tO = tmem + 2 * L::kNS;
   const WaitCtx w{abort_flag, p.timeout_ns, p.err};
-  Walk* walk = reinterpret_cast<Walk*>(sb + L::kWalkOff) + warp;
-  if (lane == 0) {
-    *walk = {to - from, 0, 0, 0, 0};
-    if (to > from) *walk = {to - from, s_start[1], (int)s_start[0], (int)(s_start[2] >> 32), (int)(s_start[2] & 0xffffffffll)};
-  }
-  __syncwarp();
-  Piece pc;
   bool ok = true;
   asm volatile("griddepcontrol.launch_dependents;");  // the merge may be set up; it waits for this grid's end
 
   if (warp == 4) {
     // ============================================================ producer
-    // Lane i of a batch of four tiles owns 16 keys: their page and its scales.
-    // The next batch's are read while this one's tiles are loaded.
+    // With the ring full, every load of the SM waits behind the ring's bytes, 2
+    // to 4 us, so nothing is read just before it is needed.  Tiles go in batches
+    // of four of a piece, lane i owning 16 keys.  When batch n's tiles have been
+    // asked for, batch n + 2's piece is announced if it is new, with its rows of
+    // Q, batch n + 2's scales are asked for, and batch n + 3's pages.  (An
+    // announcement waits until the piece kPieces before has been taken, that is
+    // until the one before that is done; its tiles lie in batch n at the latest.)
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
+    struct Batch {
+      int n;         // tiles, 0: none left
+      int first;     // number of the piece that begins (or the end) with this batch, or -1
+      int page, ph;  // page number; its K/V head's row in the tensor maps and the scales
+      int off;       // first key's slot
+      bool on;       // whether this lane's 16 keys exist
+      int hk;
+      float ks, vs;
+    };
+    Piece* s_ahead = s_piece + L::kPieces;  // [4] pieces fetched and not yet announced
+    Walk walk{to - from, 0, 0, 0, 0, 0};
+    if (to > from) {
+      const int b = (int)s_start[0];
+      walk = {to - from, s_start[1], b, (int)(s_start[2] >> 32), (int)(s_start[2] & 0xffffffffll),
+              b + 1 < p.B ? kv8_len(p, b + 1) : 0};
+    }
     const int bpb = p.box_rows / 16;  // 16-key groups per TMA box
-    int it = 0;                       // tiles of the share so far
-    while (ok && next_piece(walk, p, units, pc)) {
-      const int hk = pc.u / p.row_tiles;
-      const int g_first = (pc.beg + pc.t0 * kKv8Tile) / 16, g_end = min((pc.len + 15) / 16, g_first + (pc.t1 - pc.t0) * 8);
-      const int* table = p.block_table + (size_t)pc.b * p.max_blocks;
-      auto page_of = [&](int batch, int& page, int& off) {
-        const int g = g_first + batch * 32 + lane;
-        page = 0;
-        off = 0;
-        if (g >= g_end) return false;
-        const int blk = (int)((unsigned)(g * 16) / (unsigned)p.page_size);
-        off = g * 16 - blk * p.page_size;
-        page = table[blk];
-        return true;
-      };
-      auto checked = [&](int page, bool on) {  // report, and read a valid page instead
-        if (on && (page < 0 || page >= p.num_pages)) {
-          atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
-          return 0;
-        }
-        return page;
-      };
-      int page, off, page_n = 0, off_n = 0;
-      float ks = 0.f, vs = 0.f, ks_n = 0.f, vs_n = 0.f;
-      bool on = page_of(0, page, off), on_n = false;
-      page = checked(page, on);
-      if (on) {
-        ks = p.k_scale[(size_t)page * p.Hkv + hk];
-        vs = p.v_scale[(size_t)page * p.Hkv + hk];
+    Piece pc{};
+    int t_next = 0, pieces = 0;  // next tile of pc to fetch; pieces fetched
+    bool more = true;
+    auto fetch_pages = [&](Batch& q) {
+      q = {};
+      q.first = -1;
+      if (!more) return;
+      if (t_next == pc.t1) {
+        pc = walk.next(p, units);
+        t_next = pc.t0;
+        more = pc.t0 < pc.t1;
+        q.first = pieces++;
+        if (lane == 0) s_ahead[q.first & 3] = pc;
+        __syncwarp();
+        if (!more) return;
       }
-      for (int t = pc.t0; t < pc.t1; ++t, ++it) {
-        const int i = (t - pc.t0) & 3;
-        if (i == 0) {
-          if (t > pc.t0) page = page_n, off = off_n, on = on_n, ks = ks_n, vs = vs_n;
-          on_n = page_of(((t - pc.t0) >> 2) + 1, page_n, off_n);
-        }
-        const int boxes = (min(8, g_end - (g_first + 8 * (t - pc.t0))) + bpb - 1) / bpb;
+      q.n = min(4, pc.t1 - t_next);
+      const int g = (pc.beg + t_next * kKv8Tile) / 16 + lane;
+      q.on = lane < 8 * q.n && g < (pc.len + 15) / 16;
+      q.hk = (int)((unsigned)pc.u / (unsigned)p.row_tiles);
+      t_next += q.n;
+      if (q.on) {
+        const int blk = (int)((unsigned)(g * 16) / (unsigned)p.page_size);
+        q.off = g * 16 - blk * p.page_size;
+        q.page = p.block_table[(size_t)pc.b * p.max_blocks + blk];
+      }
+    };
+    auto announce = [&](const Batch& q) {
+      if (q.first < 0 || !ok) return;
+      const int st = q.first % L::kPieces;
+      if (q.first >= L::kPieces) ok = __all_sync(0xffffffffu, mbar_wait(TAKEN(st), (q.first / L::kPieces - 1) & 1, w, 50));
+      if (!ok) return;
+      const Piece s = s_ahead[q.first & 3];
+      const int x0 = s.u % p.row_tiles * RT, rows = s.t0 == s.t1 ? 0 : min(RT, p.Nq * p.group - x0);
+      if (lane == 0) {
+        s_piece[st] = s;
+        mbar_arrive_expect_tx(HERE(st), (uint32_t)(rows * D * 2));
+      }
+      __syncwarp();
+      if (lane < rows) {
+        const int x = x0 + lane, i = p.Nq == 1 ? 0 : (int)((unsigned)x / (unsigned)p.group);
+        const int h = (int)((unsigned)s.u / (unsigned)p.row_tiles) * p.group + x - i * p.group;
+        bulk_load(base + L::kStageOff + st * L::kStage + lane * D * 2,
+                  static_cast<const __nv_bfloat16*>(p.q) + (((size_t)s.b * p.Nq + i) * p.Hq + h) * D, D * 2, HERE(st));
+      }
+    };
+    auto fetch_scales = [&](Batch& q) {
+      if (q.on && (q.page < 0 || q.page >= p.num_pages)) {  // report, and read a valid page instead
+        atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
+        q.page = 0;
+      }
+      q.ph = q.page * p.Hkv + q.hk;
+      if (q.on) {
+        q.ks = p.k_scale[q.ph];
+        q.vs = p.v_scale[q.ph];
+      }
+    };
+    Batch now, next, after;
+    fetch_pages(now);
+    fetch_pages(next);
+    fetch_pages(after);
+    announce(now);
+    fetch_scales(now);
+    announce(next);
+    fetch_scales(next);
+    int it = 0;  // tiles of the share so far
+    while (ok && now.n > 0) {
+      const uint32_t on = __ballot_sync(0xffffffffu, now.on);
+      for (int i = 0; i < now.n; ++i, ++it) {
+        const int boxes = (__popc(on >> (8 * i) & 0xffu) + bpb - 1) / bpb;
         const uint32_t bytes = (uint32_t)(boxes * p.box_rows * D);
-        const bool issue = (lane >> 3) == i && on && (lane & (bpb - 1)) == 0;
+        const bool mine = (lane >> 3) == i, issue = mine && now.on && (lane & (bpb - 1)) == 0;
         const uint32_t at = (uint32_t)(lane & 7) * 16u * D;
-        const int ph = page * p.Hkv + hk;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int slot = (2 * it + v) % NSL, use = (2 * it + v) / NSL;
           if (use > 0) ok = mbar_wait(EMPTY(slot), (use - 1) & 1, w, 51);
           if (!__all_sync(0xffffffffu, ok)) break;
-          if (v == 1) {
-            if ((lane >> 3) == i) {
-              float* sc = reinterpret_cast<float*>(sb + L::kScOff + (slot >> 1) * L::kScBytes);
-              sc[lane & 7] = ks;
-              sc[8 + (lane & 7)] = vs;
-            }
-            __syncwarp();
+          if (issue) tma_load_3d(base + slot * L::kSlot + at, v ? &tm_v : &tm_k, FULL(slot), 0, now.off, now.ph);
+          if (v == 1 && mine) {  // the scales, behind the copies: they may still be on their way
+            float* sc = reinterpret_cast<float*>(sb + L::kScOff + (slot >> 1) * L::kScBytes);
+            sc[lane & 7] = now.ks;
+            sc[8 + (lane & 7)] = now.vs;
           }
-          if (lane == 0) mbar_arrive_expect_tx(FULL(slot), bytes);
           __syncwarp();
-          if (issue) tma_load_3d(base + slot * L::kSlot + at, v ? &tm_v : &tm_k, FULL(slot), 0, off, ph);
+          if (lane == 0) mbar_arrive_expect_tx(FULL(slot), bytes);
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (i == 2) {  // a next batch exists only if this one is full
-          page_n = checked(page_n, on_n);
-          ks_n = vs_n = 0.f;
-          if (on_n) {
-            ks_n = p.k_scale[(size_t)page_n * p.Hkv + hk];
-            vs_n = p.v_scale[(size_t)page_n * p.Hkv + hk];
-          }
-        }
       }
+      announce(after);
+      fetch_scales(after);
+      now = next;
+      next = after;
+      fetch_pages(after);
     }
   } else if (warp == 5) {
     // ============================================================ products
@@ -408,12 +454,16 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       mma_commit_w(OF);
       return true;
     };
-    int it = 0, piece = 0;
-    bool was_first = false;  // whether tile it - 1 was its piece's first
-    while (ok && next_piece(walk, p, units, pc)) {
+    for (int it = 0, piece = 0; ok; ++piece) {
+      const int st = piece % L::kPieces;
+      ok = __all_sync(0xffffffffu, mbar_wait(HERE(st), piece / L::kPieces & 1, w, 56));
+      if (!ok) break;
+      const int n = s_piece[st].t1 - s_piece[st].t0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(TAKEN(st));
+      if (n == 0) break;
       ok = __all_sync(0xffffffffu, mbar_wait(QB, piece & 1, w, 52));
-      ++piece;
-      for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
+      for (int t = 0; t < n && ok; ++t, ++it) {
         const int slot = (2 * it) % NSL;
         ok = __all_sync(0xffffffffu, mbar_wait(FULL(slot), (2 * it / NSL) & 1, w, 53));
         if (!ok) break;
@@ -425,11 +475,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
           mma_ss_f8_w(tS + (it & 1) * L::kNS, desc_add(kd, kk * 32), desc_add(qd, kk * 32), IDESC_S, kk > 0);
         mma_commit_w(EMPTY(slot));
         mma_commit_w(SF + 8u * (it & 1));
-        if (it > 0) ok = pv(it - 1, was_first);
-        was_first = t == pc.t0;
+        if (t > 0) ok = pv(it - 1, t == 1);
       }
+      if (ok) ok = pv(it - 1, n == 1);
     }
-    if (ok && it > 0) ok = pv(it - 1, was_first);
   } else {
     // ============================================================ softmax
     float* s_max = reinterpret_cast<float*>(sb + L::kMaxOff);
@@ -448,24 +497,28 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       h = (int)((unsigned)s.u / (unsigned)p.row_tiles) * p.group + x - i * p.group;
       return ((size_t)s.b * p.Nq + i) * p.Hq + h;
     };
-    // ---- Q: a warp per row, split into two e4m3 parts at the row's power of two
-    auto load_q = [&](const Piece& s, int piece) {
+    // ---- the next piece, and its Q: rows in turn for the warps, split into two
+    // e4m3 parts at each row's power of two
+    auto take = [&](int piece, Piece& s) {
+      const int st = piece % L::kPieces;
+      if (!__all_sync(0xffffffffu, mbar_wait(HERE(st), piece / L::kPieces & 1, w, 63))) return false;
+      s = s_piece[st];
       float* s_qsc = reinterpret_cast<float*>(sb + L::kRowOff + (piece & 1) * 2 * RT * 4);
       int* s_pos = reinterpret_cast<int*>(s_qsc + RT);
-      const int rows = rows_of(s);
+      const int rows = s.t0 == s.t1 ? 0 : rows_of(s);
       constexpr int LPR = D / 8, RPW = 32 / LPR;                // lanes per row, rows per warp and pass
       constexpr int PASSES = (RT + 4 * RPW - 1) / (4 * RPW);
       const int sub = lane / LPR, seg = lane % LPR;
       uint4 q[PASSES];
-      int pos[PASSES];
 #pragma unroll
       for (int x = 0; x < PASSES; ++x) {
         const int r = (x * 4 + warp) * RPW + sub;
         q[x] = make_uint4(0u, 0u, 0u, 0u);
-        int i = 0, h;
-        if (r < rows) q[x] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + q_row(s, r, i, h) * D + seg * 8);
-        pos[x] = s.len - p.Nq + i;
+        if (r < rows) q[x] = *reinterpret_cast<const uint4*>(sb + L::kStageOff + st * L::kStage + r * D * 2 + seg * 16);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(TAKEN(st));
+      if (rows == 0) return true;
 #pragma unroll
       for (int x = 0; x < PASSES; ++x) {
         const int r = (x * 4 + warp) * RPW + sub;
@@ -505,14 +558,16 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
             *reinterpret_cast<uint2*>(sb + L::kQOff + at + (seg & 1) * 8) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
           }
           if (seg == 0) {
+            const int y = s.u % p.row_tiles * RT + r;
             s_qsc[r] = sc * p.scale_log2;
-            s_pos[r] = pos[x];
+            s_pos[r] = s.len - p.Nq + (p.Nq == 1 || r >= rows ? 0 : (int)((unsigned)y / (unsigned)p.group));
           }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(QB);
+      return true;
     };
 
     int it = 0, piece = 0;
@@ -522,9 +577,9 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       if (lane == 0) mbar_arrive(XB);
       return __all_sync(0xffffffffu, mbar_wait(XB, xphase++ & 1, w, 60));
     };
-    bool have = next_piece(walk, p, units, pc);
-    if (have) load_q(pc, 0);
-    while (have) {
+    Piece pc;
+    ok = take(0, pc);
+    while (ok && pc.t0 < pc.t1) {
       const float* s_qsc = reinterpret_cast<const float*>(sb + L::kRowOff + (piece & 1) * 2 * RT * 4);
       const int* s_pos = reinterpret_cast<const int*>(s_qsc + RT);
       const int rows = rows_of(pc);
@@ -672,10 +727,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
         if (lane == 0) mbar_arrive(PF);
       }
       if (!ok) break;
-      // ---- the next piece's Q, while this one's last products run (its scores are all read)
+      // ---- the next piece's Q, while this one's last products run (its scores are all read, so Q is free)
       const Piece done = pc;
-      have = next_piece(walk, p, units, pc);
-      if (have) load_q(pc, piece + 1);
+      ok = take(piece + 1, pc);
+      if (!ok) break;
       // ---- each row's sum over the 128 key lanes
       const float row_sum = warp_row_sums<RT>(l, lane);
       if (lane % (32 / RT) == 0) s_sum[warp * RT + lane / (32 / RT)] = row_sum;
