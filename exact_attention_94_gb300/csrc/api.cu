@@ -874,7 +874,7 @@ static int kv8_span(int Nq, int max_seq_len, int window_left) {
 size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_shares) {
   if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || d < 1 || num_shares < 1) return 0;
   const size_t rows = 2 * (size_t)num_shares * kv8_row_tile(Nq * (Hq / Hkv));
-  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float)) + ((size_t)B + 1) * sizeof(long long);
+  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float));
 }
 
 int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left) {
@@ -886,7 +886,7 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
                         const float* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse, int B,
                         int Nq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_blocks, int max_seq_len,
                         int window_left, int num_shares, void* workspace, float scale, fa_stream_t stream) {
-  if (B < 1 || B > 65535 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (long long)Nq * Hq > 65535)
+  if (B < 1 || B > 16384 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (long long)Nq * Hq > 65535)
     return FA_ERR_INVALID_ARG;
   if (num_pages < 1 || max_blocks < 1 || max_seq_len < 0 || num_shares < 0 || num_shares > 65535 || window_left < -1)
     return FA_ERR_INVALID_ARG;
@@ -907,7 +907,6 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   if (window_left >= max_seq_len) window_left = -1;  // a window past every key is no window
   if (num_shares == 0) num_shares = fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, max_seq_len, window_left);
   const size_t rows = 2 * (size_t)num_shares * kv8_row_tile(Nq * (Hq / Hkv));
-  const size_t o_bytes = align256(rows * d * sizeof(float)), l_bytes = align256(rows * sizeof(float));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = q;
   p.k_codes = static_cast<const uint8_t*>(k_codes);
@@ -919,8 +918,7 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   p.o = o;
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws);
-  p.part_lse = reinterpret_cast<float*>(ws + o_bytes);
-  p.first_slot = reinterpret_cast<long long*>(ws + o_bytes + l_bytes);
+  p.part_lse = reinterpret_cast<float*>(ws + align256(rows * d * sizeof(float)));
   p.B = B;
   p.Nq = Nq;
   p.Hq = Hq;

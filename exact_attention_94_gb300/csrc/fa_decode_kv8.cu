@@ -53,7 +53,7 @@ constexpr int kThreads = 192;
 constexpr float kAtRef = 64.f;       // p at the reference
 constexpr float kHeadroom = 2.8f;    // log2(448 / 64), rounded down
 constexpr float kLeastScale = -100.f;  // log2 of a value scale, from below: a page of zeros counts as one of 2^-100
-constexpr int kLead(int RT) { return 4 + RT / 16; }  // what a unit's start and end cost, in tiles
+constexpr int kLead(int RT) { return 3 + RT / 16; }  // what a unit's start and end cost, in tiles
 constexpr float kNoRef = -3.0e38f;   // reference of a row that has seen no key
 
 // CTAs per SM: three where their registers allow it.
@@ -78,8 +78,8 @@ struct Layout {
   static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // [2][4] votes, scan, start
   // pieces announced ahead of their tiles, with their rows of Q as they lie in memory
   static constexpr int kPieces = RT == 8 && D == 128 ? 1 : RT <= 8 ? 4 : 2;  // as many as the CTAs leave room for
-  static constexpr uint32_t kPieceOff = kMiscOff + 128;                      // [kPieces] and the producer's [4], 32 bytes each
-  static constexpr uint32_t kStageOff = (kPieceOff + (kPieces + 4) * 32 + 127) / 128 * 128;
+  static constexpr uint32_t kPieceOff = kMiscOff + 128;                      // [kPieces] 32 bytes each
+  static constexpr uint32_t kStageOff = (kPieceOff + kPieces * 32 + 127) / 128 * 128;
   static constexpr uint32_t kStage = RT * D * 2u;
   static constexpr uint32_t kBarOff = kStageOff + kPieces * kStage;
   static constexpr int kBars = 2 * kSlots + 6 + 2 * kPieces;
@@ -88,14 +88,14 @@ struct Layout {
 };
 
 // A request's length as the kernels use it: clamped into [0, max_len], a length outside reported.
-__device__ __forceinline__ int kv8_len(const Kv8DecodeParams& p, int b) {
-  int n = p.seq_lens[b];
+__device__ __forceinline__ int kv8_clamp(const Kv8DecodeParams& p, int n) {
   if (n < 0 || n > p.max_len) {
     atomicCAS(p.err, 0u, FA_DEVERR_BAD_SEQLEN);
     n = n < 0 ? 0 : p.max_len;
   }
   return n;
 }
+__device__ __forceinline__ int kv8_len(const Kv8DecodeParams& p, int b) { return kv8_clamp(p, p.seq_lens[b]); }
 
 // First key any of the request's queries sees, rounded down to a tile; tiles from there.
 __device__ __forceinline__ int kv8_begin(const Kv8DecodeParams& p, int len) {
@@ -135,7 +135,7 @@ struct Walk {
   long long left;  // weight of the share still to come
   long long off;   // next slot within the weight of the request's units
   int b, tiles, len;
-  int len_next;    // length of request b + 1, read long before it is needed
+  int len_next;    // seq_lens[b + 1], read long before it is needed
 
   __device__ __forceinline__ Piece next(const Kv8DecodeParams& p, int units) {
     Piece s{};
@@ -144,9 +144,9 @@ struct Walk {
       if (tiles == 0 || off >= (long long)each * units) {  // the request's units are done (or it has no keys)
         off = 0;
         ++b;
-        len = len_next;
+        len = kv8_clamp(p, len_next);
         tiles = kv8_tiles(p, len);
-        len_next = b + 1 < p.B ? kv8_len(p, b + 1) : 0;
+        len_next = b + 1 < p.B ? p.seq_lens[b + 1] : 0;
         continue;
       }
       const int u = (int)quick_div(off, each);
@@ -244,7 +244,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     tc_fence_before();
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2 * NSL; ++s) mbar_init(FULL(s), 1);
+    for (int s = 0; s < NSL; ++s) {
+      mbar_init(FULL(s), s & 1 ? 9 : 1);  // (values: the copy's bytes, and eight lanes' scales)
+      mbar_init(EMPTY(s), 1);
+    }
     mbar_init(SF, 1);
     mbar_init(SF + 8, 1);
     mbar_init(PF, 4);
@@ -292,14 +295,6 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       at += kv8_weight(p, tiles) * units;
     }
   }
-  if (k == 0) {  // for the merge: where the requests' weights begin
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      p.first_slot[b] = at;
-      at += kv8_weight(p, kv8_tiles(p, kv8_len(p, b))) * units;
-    }
-    if (threadIdx.x == 0) p.first_slot[p.B] = total;
-  }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS = tmem, tO = tmem + 2 * L::kNS;
@@ -310,48 +305,62 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
   if (warp == 4) {
     // ============================================================ producer
     // With the ring full, every load of the SM waits behind the ring's bytes, 2
-    // to 4 us, so nothing is read just before it is needed.  Tiles go in batches
-    // of four of a piece, lane i owning 16 keys.  When batch n's tiles have been
-    // asked for, batch n + 2's piece is announced if it is new, with its rows of
-    // Q, batch n + 2's scales are asked for, and batch n + 3's pages.  (An
-    // announcement waits until the piece kPieces before has been taken, that is
-    // until the one before that is done; its tiles lie in batch n at the latest.)
+    // to 4 us, so no register waits for one that was just asked for.  Tiles go in
+    // batches of four of a piece, lane i owning 16 keys.  Page numbers are read
+    // two batches ahead (and moved to their place one later, when they have
+    // come); scales are copied asynchronously to the tile's place, and arrive on
+    // its barrier.  A piece is announced when its first batch's pages are read,
+    // with its rows of Q.  (That waits until the piece kPieces before has been
+    // taken, that is until the one before that is done; its tiles have all been
+    // asked for by then.)
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
     struct Batch {
-      int n;         // tiles, 0: none left
-      int first;     // number of the piece that begins (or the end) with this batch, or -1
-      int page, ph;  // page number; its K/V head's row in the tensor maps and the scales
-      int off;       // first key's slot
-      bool on;       // whether this lane's 16 keys exist
+      int n;     // tiles, 0: none left
+      int page;  // this lane's 16 keys: page, slot of the first, whether they exist
+      int off;
+      bool on;
       int hk;
-      float ks, vs;
     };
-    Piece* s_ahead = s_piece + L::kPieces;  // [4] pieces fetched and not yet announced
     Walk walk{to - from, 0, 0, 0, 0, 0};
     if (to > from) {
       const int b = (int)s_start[0];
       walk = {to - from, s_start[1], b, (int)(s_start[2] >> 32), (int)(s_start[2] & 0xffffffffll),
-              b + 1 < p.B ? kv8_len(p, b + 1) : 0};
+              b + 1 < p.B ? p.seq_lens[b + 1] : 0};
     }
     const int bpb = p.box_rows / 16;  // 16-key groups per TMA box
     Piece pc{};
     int t_next = 0, pieces = 0;  // next tile of pc to fetch; pieces fetched
     bool more = true;
-    auto fetch_pages = [&](Batch& q) {
+    auto announce = [&]() {
+      const int st = pieces % L::kPieces;
+      if (pieces >= L::kPieces) ok = __all_sync(0xffffffffu, mbar_wait(TAKEN(st), (pieces / L::kPieces - 1) & 1, w, 50));
+      if (!ok) return;
+      const int x0 = pc.u % p.row_tiles * RT, rows = more ? min(RT, p.Nq * p.group - x0) : 0;
+      if (lane == 0) {
+        s_piece[st] = pc;
+        mbar_arrive_expect_tx(HERE(st), (uint32_t)(rows * D * 2));
+      }
+      __syncwarp();
+      if (lane < rows) {
+        const int x = x0 + lane, i = p.Nq == 1 ? 0 : (int)((unsigned)x / (unsigned)p.group);
+        const int h = (int)((unsigned)pc.u / (unsigned)p.row_tiles) * p.group + x - i * p.group;
+        bulk_load(base + L::kStageOff + st * L::kStage + lane * D * 2,
+                  static_cast<const __nv_bfloat16*>(p.q) + (((size_t)pc.b * p.Nq + i) * p.Hq + h) * D, D * 2, HERE(st));
+      }
+      ++pieces;
+    };
+    auto fetch = [&](Batch& q) {
       q = {};
-      q.first = -1;
-      if (!more) return;
+      if (!more || !ok) return;
       if (t_next == pc.t1) {
         pc = walk.next(p, units);
         t_next = pc.t0;
         more = pc.t0 < pc.t1;
-        q.first = pieces++;
-        if (lane == 0) s_ahead[q.first & 3] = pc;
-        __syncwarp();
-        if (!more) return;
+        announce();
+        if (!more || !ok) return;
       }
       q.n = min(4, pc.t1 - t_next);
       const int g = (pc.beg + t_next * kKv8Tile) / 16 + lane;
@@ -364,46 +373,16 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
         q.page = p.block_table[(size_t)pc.b * p.max_blocks + blk];
       }
     };
-    auto announce = [&](const Batch& q) {
-      if (q.first < 0 || !ok) return;
-      const int st = q.first % L::kPieces;
-      if (q.first >= L::kPieces) ok = __all_sync(0xffffffffu, mbar_wait(TAKEN(st), (q.first / L::kPieces - 1) & 1, w, 50));
-      if (!ok) return;
-      const Piece s = s_ahead[q.first & 3];
-      const int x0 = s.u % p.row_tiles * RT, rows = s.t0 == s.t1 ? 0 : min(RT, p.Nq * p.group - x0);
-      if (lane == 0) {
-        s_piece[st] = s;
-        mbar_arrive_expect_tx(HERE(st), (uint32_t)(rows * D * 2));
-      }
-      __syncwarp();
-      if (lane < rows) {
-        const int x = x0 + lane, i = p.Nq == 1 ? 0 : (int)((unsigned)x / (unsigned)p.group);
-        const int h = (int)((unsigned)s.u / (unsigned)p.row_tiles) * p.group + x - i * p.group;
-        bulk_load(base + L::kStageOff + st * L::kStage + lane * D * 2,
-                  static_cast<const __nv_bfloat16*>(p.q) + (((size_t)s.b * p.Nq + i) * p.Hq + h) * D, D * 2, HERE(st));
-      }
-    };
-    auto fetch_scales = [&](Batch& q) {
-      if (q.on && (q.page < 0 || q.page >= p.num_pages)) {  // report, and read a valid page instead
-        atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
-        q.page = 0;
-      }
-      q.ph = q.page * p.Hkv + q.hk;
-      if (q.on) {
-        q.ks = p.k_scale[q.ph];
-        q.vs = p.v_scale[q.ph];
-      }
-    };
-    Batch now, next, after;
-    fetch_pages(now);
-    fetch_pages(next);
-    fetch_pages(after);
-    announce(now);
-    fetch_scales(now);
-    announce(next);
-    fetch_scales(next);
+    Batch now, next;
+    fetch(now);
+    fetch(next);
     int it = 0;  // tiles of the share so far
     while (ok && now.n > 0) {
+      if (now.on && (now.page < 0 || now.page >= p.num_pages)) {  // report, and read a valid page instead
+        atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
+        now.page = 0;
+      }
+      const int ph = now.page * p.Hkv + now.hk;
       const uint32_t on = __ballot_sync(0xffffffffu, now.on);
       for (int i = 0; i < now.n; ++i, ++it) {
         const int boxes = (__popc(on >> (8 * i) & 0xffu) + bpb - 1) / bpb;
@@ -415,24 +394,29 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
           const int slot = (2 * it + v) % NSL, use = (2 * it + v) / NSL;
           if (use > 0) ok = mbar_wait(EMPTY(slot), (use - 1) & 1, w, 51);
           if (!__all_sync(0xffffffffu, ok)) break;
-          if (issue) tma_load_3d(base + slot * L::kSlot + at, v ? &tm_v : &tm_k, FULL(slot), 0, now.off, now.ph);
-          if (v == 1 && mine) {  // the scales, behind the copies: they may still be on their way
-            float* sc = reinterpret_cast<float*>(sb + L::kScOff + (slot >> 1) * L::kScBytes);
-            sc[lane & 7] = now.ks;
-            sc[8 + (lane & 7)] = now.vs;
+          if (lane == 0) mbar_arrive_expect_tx(FULL(slot), bytes);
+          __syncwarp();
+          if (issue) tma_load_3d(base + slot * L::kSlot + at, v ? &tm_v : &tm_k, FULL(slot), 0, now.off, ph);
+          if (v == 1 && mine) {
+            float* sc = reinterpret_cast<float*>(sb + L::kScOff + (slot >> 1) * L::kScBytes) + (lane & 7);
+            if (now.on) {
+              cp_async4(smem_u32(sc), p.k_scale + ph);
+              cp_async4(smem_u32(sc + 8), p.v_scale + ph);
+              cp_async_arrive(FULL(slot));  // one of the barrier's eight more arrivals, when the copies are there
+            } else {
+              sc[0] = sc[8] = 0.f;
+              mbar_arrive(FULL(slot));
+            }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(FULL(slot), bytes);
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
-      announce(after);
-      fetch_scales(after);
       now = next;
-      next = after;
-      fetch_pages(after);
+      fetch(next);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 5) {
     // ============================================================ products
     constexpr uint32_t IDESC_S = idesc_e4m3(128, L::kNS), IDESC_O = idesc_e4m3(D, L::kNP, true);
@@ -800,68 +784,88 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
 }
 
 // What the shares' borders cut, and requests without keys.  One warp per query
-// row: the row's unit lies in the shares ka .. kb; one share alone has finished it.
+// row: the row's unit lies in the shares ka .. kb; one share alone has finished
+// it.  Where the work begins and ends is added up again from the lengths, by
+// each block, which needs nothing of the main kernel and so is done while that
+// one ends.
 template <int D>
 __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_constant__ Kv8DecodeParams p, int RT,
                                                                   int shares) {
   constexpr int E = D / 32;
-  const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = lane_id();
-  if (at >= (long long)p.B * p.Nq * p.Hq) return;
-  const unsigned per = (unsigned)(p.Nq * p.Hq);  // (at most 65535)
-  const int b = (int)(at / per), x0 = (int)(at - (long long)b * per);
-  const int i = (int)((unsigned)x0 / (unsigned)p.Hq), h = x0 - i * p.Hq;
-  const int hk = (int)((unsigned)h / (unsigned)p.group), x = i * p.group + h - hk * p.group;  // row of the K/V head
+  const int lane = lane_id(), units = p.Hkv * p.row_tiles;
+  const int b = blockIdx.y;
+  __shared__ long long s_before[8], s_all[8];
+  long long before = 0, total = 0;
+  for (int y = threadIdx.x; y < p.B; y += 256) {
+    const int n = p.seq_lens[y];
+    const long long wt = kv8_weight(p, kv8_tiles(p, min(max(n, 0), p.max_len))) * units;
+    total += wt;
+    if (y < b) before += wt;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  if (lane == 0) s_before[threadIdx.x >> 5] = before, s_all[threadIdx.x >> 5] = total;
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int y = 0; y < 8; ++y) before += s_before[y], total += s_all[y];
+  const long long weight = kv8_weight(p, kv8_tiles(p, min(max(p.seq_lens[b], 0), p.max_len)));
+  const long long each = quick_div(total, shares), more = total - each * shares;
+  auto share_of = [&](long long t) {
+    return (int)(t < more * (each + 1) ? quick_div(t, each + 1) : more + quick_div(t - more * (each + 1), each));
+  };
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done
-  const int units = p.Hkv * p.row_tiles, u = hk * p.row_tiles + x / RT, r = x % RT;
-  const long long total = p.first_slot[p.B], first = p.first_slot[b];
-  const long long weight = quick_div(p.first_slot[b + 1] - first, units), u0 = first + u * weight;
-  int ka = 0, kb = -1;
-  if (weight > 0) {
-    const long long each = quick_div(total, shares), more = total - each * shares;
-    auto share_of = [&](long long t) {
-      return (int)(t < more * (each + 1) ? quick_div(t, each + 1) : more + quick_div(t - more * (each + 1), each));
-    };
-    ka = share_of(u0 + p.lead);
-    kb = share_of(u0 + weight - 1);
-    if (ka == kb) return;
-  }
-  auto slot_of = [&](int k) { return (2 * (long long)k + (share_begin(total, shares, k) < u0 ? 1 : 0)) * RT + r; };
-  // four shares at a time, their loads together, against a running maximum
-  float acc[E], wsum = 0.f, m = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int k0 = ka; k0 <= kb; k0 += 4) {
-    float lc[4], v[4][E];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const bool on = k0 + x <= kb;
-      const long long sl = slot_of(on ? k0 + x : kb);
-      lc[x] = on ? p.part_lse[sl] : -INFINITY;
-      const float* src = p.part_o + sl * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[x][e] = src[e];
+  for (int x0 = blockIdx.x * 8 + (threadIdx.x >> 5); x0 < p.Nq * p.Hq; x0 += gridDim.x * 8) {
+    const int i = p.Nq == 1 ? 0 : (int)((unsigned)x0 / (unsigned)p.Hq), h = x0 - i * p.Hq;
+    const int hk = (int)((unsigned)h / (unsigned)p.group), x = i * p.group + h - hk * p.group;  // row of the K/V head
+    const int u = hk * p.row_tiles + x / RT, r = x % RT;
+    const long long u0 = before + u * weight;
+    int ka = 0, kb = -1;  // (a request without keys: nothing to merge, zeros to write)
+    if (weight > 0) {
+      ka = share_of(u0 + p.lead);
+      kb = share_of(u0 + weight - 1);
+      if (ka == kb) continue;
     }
-    const float mn = fmaxf(fmaxf(fmaxf(lc[0], lc[1]), fmaxf(lc[2], lc[3])), m), ref = mn == -INFINITY ? 0.f : mn;
-    const float al = ex2_sfu(m - ref);
-    m = mn;
-    wsum *= al;
+    // four shares at a time, their loads together, against a running maximum
+    float acc[E], wsum = 0.f, m = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= al;
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int k0 = ka; k0 <= kb; k0 += 4) {
+      float lc[4], v[4][E];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const float wc = ex2_sfu(lc[x] - ref);
-      wsum += wc;
+      for (int y = 0; y < 4; ++y) {
+        const bool on = k0 + y <= kb;
+        const int k = on ? k0 + y : kb;
+        const long long sl = (2 * (long long)k + (each * k + (k < more ? k : more) < u0 ? 1 : 0)) * RT + r;
+        lc[y] = on ? p.part_lse[sl] : -INFINITY;
+        const float* src = p.part_o + sl * D + lane * E;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(wc, v[x][e], acc[e]);
+        for (int e = 0; e < E; ++e) v[y][e] = src[e];
+      }
+      const float mn = fmaxf(fmaxf(fmaxf(lc[0], lc[1]), fmaxf(lc[2], lc[3])), m), ref = mn == -INFINITY ? 0.f : mn;
+      const float al = ex2_sfu(m - ref);
+      m = mn;
+      wsum *= al;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= al;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float wc = ex2_sfu(lc[y] - ref);
+        wsum += wc;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wc, v[y][e], acc[e]);
+      }
     }
-  }
-  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at * D + lane * E);
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)b * p.Nq * p.Hq + x0) * D + lane * E);
 #pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0)
-    p.lse[((size_t)b * p.Hq + h) * p.Nq + i] = wsum == 0.f ? -INFINITY : (m + __log2f(wsum)) * 0.69314718055994531f;
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0)
+      p.lse[((size_t)b * p.Hq + h) * p.Nq + i] = wsum == 0.f ? -INFINITY : (m + __log2f(wsum)) * 0.69314718055994531f;
+  }
 }
 
 // Query rows of one CTA.
@@ -899,12 +903,12 @@ static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the merge's launch overlaps the main kernel (programmatic dependent launch); its blocks wait for the grid's end
-  const long long rows = (long long)p.B * p.Nq * p.Hq;
   cudaLaunchAttribute a{};
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+  // (a block adds up B lengths: with many requests, one block for all rows of one)
+  cfg.gridDim = dim3(p.B <= 512 ? (unsigned)((p.Nq * p.Hq + 7) / 8) : 1u, (unsigned)p.B);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = &a;

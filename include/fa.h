@@ -564,7 +564,7 @@ fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, voi
  * What a page holds behind a request's last key is never used, whatever it
  * is.  Table entries outside the pool and lengths outside [0, max_seq_len] are
  * handled and reported as in fa_decode_paged.  page_size a multiple of 16, d = 64
- * or 128, Nq >= 1.
+ * or 128, 1 <= B <= 16384, Nq >= 1, Nq * Hq <= 65535.
  */
 fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
                         const float* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse, int B,

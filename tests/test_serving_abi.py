@@ -70,7 +70,7 @@ def test_append(lib):
 def test_decode(lib):
     def f(ptrs=(A,) * 9, B=1, Nq=1, Hq=4, Hkv=2, d=128, page=16, pages=8, blocks=4, L=64, wl=-1, shares=1, ws=A, sc=0.1):
         return lib.fa_decode_kv8(*ptrs, B, Nq, Hq, Hkv, d, page, pages, blocks, L, wl, shares, ws, sc, NUL)
-    for kw in (dict(B=0), dict(B=65536), dict(Nq=0), dict(Hq=0), dict(Hkv=0), dict(Hkv=3), dict(page=8), dict(page=20),
+    for kw in (dict(B=0), dict(B=16385), dict(Nq=0), dict(Hq=0), dict(Hkv=0), dict(Hkv=3), dict(page=8), dict(page=20),
                dict(pages=0), dict(blocks=0), dict(L=65), dict(L=-1), dict(wl=-2), dict(shares=-1), dict(shares=65536),
                dict(ws=NUL), dict(sc=0.0), dict(sc=math.nan), dict(Nq=20000), dict(pages=1 << 30, Hkv=2),
                dict(blocks=1 << 27, L=(1 << 30) + 1)):
@@ -83,7 +83,7 @@ def test_decode(lib):
 
 
 def test_workspace_and_shares(lib):
-    assert lib.fa_decode_kv8_workspace_bytes(3, 2, 8, 2, 128, 5) >= 2 * 5 * 8 * (128 + 1) * 4 + 4 * 8
+    assert lib.fa_decode_kv8_workspace_bytes(3, 2, 8, 2, 128, 5) >= 2 * 5 * 8 * (128 + 1) * 4
     assert lib.fa_decode_kv8_workspace_bytes(0, 2, 8, 2, 128, 5) == 0
     for a in ((1, 1, 8, 8, 0, -1), (1, 1, 8, 8, 1, -1), (64, 1, 64, 8, 32768, -1), (1, 8, 64, 1, 1 << 30, 5)):
         assert 1 <= lib.fa_decode_kv8_num_shares(*a) <= 65535
