@@ -63,7 +63,11 @@ template <int D, int RT>
 struct Layout {
   static constexpr uint32_t kSlot = 128u * D;                                // a tile of K or V
   static constexpr int kCtas = kv8_ctas_per_sm(RT);
-  static constexpr int kSlots = D == 64 ? 8 : 4;  // ring: K0 V0 K1 V1 ...
+  // Rings of K and of V tiles.  A V tile is held longer, until its product has
+  // been made, so where CTAs are two, V's ring has a tile more than K's.
+  static constexpr int kKs = 256 / D;
+  static constexpr int kVs = kCtas == 3 ? 256 / D : 384 / D;
+  static constexpr int kSlots = kKs + kVs;
   static constexpr int kNS = 2 * RT < 16 ? 16 : 2 * RT;                      // columns of S
   static constexpr int kNP = (3 * RT + 15) / 16 * 16;                        // columns of P and O
   static constexpr uint32_t kUsed = 2 * kNS + kNP;
@@ -73,11 +77,11 @@ struct Layout {
   static constexpr uint32_t kQOff = kPOff + (3 * RT + 7) / 8 * 1024u;
   static constexpr uint32_t kScOff = kQOff + kNS * (uint32_t)D;              // per V slot: 8 key scales, 8 value scales
   static constexpr uint32_t kScBytes = 64;
-  static constexpr uint32_t kMaxOff = kScOff + kSlots / 2 * kScBytes;        // [4][RT] each: warps' maxima, sums, references, factors
-  static constexpr uint32_t kRowOff = kMaxOff + (16 + 8) * RT * 4;           // (and [4][RT] output rows, 8 bytes each) two of: [RT] query scales, [RT] positions
+  static constexpr uint32_t kMaxOff = kScOff + kVs * kScBytes;        // [4][RT] each: warps' maxima, sums, references, factors, output rows
+  static constexpr uint32_t kRowOff = kMaxOff + 20 * RT * 4;                 // two of: [RT] query scales, [RT] positions
   static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // [2][4] votes, scan, start
   // pieces announced ahead of their tiles, with their rows of Q as they lie in memory
-  static constexpr int kPieces = RT == 8 && D == 128 ? 1 : RT <= 8 ? 4 : 2;  // as many as the CTAs leave room for
+  static constexpr int kPieces = (RT == 8 && D == 128) || RT == 32 ? 1 : RT <= 8 ? 4 : 2;  // as many as the CTAs leave room for
   static constexpr uint32_t kPieceOff = kMiscOff + 128;                      // [kPieces] 32 bytes each
   static constexpr uint32_t kStageOff = (kPieceOff + kPieces * 32 + 127) / 128 * 128;
   static constexpr uint32_t kStage = RT * D * 2u;
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     fa_decode_kv8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ Kv8DecodeParams p) {
   using L = Layout<D, RT>;
-  constexpr int NSL = L::kSlots;
+  constexpr int KS = L::kKs, VS = L::kVs, NSL = L::kSlots;
   const int k = blockIdx.x, units = p.Hkv * p.row_tiles;
   const int warp = warp_id(), lane = lane_id();
 
@@ -225,8 +229,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sb = smem_raw + (base - raw);
   const uint32_t bars = base + L::kBarOff;
+  // barriers and tiles of the rings: K's slots, then V's
   auto FULL = [&](int s) { return bars + 8u * (uint32_t)s; };
   auto EMPTY = [&](int s) { return bars + 8u * (uint32_t)(NSL + s); };
+  auto TILE = [&](int s) { return base + L::kSlot * (uint32_t)s; };
   const uint32_t SF = bars + 16u * NSL;  // S ready [2]; then P ready, O ready, the warps' exchange, Q ready
   const uint32_t PF = SF + 16, OF = SF + 24, XB = SF + 32, QB = SF + 40;
   auto HERE = [&](int s) { return SF + 48 + 8u * (uint32_t)s; };                  // piece announced
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < NSL; ++s) {
-      mbar_init(FULL(s), s & 1 ? 9 : 1);  // (values: the copy's bytes, and eight lanes' scales)
+      mbar_init(FULL(s), s < KS ? 1 : 9);  // (values: the copy's bytes, and eight lanes' scales)
       mbar_init(EMPTY(s), 1);
     }
     mbar_init(SF, 1);
@@ -391,14 +397,14 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
         const uint32_t at = (uint32_t)(lane & 7) * 16u * D;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          const int slot = (2 * it + v) % NSL, use = (2 * it + v) / NSL;
+          const int slot = v ? KS + it % VS : it % KS, use = v ? it / VS : it / KS;
           if (use > 0) ok = mbar_wait(EMPTY(slot), (use - 1) & 1, w, 51);
           if (!__all_sync(0xffffffffu, ok)) break;
           if (lane == 0) mbar_arrive_expect_tx(FULL(slot), bytes);
           __syncwarp();
-          if (issue) tma_load_3d(base + slot * L::kSlot + at, v ? &tm_v : &tm_k, FULL(slot), 0, now.off, ph);
+          if (issue) tma_load_3d(TILE(slot) + at, v ? &tm_v : &tm_k, FULL(slot), 0, now.off, ph);
           if (v == 1 && mine) {
-            float* sc = reinterpret_cast<float*>(sb + L::kScOff + (slot >> 1) * L::kScBytes) + (lane & 7);
+            float* sc = reinterpret_cast<float*>(sb + L::kScOff + (it % VS) * L::kScBytes) + (lane & 7);
             if (now.on) {
               cp_async4(smem_u32(sc), p.k_scale + ph);
               cp_async4(smem_u32(sc + 8), p.v_scale + ph);
@@ -424,12 +430,12 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     const uint64_t qd = D == 128 ? smem_desc_sw128(qa, 16, 1024) : smem_desc_sw64(qa, 16, 512);
     const uint64_t pd = smem_desc_sw128(pa, 16, 1024);
     auto pv = [&](int it, bool first) {  // O (+)= V^T P^T of tile `it`
-      const int slot = (2 * it + 1) % NSL;
+      const int slot = KS + it % VS;
       bool good = mbar_wait(PF, it & 1, w, 54);
-      if (__all_sync(0xffffffffu, good)) good = mbar_wait(FULL(slot), ((2 * it + 1) / NSL) & 1, w, 55);
+      if (__all_sync(0xffffffffu, good)) good = mbar_wait(FULL(slot), it / VS & 1, w, 55);
       if (!__all_sync(0xffffffffu, good)) return false;
       tc_fence_after();
-      const uint32_t va = base + slot * L::kSlot;
+      const uint32_t va = TILE(slot);
       const uint64_t vd = D == 128 ? smem_desc_sw128(va, 16, 1024) : smem_desc_sw64(va, 16, 512);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
@@ -448,11 +454,11 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       if (n == 0) break;
       ok = __all_sync(0xffffffffu, mbar_wait(QB, piece & 1, w, 52));
       for (int t = 0; t < n && ok; ++t, ++it) {
-        const int slot = (2 * it) % NSL;
-        ok = __all_sync(0xffffffffu, mbar_wait(FULL(slot), (2 * it / NSL) & 1, w, 53));
+        const int slot = it % KS;
+        ok = __all_sync(0xffffffffu, mbar_wait(FULL(slot), it / KS & 1, w, 53));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t ka = base + slot * L::kSlot;
+        const uint32_t ka = TILE(slot);
         const uint64_t kd = D == 128 ? smem_desc_sw128(ka, 16, 1024) : smem_desc_sw64(ka, 16, 512);
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk)
@@ -576,13 +582,13 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       __syncwarp();
 
       for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
-        const int vslot = (2 * it + 1) % NSL;
+        const int vslot = KS + it % VS;
         ok = mbar_wait(SF + 8u * (it & 1), (it >> 1) & 1, w, 58);
-        if (__all_sync(0xffffffffu, ok)) ok = mbar_wait(FULL(vslot), ((2 * it + 1) / NSL) & 1, w, 59);
+        if (__all_sync(0xffffffffu, ok)) ok = mbar_wait(FULL(vslot), it / VS & 1, w, 59);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const float* sc = reinterpret_cast<const float*>(sb + L::kScOff + (vslot >> 1) * L::kScBytes);
+        const float* sc = reinterpret_cast<const float*>(sb + L::kScOff + (it % VS) * L::kScBytes);
         const float ks = sc[chunk], vs = sc[8 + chunk], lvs = fmaxf(__log2f(vs), kLeastScale);
         const int j0 = pc.beg + t * kKv8Tile, j = j0 + key;
         // some row does not see some key of the tile
@@ -727,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       const bool has = D == 128 || lane < 16;
       const bool whole = done.t0 == 0 && done.t1 == done.tiles;
       // lane r works out row r for its warp: where it goes, what its sums are divided by; the row's lse
-      long long* my_at = reinterpret_cast<long long*>(s_max + 16 * RT) + warp * RT;
+      int* my_at = reinterpret_cast<int*>(s_max + (16 + warp) * RT);
       if (lane < rows) {
         const float sum = s_sum[lane] + s_sum[RT + lane] + s_sum[2 * RT + lane] + s_sum[3 * RT + lane];
         // sum = 0: the row sees none of these keys (a NaN passes through)
@@ -735,11 +741,11 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
         my_al[lane] = sum == 0.f ? 0.f : 1.f / (sum * kAtRef);
         if (whole) {
           int i, h;
-          my_at[lane] = (long long)q_row(done, lane, i, h) * D;
+          my_at[lane] = (int)q_row(done, lane, i, h);  // (below 2^30)
           if (warp == 0) p.lse[((size_t)done.b * p.Hq + h) * p.Nq + i] = lse2 * 0.69314718055994531f;
         } else {
           const size_t part = 2 * (size_t)k + (piece > 0 ? 1 : 0);  // a share's first piece, or its last
-          my_at[lane] = (long long)(part * RT + lane) * D;
+          my_at[lane] = (int)(part * RT) + lane;
           if (warp == 0) p.part_lse[part * RT + lane] = lse2;
         }
       }
@@ -758,9 +764,9 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
             const float f = my_al[r4 + x];
             const float val = f == 0.f ? 0.f : y * f;  // (0 * NaN would not be 0)
             if (whole)
-              static_cast<__nv_bfloat16*>(p.o)[my_at[r4 + x] + e] = __float2bfloat16_rn(val);
+              static_cast<__nv_bfloat16*>(p.o)[(size_t)my_at[r4 + x] * D + e] = __float2bfloat16_rn(val);
             else
-              p.part_o[my_at[r4 + x] + e] = val;
+              p.part_o[(size_t)my_at[r4 + x] * D + e] = val;
           }
         }
       }
