@@ -34,10 +34,10 @@
 //
 // CTA:
 //   warps 0-3  thread = key of the tile (TMEM lane) for S and P, and one of the
-//              d output elements at a unit's end
-//   warp 4     producer: block table and scales, a TMA box per page into a ring
-//              of K and V tiles, across the units' borders
-//   warp 5     issues the products
+//              d output elements at a unit's end (for 32 rows, warps 0-7)
+//   next       producer: block table and scales, a TMA box per page into rings
+//              of K and of V tiles, across the units' borders
+//   last       issues the products
 // S is double buffered in TMEM (the next tile's scores are ready when a tile's
 // softmax starts); P is not: it is written when the product before has read it.
 #include "fa_internal.h"
@@ -49,7 +49,6 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 192;
 constexpr float kAtRef = 64.f;       // p at the reference
 constexpr float kHeadroom = 2.8f;    // log2(448 / 64), rounded down
 constexpr float kLeastScale = -100.f;  // log2 of a value scale, from below: a page of zeros counts as one of 2^-100
@@ -61,6 +60,10 @@ constexpr int kv8_ctas_per_sm(int RT) { return RT <= 8 ? 3 : 2; }
 
 template <int D, int RT>
 struct Layout {
+  // Softmax warps come in groups of four (one for each quarter of a tile's
+  // keys); 32 rows are two groups' work, 16 rows each.
+  static constexpr int kGroups = RT == 32 ? 2 : 1;
+  static constexpr int kThreads = (4 * kGroups + 2) * 32;
   static constexpr uint32_t kSlot = 128u * D;                                // a tile of K or V
   static constexpr int kCtas = kv8_ctas_per_sm(RT);
   // Rings of K and of V tiles.  A V tile is held longer, until its product has
@@ -79,14 +82,14 @@ struct Layout {
   static constexpr uint32_t kScBytes = 64;
   static constexpr uint32_t kMaxOff = kScOff + kVs * kScBytes;        // [4][RT] each: warps' maxima, sums, references, factors, output rows
   static constexpr uint32_t kRowOff = kMaxOff + 20 * RT * 4;                 // two of: [RT] query scales, [RT] positions
-  static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // [2][4] votes, scan, start
+  static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // votes, scan, start
   // pieces announced ahead of their tiles, with their rows of Q as they lie in memory
   static constexpr int kPieces = (RT == 8 && D == 128) || RT == 32 ? 1 : RT <= 8 ? 4 : 2;  // as many as the CTAs leave room for
-  static constexpr uint32_t kPieceOff = kMiscOff + 128;                      // [kPieces] 32 bytes each
+  static constexpr uint32_t kPieceOff = kMiscOff + 192;                      // [kPieces] 32 bytes each
   static constexpr uint32_t kStageOff = (kPieceOff + kPieces * 32 + 127) / 128 * 128;
   static constexpr uint32_t kStage = RT * D * 2u;
   static constexpr uint32_t kBarOff = kStageOff + kPieces * kStage;
-  static constexpr int kBars = 2 * kSlots + 6 + 2 * kPieces;
+  static constexpr int kBars = 2 * kSlots + 7 + 2 * kPieces;
   static constexpr uint32_t kBytes = kBarOff + 8 * kBars + 16 + 1024;
   static_assert(kUsed <= 256, "TMEM columns");
 };
@@ -217,11 +220,12 @@ __device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
 }  // namespace
 
 template <int D, int RT>
-__global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
+__global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     fa_decode_kv8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ Kv8DecodeParams p) {
   using L = Layout<D, RT>;
   constexpr int KS = L::kKs, VS = L::kVs, NSL = L::kSlots;
+  constexpr int GROUPS = L::kGroups, SOFT = 4 * GROUPS, kThreads = L::kThreads;  // softmax warps, then the two others
   const int k = blockIdx.x, units = p.Hkv * p.row_tiles;
   const int warp = warp_id(), lane = lane_id();
 
@@ -234,17 +238,17 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
   auto EMPTY = [&](int s) { return bars + 8u * (uint32_t)(NSL + s); };
   auto TILE = [&](int s) { return base + L::kSlot * (uint32_t)s; };
   const uint32_t SF = bars + 16u * NSL;  // S ready [2]; then P ready, O ready, the warps' exchange, Q ready
-  const uint32_t PF = SF + 16, OF = SF + 24, XB = SF + 32, QB = SF + 40;
-  auto HERE = [&](int s) { return SF + 48 + 8u * (uint32_t)s; };                  // piece announced
-  auto TAKEN = [&](int s) { return SF + 48 + 8u * (uint32_t)(L::kPieces + s); };  // and taken by its five readers
+  const uint32_t PF = SF + 16, OF = SF + 24, QB = SF + 32, XB = SF + 40;           // (an exchange for each group)
+  auto HERE = [&](int s) { return SF + 56 + 8u * (uint32_t)s; };                  // piece announced
+  auto TAKEN = [&](int s) { return SF + 56 + 8u * (uint32_t)(L::kPieces + s); };  // and taken by all its readers
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::kBarOff + 8 * L::kBars);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sb + L::kBarOff + 8 * L::kBars + 4);
   Piece* s_piece = reinterpret_cast<Piece*>(sb + L::kPieceOff);
-  int* s_vote = reinterpret_cast<int*>(sb + L::kMiscOff);                       // [2][4]
-  long long* s_scan = reinterpret_cast<long long*>(sb + L::kMiscOff + 32);      // [6] warps' sums
-  volatile long long* s_start = reinterpret_cast<volatile long long*>(sb + L::kMiscOff + 80);  // b, off, tiles and len
+  int* s_vote = reinterpret_cast<int*>(sb + L::kMiscOff);                       // [2][SOFT]
+  long long* s_scan = reinterpret_cast<long long*>(sb + L::kMiscOff + 64);      // [SOFT + 2] warps' sums
+  volatile long long* s_start = reinterpret_cast<volatile long long*>(sb + L::kMiscOff + 144);  // b, off, tiles and len
 
-  if (warp == 5) {
+  if (warp == SOFT + 1) {
     tmem_alloc(base + L::kBarOff + 8 * L::kBars + 4, L::kCols);
     tmem_relinquish();
     tc_fence_before();
@@ -256,13 +260,14 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     }
     mbar_init(SF, 1);
     mbar_init(SF + 8, 1);
-    mbar_init(PF, 4);
+    mbar_init(PF, SOFT);
     mbar_init(OF, 1);
+    mbar_init(QB, SOFT);
     mbar_init(XB, 4);
-    mbar_init(QB, 4);
+    mbar_init(XB + 8, 4);
     for (int s = 0; s < L::kPieces; ++s) {
       mbar_init(HERE(s), 1);
-      mbar_init(TAKEN(s), 5);
+      mbar_init(TAKEN(s), SOFT + 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -308,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
   bool ok = true;
   asm volatile("griddepcontrol.launch_dependents;");  // the merge may be set up; it waits for this grid's end
 
-  if (warp == 4) {
+  if (warp == SOFT) {
     // ============================================================ producer
     // With the ring full, every load of the SM waits behind the ring's bytes, 2
     // to 4 us, so no register waits for one that was just asked for.  Tiles go in
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       fetch(next);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 5) {
+  } else if (warp == SOFT + 1) {
     // ============================================================ products
     constexpr uint32_t IDESC_S = idesc_e4m3(128, L::kNS), IDESC_O = idesc_e4m3(D, L::kNP, true);
     const uint32_t qa = base + L::kQOff, pa = base + L::kPOff;
@@ -471,13 +476,18 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     }
   } else {
     // ============================================================ softmax
-    float* s_max = reinterpret_cast<float*>(sb + L::kMaxOff);
-    float* s_sum = s_max + 4 * RT;
-    float* my_ref = s_max + (8 + warp) * RT;   // this warp's copies: the rows' references,
-    float* my_al = s_max + (12 + warp) * RT;   //   and what a moved one multiplies sums by
-    const uint32_t lane_sel = (uint32_t)warp << 21;  // TMEM lane 32 * warp
-    const int key = warp * 32 + lane;                // key of the tile
-    const uint32_t p_at = base + L::kPOff + (key & 15);  // this thread's byte in P's 128-byte rows
+    constexpr int RG = RT / GROUPS;                  // rows of a group
+    const int group = warp >> 2, quarter = warp & 3, g0 = group * RG;
+    float* my_max = reinterpret_cast<float*>(sb + L::kMaxOff) + warp * RG;
+    float* my_sum = my_max + 4 * RT;
+    float* my_ref = my_max + 8 * RT;                 // this warp's copies: the rows' references,
+    float* my_al = my_max + 12 * RT;                 //   what a moved one multiplies sums by,
+    int* my_at = reinterpret_cast<int*>(my_max + 16 * RT);  // and where the results go
+    const float* g_max = my_max - quarter * RG;      // the group's four warps'
+    const float* g_sum = my_sum - quarter * RG;
+    const uint32_t lane_sel = (uint32_t)quarter << 21;  // TMEM lane 32 * quarter
+    const int key = quarter * 32 + lane;             // key of the tile
+    const uint32_t p_at = base + L::kPOff + g0 * 128 + (key & 15);  // this thread's byte in P's 128-byte rows
     const uint32_t chunk = (uint32_t)key >> 4;
     auto rows_of = [&](const Piece& s) { return min(RT, p.Nq * p.group - s.u % p.row_tiles * RT); };
     // row r of a piece: its row of q and o, its query token
@@ -497,12 +507,12 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       int* s_pos = reinterpret_cast<int*>(s_qsc + RT);
       const int rows = s.t0 == s.t1 ? 0 : rows_of(s);
       constexpr int LPR = D / 8, RPW = 32 / LPR;                // lanes per row, rows per warp and pass
-      constexpr int PASSES = (RT + 4 * RPW - 1) / (4 * RPW);
+      constexpr int PASSES = (RT + SOFT * RPW - 1) / (SOFT * RPW);
       const int sub = lane / LPR, seg = lane % LPR;
       uint4 q[PASSES];
 #pragma unroll
       for (int x = 0; x < PASSES; ++x) {
-        const int r = (x * 4 + warp) * RPW + sub;
+        const int r = (x * SOFT + warp) * RPW + sub;
         q[x] = make_uint4(0u, 0u, 0u, 0u);
         if (r < rows) q[x] = *reinterpret_cast<const uint4*>(sb + L::kStageOff + st * L::kStage + r * D * 2 + seg * 16);
       }
@@ -511,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       if (rows == 0) return true;
 #pragma unroll
       for (int x = 0; x < PASSES; ++x) {
-        const int r = (x * 4 + warp) * RPW + sub;
+        const int r = (x * SOFT + warp) * RPW + sub;
         const uint32_t wd[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
         float f[8], mx = 0.f;
 #pragma unroll
@@ -562,23 +572,23 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
 
     int it = 0, piece = 0;
     uint32_t xphase = 0;  // phase of the warps' exchange
-    auto exchange = [&]() {  // every warp has written what the others read next
+    auto exchange = [&]() {  // every warp of the group has written what the others read next
       __syncwarp();
-      if (lane == 0) mbar_arrive(XB);
-      return __all_sync(0xffffffffu, mbar_wait(XB, xphase++ & 1, w, 60));
+      if (lane == 0) mbar_arrive(XB + 8 * group);
+      return __all_sync(0xffffffffu, mbar_wait(XB + 8 * group, xphase++ & 1, w, 60));
     };
     Piece pc;
     ok = take(0, pc);
     while (ok && pc.t0 < pc.t1) {
-      const float* s_qsc = reinterpret_cast<const float*>(sb + L::kRowOff + (piece & 1) * 2 * RT * 4);
-      const int* s_pos = reinterpret_cast<const int*>(s_qsc + RT);
+      const float* s_qsc = reinterpret_cast<const float*>(sb + L::kRowOff + (piece & 1) * 2 * RT * 4) + g0;
+      const int* s_pos = reinterpret_cast<const int*>(s_qsc + RT);  // (both from the group's first row)
       const int rows = rows_of(pc);
       ok = __all_sync(0xffffffffu, mbar_wait(QB, piece & 1, w, 56));
-      float l[RT];
+      float l[RG];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) l[r] = 0.f;
+      for (int r = 0; r < RG; ++r) l[r] = 0.f;
       __syncwarp();
-      if (lane < RT) my_ref[lane] = kNoRef;
+      if (lane < RG) my_ref[lane] = kNoRef;
       __syncwarp();
 
       for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
@@ -596,7 +606,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
         if (partial) {
           bool any = false;
 #pragma unroll 4
-          for (int r = 0; r < RT; ++r) any |= r < rows && j <= s_pos[r] && (p.win_left < 0 || j >= s_pos[r] - p.win_left);
+          for (int r = -g0; r < RT - g0; ++r)  // (all groups' rows)
+            any |= g0 + r < rows && j <= s_pos[r] && (p.win_left < 0 || j >= s_pos[r] - p.win_left);
           if (!any) {  // a key that no row sees: its value row may hold anything, and 0 * NaN would not be 0
             uint4* row = reinterpret_cast<uint4*>(sb + vslot * L::kSlot + key * D);
 #pragma unroll
@@ -604,15 +615,15 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
           }
         }
         auto sees = [&](int r) { return j <= s_pos[r] && (p.win_left < 0 || j >= s_pos[r] - p.win_left); };
-        float s[RT];
+        float s[RG];
         for (bool settled = false;;) {
           // ---- scores less the references, in log2 units
-          constexpr int H = RT > 16 ? 16 : RT;  // rows per load
+          constexpr int H = RG > 8 ? 8 : RG;  // rows per load
 #pragma unroll
-          for (int h = 0; h < RT; h += H) {
+          for (int h = 0; h < RG; h += H) {
             uint32_t s1[H], s2[H];
-            tmem_load<H>(tS + (it & 1) * L::kNS + lane_sel + h, s1);
-            tmem_load<H>(tS + (it & 1) * L::kNS + lane_sel + RT + h, s2);
+            tmem_load<H>(tS + (it & 1) * L::kNS + lane_sel + g0 + h, s1);
+            tmem_load<H>(tS + (it & 1) * L::kNS + lane_sel + RT + g0 + h, s2);
             tmem_ld_wait();
 #pragma unroll
             for (int r = 0; r < H; ++r) {
@@ -622,26 +633,26 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
           }
           if (partial) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) s[r] = sees(r) ? s[r] : -INFINITY;
+            for (int r = 0; r < RG; ++r) s[r] = sees(r) ? s[r] : -INFINITY;
           }
           if (settled) break;
           // ---- does any p pass what e4m3 holds?
           float top = s[0];
 #pragma unroll
-          for (int r = 1; r < RT; ++r) top = fmaxf(top, s[r]);
+          for (int r = 1; r < RG; ++r) top = fmaxf(top, s[r]);
           const bool move = __any_sync(0xffffffffu, top > kHeadroom - lvs);
-          if (lane == 0) s_vote[(it & 1) * 4 + warp] = move;
+          if (lane == 0) s_vote[(it & 1) * SOFT + warp] = move;
           ok = exchange();
           if (!ok) break;
-          const int4 votes = *reinterpret_cast<const int4*>(s_vote + (it & 1) * 4);
+          const int4 votes = *reinterpret_cast<const int4*>(s_vote + (it & 1) * SOFT + group * 4);
           if ((votes.x | votes.y | votes.z | votes.w) == 0) break;
           // ---- new references: the largest up to here (rolled loops: rare, and the code is long already)
-          constexpr int G = RT > 8 ? 8 : RT;  // rows at a time
+          constexpr int G = RG > 8 ? 8 : RG;  // rows at a time
 #pragma unroll 1
-          for (int r = 0; r < RT; r += G) {
+          for (int r = 0; r < RG; r += G) {
             uint32_t s1[G], s2[G];
-            tmem_load<G>(tS + (it & 1) * L::kNS + lane_sel + r, s1);
-            tmem_load<G>(tS + (it & 1) * L::kNS + lane_sel + RT + r, s2);
+            tmem_load<G>(tS + (it & 1) * L::kNS + lane_sel + g0 + r, s1);
+            tmem_load<G>(tS + (it & 1) * L::kNS + lane_sel + RT + g0 + r, s2);
             tmem_ld_wait();
             float x[G];
 #pragma unroll
@@ -653,33 +664,32 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
             if (lane == 0) {
 #pragma unroll
               for (int e = 0; e < G; e += 4)
-                *reinterpret_cast<float4*>(s_max + warp * RT + r + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                *reinterpret_cast<float4*>(my_max + r + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
             }
           }
           ok = exchange();
           if (!ok) break;
-          if (lane < RT) {
-            const float x = fmaxf(fmaxf(s_max[lane], s_max[RT + lane]), fmaxf(s_max[2 * RT + lane], s_max[3 * RT + lane]));
+          if (lane < RG) {
+            const float x = fmaxf(fmaxf(g_max[lane], g_max[RG + lane]), fmaxf(g_max[2 * RG + lane], g_max[3 * RG + lane]));
             const float old = my_ref[lane], now = fmaxf(old, x);  // (a row that sees no key yet has -inf in x)
             my_ref[lane] = now;
             my_al[lane] = ex2_sfu(old - now);
           }
           __syncwarp();
 #pragma unroll
-          for (int r = 0; r < RT; ++r) l[r] *= my_al[r];
+          for (int r = 0; r < RG; ++r) l[r] *= my_al[r];
           if (t > pc.t0) {  // O stands at the old ones
             ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 62));
             if (!ok) break;
             tc_fence_after();
-            constexpr int H = RT > 16 ? 16 : RT;  // columns at a time
 #pragma unroll 1
-            for (int h = 0; h < 3 * RT; h += H) {
-              uint32_t o[H];
-              tmem_load<H>(tO + lane_sel + h, o);
+            for (int part = 0; part < 3; ++part) {
+              uint32_t o[RG];
+              tmem_load<RG>(tO + lane_sel + part * RT + g0, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < H; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * my_al[h % RT + e]);
-              tmem_store<H>(tO + lane_sel + h, o);
+              for (int e = 0; e < RG; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * my_al[e]);
+              tmem_store<RG>(tO + lane_sel + part * RT + g0, o);
             }
             tmem_st_wait();
           }
@@ -693,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
         }
         const float vn = vs * kAtRef;
 #pragma unroll
-        for (int r = 0; r < RT; r += 2) {
+        for (int r = 0; r < RG; r += 2) {
           const float p0 = ex2_sfu(s[r]), p1 = ex2_sfu(s[r + 1]);
           l[r] += p0;
           l[r + 1] += p1;
@@ -701,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
             const uint32_t two = pack_e4m3x2(x, y);
-            const int col = part * RT + r;
+            const int col = part * RT + r;  // (from the group's first row)
             sts_u8(p_at + col * 128 + ((chunk ^ (col & 7)) << 4), two & 0xffu);
             sts_u8(p_at + (col + 1) * 128 + ((chunk ^ ((col + 1) & 7)) << 4), two >> 8);
             if (part < 2) {
@@ -722,44 +732,44 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
       ok = take(piece + 1, pc);
       if (!ok) break;
       // ---- each row's sum over the 128 key lanes
-      const float row_sum = warp_row_sums<RT>(l, lane);
-      if (lane % (32 / RT) == 0) s_sum[warp * RT + lane / (32 / RT)] = row_sum;
+      const float row_sum = warp_row_sums<RG>(l, lane);
+      if (lane % (32 / RG) == 0) my_sum[lane / (32 / RG)] = row_sum;
       ok = exchange();
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 61));
       if (!ok) break;
       tc_fence_after();
       // output element of this thread: its TMEM lane; an M = 64 product uses lanes 0 .. 15 of each warp's 32
-      const int e = D == 128 ? key : warp * 16 + lane;
+      const int e = D == 128 ? key : quarter * 16 + lane;
       const bool has = D == 128 || lane < 16;
       const bool whole = done.t0 == 0 && done.t1 == done.tiles;
-      // lane r works out row r for its warp: where it goes, what its sums are divided by; the row's lse
-      int* my_at = reinterpret_cast<int*>(s_max + (16 + warp) * RT);
-      if (lane < rows) {
-        const float sum = s_sum[lane] + s_sum[RT + lane] + s_sum[2 * RT + lane] + s_sum[3 * RT + lane];
+      // lane r works out row r of the group for its warp: where it goes, what its sums are divided by; the row's lse
+      const int mine = min(RG, rows - g0);
+      if (lane < mine) {
+        const float sum = g_sum[lane] + g_sum[RG + lane] + g_sum[2 * RG + lane] + g_sum[3 * RG + lane];
         // sum = 0: the row sees none of these keys (a NaN passes through)
         const float lse2 = sum == 0.f ? -INFINITY : my_ref[lane] + __log2f(sum);
         my_al[lane] = sum == 0.f ? 0.f : 1.f / (sum * kAtRef);
         if (whole) {
           int i, h;
-          my_at[lane] = (int)q_row(done, lane, i, h);  // (below 2^30)
-          if (warp == 0) p.lse[((size_t)done.b * p.Hq + h) * p.Nq + i] = lse2 * 0.69314718055994531f;
+          my_at[lane] = (int)q_row(done, g0 + lane, i, h);  // (below 2^30)
+          if (quarter == 0) p.lse[((size_t)done.b * p.Hq + h) * p.Nq + i] = lse2 * 0.69314718055994531f;
         } else {
           const size_t part = 2 * (size_t)k + (piece > 0 ? 1 : 0);  // a share's first piece, or its last
-          my_at[lane] = (int)(part * RT) + lane;
-          if (warp == 0) p.part_lse[part * RT + lane] = lse2;
+          my_at[lane] = (int)(part * RT) + g0 + lane;
+          if (quarter == 0) p.part_lse[part * RT + g0 + lane] = lse2;
         }
       }
       __syncwarp();
 #pragma unroll 1
-      for (int r4 = 0; r4 < rows; r4 += 4) {
+      for (int r4 = 0; r4 < mine; r4 += 4) {
         uint32_t o1[4], o2[4], o3[4];
-        tmem_ld4(tO + lane_sel + r4, o1);
-        tmem_ld4(tO + lane_sel + RT + r4, o2);
-        tmem_ld4(tO + lane_sel + 2 * RT + r4, o3);
+        tmem_ld4(tO + lane_sel + g0 + r4, o1);
+        tmem_ld4(tO + lane_sel + RT + g0 + r4, o2);
+        tmem_ld4(tO + lane_sel + 2 * RT + g0 + r4, o3);
         tmem_ld_wait();
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          if (r4 + x < rows && has) {
+          if (r4 + x < mine && has) {
             const float y = fmaf(fmaf(__uint_as_float(o3[x]), 0.0625f, __uint_as_float(o2[x])), 0.0625f, __uint_as_float(o1[x]));
             const float f = my_al[r4 + x];
             const float val = f == 0.f ? 0.f : y * f;  // (0 * NaN would not be 0)
@@ -771,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
         }
       }
       tc_fence_before();
-      ok = exchange();  // s_sum is free again
+      ok = exchange();  // the sums' places are free again
       if (!ok) break;
       ++piece;
     }
@@ -783,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, RT>::kCtas)
     }
   }
   __syncthreads();
-  if (warp == 5) {
+  if (warp == SOFT + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
   }
@@ -905,7 +915,7 @@ static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8
   p.row_tiles = (p.Nq * p.group + RT - 1) / RT;
   // Where a share is a tile or less, nothing is gained by making room for starts.
   p.lead = kv8_most_tiles(p.B, p.Nq, p.Hkv, p.group, span) > kv8_ctas(p.Nq, p.group) ? kLead(RT) : 0;
-  kern<<<shares, kThreads, smem, stream>>>(tk, tv, p);
+  kern<<<shares, Layout<D, RT>::kThreads, smem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the merge's launch overlaps the main kernel (programmatic dependent launch); its blocks wait for the grid's end
