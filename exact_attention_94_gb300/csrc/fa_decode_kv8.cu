@@ -89,7 +89,7 @@ struct Layout {
   static constexpr uint32_t kStageOff = (kPieceOff + kPieces * 32 + 127) / 128 * 128;
   static constexpr uint32_t kStage = RT * D * 2u;
   static constexpr uint32_t kBarOff = kStageOff + kPieces * kStage;
-  static constexpr int kBars = 2 * kSlots + 7 + 2 * kPieces;
+  static constexpr int kBars = 2 * kSlots + 8 + 2 * kPieces;
   static constexpr uint32_t kBytes = kBarOff + 8 * kBars + 16 + 1024;
   static_assert(kUsed <= 256, "TMEM columns");
 };
@@ -238,9 +238,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
   auto EMPTY = [&](int s) { return bars + 8u * (uint32_t)(NSL + s); };
   auto TILE = [&](int s) { return base + L::kSlot * (uint32_t)s; };
   const uint32_t SF = bars + 16u * NSL;  // S ready [2]; then P ready, O ready, the warps' exchange, Q ready
-  const uint32_t PF = SF + 16, OF = SF + 24, QB = SF + 32, XB = SF + 40;           // (an exchange for each group)
-  auto HERE = [&](int s) { return SF + 56 + 8u * (uint32_t)s; };                  // piece announced
-  auto TAKEN = [&](int s) { return SF + 56 + 8u * (uint32_t)(L::kPieces + s); };  // and taken by all its readers
+  const uint32_t PF = SF + 16, OF = SF + 24, QB = SF + 32, XB = SF + 40;           // (an exchange for each group, one for all)
+  auto HERE = [&](int s) { return SF + 64 + 8u * (uint32_t)s; };                  // piece announced
+  auto TAKEN = [&](int s) { return SF + 64 + 8u * (uint32_t)(L::kPieces + s); };  // and taken by all its readers
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::kBarOff + 8 * L::kBars);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sb + L::kBarOff + 8 * L::kBars + 4);
   Piece* s_piece = reinterpret_cast<Piece*>(sb + L::kPieceOff);
@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     mbar_init(QB, SOFT);
     mbar_init(XB, 4);
     mbar_init(XB + 8, 4);
+    mbar_init(XB + 16, SOFT);
     for (int s = 0; s < L::kPieces; ++s) {
       mbar_init(HERE(s), 1);
       mbar_init(TAKEN(s), SOFT + 1);
@@ -577,6 +578,12 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       if (lane == 0) mbar_arrive(XB + 8 * group);
       return __all_sync(0xffffffffu, mbar_wait(XB + 8 * group, xphase++ & 1, w, 60));
     };
+    uint32_t bphase = 0;
+    auto both = [&]() {  // all softmax warps have come this far
+      __syncwarp();
+      if (lane == 0) mbar_arrive(XB + 16);
+      return __all_sync(0xffffffffu, mbar_wait(XB + 16, bphase++ & 1, w, 64));
+    };
     Piece pc;
     ok = take(0, pc);
     while (ok && pc.t0 < pc.t1) {
@@ -603,18 +610,42 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         const int j0 = pc.beg + t * kKv8Tile, j = j0 + key;
         // some row does not see some key of the tile
         const bool partial = j0 + kKv8Tile > pc.len - p.Nq + 1 || (p.win_left >= 0 && j0 < pc.len - 1 - p.win_left);
+        auto sees = [&](int r) { return j <= s_pos[r] && (p.win_left < 0 || j >= s_pos[r] - p.win_left); };
+        // A key's value row may hold NaN, and 0 * NaN is not 0.  Where no row sees
+        // the key (it may be anything behind the last), its values count as zero.
+        // Where some rows do and some don't (drafts), a row with a NaN counts as
+        // zero too, and as NaN to the rows that see it: in all their elements.
+        bool poison = false;
         if (partial) {
-          bool any = false;
+          bool any = false, all = true;
 #pragma unroll 4
-          for (int r = -g0; r < RT - g0; ++r)  // (all groups' rows)
-            any |= g0 + r < rows && j <= s_pos[r] && (p.win_left < 0 || j >= s_pos[r] - p.win_left);
-          if (!any) {  // a key that no row sees: its value row may hold anything, and 0 * NaN would not be 0
-            uint4* row = reinterpret_cast<uint4*>(sb + vslot * L::kSlot + key * D);
+          for (int r = -g0; r < RT - g0; ++r) {  // (all groups' rows)
+            if (g0 + r < rows) {
+              any |= sees(r);
+              all &= sees(r);
+            }
+          }
+          uint4* row = reinterpret_cast<uint4*>(sb + vslot * L::kSlot + key * D);
+          if (any && !all) {
+            uint32_t nan = 0;
+#pragma unroll 1
+            for (int e = 0; e < D / 16; ++e) {
+              const uint4 v = row[e];
+              nan |= __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                     __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            }
+            poison = nan != 0;
+          }
+          if (GROUPS > 1) {  // (one group's row is the other's: both have read it before either writes)
+            // every softmax warp passes here: the tile is partial for all of them
+            ok = both();
+            if (!ok) break;
+          }
+          if (!any || poison) {
 #pragma unroll
             for (int e = 0; e < D / 16; ++e) row[e] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        auto sees = [&](int r) { return j <= s_pos[r] && (p.win_left < 0 || j >= s_pos[r] - p.win_left); };
         float s[RG];
         for (bool settled = false;;) {
           // ---- scores less the references, in log2 units
@@ -701,7 +732,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 57));
           if (!ok) break;
         }
-        const float vn = vs * kAtRef;
+        const float vn = poison ? 0.f : vs * kAtRef;
 #pragma unroll
         for (int r = 0; r < RG; r += 2) {
           const float p0 = ex2_sfu(s[r]), p1 = ex2_sfu(s[r + 1]);
@@ -720,6 +751,11 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
               y = (y - f.y) * 16.f;
             }
           }
+        }
+        if (poison) {
+#pragma unroll 1
+          for (int r = 0; r < RG; ++r)
+            if (sees(r)) sts_u8(p_at + r * 128 + ((chunk ^ (r & 7)) << 4), 0x7fu);
         }
         fence_proxy_async_smem();
         tc_fence_before();

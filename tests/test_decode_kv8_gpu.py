@@ -248,3 +248,67 @@ def test_refusals():
         ops.decode_kv8(a[0][:, :, :3].contiguous(), *a[1:], 20)
     with pytest.raises(ValueError):
         ops.decode_kv8(a[0].repeat(1, 1, 1, 2)[..., ::2], *a[1:], 20)
+
+
+@pytest.mark.parametrize("Hq,d", [(2, 64), (8, 128), (16, 128)])
+def test_nan_in_a_draft_stays_with_the_rows_that_see_it(Hq, d):
+    """A NaN among the values (or keys) of a draft token: rows before that token are
+    what they are without it; rows that see it are NaN, their lse only if the key is."""
+    Nq, Hkv, n = 4, 2, [130, 257]
+    case = make(n, Nq, Hq, Hkv, d, 16, seed=Hq + d)
+    q, (kc, ks), (vc, vs), table, lens = case
+    j = n[0] - 2                                   # seen by the last two rows of request 0
+    vc[table[0, j // 16], 0, j % 16, 5] = 0xFF
+    j = n[1] - 1                                   # seen by the last row of request 1
+    kc[table[1, j // 16], 1, j % 16, 3] = 0x7F
+    o, lse = ops.decode_kv8(*dev(case), 257)
+    assert ops.device_error() == 0
+    with np.errstate(invalid="ignore"):
+        o_ref, l_ref, a, f = serving.decode_kv8(synth.to_f64(q), kc, vc, ks, vs, table, lens, -1, d ** -0.5)
+    bad = np.zeros((2, Nq, Hq), bool)
+    bad[0, 2:, :Hq // 2] = True
+    bad[1, 3:, Hq // 2:] = True
+    o, lse = synth.to_f64(o), lse.cpu().numpy()
+    assert np.all(np.isnan(o[bad])) and np.all(np.isnan(o_ref[bad]).any(-1))
+    good = ~bad
+    assert np.all(np.abs(o - o_ref)[good] <= (2.0 ** -8 * np.abs(o_ref) + 2.0 ** -11 * a + 2.0 ** -24 * f)[good])
+    none = np.isnan(l_ref)
+    assert np.array_equal(np.isnan(lse), none) and none.sum() == Hq // 2
+    assert np.all(np.abs(lse - l_ref)[~none] <= 2.0 ** -13)
+
+
+def test_queries_that_are_no_numbers():
+    """An infinity or a NaN in a query row makes that row NaN, and no other."""
+    q, k, v, table, lens = make([200, 3], 2, 8, 2, 128, 16, seed=12)
+    q[0, 0, 1, 7], q[1, 1, 6, 0] = float("inf"), float("nan")
+    o, lse = ops.decode_kv8(*dev((q, k, v, table, lens)), 200)
+    bad = torch.zeros((2, 2, 8), dtype=torch.bool, device="cuda")
+    bad[0, 0, 1] = bad[1, 1, 6] = True
+    assert torch.equal(torch.isnan(o).all(-1), bad) and torch.equal(torch.isnan(o).any(-1), bad)
+    assert torch.equal(torch.isnan(lse).transpose(1, 2), bad)
+
+
+def test_pages_beyond_4_gib():
+    """Offsets that pass 32 bits: a few pages at the end of a cache of 5 GiB a side."""
+    Hkv, P, d, pages = 8, 64, 128, 5 * 2 ** 30 // (8 * 64 * 128)
+    kc, vc = (torch.zeros((pages, Hkv, P, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((pages, Hkv), device="cuda") for _ in range(2))
+    n = 150
+    table = np.array([[pages - 1, 3, pages - 2]])
+    rows = np.arange(n)
+    x = torch.randn((2, n, Hkv, d), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    ops.kv8_append(x[0].cuda(), x[1].cuda(), kc, vc, ks, vs, cu(table[0, rows // P], torch.int32),
+                   cu(rows % P, torch.int32))
+    q = torch.randn((1, 1, 16, d), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    o, lse = ops.decode_kv8(q.cuda(), kc, vc, ks, vs, cu(table, torch.int32), cu([n], torch.int32), n)
+    assert ops.device_error() == 0
+    at = torch.tensor(table[0], device="cuda")
+    small = [t[at].cpu().numpy() for t in (kc, vc, ks, vs)]
+    ref = [(np.zeros((3, Hkv, P, d), np.uint8), np.zeros((3, Hkv), np.float32)) for _ in range(2)]
+    for y, (c, s) in zip(x, ref):
+        serving.kv8_append(synth.to_f64(y), c, s, (rows // P).tolist(), (rows % P).tolist())
+    for side in (0, 1):
+        assert np.array_equal(small[side], ref[side][0]) and np.array_equal(small[2 + side], ref[side][1])
+    assert_close(o, lse, serving.decode_kv8(synth.to_f64(q), ref[0][0], ref[1][0], ref[0][1], ref[1][1], np.array([[0, 1, 2]]),
+                                            [n], -1, d ** -0.5))
+    assert int((kc[4:-2] != 0).sum()) == 0 and int((vc[:3] != 0).sum()) == 0
