@@ -312,3 +312,21 @@ def test_pages_beyond_4_gib():
     assert_close(o, lse, serving.decode_kv8(synth.to_f64(q), ref[0][0], ref[1][0], ref[0][1], ref[1][1], np.array([[0, 1, 2]]),
                                             [n], -1, d ** -0.5))
     assert int((kc[4:-2] != 0).sum()) == 0 and int((vc[:3] != 0).sum()) == 0
+
+
+def test_what_the_workspace_held_does_not_matter():
+    """A captured call replayed over a workspace of every sort of content, and with many pieces a unit."""
+    a = dev(make([3000, 17], 1, 4, 2, 64, 16, seed=13))
+    ws = torch.empty(_lib.load().fa_decode_kv8_workspace_bytes(2, 1, 4, 2, 64, 90), dtype=torch.uint8, device="cuda")
+    want = ops.decode_kv8(*a, 3000, num_shares=90)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = ops.decode_kv8(*a, 3000, num_shares=90, workspace=ws)
+    for fill in (0, 0xFF, 0x01, None, None, 0x80):
+        if fill is not None:
+            ws.fill_(fill)
+        o.zero_(), lse.zero_()
+        g.replay()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    q, k, v, table, lens = make([3000, 17], 1, 4, 2, 64, 16, seed=13)
+    assert_close(o, lse, serving.decode_kv8(synth.to_f64(q), k[0], v[0], k[1], v[1], table, lens, -1, 64 ** -0.5))
