@@ -9,13 +9,10 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
-#include <atomic>
-#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
-#include <random>
 
 namespace fa {
 
@@ -868,23 +865,6 @@ fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, voi
   return launch_kv8_append(p, d, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-// A tag for a call's counts in its workspace: 48 bits, no two calls' of a process
-// alike, from a random start, so that words of other programs' workspaces are
-// hardly ever taken for this call's.
-static unsigned long long kv8_next_tag() {
-  static std::atomic<unsigned long long> next{[] {
-    unsigned long long at = (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() * 0x9e3779b97f4a7c15ull;
-    try {
-      std::random_device r;
-      at ^= ((unsigned long long)r() << 32) ^ r();
-    } catch (...) {  // (no source of random numbers: the clock alone)
-    }
-    return at;
-  }()};
-  const unsigned long long t = next.fetch_add(1) & 0xffffffffffffull;
-  return t == 0 || t == 0xffffffffffffull ? kv8_next_tag() : t;
-}
-
 // Keys that the queries of a request see at most.
 static int kv8_span(int Nq, int max_seq_len, int window_left) {
   if (window_left < 0 || (long long)window_left + Nq >= max_seq_len) return max_seq_len;
@@ -894,7 +874,7 @@ static int kv8_span(int Nq, int max_seq_len, int window_left) {
 size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_shares) {
   if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || d < 1 || num_shares < 1) return 0;
   const size_t rows = 2 * (size_t)num_shares * kv8_row_tile(Nq * (Hq / Hkv));
-  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float)) + 2 * (size_t)num_shares * sizeof(uint64_t);
+  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float));
 }
 
 int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left) {
@@ -927,7 +907,6 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   if (window_left >= max_seq_len) window_left = -1;  // a window past every key is no window
   if (num_shares == 0) num_shares = fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, max_seq_len, window_left);
   const size_t rows = 2 * (size_t)num_shares * kv8_row_tile(Nq * (Hq / Hkv));
-  const size_t o_bytes = align256(rows * d * sizeof(float)), l_bytes = align256(rows * sizeof(float));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = q;
   p.k_codes = static_cast<const uint8_t*>(k_codes);
@@ -939,9 +918,7 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   p.o = o;
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws);
-  p.part_lse = reinterpret_cast<float*>(ws + o_bytes);
-  p.done = reinterpret_cast<unsigned long long*>(ws + o_bytes + l_bytes);
-  p.tag = kv8_next_tag();
+  p.part_lse = reinterpret_cast<float*>(ws + align256(rows * d * sizeof(float)));
   p.B = B;
   p.Nq = Nq;
   p.Hq = Hq;

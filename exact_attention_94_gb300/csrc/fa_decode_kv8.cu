@@ -28,13 +28,9 @@
 // Work: the tiles of 128 keys of all (request, K/V head, row tile) units in
 // one list, dealt in equal shares to the CTAs (two per SM), which balances
 // requests of any lengths; a unit counts some tiles more than it has, for its
-// start and end.  A unit inside one share is finished there; one that shares'
-// borders cut leaves normalised partials, and the CTA that adds the last of them
-// merges them all, in the shares' order: lse = log sum_c e^(lse_c), O = sum_c
-// e^(lse_c - lse) O_c.  Which is the last, a word per unit in the workspace
-// counts.  A word that does not carry the call's own tag counts as zero, so what
-// the workspace held before does not matter, and the last sets it back to zero,
-// so a replayed call, which has its tag again, finds none of it.
+// start and end.  A unit inside one share is finished there; one that
+// a share's border cuts leaves normalised partials, which a second kernel
+// merges: lse = log sum_c e^(lse_c), O = sum_c e^(lse_c - lse) O_c.
 //
 // CTA:
 //   warps 0-3  thread = key of the tile (TMEM lane) for S and P, and one of the
@@ -89,7 +85,7 @@ struct Layout {
   static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // votes, scan, start
   // pieces announced ahead of their tiles, with their rows of Q as they lie in memory
   static constexpr int kPieces = (RT == 8 && D == 128) || RT == 32 ? 1 : RT <= 8 ? 4 : 2;  // as many as the CTAs leave room for
-  static constexpr uint32_t kPieceOff = kMiscOff + 208;                      // [kPieces] 32 bytes each
+  static constexpr uint32_t kPieceOff = kMiscOff + 192;                      // [kPieces] 32 bytes each
   static constexpr uint32_t kStageOff = (kPieceOff + kPieces * 32 + 127) / 128 * 128;
   static constexpr uint32_t kStage = RT * D * 2u;
   static constexpr uint32_t kBarOff = kStageOff + kPieces * kStage;
@@ -123,6 +119,12 @@ __host__ __device__ __forceinline__ long long quick_div(long long a, long long b
   return (((unsigned long long)a | (unsigned long long)b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
+// First slot of a CTA's share of the whole weight.
+__host__ __device__ __forceinline__ long long share_begin(long long total, int shares, int k) {
+  const long long each = quick_div(total, shares), more = total - each * shares;  // the first `more` shares have one slot more
+  return each * k + (k < more ? k : more);
+}
+
 // A unit weighs its tiles and p.lead more, what its start and end cost a CTA in
 // tiles; slot p.lead + t of its weight is tile t.
 __device__ __forceinline__ long long kv8_weight(const Kv8DecodeParams& p, int tiles) {
@@ -130,37 +132,21 @@ __device__ __forceinline__ long long kv8_weight(const Kv8DecodeParams& p, int ti
 }
 
 // A piece of a share: tiles t0 .. t1 - 1 of unit u (K/V head and row tile) of
-// request b; t0 = t1 marks the share's end.  The unit's first piece leaves its
-// partial in slot `slot`, the others, of the shares up to `last`, in slots twice
-// their shares' numbers.
+// request b; t0 = t1 marks the share's end.
 struct Piece {
-  int b, u, t0, t1, tiles, len, slot, last;
-};
-
-// How the whole weight is dealt: the first `more` shares have one slot more than `each`.
-struct Deal {
-  long long each, more;
-  __device__ __forceinline__ Deal(long long total, int shares) {
-    each = quick_div(total, shares);
-    more = total - each * shares;
-  }
-  __device__ __forceinline__ long long begin(int k) const { return each * k + (k < more ? k : more); }
-  __device__ __forceinline__ int share_of(long long t) const {
-    return (int)(t < more * (each + 1) ? quick_div(t, each + 1) : more + quick_div(t - more * (each + 1), each));
-  }
+  int b, u, t0, t1, tiles, len, beg, pad;
 };
 
 // The producer's walk over the share, piece by piece.
 struct Walk {
-  long long at;    // next slot of the whole weight, and the share's end
-  long long to;
-  long long off;   // the same slot within the weight of the request's units
+  long long left;  // weight of the share still to come
+  long long off;   // next slot within the weight of the request's units
   int b, tiles, len;
   int len_next;    // seq_lens[b + 1], read long before it is needed
 
-  __device__ __forceinline__ Piece next(const Kv8DecodeParams& p, int units, const Deal& deal) {
+  __device__ __forceinline__ Piece next(const Kv8DecodeParams& p, int units) {
     Piece s{};
-    while (at < to) {
+    while (left > 0) {
       const int each = tiles + p.lead;
       if (tiles == 0 || off >= (long long)each * units) {  // the request's units are done (or it has no keys)
         off = 0;
@@ -171,41 +157,16 @@ struct Walk {
         continue;
       }
       const int u = (int)quick_div(off, each);
-      const int w0 = (int)(off - (long long)u * each), w1 = (int)(to - at < each - w0 ? w0 + (to - at) : each);
-      const long long u0 = at - w0;  // the unit's first slot
+      const int w0 = (int)(off - (long long)u * each), w1 = (int)(left < each - w0 ? w0 + left : each);
       off += w1 - w0;
-      at += w1 - w0;
-      s = {b, u, max(w0 - p.lead, 0), max(w1 - p.lead, 0), tiles, len, 0, 0};
-      if (s.t0 < s.t1) {
-        if (s.t1 - s.t0 < tiles) {
-          const int first = deal.share_of(u0 + p.lead);
-          s.slot = 2 * first + (deal.begin(first) < u0 ? 1 : 0);  // (not that share's first piece, if it begins before the unit)
-          s.last = deal.share_of(u0 + each - 1);
-        }
-        return s;
-      }
+      left -= w1 - w0;
+      s = {b, u, max(w0 - p.lead, 0), max(w1 - p.lead, 0), tiles, len, kv8_begin(p, len), 0};
+      if (s.t0 < s.t1) return s;
     }
     s.t0 = s.t1 = 0;
     return s;
   }
 };
-
-// Counts a piece of a cut unit as done; true for the last of n.  What the CTA has
-// written before is there for whoever finds the count, and the other pieces'
-// partials for the last.
-__device__ __forceinline__ bool kv8_done(unsigned long long* word, unsigned long long tag, int n) {
-  __threadfence();
-  unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(word), now, was;
-  do {
-    was = seen;
-    now = ((was >> 16) == tag ? was : tag << 16) + 1;
-    seen = atomicCAS(word, was, now);
-  } while (seen != was);
-  __threadfence();
-  if ((int)(now & 0xffffu) < n) return false;
-  atomicExch(word, 0ull);
-  return true;
-}
 
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r) {
@@ -283,9 +244,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::kBarOff + 8 * L::kBars);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sb + L::kBarOff + 8 * L::kBars + 4);
   Piece* s_piece = reinterpret_cast<Piece*>(sb + L::kPieceOff);
-  int* s_vote = reinterpret_cast<int*>(sb + L::kMiscOff);                       // [2][SOFT], then [SOFT] for who is last
-  long long* s_scan = reinterpret_cast<long long*>(sb + L::kMiscOff + 96);      // [SOFT + 2] warps' sums
-  volatile long long* s_start = reinterpret_cast<volatile long long*>(sb + L::kMiscOff + 176);  // b, off, tiles and len
+  int* s_vote = reinterpret_cast<int*>(sb + L::kMiscOff);                       // [2][SOFT]
+  long long* s_scan = reinterpret_cast<long long*>(sb + L::kMiscOff + 64);      // [SOFT + 2] warps' sums
+  volatile long long* s_start = reinterpret_cast<volatile long long*>(sb + L::kMiscOff + 144);  // b, off, tiles and len
 
   if (warp == SOFT + 1) {
     tmem_alloc(base + L::kBarOff + 8 * L::kBars + 4, L::kCols);
@@ -332,8 +293,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     if (x < warp) before += s_scan[x];
     total += s_scan[x];
   }
-  const Deal deal(total, (int)gridDim.x);
-  const long long from = deal.begin(k), to = deal.begin(k + 1);
+  const long long from = share_begin(total, (int)gridDim.x, k), to = share_begin(total, (int)gridDim.x, k + 1);
   if (from >= before && from < before + mine) {  // the share begins in one of this thread's requests
     long long at = before;
     for (int b = b0; b < b1; ++b) {
@@ -352,6 +312,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
   const uint32_t tS = tmem, tO = tmem + 2 * L::kNS;
   const WaitCtx w{abort_flag, p.timeout_ns, p.err};
   bool ok = true;
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge may be set up; it waits for this grid's end
 
   if (warp == SOFT) {
     // ============================================================ producer
@@ -375,10 +336,10 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       bool on;
       int hk;
     };
-    Walk walk{from, from, 0, 0, 0, 0, 0};
+    Walk walk{to - from, 0, 0, 0, 0, 0};
     if (to > from) {
       const int b = (int)s_start[0];
-      walk = {from, to, s_start[1], b, (int)(s_start[2] >> 32), (int)(s_start[2] & 0xffffffffll),
+      walk = {to - from, s_start[1], b, (int)(s_start[2] >> 32), (int)(s_start[2] & 0xffffffffll),
               b + 1 < p.B ? p.seq_lens[b + 1] : 0};
     }
     const int bpb = p.box_rows / 16;  // 16-key groups per TMA box
@@ -407,14 +368,14 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       q = {};
       if (!more || !ok) return;
       if (t_next == pc.t1) {
-        pc = walk.next(p, units, deal);
+        pc = walk.next(p, units);
         t_next = pc.t0;
         more = pc.t0 < pc.t1;
         announce();
         if (!more || !ok) return;
       }
       q.n = min(4, pc.t1 - t_next);
-      const int g = (kv8_begin(p, pc.len) + t_next * kKv8Tile) / 16 + lane;
+      const int g = (pc.beg + t_next * kKv8Tile) / 16 + lane;
       q.on = lane < 8 * q.n && g < (pc.len + 15) / 16;
       q.hk = (int)((unsigned)pc.u / (unsigned)p.row_tiles);
       t_next += q.n;
@@ -513,13 +474,6 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         if (t > 0) ok = pv(it - 1, t == 1);
       }
       if (ok) ok = pv(it - 1, n == 1);
-    }
-    // requests without keys, in turn for the CTAs
-    for (int b = k; b < p.B; b += (int)gridDim.x) {
-      if (kv8_tiles(p, kv8_len(p, b)) > 0) continue;
-      uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (size_t)b * p.Nq * p.Hq * D);
-      for (int e = lane; e < p.Nq * p.Hq * (D / 8); e += 32) o[e] = make_uint4(0u, 0u, 0u, 0u);
-      for (int e = lane; e < p.Nq * p.Hq; e += 32) p.lse[(size_t)b * p.Nq * p.Hq + e] = -INFINITY;
     }
   } else {
     // ============================================================ softmax
@@ -633,7 +587,6 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     Piece pc;
     ok = take(0, pc);
     while (ok && pc.t0 < pc.t1) {
-      const int beg = kv8_begin(p, pc.len);
       const float* s_qsc = reinterpret_cast<const float*>(sb + L::kRowOff + (piece & 1) * 2 * RT * 4) + g0;
       const int* s_pos = reinterpret_cast<const int*>(s_qsc + RT);  // (both from the group's first row)
       const int rows = rows_of(pc);
@@ -654,7 +607,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         tc_fence_after();
         const float* sc = reinterpret_cast<const float*>(sb + L::kScOff + (it % VS) * L::kScBytes);
         const float ks = sc[chunk], vs = sc[8 + chunk], lvs = fmaxf(__log2f(vs), kLeastScale);
-        const int j0 = beg + t * kKv8Tile, j = j0 + key;
+        const int j0 = pc.beg + t * kKv8Tile, j = j0 + key;
         // some row does not see some key of the tile
         const bool partial = j0 + kKv8Tile > pc.len - p.Nq + 1 || (p.win_left >= 0 && j0 < pc.len - 1 - p.win_left);
         auto sees = [&](int r) { return j <= s_pos[r] && (p.win_left < 0 || j >= s_pos[r] - p.win_left); };
@@ -864,64 +817,6 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         }
       }
       tc_fence_before();
-      if (!whole) {
-        __threadfence();  // this thread's part of the partial, before the count says that it is there
-        ok = exchange();
-        if (!ok) break;
-        const int n = done.last - (done.slot >> 1) + 1;
-        if (quarter == 0 && lane == 0) s_vote[2 * SOFT + warp] = kv8_done(p.done + (done.slot >> 1) * GROUPS + group, p.tag, n);
-        ok = exchange();
-        if (!ok) break;
-        if (s_vote[2 * SOFT + group * 4]) {  // the unit's last: merge, a warp per row, AT partials' loads at a time
-          __threadfence();
-          constexpr int E = D / 32, AT = GROUPS > 1 ? 4 : 8;
-#pragma unroll 1
-          for (int r = quarter; r < mine; r += 4) {
-            float sum[E], wsum = 0.f, m = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < E; ++x) sum[x] = 0.f;
-#pragma unroll 1
-            for (int c0 = 0; c0 < n; c0 += AT) {
-              float lc[AT], v[AT][E];
-#pragma unroll
-              for (int y = 0; y < AT; ++y) {
-                const int c = min(c0 + y, n - 1);
-                const size_t at = (size_t)(c == 0 ? done.slot : 2 * ((done.slot >> 1) + c)) * RT + g0 + r;
-                lc[y] = c0 + y < n ? __ldcg(p.part_lse + at) : -INFINITY;
-#pragma unroll
-                for (int x = 0; x < E; x += 2) {
-                  const float2 t = __ldcg(reinterpret_cast<const float2*>(p.part_o + at * D + lane * E + x));
-                  v[y][x] = t.x, v[y][x + 1] = t.y;
-                }
-              }
-              float mn = m;
-#pragma unroll
-              for (int y = 0; y < AT; ++y) mn = fmaxf(mn, lc[y]);
-              const float ref = mn == -INFINITY ? 0.f : mn, al = ex2_sfu(m - ref);
-              m = mn;
-              wsum *= al;
-#pragma unroll
-              for (int x = 0; x < E; ++x) sum[x] *= al;
-#pragma unroll
-              for (int y = 0; y < AT; ++y) {
-                const float wc = ex2_sfu(lc[y] - ref);
-                wsum += wc;
-#pragma unroll
-                for (int x = 0; x < E; ++x) sum[x] = fmaf(wc, v[y][x], sum[x]);
-              }
-            }
-            int i, h;
-            const size_t row = q_row(done, g0 + r, i, h);
-            const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D + lane * E);
-#pragma unroll
-            for (int x = 0; x < E; x += 2) dst[x / 2] = pack_bf16x2(sum[x] * inv, sum[x + 1] * inv);
-            if (lane == 0)
-              p.lse[((size_t)done.b * p.Hq + h) * p.Nq + i] =
-                  wsum == 0.f ? -INFINITY : (m + __log2f(wsum)) * 0.69314718055994531f;
-          }
-        }
-      }
       ok = exchange();  // the sums' places are free again
       if (!ok) break;
       ++piece;
@@ -937,6 +832,91 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
   if (warp == SOFT + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+// What the shares' borders cut, and requests without keys.  One warp per query
+// row: the row's unit lies in the shares ka .. kb; one share alone has finished
+// it.  Where the work begins and ends is added up again from the lengths, by
+// each block, which needs nothing of the main kernel and so is done while that
+// one ends.
+template <int D>
+__global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_constant__ Kv8DecodeParams p, int RT,
+                                                                  int shares) {
+  constexpr int E = D / 32;
+  const int lane = lane_id(), units = p.Hkv * p.row_tiles;
+  const int b = blockIdx.y;
+  __shared__ long long s_before[8], s_all[8];
+  long long before = 0, total = 0;
+  for (int y = threadIdx.x; y < p.B; y += 256) {
+    const int n = p.seq_lens[y];
+    const long long wt = kv8_weight(p, kv8_tiles(p, min(max(n, 0), p.max_len))) * units;
+    total += wt;
+    if (y < b) before += wt;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  if (lane == 0) s_before[threadIdx.x >> 5] = before, s_all[threadIdx.x >> 5] = total;
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int y = 0; y < 8; ++y) before += s_before[y], total += s_all[y];
+  const long long weight = kv8_weight(p, kv8_tiles(p, min(max(p.seq_lens[b], 0), p.max_len)));
+  const long long each = quick_div(total, shares), more = total - each * shares;
+  auto share_of = [&](long long t) {
+    return (int)(t < more * (each + 1) ? quick_div(t, each + 1) : more + quick_div(t - more * (each + 1), each));
+  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done
+  for (int x0 = blockIdx.x * 8 + (threadIdx.x >> 5); x0 < p.Nq * p.Hq; x0 += gridDim.x * 8) {
+    const int i = p.Nq == 1 ? 0 : (int)((unsigned)x0 / (unsigned)p.Hq), h = x0 - i * p.Hq;
+    const int hk = (int)((unsigned)h / (unsigned)p.group), x = i * p.group + h - hk * p.group;  // row of the K/V head
+    const int u = hk * p.row_tiles + x / RT, r = x % RT;
+    const long long u0 = before + u * weight;
+    int ka = 0, kb = -1;  // (a request without keys: nothing to merge, zeros to write)
+    if (weight > 0) {
+      ka = share_of(u0 + p.lead);
+      kb = share_of(u0 + weight - 1);
+      if (ka == kb) continue;
+    }
+    // four shares at a time, their loads together, against a running maximum
+    float acc[E], wsum = 0.f, m = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int k0 = ka; k0 <= kb; k0 += 4) {
+      float lc[4], v[4][E];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const bool on = k0 + y <= kb;
+        const int k = on ? k0 + y : kb;
+        const long long sl = (2 * (long long)k + (each * k + (k < more ? k : more) < u0 ? 1 : 0)) * RT + r;
+        lc[y] = on ? p.part_lse[sl] : -INFINITY;
+        const float* src = p.part_o + sl * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[y][e] = src[e];
+      }
+      const float mn = fmaxf(fmaxf(fmaxf(lc[0], lc[1]), fmaxf(lc[2], lc[3])), m), ref = mn == -INFINITY ? 0.f : mn;
+      const float al = ex2_sfu(m - ref);
+      m = mn;
+      wsum *= al;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= al;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float wc = ex2_sfu(lc[y] - ref);
+        wsum += wc;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wc, v[y][e], acc[e]);
+      }
+    }
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)b * p.Nq * p.Hq + x0) * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0)
+      p.lse[((size_t)b * p.Hq + h) * p.Nq + i] = wsum == 0.f ? -INFINITY : (m + __log2f(wsum)) * 0.69314718055994531f;
   }
 }
 
@@ -972,7 +952,20 @@ static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8
   // Where a share is a tile or less, nothing is gained by making room for starts.
   p.lead = kv8_most_tiles(p.B, p.Nq, p.Hkv, p.group, span) > kv8_ctas(p.Nq, p.group) ? kLead(RT) : 0;
   kern<<<shares, Layout<D, RT>::kThreads, smem, stream>>>(tk, tv, p);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the merge's launch overlaps the main kernel (programmatic dependent launch); its blocks wait for the grid's end
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  // (a block adds up B lengths: with many requests, one block for all rows of one)
+  cfg.gridDim = dim3(p.B <= 512 ? (unsigned)((p.Nq * p.Hq + 7) / 8) : 1u, (unsigned)p.B);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_decode_kv8_merge_kernel<D>, static_cast<const Kv8DecodeParams&>(p), (int)RT, shares);
 }
 
 template <int D>

@@ -229,8 +229,6 @@ struct Kv8DecodeParams {
   float* lse;
   float* part_o;             // [2 * shares, RT, d] fp32: the pieces a share's borders cut, each normalised
   float* part_lse;           // [2 * shares, RT] log2 of each piece's softmax mass
-  unsigned long long* done;  // [2 * shares] pieces done of the units that borders cut: tag << 16 | count
-  unsigned long long tag;    // this call's, 48 bits
   int B, Nq, Hq, Hkv, group;
   int page_size, num_pages, max_blocks, max_len;
   int win_left;              // -1: no window

@@ -559,10 +559,8 @@ fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, voi
  *   num_shares   : shares (CTAs) that the work is dealt to, 1 .. 65535; 0 =
  *                  choose (fa_decode_kv8_num_shares)
  *   workspace    : fa_decode_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, shares) bytes,
- *                  16-byte aligned, contents on entry do not matter (but after
- *                  a FA_ERR_TIMEOUT, fill it anew before the captured call that
- *                  met it is replayed); calls whose work overlaps on the GPU
- *                  need one each
+ *                  16-byte aligned, contents on entry do not matter; calls
+ *                  whose work overlaps on the GPU need one each
  * What a page holds behind a request's last key is never used, whatever it
  * is.  Table entries outside the pool and lengths outside [0, max_seq_len] are
  * handled and reported as in fa_decode_paged.  page_size a multiple of 16, d = 64
