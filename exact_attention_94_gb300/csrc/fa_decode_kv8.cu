@@ -72,19 +72,22 @@ struct Layout {
   static constexpr int kVs = kCtas == 3 ? 256 / D : 384 / D;
   static constexpr int kSlots = kKs + kVs;
   static constexpr int kNS = 2 * RT < 16 ? 16 : 2 * RT;                      // columns of S
-  static constexpr int kNP = (3 * RT + 15) / 16 * 16;                        // columns of P and O
+  // Columns of P and O: three parts of RT, and what is left of a strip's 32,
+  // which holds anything and is not read.  P lies in strips of 32 columns, a
+  // key's 32 bytes after another's, so that its thread writes 16 at a time.
+  static constexpr int kNP = (3 * RT + 31) / 32 * 32;
+  static constexpr uint32_t kStrip = kKv8Tile * 32u;
   static constexpr uint32_t kUsed = 2 * kNS + kNP;
   static constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;  // TMEM columns, two CTAs' 512 at most
   static constexpr uint32_t kPOff = kSlots * kSlot;
-  // (P's rows past 3 RT, whole eights of them, are no rows of its own: the product's columns there are not read)
-  static constexpr uint32_t kQOff = kPOff + (3 * RT + 7) / 8 * 1024u;
+  static constexpr uint32_t kQOff = kPOff + kKv8Tile * (uint32_t)kNP;
   static constexpr uint32_t kScOff = kQOff + kNS * (uint32_t)D;              // per V slot: 8 key scales, 8 value scales
   static constexpr uint32_t kScBytes = 64;
   static constexpr uint32_t kMaxOff = kScOff + kVs * kScBytes;        // [4][RT] each: warps' maxima, sums, references, factors, output rows
   static constexpr uint32_t kRowOff = kMaxOff + 20 * RT * 4;                 // two of: [RT] query scales, [RT] positions
   static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // votes, scan, start
   // pieces announced ahead of their tiles, with their rows of Q as they lie in memory
-  static constexpr int kPieces = (RT == 8 && D == 128) || RT == 32 ? 1 : RT <= 8 ? 4 : 2;  // as many as the CTAs leave room for
+  static constexpr int kPieces = (RT == 8 && D == 128) || RT == 32 ? 1 : RT == 8 ? 3 : 2;  // as many as the CTAs leave room for
   static constexpr uint32_t kPieceOff = kMiscOff + 192;                      // [kPieces] 32 bytes each
   static constexpr uint32_t kStageOff = (kPieceOff + kPieces * 32 + 127) / 128 * 128;
   static constexpr uint32_t kStage = RT * D * 2u;
@@ -211,10 +214,6 @@ __device__ __forceinline__ float warp_row_sums(float (&v)[RT], int lane) {
 #pragma unroll
   for (int b = 16 / RT; b > 0; b >>= 1) x += __shfl_xor_sync(0xffffffffu, x, b);
   return x;
-}
-
-__device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 }  // namespace
@@ -431,10 +430,10 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == SOFT + 1) {
     // ============================================================ products
-    constexpr uint32_t IDESC_S = idesc_e4m3(128, L::kNS), IDESC_O = idesc_e4m3(D, L::kNP, true);
+    constexpr uint32_t IDESC_S = idesc_e4m3(128, L::kNS), IDESC_O = idesc_e4m3(D, L::kNP, true, true);
     const uint32_t qa = base + L::kQOff, pa = base + L::kPOff;
     const uint64_t qd = D == 128 ? smem_desc_sw128(qa, 16, 1024) : smem_desc_sw64(qa, 16, 512);
-    const uint64_t pd = smem_desc_sw128(pa, 16, 1024);
+    const uint64_t pd = smem_desc_sw32(pa, L::kStrip, 256);
     auto pv = [&](int it, bool first) {  // O (+)= V^T P^T of tile `it`
       const int slot = KS + it % VS;
       bool good = mbar_wait(PF, it & 1, w, 54);
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       const uint64_t vd = D == 128 ? smem_desc_sw128(va, 16, 1024) : smem_desc_sw64(va, 16, 512);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_ss_f8_w(tO, desc_add(vd, kk * 32 * D), desc_add(pd, kk * 32), IDESC_O, (kk > 0 || !first) ? 1u : 0u);
+        mma_ss_f8_w(tO, desc_add(vd, kk * 32 * D), desc_add(pd, kk * 32 * 32), IDESC_O, (kk > 0 || !first) ? 1u : 0u);
       mma_commit_w(EMPTY(slot));
       mma_commit_w(OF);
       return true;
@@ -488,8 +487,11 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     const float* g_sum = my_sum - quarter * RG;
     const uint32_t lane_sel = (uint32_t)quarter << 21;  // TMEM lane 32 * quarter
     const int key = quarter * 32 + lane;             // key of the tile
-    const uint32_t p_at = base + L::kPOff + g0 * 128 + (key & 15);  // this thread's byte in P's 128-byte rows
-    const uint32_t chunk = (uint32_t)key >> 4;
+    // column c of this thread's key in P: its strip, the key's 32 bytes, their swizzle
+    uint8_t* p_row = sb + L::kPOff + key * 32;
+    const int p_flip = key << 2 & 16;
+    auto p_at = [&](int c) { return p_row + (c >> 5) * L::kStrip + ((c & 31) ^ p_flip); };
+    const int group16 = key >> 4;                    // of the tile's keys: where its scales are
     auto rows_of = [&](const Piece& s) { return min(RT, p.Nq * p.group - s.u % p.row_tiles * RT); };
     // row r of a piece: its row of q and o, its query token
     auto q_row = [&](const Piece& s, int r, int& i, int& h) {
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         if (!ok) break;
         tc_fence_after();
         const float* sc = reinterpret_cast<const float*>(sb + L::kScOff + (it % VS) * L::kScBytes);
-        const float ks = sc[chunk], vs = sc[8 + chunk], lvs = fmaxf(__log2f(vs), kLeastScale);
+        const float ks = sc[group16], vs = sc[8 + group16], lvs = fmaxf(__log2f(vs), kLeastScale);
         const int j0 = pc.beg + t * kKv8Tile, j = j0 + key;
         // some row does not see some key of the tile
         const bool partial = j0 + kKv8Tile > pc.len - p.Nq + 1 || (p.win_left >= 0 && j0 < pc.len - 1 - p.win_left);
@@ -657,9 +659,15 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
             tmem_load<H>(tS + (it & 1) * L::kNS + lane_sel + RT + g0 + h, s2);
             tmem_ld_wait();
 #pragma unroll
-            for (int r = 0; r < H; ++r) {
-              const float x = fmaf(__uint_as_float(s2[r]), 0.0625f, __uint_as_float(s1[r]));
-              s[h + r] = fmaf(x, ks * s_qsc[h + r], -my_ref[h + r]);
+            for (int r = 0; r < H; r += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(s_qsc + h + r);
+              const float4 g = *reinterpret_cast<const float4*>(my_ref + h + r);
+              const float qsc[4] = {f.x, f.y, f.z, f.w}, ref[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float x = fmaf(__uint_as_float(s2[r + e]), 0.0625f, __uint_as_float(s1[r + e]));
+                s[h + r + e] = fmaf(x, ks * qsc[e], -ref[e]);
+              }
             }
           }
           if (partial) {
@@ -732,30 +740,37 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 57));
           if (!ok) break;
         }
+        // The split works on p rounded to f16, by 2^-12 of itself at most: 11 bits,
+        // which the three parts hold exactly, and every difference of theirs too.
         const float vn = poison ? 0.f : vs * kAtRef;
+        uint32_t code[3][RG / 4];
 #pragma unroll
         for (int r = 0; r < RG; r += 2) {
           const float p0 = ex2_sfu(s[r]), p1 = ex2_sfu(s[r + 1]);
           l[r] += p0;
           l[r + 1] += p1;
-          float x = p0 * vn, y = p1 * vn;
+          __half2 x = pack_f16x2(p0 * vn, p1 * vn);
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
-            const uint32_t two = pack_e4m3x2(x, y);
-            const int col = part * RT + r;  // (from the group's first row)
-            sts_u8(p_at + col * 128 + ((chunk ^ (col & 7)) << 4), two & 0xffu);
-            sts_u8(p_at + (col + 1) * 128 + ((chunk ^ ((col + 1) & 7)) << 4), two >> 8);
-            if (part < 2) {
-              const float2 f = unpack_e4m3x2(two);
-              x = (x - f.x) * 16.f;
-              y = (y - f.y) * 16.f;
-            }
+            const uint32_t two = pack_e4m3x2(x);
+            code[part][r / 4] = r & 2 ? code[part][r / 4] | two << 16 : two;
+            if (part < 2) x = __hmul2(__hsub2(x, unpack_e4m3x2_f16(two)), __float2half2_rn(16.f));
           }
+        }
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          uint8_t* at = p_at(part * RT + g0);
+          if constexpr (RG == 16)
+            *reinterpret_cast<uint4*>(at) = make_uint4(code[part][0], code[part][1], code[part][2], code[part][3]);
+          else if constexpr (RG == 8)
+            *reinterpret_cast<uint2*>(at) = make_uint2(code[part][0], code[part][1]);
+          else
+            *reinterpret_cast<uint32_t*>(at) = code[part][0];
         }
         if (poison) {
 #pragma unroll 1
           for (int r = 0; r < RG; ++r)
-            if (sees(r)) sts_u8(p_at + r * 128 + ((chunk ^ (r & 7)) << 4), 0x7fu);
+            if (sees(r)) *p_at(g0 + r) = 0x7f;
         }
         fence_proxy_async_smem();
         tc_fence_before();

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 namespace fa {
 
@@ -265,6 +266,17 @@ __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t lbo_
   return d;
 }
 
+// The same for rows of 32 bytes and the 32-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1u << 46;  // descriptor version for tcgen05
+  d |= (uint64_t)6u << 61;  // swizzle mode: 32-byte
+  return d;
+}
+
 // Advances a descriptor's start address by a byte offset (a multiple of 16).
 // Shared-memory addresses stay below 2^18 bytes, so the 14-bit address field
 // never carries into the neighbouring fields.
@@ -284,12 +296,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
          | ((uint32_t)(M >> 4) << 24);      // M / 16
 }
 
-// Instruction descriptor for kind::f8f6f4 with e4m3 A and B (format code 0), f32 D, B K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn = false) {
+// Instruction descriptor for kind::f8f6f4 with e4m3 A and B (format code 0) and f32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn = false, bool b_mn = false) {
   return (1u << 4)                          // D format: f32
          | (0u << 7)                        // A format: e4m3
          | (0u << 10)                       // B format: e4m3
          | ((a_mn ? 1u : 0u) << 15)         // A major-ness
+         | ((b_mn ? 1u : 0u) << 16)         // B major-ness
          | ((uint32_t)(N >> 3) << 17)       // N / 8
          | ((uint32_t)(M >> 4) << 24);      // M / 16
 }
@@ -427,6 +440,23 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t two) {
       : "=f"(f.x), "=f"(f.y)
       : "r"(h));
   return f;
+}
+
+// Two floats -> f16x2, e0 in the low half; f16x2 -> two e4m3 codes and back (exact).
+__device__ __forceinline__ __half2 pack_f16x2(float e0, float e1) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(e0), "f"(e1));
+  return *reinterpret_cast<__half2*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_e4m3x2(__half2 h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t*>(&h)));
+  return r;
+}
+__device__ __forceinline__ __half2 unpack_e4m3x2_f16(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+  return *reinterpret_cast<__half2*>(&h);
 }
 
 // The largest of a warp's 32 values, in every lane.
