@@ -16,7 +16,8 @@
 // 4) for what is within 2^13 of the row's largest, and to 2^-22 of the largest
 // below;  p = p1 + p2 / 16 + p3 / 256 to 2^-12 of itself, or, far below the
 // largest, to 2^-24 of that.  Page scales are one factor per key: k_scale
-// joins the score, v_scale the probability.
+// joins the score, v_scale the probability.  P lies by key (N-major), so a
+// thread, which has all rows of a key, stores 16 codes at a time.
 //
 // O stays in TMEM over the tiles.  It is made against a reference per row, in
 // log2 units of probability times value scale, at which p = 64: the reference
@@ -26,11 +27,14 @@
 // reference; fp32 holds them over the whole range of value scales.
 //
 // Work: the tiles of 128 keys of all (request, K/V head, row tile) units in
-// one list, dealt in equal shares to the CTAs (two per SM), which balances
-// requests of any lengths; a unit counts some tiles more than it has, for its
-// start and end.  A unit inside one share is finished there; one that
+// one list, dealt in equal shares to the CTAs (two or three per SM), which
+// balances requests of any lengths; a unit counts some tiles more than it has,
+// for its start and end.  A unit inside one share is finished there; one that
 // a share's border cuts leaves normalised partials, which a second kernel
-// merges: lse = log sum_c e^(lse_c), O = sum_c e^(lse_c - lse) O_c.
+// merges: lse = log sum_c e^(lse_c), O = sum_c e^(lse_c - lse) O_c.  (Merged by
+// the unit's last CTA instead, in the one kernel, a single request of 777
+// tokens took 13.3 us and not 9.6, 32 rows 78.8 and not 72.3: the fences and
+// the count cost more than a launch that overlaps the main kernel's end.)
 //
 // CTA:
 //   warps 0-3  thread = key of the tile (TMEM lane) for S and P, and one of the
@@ -40,6 +44,20 @@
 //   last       issues the products
 // S is double buffered in TMEM (the next tile's scores are ready when a tile's
 // softmax starts); P is not: it is written when the product before has read it.
+//
+// Measured, d = 128, pages of 16 to 64, replayed graphs of many calls:
+//   64 requests of 16385 to 32768 tokens, 64 heads over 8      473 us  6.83 TB/s
+//   8 requests of 1000 to 8192, 32 heads over 32                53 us  5.66 TB/s
+//   16 requests of 100 to 16384, 4 drafts, 64 heads over 8      61 us  4.44 TB/s
+//   32 requests, a window of 4096, 16 heads over 4, d = 64      21 us  2.98 TB/s
+//   1 request of 777, 32 heads over 8                          9.5 us
+// The first is as fast as the card copies.  The calls of 20 to 60 us lose some
+// 5 us to the start (lengths, page numbers, pages: three reads one after the
+// other before the first tile) and the merge.  32 rows are bound by the softmax
+// warps' instructions (issue slots 60% busy): they came from 82 us with one
+// group of warps and a byte store per code, by two groups (72), P by key and
+// its split in half precision (66), all scores read at once (62.5) and packed
+// fp32 arithmetic (61).
 #include "fa_internal.h"
 #include "ptx.cuh"
 
@@ -52,17 +70,24 @@ namespace {
 constexpr float kAtRef = 64.f;       // p at the reference
 constexpr float kHeadroom = 2.8f;    // log2(448 / 64), rounded down
 constexpr float kLeastScale = -100.f;  // log2 of a value scale, from below: a page of zeros counts as one of 2^-100
-constexpr int kLead(int RT) { return 3 + RT / 16; }  // what a unit's start and end cost, in tiles
+// What a unit's start and end cost, in tiles.  Against none at all: 16 requests
+// of 100 to 16384 tokens with 32 rows 110 -> 66 us, with 8 rows 70 -> 52; a
+// window of 4096 27.5 -> 21.  With 2 the 32 rows took 84, with 6 none gained.
+constexpr int kLead(int RT) { return 3 + RT / 16; }
 constexpr float kNoRef = -3.0e38f;   // reference of a row that has seen no key
 
-// CTAs per SM: three where their registers allow it.
+// CTAs per SM: three where registers and shared memory allow it, for the loads
+// in flight (two: 64 long requests, 8 rows, 484 us, and not 480; with d = 64, 128
+// requests up to 2000 tokens, 41.6 and not 36.5).
 constexpr int kv8_ctas_per_sm(int RT) { return RT <= 8 ? 3 : 2; }
 
 template <int D, int RT>
 struct Layout {
   // Softmax warps come in groups of four (one for each quarter of a tile's
-  // keys); 32 rows are two groups' work, 16 rows each.
+  // keys); 32 rows are two groups' work, 16 rows each (one group: 66 us for the
+  // 62.5 of two; for 16 rows and fewer two gain nothing).
   static constexpr int kGroups = RT == 32 ? 2 : 1;
+  static_assert(RT / kGroups <= 16, "rows of a group");
   static constexpr int kThreads = (4 * kGroups + 2) * 32;
   static constexpr uint32_t kSlot = 128u * D;                                // a tile of K or V
   static constexpr int kCtas = kv8_ctas_per_sm(RT);
@@ -480,7 +505,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     const int group = warp >> 2, quarter = warp & 3, g0 = group * RG;
     float* my_max = reinterpret_cast<float*>(sb + L::kMaxOff) + warp * RG;
     float* my_sum = my_max + 4 * RT;
-    float* my_ref = my_max + 8 * RT;                 // this warp's copies: the rows' references,
+    float* my_neg = my_max + 8 * RT;                 // this warp's copies: the rows' references, negated,
     float* my_al = my_max + 12 * RT;                 //   what a moved one multiplies sums by,
     int* my_at = reinterpret_cast<int*>(my_max + 16 * RT);  // and where the results go
     const float* g_max = my_max - quarter * RG;      // the group's four warps'
@@ -593,11 +618,11 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       const int* s_pos = reinterpret_cast<const int*>(s_qsc + RT);  // (both from the group's first row)
       const int rows = rows_of(pc);
       ok = __all_sync(0xffffffffu, mbar_wait(QB, piece & 1, w, 56));
-      float l[RG];
+      uint64_t l2[RG / 2];  // rows' sums of this key lane, in twos
 #pragma unroll
-      for (int r = 0; r < RG; ++r) l[r] = 0.f;
+      for (int r = 0; r < RG / 2; ++r) l2[r] = 0;
       __syncwarp();
-      if (lane < RG) my_ref[lane] = kNoRef;
+      if (lane < RG) my_neg[lane] = -kNoRef;
       __syncwarp();
 
       for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
@@ -651,22 +676,20 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         float s[RG];
         for (bool settled = false;;) {
           // ---- scores less the references, in log2 units
-          constexpr int H = RG > 8 ? 8 : RG;  // rows per load
-#pragma unroll
-          for (int h = 0; h < RG; h += H) {
-            uint32_t s1[H], s2[H];
-            tmem_load<H>(tS + (it & 1) * L::kNS + lane_sel + g0 + h, s1);
-            tmem_load<H>(tS + (it & 1) * L::kNS + lane_sel + RT + g0 + h, s2);
+          {
+            uint32_t s1[RG], s2[RG];
+            tmem_load<RG>(tS + (it & 1) * L::kNS + lane_sel + g0, s1);
+            tmem_load<RG>(tS + (it & 1) * L::kNS + lane_sel + RT + g0, s2);
             tmem_ld_wait();
 #pragma unroll
-            for (int r = 0; r < H; r += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(s_qsc + h + r);
-              const float4 g = *reinterpret_cast<const float4*>(my_ref + h + r);
-              const float qsc[4] = {f.x, f.y, f.z, f.w}, ref[4] = {g.x, g.y, g.z, g.w};
+            for (int r = 0; r < RG; r += 4) {
+              const ulonglong2 qsc = *reinterpret_cast<const ulonglong2*>(s_qsc + r);
+              const ulonglong2 neg = *reinterpret_cast<const ulonglong2*>(my_neg + r);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float x = fmaf(__uint_as_float(s2[r + e]), 0.0625f, __uint_as_float(s1[r + e]));
-                s[h + r + e] = fmaf(x, ks * qsc[e], -ref[e]);
+              for (int e = 0; e < 4; e += 2) {  // (two rows an instruction)
+                const uint64_t x = f2_fma(f2_pack(__uint_as_float(s2[r + e]), __uint_as_float(s2[r + e + 1])), f2_pack(0.0625f, 0.0625f),
+                                          f2_pack(__uint_as_float(s1[r + e]), __uint_as_float(s1[r + e + 1])));
+                f2_unpack(f2_fma(x, f2_mul(e ? qsc.y : qsc.x, f2_pack(ks, ks)), e ? neg.y : neg.x), s[r + e], s[r + e + 1]);
               }
             }
           }
@@ -676,9 +699,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           }
           if (settled) break;
           // ---- does any p pass what e4m3 holds?
-          float top = s[0];
+          float top = fmaxf(s[0], s[1]);
 #pragma unroll
-          for (int r = 1; r < RG; ++r) top = fmaxf(top, s[r]);
+          for (int r = 2; r < RG; r += 2) top = max3f(top, s[r], s[r + 1]);
           const bool move = __any_sync(0xffffffffu, top > kHeadroom - lvs);
           if (lane == 0) s_vote[(it & 1) * SOFT + warp] = move;
           ok = exchange();
@@ -710,13 +733,13 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           if (!ok) break;
           if (lane < RG) {
             const float x = fmaxf(fmaxf(g_max[lane], g_max[RG + lane]), fmaxf(g_max[2 * RG + lane], g_max[3 * RG + lane]));
-            const float old = my_ref[lane], now = fmaxf(old, x);  // (a row that sees no key yet has -inf in x)
-            my_ref[lane] = now;
+            const float old = -my_neg[lane], now = fmaxf(old, x);  // (a row that sees no key yet has -inf in x)
+            my_neg[lane] = -now;
             my_al[lane] = ex2_sfu(old - now);
           }
           __syncwarp();
 #pragma unroll
-          for (int r = 0; r < RG; ++r) l[r] *= my_al[r];
+          for (int r = 0; r < RG; r += 2) l2[r / 2] = f2_mul(l2[r / 2], f2_pack(my_al[r], my_al[r + 1]));
           if (t > pc.t0) {  // O stands at the old ones
             ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 62));
             if (!ok) break;
@@ -747,9 +770,10 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
 #pragma unroll
         for (int r = 0; r < RG; r += 2) {
           const float p0 = ex2_sfu(s[r]), p1 = ex2_sfu(s[r + 1]);
-          l[r] += p0;
-          l[r + 1] += p1;
-          __half2 x = pack_f16x2(p0 * vn, p1 * vn);
+          l2[r / 2] = f2_add(l2[r / 2], f2_pack(p0, p1));
+          float y0, y1;
+          f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(vn, vn)), y0, y1);
+          __half2 x = pack_f16x2(y0, y1);
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
             const uint32_t two = pack_e4m3x2(x);
@@ -759,13 +783,14 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         }
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
+          const uint32_t* c = code[part];
           uint8_t* at = p_at(part * RT + g0);
           if constexpr (RG == 16)
-            *reinterpret_cast<uint4*>(at) = make_uint4(code[part][0], code[part][1], code[part][2], code[part][3]);
+            *reinterpret_cast<uint4*>(at) = make_uint4(c[0], c[1], c[2], c[3]);
           else if constexpr (RG == 8)
-            *reinterpret_cast<uint2*>(at) = make_uint2(code[part][0], code[part][1]);
+            *reinterpret_cast<uint2*>(at) = make_uint2(c[0], c[1]);
           else
-            *reinterpret_cast<uint32_t*>(at) = code[part][0];
+            *reinterpret_cast<uint32_t*>(at) = c[0];
         }
         if (poison) {
 #pragma unroll 1
@@ -783,6 +808,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       ok = take(piece + 1, pc);
       if (!ok) break;
       // ---- each row's sum over the 128 key lanes
+      float l[RG];
+#pragma unroll
+      for (int r = 0; r < RG; r += 2) f2_unpack(l2[r / 2], l[r], l[r + 1]);
       const float row_sum = warp_row_sums<RG>(l, lane);
       if (lane % (32 / RG) == 0) my_sum[lane / (32 / RG)] = row_sum;
       ok = exchange();
@@ -798,7 +826,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       if (lane < mine) {
         const float sum = g_sum[lane] + g_sum[RG + lane] + g_sum[2 * RG + lane] + g_sum[3 * RG + lane];
         // sum = 0: the row sees none of these keys (a NaN passes through)
-        const float lse2 = sum == 0.f ? -INFINITY : my_ref[lane] + __log2f(sum);
+        const float lse2 = sum == 0.f ? -INFINITY : __log2f(sum) - my_neg[lane];
         my_al[lane] = sum == 0.f ? 0.f : 1.f / (sum * kAtRef);
         if (whole) {
           int i, h;
@@ -935,7 +963,12 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
   }
 }
 
-// Query rows of one CTA.
+// Query rows of one CTA.  A tile of fewer rows leaves room for a third CTA and
+// has less to do at a unit's start and end: 4 rows took 21.1 us in a tile of 4,
+// 22.9 in one of 8 and 26.1 in one of 16 (32 requests, a window of 4096, d = 64);
+// 8 rows 36.5 and 56.6 in tiles of 8 and 16 (128 requests up to 2000, d = 64); 16
+// rows 53.2 and 61.0 in tiles of 16 and 32 (two drafts of eight heads); and 32
+// rows 66 in one tile and 81 in two, which read the cache twice (four drafts).
 int kv8_row_tile(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 // CTAs that run at once, and the most tiles a call can have.
@@ -974,7 +1007,7 @@ static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  // (a block adds up B lengths: with many requests, one block for all rows of one)
+  // (a block adds up B lengths: with many requests, one block for all rows of a request, not B * rows / 8 sums of B)
   cfg.gridDim = dim3(p.B <= 512 ? (unsigned)((p.Nq * p.Hq + 7) / 8) : 1u, (unsigned)p.B);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
