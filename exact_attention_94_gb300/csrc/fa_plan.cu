@@ -10,8 +10,10 @@
 //     token c_b + i of request b: row cu_b + i, block (c_b + i) / P, whose page
 //     is the table's for a block held before, else
 //     free[count - 1 - (base_b + block - ceil(c_b / P))].
-// The step is bound by latency: a few thousand integers in, 12 bytes out per
-// row.  Every CTA scans all requests for itself (the sums stay in its shared
+// The step is bound by latency, a launch, two barriers and three reads one after
+// the other (lengths, free page, its entry): 3.4 us for 256 requests of a token,
+// against 2.8 of a kernel that does next to nothing; the 1.5 MB of 61 prompts take
+// 5.4.  A few thousand integers come in, 12 bytes go out per row.  Every CTA scans all requests for itself (the sums stay in its shared
 // memory; nothing passes between CTAs) and serves its part of the rows.  One
 // CTA does a step of few rows, in one launch.  Where there are many, the CTAs
 // that read ctx_lens and free_count have no order among themselves, so seq_lens
@@ -178,15 +180,17 @@ static cudaError_t launch_page_plan_t(const PlanParams& p, int ctas, cudaStream_
 }
 
 cudaError_t launch_page_plan(PlanParams& p, cudaStream_t stream) {
-  // One CTA for few rows; a small one starts and synchronises sooner.
-  if (p.max_tokens <= 4096) {
+  // One small CTA for few rows: it starts and synchronises sooner (256 requests of
+  // a token: 3.5 us, and 5.1 with 1024 threads; 1024 requests 6.8 and 6.5).  CTAs of
+  // 1024 rows for more (2048 requests 7.0 us, and 8.4 in one CTA; the 126,000 rows
+  // of 61 prompts 5.4 and 108).
+  if (p.max_tokens <= 1024 && p.B <= 1024) {
     p.totals_later = 0;
-    return p.max_tokens <= 1024 && p.B <= 1024 ? launch_page_plan_t<256>(p, 1, stream)
-                                               : launch_page_plan_t<1024>(p, 1, stream);
+    return launch_page_plan_t<256>(p, 1, stream);
   }
-  p.totals_later = p.seq_lens == p.ctx_lens || p.free_count_out == p.free_count;
   const int ctas = (p.max_tokens + 1023) / 1024;
-  const cudaError_t e = launch_page_plan_t<1024>(p, ctas < 304 ? ctas : 304, stream);
+  p.totals_later = ctas > 1 && (p.seq_lens == p.ctx_lens || p.free_count_out == p.free_count);
+  const cudaError_t e = launch_page_plan_t<1024>(p, ctas < 304 ? (ctas > 0 ? ctas : 1) : 304, stream);
   if (e != cudaSuccess || !p.totals_later) return e;
   fa_page_plan_totals_kernel<<<1, 1024, 0, stream>>>(p);
   return cudaGetLastError();

@@ -11,7 +11,11 @@
 //
 // Bound by HBM: each element of q and k is read and written once.  A thread
 // holds 8 pairs (two 16-byte vectors) of a token, takes their sines once and
-// rotates heads_per_thread heads with them.
+// rotates heads_per_thread heads with them, four at a time: their loads are all
+// asked for before the first is used, which takes 80 registers, three CTAs per SM.
+// Measured: 16384 tokens of 32 + 8 heads of 128 53 us, 6.3 TB/s; the gradient of
+// 12289 tokens of 16 + 16 heads of 64, neighbouring pairs, 19 us, 5.3 TB/s; 64 tokens
+// of 32 + 8 heads 3.0 us, a launch.
 #include "fa_internal.h"
 #include "ptx.cuh"
 
@@ -20,7 +24,8 @@ namespace fa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr long long kRopeFull = 152 * 1024;  // threads that keep the SMs busy
+constexpr long long kRopeFull = 152 * 512;  // threads that keep the SMs busy
+constexpr int kRopeHeads = 8;               // heads of a thread at most
 
 __device__ __forceinline__ float2 bf2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -31,6 +36,15 @@ __device__ __forceinline__ float2 bf2(uint32_t w) {
 template <int D, bool NB, int BATCH>
 __global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int TPT = D / 16;  // threads per token and head: 8 pairs each
+  // Lanes with different pairs would read the plan, where it lies among the
+  // parameters, one after the other (64 tokens of 32 + 8 heads: 3.4 us, and 2.9 from here).
+  __shared__ __align__(16) uint64_t s_turn[D / 2];
+  __shared__ int s_axis[D / 2];
+  if (threadIdx.x < D / 2) {
+    s_turn[threadIdx.x] = p.turn[threadIdx.x];
+    s_axis[threadIdx.x] = p.axis[threadIdx.x];
+  }
+  __syncthreads();
   const long long item = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) / TPT;
   const int j = threadIdx.x % TPT;
   const long long t = item / p.chunks;
@@ -42,8 +56,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const __grid_c
   uint32_t turned = 0;  // bit e: pair 8j + e turns
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int ax = p.axis[8 * j + e];
-    const uint64_t f = p.turn[8 * j + e];
+    const int ax = s_axis[8 * j + e];
+    const uint64_t f = s_turn[8 * j + e];
     co[e] = 1.f;
     si[e] = 0.f;
     if (ax >= 0) {
@@ -121,7 +135,13 @@ static void launch_rope_t(const RopeParams& p, unsigned blocks, cudaStream_t str
 cudaError_t launch_rope(RopeParams& p, int D, bool neighbours, cudaStream_t stream) {
   const int H = p.Hq + p.Hkv, tpt = D / 16;
   const long long one = (long long)p.T * H * tpt;  // threads with a head each
-  p.chunks = one >= 8 * kRopeFull ? (H + 7) / 8 : H;
+  // More heads a thread share its sines, as long as enough threads are left.
+  // Microseconds with 1 / 4 / 8 / 16 heads, 32 + 8 heads of 128: 64 tokens 2.9 /
+  // 3.5 / 4.3 / 5.9, 1024 8.2 / 5.7 / 6.0 / 6.3, 2048 14.0 / 8.4 / 8.1 / 9.3, 16384 99 /
+  // 56 / 53 / 56.
+  const long long heads = (one + kRopeFull - 1) / kRopeFull;
+  p.heads_per_thread = (int)(heads < kRopeHeads ? heads : kRopeHeads);
+  p.chunks = (H + p.heads_per_thread - 1) / p.heads_per_thread;
   p.heads_per_thread = (H + p.chunks - 1) / p.chunks;
   p.chunks = (H + p.heads_per_thread - 1) / p.heads_per_thread;
   const long long blocks = ((long long)p.T * p.chunks * tpt + kRopeThreads - 1) / kRopeThreads;
