@@ -14,7 +14,7 @@
 // One warp takes a run's rows of one K/V head, for K or for V: the largest
 // magnitude first, then the codes.  Bound by HBM for prompts (2 bytes read and
 // 1 written per element), by latency for a step of single tokens.  Measured, 8
-// K/V heads of 128: 9 prompts of 1 to 2047 tokens into pages of 32 25 us, 4.5 TB/s (three
+// K/V heads of 128: 9 prompts of 1 to 2047 tokens into pages of 32 25 us, 4.4 TB/s (three
 // times as many 62 us, 5.5 TB/s); 64 requests of a token 3.3 us, a launch.
 #include "fa_internal.h"
 #include "ptx.cuh"
@@ -92,8 +92,12 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) fa_kv8_appen
   const int sub = lane / LPR, seg = lane % LPR;
 
   // ---- rows of this tile that begin a run
-  int pg = -1, sl = -1;
+  int pg = -1, sl = -1, pg2 = -1, sl2 = -1;  // of row r0 + lane, and of r0 + 32 + lane, where runs may end
   bool lead = false;
+  if (r0 + 32 + lane < p.n) {
+    pg2 = p.page[r0 + 32 + lane];
+    sl2 = p.slot[r0 + 32 + lane];
+  }
   if (lane < rows) {
     const long long i = r0 + lane;
     pg = p.page[i];
@@ -117,9 +121,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) fa_kv8_appen
     if (pass == 1 && src < 0) continue;
     if (pass == 2 && src >= 0) continue;
     // ---- length of the run
-    int len = 1;
     const int most = (int)min((long long)(p.page_size - first), p.n - row);
-    while (len < most) {
+    uint32_t ends = ~__ballot_sync(0xffffffffu, lane < l || (pg == page && sl == first + lane - l));
+    int len = ends != 0 ? __ffs(ends) - 1 - l : 32 - l;
+    bool goes_on = ends == 0;
+    if (goes_on) {
+      ends = ~__ballot_sync(0xffffffffu, pg2 == page && sl2 == first + 32 + lane - l);
+      len += ends != 0 ? __ffs(ends) - 1 : 32;
+      goes_on = ends == 0;
+    }
+    len = min(len, most);
+    while (goes_on && len < most) {
       const int i = len + lane;
       const bool on = i < most && p.page[row + i] == page && p.slot[row + i] == first + i;
       const uint32_t m = __ballot_sync(0xffffffffu, on);

@@ -10,15 +10,17 @@
 //     token c_b + i of request b: row cu_b + i, block (c_b + i) / P, whose page
 //     is the table's for a block held before, else
 //     free[count - 1 - (base_b + block - ceil(c_b / P))].
-// The step is bound by latency, a launch, two barriers and three reads one after
-// the other (lengths, free page, its entry): 3.4 us for 256 requests of a token,
-// against 2.8 of a kernel that does next to nothing; the 1.5 MB of 61 prompts take
-// 5.4.  A few thousand integers come in, 12 bytes go out per row.  Every CTA scans all requests for itself (the sums stay in its shared
-// memory; nothing passes between CTAs) and serves its part of the rows.  One
-// CTA does a step of few rows, in one launch.  Where there are many, the CTAs
-// that read ctx_lens and free_count have no order among themselves, so seq_lens
-// and free_count_out, which may be the same arrays, are then written by a
-// second launch of one CTA, from cu_new and what the first has left of the count.
+// A few thousand integers come in, 12 bytes go out per row; the step is bound by
+// latency: a launch, two barriers and three reads one after the other (lengths,
+// free page, its entry).  256 requests of a token take 3.4 us, where a kernel that
+// does next to nothing takes 2.8; the 1.5 MB of 61 prompts take 5.4.
+//
+// Every CTA scans all requests for itself (the sums stay in its shared memory;
+// nothing passes between CTAs) and serves its part of the rows.  One CTA does a
+// step of few rows.  Where there are many, the CTAs that read ctx_lens and
+// free_count have no order among themselves, so seq_lens and free_count_out,
+// where they are the same arrays, are then written by a second launch of one
+// CTA, from cu_new and the old count.
 #include "fa_internal.h"
 #include "ptx.cuh"
 
