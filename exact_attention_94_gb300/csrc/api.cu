@@ -872,13 +872,14 @@ static int kv8_span(int Nq, int max_seq_len, int window_left) {
 }
 
 size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_shares) {
-  if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || d < 1 || num_shares < 1) return 0;
+  if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || d < 1 || num_shares < 1 || num_shares > 65535) return 0;
+  if ((long long)Nq * Hq > 65535) return 0;
   const size_t rows = 2 * (size_t)num_shares * kv8_row_tile(Nq * (Hq / Hkv));
   return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float));
 }
 
 int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left) {
-  if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || max_seq_len < 1) return 1;
+  if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || max_seq_len < 1 || (long long)Nq * Hq > 65535) return 1;
   return kv8_auto_shares(B, Nq, Hkv, Hq / Hkv, kv8_span(Nq, max_seq_len, window_left));
 }
 
@@ -938,7 +939,8 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
   if (!make_tmap_codes(&tk, k_codes, d, page_size, (long long)num_pages * Hkv, p.box_rows) ||
       !make_tmap_codes(&tv, v_codes, d, page_size, (long long)num_pages * Hkv, p.box_rows))
     return FA_ERR_INVALID_ARG;
-  return launch_decode_kv8(tk, tv, p, d, num_shares, kv8_span(Nq, max_seq_len, window_left), (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  const int span = kv8_span(Nq, max_seq_len, window_left);
+  return launch_decode_kv8(tk, tv, p, d, num_shares, span, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

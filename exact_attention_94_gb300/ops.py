@@ -677,6 +677,14 @@ def _check_dims(name, t, dtype, dev, dims, what):
     return t.shape
 
 
+def _check_int(name, n):
+    """A size as the C interface takes it (which would drop higher bits)."""
+    n = int(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} does not fit 32 bits")
+    return n
+
+
 def _check_rows(name, t, dev, shape=None):
     """A bf16 [..., H, d] tensor whose heads lie side by side and whose rows lie
     one stride apart (a slice of a fused projection, say).  Returns that stride."""
@@ -724,7 +732,7 @@ def page_plan(ctx_lens, new_lens, free_pages, free_count, block_table, page_size
     _check("ctx_lens", ctx_lens, i32, dev, (B,))
     _check("new_lens", new_lens, i32, dev, (B,))
     _check("free_count", free_count, i32, dev, (1,))
-    n = int(max_tokens)
+    n = _check_int("max_tokens", max_tokens)
     if n < 0:
         raise ValueError("max_tokens must not be negative")
     if out is None:  # one buffer, cut up
@@ -735,7 +743,7 @@ def page_plan(ctx_lens, new_lens, free_pages, free_count, block_table, page_size
         for name, t, size in zip(PagePlan._fields, out, (B, B + 1, n, n, n, 1)):
             _check(f"out.{name}", t, i32, dev, (size,))
     st = lib().fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
-                            block_table.data_ptr(), *[t.data_ptr() for t in out], B, n, int(page_size), num_pages,
+                            block_table.data_ptr(), *[t.data_ptr() for t in out], B, n, _check_int("page_size", page_size), num_pages,
                             max_blocks, raw)
     if st:
         _lib.check(st, "fa_page_plan")
@@ -860,6 +868,8 @@ def kv8_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, page, slot, cop
 @functools.lru_cache(maxsize=1024)
 def _kv8_shares(dev, B, Nq, Hq, Hkv, d, L, window_left, shares):
     """(shares, workspace bytes) of a call: they depend on its sizes and the device alone."""
+    for name, n in (("max_seq_len", L), ("window_left", window_left), ("num_shares", shares)):
+        _check_int(name, n)
     if shares == 0:
         shares = lib().fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, L, window_left)
     return shares, max(16, lib().fa_decode_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, max(shares, 1)))

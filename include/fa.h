@@ -562,7 +562,9 @@ fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, voi
  *                  16-byte aligned, contents on entry do not matter; calls
  *                  whose work overlaps on the GPU need one each
  * What a page holds behind a request's last key is never used, whatever it
- * is.  Table entries outside the pool and lengths outside [0, max_seq_len] are
+ * is.  A NaN among the cached values reaches the queries that see its key, and
+ * no others; where the drafts of a tile of rows do not all see the key, in all
+ * d elements of their O, not in its own alone.  Table entries outside the pool and lengths outside [0, max_seq_len] are
  * handled and reported as in fa_decode_paged.  page_size a multiple of 16, d = 64
  * or 128, 1 <= B <= 16384, Nq >= 1, Nq * Hq <= 65535.
  */
@@ -573,6 +575,7 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
 
 /* Shares fa_decode_kv8 uses when it is given num_shares = 0 (window_left as there). */
 int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left);
+/* 0 for arguments that the call refuses. */
 size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_shares);
 
 /*

@@ -89,6 +89,23 @@ def test_workspace_and_shares(lib):
         assert 1 <= lib.fa_decode_kv8_num_shares(*a) <= 65535
 
 
+def test_sizes_that_a_call_refuses_have_no_workspace(lib):
+    big = 2 ** 31 - 1
+    for a in ((1, big, big, 1, 128, 5), (1, 70000, 1, 1, 128, 5), (1, 1, 70000, 1, 128, 5), (1, 1, 8, 8, 128, big)):
+        assert lib.fa_decode_kv8_workspace_bytes(*a) == 0
+    assert lib.fa_decode_kv8_num_shares(1, big, big, 1, 777, -1) == 1
+
+
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1])
+def test_numbers_beyond_32_bits(n):
+    """ctypes would pass their lower bits on."""
+    for args in ((n, -1, 0), (777, n, 0), (777, -1, n)):
+        with pytest.raises(ValueError):
+            ops._kv8_shares(0, 1, 1, 8, 8, 128, *args)
+    with pytest.raises(ValueError):
+        ops._check_int("max_tokens", n)
+
+
 def test_python_side():
     with pytest.raises(ValueError):
         ops.RopePlan(64, [0] * 31, [1.0] * 31)
