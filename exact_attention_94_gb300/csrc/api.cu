@@ -2,8 +2,7 @@
 // workspace sizing and kernel launches.  See include/fa.h for the contract of
 // every entry point.
 #include "../../include/fa.h"
-#include "fa_internal.h"
-#include "ptx.cuh"
+#include "serving.cuh"
 
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -58,8 +58,7 @@
 // group of warps and a byte store per code, by two groups (72), P by key and
 // its split in half precision (66), all scores read at once (62.5) and packed
 // fp32 arithmetic (61).
-#include "fa_internal.h"
-#include "ptx.cuh"
+#include "serving.cuh"
 
 #include <cmath>
 

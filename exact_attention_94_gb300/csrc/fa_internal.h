@@ -157,95 +157,6 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, void* k_pa
                                 const int* slot, const int* copy_src, int n, int Hkv, int d, int page_size,
                                 int num_pages, unsigned* err, cudaStream_t stream);
 
-// Planning a step (see fa_page_plan in fa.h).
-struct PlanParams {
-  const int* ctx_lens;       // [B]
-  const int* new_lens;       // [B]
-  const int* free_pages;     // [num_pages]
-  const int* free_count;     // [1]
-  int* block_table;          // [B, max_blocks]
-  int* seq_lens;             // [B], may be ctx_lens
-  int* cu_new;               // [B + 1]
-  int* page;                 // [max_tokens] x 3
-  int* slot;
-  int* position;
-  int* free_count_out;       // [1], may be free_count
-  int B;
-  int max_tokens;
-  int page_size;
-  int num_pages;
-  int max_blocks;
-  int totals_later;          // set by the launch: seq_lens and free_count_out come from a second kernel
-  unsigned* err;
-};
-cudaError_t launch_page_plan(PlanParams& p, cudaStream_t stream);
-
-// Rotary positions (see fa_rope_axes in fa.h).
-struct RopeParams {
-  const void* q;
-  const void* k;
-  void* q_out;
-  void* k_out;
-  const int* positions;      // [n_axes, T]
-  long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements between rows
-  int T, Hq, Hkv;
-  int inverse;
-  int heads_per_thread;      // set by the launch
-  int chunks;                //   thread chunks of a token's Hq + Hkv heads
-  signed char axis[64];      // axis of pair p, -1: not rotated
-  uint64_t turn[64];         // its frequency: fraction of a turn per position, in 2^-64
-};
-cudaError_t launch_rope(RopeParams& p, int D, bool neighbours, cudaStream_t stream);
-
-// 8-bit paged cache, write side (see fa_kv8_append in fa.h).
-struct Kv8AppendParams {
-  const void* k_new;
-  const void* v_new;
-  void* k_codes;
-  void* v_codes;
-  float* k_scale;
-  float* v_scale;
-  const int* page;           // [n]
-  const int* slot;           // [n]
-  const int* copy_src;       // [n] or nullptr
-  long long k_stride, v_stride;
-  int n, Hkv, page_size, num_pages;
-  int split;                 // warps that share 32 rows' runs, set by the launch
-  unsigned* err;
-};
-cudaError_t launch_kv8_append(Kv8AppendParams& p, int D, cudaStream_t stream);
-
-// Attention over the 8-bit paged cache (see fa_decode_kv8 in fa.h).
-constexpr int kKv8Tile = 128;  // keys per tile
-struct Kv8DecodeParams {
-  const void* q;             // [B, Nq, Hq, d] bf16
-  const uint8_t* k_codes;    // [num_pages, Hkv, page_size, d]
-  const uint8_t* v_codes;
-  const float* k_scale;      // [num_pages, Hkv]
-  const float* v_scale;
-  const int* block_table;    // [B, max_blocks]
-  const int* seq_lens;       // [B]
-  void* o;
-  float* lse;
-  float* part_o;             // [2 * shares, RT, d] fp32: the pieces a share's borders cut, each normalised
-  float* part_lse;           // [2 * shares, RT] log2 of each piece's softmax mass
-  int B, Nq, Hq, Hkv, group;
-  int page_size, num_pages, max_blocks, max_len;
-  int win_left;              // -1: no window
-  int box_rows;              // keys per TMA box: 16 .. 128, divides the page and the tile
-  int lead;                  // tiles that a unit counts for its start and end, set by the launch
-  int row_tiles;             // tiles of query rows per K/V head, set by the launch
-  float scale_log2;
-  unsigned* err;
-  unsigned long long timeout_ns;
-};
-int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span);
-int kv8_row_tile(int rows);  // query rows of a CTA for `rows` rows per K/V head
-// 3-D uint8 tensor map of the codes, [heads of pages][page_size][D], swizzled at the row's length.
-bool make_tmap_codes(CUtensorMap* m, const void* ptr, int D, int page_size, long long page_heads, int box_rows);
-cudaError_t launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, Kv8DecodeParams& p, int D, int shares, int span,
-                              cudaStream_t stream);
-
 int decode_stages(int G, int D);
 size_t decode_smem_bytes(int G, int D);
 cudaError_t launch_decode(const DecodeParams& p, int D, void* o, float* lse, cudaStream_t stream);

@@ -16,8 +16,7 @@
 // 1 written per element), by latency for a step of single tokens.  Measured, 8
 // K/V heads of 128: 9 prompts of 1 to 2047 tokens into pages of 32 25 us, 4.4 TB/s (three
 // times as many 62 us, 5.5 TB/s); 64 requests of a token 3.3 us, a launch.
-#include "fa_internal.h"
-#include "ptx.cuh"
+#include "serving.cuh"
 
 namespace fa {
 

@@ -21,8 +21,7 @@
 // free_count have no order among themselves, so seq_lens and free_count_out,
 // where they are the same arrays, are then written by a second launch of one
 // CTA, from cu_new and the old count.
-#include "fa_internal.h"
-#include "ptx.cuh"
+#include "serving.cuh"
 
 namespace fa {
 

@@ -16,8 +16,7 @@
 // Measured: 16384 tokens of 32 + 8 heads of 128 53 us, 6.3 TB/s; the gradient of
 // 12289 tokens of 16 + 16 heads of 64, neighbouring pairs, 19 us, 5.3 TB/s; 64 tokens
 // of 32 + 8 heads 3.0 us, a launch.
-#include "fa_internal.h"
-#include "ptx.cuh"
+#include "serving.cuh"
 
 namespace fa {
 

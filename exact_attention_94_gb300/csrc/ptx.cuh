@@ -8,7 +8,6 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 namespace fa {
 
@@ -16,7 +15,6 @@ enum : unsigned {
   FA_DEVERR_TIMEOUT_BASE = 0x1000u,  // + site id
   FA_DEVERR_BAD_PAGE = 0x2000u,      // a block-table entry outside the page pool
   FA_DEVERR_BAD_SEQLEN = 0x2001u,    // a sequence length outside [0, max_seq_len]
-  FA_DEVERR_OUT_OF_PAGES = 0x2002u,  // a plan needs more pages than the free stack has
   FA_DEVERR_BOUNDS_BASE = 0x3000u,   // + site id: an index outside its buffer (bounds-checked builds only)
 };
 
@@ -122,28 +120,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-      "[%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
 // Plain (untiled) bulk copy global -> shared; addresses and size multiples of 16.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
-}
-
-// Four bytes global -> shared without a register; cp_async_arrive has the
-// thread's earlier ones, when they are there, arrive once on an mbarrier.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -255,28 +236,6 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return d;
 }
 
-// The same for rows of 64 bytes and the 64-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1u << 46;  // descriptor version for tcgen05
-  d |= (uint64_t)4u << 61;  // swizzle mode: 64-byte
-  return d;
-}
-
-// The same for rows of 32 bytes and the 32-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1u << 46;  // descriptor version for tcgen05
-  d |= (uint64_t)6u << 61;  // swizzle mode: 32-byte
-  return d;
-}
-
 // Advances a descriptor's start address by a byte offset (a multiple of 16).
 // Shared-memory addresses stay below 2^18 bytes, so the 14-bit address field
 // never carries into the neighbouring fields.
@@ -296,13 +255,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
          | ((uint32_t)(M >> 4) << 24);      // M / 16
 }
 
-// Instruction descriptor for kind::f8f6f4 with e4m3 A and B (format code 0) and f32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn = false, bool b_mn = false) {
+// Instruction descriptor for kind::f8f6f4 with e4m3 A and B (format code 0), f32 D, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4)                          // D format: f32
          | (0u << 7)                        // A format: e4m3
          | (0u << 10)                       // B format: e4m3
-         | ((a_mn ? 1u : 0u) << 15)         // A major-ness
-         | ((b_mn ? 1u : 0u) << 16)         // B major-ness
          | ((uint32_t)(N >> 3) << 17)       // N / 8
          | ((uint32_t)(M >> 4) << 24);      // M / 16
 }
@@ -326,16 +283,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
 }
 // As tmem_ld32, and m receives the largest of the thread's 32 values: the
 // reducing form of the TMEM load (.red .max), which sm_103a adds.  Values are
@@ -364,11 +311,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
-}
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3])
-               : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -424,46 +366,6 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float e0, float e1, float e2, fl
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(lo) : "f"(e0), "f"(e1));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(hi) : "f"(e2), "f"(e3));
   return (uint32_t)lo | ((uint32_t)hi << 16);
-}
-
-// Two floats -> two e4m3 codes, e0 in the low byte; two codes -> their values, exact.
-__device__ __forceinline__ uint32_t pack_e4m3x2(float e0, float e1) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(e0), "f"(e1));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_e4m3x2(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-  float2 f;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-      : "=f"(f.x), "=f"(f.y)
-      : "r"(h));
-  return f;
-}
-
-// Two floats -> f16x2, e0 in the low half; f16x2 -> two e4m3 codes and back (exact).
-__device__ __forceinline__ __half2 pack_f16x2(float e0, float e1) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(e0), "f"(e1));
-  return *reinterpret_cast<__half2*>(&h);
-}
-__device__ __forceinline__ uint32_t pack_e4m3x2(__half2 h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t*>(&h)));
-  return r;
-}
-__device__ __forceinline__ __half2 unpack_e4m3x2_f16(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-  return *reinterpret_cast<__half2*>(&h);
-}
-
-// The largest of a warp's 32 values, in every lane.
-__device__ __forceinline__ float warp_max(float v) {
-  float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
 }
 
 // Cubic for 2^f on [0, 1) with c0 = 1 (minimax relative error 8.6e-5),
