@@ -12,17 +12,17 @@
 // Bound by HBM: each element of q and k is read and written once.  A thread
 // holds 8 pairs (two 16-byte vectors) of a token, takes their sines once and
 // rotates heads_per_thread heads with them, four at a time: their loads are all
-// asked for before the first is used, which takes 80 registers, three CTAs per SM.
+// asked for before the first is used, which takes 80 registers, 24 warps per SM.
 // Measured: 16384 tokens of 32 + 8 heads of 128 53 us, 6.3 TB/s; the gradient of
-// 12289 tokens of 16 + 16 heads of 64, neighbouring pairs, 19 us, 5.3 TB/s; 64 tokens
-// of 32 + 8 heads 3.0 us, a launch.
+// 12289 tokens of 16 + 16 heads of 64, neighbouring pairs, 18 us, 5.5 TB/s; 64 tokens
+// of 32 + 8 heads 2.9 us, a launch.
 #include "serving.cuh"
 
 namespace fa {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;  // (256: 12289 tokens of 16 + 16 heads of 64 19.0 us for 18.3, a longer last wave)
 constexpr long long kRopeFull = 152 * 512;  // threads that keep the SMs busy
 constexpr int kRopeHeads = 8;               // heads of a thread at most
 
@@ -33,15 +33,15 @@ __device__ __forceinline__ float2 bf2(uint32_t w) {
 }  // namespace
 
 template <int D, bool NB, int BATCH>
-__global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 6) fa_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int TPT = D / 16;  // threads per token and head: 8 pairs each
   // Lanes with different pairs would read the plan, where it lies among the
   // parameters, one after the other (64 tokens of 32 + 8 heads: 3.4 us, and 2.9 from here).
-  __shared__ __align__(16) uint64_t s_turn[D / 2];
-  __shared__ int s_axis[D / 2];
+  __shared__ uint64_t s_turn[8][TPT];  // pair 8j + e at [e][j]
+  __shared__ int s_axis[8][TPT];
   if (threadIdx.x < D / 2) {
-    s_turn[threadIdx.x] = p.turn[threadIdx.x];
-    s_axis[threadIdx.x] = p.axis[threadIdx.x];
+    s_turn[threadIdx.x % 8][threadIdx.x / 8] = p.turn[threadIdx.x];
+    s_axis[threadIdx.x % 8][threadIdx.x / 8] = p.axis[threadIdx.x];
   }
   __syncthreads();
   const long long item = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) / TPT;
@@ -55,8 +55,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const __grid_c
   uint32_t turned = 0;  // bit e: pair 8j + e turns
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int ax = s_axis[8 * j + e];
-    const uint64_t f = s_turn[8 * j + e];
+    const int ax = s_axis[e][j];
+    const uint64_t f = s_turn[e][j];
     co[e] = 1.f;
     si[e] = 0.f;
     if (ax >= 0) {
