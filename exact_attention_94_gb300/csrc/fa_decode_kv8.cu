@@ -399,7 +399,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       }
       q.n = min(4, pc.t1 - t_next);
       const int g = (pc.beg + t_next * kKv8Tile) / 16 + lane;
-      q.on = lane < 8 * q.n && g < (pc.len + 15) / 16;
+      // (pages that no query's window reaches may be gone; a box that it reaches lies in one that is not)
+      const int lo = p.win_left < 0 ? 0 : max(0, pc.len - p.Nq - p.win_left) / 16 / bpb * bpb;
+      q.on = lane < 8 * q.n && g < (pc.len + 15) / 16 && g >= lo;
       q.hk = (int)((unsigned)pc.u / (unsigned)p.row_tiles);
       t_next += q.n;
       if (q.on) {
@@ -638,7 +640,8 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         const bool partial = j0 + kKv8Tile > pc.len - p.Nq + 1 || (p.win_left >= 0 && j0 < pc.len - 1 - p.win_left);
         auto sees = [&](int r) { return j <= s_pos[r] && (p.win_left < 0 || j >= s_pos[r] - p.win_left); };
         // A key's value row may hold NaN, and 0 * NaN is not 0.  Where no row sees
-        // the key (it may be anything behind the last), its values count as zero.
+        // the key (it may be anything behind the last or before the window), its
+        // values count as zero.
         // Where some rows do and some don't (drafts), a row with a NaN counts as
         // zero too, and as NaN to the rows that see it: in all their elements.
         bool poison = false;

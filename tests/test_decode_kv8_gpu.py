@@ -314,6 +314,25 @@ def test_pages_beyond_4_gib():
     assert int((kc[4:-2] != 0).sum()) == 0 and int((vc[:3] != 0).sum()) == 0
 
 
+@pytest.mark.parametrize("P,d", [(16, 64), (16, 128), (32, 128), (64, 64), (128, 128), (256, 64), (48, 128)])
+@pytest.mark.parametrize("window,Nq", [(0, 1), (60, 1), (127, 3), (200, 4)])
+def test_pages_before_the_window_may_be_gone(P, d, window, Nq):
+    """A server frees them: their entries are nonsense, and the pages, if they still
+    are any, hold NaN codes and NaN scales."""
+    lens = [700, 333, 1, 129 + Nq, 512]
+    q, (kc, ks), (vc, vs), table, lens = make(lens, Nq, 4, 2, d, P, seed=P + window)
+    ref = serving.decode_kv8(synth.to_f64(q), kc, vc, ks, vs, table, lens, window, d ** -0.5)
+    for b, n in enumerate(lens):
+        for blk in range(max(0, n - Nq - window) // P):
+            for codes, scales in ((kc, ks), (vc, vs)):
+                codes[table[b, blk]], scales[table[b, blk]] = 0x7F, np.nan
+            table[b, blk] = (-1, 10 ** 6, table[b, blk])[blk % 3]
+    for shares in (0, 1, 7):
+        o, lse = ops.decode_kv8(*dev((q, (kc, ks), (vc, vs), table, lens)), 700, window_left=window, num_shares=shares)
+        assert ops.device_error() == 0
+        assert_close(o, lse, ref)
+
+
 def test_what_the_workspace_held_does_not_matter():
     """A captured call replayed over a workspace of every sort of content, and with many pieces a unit."""
     a = dev(make([3000, 17], 1, 4, 2, 64, 16, seed=13))
