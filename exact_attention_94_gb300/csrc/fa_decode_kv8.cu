@@ -164,6 +164,14 @@ struct Piece {
   int b, u, t0, t1, tiles, len, beg, pad;
 };
 
+// Row tile and K/V head of a unit.
+__device__ __forceinline__ int row_tile(const Kv8DecodeParams& p, int u) {
+  return p.row_tiles == 1 ? 0 : (int)((unsigned)u % (unsigned)p.row_tiles);
+}
+__device__ __forceinline__ int kv_head(const Kv8DecodeParams& p, int u) {
+  return p.row_tiles == 1 ? u : (int)((unsigned)u / (unsigned)p.row_tiles);
+}
+
 // The producer's walk over the share, piece by piece.
 struct Walk {
   long long left;  // weight of the share still to come
@@ -344,10 +352,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     // batches of four of a piece, lane i owning 16 keys.  Page numbers are read
     // two batches ahead (and moved to their place one later, when they have
     // come); scales are copied asynchronously to the tile's place, and arrive on
-    // its barrier.  A piece is announced when its first batch's pages are read,
-    // with its rows of Q.  (That waits until the piece kPieces before has been
-    // taken, that is until the one before that is done; its tiles have all been
-    // asked for by then.)
+    // its barrier.  A piece is announced, with its rows of Q, before its first
+    // tile is asked for.  (That waits until the piece kPieces before has been
+    // taken, for which it takes no tile that has not been asked for.)
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -358,6 +365,8 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       int off;
       bool on;
       int hk;
+      bool first;  // the piece's first batch
+      Piece pc;
     };
     Walk walk{to - from, 0, 0, 0, 0, 0};
     if (to > from) {
@@ -369,11 +378,11 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     Piece pc{};
     int t_next = 0, pieces = 0;  // next tile of pc to fetch; pieces fetched
     bool more = true;
-    auto announce = [&]() {
+    auto announce = [&](const Piece& pc) {
       const int st = pieces % L::kPieces;
       if (pieces >= L::kPieces) ok = __all_sync(0xffffffffu, mbar_wait(TAKEN(st), (pieces / L::kPieces - 1) & 1, w, 50));
       if (!ok) return;
-      const int x0 = pc.u % p.row_tiles * RT, rows = more ? min(RT, p.Nq * p.group - x0) : 0;
+      const int x0 = row_tile(p, pc.u) * RT, rows = pc.t0 < pc.t1 ? min(RT, p.Nq * p.group - x0) : 0;
       if (lane == 0) {
         s_piece[st] = pc;
         mbar_arrive_expect_tx(HERE(st), (uint32_t)(rows * D * 2));
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       __syncwarp();
       if (lane < rows) {
         const int x = x0 + lane, i = p.Nq == 1 ? 0 : (int)((unsigned)x / (unsigned)p.group);
-        const int h = (int)((unsigned)pc.u / (unsigned)p.row_tiles) * p.group + x - i * p.group;
+        const int h = kv_head(p, pc.u) * p.group + x - i * p.group;
         bulk_load(base + L::kStageOff + st * L::kStage + lane * D * 2,
                   static_cast<const __nv_bfloat16*>(p.q) + (((size_t)pc.b * p.Nq + i) * p.Hq + h) * D, D * 2, HERE(st));
       }
@@ -389,20 +398,21 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     };
     auto fetch = [&](Batch& q) {
       q = {};
-      if (!more || !ok) return;
+      if (!more) return;
       if (t_next == pc.t1) {
         pc = walk.next(p, units);
         t_next = pc.t0;
         more = pc.t0 < pc.t1;
-        announce();
-        if (!more || !ok) return;
+        if (!more) return;
+        q.first = true;
+        q.pc = pc;
       }
       q.n = min(4, pc.t1 - t_next);
       const int g = (pc.beg + t_next * kKv8Tile) / 16 + lane;
       // (pages that no query's window reaches may be gone; a box that it reaches lies in one that is not)
       const int lo = p.win_left < 0 ? 0 : max(0, pc.len - p.Nq - p.win_left) / 16 / bpb * bpb;
       q.on = lane < 8 * q.n && g < (pc.len + 15) / 16 && g >= lo;
-      q.hk = (int)((unsigned)pc.u / (unsigned)p.row_tiles);
+      q.hk = kv_head(p, pc.u);
       t_next += q.n;
       if (q.on) {
         const int blk = (int)((unsigned)(g * 16) / (unsigned)p.page_size);
@@ -419,6 +429,8 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
         now.page = 0;
       }
+      if (now.first) announce(now.pc);
+      if (!ok) break;
       const int ph = now.page * p.Hkv + now.hk;
       const uint32_t on = __ballot_sync(0xffffffffu, now.on);
       for (int i = 0; i < now.n; ++i, ++it) {
@@ -453,6 +465,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       now = next;
       fetch(next);
     }
+    if (ok) announce(pc);  // the end
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == SOFT + 1) {
     // ============================================================ products
@@ -518,12 +531,12 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     const int p_flip = key << 2 & 16;
     auto p_at = [&](int c) { return p_row + (c >> 5) * L::kStrip + ((c & 31) ^ p_flip); };
     const int group16 = key >> 4;                    // of the tile's keys: where its scales are
-    auto rows_of = [&](const Piece& s) { return min(RT, p.Nq * p.group - s.u % p.row_tiles * RT); };
+    auto rows_of = [&](const Piece& s) { return min(RT, p.Nq * p.group - row_tile(p, s.u) * RT); };
     // row r of a piece: its row of q and o, its query token
     auto q_row = [&](const Piece& s, int r, int& i, int& h) {
-      const int x = s.u % p.row_tiles * RT + r;
+      const int x = row_tile(p, s.u) * RT + r;
       i = p.Nq == 1 ? 0 : (int)((unsigned)x / (unsigned)p.group);
-      h = (int)((unsigned)s.u / (unsigned)p.row_tiles) * p.group + x - i * p.group;
+      h = kv_head(p, s.u) * p.group + x - i * p.group;
       return ((size_t)s.b * p.Nq + i) * p.Hq + h;
     };
     // ---- the next piece, and its Q: rows in turn for the warps, split into two
@@ -587,7 +600,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
             *reinterpret_cast<uint2*>(sb + L::kQOff + at + (seg & 1) * 8) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
           }
           if (seg == 0) {
-            const int y = s.u % p.row_tiles * RT + r;
+            const int y = row_tile(p, s.u) * RT + r;
             s_qsc[r] = sc * p.scale_log2;
             s_pos[r] = s.len - p.Nq + (p.Nq == 1 || r >= rows ? 0 : (int)((unsigned)y / (unsigned)p.group));
           }
@@ -618,6 +631,10 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       const float* s_qsc = reinterpret_cast<const float*>(sb + L::kRowOff + (piece & 1) * 2 * RT * 4) + g0;
       const int* s_pos = reinterpret_cast<const int*>(s_qsc + RT);  // (both from the group's first row)
       const int rows = rows_of(pc);
+      // positions of the tile's first and last row; between them they rise by one or not at all
+      const int x0 = row_tile(p, pc.u) * RT, at0 = pc.len - p.Nq;
+      const int pos_first = p.Nq == 1 ? at0 : at0 + (int)((unsigned)x0 / (unsigned)p.group);
+      const int pos_last = p.Nq == 1 ? at0 : at0 + (int)((unsigned)(x0 + rows - 1) / (unsigned)p.group);
       ok = __all_sync(0xffffffffu, mbar_wait(QB, piece & 1, w, 56));
       uint64_t l2[RG / 2];  // rows' sums of this key lane, in twos
 #pragma unroll
@@ -644,22 +661,17 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         // values count as zero.
         // Where some rows do and some don't (drafts), a row with a NaN counts as
         // zero too, and as NaN to the rows that see it: in all their elements.
-        bool poison = false;
+        bool poison = false, any = true, all = true;
         if (partial) {
-          bool any = false, all = true;
-#pragma unroll 4
-          for (int r = -g0; r < RT - g0; ++r) {  // (all groups' rows)
-            if (g0 + r < rows) {
-              any |= sees(r);
-              all &= sees(r);
-            }
-          }
+          any = j <= pos_last && (p.win_left < 0 || j >= pos_first - p.win_left);
+          all = j <= pos_first && (p.win_left < 0 || j >= pos_last - p.win_left);
           uint4* row = reinterpret_cast<uint4*>(sb + vslot * L::kSlot + key * D);
+          auto turn = [&](int e) { return (e + (D == 128 ? lane : lane >> 1)) & (D / 16 - 1); };  // (other banks for each lane)
           if (any && !all) {
             uint32_t nan = 0;
 #pragma unroll 1
             for (int e = 0; e < D / 16; ++e) {
-              const uint4 v = row[e];
+              const uint4 v = row[turn(e)];
               nan |= __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
                      __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
             }
@@ -672,13 +684,14 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           }
           if (!any || poison) {
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) row[e] = make_uint4(0u, 0u, 0u, 0u);
+            for (int e = 0; e < D / 16; ++e) row[turn(e)] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         float s[RG];
+        // The references: a piece's first tile makes them, another moves them if one of its p passes what e4m3 holds.
         for (bool settled = false;;) {
-          // ---- scores less the references, in log2 units
-          {
+          if (settled || t > pc.t0) {
+            // ---- scores less the references, in log2 units
             uint32_t s1[RG], s2[RG];
             tmem_load<RG>(tS + (it & 1) * L::kNS + lane_sel + g0, s1);
             tmem_load<RG>(tS + (it & 1) * L::kNS + lane_sel + RT + g0, s2);
@@ -694,22 +707,22 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
                 f2_unpack(f2_fma(x, f2_mul(e ? qsc.y : qsc.x, f2_pack(ks, ks)), e ? neg.y : neg.x), s[r + e], s[r + e + 1]);
               }
             }
-          }
-          if (partial) {
+            if (!all) {
 #pragma unroll
-            for (int r = 0; r < RG; ++r) s[r] = sees(r) ? s[r] : -INFINITY;
-          }
-          if (settled) break;
-          // ---- does any p pass what e4m3 holds?
-          float top = fmaxf(s[0], s[1]);
+              for (int r = 0; r < RG; ++r) s[r] = any && sees(r) ? s[r] : -INFINITY;
+            }
+            if (settled) break;
+            // ---- does any p pass that?
+            float top = fmaxf(s[0], s[1]);
 #pragma unroll
-          for (int r = 2; r < RG; r += 2) top = max3f(top, s[r], s[r + 1]);
-          const bool move = __any_sync(0xffffffffu, top > kHeadroom - lvs);
-          if (lane == 0) s_vote[(it & 1) * SOFT + warp] = move;
-          ok = exchange();
-          if (!ok) break;
-          const int4 votes = *reinterpret_cast<const int4*>(s_vote + (it & 1) * SOFT + group * 4);
-          if ((votes.x | votes.y | votes.z | votes.w) == 0) break;
+            for (int r = 2; r < RG; r += 2) top = max3f(top, s[r], s[r + 1]);
+            const bool move = __any_sync(0xffffffffu, top > kHeadroom - lvs);
+            if (lane == 0) s_vote[(it & 1) * SOFT + warp] = move;
+            ok = exchange();
+            if (!ok) break;
+            const int4 votes = *reinterpret_cast<const int4*>(s_vote + (it & 1) * SOFT + group * 4);
+            if ((votes.x | votes.y | votes.z | votes.w) == 0) break;
+          }
           // ---- new references: the largest up to here (rolled loops: rare, and the code is long already)
           constexpr int G = RG > 8 ? 8 : RG;  // rows at a time
 #pragma unroll 1
@@ -722,7 +735,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
 #pragma unroll
             for (int e = 0; e < G; ++e) {
               x[e] = fmaf(__uint_as_float(s2[e]), 0.0625f, __uint_as_float(s1[e])) * (ks * s_qsc[r + e]) + lvs;
-              if (partial && !sees(r + e)) x[e] = -INFINITY;
+              if (!all && !(any && sees(r + e))) x[e] = -INFINITY;
               x[e] = warp_max(x[e]);
             }
             if (lane == 0) {
@@ -841,23 +854,24 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         }
       }
       __syncwarp();
+      constexpr int OB = RG > 8 ? 8 : RG;  // rows at a time
 #pragma unroll 1
-      for (int r4 = 0; r4 < mine; r4 += 4) {
-        uint32_t o1[4], o2[4], o3[4];
-        tmem_ld4(tO + lane_sel + g0 + r4, o1);
-        tmem_ld4(tO + lane_sel + RT + g0 + r4, o2);
-        tmem_ld4(tO + lane_sel + 2 * RT + g0 + r4, o3);
+      for (int r0 = 0; r0 < mine; r0 += OB) {
+        uint32_t o1[OB], o2[OB], o3[OB];
+        tmem_load<OB>(tO + lane_sel + g0 + r0, o1);
+        tmem_load<OB>(tO + lane_sel + RT + g0 + r0, o2);
+        tmem_load<OB>(tO + lane_sel + 2 * RT + g0 + r0, o3);
         tmem_ld_wait();
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (r4 + x < mine && has) {
+        for (int x = 0; x < OB; ++x) {
+          if (r0 + x < mine && has) {
             const float y = fmaf(fmaf(__uint_as_float(o3[x]), 0.0625f, __uint_as_float(o2[x])), 0.0625f, __uint_as_float(o1[x]));
-            const float f = my_al[r4 + x];
+            const float f = my_al[r0 + x];
             const float val = f == 0.f ? 0.f : y * f;  // (0 * NaN would not be 0)
             if (whole)
-              static_cast<__nv_bfloat16*>(p.o)[(size_t)my_at[r4 + x] * D + e] = __float2bfloat16_rn(val);
+              static_cast<__nv_bfloat16*>(p.o)[(size_t)my_at[r0 + x] * D + e] = __float2bfloat16_rn(val);
             else
-              p.part_o[(size_t)my_at[r4 + x] * D + e] = val;
+              p.part_o[(size_t)my_at[r0 + x] * D + e] = val;
           }
         }
       }
