@@ -164,6 +164,50 @@ struct Piece {
   int b, u, t0, t1, tiles, len, beg, pad;
 };
 
+// Where the requests' weights begin: thread t of the block adds up requests b0 .. b1 - 1.
+struct Scan {
+  long long before, mine, total;  // weight before the thread's requests, of them, of all
+  int b0, b1;
+};
+template <int WARPS>
+__device__ __forceinline__ Scan kv8_scan(const Kv8DecodeParams& p, int units, long long* s_scan) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = (p.B + 32 * WARPS - 1) / (32 * WARPS);
+  Scan c{0, 0, 0, min(p.B, tid * n), min(p.B, tid * n + n)};
+  for (int b = c.b0; b < c.b1; ++b) c.mine += kv8_weight(p, kv8_tiles(p, kv8_len(p, b))) * units;
+  long long sum = c.mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += x;
+  }
+  if (lane == 31) s_scan[warp] = sum;
+  __syncthreads();
+  c.before = sum - c.mine;
+#pragma unroll
+  for (int x = 0; x < WARPS; ++x) {
+    if (x < warp) c.before += s_scan[x];
+    c.total += s_scan[x];
+  }
+  return c;
+}
+// The request that holds a slot of the whole weight, by the thread that has it:
+// its number, the slot within it, its tiles and its length.
+__device__ __forceinline__ void kv8_find(const Kv8DecodeParams& p, int units, const Scan& c, long long slot,
+                                         volatile long long* out) {
+  if (slot < c.before || slot >= c.before + c.mine) return;
+  long long at = c.before;
+  for (int b = c.b0; b < c.b1; ++b) {
+    const int len = kv8_len(p, b), tiles = kv8_tiles(p, len);
+    if (slot < at + kv8_weight(p, tiles) * units) {
+      out[0] = b;
+      out[1] = slot - at;
+      out[2] = (long long)tiles << 32 | (unsigned)len;
+      return;
+    }
+    at += kv8_weight(p, tiles) * units;
+  }
+}
+
 // Row tile and K/V head of a unit.
 __device__ __forceinline__ int row_tile(const Kv8DecodeParams& p, int u) {
   return p.row_tiles == 1 ? 0 : (int)((unsigned)u % (unsigned)p.row_tiles);
@@ -304,41 +348,11 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  // ---- the share: the weight of all requests, thread t adding up requests t*n .. t*n + n - 1
-  long long mine = 0, before;
-  const int n = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, (int)threadIdx.x * n), b1 = min(p.B, b0 + n);
-  for (int b = b0; b < b1; ++b) mine += kv8_weight(p, kv8_tiles(p, kv8_len(p, b))) * units;
-  before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
-  }
-  if (lane == 31) s_scan[warp] = before;
+  const Scan scan = kv8_scan<kThreads / 32>(p, units, s_scan);
+  const long long from = share_begin(scan.total, (int)gridDim.x, k), to = share_begin(scan.total, (int)gridDim.x, k + 1);
+  kv8_find(p, units, scan, from, s_start);
   __syncthreads();
   tc_fence_after();
-  before -= mine;
-  long long total = 0;
-#pragma unroll
-  for (int x = 0; x < kThreads / 32; ++x) {
-    if (x < warp) before += s_scan[x];
-    total += s_scan[x];
-  }
-  const long long from = share_begin(total, (int)gridDim.x, k), to = share_begin(total, (int)gridDim.x, k + 1);
-  if (from >= before && from < before + mine) {  // the share begins in one of this thread's requests
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      const int len = kv8_len(p, b), tiles = kv8_tiles(p, len);
-      if (from < at + kv8_weight(p, tiles) * units) {
-        s_start[0] = b;
-        s_start[1] = from - at;
-        s_start[2] = (long long)tiles << 32 | (unsigned)len;
-        break;
-      }
-      at += kv8_weight(p, tiles) * units;
-    }
-  }
-  __syncthreads();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS = tmem, tO = tmem + 2 * L::kNS;
   const WaitCtx w{abort_flag, p.timeout_ns, p.err};
@@ -894,63 +908,90 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
   }
 }
 
-// What the shares' borders cut, and requests without keys.  One warp per query
-// row: the row's unit lies in the shares ka .. kb; one share alone has finished
-// it.  Where the work begins and ends is added up again from the lengths, by
-// each block, which needs nothing of the main kernel and so is done while that
-// one ends.
-template <int D>
+// What the shares' borders cut, and requests without keys.  Block x looks at
+// unit x, or, where units are more than shares, at the border behind share x
+// and the unit that begins in that share and goes on behind it.  A unit that lies
+// in the shares first .. last is merged, W warps to a row, each four shares at a
+// time.  Where that is, is worked out from the lengths again, which needs
+// nothing of the main kernel and so is done while that one ends.
+//   Blocks for units always: 16384 requests up to 64 tokens, whose lengths every
+// block of theirs adds up, 536 us, and 370 so.  Blocks for borders always: 8
+// requests up to 1000 tokens 17.2 us, and 13.0.  One warp to a row always: a request of
+// 131072 tokens 61 us, and 53.
+template <int D, int W, bool BY_UNIT>
 __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_constant__ Kv8DecodeParams p, int RT,
                                                                   int shares) {
-  constexpr int E = D / 32;
-  const int lane = lane_id(), units = p.Hkv * p.row_tiles;
-  const int b = blockIdx.y;
-  __shared__ long long s_before[8], s_all[8];
-  long long before = 0, total = 0;
-  for (int y = threadIdx.x; y < p.B; y += 256) {
-    const int n = p.seq_lens[y];
-    const long long wt = kv8_weight(p, kv8_tiles(p, min(max(n, 0), p.max_len))) * units;
-    total += wt;
-    if (y < b) before += wt;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (lane == 0) s_before[threadIdx.x >> 5] = before, s_all[threadIdx.x >> 5] = total;
-  __syncthreads();
-  before = total = 0;
-#pragma unroll
-  for (int y = 0; y < 8; ++y) before += s_before[y], total += s_all[y];
-  const long long weight = kv8_weight(p, kv8_tiles(p, min(max(p.seq_lens[b], 0), p.max_len)));
-  const long long each = quick_div(total, shares), more = total - each * shares;
+  constexpr int E = D / 32, ROWS = 8 / W;
+  const int units = p.Hkv * p.row_tiles, lane = lane_id(), warp = threadIdx.x >> 5, row = warp / W, part = warp % W;
+  __shared__ long long s_sum[16], s_at[3];
+  __shared__ float s_m[8], s_w[8], s_o[W > 1 ? 8 : 1][D];
+  long long each, more;
   auto share_of = [&](long long t) {
     return (int)(t < more * (each + 1) ? quick_div(t, each + 1) : more + quick_div(t - more * (each + 1), each));
   };
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done
-  for (int x0 = blockIdx.x * 8 + (threadIdx.x >> 5); x0 < p.Nq * p.Hq; x0 += gridDim.x * 8) {
-    const int i = p.Nq == 1 ? 0 : (int)((unsigned)x0 / (unsigned)p.Hq), h = x0 - i * p.Hq;
-    const int hk = (int)((unsigned)h / (unsigned)p.group), x = i * p.group + h - hk * p.group;  // row of the K/V head
-    const int u = hk * p.row_tiles + x / RT, r = x % RT;
-    const long long u0 = before + u * weight;
-    int ka = 0, kb = -1;  // (a request without keys: nothing to merge, zeros to write)
-    if (weight > 0) {
-      ka = share_of(u0 + p.lead);
-      kb = share_of(u0 + weight - 1);
-      if (ka == kb) continue;
+  int b, u, first = 0, last = -1;
+  long long u0 = 0;
+  if constexpr (BY_UNIT) {
+    b = blockIdx.x / units;
+    u = blockIdx.x - b * units;
+    long long before = 0, total = 0;
+    for (int x = threadIdx.x; x < p.B; x += 256) {
+      const long long weight = kv8_weight(p, kv8_tiles(p, kv8_len(p, x))) * units;
+      total += weight;
+      if (x < b) before += weight;
     }
-    // four shares at a time, their loads together, against a running maximum
+    const long long weight = kv8_weight(p, kv8_tiles(p, kv8_len(p, b)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 0) s_sum[warp] = before, s_sum[8 + warp] = total;
+    __syncthreads();
+    before = total = 0;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) before += s_sum[x], total += s_sum[8 + x];
+    each = quick_div(total, shares), more = total - each * shares;
+    u0 = before + u * weight;
+    if (weight > 0) first = share_of(u0 + p.lead), last = share_of(u0 + weight - 1);
+  } else {
+    const Scan scan = kv8_scan<8>(p, units, s_sum);
+    each = quick_div(scan.total, shares), more = scan.total - each * shares;
+    const long long border = share_begin(scan.total, shares, blockIdx.x + 1);
+    kv8_find(p, units, scan, border, s_at);
+    __syncthreads();
+    b = u = 0;
+    if (border < scan.total) {
+      b = (int)s_at[0];
+      const int weight = (int)(s_at[2] >> 32) + p.lead;
+      u = (int)quick_div(s_at[1], weight);
+      u0 = border - s_at[1] + (long long)u * weight;
+      first = share_of(u0 + p.lead);
+      if (first == (int)blockIdx.x) last = share_of(u0 + weight - 1);
+    }
+  }
+  for (int x0 = blockIdx.x; x0 < p.B; x0 += gridDim.x) {  // requests without keys
+    if (kv8_len(p, x0) > 0) continue;
+    const int n = p.Nq * p.Hq;
+    for (int x = blockIdx.y * 256 + threadIdx.x; x < n * (D / 8); x += gridDim.y * 256)
+      static_cast<uint4*>(p.o)[(size_t)x0 * n * (D / 8) + x] = make_uint4(0u, 0u, 0u, 0u);
+    for (int x = blockIdx.y * 256 + threadIdx.x; x < n; x += gridDim.y * 256) p.lse[(size_t)x0 * n + x] = -INFINITY;
+  }
+  const int rows = min(RT, p.Nq * p.group - row_tile(p, u) * RT);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done
+  if (last <= first) return;
+  for (int r0 = blockIdx.y * ROWS; r0 < rows; r0 += gridDim.y * ROWS) {
+    const int r = min(r0 + row, rows - 1);
     float acc[E], wsum = 0.f, m = -INFINITY;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int k0 = ka; k0 <= kb; k0 += 4) {
+    for (int k0 = first + part; k0 <= last; k0 += 4 * W) {
       float lc[4], v[4][E];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const bool on = k0 + y <= kb;
-        const int k = on ? k0 + y : kb;
-        const long long sl = (2 * (long long)k + (each * k + (k < more ? k : more) < u0 ? 1 : 0)) * RT + r;
+        const bool on = k0 + W * y <= last;
+        const int kk = on ? k0 + W * y : k0;
+        const long long sl = (2 * (long long)kk + (each * kk + (kk < more ? kk : more) < u0 ? 1 : 0)) * RT + r;  // its last piece, or its first
         lc[y] = on ? p.part_lse[sl] : -INFINITY;
         const float* src = p.part_o + sl * D + lane * E;
 #pragma unroll
@@ -970,12 +1011,37 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
         for (int e = 0; e < E; ++e) acc[e] = fmaf(wc, v[y][e], acc[e]);
       }
     }
-    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + ((size_t)b * p.Nq * p.Hq + x0) * D + lane * E);
+    if constexpr (W > 1) {  // the warps' parts, against their largest
 #pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0)
-      p.lse[((size_t)b * p.Hq + h) * p.Nq + i] = wsum == 0.f ? -INFINITY : (m + __log2f(wsum)) * 0.69314718055994531f;
+      for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+      if (lane == 0) s_m[warp] = m, s_w[warp] = wsum;
+      __syncthreads();
+      const int w0 = row * W;
+#pragma unroll
+      for (int y = 0; y < W; ++y) m = fmaxf(m, s_m[w0 + y]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      wsum = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int y = 0; y < W; ++y) {
+        const float f = ex2_sfu(s_m[w0 + y] - ref);
+        wsum = fmaf(f, s_w[w0 + y], wsum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(f, s_o[w0 + y][lane * E + e], acc[e]);
+      }
+      __syncthreads();
+    }
+    if (part == 0 && r0 + row < rows) {
+      const int x = row_tile(p, u) * RT + r, i = p.Nq == 1 ? 0 : (int)((unsigned)x / (unsigned)p.group);
+      const int h = kv_head(p, u) * p.group + x - i * p.group;
+      const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (((size_t)b * p.Nq + i) * p.Hq + h) * D + lane * E);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+      if (lane == 0)
+        p.lse[((size_t)b * p.Hq + h) * p.Nq + i] = wsum == 0.f ? -INFINITY : (m + __log2f(wsum)) * 0.69314718055994531f;
+    }
   }
 }
 
@@ -1023,13 +1089,18 @@ static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  // (a block adds up B lengths: with many requests, one block for all rows of a request, not B * rows / 8 sums of B)
-  cfg.gridDim = dim3(p.B <= 512 ? (unsigned)((p.Nq * p.Hq + 7) / 8) : 1u, (unsigned)p.B);
+  // four warps to a row where units lie in four shares or more
+  const long long units = (long long)p.B * p.Hkv * p.row_tiles;
+  const bool by_unit = units <= shares, wide = 4 * units <= shares;
+  cfg.gridDim = dim3((unsigned)(by_unit ? units : shares), wide ? RT / 2 : (RT + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = &a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_decode_kv8_merge_kernel<D>, static_cast<const Kv8DecodeParams&>(p), (int)RT, shares);
+  auto merge = wide      ? fa_decode_kv8_merge_kernel<D, 4, true>
+               : by_unit ? fa_decode_kv8_merge_kernel<D, 1, true>
+                         : fa_decode_kv8_merge_kernel<D, 1, false>;
+  return cudaLaunchKernelEx(&cfg, merge, static_cast<const Kv8DecodeParams&>(p), (int)RT, shares);
 }
 
 template <int D>
