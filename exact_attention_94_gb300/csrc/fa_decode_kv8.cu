@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
 #pragma unroll
       for (int r = 0; r < RG / 2; ++r) l2[r] = 0;
       __syncwarp();
-      if (lane < RG) my_neg[lane] = -kNoRef;
+      if (lane < RG) my_neg[lane] = 0.f;
       __syncwarp();
 
       for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
@@ -702,41 +702,62 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           }
         }
         float s[RG];
-        // The references: a piece's first tile makes them, another moves them if one of its p passes what e4m3 holds.
         for (bool settled = false;;) {
-          if (settled || t > pc.t0) {
-            // ---- scores less the references, in log2 units
-            uint32_t s1[RG], s2[RG];
-            tmem_load<RG>(tS + (it & 1) * L::kNS + lane_sel + g0, s1);
-            tmem_load<RG>(tS + (it & 1) * L::kNS + lane_sel + RT + g0, s2);
-            tmem_ld_wait();
+          // ---- scores less the references, in log2 units
+          uint32_t s1[RG], s2[RG];
+          tmem_load<RG>(tS + (it & 1) * L::kNS + lane_sel + g0, s1);
+          tmem_load<RG>(tS + (it & 1) * L::kNS + lane_sel + RT + g0, s2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int r = 0; r < RG; r += 4) {
+            const ulonglong2 qsc = *reinterpret_cast<const ulonglong2*>(s_qsc + r);
+            const ulonglong2 neg = *reinterpret_cast<const ulonglong2*>(my_neg + r);
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {  // (two rows an instruction)
+              const uint64_t x = f2_fma(f2_pack(__uint_as_float(s2[r + e]), __uint_as_float(s2[r + e + 1])), f2_pack(0.0625f, 0.0625f),
+                                        f2_pack(__uint_as_float(s1[r + e]), __uint_as_float(s1[r + e + 1])));
+              f2_unpack(f2_fma(x, f2_mul(e ? qsc.y : qsc.x, f2_pack(ks, ks)), e ? neg.y : neg.x), s[r + e], s[r + e + 1]);
+            }
+          }
+          if (!all) {
+#pragma unroll
+            for (int r = 0; r < RG; ++r) s[r] = any && sees(r) ? s[r] : -INFINITY;
+          }
+          if (settled) break;
+          if (t == pc.t0) {  // a piece's first tile makes the references (0 so far): its largest
 #pragma unroll
             for (int r = 0; r < RG; r += 4) {
-              const ulonglong2 qsc = *reinterpret_cast<const ulonglong2*>(s_qsc + r);
-              const ulonglong2 neg = *reinterpret_cast<const ulonglong2*>(my_neg + r);
+              float x[4];
 #pragma unroll
-              for (int e = 0; e < 4; e += 2) {  // (two rows an instruction)
-                const uint64_t x = f2_fma(f2_pack(__uint_as_float(s2[r + e]), __uint_as_float(s2[r + e + 1])), f2_pack(0.0625f, 0.0625f),
-                                          f2_pack(__uint_as_float(s1[r + e]), __uint_as_float(s1[r + e + 1])));
-                f2_unpack(f2_fma(x, f2_mul(e ? qsc.y : qsc.x, f2_pack(ks, ks)), e ? neg.y : neg.x), s[r + e], s[r + e + 1]);
-              }
+              for (int e = 0; e < 4; ++e) x[e] = warp_max(s[r + e] + lvs);
+              if (lane == 0) *reinterpret_cast<float4*>(my_max + r) = make_float4(x[0], x[1], x[2], x[3]);
             }
-            if (!all) {
-#pragma unroll
-              for (int r = 0; r < RG; ++r) s[r] = any && sees(r) ? s[r] : -INFINITY;
-            }
-            if (settled) break;
-            // ---- does any p pass that?
-            float top = fmaxf(s[0], s[1]);
-#pragma unroll
-            for (int r = 2; r < RG; r += 2) top = max3f(top, s[r], s[r + 1]);
-            const bool move = __any_sync(0xffffffffu, top > kHeadroom - lvs);
-            if (lane == 0) s_vote[(it & 1) * SOFT + warp] = move;
             ok = exchange();
             if (!ok) break;
-            const int4 votes = *reinterpret_cast<const int4*>(s_vote + (it & 1) * SOFT + group * 4);
-            if ((votes.x | votes.y | votes.z | votes.w) == 0) break;
+            if (lane < RG) {  // (of a row that sees no key yet, kNoRef)
+              const float x = fmaxf(fmaxf(g_max[lane], g_max[RG + lane]), fmaxf(g_max[2 * RG + lane], g_max[3 * RG + lane]));
+              my_neg[lane] = -fmaxf(x, kNoRef);
+            }
+            __syncwarp();
+            if constexpr (RG > 4) {
+#pragma unroll
+              for (int r = 0; r < RG; ++r) s[r] += my_neg[r];
+              break;
+            } else {  // (4 rows are faster read again: a window of 4096, d = 64, 20.9 us, and 22.1)
+              settled = true;
+              continue;
+            }
           }
+          // ---- another moves them if one of its p passes what e4m3 holds
+          float top = fmaxf(s[0], s[1]);
+#pragma unroll
+          for (int r = 2; r < RG; r += 2) top = max3f(top, s[r], s[r + 1]);
+          const bool move = __any_sync(0xffffffffu, top > kHeadroom - lvs);
+          if (lane == 0) s_vote[(it & 1) * SOFT + warp] = move;
+          ok = exchange();
+          if (!ok) break;
+          const int4 votes = *reinterpret_cast<const int4*>(s_vote + (it & 1) * SOFT + group * 4);
+          if ((votes.x | votes.y | votes.z | votes.w) == 0) break;
           // ---- new references: the largest up to here (rolled loops: rare, and the code is long already)
           constexpr int G = RG > 8 ? 8 : RG;  // rows at a time
 #pragma unroll 1
@@ -769,21 +790,20 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           __syncwarp();
 #pragma unroll
           for (int r = 0; r < RG; r += 2) l2[r / 2] = f2_mul(l2[r / 2], f2_pack(my_al[r], my_al[r + 1]));
-          if (t > pc.t0) {  // O stands at the old ones
-            ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 62));
-            if (!ok) break;
-            tc_fence_after();
+          // O stands at the old ones
+          ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 62));
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
-            for (int part = 0; part < 3; ++part) {
-              uint32_t o[RG];
-              tmem_load<RG>(tO + lane_sel + part * RT + g0, o);
-              tmem_ld_wait();
+          for (int part = 0; part < 3; ++part) {
+            uint32_t o[RG];
+            tmem_load<RG>(tO + lane_sel + part * RT + g0, o);
+            tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < RG; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * my_al[e]);
-              tmem_store<RG>(tO + lane_sel + part * RT + g0, o);
-            }
-            tmem_st_wait();
+            for (int e = 0; e < RG; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * my_al[e]);
+            tmem_store<RG>(tO + lane_sel + part * RT + g0, o);
           }
+          tmem_st_wait();
           settled = true;
         }
         if (!ok) break;
@@ -877,15 +897,22 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         tmem_load<OB>(tO + lane_sel + 2 * RT + g0 + r0, o3);
         tmem_ld_wait();
 #pragma unroll
-        for (int x = 0; x < OB; ++x) {
-          if (r0 + x < mine && has) {
-            const float y = fmaf(fmaf(__uint_as_float(o3[x]), 0.0625f, __uint_as_float(o2[x])), 0.0625f, __uint_as_float(o1[x]));
-            const float f = my_al[r0 + x];
-            const float val = f == 0.f ? 0.f : y * f;  // (0 * NaN would not be 0)
-            if (whole)
-              static_cast<__nv_bfloat16*>(p.o)[(size_t)my_at[r0 + x] * D + e] = __float2bfloat16_rn(val);
-            else
-              p.part_o[(size_t)my_at[r0 + x] * D + e] = val;
+        for (int x0 = 0; x0 < OB; x0 += 4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(my_al + r0 + x0);
+          const int4 a4 = *reinterpret_cast<const int4*>(my_at + r0 + x0);
+          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+          const int at[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int x = x0 + z;
+            if (r0 + x < mine && has) {
+              const float y = fmaf(fmaf(__uint_as_float(o3[x]), 0.0625f, __uint_as_float(o2[x])), 0.0625f, __uint_as_float(o1[x]));
+              const float val = f[z] == 0.f ? 0.f : y * f[z];  // (0 * NaN would not be 0)
+              if (whole)
+                static_cast<__nv_bfloat16*>(p.o)[(size_t)at[z] * D + e] = __float2bfloat16_rn(val);
+              else
+                p.part_o[(size_t)at[z] * D + e] = val;
+            }
           }
         }
       }
