@@ -110,13 +110,12 @@ struct Layout {
   static constexpr uint32_t kMaxOff = kScOff + kVs * kScBytes;        // [4][RT] each: warps' maxima, sums, references, factors, output rows
   static constexpr uint32_t kRowOff = kMaxOff + 20 * RT * 4;                 // two of: [RT] query scales, [RT] positions
   static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // votes, scan, start
-  // pieces announced ahead of their tiles, with their rows of Q as they lie in memory
-  static constexpr int kPieces = (RT == 8 && D == 128) || RT == 32 ? 1 : RT == 8 ? 3 : 2;  // as many as the CTAs leave room for
-  static constexpr uint32_t kPieceOff = kMiscOff + 192;                      // [kPieces] 32 bytes each
-  static constexpr uint32_t kStageOff = (kPieceOff + kPieces * 32 + 127) / 128 * 128;
+  // the piece announced ahead of its tiles, with its rows of Q as they lie in memory
+  static constexpr uint32_t kPieceOff = kMiscOff + 192;
+  static constexpr uint32_t kStageOff = (kPieceOff + 32 + 127) / 128 * 128;
   static constexpr uint32_t kStage = RT * D * 2u;
-  static constexpr uint32_t kBarOff = kStageOff + kPieces * kStage;
-  static constexpr int kBars = 2 * kSlots + 8 + 2 * kPieces;
+  static constexpr uint32_t kBarOff = kStageOff + kStage;
+  static constexpr int kBars = 2 * kSlots + 10;
   static constexpr uint32_t kBytes = kBarOff + 8 * kBars + 16 + 1024;
   static_assert(kUsed <= 256, "TMEM columns");
 };
@@ -314,8 +313,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
   auto TILE = [&](int s) { return base + L::kSlot * (uint32_t)s; };
   const uint32_t SF = bars + 16u * NSL;  // S ready [2]; then P ready, O ready, the warps' exchange, Q ready
   const uint32_t PF = SF + 16, OF = SF + 24, QB = SF + 32, XB = SF + 40;           // (an exchange for each group, one for all)
-  auto HERE = [&](int s) { return SF + 64 + 8u * (uint32_t)s; };                  // piece announced
-  auto TAKEN = [&](int s) { return SF + 64 + 8u * (uint32_t)(L::kPieces + s); };  // and taken by all its readers
+  const uint32_t HERE = SF + 64, TAKEN = SF + 72;                                   // piece announced, and taken by all its readers
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::kBarOff + 8 * L::kBars);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sb + L::kBarOff + 8 * L::kBars + 4);
   Piece* s_piece = reinterpret_cast<Piece*>(sb + L::kPieceOff);
@@ -341,10 +339,8 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     mbar_init(XB, 4);
     mbar_init(XB + 8, 4);
     mbar_init(XB + 16, SOFT);
-    for (int s = 0; s < L::kPieces; ++s) {
-      mbar_init(HERE(s), 1);
-      mbar_init(TAKEN(s), SOFT + 1);
-    }
+    mbar_init(HERE, 1);
+    mbar_init(TAKEN, SOFT + 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -367,8 +363,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     // two batches ahead (and moved to their place one later, when they have
     // come); scales are copied asynchronously to the tile's place, and arrive on
     // its barrier.  A piece is announced, with its rows of Q, before its first
-    // tile is asked for.  (That waits until the piece kPieces before has been
-    // taken, for which it takes no tile that has not been asked for.)
+    // tile is asked for.  (That waits until the piece before has been taken, which
+    // needs no tile that has not been asked for.  Announcing two or three pieces
+    // ahead where shared memory allows it gained nothing.)
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -393,20 +390,19 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     int t_next = 0, pieces = 0;  // next tile of pc to fetch; pieces fetched
     bool more = true;
     auto announce = [&](const Piece& pc) {
-      const int st = pieces % L::kPieces;
-      if (pieces >= L::kPieces) ok = __all_sync(0xffffffffu, mbar_wait(TAKEN(st), (pieces / L::kPieces - 1) & 1, w, 50));
+      if (pieces > 0) ok = __all_sync(0xffffffffu, mbar_wait(TAKEN, (pieces - 1) & 1, w, 50));
       if (!ok) return;
       const int x0 = row_tile(p, pc.u) * RT, rows = pc.t0 < pc.t1 ? min(RT, p.Nq * p.group - x0) : 0;
       if (lane == 0) {
-        s_piece[st] = pc;
-        mbar_arrive_expect_tx(HERE(st), (uint32_t)(rows * D * 2));
+        *s_piece = pc;
+        mbar_arrive_expect_tx(HERE, (uint32_t)(rows * D * 2));
       }
       __syncwarp();
       if (lane < rows) {
         const int x = x0 + lane, i = p.Nq == 1 ? 0 : (int)((unsigned)x / (unsigned)p.group);
         const int h = kv_head(p, pc.u) * p.group + x - i * p.group;
-        bulk_load(base + L::kStageOff + st * L::kStage + lane * D * 2,
-                  static_cast<const __nv_bfloat16*>(p.q) + (((size_t)pc.b * p.Nq + i) * p.Hq + h) * D, D * 2, HERE(st));
+        bulk_load(base + L::kStageOff + lane * D * 2,
+                  static_cast<const __nv_bfloat16*>(p.q) + (((size_t)pc.b * p.Nq + i) * p.Hq + h) * D, D * 2, HERE);
       }
       ++pieces;
     };
@@ -503,12 +499,11 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       return true;
     };
     for (int it = 0, piece = 0; ok; ++piece) {
-      const int st = piece % L::kPieces;
-      ok = __all_sync(0xffffffffu, mbar_wait(HERE(st), piece / L::kPieces & 1, w, 56));
+      ok = __all_sync(0xffffffffu, mbar_wait(HERE, piece & 1, w, 56));
       if (!ok) break;
-      const int n = s_piece[st].t1 - s_piece[st].t0;
+      const int n = s_piece->t1 - s_piece->t0;
       __syncwarp();
-      if (lane == 0) mbar_arrive(TAKEN(st));
+      if (lane == 0) mbar_arrive(TAKEN);
       if (n == 0) break;
       ok = __all_sync(0xffffffffu, mbar_wait(QB, piece & 1, w, 52));
       for (int t = 0; t < n && ok; ++t, ++it) {
@@ -556,9 +551,8 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     // ---- the next piece, and its Q: rows in turn for the warps, split into two
     // e4m3 parts at each row's power of two
     auto take = [&](int piece, Piece& s) {
-      const int st = piece % L::kPieces;
-      if (!__all_sync(0xffffffffu, mbar_wait(HERE(st), piece / L::kPieces & 1, w, 63))) return false;
-      s = s_piece[st];
+      if (!__all_sync(0xffffffffu, mbar_wait(HERE, piece & 1, w, 63))) return false;
+      s = *s_piece;
       float* s_qsc = reinterpret_cast<float*>(sb + L::kRowOff + (piece & 1) * 2 * RT * 4);
       int* s_pos = reinterpret_cast<int*>(s_qsc + RT);
       const int rows = s.t0 == s.t1 ? 0 : rows_of(s);
@@ -570,10 +564,10 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       for (int x = 0; x < PASSES; ++x) {
         const int r = (x * SOFT + warp) * RPW + sub;
         q[x] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) q[x] = *reinterpret_cast<const uint4*>(sb + L::kStageOff + st * L::kStage + r * D * 2 + seg * 16);
+        if (r < rows) q[x] = *reinterpret_cast<const uint4*>(sb + L::kStageOff + r * D * 2 + seg * 16);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(TAKEN(st));
+      if (lane == 0) mbar_arrive(TAKEN);
       if (rows == 0) return true;
 #pragma unroll
       for (int x = 0; x < PASSES; ++x) {
@@ -888,7 +882,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         }
       }
       __syncwarp();
-      constexpr int OB = RG > 8 ? 8 : RG;  // rows at a time
+      constexpr int OB = 4;  // rows at a time (8 are more code: 4096 requests up to 512 tokens 538 us, and 506)
 #pragma unroll 1
       for (int r0 = 0; r0 < mine; r0 += OB) {
         uint32_t o1[OB], o2[OB], o3[OB];
