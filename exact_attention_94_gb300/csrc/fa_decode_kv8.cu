@@ -45,19 +45,22 @@
 // S is double buffered in TMEM (the next tile's scores are ready when a tile's
 // softmax starts); P is not: it is written when the product before has read it.
 //
-// Measured, d = 128, pages of 16 to 64, replayed graphs of many calls:
-//   64 requests of 16385 to 32768 tokens, 64 heads over 8      473 us  6.83 TB/s
-//   8 requests of 1000 to 8192, 32 heads over 32                53 us  5.66 TB/s
-//   16 requests of 100 to 16384, 4 drafts, 64 heads over 8      61 us  4.44 TB/s
-//   32 requests, a window of 4096, 16 heads over 4, d = 64      21 us  2.98 TB/s
-//   1 request of 777, 32 heads over 8                          9.5 us
+// Measured, d = 128 unless said, pages of 16 to 64, replayed graphs of many calls:
+//   64 requests of 16385 to 32768 tokens, 64 heads over 8      478 us  6.76 TB/s
+//   256 requests of 1 to 2048, 64 heads over 8                  98 us  5.6 TB/s
+//   8 requests of 1000 to 8192, 32 heads over 32                54 us  5.5 TB/s
+//   16 requests of 100 to 16384, 4 drafts, 64 heads over 8      60 us  4.6 TB/s
+//   4096 requests of 1 to 128, 64 heads over 8                 229 us  2.9 TB/s
+//   32 requests, a window of 4096, 16 heads over 4, d = 64      21 us  3.0 TB/s
+//   1 request of 777, 32 heads over 8                          8.6 us
 // The first is as fast as the card copies.  The calls of 20 to 60 us lose some
 // 5 us to the start (lengths, page numbers, pages: three reads one after the
-// other before the first tile) and the merge.  32 rows are bound by the softmax
-// warps' instructions (issue slots 60% busy): they came from 82 us with one
-// group of warps and a byte store per code, by two groups (72), P by key and
-// its split in half precision (66), all scores read at once (62.5) and packed
-// fp32 arithmetic (61).
+// other before the first tile) and the merge.  Units of one tile are a chain of
+// exchanges between the warps, 3.2 us each, three at once per SM.  32 rows are
+// bound by the softmax warps' instructions (issue slots 51% busy) and their
+// waits for one another: they came from 82 us with one group of warps and a
+// byte store per code, by two groups (72), P by key and its split in half
+// precision (66), all scores read at once (62.5) and packed fp32 arithmetic (61).
 #include "serving.cuh"
 
 #include <cmath>
@@ -70,21 +73,23 @@ constexpr float kAtRef = 64.f;       // p at the reference
 constexpr float kHeadroom = 2.8f;    // log2(448 / 64), rounded down
 constexpr float kLeastScale = -100.f;  // log2 of a value scale, from below: a page of zeros counts as one of 2^-100
 // What a unit's start and end cost, in tiles.  Against none at all: 16 requests
-// of 100 to 16384 tokens with 32 rows 110 -> 66 us, with 8 rows 70 -> 52; a
-// window of 4096 27.5 -> 21.  With 2 the 32 rows took 84, with 6 none gained.
+// of 100 to 16384 tokens with 32 rows 82 -> 60 us, with 8 rows 53.3 -> 51.9; 128 up
+// to 2000, d = 64, 49 -> 37; a window of 4096 24.3 -> 20.6.  With 2 the 32 rows take
+// 63.5; with 6 the 128 requests take 40.
 constexpr int kLead(int RT) { return 3 + RT / 16; }
 constexpr float kNoRef = -3.0e38f;   // reference of a row that has seen no key
 
 // CTAs per SM: three where registers and shared memory allow it, for the loads
-// in flight (two: 64 long requests, 8 rows, 484 us, and not 480; with d = 64, 128
-// requests up to 2000 tokens, 41.6 and not 36.5).
+// and the units in flight (two: 4096 requests up to 128 tokens, 8 rows, 331 us, and
+// not 229; 128 up to 2000, d = 64, 39.8 and not 37.2; only 16 or more tiles a unit
+// would have it the other way, by 2%).
 constexpr int kv8_ctas_per_sm(int RT) { return RT <= 8 ? 3 : 2; }
 
 template <int D, int RT>
 struct Layout {
   // Softmax warps come in groups of four (one for each quarter of a tile's
-  // keys); 32 rows are two groups' work, 16 rows each (one group: 66 us for the
-  // 62.5 of two; for 16 rows and fewer two gain nothing).
+  // keys); 32 rows are two groups' work, 16 rows each (one group, when both were
+  // measured, 66 us for the 62.5 of two; for 16 rows and fewer two gain nothing).
   static constexpr int kGroups = RT == 32 ? 2 : 1;
   static_assert(RT / kGroups <= 16, "rows of a group");
   static constexpr int kThreads = (4 * kGroups + 2) * 32;
@@ -107,7 +112,8 @@ struct Layout {
   static constexpr uint32_t kQOff = kPOff + kKv8Tile * (uint32_t)kNP;
   static constexpr uint32_t kScOff = kQOff + kNS * (uint32_t)D;              // per V slot: 8 key scales, 8 value scales
   static constexpr uint32_t kScBytes = 64;
-  static constexpr uint32_t kMaxOff = kScOff + kVs * kScBytes;        // [4][RT] each: warps' maxima, sums, references, factors, output rows
+  // [4][RT] each: warps' maxima, sums, references, factors, output rows
+  static constexpr uint32_t kMaxOff = kScOff + kVs * kScBytes;
   static constexpr uint32_t kRowOff = kMaxOff + 20 * RT * 4;                 // two of: [RT] query scales, [RT] positions
   static constexpr uint32_t kMiscOff = (kRowOff + 2 * 2 * RT * 4 + 15) / 16 * 16;  // votes, scan, start
   // the piece announced ahead of its tiles, with its rows of Q as they lie in memory
@@ -604,7 +610,8 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           for (int part = 0; part < 2; ++part) {
             const int col = part * RT + r;
             const uint32_t* c = part ? c2 : c1;
-            const uint32_t at = D == 128 ? col * 128 + (((seg >> 1) ^ (col & 7)) << 4) : col * 64 + (((seg >> 1) ^ ((col >> 1) & 3)) << 4);
+            const uint32_t at = D == 128 ? col * 128 + (((seg >> 1) ^ (col & 7)) << 4)
+                                         : col * 64 + (((seg >> 1) ^ ((col >> 1) & 3)) << 4);
             *reinterpret_cast<uint2*>(sb + L::kQOff + at + (seg & 1) * 8) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
           }
           if (seg == 0) {
@@ -708,7 +715,8 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
             const ulonglong2 neg = *reinterpret_cast<const ulonglong2*>(my_neg + r);
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {  // (two rows an instruction)
-              const uint64_t x = f2_fma(f2_pack(__uint_as_float(s2[r + e]), __uint_as_float(s2[r + e + 1])), f2_pack(0.0625f, 0.0625f),
+              const uint64_t x = f2_fma(f2_pack(__uint_as_float(s2[r + e]), __uint_as_float(s2[r + e + 1])),
+                                        f2_pack(0.0625f, 0.0625f),
                                         f2_pack(__uint_as_float(s1[r + e]), __uint_as_float(s1[r + e + 1])));
               f2_unpack(f2_fma(x, f2_mul(e ? qsc.y : qsc.x, f2_pack(ks, ks)), e ? neg.y : neg.x), s[r + e], s[r + e + 1]);
             }
@@ -737,7 +745,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
 #pragma unroll
               for (int r = 0; r < RG; ++r) s[r] += my_neg[r];
               break;
-            } else {  // (4 rows are faster read again: a window of 4096, d = 64, 20.9 us, and 22.1)
+            } else {
+              // (four rows are faster read again: a window of 4096, d = 64, 20.9 us, and 22.1; eight are
+              // not: 512 requests with a window of 128 64.5, and 61.8)
               settled = true;
               continue;
             }
@@ -937,8 +947,8 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
 // nothing of the main kernel and so is done while that one ends.
 //   Blocks for units always: 16384 requests up to 64 tokens, whose lengths every
 // block of theirs adds up, 536 us, and 370 so.  Blocks for borders always: 8
-// requests up to 1000 tokens 17.2 us, and 13.0.  One warp to a row always: a request of
-// 131072 tokens 61 us, and 53.
+// requests up to 1000 tokens 17.2 us, and 12.5.  One warp to a row always: a request of
+// 131072 tokens 62 us, and 52.5.
 template <int D, int W, bool BY_UNIT>
 __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_constant__ Kv8DecodeParams p, int RT,
                                                                   int shares) {
@@ -1012,7 +1022,8 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
       for (int y = 0; y < 4; ++y) {
         const bool on = k0 + W * y <= last;
         const int kk = on ? k0 + W * y : k0;
-        const long long sl = (2 * (long long)kk + (each * kk + (kk < more ? kk : more) < u0 ? 1 : 0)) * RT + r;  // its last piece, or its first
+        // the share's last piece, if it begins before the unit, or its first
+        const long long sl = (2 * (long long)kk + (each * kk + (kk < more ? kk : more) < u0 ? 1 : 0)) * RT + r;
         lc[y] = on ? p.part_lse[sl] : -INFINITY;
         const float* src = p.part_o + sl * D + lane * E;
 #pragma unroll
@@ -1057,7 +1068,8 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
       const int x = row_tile(p, u) * RT + r, i = p.Nq == 1 ? 0 : (int)((unsigned)x / (unsigned)p.group);
       const int h = kv_head(p, u) * p.group + x - i * p.group;
       const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (((size_t)b * p.Nq + i) * p.Hq + h) * D + lane * E);
+      const size_t out = ((size_t)b * p.Nq + i) * p.Hq + h;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + out * D + lane * E);
 #pragma unroll
       for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
       if (lane == 0)
@@ -1067,11 +1079,11 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
 }
 
 // Query rows of one CTA.  A tile of fewer rows leaves room for a third CTA and
-// has less to do at a unit's start and end: 4 rows took 21.1 us in a tile of 4,
-// 22.9 in one of 8 and 26.1 in one of 16 (32 requests, a window of 4096, d = 64);
-// 8 rows 36.5 and 56.6 in tiles of 8 and 16 (128 requests up to 2000, d = 64); 16
-// rows 53.2 and 61.0 in tiles of 16 and 32 (two drafts of eight heads); and 32
-// rows 66 in one tile and 81 in two, which read the cache twice (four drafts).
+// has less to do at a unit's start and end: 4 rows take 20.6 us in a tile of 4,
+// 22.9 in one of 8 and 27.6 in one of 16 (32 requests, a window of 4096, d = 64);
+// 8 rows 37 and 56 in tiles of 8 and 16 (128 requests up to 2000, d = 64); 16 rows
+// 53.9 and 57.0 in tiles of 16 and 32 (two drafts of eight heads); and 32 rows 60
+// in one tile and 79 in two, which read the cache twice (four drafts).
 int kv8_row_tile(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 // CTAs that run at once, and the most tiles a call can have.
