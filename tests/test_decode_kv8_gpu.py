@@ -333,6 +333,17 @@ def test_pages_before_the_window_may_be_gone(P, d, window, Nq):
         assert_close(o, lse, ref)
 
 
+@pytest.mark.parametrize("B,Nq,Hq,Hkv,shares", [(240, 1, 4, 2, 0), (90, 1, 4, 2, 37), (200, 3, 12, 1, 0), (600, 1, 1, 1, 11),
+                                                (1, 1, 8, 2, 0), (1, 4, 16, 1, 0), (3, 1, 1, 1, 900)])
+def test_units_fewer_and_more_than_shares(B, Nq, Hq, Hkv, shares):
+    """Many short requests, some without keys, whose units the borders of few shares
+    cut; and few long ones, each in many shares."""
+    rng = np.random.default_rng(B + Nq)
+    lens = rng.integers(0, 260, B) * (rng.random(B) < 0.9) if B > 3 else [5000, 0, 1700][:B]
+    check(make([int(n) for n in lens], Nq, Hq, Hkv, 64, 16, seed=B), shares=shares)
+    check(make([int(n) for n in lens], Nq, Hq, Hkv, 64, 16, seed=B), shares=shares, window=130)
+
+
 def test_what_the_workspace_held_does_not_matter():
     """A captured call replayed over a workspace of every sort of content, and with many pieces a unit."""
     a = dev(make([3000, 17], 1, 4, 2, 64, 16, seed=13))
