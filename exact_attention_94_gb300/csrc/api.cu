@@ -871,8 +871,9 @@ static int kv8_span(int Nq, int max_seq_len, int window_left) {
 }
 
 size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_shares) {
-  if (B < 1 || Nq < 1 || Hkv < 1 || Hq < Hkv || d < 1 || num_shares < 1 || num_shares > 65535) return 0;
-  if ((long long)Nq * Hq > 65535) return 0;
+  if (B < 1 || B > 16384 || Nq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  if (num_shares < 0 || num_shares > 65535 || (long long)Nq * Hq > 65535) return 0;
+  if (num_shares == 0) num_shares = kv8_most_shares(Nq, Hq / Hkv);
   const size_t rows = 2 * (size_t)num_shares * kv8_row_tile(Nq * (Hq / Hkv));
   return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float));
 }

@@ -1086,8 +1086,8 @@ __global__ void __launch_bounds__(256) fa_decode_kv8_merge_kernel(const __grid_c
 // in one tile and 79 in two, which read the cache twice (four drafts).
 int kv8_row_tile(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
-// CTAs that run at once, and the most tiles a call can have.
-static int kv8_ctas(int Nq, int group) {
+// CTAs that run at once, the most shares dealt of the library's own choice, and the most tiles a call can have.
+int kv8_most_shares(int Nq, int group) {
   int dev = 0, n_sm = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   return n_sm * kv8_ctas_per_sm(kv8_row_tile(Nq * group));
@@ -1099,7 +1099,7 @@ static long long kv8_most_tiles(int B, int Nq, int Hkv, int group, int span) {
 
 int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span) {
   const long long tiles = kv8_most_tiles(B, Nq, Hkv, group, span);
-  const int ctas = kv8_ctas(Nq, group);
+  const int ctas = kv8_most_shares(Nq, group);
   return (int)(tiles < 1 ? 1 : tiles < ctas ? tiles : ctas);
 }
 
@@ -1113,7 +1113,7 @@ static cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, Kv8
   if (e != cudaSuccess) return e;
   p.row_tiles = (p.Nq * p.group + RT - 1) / RT;
   // Where a share is a tile or less, nothing is gained by making room for starts.
-  p.lead = kv8_most_tiles(p.B, p.Nq, p.Hkv, p.group, span) > kv8_ctas(p.Nq, p.group) ? kLead(RT) : 0;
+  p.lead = kv8_most_tiles(p.B, p.Nq, p.Hkv, p.group, span) > kv8_most_shares(p.Nq, p.group) ? kLead(RT) : 0;
   kern<<<shares, Layout<D, RT>::kThreads, smem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

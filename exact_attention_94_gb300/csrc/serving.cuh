@@ -95,6 +95,7 @@ struct Kv8DecodeParams {
   unsigned long long timeout_ns;
 };
 int kv8_auto_shares(int B, int Nq, int Hkv, int group, int span);
+int kv8_most_shares(int Nq, int group);  // that kv8_auto_shares can choose on the current device
 int kv8_row_tile(int rows);  // query rows of a CTA for `rows` rows per K/V head
 // 3-D uint8 tensor map of the codes, [heads of pages][page_size][D], swizzled at the row's length.
 bool make_tmap_codes(CUtensorMap* m, const void* ptr, int D, int page_size, long long page_heads, int box_rows);

@@ -575,7 +575,11 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
 
 /* Shares fa_decode_kv8 uses when it is given num_shares = 0 (window_left as there). */
 int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int max_seq_len, int window_left);
-/* 0 for arguments that the call refuses. */
+/*
+ * Bytes of workspace for a call with these arguments; num_shares = 0: enough for
+ * every choice that the call can make on the current device.  0 for sizes that
+ * the call refuses.
+ */
 size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_shares);
 
 /*

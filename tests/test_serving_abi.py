@@ -129,3 +129,25 @@ def test_python_side():
         ops.page_plan(i, i, i, i, torch.zeros((1, 1), dtype=torch.int32), 16, 1)
     with pytest.raises(ValueError):
         ops.kv8_append(x, x, x, x, x, x, i, i)
+
+
+def test_workspace_of_an_automatic_choice(lib):
+    """num_shares = 0, which the call takes: the query's bytes cover whatever it chooses."""
+    for Nq, Hq, Hkv in ((1, 1, 1), (1, 8, 8), (1, 64, 8), (2, 64, 8), (4, 64, 8), (8, 64, 1), (65535, 1, 1)):
+        for d in (64, 128):
+            most = lib.fa_decode_kv8_workspace_bytes(16384, Nq, Hq, Hkv, d, 0)
+            for B, L, window in ((1, 1, -1), (1, 777, -1), (64, 32768, -1), (16384, 1 << 30, -1), (16384, 1 << 30, 4095)):
+                shares = lib.fa_decode_kv8_num_shares(B, Nq, Hq, Hkv, L, window)
+                assert most >= lib.fa_decode_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, shares) > 0
+                assert lib.fa_decode_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, 0) == most
+
+
+@pytest.mark.parametrize("bad", [dict(B=0), dict(B=16385), dict(Nq=0), dict(Hq=0), dict(Hkv=0), dict(Hkv=3), dict(Hkv=8),
+                                 dict(d=96), dict(d=32), dict(shares=-1), dict(shares=65536), dict(Nq=20000)])
+def test_the_workspace_query_refuses_what_the_call_refuses(lib, bad):
+    a = dict(B=1, Nq=1, Hq=4, Hkv=2, d=128, shares=1)
+    assert lib.fa_decode_kv8_workspace_bytes(*a.values()) > 0
+    a.update(bad)
+    assert lib.fa_decode_kv8_workspace_bytes(*a.values()) == 0
+    sizes = [a[x] for x in ("B", "Nq", "Hq", "Hkv", "d")]
+    assert lib.fa_decode_kv8(*(A,) * 9, *sizes, 16, 8, 4, 64, -1, a["shares"], A, 0.1, NUL) in (INV, UNS)
