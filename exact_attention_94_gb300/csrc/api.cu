@@ -748,7 +748,7 @@ fa_status fa_page_plan(const int* ctx_lens, const int* new_lens, const int* free
                        int* block_table, int* seq_lens, int* cu_new, int* page, int* slot, int* position,
                        int* free_count_out, int B, int max_tokens, int page_size, int num_pages, int max_blocks,
                        fa_stream_t stream) {
-  if (B < 1 || B > 16384 || max_tokens < 0 || page_size < 1 || num_pages < 1 || max_blocks < 1)
+  if (B < 1 || B > kPlanMaxB || max_tokens < 0 || page_size < 1 || num_pages < 1 || max_blocks < 1)
     return FA_ERR_INVALID_ARG;
   if (!ctx_lens || !new_lens || !free_pages || !free_count || !block_table || !seq_lens || !cu_new || !free_count_out)
     return FA_ERR_INVALID_ARG;

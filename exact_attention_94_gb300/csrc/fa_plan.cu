@@ -168,12 +168,18 @@ __global__ void __launch_bounds__(1024) fa_page_plan_totals_kernel(const PlanPar
   }
 }
 
+static constexpr size_t plan_smem(int B) { return (3 * (size_t)B + 1) * sizeof(int); }
+
 template <int THREADS>
 static cudaError_t launch_page_plan_t(const PlanParams& p, int ctas, cudaStream_t stream) {
-  const size_t smem = (3 * (size_t)p.B + 1) * sizeof(int);
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(fa_page_plan_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = plan_smem(p.B);
+  // More than the 48 KiB that every launch may have, less the kernel's static
+  // part, is asked for, and always as much as the largest batch takes: the limit
+  // belongs to the process, and a call on another thread may set it between here
+  // and the launch.
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(fa_page_plan_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)plan_smem(kPlanMaxB));
     if (e != cudaSuccess) return e;
   }
   fa_page_plan_kernel<THREADS><<<ctas, THREADS, smem, stream>>>(p);

@@ -13,6 +13,7 @@ namespace fa {
 constexpr unsigned FA_DEVERR_OUT_OF_PAGES = 0x2002u;  // a plan needs more pages than the free stack has
 
 // Planning a step (see fa_page_plan in fa.h).
+constexpr int kPlanMaxB = 16384;  // requests at most
 struct PlanParams {
   const int* ctx_lens;       // [B]
   const int* new_lens;       // [B]

@@ -1,11 +1,18 @@
 """fa_page_plan against the reference plan: every output equal, in place and
 replayed, and the refusals that the device makes."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 from exact_attention_94_gb300 import ops
 from oracle import serving
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +137,48 @@ def test_on_another_stream():
     got = ops.page_plan(*args, 16, cap, stream=s)
     s.synchronize()
     check(got, want, args[4])
+
+
+FRESH = """
+import sys
+import torch
+from exact_attention_94_gb300 import ops
+i32 = dict(dtype=torch.int32, device="cuda")
+for B in map(int, sys.argv[1:]):
+    p = ops.page_plan(torch.zeros(B, **i32), torch.ones(B, **i32), torch.arange(B, **i32), torch.full((1,), B, **i32),
+                      torch.zeros((B, 1), **i32), 16, B)
+    assert p.page.tolist() == list(range(B - 1, -1, -1)) and p.free_count.item() == 0, B
+assert ops.device_error() == 0
+"""
+
+
+def test_every_batch_size_launches_in_a_fresh_process():
+    """The batches around 48 KiB of shared memory, in rising order: no larger one has gone before."""
+    sizes = [1025, 4050, 4051, 4052, 4060, 4094, 4095, 4096, 4097, 16384]
+    r = subprocess.run([sys.executable, "-c", FRESH, *map(str, sizes)], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_threads_with_batches_of_different_sizes():
+    """One thread's batch of 5000 does not take the shared memory from another's of 16384."""
+    def plan(B, n, failures):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            a = [torch.zeros(B, dtype=torch.int32, device="cuda"), torch.ones(B, dtype=torch.int32, device="cuda"),
+                 torch.arange(B, dtype=torch.int32, device="cuda"), i32([B]), torch.zeros((B, 1), dtype=torch.int32, device="cuda")]
+            out = ops.page_plan(*a, 16, B)
+            for _ in range(n):
+                try:
+                    ops.page_plan(*a, 16, B, out=out)
+                except Exception as e:  # noqa: BLE001 - the thread's failures are the test's result
+                    failures.append(str(e))
+            torch.cuda.current_stream().synchronize()
+            assert out.page.tolist() == list(range(B - 1, -1, -1))
+
+    failures = []
+    threads = [threading.Thread(target=plan, args=(B, 3000, failures)) for B in (4500, 5000, 16384)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, (len(failures), failures[0])
+    assert ops.device_error() == 0
