@@ -666,7 +666,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         if (!ok) break;
         tc_fence_after();
         const float* sc = reinterpret_cast<const float*>(sb + L::kScOff + (it % VS) * L::kScBytes);
-        const float ks = sc[group16], vs = sc[8 + group16], lvs = fmaxf(__log2f(vs), kLeastScale);
+        const float ks = sc[group16], vs0 = sc[8 + group16];
+        const bool odd_scale = !(fabsf(vs0) <= 3.4e38f);  // (an infinity would pass as e4m3's largest)
+        const float vs = odd_scale ? __uint_as_float(0x7fffffffu) : vs0, lvs = fmaxf(__log2f(vs), kLeastScale);
         const int j0 = pc.beg + t * kKv8Tile, j = j0 + key;
         // some row does not see some key of the tile
         const bool partial = j0 + kKv8Tile > pc.len - p.Nq + 1 || (p.win_left >= 0 && j0 < pc.len - 1 - p.win_left);
@@ -674,8 +676,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         // A key's value row may hold NaN, and 0 * NaN is not 0.  Where no row sees
         // the key (it may be anything behind the last or before the window), its
         // values count as zero.
-        // Where some rows do and some don't (drafts), a row with a NaN counts as
-        // zero too, and as NaN to the rows that see it: in all their elements.
+        // Where some rows do and some don't (drafts), a row with a NaN, or of a page
+        // whose scale is no number, counts as zero too, and as NaN to the rows that see
+        // it: in all their elements.
         bool poison = false, any = true, all = true;
         if (partial) {
           any = j <= pos_last && (p.win_left < 0 || j >= pos_first - p.win_left);
@@ -690,7 +693,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
               nan |= __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
                      __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
             }
-            poison = nan != 0;
+            poison = nan != 0 || odd_scale;
           }
           if (GROUPS > 1) {  // (one group's row is the other's: both have read it before either writes)
             // every softmax warp passes here: the tile is partial for all of them
@@ -818,7 +821,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         }
         // The split works on p rounded to f16, by 2^-12 of itself at most: 11 bits,
         // which the three parts hold exactly, and every difference of theirs too.
-        const float vn = poison ? 0.f : vs * kAtRef;
+        const float vn = poison || !any ? 0.f : vs * kAtRef;
         uint32_t code[3][RG / 4];
 #pragma unroll
         for (int r = 0; r < RG; r += 2) {

@@ -562,11 +562,14 @@ fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, voi
  *                  16-byte aligned, contents on entry do not matter; calls
  *                  whose work overlaps on the GPU need one each
  * What a page holds behind a request's last key is never used, whatever it
- * is, nor is a page that no query's window reaches, or its table entry.  A NaN among the cached values reaches the queries that see its key, and
- * no others; where the drafts of a tile of rows do not all see the key, in all
- * d elements of their O, not in its own alone.  Table entries outside the pool and lengths outside [0, max_seq_len] are
- * handled and reported as in fa_decode_paged.  page_size a multiple of 16, d = 64
- * or 128, 1 <= B <= 16384, Nq >= 1, Nq * Hq <= 65535.
+ * is, nor is a page that no query's window reaches, or its table entry.  A NaN
+ * among the cached values reaches the queries that see its key, and no others;
+ * where the drafts of a tile of rows do not all see the key, in all d elements
+ * of their O, not in its own alone.  A value scale that is NaN or infinite makes
+ * every value of its page a NaN.  Table entries outside the pool and lengths
+ * outside [0, max_seq_len] are handled and reported as in fa_decode_paged.
+ * page_size a multiple of 16, d = 64 or 128, 1 <= B <= 16384, Nq >= 1,
+ * Nq * Hq <= 65535.
  */
 fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
                         const float* v_scale, const int* block_table, const int* seq_lens, void* o, float* lse, int B,

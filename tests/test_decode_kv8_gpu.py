@@ -360,3 +360,26 @@ def test_what_the_workspace_held_does_not_matter():
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     q, k, v, table, lens = make([3000, 17], 1, 4, 2, 64, 16, seed=13)
     assert_close(o, lse, serving.decode_kv8(synth.to_f64(q), k[0], v[0], k[1], v[1], table, lens, -1, 64 ** -0.5))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Hq,d", [(2, 64), (4, 128), (8, 128), (16, 64), (16, 128)])
+def test_a_value_scale_that_is_no_number_stays_with_the_rows_that_see_its_page(Hq, d, value):
+    """A page that opens between two drafts, and one that ends between two drafts' windows."""
+    Nq, Hkv, n, window = 4, 2, [130, 257], 15
+    case = make(n, Nq, Hq, Hkv, d, 16, seed=Hq + d)
+    q, (kc, ks), (vc, vs), table, lens = case
+    ref = serving.decode_kv8(synth.to_f64(q), kc, vc, ks, vs, table, lens, window, d ** -0.5)
+    vs[table[0, 8], 0] = value        # keys 128, 129: the last two rows of request 0
+    vs[table[1, 14], 1] = value       # keys up to 239, windows from 238, 239, 240, 241: the first two of request 1
+    bad = np.zeros((2, Nq, Hq), bool)
+    bad[0, 2:, :Hq // 2] = True
+    bad[1, :2, Hq // 2:] = True
+    for shares in (0, 1):
+        o, lse = ops.decode_kv8(*dev(case), 257, window_left=window, num_shares=shares)
+        assert ops.device_error() == 0
+        o, lse = synth.to_f64(o), lse.cpu().numpy()
+        o_ref, l_ref, a, f = ref
+        assert np.all(np.isnan(o[bad]))
+        assert np.all(np.abs(o - o_ref)[~bad] <= (2.0 ** -8 * np.abs(o_ref) + 2.0 ** -11 * a + 2.0 ** -24 * f)[~bad])
+        assert np.all(np.abs(lse - l_ref) <= 2.0 ** -13)
