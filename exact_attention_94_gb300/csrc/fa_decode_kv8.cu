@@ -11,20 +11,24 @@
 //     S^T [128 keys x rows] = K8 Q^T        A = K tile, B = Q
 //     O^T [d x rows]       += V8^T P^T      A = V tile read MN-major, B = P
 // B is then what has to be made 8-bit, and it is made so without loss that
-// counts, as a sum of e4m3 numbers 16 times apart, each part a column of its
-// own:  q = 2^k (q1 + q2 / 16) exactly (a bf16 has 8 significant bits, an e4m3
-// 4) for what is within 2^13 of the row's largest, and to 2^-22 of the largest
-// below;  p = p1 + p2 / 16 + p3 / 256 to 2^-12 of itself, or, far below the
-// largest, to 2^-24 of that.  Page scales are one factor per key: k_scale
-// joins the score, v_scale the probability.  P lies by key (N-major), so a
-// thread, which has all rows of a key, stores 16 codes at a time.
+// counts, as a sum of 8-bit numbers, each part a column of its own:
+//     q = 2^k (q1 + q2 / 16), e4m3, exactly (a bf16 has 8 significant bits, an e4m3 4)
+//         for what is within 2^13 of the row's largest, to 2^-22 of the largest below
+//     p = p1 + p2 / 8 + p3 / 64 + p4 / 512, e5m2, exactly for p rounded to f16
+// p's rounding is what the products lose: 2^-12 of a probability, or 2^-37 of the
+// row's largest (its reference, below) where that is more.  (Three e4m3 parts 16 times
+// apart, which need fewer columns, hold 11 bits too, but nothing below 2^-24 of the
+// reference: of a first key 17 above 32767 others whose values alone count, nothing
+// was left of O = 0.00135.)  Page scales are one factor per key: k_scale joins the
+// score, v_scale the probability.  P lies by key (N-major), so a thread, which has
+// all rows of a key, stores 16 codes at a time.
 //
 // O stays in TMEM over the tiles.  It is made against a reference per row, in
-// log2 units of probability times value scale, at which p = 64: the reference
-// moves only when a p would pass e4m3's 448 (2^2.8 times the largest at the
+// log2 units of probability times value scale, at which p = 4096: the reference
+// moves only when a p would pass f16's 65504 (2^3.9 times the largest at the
 // reference's making), and O is rescaled then.  A tile costs a vote of the four
 // softmax warps on that, and no exchange of maxima.  The row sums share the
-// reference; fp32 holds them over the whole range of value scales.
+// reference.
 //
 // Work: the tiles of 128 keys of all (request, K/V head, row tile) units in
 // one list, dealt in equal shares to the CTAs (two or three per SM), which
@@ -69,9 +73,12 @@ namespace fa {
 
 namespace {
 
-constexpr float kAtRef = 64.f;       // p at the reference
-constexpr float kHeadroom = 2.8f;    // log2(448 / 64), rounded down
-constexpr float kLeastScale = -100.f;  // log2 of a value scale, from below: a page of zeros counts as one of 2^-100
+constexpr int kParts = 4;            // of a P
+constexpr float kAtRef = 4096.f;     // p at the reference
+constexpr float kHeadroom = 3.9f;    // log2(65504 / 4096), rounded down
+// log2 of a value scale, from below: a page of zeros counts as one of 2^-80 (with
+// 2^-100 the sums of a long row times kAtRef could overflow)
+constexpr float kLeastScale = -80.f;
 // What a unit's start and end cost, in tiles.  Against none at all: 16 requests
 // of 100 to 16384 tokens with 32 rows 82 -> 60 us, with 8 rows 53.3 -> 51.9; 128 up
 // to 2000, d = 64, 49 -> 37; a window of 4096 24.3 -> 20.6.  With 2 the 32 rows take
@@ -96,15 +103,17 @@ struct Layout {
   static constexpr uint32_t kSlot = 128u * D;                                // a tile of K or V
   static constexpr int kCtas = kv8_ctas_per_sm(RT);
   // Rings of K and of V tiles.  A V tile is held longer, until its product has
-  // been made, so where CTAs are two, V's ring has a tile more than K's.
+  // been made, so where CTAs are two, V's ring has a tile more than K's; but for 32
+  // rows of 128, whose P takes its place (four drafts of eight heads 62.6 us, and
+  // 59.7 with three V tiles and a P of three parts).
   static constexpr int kKs = 256 / D;
-  static constexpr int kVs = kCtas == 3 ? 256 / D : 384 / D;
+  static constexpr int kVs = kCtas == 3 || RT * D == 32 * 128 ? 256 / D : 384 / D;
   static constexpr int kSlots = kKs + kVs;
   static constexpr int kNS = 2 * RT < 16 ? 16 : 2 * RT;                      // columns of S
-  // Columns of P and O: three parts of RT, and what is left of a strip's 32,
-  // which holds anything and is not read.  P lies in strips of 32 columns, a
+  // Columns of P and O: four parts of RT, and what is left of a strip's 32 (for 4
+  // rows), which holds anything and is not read.  P lies in strips of 32 columns, a
   // key's 32 bytes after another's, so that its thread writes 16 at a time.
-  static constexpr int kNP = (3 * RT + 31) / 32 * 32;
+  static constexpr int kNP = (kParts * RT + 31) / 32 * 32;
   static constexpr uint32_t kStrip = kKv8Tile * 32u;
   static constexpr uint32_t kUsed = 2 * kNS + kNP;
   static constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;  // TMEM columns, two CTAs' 512 at most
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == SOFT + 1) {
     // ============================================================ products
-    constexpr uint32_t IDESC_S = idesc_e4m3(128, L::kNS), IDESC_O = idesc_e4m3(D, L::kNP, true, true);
+    constexpr uint32_t IDESC_S = idesc_e4m3(128, L::kNS), IDESC_O = idesc_e4m3_e5m2(D, L::kNP, true, true);
     const uint32_t qa = base + L::kQOff, pa = base + L::kPOff;
     const uint64_t qd = D == 128 ? smem_desc_sw128(qa, 16, 1024) : smem_desc_sw64(qa, 16, 512);
     const uint64_t pd = smem_desc_sw32(pa, L::kStrip, 256);
@@ -755,7 +764,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
               continue;
             }
           }
-          // ---- another moves them if one of its p passes what e4m3 holds
+          // ---- another moves them if one of its p passes what f16 holds
           float top = fmaxf(s[0], s[1]);
 #pragma unroll
           for (int r = 2; r < RG; r += 2) top = max3f(top, s[r], s[r + 1]);
@@ -802,7 +811,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int part = 0; part < 3; ++part) {
+          for (int part = 0; part < kParts; ++part) {
             uint32_t o[RG];
             tmem_load<RG>(tO + lane_sel + part * RT + g0, o);
             tmem_ld_wait();
@@ -819,26 +828,31 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 57));
           if (!ok) break;
         }
-        // The split works on p rounded to f16, by 2^-12 of itself at most: 11 bits,
-        // which the three parts hold exactly, and every difference of theirs too.
+        // p rounded to f16, by 2^-12 of itself at most (far below the reference, by 2^-25,
+        // 2^-37 of that).  The upper byte of an f16 is an e5m2, its first three
+        // significant bits; eight times the rest is an f16 again, exactly, and after
+        // four such bytes nothing is left of the eleven bits.
         const float vn = poison || !any ? 0.f : vs * kAtRef;
-        uint32_t code[3][RG / 4];
+        uint32_t code[kParts][RG / 4];
 #pragma unroll
-        for (int r = 0; r < RG; r += 2) {
-          const float p0 = ex2_sfu(s[r]), p1 = ex2_sfu(s[r + 1]);
-          l2[r / 2] = f2_add(l2[r / 2], f2_pack(p0, p1));
-          float y0, y1;
-          f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(vn, vn)), y0, y1);
-          __half2 x = pack_f16x2(y0, y1);
+        for (int r = 0; r < RG; r += 4) {
+          uint32_t x[2];
 #pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            const uint32_t two = pack_e4m3x2(x);
-            code[part][r / 4] = r & 2 ? code[part][r / 4] | two << 16 : two;
-            if (part < 2) x = __hmul2(__hsub2(x, unpack_e4m3x2_f16(two)), __float2half2_rn(16.f));
+          for (int e = 0; e < 2; ++e) {
+            const float p0 = ex2_sfu(s[r + 2 * e]), p1 = ex2_sfu(s[r + 2 * e + 1]);
+            l2[r / 2 + e] = f2_add(l2[r / 2 + e], f2_pack(p0, p1));
+            float y0, y1;
+            f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(vn, vn)), y0, y1);
+            x[e] = pack_f16x2(y0, y1);
+          }
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) {
+            code[part][r / 4] = __byte_perm(x[0], x[1], 0x7531);
+            if (part + 1 < kParts) x[0] = e5m2_rest8(x[0]), x[1] = e5m2_rest8(x[1]);
           }
         }
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
+        for (int part = 0; part < kParts; ++part) {
           const uint32_t* c = code[part];
           uint8_t* at = p_at(part * RT + g0);
           if constexpr (RG == 16)
@@ -898,10 +912,11 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       constexpr int OB = 4;  // rows at a time (8 are more code: 4096 requests up to 512 tokens 538 us, and 506)
 #pragma unroll 1
       for (int r0 = 0; r0 < mine; r0 += OB) {
-        uint32_t o1[OB], o2[OB], o3[OB];
+        uint32_t o1[OB], o2[OB], o3[OB], o4[OB];
         tmem_load<OB>(tO + lane_sel + g0 + r0, o1);
         tmem_load<OB>(tO + lane_sel + RT + g0 + r0, o2);
         tmem_load<OB>(tO + lane_sel + 2 * RT + g0 + r0, o3);
+        tmem_load<OB>(tO + lane_sel + 3 * RT + g0 + r0, o4);
         tmem_ld_wait();
 #pragma unroll
         for (int x0 = 0; x0 < OB; x0 += 4) {
@@ -913,7 +928,8 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           for (int z = 0; z < 4; ++z) {
             const int x = x0 + z;
             if (r0 + x < mine && has) {
-              const float y = fmaf(fmaf(__uint_as_float(o3[x]), 0.0625f, __uint_as_float(o2[x])), 0.0625f, __uint_as_float(o1[x]));
+              const float rest = fmaf(__uint_as_float(o4[x]), 0.125f, __uint_as_float(o3[x]));
+              const float y = fmaf(fmaf(rest, 0.125f, __uint_as_float(o2[x])), 0.125f, __uint_as_float(o1[x]));
               const float val = f[z] == 0.f ? 0.f : y * f[z];  // (0 * NaN would not be 0)
               if (whole)
                 static_cast<__nv_bfloat16*>(p.o)[(size_t)at[z] * D + e] = __float2bfloat16_rn(val);

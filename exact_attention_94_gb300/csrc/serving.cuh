@@ -147,6 +147,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
   return idesc_e4m3(M, N) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16);
 }
 
+// The same with A of e4m3 and B of e5m2.
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(int M, int N, bool a_mn, bool b_mn) {
+  return idesc_e4m3(M, N, a_mn, b_mn) | (1u << 10);
+}
+
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -179,21 +184,19 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t two) {
   return f;
 }
 
-// Two floats -> f16x2, e0 in the low half; f16x2 -> two e4m3 codes and back (exact).
-__device__ __forceinline__ __half2 pack_f16x2(float e0, float e1) {
+// Two floats -> f16x2, e0 in the low half.
+__device__ __forceinline__ uint32_t pack_f16x2(float e0, float e1) {
   uint32_t h;
   asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(e0), "f"(e1));
-  return *reinterpret_cast<__half2*>(&h);
+  return h;
 }
-__device__ __forceinline__ uint32_t pack_e4m3x2(__half2 h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t*>(&h)));
-  return r;
-}
-__device__ __forceinline__ __half2 unpack_e4m3x2_f16(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-  return *reinterpret_cast<__half2*>(&h);
+// Eight times what the upper bytes of two f16 (each an e5m2) leave of them, exact
+// (and below 2^16 for every f16 below 2^16).
+__device__ __forceinline__ uint32_t e5m2_rest8(uint32_t two) {
+  const uint32_t up = two & 0xff00ff00u;
+  const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&two), *reinterpret_cast<const __half2*>(&up));
+  const __half2 r = __hmul2(rest, __float2half2_rn(8.f));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // The largest of a warp's 32 values, in every lane.

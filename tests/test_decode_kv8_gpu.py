@@ -4,15 +4,13 @@ Tolerances, with A = sum_j P_j |v_j| and F = max_j (P_j vs_j) sum_j |v8_j|
 (element by element; v8 the codes' values, vs their scales):
   O   : half a bf16 step of the result, 2^-8 |O|, plus 2^-11 A + 2^-24 F for
         what comes before it.  The products are exact in the tensor cores'
-        inputs but for P vs, which is held as the sum of three e4m3 numbers 16
-        times apart, at a scale where a row's largest is 64 or more.  Each part
-        leaves half a step of itself, 2^-4, to the next: 2^-12 of P vs, as long
-        as the last part is in e4m3's normal range.  Below it the last part's
-        step is 2^-9, half of it over 256 is 2^-18, and against the largest's
-        64, 2^-24 of max_j (P_j vs_j), for each key's |v8|: that is 2^-24 F (it
-        shows where the row's loudest key is nearly zero in one channel, so that
-        A is small there).  Scores and sums are fp32: with |s| <= 2^6 a score is
-        off by a few 2^-24 * 2^6 = 2^-18, its exponential by as much of itself.
+        inputs but for P vs, which is rounded to f16, by 2^-12 of itself, at a
+        scale where a row's largest is 4096 or more (and held as the sum of four
+        e5m2 numbers, exactly).  Below f16's normal range half a step is 2^-25,
+        against the largest's 4096 2^-37 of max_j (P_j vs_j), for each key's |v8|:
+        that is 2^-37 F; the 2^-24 F here are from a form of three e4m3 parts.
+        Scores and sums are fp32: with |s| <= 2^6 a score is off by a few 2^-24 *
+        2^6 = 2^-18, its exponential by as much of itself.
   lse : 2^-13 absolute: the score error above, the fp32 logarithm and sum.
 """
 import math
@@ -383,3 +381,55 @@ def test_a_value_scale_that_is_no_number_stays_with_the_rows_that_see_its_page(H
         assert np.all(np.isnan(o[bad]))
         assert np.all(np.abs(o - o_ref)[~bad] <= (2.0 ** -8 * np.abs(o_ref) + 2.0 ** -11 * a + 2.0 ** -24 * f)[~bad])
         assert np.all(np.abs(lse - l_ref) <= 2.0 ** -13)
+
+
+@pytest.mark.parametrize("n", [1000, 32768, 300000])
+@pytest.mark.parametrize("Hq,d", [(1, 64), (8, 128), (16, 64), (32, 128)])
+@pytest.mark.parametrize("gap", [10.0, 17.0, 24.0])
+def test_many_quiet_keys_beside_a_loud_one(gap, Hq, d, n):
+    """A first key `gap` above all others, whose value is 0 where theirs is 1: O = m / (1 + m)
+    with m = (n - 1) e^-gap, in one piece.  Each probability is rounded to f16, by 2^-12
+    of itself, or, below 2^-26 of the largest, by 2^-37 of that."""
+    P, blocks = 128, -(-n // 128)
+    kc = torch.zeros((2, 1, P, d), dtype=torch.uint8, device="cuda")
+    vc = torch.full_like(kc, 0x38)                   # 1
+    kc[1, 0, 0, 0], vc[1, 0, 0] = 0x38, 0
+    ones = torch.ones((2, 1), device="cuda")
+    table = torch.zeros((1, blocks), dtype=torch.int32, device="cuda")
+    table[0, 0] = 1
+    q = torch.zeros((1, 1, Hq, d), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    o, lse = ops.decode_kv8(q, kc, vc, ones, ones, table, cu([n], torch.int32), n, num_shares=1, scale=gap)
+    assert ops.device_error() == 0
+    m = (n - 1) * math.exp(-gap)
+    want = m / (1 + m)
+    tol = (2.0 ** -8 + 2.0 ** -11) * want + n * 2.0 ** -37
+    assert np.all(np.abs(synth.to_f64(o) - want) <= tol), (float(o.float().max()), want)
+    assert np.all(np.abs(lse.cpu().numpy() - gap - math.log1p(m)) <= 2.0 ** -13)
+
+
+@pytest.mark.parametrize("Hq,d", [(2, 64), (8, 128), (16, 128), (32, 64)])
+def test_scores_that_fall_and_rise(Hq, d):
+    """Keys whose scores fall tile by tile, jump, and fall again; the loudest tiles' values are zero in the
+    first half of the channels, so that the quiet tiles' weigh alone there."""
+    P, tiles, Hkv = 128, 20, 1
+    rng = np.random.default_rng(Hq)
+    for step in (2.0, 7.0, 18.0):                    # log2 units a tile
+        level = -step * (np.arange(tiles) % 7) + 3.0 * (np.arange(tiles) // 7)
+        q, (kc, ks), (vc, vs), table, lens = make([tiles * P - 5], 1, Hq, Hkv, d, P, seed=Hq, garbage=False)
+        q = torch.zeros_like(q)
+        q[..., 0] = 1
+        q[0, 0, :, 1] = torch.linspace(0.25, 1.0, Hq)    # rows differ by how far their keys spread
+        for t in range(tiles):
+            pg = table[0, t]
+            kc[pg], ks[pg] = 0, 1.0
+            x = np.zeros((P, d))
+            x[:, 0] = abs(level[t]) if level[t] else 0
+            x[:, 1] = rng.uniform(-2, 2, P)
+            kc[pg, 0] = serving._encode(x * (np.arange(d) < 2) * np.where(np.arange(d) == 0, np.sign(level[t]), 1))
+            if t % 7 == 0:
+                vc[pg, 0, :, :d // 2] = 0
+            vs[pg] = 2.0 ** rng.integers(-4, 4)
+        case = (q, (kc, ks), (vc, vs), table, lens)
+        for shares in (1, 2):
+            check(case, shares=shares, scale=math.log(2))
