@@ -28,7 +28,9 @@
 // moves only when a p would pass f16's 65504 (2^3.9 times the largest at the
 // reference's making), and O is rescaled then.  A tile costs a vote of the four
 // softmax warps on that, and no exchange of maxima.  The row sums share the
-// reference.
+// reference, so they are a row's mass divided by the value scale of its loudest
+// key: fp32 holds them for value scales of 2^-80 to 2^80, and beyond drops keys
+// (with scales of 2^L what is below 2^(L - 126) of the largest).
 //
 // Work: the tiles of 128 keys of all (request, K/V head, row tile) units in
 // one list, dealt in equal shares to the CTAs (two or three per SM), which

@@ -433,3 +433,13 @@ def test_scores_that_fall_and_rise(Hq, d):
         case = (q, (kc, ks), (vc, vs), table, lens)
         for shares in (1, 2):
             check(case, shares=shares, scale=math.log(2))
+
+
+@pytest.mark.parametrize("up", [84, 40, -40, -70])
+@pytest.mark.parametrize("Hq,d", [(2, 64), (16, 128), (64, 128)])
+def test_value_scales_at_both_ends_of_their_range(Hq, d, up):
+    """Scales (2^-10 to 2^-4 before) up to 2^80 and down to 2^-80, with scores of a hundred and more."""
+    q, k, (vc, vs), table, lens = make([300, 40], 1, Hq, 2, d, 16, seed=abs(up))
+    assert 2.0 ** -80 <= np.nanmin(vs) * 2.0 ** up and np.nanmax(vs) * 2.0 ** up <= 2.0 ** 80
+    for scale in (30.0 / 8, d ** -0.5, 0.001):
+        check((q, k, (vc, (vs * 2.0 ** up).astype(np.float32)), table, lens), scale=scale)
