@@ -754,9 +754,10 @@ class RopePlan:
     """Which axis each pair of a head turns with, and how fast; kept by the
     caller.  ``axis``: d / 2 integers, -1 for a pair that is copied; ``inv_freq``:
     d / 2 numbers, radians per position; ``neighbours``: pairs (2p, 2p + 1)
-    instead of (p, p + d / 2)."""
+    instead of (p, p + d / 2); ``n_axes``: axes that positions have, 1 to 4, those
+    that some pair turns with unless given."""
 
-    def __init__(self, d: int, axis, inv_freq, neighbours: bool = False):
+    def __init__(self, d: int, axis, inv_freq, neighbours: bool = False, n_axes: Optional[int] = None):
         axis, inv_freq = [int(a) for a in axis], [float(f) for f in inv_freq]
         if d not in (64, 128):
             raise _lib.FaError(_lib.FA_ERR_UNSUPPORTED, "RopePlan")
@@ -764,7 +765,10 @@ class RopePlan:
             raise ValueError(f"axis and inv_freq must have {d // 2} entries")
         if any(not -1 <= a < 4 for a in axis) or not all(math.isfinite(f) for f in inv_freq):
             raise ValueError("axis entries must be -1 .. 3 and inv_freq finite")
-        self.d, self.n_axes = d, max(1, max(axis) + 1)
+        self.d, self.used_axes = d, max(1, max(axis) + 1)
+        self.n_axes = self.used_axes if n_axes is None else int(n_axes)
+        if not self.used_axes <= self.n_axes <= 4:
+            raise ValueError(f"n_axes must be {self.used_axes} (the axes in use) to 4")
         self.struct = _lib.RopePlanStruct(self.n_axes, int(bool(neighbours)))
         self.struct.axis[:d // 2] = axis
         self.struct.inv_freq[:d // 2] = inv_freq
@@ -772,8 +776,8 @@ class RopePlan:
 
 
 def rope_plan(d: int, sections, theta: float = 10000.0, per_axis: bool = False, neighbours: bool = False) -> RopePlan:
-    """The usual plans.  ``sections``: pairs of each axis, in order; what they
-    leave of the d / 2 pairs is copied.  Frequencies are theta^(-p / (d / 2)) of
+    """The usual plans.  ``sections``: pairs of each axis, in order, some of them
+    none if need be; what they leave of the d / 2 pairs is copied.  Frequencies are theta^(-p / (d / 2)) of
     pair p (one ladder over the head, shared by the axes), or, per_axis, a
     ladder for each axis: theta^(-j / n) of pair j of its n."""
     sections = [int(n) for n in sections]
@@ -785,7 +789,7 @@ def rope_plan(d: int, sections, theta: float = 10000.0, per_axis: bool = False, 
     else:
         freq = [theta ** (-p / (d // 2)) for p in range(len(axis))]
     rest = d // 2 - len(axis)
-    return RopePlan(d, axis + [-1] * rest, freq + [0.0] * rest, neighbours)
+    return RopePlan(d, axis + [-1] * rest, freq + [0.0] * rest, neighbours, len(sections))
 
 
 def _rope_side(name, t, o, plan, dev):
@@ -814,7 +818,10 @@ def _rope(q, k, positions, plan, inverse, out, dev, raw):
     if nq is not None and nk is not None and nq != nk:
         raise ValueError("q and k must have the same rows")
     rows = nq if nq is not None else nk
-    _check("positions", positions, torch.int32, dev, (plan.n_axes, rows))
+    axes = plan.n_axes
+    if plan.used_axes < axes and isinstance(positions, torch.Tensor) and positions.dim() == 2:
+        axes = min(max(positions.shape[0], plan.used_axes), axes)  # (last axes that no pair turns with may be left out)
+    _check("positions", positions, torch.int32, dev, (axes, rows))
     st = lib().fa_rope_axes(pq, pk, poq, pok, positions.data_ptr(), plan._ref, rows, Hq, Hkv, plan.d, qs, ks, qos, kos,
                             inverse, raw)
     if st:
@@ -825,7 +832,8 @@ def _rope(q, k, positions, plan, inverse, out, dev, raw):
 @_on_call_stream
 def rope_axes(q, k, positions, plan: RopePlan, out=None, *, dev, raw):
     """Rotates q [..., Hq, d] and k [..., Hkv, d] (either may be None) by their
-    rows' positions, int32 [plan.n_axes, rows].  Rows may lie a stride apart.
+    rows' positions, int32 [plan.n_axes, rows]; last axes that no pair turns with
+    may be left out of them.  Rows may lie a stride apart.
     Returns (q, k) rotated, in ``out`` = (q_out, k_out) when given (q_out may be q)."""
     return _rope(q, k, positions, plan, 0, out, dev, raw)
 

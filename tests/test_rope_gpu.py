@@ -138,3 +138,21 @@ def test_a_gradient_by_differences():
     a, b = (synth.to_f64(y) * synth.to_f64(g)).sum((1, 2)), (synth.to_f64(x) * synth.to_f64(dx)).sum((1, 2))
     size = (np.abs(synth.to_f64(y) * synth.to_f64(g))).sum((1, 2)) + (np.abs(synth.to_f64(x) * synth.to_f64(dx))).sum((1, 2))
     assert np.all(np.abs(a - b) <= 2.0 ** -8 * 1.01 * size)
+
+
+@pytest.mark.parametrize("sections", [[32, 0, 0], [16, 16, 0], [0, 20, 0], [0, 0, 0]])
+def test_axes_without_pairs(sections):
+    """Positions have a row for each section, empty or not; the last empty ones' may be left out."""
+    d, T = 64, 50
+    plan = ops.rope_plan(d, sections)
+    axis, freq = list(plan.struct.axis[:d // 2]), list(plan.struct.inv_freq[:d // 2])
+    x = bf((T, 3, d), 11)
+    pos = np.random.default_rng(1).integers(0, 5000, (3, T))
+    p = torch.tensor(pos, dtype=torch.int32).cuda()
+    for n in range(plan.used_axes, 4):
+        for f, inverse in ((ops.rope_axes, False), (ops.rope_axes_bwd, True)):
+            y, _ = f(x, None, p[:n].contiguous(), plan)
+            check(y, x, pos, axis, freq, False, inverse)
+    for bad in (p[:plan.used_axes - 1].contiguous(), torch.cat([p, p[:1]]), p[0].contiguous()):
+        with pytest.raises(ValueError):
+            ops.rope_axes(x, None, bad, plan)

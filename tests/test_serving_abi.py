@@ -151,3 +151,16 @@ def test_the_workspace_query_refuses_what_the_call_refuses(lib, bad):
     assert lib.fa_decode_kv8_workspace_bytes(*a.values()) == 0
     sizes = [a[x] for x in ("B", "Nq", "Hq", "Hkv", "d")]
     assert lib.fa_decode_kv8(*(A,) * 9, *sizes, 16, 8, 4, 64, -1, a["shares"], A, 0.1, NUL) in (INV, UNS)
+
+
+def test_axes_without_pairs():
+    """A model with three axes may give a head's pairs to fewer; its positions still have three."""
+    for sections, n, used in (([32, 0, 0], 3, 1), ([16, 16, 0], 3, 2), ([0, 0, 8], 3, 3), ([0, 0], 2, 1), ([32], 1, 1),
+                              ([8, 0, 8, 0], 4, 3)):
+        p = ops.rope_plan(64, sections)
+        assert p.n_axes == p.struct.n_axes == n and p.used_axes == used, sections
+    assert ops.RopePlan(64, [0] * 32, [1.0] * 32).n_axes == 1
+    assert ops.RopePlan(64, [0] * 32, [1.0] * 32, n_axes=4).n_axes == 4
+    for axis, n in ((2, 2), (0, 0), (0, 5), (0, -1)):
+        with pytest.raises(ValueError):
+            ops.RopePlan(64, [axis] * 32, [1.0] * 32, n_axes=n)
