@@ -443,3 +443,23 @@ def test_value_scales_at_both_ends_of_their_range(Hq, d, up):
     assert 2.0 ** -80 <= np.nanmin(vs) * 2.0 ** up and np.nanmax(vs) * 2.0 ** up <= 2.0 ** 80
     for scale in (30.0 / 8, d ** -0.5, 0.001):
         check((q, k, (vc, (vs * 2.0 ** up).astype(np.float32)), table, lens), scale=scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq,Hq,Hkv", [(1, 4, 2), (1, 16, 2), (1, 32, 2), (2, 16, 2), (4, 16, 2), (1, 12, 1)])
+def test_more_tiles_than_ctas(Nq, Hq, Hkv, d):
+    """Where the tiles outnumber the CTAs that run at once, units weigh more than their
+    tiles when work is dealt: for every tile of rows, of 4 to 32, with and without a window."""
+    B = 240 if Hkv > 1 else 320
+    rng = np.random.default_rng(Hq + d)
+    lens = [int(n) for n in rng.integers(0, 300, B) * (rng.random(B) < 0.9)]
+    tiles = B * Hkv * -(-Nq * Hq // Hkv // 32) * -(-max(lens) // 128)
+    assert tiles > 2 * 3 * 152
+    case = make(lens, Nq, Hq, Hkv, d, 32, seed=B)
+    q, (kc, ks), (vc, vs), table, _ = case
+    for window in (-1, 150):
+        ref = serving.decode_kv8(synth.to_f64(q), kc, vc, ks, vs, table, np.array(lens), window, d ** -0.5)
+        for shares in (0, 101):
+            o, lse = ops.decode_kv8(*dev(case), max(lens), window_left=window, num_shares=shares)
+            assert_close(o, lse, ref)
+    assert ops.device_error() == 0

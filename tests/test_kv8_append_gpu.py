@@ -158,3 +158,24 @@ def test_refusals():
                 lambda: ops.kv8_append(x, x, c, c, s.half(), s, i, i), lambda: ops.kv8_append(x, x, c, c, s, s, i.long(), i)):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("n,Hkv,d,P", [(1500, 8, 64, 16), (3001, 8, 64, 32), (9011, 8, 64, 32), (2300, 32, 128, 16),
+                                       (700, 32, 64, 48)])
+def test_from_few_rows_to_many(n, Hkv, d, P):
+    """How many warps share 32 rows goes by rows times heads: 5, 2, 1, 1 and 3 in these cases.  Prompts and single tokens in one call, that begin anywhere in their pages, padding between them."""
+    rng = np.random.default_rng(n)
+    page, slot, used = [], [], 0
+    order = rng.permutation(n)          # (more pages than are used)
+    while len(page) < n:
+        new, first = (1 if rng.random() < 0.4 else int(rng.integers(2, 150))), int(rng.integers(0, P))
+        for t in range(first, first + min(new, n - len(page))):
+            page.append(int(order[used + t // P]))
+            slot.append(t % P)
+        used += (first + new - 1) // P + 1
+        if rng.random() < 0.1:
+            page, slot = page + [-1] * 3, slot + [-1] * 3
+    pages = int(max(page)) + 1
+    amp = 2.0 ** rng.integers(-6, 6, len(page))
+    run(rng, pages, Hkv, P, d, page, slot, amp=amp, stride=8)
+    assert ops.device_error() == 0
