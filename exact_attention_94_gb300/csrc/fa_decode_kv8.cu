@@ -14,19 +14,20 @@
 // counts, as a sum of 8-bit numbers, each part a column of its own:
 //     q = 2^k (q1 + q2 / 16), e4m3, exactly (a bf16 has 8 significant bits, an e4m3 4)
 //         for what is within 2^13 of the row's largest, to 2^-22 of the largest below
-//     p = p1 + p2 / 8 + p3 / 64 + p4 / 512, e5m2, exactly for p rounded to f16
-// p's rounding is what the products lose: 2^-12 of a probability, or 2^-37 of the
+//     p = p1 + p2 / 8 + p3 / 128, e5m2, exactly for p rounded to f16
+// p's rounding is what the products lose: 2^-11 of a probability, or 2^-35 of the
 // row's largest (its reference, below) where that is more.  (Three e4m3 parts 16 times
-// apart, which need fewer columns, hold 11 bits too, but nothing below 2^-24 of the
-// reference: of a first key 17 above 32767 others whose values alone count, nothing
-// was left of O = 0.00135.)  Page scales are one factor per key: k_scale joins the
-// score, v_scale the probability.  P lies by key (N-major), so a thread, which has
-// all rows of a key, stores 16 codes at a time.
+// apart hold the f16 too, but nothing below 2^-24 of the reference: of a first key
+// 17 above 32767 others whose values alone count, nothing was left of O = 0.00135.
+// Four e5m2 parts cut off, not rounded, need a fourth of P's columns more.)  Page
+// scales are one factor per key: k_scale joins the score, v_scale the probability.
+// P lies by key (N-major), so a thread, which has all rows of a key, stores 16 codes
+// at a time.
 //
 // O stays in TMEM over the tiles.  It is made against a reference per row, in
 // log2 units of probability times value scale, at which p = 4096: the reference
-// moves only when a p would pass f16's 65504 (2^3.9 times the largest at the
-// reference's making), and O is rescaled then.  A tile costs a vote of the four
+// moves only when a p would pass what rounds to e5m2's largest (2^3.9 times the
+// largest at the reference's making), and O is rescaled then.  A tile costs a vote of the four
 // softmax warps on that, and no exchange of maxima.  The row sums share the
 // reference, so they are a row's mass divided by the value scale of its loudest
 // key: fp32 holds them for value scales of 2^-80 to 2^80, and beyond drops keys
@@ -75,9 +76,9 @@ namespace fa {
 
 namespace {
 
-constexpr int kParts = 4;            // of a P
+constexpr int kParts = 3;            // of a P
 constexpr float kAtRef = 4096.f;     // p at the reference
-constexpr float kHeadroom = 3.9f;    // log2(65504 / 4096), rounded down
+constexpr float kHeadroom = 3.9f;    // log2(61440 / 4096), rounded down: from 61440 on p1 would be infinite
 // log2 of a value scale, from below: a page of zeros counts as one of 2^-80 (with
 // 2^-100 the sums of a long row times kAtRef could overflow)
 constexpr float kLeastScale = -80.f;
@@ -105,15 +106,14 @@ struct Layout {
   static constexpr uint32_t kSlot = 128u * D;                                // a tile of K or V
   static constexpr int kCtas = kv8_ctas_per_sm(RT);
   // Rings of K and of V tiles.  A V tile is held longer, until its product has
-  // been made, so where CTAs are two, V's ring has a tile more than K's; but for 32
-  // rows of 128, whose P takes its place (four drafts of eight heads 62.6 us, and
-  // 59.7 with three V tiles and a P of three parts).
+  // been made, so where CTAs are two, V's ring has a tile more than K's (with as
+  // many, four drafts of eight heads 62.1 us, not 59.4).
   static constexpr int kKs = 256 / D;
-  static constexpr int kVs = kCtas == 3 || RT * D == 32 * 128 ? 256 / D : 384 / D;
+  static constexpr int kVs = kCtas == 3 ? 256 / D : 384 / D;
   static constexpr int kSlots = kKs + kVs;
   static constexpr int kNS = 2 * RT < 16 ? 16 : 2 * RT;                      // columns of S
-  // Columns of P and O: four parts of RT, and what is left of a strip's 32 (for 4
-  // rows), which holds anything and is not read.  P lies in strips of 32 columns, a
+  // Columns of P and O: three parts of RT, and what is left of a strip's 32,
+  // which holds anything and is not read.  P lies in strips of 32 columns, a
   // key's 32 bytes after another's, so that its thread writes 16 at a time.
   static constexpr int kNP = (kParts * RT + 31) / 32 * 32;
   static constexpr uint32_t kStrip = kKv8Tile * 32u;
@@ -687,10 +687,10 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
         // A key's value row may hold NaN, and 0 * NaN is not 0.  Where no row sees
         // the key (it may be anything behind the last or before the window), its
         // values count as zero.
-        // Where some rows do and some don't (drafts), a row with a NaN, or of a page
-        // whose scale is no number, counts as zero too, and as NaN to the rows that see
-        // it: in all their elements.
-        bool poison = false, any = true, all = true;
+        // Where some rows do and some don't (drafts), a row with a NaN counts as zero
+        // too, and as NaN to the rows that see it: in all their elements.  So does every
+        // row of a page whose scale is no number.
+        bool poison = odd_scale, any = true, all = true;
         if (partial) {
           any = j <= pos_last && (p.win_left < 0 || j >= pos_first - p.win_left);
           all = j <= pos_first && (p.win_left < 0 || j >= pos_last - p.win_left);
@@ -704,8 +704,9 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
               nan |= __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
                      __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
             }
-            poison = nan != 0 || odd_scale;
+            poison |= nan != 0;
           }
+          poison &= any;
           if (GROUPS > 1) {  // (one group's row is the other's: both have read it before either writes)
             // every softmax warp passes here: the tile is partial for all of them
             ok = both();
@@ -766,7 +767,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
               continue;
             }
           }
-          // ---- another moves them if one of its p passes what f16 holds
+          // ---- another moves them if one of its p passes what e5m2 holds
           float top = fmaxf(s[0], s[1]);
 #pragma unroll
           for (int r = 2; r < RG; r += 2) top = max3f(top, s[r], s[r + 1]);
@@ -830,10 +831,11 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           ok = __all_sync(0xffffffffu, mbar_wait(OF, (it - 1) & 1, w, 57));
           if (!ok) break;
         }
-        // p rounded to f16, by 2^-12 of itself at most (far below the reference, by 2^-25,
-        // 2^-37 of that).  The upper byte of an f16 is an e5m2, its first three
-        // significant bits; eight times the rest is an f16 again, exactly, and after
-        // four such bytes nothing is left of the eleven bits.
+        // p rounded to f16, by 2^-11 of itself at most.  An e5m2 is an f16's upper byte:
+        // the first part is that byte, rounded, which leaves 2^-3 at most, in eight
+        // bits; the second leaves 2^-7, a multiple of 2^-10 that the third is exactly.
+        // (Below 2^-13 the parts' own steps end; with the f16's they lose 2^-23 at most,
+        // 2^-35 of the reference.)
         const float vn = poison || !any ? 0.f : vs * kAtRef;
         uint32_t code[kParts][RG / 4];
 #pragma unroll
@@ -849,8 +851,12 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           }
 #pragma unroll
           for (int part = 0; part < kParts; ++part) {
-            code[part][r / 4] = __byte_perm(x[0], x[1], 0x7531);
-            if (part + 1 < kParts) x[0] = e5m2_rest8(x[0]), x[1] = e5m2_rest8(x[1]);
+            const uint32_t up[2] = {e5m2_round(x[0]), e5m2_round(x[1])};
+            code[part][r / 4] = __byte_perm(up[0], up[1], 0x7531);
+            if (part + 1 < kParts) {
+              const float more = part == 0 ? 8.f : 16.f;
+              x[0] = e5m2_rest(x[0], up[0], more), x[1] = e5m2_rest(x[1], up[1], more);
+            }
           }
         }
 #pragma unroll
@@ -914,11 +920,10 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
       constexpr int OB = 4;  // rows at a time (8 are more code: 4096 requests up to 512 tokens 538 us, and 506)
 #pragma unroll 1
       for (int r0 = 0; r0 < mine; r0 += OB) {
-        uint32_t o1[OB], o2[OB], o3[OB], o4[OB];
+        uint32_t o1[OB], o2[OB], o3[OB];
         tmem_load<OB>(tO + lane_sel + g0 + r0, o1);
         tmem_load<OB>(tO + lane_sel + RT + g0 + r0, o2);
         tmem_load<OB>(tO + lane_sel + 2 * RT + g0 + r0, o3);
-        tmem_load<OB>(tO + lane_sel + 3 * RT + g0 + r0, o4);
         tmem_ld_wait();
 #pragma unroll
         for (int x0 = 0; x0 < OB; x0 += 4) {
@@ -930,8 +935,7 @@ __global__ void __launch_bounds__(Layout<D, RT>::kThreads, Layout<D, RT>::kCtas)
           for (int z = 0; z < 4; ++z) {
             const int x = x0 + z;
             if (r0 + x < mine && has) {
-              const float rest = fmaf(__uint_as_float(o4[x]), 0.125f, __uint_as_float(o3[x]));
-              const float y = fmaf(fmaf(rest, 0.125f, __uint_as_float(o2[x])), 0.125f, __uint_as_float(o1[x]));
+              const float y = fmaf(fmaf(__uint_as_float(o3[x]), 0.0625f, __uint_as_float(o2[x])), 0.125f, __uint_as_float(o1[x]));
               const float val = f[z] == 0.f ? 0.f : y * f[z];  // (0 * NaN would not be 0)
               if (whole)
                 static_cast<__nv_bfloat16*>(p.o)[(size_t)at[z] * D + e] = __float2bfloat16_rn(val);

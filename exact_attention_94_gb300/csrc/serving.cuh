@@ -190,12 +190,15 @@ __device__ __forceinline__ uint32_t pack_f16x2(float e0, float e1) {
   asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(e0), "f"(e1));
   return h;
 }
-// Eight times what the upper bytes of two f16 (each an e5m2) leave of them, exact
-// (and below 2^16 for every f16 below 2^16).
-__device__ __forceinline__ uint32_t e5m2_rest8(uint32_t two) {
-  const uint32_t up = two & 0xff00ff00u;
+// Two f16 whose upper bytes are the nearest e5m2 to the given ones, below 61440 in
+// magnitude (a tie goes up; a NaN does not stay one, but 0x7fff, as conversions
+// and arithmetic make it, carries nothing into its neighbour); and `more` times what
+// those bytes leave, exact where it is no subnormal.
+__device__ __forceinline__ uint32_t e5m2_round(uint32_t two) { return two + 0x00800080u; }
+__device__ __forceinline__ uint32_t e5m2_rest(uint32_t two, uint32_t rounded, float more) {
+  const uint32_t up = rounded & 0xff00ff00u;
   const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&two), *reinterpret_cast<const __half2*>(&up));
-  const __half2 r = __hmul2(rest, __float2half2_rn(8.f));
+  const __half2 r = __hmul2(rest, __float2half2_rn(more));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 

@@ -569,10 +569,10 @@ fa_status fa_kv8_append(const void* k_new, const void* v_new, void* k_codes, voi
  * every value of its page a NaN.  Table entries outside the pool and lengths
  * outside [0, max_seq_len] are handled and reported as in fa_decode_paged.
  * Scores, their sums and O are held in fp32; a probability (times its value
- * scale) is rounded by 2^-12 of itself, or by 2^-37 of the row's largest where
+ * scale) is rounded by 2^-11 of itself, or by 2^-35 of the row's largest where
  * that is more, before it meets its values.  That holds for value scales of
  * 2^-80 to 2^80 (and 0); where a row's loudest pages have scales of 2^L beyond
- * them, keys below 2^(L - 126) or 2^(-117 - L) of the largest drop out.
+ * them, keys below 2^(L - 126) or 2^(-115 - L) of the largest drop out.
  * page_size a multiple of 16, d = 64 or 128, 1 <= B <= 16384, Nq >= 1,
  * Nq * Hq <= 65535.
  */
