@@ -723,7 +723,9 @@ def page_plan(ctx_lens, new_lens, free_pages, free_count, block_table, page_size
     """Plans a step on the GPU.  ctx_lens, new_lens int32 [B]: tokens each
     request holds and gets; free_pages int32 [num_pages] and free_count int32
     [1]: the stack of free pages; block_table int32 [B, max_blocks], whose new
-    entries are written.  max_tokens: rows of the outputs, at least the step's
+    entries are written.  No two requests may share a partly filled page (plan
+    forks with PagePool); a finished request's pages go back by writing them
+    behind the stack's top and raising free_count.  max_tokens: rows of the outputs, at least the step's
     tokens.  ``out``: a PagePlan to write into; its seq_lens may be ctx_lens and
     its free_count the given one, which advances them in place."""
     i32 = torch.int32

@@ -439,7 +439,11 @@ fa_status fa_decode_paged_window(const void* q, const void* k_pages, const void*
 /*
  * Plans a step on the GPU: what fa_pool_reserve_append does on the host for
  * one token a sequence, for any number of tokens a request and without the
- * host knowing the lengths.  Request b has ctx_lens[b] tokens in the pages of
+ * host knowing the lengths, but for pages that belong to one request alone.  (A
+ * plan counts no references and copies nothing: two requests whose tables
+ * share a partly filled last page would both be sent to its next slots.  Shared
+ * full pages may stand in the tables.  What fa_pool_fork shares is
+ * fa_pool_reserve_append's to plan.)  Request b has ctx_lens[b] tokens in the pages of
  * its block-table row and gets new_lens[b] more (0 allowed).  It needs
  *     ceil((ctx + new) / page_size) - ceil(ctx / page_size)
  * new pages; they come off the top of the free stack, for request 0 first and
@@ -447,7 +451,9 @@ fa_status fa_decode_paged_window(const void* q, const void* k_pages, const void*
  * free_pages[free_count - 1 - j].
  *   ctx_lens, new_lens : int32 [B], device
  *   free_pages  : int32 [num_pages], device; entries 0 .. *free_count - 1 are
- *                 free pages (the stack is only read: popping is free_count_out)
+ *                 free pages (the stack is only read: popping is free_count_out).
+ *                 A finished request gives its pages back when their numbers are
+ *                 written to free_pages[*free_count ...] and *free_count is raised
  *   free_count  : int32 [1], device
  *   block_table : int32 [B, max_blocks], device; the new pages' entries are
  *                 written, all others left as they are

@@ -182,3 +182,37 @@ def test_threads_with_batches_of_different_sizes():
         t.join()
     assert not failures, (len(failures), failures[0])
     assert ops.device_error() == 0
+
+
+def test_finished_requests_give_their_pages_back():
+    """Requests come and go in their rows of the table, without the host reading a length: a finished one's pages
+    are written behind the stack's top."""
+    B, P, pages, blocks, cap = 5, 8, 48, 9, 64
+    rng = np.random.default_rng(21)
+    free, count, lens, table = i32(rng.permutation(pages)), i32([pages]), i32([0] * B), i32(np.zeros((B, blocks)))
+    cols = torch.arange(blocks, device="cuda")
+    w_free, w_lens, w_table = free.tolist(), [0] * B, np.zeros((B, blocks), np.int64)
+    w_count = pages
+    for step in range(30):
+        n = rng.integers(0, 12, B).tolist()
+        for b in range(B):  # a row whose next tokens do not fit ends, and starts anew
+            if w_lens[b] + n[b] > blocks * P or rng.random() < 0.1:
+                held = (lens[b] + P - 1) // P
+                at = torch.where(cols < held, count + cols, pages + cols)
+                spare = torch.cat([free, torch.zeros(blocks, dtype=torch.int32, device="cuda")])
+                spare[torch.where(at < pages, at, pages + cols).long()] = table[b]
+                free.copy_(spare[:pages])
+                count += held
+                lens[b] = 0
+                w = -(-w_lens[b] // P)
+                w_free[w_count:w_count + w] = w_table[b, :w].tolist()
+                w_count += w
+                w_lens[b] = 0
+        p = ops.page_plan(lens, i32(n), free, count, table, P, cap)
+        want = serving.page_plan(w_lens, n, w_free, w_count, w_table, P, cap)
+        check(p, want, table)
+        lens, count = p.seq_lens.clone(), p.free_count.clone()
+        w_lens, w_count, w_table = list(want[0]), want[5], want[6]
+        live = [int(x) for b in range(B) for x in w_table[b, :-(-w_lens[b] // P)]]
+        assert sorted(live + w_free[:w_count]) == list(range(pages))  # every page is held once or free
+    assert ops.device_error() == 0
