@@ -14,8 +14,8 @@
 // One warp takes a run's rows of one K/V head, for K or for V: the largest
 // magnitude first, then the codes.  Bound by HBM for prompts (2 bytes read and
 // 1 written per element), by latency for a step of single tokens.  Measured, 8
-// K/V heads of 128: 9 prompts of 1 to 2047 tokens into pages of 32 25 us, 4.4 TB/s (three
-// times as many 62 us, 5.5 TB/s); 64 requests of a token 3.3 us, a launch.
+// K/V heads of 128: 9 prompts of 2047 tokens each into pages of 32 25 us, 4.4 TB/s (27 of
+// them 62 us, 5.5 TB/s); 64 requests of a token 3.3 us, a launch.
 #include "serving.cuh"
 
 namespace fa {
@@ -23,7 +23,7 @@ namespace fa {
 namespace {
 
 constexpr int kAppendWarps = 4;
-constexpr int kAppendBlocks = 7;  // CTAs per SM: all the registers allow (9 prompts: 26.1 us, and 27.8 with four)
+constexpr int kAppendBlocks = 7;  // CTAs per SM: all the registers allow (9 prompts of 2047: 26.1 us, and 27.8 with four)
 constexpr int kHeld = 8;  // vectors of a run that a lane holds in registers (with 4, 28.9 us; with 16, four CTAs, 25.8)
 
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
@@ -218,7 +218,7 @@ static cudaError_t launch_kv8_append_t(Kv8AppendParams& p, cudaStream_t stream) 
   // tokens take 3.5 us so and 36 with split 1; 9 prompts of 1024 tokens 16.4, and 55
   // with split 32.
   const long long tiles = ((long long)p.n + 31) / 32 * 2 * p.Hkv;
-  const long long split = 152ll * kAppendBlocks * kAppendWarps / tiles;
+  const long long split = (long long)kSms * kAppendBlocks * kAppendWarps / tiles;
   p.split = (int)(split < 1 ? 1 : split > 32 ? 32 : split);
   const long long blocks = (tiles * p.split + kAppendWarps - 1) / kAppendWarps;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;

@@ -197,7 +197,7 @@ cudaError_t launch_page_plan(PlanParams& p, cudaStream_t stream) {
   }
   const int ctas = (p.max_tokens - 1) / 1024 + 1;  // (1 for no rows)
   p.totals_later = ctas > 1 && (p.seq_lens == p.ctx_lens || p.free_count_out == p.free_count);
-  const cudaError_t e = launch_page_plan_t<1024>(p, ctas < 304 ? ctas : 304, stream);
+  const cudaError_t e = launch_page_plan_t<1024>(p, ctas < 2 * kSms ? ctas : 2 * kSms, stream);
   if (e != cudaSuccess || !p.totals_later) return e;
   fa_page_plan_totals_kernel<<<1, 1024, 0, stream>>>(p);
   return cudaGetLastError();

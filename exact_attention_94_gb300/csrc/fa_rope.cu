@@ -12,7 +12,8 @@
 // Bound by HBM: each element of q and k is read and written once.  A thread
 // holds 8 pairs (two 16-byte vectors) of a token, takes their sines once and
 // rotates heads_per_thread heads with them, four at a time: their loads are all
-// asked for before the first is used, which takes 80 registers, 24 warps per SM.
+// asked for before the first is used, which takes 80 registers, 24 warps per SM
+// (and, with pairs in halves, five more that wait in local memory).
 // Measured: 16384 tokens of 32 + 8 heads of 128 53 us, 6.3 TB/s; the gradient of
 // 12289 tokens of 16 + 16 heads of 64, neighbouring pairs, 18 us, 5.5 TB/s; 64 tokens
 // of 32 + 8 heads 2.9 us, a launch.
@@ -23,7 +24,7 @@ namespace fa {
 namespace {
 
 constexpr int kRopeThreads = 128;  // (256: 12289 tokens of 16 + 16 heads of 64 19.0 us for 18.3, a longer last wave)
-constexpr long long kRopeFull = 152 * 512;  // threads that keep the SMs busy
+constexpr long long kRopeFull = kSms * 512;  // threads that keep the SMs busy
 constexpr int kRopeHeads = 8;               // heads of a thread at most
 
 __device__ __forceinline__ float2 bf2(uint32_t w) {

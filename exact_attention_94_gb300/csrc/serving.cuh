@@ -10,6 +10,7 @@
 
 namespace fa {
 
+constexpr int kSms = 152;  // of a GB300: the rules that fill it were measured there
 constexpr unsigned FA_DEVERR_OUT_OF_PAGES = 0x2002u;  // a plan needs more pages than the free stack has
 
 // Planning a step (see fa_page_plan in fa.h).

@@ -509,8 +509,9 @@ typedef struct {
  *   inverse  : 0 or 1 = rotate by -a: the gradient of the call with 0 (dq, dk
  *              from the gradients of q_out, k_out)
  * The angle is reduced to one turn in 64-bit fixed point before its sine and
- * cosine are taken in fp32, so far positions lose nothing; the result is
- * rounded once, to bf16.  T >= 0.
+ * cosine are taken in fp32, by the fast functions, off by 2^-20 at most: far
+ * positions lose nothing, and an element is off by 2^-18 of its pair's larger
+ * one and half a bf16 step.  T >= 0.
  */
 fa_status fa_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
                        const fa_rope_plan* plan, int T, int Hq, int Hkv, int d, long long q_stride,
@@ -521,8 +522,9 @@ fa_status fa_rope_axes(const void* q, const void* k, void* q_out, void* k_out, c
  * 8-bit paged cache.  Codes are e4m3, one scale per page and K/V head:
  *   k_codes, v_codes : uint8 [num_pages, Hkv, page_size, d], device
  *   k_scale, v_scale : fp32 [num_pages, Hkv], device; a value is code * scale
- * A scale is a power of two, the smallest with |x| <= 448 scale for every
- * (finite) x the page has held since its slot 0 was written, 0 if all were 0.
+ * A scale is a power of two, 2^-126 or the smallest above with |x| <= 448 scale
+ * for every (finite) x the page has held since its slot 0 was written, 0 if all
+ * were 0.
  * e4m3 is a floating format, so a power of two costs its values no precision
  * and a growing scale moves older codes almost always exactly.
  *
