@@ -53,13 +53,14 @@
 // softmax starts); P is not: it is written when the product before has read it.
 //
 // Measured, d = 128 unless said, pages of 16 to 64, replayed graphs of many calls:
-//   64 requests of 16385 to 32768 tokens, 64 heads over 8      478 us  6.76 TB/s
-//   256 requests of 1 to 2048, 64 heads over 8                  98 us  5.6 TB/s
+//   64 requests of 16385 to 32768 tokens, 64 heads over 8      479 us  6.74 TB/s
+//   256 requests of 1 to 2048, 64 heads over 8                  97 us  5.6 TB/s
 //   8 requests of 1000 to 8192, 32 heads over 32                54 us  5.5 TB/s
-//   16 requests of 100 to 16384, 4 drafts, 64 heads over 8      60 us  4.6 TB/s
+//   16 requests of 100 to 16384, 4 drafts, 64 heads over 8      59 us  4.6 TB/s
+//   the same with 8 drafts, 64 rows in two tiles                99 us  2.8 TB/s
 //   4096 requests of 1 to 128, 64 heads over 8                 229 us  2.9 TB/s
-//   32 requests, a window of 4096, 16 heads over 4, d = 64      21 us  3.0 TB/s
-//   1 request of 777, 32 heads over 8                          8.6 us
+//   32 requests, a window of 4096, 16 heads over 4, d = 64      20 us  3.0 TB/s
+//   1 request of 777, 32 heads over 8                          8.4 us
 // The first is as fast as the card copies.  The calls of 20 to 60 us lose some
 // 5 us to the start (lengths, page numbers, pages: three reads one after the
 // other before the first tile) and the merge.  Units of one tile are a chain of
@@ -67,7 +68,10 @@
 // bound by the softmax warps' instructions (issue slots 51% busy) and their
 // waits for one another: they came from 82 us with one group of warps and a
 // byte store per code, by two groups (72), P by key and its split in half
-// precision (66), all scores read at once (62.5) and packed fp32 arithmetic (61).
+// precision (66), all scores read at once (62.5), packed fp32 arithmetic (60) and
+// parts of P that are bytes of an f16 (59).  More than 32 rows are tiles of 32 that
+// follow one another in a share, so each reads the cache again (64 rows: 1.6
+// times its bytes from HBM, the rest from L2) and pays for 32 rows: 33 cost 64's.
 #include "serving.cuh"
 
 #include <cmath>
