@@ -463,3 +463,13 @@ def test_more_tiles_than_ctas(Nq, Hq, Hkv, d):
             o, lse = ops.decode_kv8(*dev(case), max(lens), window_left=window, num_shares=shares)
             assert_close(o, lse, ref)
     assert ops.device_error() == 0
+
+
+def test_no_keys_at_all():
+    """Room for no key, and lengths of 0: O = 0, lse = -inf, whatever the table and the pages hold."""
+    for B, Nq, Hq, Hkv in ((1, 1, 1, 1), (3, 4, 16, 2), (500, 1, 8, 2)):
+        q, k, v, table, lens = make([0] * B, Nq, Hq, Hkv, 64, 16)
+        for L in (0, 16):
+            o, lse = ops.decode_kv8(*dev((q, k, v, table, lens)), L)
+            assert ops.device_error() == 0
+            assert torch.all(o == 0) and torch.all(lse == -math.inf)

@@ -163,7 +163,9 @@ def test_refusals():
 @pytest.mark.parametrize("n,Hkv,d,P", [(1500, 8, 64, 16), (3001, 8, 64, 32), (9011, 8, 64, 32), (2300, 32, 128, 16),
                                        (700, 32, 64, 48)])
 def test_from_few_rows_to_many(n, Hkv, d, P):
-    """How many warps share 32 rows goes by rows times heads: 5, 2, 1, 1 and 3 in these cases.  Prompts and single tokens in one call, that begin anywhere in their pages, padding between them."""
+    """How many warps share 32 rows goes by rows times heads: 5, 2, 1, 1 and 3 in these
+    cases.  Prompts and single tokens in one call, that begin anywhere in their pages,
+    padding between them."""
     rng = np.random.default_rng(n)
     page, slot, used = [], [], 0
     order = rng.permutation(n)          # (more pages than are used)

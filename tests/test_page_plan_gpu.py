@@ -155,7 +155,8 @@ assert ops.device_error() == 0
 def test_every_batch_size_launches_in_a_fresh_process():
     """The batches around 48 KiB of shared memory, in rising order: no larger one has gone before."""
     sizes = [1025, 4050, 4051, 4052, 4060, 4094, 4095, 4096, 4097, 16384]
-    r = subprocess.run([sys.executable, "-c", FRESH, *map(str, sizes)], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    r = subprocess.run([sys.executable, "-c", FRESH, *map(str, sizes)], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
 
 
@@ -163,8 +164,7 @@ def test_threads_with_batches_of_different_sizes():
     """One thread's batch of 5000 does not take the shared memory from another's of 16384."""
     def plan(B, n, failures):
         with torch.cuda.stream(torch.cuda.Stream()):
-            a = [torch.zeros(B, dtype=torch.int32, device="cuda"), torch.ones(B, dtype=torch.int32, device="cuda"),
-                 torch.arange(B, dtype=torch.int32, device="cuda"), i32([B]), torch.zeros((B, 1), dtype=torch.int32, device="cuda")]
+            a = [i32([0] * B), i32([1] * B), i32(range(B)), i32([B]), i32([[0]] * B)]
             out = ops.page_plan(*a, 16, B)
             for _ in range(n):
                 try:
@@ -216,3 +216,19 @@ def test_finished_requests_give_their_pages_back():
         live = [int(x) for b in range(B) for x in w_table[b, :-(-w_lens[b] // P)]]
         assert sorted(live + w_free[:w_count]) == list(range(pages))  # every page is held once or free
     assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("B", [4095, 16384])
+def test_a_large_batch_captured_and_in_place(B):
+    lens, count, table = i32([0] * B), i32([2 * B]), i32(np.zeros((B, 2)))
+    new, free = i32([1] * B), i32(range(2 * B))
+    out = ops.page_plan(lens, new, free, count, table, 1, B)._replace(seq_lens=lens, free_count=count)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.page_plan(lens, new, free, count, table, 1, B, out=out)
+    for step in range(2):
+        g.replay()
+        assert out.page.tolist() == list(range(2 * B - 1 - step * B, B - 1 - step * B, -1))
+        assert lens.tolist() == [step + 1] * B and count.item() == (1 - step) * B
+    g.replay()                                        # a third token, and no block for it
+    assert ops.device_error() == 0x2001 and lens.tolist() == [2] * B and set(out.page.tolist()) == {-1}
