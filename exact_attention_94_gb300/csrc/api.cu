@@ -2,7 +2,7 @@
 // workspace sizing and kernel launches.  See include/fa.h for the contract of
 // every entry point.
 #include "../../include/fa.h"
-#include "serving.cuh"
+#include "sampling.cuh"
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -779,6 +779,22 @@ fa_status fa_page_plan(const int* ctx_lens, const int* new_lens, const int* free
   return launch_page_plan(p, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
+// A plan as the kernels take it; false for one with an axis or a frequency out of range.
+static bool rope_turns(const fa_rope_plan* plan, int d, signed char* axis, uint64_t* turn) {
+  if (plan->n_axes < 1 || plan->n_axes > 4 || (plan->neighbours != 0 && plan->neighbours != 1)) return false;
+  for (int i = 0; i < d / 2; ++i) {
+    const int a = plan->axis[i];
+    const double f = plan->inv_freq[i];
+    if (a < -1 || a >= plan->n_axes || !std::isfinite(f)) return false;
+    axis[i] = (signed char)a;
+    // the fraction of a turn in 2^-64, rounded; a negative frequency's wraps like the product with it
+    const double turns = f / 6.283185307179586477;
+    const double scaled = std::nearbyint(std::ldexp(turns - std::floor(turns), 64));
+    turn[i] = scaled >= 18446744073709551616.0 ? 0 : (uint64_t)scaled;
+  }
+  return true;
+}
+
 fa_status fa_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
                        const fa_rope_plan* plan, int T, int Hq, int Hkv, int d, long long q_stride,
                        long long k_stride, long long q_out_stride, long long k_out_stride, int inverse,
@@ -787,19 +803,8 @@ fa_status fa_rope_axes(const void* q, const void* k, void* q_out, void* k_out, c
     return FA_ERR_INVALID_ARG;
   if (inverse != 0 && inverse != 1) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  if (plan->n_axes < 1 || plan->n_axes > 4 || (plan->neighbours != 0 && plan->neighbours != 1))
-    return FA_ERR_INVALID_ARG;
   RopeParams p{};
-  for (int i = 0; i < d / 2; ++i) {
-    const int a = plan->axis[i];
-    const double f = plan->inv_freq[i];
-    if (a < -1 || a >= plan->n_axes || !std::isfinite(f)) return FA_ERR_INVALID_ARG;
-    p.axis[i] = (signed char)a;
-    // the fraction of a turn in 2^-64, rounded; a negative frequency's wraps like the product with it
-    const double turns = f / 6.283185307179586477;
-    const double scaled = std::nearbyint(std::ldexp(turns - std::floor(turns), 64));
-    p.turn[i] = scaled >= 18446744073709551616.0 ? 0 : (uint64_t)scaled;
-  }
+  if (!rope_turns(plan, d, p.axis, p.turn)) return FA_ERR_INVALID_ARG;
   if (T == 0) return FA_OK;
   if (!positions || (Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out))) return FA_ERR_INVALID_ARG;
   if (!aligned4(positions)) return FA_ERR_MISALIGNED;
@@ -941,6 +946,95 @@ fa_status fa_decode_kv8(const void* q, const void* k_codes, const void* v_codes,
     return FA_ERR_INVALID_ARG;
   const int span = kv8_span(Nq, max_seq_len, window_left);
   return launch_decode_kv8(tk, tv, p, d, num_shares, span, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+// ---------------------------------------------------------------- sampling steps
+
+// One side (query or key heads) of the norms' tensors: `n` of them, all there, aligned, rows a stride apart.
+static fa_status norm_side(int H, int d, const void* w, int n, const void* const* ptr, const long long* stride) {
+  if (H == 0) return FA_OK;
+  if (!w) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (!ptr[i] || stride[i] < (long long)H * d) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (!aligned16(ptr[i]) || stride[i] % 8 != 0) return FA_ERR_MISALIGNED;
+  for (int i = 0; i + 1 < n; ++i)  // the last is written: in place only with the same rows
+    if (ptr[i] == ptr[n - 1] && stride[i] != stride[n - 1]) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+static fa_status norm_sizes(const fa_rope_plan* plan, int T, int Hq, int Hkv, int d, int w_fp32, float eps) {
+  if (T < 0 || Hq < 0 || Hkv < 0 || Hq + (long long)Hkv < 1 || Hq + (long long)Hkv > 65535 || !plan)
+    return FA_ERR_INVALID_ARG;
+  if ((w_fp32 != 0 && w_fp32 != 1) || !(eps >= 0.f) || !std::isfinite(eps)) return FA_ERR_INVALID_ARG;
+  return d == 64 || d == 128 ? FA_OK : FA_ERR_UNSUPPORTED;
+}
+
+static bool norm_weights_ok(const void* wq, const void* wk, int w_fp32) {
+  return ((reinterpret_cast<uintptr_t>(wq) | reinterpret_cast<uintptr_t>(wk)) & (w_fp32 ? 3u : 1u)) == 0;
+}
+
+fa_status fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const void* wq, const void* wk,
+                          const int* positions, const fa_rope_plan* plan, int T, int Hq, int Hkv, int d,
+                          long long q_stride, long long k_stride, long long q_out_stride, long long k_out_stride,
+                          int w_fp32, float eps, fa_stream_t stream) {
+  fa_status st = norm_sizes(plan, T, Hq, Hkv, d, w_fp32, eps);
+  if (st != FA_OK) return st;
+  NormRopeParams p{};
+  if (!rope_turns(plan, d, p.axis, p.turn)) return FA_ERR_INVALID_ARG;
+  if (T == 0) return FA_OK;
+  const void *qs[] = {q, q_out}, *ks[] = {k, k_out};
+  const long long q_strides[] = {q_stride, q_out_stride}, k_strides[] = {k_stride, k_out_stride};
+  if (!positions) return FA_ERR_INVALID_ARG;
+  if ((st = norm_side(Hq, d, wq, 2, qs, q_strides)) != FA_OK) return st;
+  if ((st = norm_side(Hkv, d, wk, 2, ks, k_strides)) != FA_OK) return st;
+  if (!aligned4(positions) || !norm_weights_ok(wq, wk, w_fp32)) return FA_ERR_MISALIGNED;
+  p.q = q, p.k = k, p.q_out = q_out, p.k_out = k_out;
+  p.wq = wq, p.wk = wk;
+  p.positions = positions;
+  p.q_stride = q_stride, p.k_stride = k_stride, p.q_out_stride = q_out_stride, p.k_out_stride = k_out_stride;
+  p.T = T, p.Hq = Hq, p.Hkv = Hkv;
+  p.w_fp32 = w_fp32;
+  p.eps = eps;
+  return launch_norm_rope(p, d, plan->neighbours != 0, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int T, int Hq, int Hkv, int d) {
+  if (T < 0 || Hq < 0 || Hkv < 0 || Hq + (long long)Hkv < 1 || Hq + (long long)Hkv > 65535 || (d != 64 && d != 128)) return 0;
+  int q_blocks;
+  return align256((size_t)norm_rope_bwd_blocks(T, Hq, Hkv, d, &q_blocks) * d * sizeof(float) + 1);
+}
+
+fa_status fa_qk_norm_rope_bwd(const void* dyq, const void* dyk, const void* q, const void* k, void* dq, void* dk,
+                              const void* wq, const void* wk, float* dwq, float* dwk, const int* positions,
+                              const fa_rope_plan* plan, int T, int Hq, int Hkv, int d, long long dyq_stride,
+                              long long dyk_stride, long long q_stride, long long k_stride, long long dq_stride,
+                              long long dk_stride, int w_fp32, float eps, void* workspace, fa_stream_t stream) {
+  fa_status st = norm_sizes(plan, T, Hq, Hkv, d, w_fp32, eps);
+  if (st != FA_OK) return st;
+  NormRopeParams p{};
+  if (!rope_turns(plan, d, p.axis, p.turn)) return FA_ERR_INVALID_ARG;
+  if (!workspace || (Hq > 0 && !dwq) || (Hkv > 0 && !dwk)) return FA_ERR_INVALID_ARG;
+  if (T > 0) {
+    const void *qs[] = {dyq, q, dq}, *ks[] = {dyk, k, dk};
+    const long long q_strides[] = {dyq_stride, q_stride, dq_stride}, k_strides[] = {dyk_stride, k_stride, dk_stride};
+    if (!positions) return FA_ERR_INVALID_ARG;
+    if ((st = norm_side(Hq, d, wq, 3, qs, q_strides)) != FA_OK) return st;
+    if ((st = norm_side(Hkv, d, wk, 3, ks, k_strides)) != FA_OK) return st;
+  }
+  if (!aligned16(workspace) || !aligned4(dwq) || !aligned4(dwk) || !aligned4(positions) || !norm_weights_ok(wq, wk, w_fp32))
+    return FA_ERR_MISALIGNED;
+  p.dyq = dyq, p.dyk = dyk, p.q = q, p.k = k, p.q_out = dq, p.k_out = dk;
+  p.wq = wq, p.wk = wk;
+  p.positions = positions;
+  p.dw_part = static_cast<float*>(workspace);
+  p.dyq_stride = dyq_stride, p.dyk_stride = dyk_stride, p.q_stride = q_stride, p.k_stride = k_stride;
+  p.q_out_stride = dq_stride, p.k_out_stride = dk_stride;
+  p.T = T, p.Hq = Hq, p.Hkv = Hkv;
+  p.w_fp32 = w_fp32;
+  p.eps = eps;
+  return launch_norm_rope_bwd(p, d, plan->neighbours != 0, Hq > 0 ? dwq : nullptr, Hkv > 0 ? dwk : nullptr,
+                              (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -707,6 +707,17 @@ def _check_rows(name, t, dev, shape=None):
     return rows[-1][1] if rows else H * d
 
 
+def _workspace(workspace, nbytes, dev, device):
+    """The caller's workspace, checked, or one of the call's own."""
+    if workspace is None:
+        return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of the other tensors")
+    if workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError("workspace too small")
+    return workspace
+
+
 class PagePlan(NamedTuple):
     """What page_plan returns; int32 device tensors."""
     seq_lens: torch.Tensor    # [B] tokens of each request after the step
@@ -808,6 +819,14 @@ def _rope_side(name, t, o, plan, dev):
     return t.numel() // max(1, H * d), H, t.data_ptr(), o.data_ptr(), stride, out_stride, o
 
 
+def _plan_axes(plan, positions):
+    """Axes that positions must have (last ones that no pair turns with may be left out)."""
+    axes = plan.n_axes
+    if plan.used_axes < axes and isinstance(positions, torch.Tensor) and positions.dim() == 2:
+        axes = min(max(positions.shape[0], plan.used_axes), axes)
+    return axes
+
+
 def _rope(q, k, positions, plan, inverse, out, dev, raw):
     if not isinstance(plan, RopePlan):
         raise TypeError("plan must be a RopePlan")
@@ -820,10 +839,7 @@ def _rope(q, k, positions, plan, inverse, out, dev, raw):
     if nq is not None and nk is not None and nq != nk:
         raise ValueError("q and k must have the same rows")
     rows = nq if nq is not None else nk
-    axes = plan.n_axes
-    if plan.used_axes < axes and isinstance(positions, torch.Tensor) and positions.dim() == 2:
-        axes = min(max(positions.shape[0], plan.used_axes), axes)  # (last axes that no pair turns with may be left out)
-    _check("positions", positions, torch.int32, dev, (axes, rows))
+    _check("positions", positions, torch.int32, dev, (_plan_axes(plan, positions), rows))
     st = lib().fa_rope_axes(pq, pk, poq, pok, positions.data_ptr(), plan._ref, rows, Hq, Hkv, plan.d, qs, ks, qos, kos,
                             inverse, raw)
     if st:
@@ -917,3 +933,82 @@ def decode_kv8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, max
     if st:
         _lib.check(st, "fa_decode_kv8")
     return o, lse
+
+
+# ---------------------------------------------------------------- sampling steps: head norms with the rotation
+
+def _norm_side(name, plan, dev, w, tensors, out):
+    """(rows, heads, addresses, strides, output, weights are fp32) of q or k: the
+    inputs `tensors`, of one shape, and the output."""
+    x = tensors[0]
+    strides = [_check_rows(name, x, dev)]
+    size = x.shape
+    H, d = size[-2], size[-1]
+    if d != plan.d:
+        raise ValueError(f"{name} has head dim {d}, the plan {plan.d}")
+    strides += [_check_rows(f"d{name}", t, dev, size) for t in tensors[1:]]
+    wide = isinstance(w, torch.Tensor) and w.dtype is torch.float32
+    _check(f"w{name}", w, torch.float32 if wide else torch.bfloat16, dev, (d,))
+    if out is None:
+        out = torch.empty(size, dtype=torch.bfloat16, device=x.device)
+        strides.append(H * d)
+    else:
+        strides.append(_check_rows(f"out {name}", out, dev, size))
+    return x.numel() // max(1, H * d), H, [t.data_ptr() for t in (*tensors, out)], strides, out, wide
+
+
+def _norm_sides(qs, ks, wq, wk, positions, plan, out, dev):
+    """Both sides' checks; an absent one has no addresses and no heads."""
+    if not isinstance(plan, RopePlan):
+        raise TypeError("plan must be a RopePlan")
+    if qs[0] is None and ks[0] is None:
+        raise ValueError("q or k must be given")
+    oq, ok = out if out is not None else (None, None)
+    n = len(qs) + 1
+    none = (None, 0, [None] * n, [0] * n, None, None)
+    q = _norm_side("q", plan, dev, wq, qs, oq) if qs[0] is not None else none
+    k = _norm_side("k", plan, dev, wk, ks, ok) if ks[0] is not None else none
+    if q[0] is not None and k[0] is not None and q[0] != k[0]:
+        raise ValueError("q and k must have the same rows")
+    if q[5] is not None and k[5] is not None and q[5] != k[5]:
+        raise ValueError("wq and wk must have one dtype")
+    rows = q[0] if q[0] is not None else k[0]
+    _check("positions", positions, torch.int32, dev, (_plan_axes(plan, positions), rows))
+    return q, k, rows, int(bool(q[5] or k[5]))
+
+
+@_on_call_stream
+def qk_norm_rope(q, k, wq, wk, positions, plan: RopePlan, eps: float = 1e-6, out=None, *, dev, raw):
+    """Root-mean-square norms of the heads of q [..., Hq, d] and k [..., Hkv, d]
+    (either may be None) with weights wq, wk [d] (bf16 or fp32), and their
+    rotation as rope_axes does it, in one pass.  Returns (q, k), in ``out`` =
+    (q_out, k_out) when given (q_out may be q)."""
+    q, k, rows, wide = _norm_sides((q,), (k,), wq, wk, positions, plan, out, dev)
+    st = lib().fa_qk_norm_rope(q[2][0], k[2][0], q[2][1], k[2][1], wq.data_ptr() if q[1] else None,
+                               wk.data_ptr() if k[1] else None, positions.data_ptr(), plan._ref, rows, q[1], k[1], plan.d,
+                               q[3][0], k[3][0], q[3][1], k[3][1], wide, float(eps), raw)
+    if st:
+        _lib.check(st, "fa_qk_norm_rope")
+    return q[4], k[4]
+
+
+@_on_call_stream
+def qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, positions, plan: RopePlan, eps: float = 1e-6, out=None, workspace=None, *,
+                     dev, raw):
+    """Gradients of qk_norm_rope from those of what it returned: (dq, dk, dwq,
+    dwk), the weights' in fp32; dq and dk in ``out`` when given (which may be dyq
+    and dyk, or q and k)."""
+    if (dyq is None) != (q is None) or (dyk is None) != (k is None):
+        raise ValueError("q and dyq, k and dyk go together")
+    q, k, rows, wide = _norm_sides((q, dyq), (k, dyk), wq, wk, positions, plan, out, dev)
+    d = plan.d
+    dwq, dwk = (torch.empty(d, dtype=torch.float32, device=positions.device) if x[1] else None for x in (q, k))
+    workspace = _workspace(workspace, lib().fa_qk_norm_rope_bwd_workspace_bytes(rows, q[1], k[1], d), dev, positions.device)
+    st = lib().fa_qk_norm_rope_bwd(q[2][1], k[2][1], q[2][0], k[2][0], q[2][2], k[2][2], wq.data_ptr() if q[1] else None,
+                                   wk.data_ptr() if k[1] else None, dwq.data_ptr() if q[1] else None,
+                                   dwk.data_ptr() if k[1] else None, positions.data_ptr(), plan._ref, rows, q[1], k[1], d,
+                                   q[3][1], k[3][1], q[3][0], k[3][0], q[3][2], k[3][2], wide, float(eps),
+                                   workspace.data_ptr(), raw)
+    if st:
+        _lib.check(st, "fa_qk_norm_rope_bwd")
+    return q[4], k[4], dwq, dwk

@@ -599,6 +599,52 @@ int fa_decode_kv8_num_shares(int B, int Nq, int Hq, int Hkv, int max_seq_len, in
 size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_shares);
 
 /*
+ * ---------------------------------------------------------------- sampling steps
+ * Many answers to one prompt, by a model with norms on its query and key heads:
+ * fa_qk_norm_rope (and its gradient, for the policy's training).
+ */
+
+/*
+ * Root-mean-square norms of query and key heads, and the rotation of
+ * fa_rope_axes, in one pass.  A head x of d elements with the side's weights w
+ * (one vector for all query heads, one for all key heads) becomes
+ *     y = Rot(w n),   n = x r,   r = (mean(x^2) + eps)^(-1/2),
+ * worked out in fp32 and rounded once.  A plan whose pairs all have axis -1 is
+ * the norm alone.  Tensors, strides, positions and plan as in fa_rope_axes
+ * (q or k may be absent: NULL, with 0 heads; q_out may be q with the same stride).
+ *   wq, wk : [d] bf16, or fp32 with w_fp32 = 1
+ *   eps    : finite, >= 0 (a head of zeros with eps = 0 gives NaN)
+ * Squares of values beyond 2^64 are taken at a smaller scale, so a head of any
+ * finite values has a finite norm.  A head with an infinity or a NaN has an r
+ * of 0 or NaN, and NaN where those stand and in the other element of their pairs.
+ */
+fa_status fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const void* wq, const void* wk,
+                          const int* positions, const fa_rope_plan* plan, int T, int Hq, int Hkv, int d,
+                          long long q_stride, long long k_stride, long long q_out_stride, long long k_out_stride,
+                          int w_fp32, float eps, fa_stream_t stream);
+
+/* Scratch bytes fa_qk_norm_rope_bwd needs; 0 for sizes that it refuses. */
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int T, int Hq, int Hkv, int d);
+
+/*
+ * Gradients of fa_qk_norm_rope from those of its outputs.  With g = Rot^T dy
+ * and u = w g:
+ *     dx = r (u - n mean(u n)),   dw = sum over tokens and heads of g n.
+ *   dyq, dyk : gradients of q_out and k_out;  q, k : the call's inputs
+ *   dq, dk   : written, bf16; may be dyq / q (dyk / k) with the same stride
+ *   dwq, dwk : fp32 [d], written (zeros for T = 0); NULL for an absent side.  The
+ *              same call gives the same bits: sums are taken in a fixed order, in fp32
+ *   workspace: fa_qk_norm_rope_bwd_workspace_bytes(T, Hq, Hkv, d) bytes, 16-byte
+ *              aligned, contents on entry do not matter; calls whose work overlaps
+ *              on the GPU need one each
+ */
+fa_status fa_qk_norm_rope_bwd(const void* dyq, const void* dyk, const void* q, const void* k, void* dq, void* dk,
+                              const void* wq, const void* wk, float* dwq, float* dwk, const int* positions,
+                              const fa_rope_plan* plan, int T, int Hq, int Hkv, int d, long long dyq_stride,
+                              long long dyk_stride, long long q_stride, long long k_stride, long long dq_stride,
+                              long long dk_stride, int w_fp32, float eps, void* workspace, fa_stream_t stream);
+
+/*
  * Synchronises the device, then returns FA_OK if no kernel of this library
  * recorded an error since the last call, FA_ERR_TIMEOUT if a bounded wait ran
  * out (code 0x1000 + wait site), FA_ERR_INVALID_ARG if a kernel met a bad

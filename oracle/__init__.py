@@ -16,3 +16,4 @@ from .masked import (  # noqa: F401
 from . import fp8  # noqa: F401  (e4m3 block quantisation with incoherent processing)
 from . import paged  # noqa: F401  (write side of the paged cache: append, free list, copy-on-write)
 from . import serving  # noqa: F401  (one serving step: page planning, rotary axes, the 8-bit paged cache)
+from . import sampling  # noqa: F401  (one sampling step: head norms with the rotation, attention of shared prefixes)
