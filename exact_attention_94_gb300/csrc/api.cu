@@ -137,6 +137,28 @@ bool make_tmap_codes(CUtensorMap* m, const void* ptr, int D, int page_size, long
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_queries(CUtensorMap* m, const void* ptr, int D, int Hq, long long tokens, int heads, int tile_tokens) {
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tile_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_pages(CUtensorMap* m, const void* ptr, int D, int Hkv, int page_size, int num_pages, int box_rows) {
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)page_size, (cuuint64_t)num_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2, (cuuint64_t)page_size * Hkv * D * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace fa
 
 using namespace fa;
@@ -1035,6 +1057,93 @@ fa_status fa_qk_norm_rope_bwd(const void* dyq, const void* dyk, const void* q, c
   p.eps = eps;
   return launch_norm_rope_bwd(p, d, plan->neighbours != 0, Hq > 0 ? dwq : nullptr, Hkv > 0 ? dwk : nullptr,
                               (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+static bool shared_sizes_ok(int B, int Nq, int Hq, int Hkv, int num_groups, int num_shares) {
+  return B >= 1 && B <= 16384 && Nq >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && (long long)Nq * Hq <= 65535 &&
+         num_groups >= 1 && num_groups <= B && num_shares >= 0 && num_shares <= 65535;
+}
+
+static int shared_auto_shares() {  // a CTA per SM
+  int dev = 0, n_sm = kSms;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  return n_sm;
+}
+
+// Rows of partial results: four of each query row, and the cut pieces'.
+static size_t shared_rows(int B, int Nq, int Hq, int shares) { return 4 * (size_t)B * Nq * Hq + 512 * (size_t)shares; }
+
+size_t fa_decode_shared_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_groups, int num_shares) {
+  if (!shared_sizes_ok(B, Nq, Hq, Hkv, num_groups, num_shares) || Hq / Hkv > 128 || (d != 64 && d != 128)) return 0;
+  if (num_shares == 0) num_shares = shared_auto_shares();
+  const size_t rows = shared_rows(B, Nq, Hq, num_shares);
+  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float)) +
+         align256(shared_plan_bytes(B, num_groups, num_shares));
+}
+
+// What the calls over either cache have in common: sizes, pointers, the parameters.
+static fa_status shared_common(SharedParams& p, CUtensorMap& tq, const void* q, const int* block_table, const int* seq_lens,
+                               const int* group_starts, const int* shared_lens, void* o, float* lse, int B, int Nq, int Hq,
+                               int Hkv, int d, int page_size, int num_pages, int max_blocks, int max_seq_len, int num_groups,
+                               int window_left, int num_shares, void* workspace, float scale) {
+  if (!shared_sizes_ok(B, Nq, Hq, Hkv, num_groups, num_shares)) return FA_ERR_INVALID_ARG;
+  if (num_pages < 1 || max_blocks < 1 || max_seq_len < 0 || window_left < -1) return FA_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size % 16 != 0 || (long long)max_blocks * page_size < max_seq_len) return FA_ERR_INVALID_ARG;
+  if ((long long)num_pages * Hkv > 0x7fffffffll || max_seq_len > (1 << 30)) return FA_ERR_INVALID_ARG;
+  if (!q || !block_table || !seq_lens || !group_starts || !shared_lens || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || Hq / Hkv > 128) return FA_ERR_UNSUPPORTED;
+  if (!scale_ok(scale)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(workspace)) return FA_ERR_MISALIGNED;
+  if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(group_starts) || !aligned4(shared_lens) || !aligned4(lse))
+    return FA_ERR_MISALIGNED;
+  if (!ensure_init()) return FA_ERR_LAUNCH;
+  if (num_shares == 0) num_shares = shared_auto_shares();
+  const size_t rows = shared_rows(B, Nq, Hq, num_shares);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.starts = group_starts;
+  p.shared_lens = shared_lens;
+  p.o = o;
+  p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(ws);
+  ws += align256(rows * d * sizeof(float));
+  p.part_lse = reinterpret_cast<float*>(ws);
+  ws += align256(rows * sizeof(float));
+  shared_plan_at(p.plan, ws, B, num_groups, num_shares);
+  p.B = B, p.Nq = Nq, p.Hq = Hq, p.Hkv = Hkv, p.heads = Hq / Hkv;
+  p.G = num_groups;
+  p.tile_tokens = kSharedTile / p.heads;
+  p.page_size = page_size, p.num_pages = num_pages, p.max_blocks = max_blocks, p.max_len = max_seq_len;
+  p.win_left = window_left >= max_seq_len ? -1 : window_left;  // a window past every key is no window
+  p.box_rows = 16;
+  while (p.box_rows < kSharedTile && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+  p.shares = num_shares;
+  p.lead = 2;
+  p.scale_log2 = scale * kLog2e;
+  p.tau = g_opt.tau;
+  p.err = g_err_ptr;
+  p.timeout_ns = g_opt.timeout_ns;
+  return make_tmap_queries(&tq, q, d, Hq, (long long)B * Nq, p.heads, p.tile_tokens) ? FA_OK : FA_ERR_INVALID_ARG;
+}
+
+fa_status fa_decode_paged_shared(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                                 const int* seq_lens, const int* group_starts, const int* shared_lens, void* o, float* lse,
+                                 int B, int Nq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_blocks,
+                                 int max_seq_len, int num_groups, int window_left, int num_shares, void* workspace,
+                                 float scale, fa_stream_t stream) {
+  if (!k_pages || !v_pages) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_MISALIGNED;
+  SharedParams p{};
+  CUtensorMap tq, tk, tv;
+  const fa_status st = shared_common(p, tq, q, block_table, seq_lens, group_starts, shared_lens, o, lse, B, Nq, Hq, Hkv, d,
+                                     page_size, num_pages, max_blocks, max_seq_len, num_groups, window_left, num_shares,
+                                     workspace, scale);
+  if (st != FA_OK) return st;
+  if (!make_tmap_pages(&tk, k_pages, d, Hkv, page_size, num_pages, p.box_rows) ||
+      !make_tmap_pages(&tv, v_pages, d, Hkv, page_size, num_pages, p.box_rows))
+    return FA_ERR_INVALID_ARG;
+  return launch_decode_shared(tq, tk, tv, p, d, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -1012,3 +1012,54 @@ def qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, positions, plan: RopePlan, eps: flo
     if st:
         _lib.check(st, "fa_qk_norm_rope_bwd")
     return q[4], k[4], dwq, dwk
+
+
+# ---------------------------------------------------------------- sampling steps: attention of shared prefixes
+
+@functools.lru_cache(maxsize=1024)
+def _shared_bytes(dev, B, Nq, Hq, Hkv, d, groups, max_seq_len, window_left, shares):
+    """Workspace bytes of a call: they depend on its sizes and the device alone."""
+    for name, n in (("max_seq_len", max_seq_len), ("window_left", window_left), ("num_shares", shares)):
+        _check_int(name, n)
+    return lib().fa_decode_shared_workspace_bytes(B, Nq, Hq, Hkv, d, groups, shares)
+
+
+def _shared_args(q, d, Hkv, block_table, seq_lens, group_starts, shared_lens, max_seq_len, window_left, num_shares, workspace,
+                 dev):
+    """Checks what both caches' calls take; (B, Nq, Hq, table's columns, groups, longest, window, shares, workspace, o, lse)."""
+    B, Nq, Hq, dq = _check_dims("q", q, torch.bfloat16, dev, 4, f"[B, Nq, Hq, {d}]")
+    if dq != d:
+        raise ValueError(f"q must be [B, Nq, Hq, {d}]")
+    rows, max_blocks = _check_dims("block_table", block_table, torch.int32, dev, 2, "[B, max_blocks]")
+    if rows != B:
+        raise ValueError(f"block_table has {rows} rows for {B} requests")
+    (groups,) = _check_dims("shared_lens", shared_lens, torch.int32, dev, 1, "[groups]")
+    _check("seq_lens", seq_lens, torch.int32, dev, (B,))
+    _check("group_starts", group_starts, torch.int32, dev, (groups + 1,))
+    L, wl, shares = int(max_seq_len), int(window_left), int(num_shares)
+    device = q.device
+    workspace = _workspace(workspace, _shared_bytes(dev, B, Nq, Hq, Hkv, d, groups, L, wl, shares), dev, device)
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
+    return B, Nq, Hq, max_blocks, groups, L, wl, shares, workspace, torch.empty_like(q), lse
+
+
+@_on_call_stream
+def decode_paged_shared(q, k_pages, v_pages, block_table, seq_lens, group_starts, shared_lens, max_seq_len: int,
+                        window_left: int = -1, num_shares: int = 0, scale: Optional[float] = None, workspace=None, *, dev,
+                        raw):
+    """Attention of q [B, Nq, Hq, d] over pages [num_pages, page_size, Hkv, d],
+    for requests in groups that share their first tokens, which are read once for
+    all.  Requests group_starts[g] .. group_starts[g + 1] - 1 share shared_lens[g]
+    tokens (int32 on the device; 0 for none); query i of a request stands at
+    seq_lens - Nq + i.  Returns (o [B, Nq, Hq, d], lse [B, Hq, Nq])."""
+    num_pages, P, Hkv, d = _check_dims("k_pages", k_pages, torch.bfloat16, dev, 4, "[num_pages, page_size, Hkv, d]")
+    _check("v_pages", v_pages, torch.bfloat16, dev, k_pages.shape)
+    B, Nq, Hq, blocks, groups, L, wl, shares, workspace, o, lse = _shared_args(
+        q, d, Hkv, block_table, seq_lens, group_starts, shared_lens, max_seq_len, window_left, num_shares, workspace, dev)
+    st = lib().fa_decode_paged_shared(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                                      seq_lens.data_ptr(), group_starts.data_ptr(), shared_lens.data_ptr(), o.data_ptr(),
+                                      lse.data_ptr(), B, Nq, Hq, Hkv, d, P, num_pages, blocks, L, groups, wl, shares,
+                                      workspace.data_ptr(), 1.0 / math.sqrt(d) if scale is None else float(scale), raw)
+    if st:
+        _lib.check(st, "fa_decode_paged_shared")
+    return o, lse

@@ -601,7 +601,8 @@ size_t fa_decode_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int 
 /*
  * ---------------------------------------------------------------- sampling steps
  * Many answers to one prompt, by a model with norms on its query and key heads:
- * fa_qk_norm_rope (and its gradient, for the policy's training).
+ * fa_qk_norm_rope (and its gradient, for the policy's training), and attention
+ * that reads the prompt's keys once for all answers.
  */
 
 /*
@@ -643,6 +644,54 @@ fa_status fa_qk_norm_rope_bwd(const void* dyq, const void* dyk, const void* q, c
                               const fa_rope_plan* plan, int T, int Hq, int Hkv, int d, long long dyq_stride,
                               long long dyk_stride, long long q_stride, long long k_stride, long long dq_stride,
                               long long dk_stride, int w_fp32, float eps, void* workspace, fa_stream_t stream);
+
+/*
+ * Attention of a few query tokens per request over a paged cache, for a batch
+ * whose requests come in groups that share their first tokens (a system prompt,
+ * or a prompt of which many answers are sampled): what fa_decode_paged_window
+ * gives request by request, with the shared keys read once for a group.
+ * Requests group_starts[g] .. group_starts[g + 1] - 1 share their first
+ * shared_lens[g] tokens.  Those are read through the table row of the group's
+ * longest request (the first of them), all others through the request's own row;
+ * a request may be shorter than what its group shares.  Query i of the Nq of
+ * request b sits at key position seq_lens[b] - Nq + i and sees the keys up to
+ * its own position, from position - window_left on (window_left = -1: from 0).
+ * A query that sees no key gets O = 0 and lse = -inf.
+ *   q            : [B, Nq, Hq, d] bf16;   o the same, written
+ *   lse          : [B, Hq, Nq] fp32, written
+ *   k_pages, v_pages : [num_pages, page_size, Hkv, d] bf16; Hkv divides Hq,
+ *                  Hq / Hkv <= 128
+ *   block_table  : int32 [B, max_blocks], seq_lens : int32 [B], device
+ *   group_starts : int32 [num_groups + 1], device: 0, not falling, B at the end
+ *   shared_lens  : int32 [num_groups], device; 0: nothing is shared
+ *   max_seq_len  : <= max_blocks * page_size and <= 2^30
+ *   num_shares   : shares (CTAs) that the work is dealt to, 1 .. 65535; 0 = one
+ *                  for each SM
+ *   workspace    : fa_decode_shared_workspace_bytes(...) bytes, 16-byte aligned,
+ *                  contents on entry do not matter; calls whose work overlaps on
+ *                  the GPU need one each
+ * What a page holds behind a request's last key is never used, whatever it is,
+ * nor is a page that no query's window reaches, or its table entry.  A NaN or an
+ * infinity among the cached values reaches the queries that see its key, and no
+ * others; where not all queries of a group (or of a request, for its own keys)
+ * see the key, as NaN in all d elements of their O.
+ * Starts that do not cut the batch into runs are reported by fa_device_error
+ * (code 0x2001) and nothing is shared, nor by a group whose shared length is
+ * outside [0, max_seq_len] (reported too); table entries outside the pool and
+ * lengths outside [0, max_seq_len] are handled and reported as in
+ * fa_decode_paged.  Scores, sums and O are held in fp32; a probability is rounded
+ * to bf16 before it meets its values.
+ * page_size a multiple of 16, d = 64 or 128, 1 <= B <= 16384, Nq >= 1,
+ * Nq * Hq <= 65535, 1 <= num_groups <= B.
+ */
+fa_status fa_decode_paged_shared(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                                 const int* seq_lens, const int* group_starts, const int* shared_lens, void* o, float* lse,
+                                 int B, int Nq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_blocks,
+                                 int max_seq_len, int num_groups, int window_left, int num_shares, void* workspace,
+                                 float scale, fa_stream_t stream);
+
+/* Bytes of workspace for a call with these arguments; 0 for sizes that the call refuses. */
+size_t fa_decode_shared_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_groups, int num_shares);
 
 /*
  * Synchronises the device, then returns FA_OK if no kernel of this library
