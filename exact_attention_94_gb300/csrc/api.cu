@@ -149,11 +149,13 @@ bool make_tmap_queries(CUtensorMap* m, const void* ptr, int D, int Hq, long long
 }
 
 bool make_tmap_pages(CUtensorMap* m, const void* ptr, int D, int Hkv, int page_size, int num_pages, int box_rows) {
-  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)page_size, (cuuint64_t)num_pages};
-  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2, (cuuint64_t)page_size * Hkv * D * 2};
-  cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+  // [64 of d][8 keys][d / 64][eights of keys of all pages][heads]
+  const cuuint64_t row = (cuuint64_t)Hkv * D * 2;
+  cuuint64_t dims[5] = {64, 8, (cuuint64_t)D / 64, (cuuint64_t)num_pages * (page_size / 8), (cuuint64_t)Hkv};
+  cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)D * 2};
+  cuuint32_t box[5] = {64, 8, (cuuint32_t)D / 64, (cuuint32_t)box_rows / 8, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
@@ -1070,13 +1072,10 @@ static int shared_auto_shares() {  // a CTA per SM
   return n_sm;
 }
 
-// Rows of partial results: four of each query row, and the cut pieces'.
-static size_t shared_rows(int B, int Nq, int Hq, int shares) { return 4 * (size_t)B * Nq * Hq + 512 * (size_t)shares; }
-
 size_t fa_decode_shared_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_groups, int num_shares) {
   if (!shared_sizes_ok(B, Nq, Hq, Hkv, num_groups, num_shares) || Hq / Hkv > 128 || (d != 64 && d != 128)) return 0;
   if (num_shares == 0) num_shares = shared_auto_shares();
-  const size_t rows = shared_rows(B, Nq, Hq, num_shares);
+  const size_t rows = shared_part_rows(B, Nq, Hq, Hq / Hkv, num_shares);
   return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float)) +
          align256(shared_plan_bytes(B, num_groups, num_shares));
 }
@@ -1098,7 +1097,7 @@ static fa_status shared_common(SharedParams& p, CUtensorMap& tq, const void* q, 
     return FA_ERR_MISALIGNED;
   if (!ensure_init()) return FA_ERR_LAUNCH;
   if (num_shares == 0) num_shares = shared_auto_shares();
-  const size_t rows = shared_rows(B, Nq, Hq, num_shares);
+  const size_t rows = shared_part_rows(B, Nq, Hq, Hq / Hkv, num_shares);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.block_table = block_table;
   p.seq_lens = seq_lens;
@@ -1119,7 +1118,7 @@ static fa_status shared_common(SharedParams& p, CUtensorMap& tq, const void* q, 
   p.box_rows = 16;
   while (p.box_rows < kSharedTile && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
   p.shares = num_shares;
-  p.lead = 2;
+  p.own_side = shared_own_side(Nq, p.heads);
   p.scale_log2 = scale * kLog2e;
   p.tau = g_opt.tau;
   p.err = g_err_ptr;
@@ -1132,7 +1131,7 @@ fa_status fa_decode_paged_shared(const void* q, const void* k_pages, const void*
                                  int B, int Nq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_blocks,
                                  int max_seq_len, int num_groups, int window_left, int num_shares, void* workspace,
                                  float scale, fa_stream_t stream) {
-  if (!k_pages || !v_pages) return FA_ERR_INVALID_ARG;
+  if (!k_pages || !v_pages || (long long)num_pages * (page_size / 8) > 0x7fffffffll) return FA_ERR_INVALID_ARG;
   if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_MISALIGNED;
   SharedParams p{};
   CUtensorMap tq, tk, tv;

@@ -25,9 +25,13 @@
 // Rows of a tile are query tokens times the query heads of one K/V head, as they
 // lie in Q: a TMA box of [tokens][heads][64 elements].
 //
-// Main kernel's warps: 0 loads (Q, and a TMA box per page into a ring of K and V
-// tiles, across units), 1 issues the products, 4-7 and 8-11 are the softmax of
-// the two tiles, a thread per row.
+// Main kernel's warps: 2 walks over the shares and announces their pieces; 0 loads
+// K and 3 loads Q and V (K and V into one ring, across units); 1 issues the products;
+// 4-7 and 8-11 are the softmax of the two tiles, a thread per row.
+//
+// A TMA box is a page's keys (128 at most) of one head, all d of them: a tile of K or
+// V lies in shared memory as [8 keys][64 elements of d][8 x 128 bytes], so that one
+// box fills whole eights of keys.
 #include "sampling.cuh"
 
 #include <cmath>
@@ -37,13 +41,19 @@ namespace fa {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPieces = 4;  // announced ahead
+// What units of one and of two tiles of rows weigh (half microseconds, about).
+constexpr int kLeadOne = 5, kTileOne = 2, kLeadTwo = 12, kTileTwo = 3;
+constexpr int kLateShares = 4, kOwnShares = 1 + kLateShares;  // of own keys, for each CTA at most: late ones, all
+constexpr int kLate = 8;           // one in kLate of all work is own keys that are dealt late
+constexpr int kLateShare = 12;     //   in shares that weigh so much at least
+constexpr int kPlanSmem = 1024;  // groups, entries in the plan's shared memory
+constexpr int kPieces = 6;  // announced ahead
 
 template <int D>
 struct SharedLayout {
   static constexpr uint32_t kTile = 128u * D * 2u;  // a tile of Q, K or V
-  static constexpr uint32_t kChunk = 128u * 128u;   // 128 rows x 128 bytes (one 128-byte swizzle column)
-  static constexpr int kStages = D == 64 ? 8 : 4;   // K/V ring slots
+  static constexpr uint32_t kChunk = 128u * 128u;   // of Q: 128 rows x 128 bytes (one 128-byte swizzle column)
+  static constexpr int kStages = D == 64 ? 10 : 5;  // K/V ring slots
   static constexpr uint32_t kQOff = 0;              // two tiles of Q
   static constexpr uint32_t kKVOff = 2 * kTile;
   static constexpr uint32_t kMiscOff = kKVOff + kStages * kTile;
@@ -51,26 +61,17 @@ struct SharedLayout {
 };
 constexpr int kThreads = 384;
 
-// Tiles t0 .. t1 - 1 of a unit, as the producer announces them; t0 = t1 marks the share's end.
+// Tiles t0 .. t1 - 1 of a unit, as the walk announces them; t0 = t1 marks the end.
 struct Piece {
+  long long place;     // row of the results: of the query row itself (times Hq: whole units), or of a cut piece's first
+  int side;            // rows between the two runs' or tiles' results (cut pieces); 0: the unit's only piece
+  int kind;            // 0: shared keys, 1: a request's own
   int tok0, ntok;      // query tokens of the unit
   int head;            // K/V head
+  int row;             // of the block table
   int lo, end, all_lo, all_hi, beg;
-  int t0, t1;
-  int whole;           // the unit's only piece
-  int kind;            // 0: shared keys, 1: a request's own
-  int slot;            // where a cut piece's results go
-  int pad[3];
+  int t0, t1, pad;
 };
-
-__device__ __forceinline__ int shared_len(const SharedParams& p, int b) {
-  int n = p.seq_lens[b];
-  if (n < 0 || n > p.max_len) {
-    atomicCAS(p.err, 0u, FA_DEVERR_BAD_SEQLEN);
-    n = n < 0 ? 0 : p.max_len;
-  }
-  return n;
-}
 
 __device__ __forceinline__ int chunks_of(const SharedParams& p, int ntok) {  // of 256 rows
   return (ntok + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
@@ -78,144 +79,261 @@ __device__ __forceinline__ int chunks_of(const SharedParams& p, int ntok) {  // 
 __device__ __forceinline__ long long units_of(const SharedParams& p, int ntok) {
   return (long long)p.Hkv * chunks_of(p, ntok);
 }
+// What a unit weighs: its start and end, and each of its tiles of keys.  Slot
+// lead + tile * t of its weight is where tile t begins.
+struct Weight {
+  int lead, tile;
+};
+__device__ __forceinline__ Weight weight_of(const SharedParams& p, int ntok) {
+  return ntok > p.tile_tokens ? Weight{kLeadTwo, kTileTwo} : Weight{kLeadOne, kTileOne};
+}
 
 // a / b for a >= 0, b > 0, in 32 bits where both fit
 __device__ __forceinline__ long long div_ll(long long a, long long b) {
   return (((unsigned long long)a | (unsigned long long)b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
-__device__ __forceinline__ long long share_begin(long long total, int shares, long long k) {
-  const long long each = div_ll(total, shares), more = total - each * shares;  // the first `more` shares have one more
-  return each * k + (k < more ? k : more);
+// `total` slots of weight in n equal shares: the first `more` have each + 1.
+struct Equal {
+  long long total, each, more;
+  int n;
+  __device__ __forceinline__ Equal(long long t, int shares)
+      : total(t), each(shares > 0 ? div_ll(t, shares) : 0), more(shares > 0 ? t - each * shares : 0), n(shares) {}
+  __device__ __forceinline__ long long begin(long long k) const { return each * k + (k < more ? k : more); }
+  __device__ __forceinline__ int of(long long slot) const {
+    return (int)(slot < more * (each + 1) ? div_ll(slot, each + 1) : more + div_ll(slot - more * (each + 1), each));
+  }
+};
+// The shares of a list: early ones, then late ones.
+struct Deal {
+  Equal early, late;
+  __device__ __forceinline__ long long begin(int k) const {
+    return k < early.n ? early.begin(k) : early.total + late.begin(k - early.n);
+  }
+  __device__ __forceinline__ int of(long long slot) const {
+    return slot < early.total ? early.of(slot) : early.n + late.of(slot - early.total);
+  }
+};
+__device__ __forceinline__ Deal deal_of(const SharedHead& h, int kind) {
+  return kind ? Deal{Equal(h.total[1], h.shares[1]), Equal(h.total[2], h.shares[2])}
+              : Deal{Equal(h.total[0], h.shares[0]), Equal(0, 0)};
 }
 
 }  // namespace
 
 // ---------------------------------------------------------------- plan
 
-__global__ void __launch_bounds__(kPlanThreads) fa_shared_plan_kernel(const __grid_constant__ SharedParams p) {
+__global__ void __launch_bounds__(kPlanThreads, 1) fa_shared_plan_kernel(const __grid_constant__ SharedParams p) {
   __shared__ long long s_w[32];
   __shared__ int s_n[32];
+  __shared__ int s_starts[kPlanSmem + 1], s_shared[kPlanSmem], s_least[kPlanSmem];
+  __shared__ unsigned long long s_most[kPlanSmem];
+  __shared__ long long s_cum[2][kPlanSmem];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const SharedPlan& pl = p.plan;
   asm volatile("griddepcontrol.launch_dependents;");
+  const bool small = p.G <= kPlanSmem;  // groups' numbers in shared memory
+  const int* starts = small ? s_starts : p.starts;
+  int *least = small ? s_least : pl.g_least, *shared = small ? s_shared : pl.g_shared;
+  unsigned long long* most = small ? s_most : pl.g_most;  // longest length, and the first request that has it
+  int* of_group = small ? s_shared : pl.g_shared;         // (in the shared lengths' places, at the end)
+  const int len0 = tid < p.B ? p.seq_lens[tid] : 0;       // (asked for early)
   // groups that do not cut the batch into runs are reported, and nothing counts as shared
   bool bad = false;
   for (int g = tid; g <= p.G; g += kPlanThreads) {
-    const int s = p.starts[g];
-    bad |= g == 0 ? s != 0 : s < p.starts[g - 1];
+    const int s = p.starts[g], s0 = g > 0 ? p.starts[g - 1] : 0;
+    bad |= g == 0 ? s != 0 : s < s0;
     bad |= g == p.G && s != p.B;
-  }
-  const bool grouped = __syncthreads_or(bad) == 0;
-  if (!grouped && tid == 0) atomicCAS(p.err, 0u, FA_DEVERR_BAD_SEQLEN);
-  // a group's shared keys: a warp each
-  for (int g = warp; g < p.G; g += 32) {
-    const int b0 = grouped ? p.starts[g] : 0, b1 = grouped ? p.starts[g + 1] : 0;
-    int most = 0, least = 0x7fffffff, at = b1;
-    for (int b = b0 + lane; b < b1; b += 32) {
-      const int n = shared_len(p, b);
-      pl.group[b] = g;
-      if (n > most) most = n, at = b;
-      if (n > 0) least = min(least, n);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const int m2 = __shfl_xor_sync(0xffffffffu, most, o), a2 = __shfl_xor_sync(0xffffffffu, at, o);
-      if (m2 > most || (m2 == most && a2 < at)) most = m2, at = a2;
-      least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-    }
-    if (lane == 0) {
+    if (small) s_starts[g] = s;
+    if (g < p.G) {
       int n = p.shared_lens[g];
       if (n < 0 || n > p.max_len) {
         atomicCAS(p.err, 0u, FA_DEVERR_BAD_SEQLEN);
         n = 0;
       }
-      if (b1 - b0 < 2) n = 0;  // a request alone: all its keys are its own
-      n = min(n, most);
-      pl.g_shared[g] = n;
-      SharedEntry e{b0 * p.Nq, (b1 - b0) * p.Nq, at, 0, n, 0, 0, 0, 0};
-      if (n > 0) {
-        if (p.win_left >= 0) {
-          e.lo = max(0, least - p.Nq - p.win_left);
-          e.all_lo = max(0, most - 1 - p.win_left);
-        }
-        e.all_lo = max(e.all_lo, e.lo);
-        e.all_hi = min(n, least - p.Nq + 1);
-        if (e.lo < n) e.tiles = (n - e.lo / p.box_rows * p.box_rows + kSharedTile - 1) / kSharedTile;
-      }
-      // (each group's before its place in the list is known: at the end of the array of entries)
-      pl.entry[p.G + p.B + g] = e;
+      shared[g] = n, least[g] = 0x7fffffff, most[g] = 0;
     }
   }
-  __syncthreads();
-  // the list: groups, then requests, those with keys
-  const int items = p.G + p.B, n = (items + kPlanThreads - 1) / kPlanThreads;
-  auto make = [&](int i) {
-    if (i < p.G) return pl.entry[p.G + p.B + i];
-    const int b = i - p.G, len = shared_len(p, b);
-    SharedEntry e{b * p.Nq, p.Nq, b, 0, len, 0, 0, 0, 1};
-    if (grouped) e.lo = min(pl.g_shared[pl.group[b]], len);
-    if (p.win_left >= 0) {
-      e.lo = max(e.lo, len - p.Nq - p.win_left);
-      e.all_lo = len - 1 - p.win_left;
+  const bool grouped = __syncthreads_or(bad) == 0;
+  if (!grouped && tid == 0) atomicCAS(p.err, 0u, FA_DEVERR_BAD_SEQLEN);
+  auto group_of = [&](int b) {  // the group that begins last at or before b, and has requests
+    int g = 0, z = p.G;
+    while (z - g > 1) {
+      const int m = (g + z) / 2;
+      if (starts[m] <= b) g = m; else z = m;
     }
-    e.all_lo = max(e.all_lo, e.lo);
-    e.all_hi = len - p.Nq + 1;
-    if (e.lo < len) e.tiles = (len - e.lo / p.box_rows * p.box_rows + kSharedTile - 1) / kSharedTile;
-    return e;
+    return g;
   };
-  const int i0 = min(items, tid * n), i1 = min(items, i0 + n);
-  long long w = 0;
-  int c = 0;
-  for (int i = i0; i < i1; ++i) {
-    const SharedEntry e = make(i);
-    if (e.tiles > 0) w += (e.tiles + p.lead) * units_of(p, e.ntok), ++c;
+  auto length = [&](int b) { return min(max(b < kPlanThreads ? len0 : p.seq_lens[b], 0), p.max_len); };
+  // each group's longest request and shortest with keys
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int g = -1, len = 0;
+    if (b < p.B) {
+      len = b0 == 0 ? len0 : p.seq_lens[b];
+      if (len < 0 || len > p.max_len) {
+        atomicCAS(p.err, 0u, FA_DEVERR_BAD_SEQLEN);
+        len = len < 0 ? 0 : p.max_len;
+      }
+      if (grouped) g = group_of(b);
+    }
+    const unsigned long long key = (unsigned long long)(unsigned)len << 32 | (unsigned)(0x7fffffff - b);
+    int same;
+    __match_all_sync(0xffffffffu, g, &same);
+    if (same) {  // one group's: the warp's together
+      const unsigned top = __reduce_max_sync(0xffffffffu, (unsigned)len);
+      const unsigned who = __ballot_sync(0xffffffffu, (unsigned)len == top);
+      const int low = __reduce_min_sync(0xffffffffu, len > 0 ? len : 0x7fffffff);
+      if (g >= 0 && lane == __ffs(who) - 1) {
+        atomicMax(&most[g], key);
+        atomicMin(&least[g], low);
+      }
+    } else if (g >= 0) {
+      atomicMax(&most[g], key);
+      if (len > 0) atomicMin(&least[g], len);
+    }
   }
-  long long ws = w;
-  int cs = c;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, ws, o);
-    const int y = __shfl_up_sync(0xffffffffu, cs, o);
-    if (lane >= o) ws += x, cs += y;
-  }
-  if (lane == 31) s_w[warp] = ws, s_n[warp] = cs;
   __syncthreads();
+  auto tile_count = [&](int lo, int end) {
+    return lo < end ? (end - lo / p.box_rows * p.box_rows + kSharedTile - 1) / kSharedTile : 0;
+  };
+  // keys that group g shares, as used: none for a request alone, whose keys are all its own
+  auto shares_of = [&](int g) {
+    const int n = starts[g + 1] - starts[g] < 2 ? 0 : shared[g];
+    return min(n, (int)(most[g] >> 32));
+  };
+  // A list of entries, a block's threads at a time: those that have keys get the next places.
   long long total = 0;
   int count = 0;
-  ws -= w, cs -= c;
-#pragma unroll
-  for (int x = 0; x < 32; ++x) {
-    if (x < warp) ws += s_w[x], cs += s_n[x];
-    total += s_w[x], count += s_n[x];
-  }
-  for (int i = i0; i < i1; ++i) {
-    const SharedEntry e = make(i);
+  auto place = [&](const SharedList& list, long long* cum, const SharedEntry& e) {
     const bool on = e.tiles > 0;
+    const Weight u = weight_of(p, e.ntok);
+    const long long w = on ? (u.lead + (long long)u.tile * e.tiles) * units_of(p, e.ntok) : 0;
+    long long sum = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const unsigned votes = __ballot_sync(0xffffffffu, on);
+    __syncthreads();  // (the last call's have been read)
+    if (lane == 31) s_w[warp] = sum, s_n[warp] = __popc(votes);
+    __syncthreads();
+    long long ws = s_w[lane];
+    int ns = s_n[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, ws, o);
+      const int y = __shfl_up_sync(0xffffffffu, ns, o);
+      if (lane >= o) ws += x, ns += y;
+    }
+    const long long ahead_w = __shfl_sync(0xffffffffu, ws, (warp + 31) & 31);
+    const int ahead_n = __shfl_sync(0xffffffffu, ns, (warp + 31) & 31);
+    const int at = count + (warp > 0 ? ahead_n : 0) + __popc(votes & ((1u << lane) - 1u));
+    const long long before = total + (warp > 0 ? ahead_w : 0) + sum - w;
     if (on) {
-      pl.entry[cs] = e;
-      pl.cum[cs] = ws;
+      list.entry[at] = e;
+      list.cum[at] = before;
+      if (at < kPlanSmem) cum[at] = before;
     }
-    (i < p.G ? pl.of_group[i] : pl.of_request[i - p.G]) = on ? cs : -1;
-    if (on) ws += (e.tiles + p.lead) * units_of(p, e.ntok), ++cs;
+    total += __shfl_sync(0xffffffffu, ws, 31);
+    count += __shfl_sync(0xffffffffu, ns, 31);
+    return on ? at : -1;
+  };
+  // groups' shared keys
+  for (int g0 = 0; g0 < p.G; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    SharedEntry e{};
+    int n = 0;
+    if (g < p.G && grouped) {
+      n = shares_of(g);
+      if (n > 0) {
+        const int b0 = starts[g], top = (int)(most[g] >> 32), low = least[g];
+        e = {b0 * p.Nq, (starts[g + 1] - b0) * p.Nq, 0x7fffffff - (int)(unsigned)most[g], 0, n, 0, 0, 0};
+        if (p.win_left >= 0) {
+          e.lo = max(0, low - p.Nq - p.win_left);
+          e.all_lo = top - 1 - p.win_left;
+        }
+        e.all_lo = max(e.all_lo, e.lo);
+        e.all_hi = min(n, low - p.Nq + 1);
+        e.tiles = tile_count(e.lo, n);
+      }
+    }
+    const int at = place(pl.shared, s_cum[0], e);
+    if (g < p.G) {
+      least[g] = n;     // from here on: keys that the group shares,
+      of_group[g] = at; //   and its entry
+    }
   }
-  if (!grouped)
-    for (int b = tid; b < p.B; b += kPlanThreads) pl.group[b] = -1;
-  if (tid == 0) {
-    *pl.count = count;
-    *pl.total = total;
-    pl.cum[count] = total;
-  }
+  const long long total_shared = total;
+  const int count_shared = count;
+  total = 0, count = 0;
   __syncthreads();
-  // where the shares begin
-  for (int k = tid; k < p.shares; k += kPlanThreads) {
-    const long long at = share_begin(total, p.shares, k);
-    int a = 0, z = count;  // the last entry that begins at or before it
-    while (z - a > 1) {
-      const int m = (a + z) / 2;
-      if (pl.cum[m] <= at) a = m; else z = m;
+  // requests' own
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    SharedEntry e{};
+    int common = -1;
+    if (b < p.B) {
+      const int n = length(b), g = grouped ? group_of(b) : -1;
+      e = {b * p.Nq, p.Nq, b, 0, n, 0, 0, 0};
+      if (g >= 0) {
+        e.lo = min(least[g], n);
+        common = of_group[g];
+      }
+      if (p.win_left >= 0) {
+        e.lo = max(e.lo, n - p.Nq - p.win_left);
+        e.all_lo = n - 1 - p.win_left;
+      }
+      e.all_lo = max(e.all_lo, e.lo);
+      e.all_hi = n - p.Nq + 1;
+      e.tiles = tile_count(e.lo, n);
     }
-    pl.start_entry[k] = a;
-    pl.start_off[k] = count > 0 ? at - pl.cum[a] : 0;
+    const int at = place(pl.own, s_cum[1], e);
+    if (b < p.B) pl.of_request[b] = make_int2(common, at);
+  }
+  // Shares, no shorter than a tile each (or a unit's piece could be empty).  Shared
+  // keys and most of the own go to CTAs in proportion to what they weigh; the rest of
+  // the own to many small shares, which CTAs take as they come to an end.
+  SharedHead head{};
+  head.total[0] = total_shared;
+  head.total[2] = min(total, (total_shared + total) / kLate);
+  head.total[1] = total - head.total[2];
+  const float part = (float)total_shared / (float)max(total_shared + head.total[1], 1ll);
+  auto shares_in = [&](long long most, long long weight, int least) { return (int)min(most, weight / least); };
+  head.shares[0] = shares_in(min((long long)p.shares, (long long)(part * (float)p.shares + 0.999f)), total_shared, kTileTwo);
+  head.shares[1] = shares_in(head.total[1] > 0 ? max(p.shares - head.shares[0], 1) : 0, head.total[1], kTileTwo);
+  if (head.shares[1] == 0) head.total[2] += head.total[1], head.total[1] = 0;
+  head.shares[2] = shares_in((long long)kLateShares * p.shares, head.total[2], kLateShare);
+  if (head.total[2] > 0 && head.shares[2] == 0) {
+    if (head.shares[1] > 0) head.total[1] += head.total[2], head.total[2] = 0;
+    else head.shares[2] = 1;
+  }
+  head.queue = p.shares - head.shares[0];  // (shares of own keys that CTAs begin with)
+  if (tid == 0) *pl.head = head;
+  __syncthreads();
+  // where they begin
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    const SharedList& list = kind ? pl.own : pl.shared;
+    const int n = kind ? count : count_shared, shares = kind ? head.shares[1] + head.shares[2] : head.shares[0];
+    const long long* cum = n <= kPlanSmem ? s_cum[kind] : list.cum;
+    const Deal deal = deal_of(head, kind);
+    for (int k = tid; k < shares; k += kPlanThreads) {
+      const long long at = deal.begin(k);
+      int a = 0, z = n;  // the last entry that begins at or before it
+      while (z - a > 1) {
+        const int m = (a + z) / 2;
+        if (cum[m] <= at) a = m; else z = m;
+      }
+      SharedStart start{};
+      start.begin = at;
+      start.size = deal.begin(k + 1) - at;
+      start.off = at - cum[a];
+      start.e = a;
+      start.count = n;
+      start.entry = list.entry[a];
+      list.start[k] = start;
+    }
   }
 }
 
@@ -240,11 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(sizeof(Piece) == 64, "pieces");
   const uint32_t bar0 = base + L::kMiscOff + 64 * kPieces + 64;
   // Rings: K/V tiles, pieces.  Q[s]: a tile of Q has landed; its last S product is
-  // done.  Per tile t in turn: S ready, P ready, the last product of a run of key
-  // tiles done (O), and O read.  X: the softmax warps of a tile, and of both, have
-  // come this far.
+  // done.  Per tile t in turn: S ready, P's first and second 64 keys ready, the last
+  // product of a run of key tiles done (O), and O read.  X: the softmax warps of a
+  // tile, and of both, have come this far.
   enum { KV_FULL = 0, KV_EMPTY = NS, PC_FULL = 2 * NS, PC_EMPTY = PC_FULL + kPieces, Q_FULL = PC_EMPTY + kPieces,
-         Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 2, O_FINAL = P_FULL + 2, O_EMPTY = O_FINAL + 2,
+         Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 2, O_FINAL = P_FULL + 4, O_EMPTY = O_FINAL + 2,
          XB = O_EMPTY + 2, DRAIN = XB + 3, NBARS = DRAIN + 1 };
   static_assert(64 * kPieces + 64 + 8 * NBARS + 16 <= 1024, "misc area");
   auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
@@ -254,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBARS; ++i) {
       int n = 1;
-      if (i >= PC_EMPTY && i < PC_EMPTY + kPieces) n = 9;  // the products' warp and eight of softmax
-      if (i == P_FULL || i == P_FULL + 1 || i == O_EMPTY || i == O_EMPTY + 1) n = 128;
+      if (i >= PC_EMPTY && i < PC_EMPTY + kPieces) n = 11;  // who loads, who multiplies, eight warps of softmax
+      if ((i >= P_FULL && i < P_FULL + 4) || i == O_EMPTY || i == O_EMPTY + 1) n = 128;
       if (i == XB || i == XB + 1) n = 4;
       if (i == XB + 2) n = 8;
       mbar_init(BAR(i), n);
@@ -272,47 +390,68 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx w{abort_flag, p.timeout_ns, p.err};
-  asm volatile("griddepcontrol.launch_dependents;");  // the merge may be set up; it waits for this grid's end
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is there
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge may be set up from the plan; it waits for this grid's end
 
-  if (warp == 0) {
-    // ============================================================ loads
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
-    bool ok = true;
-    const int k = blockIdx.x;
-    const long long total = *p.plan.total, from = share_begin(total, p.shares, k), to = share_begin(total, p.shares, k + 1);
-    const int count = *p.plan.count;
-    const int bpb = p.box_rows / 16;  // 16-key groups per TMA box
-    // the walk over the share
-    long long at = from, off = p.plan.start_off[k];
-    int e = p.plan.start_entry[k], pieces = 0, row = 0;
+  // the next piece announced, read by every lane of a warp
+  auto take = [&](int piece, Piece& s, unsigned site) {
+    const int slot = piece % kPieces;
+    if (!__all_sync(0xffffffffu, mbar_wait(BAR(PC_FULL + slot), piece / kPieces & 1, w, site))) return false;
+    s = s_piece[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(BAR(PC_EMPTY + slot));
+    return true;
+  };
+  // Ring places of key tile `it`: its K comes before the V of the tile in front, as
+  // the products take them.
+  auto k_place = [](int it) { return it == 0 ? 0 : 2 * it - 1; };
+  auto v_place = [](int it) { return 2 * it + 2; };
+
+  if (warp == 2) {
+    // ============================================================ walk over the shares
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    const SharedHead* head = p.plan.head;
+    const int n_shared = head->shares[0], n_own = head->shares[1] + head->shares[2];
+    const long long rows = (long long)p.B * p.Nq * p.Hq;
+    int kind = (int)blockIdx.x < n_shared ? 0 : 1, k = (int)blockIdx.x - (kind ? n_shared : 0);
+    SharedStart st = {};
     SharedEntry ent = {}, ahead = {};
-    if (from < to) {
-      ent = p.plan.entry[e];
-      if (e + 1 < count) ahead = p.plan.entry[e + 1];
-    }
-    auto next = [&]() {  // the share's next piece; t0 = t1: none is left
+    long long at = 0, to = 0, off = 0;
+    auto begin = [&]() {  // share k of the list
+      const SharedList& list = kind ? p.plan.own : p.plan.shared;
+      st = list.start[k];
+      at = st.begin, to = at + st.size, off = st.off;
+      ent = st.entry;
+      if (st.e + 1 < st.count) ahead = list.entry[st.e + 1];
+    };
+    if (k < (kind ? n_own : n_shared)) begin();
+    for (int pieces = 0;; ++pieces) {
       Piece s = {};
-      while (at < to) {
-        const int weight = ent.tiles + p.lead;
-        const int chunks = chunks_of(p, ent.ntok);
+      for (;;) {  // the next piece; t0 = t1: none is left
+        if (at == to) {
+          if (kind == 1 && k >= n_own) break;
+          kind = 1;
+          if (lane == 0) k = atomicAdd(&p.plan.head->queue, 1);
+          k = __shfl_sync(0xffffffffu, k, 0);
+          if (k >= n_own) break;
+          begin();
+        }
+        const Weight wt = weight_of(p, ent.ntok);
+        const int weight = wt.lead + wt.tile * ent.tiles, chunks = chunks_of(p, ent.ntok);
         if (off >= (long long)weight * p.Hkv * chunks) {
           off = 0;
-          ++e;
+          ++st.e;
           ent = ahead;
-          if (e + 1 < count) ahead = p.plan.entry[e + 1];  // (read long before it is needed)
+          if (st.e + 1 < st.count) ahead = (kind ? p.plan.own : p.plan.shared).entry[st.e + 1];
           continue;
         }
         const int u = (int)div_ll(off, weight), w0 = (int)(off - (long long)u * weight);
         const int w1 = (int)(to - at < weight - w0 ? w0 + (to - at) : weight);
-        const bool later = w0 == 0 && at > from;  // the unit begins behind the share's first slot
+        const bool later = w0 == 0 && at > st.begin;  // the unit begins behind the share's first slot
         off += w1 - w0;
         at += w1 - w0;
-        s.t0 = max(w0 - p.lead, 0), s.t1 = max(w1 - p.lead, 0);
+        s.t0 = w0 <= wt.lead ? 0 : (w0 - wt.lead + wt.tile - 1) / wt.tile;
+        s.t1 = w1 <= wt.lead ? 0 : (w1 - wt.lead + wt.tile - 1) / wt.tile;
         if (s.t0 == s.t1) continue;
         s.head = (int)((unsigned)u / (unsigned)chunks);
         const int c = u - s.head * chunks;
@@ -320,106 +459,107 @@ __global__ void __launch_bounds__(kThreads, 1)
         s.ntok = min(2 * p.tile_tokens, ent.ntok - c * 2 * p.tile_tokens);
         s.lo = ent.lo, s.end = ent.end, s.all_lo = ent.all_lo, s.all_hi = ent.all_hi;
         s.beg = ent.lo / p.box_rows * p.box_rows;
-        s.whole = s.t0 == 0 && s.t1 == ent.tiles;
-        s.kind = ent.kind;
-        s.slot = 2 * k + (later ? 1 : 0);
-        row = ent.row;
-        return s;
+        s.kind = kind;
+        s.row = ent.row;
+        const long long slot = 2 * (long long)k + (later ? 1 : 0);
+        if (s.t0 == 0 && s.t1 == ent.tiles) {
+          s.side = 0;
+          s.place = 2 * kind * rows;
+        } else {
+          s.side = kind ? p.own_side : kSharedTile;
+          s.place = 4 * rows + (kind ? 512ll * p.shares : 0) + slot * 2 * s.side;
+        }
+        break;
       }
-      s.t0 = s.t1 = 0;
-      return s;
-    };
-    struct Batch {  // up to four tiles of a piece, lane i owning 16 keys
-      int n, page, off, head;
-      bool on, first;
-      Piece pc;
-    };
-    Piece pc = {};
-    int t_next = 0;
-    bool more = true;
-    auto fetch = [&](Batch& q) {
-      q.n = 0, q.on = q.first = false;
-      if (!more) return;
-      if (t_next == pc.t1) {
-        pc = next();
-        t_next = pc.t0;
-        more = pc.t0 < pc.t1;
-        if (!more) return;
-        q.first = true;
-      }
-      q.pc = pc;
-      q.n = min(4, pc.t1 - t_next);
-      const int g = (pc.beg + t_next * kSharedTile) / 16 + lane;
-      q.on = lane < 8 * q.n && g < (pc.end + 15) / 16;
-      q.head = pc.head;
-      t_next += q.n;
-      if (q.on) {
-        const int blk = (int)((unsigned)(g * 16) / (unsigned)p.page_size);
-        q.off = g * 16 - blk * p.page_size;
-        q.page = p.block_table[(size_t)row * p.max_blocks + blk];
-      }
-    };
-    auto announce = [&](const Piece& s) {
       const int slot = pieces % kPieces;
-      if (pieces >= kPieces) ok = __all_sync(0xffffffffu, mbar_wait(BAR(PC_EMPTY + slot), (pieces / kPieces - 1) & 1, w, 70));
-      if (!ok) return;
+      if (pieces >= kPieces &&
+          !__all_sync(0xffffffffu, mbar_wait(BAR(PC_EMPTY + slot), (pieces / kPieces - 1) & 1, w, 70)))
+        break;
       if (lane == 0) {
         s_piece[slot] = s;
         mbar_arrive(BAR(PC_FULL + slot));
       }
-      ++pieces;
+      __syncwarp();
+      if (s.t0 == s.t1) break;
+    }
+  } else if (warp == 0 || warp == 3) {
+    // ============================================================ loads of K, and of Q and V
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    const CUtensorMap* map = warp == 0 ? &tm_k : &tm_v;
+    if (lane == 0) {
+      tma_prefetch_desc(map);
+      if (warp == 3) tma_prefetch_desc(&tm_q);
+    }
+    const int boxes = kSharedTile / p.box_rows, shift = __ffs(p.box_rows) - 5;  // TMA boxes of a tile; 16-key groups of one, log2
+    bool ok = true, more = true;
+    Piece pc;
+    pc.t0 = pc.t1 = 0;
+    int t_next = 0, piece = 0;
+    struct Batch {  // up to four tiles of a piece, lane i owning 16 keys; their pages are read two batches ahead
+      int n, rows8, page, head, last;  // rows8: of the cache, in eights, less the page's; last: 16-key groups there are
+      int tok0, ntok;                  // a piece's first batch: its query tokens; else 0
     };
-    int it = 0, qt = 0;  // key tiles, tiles of Q so far
+    auto fetch = [&](Batch& q) {
+      q.n = q.ntok = 0;
+      if (!more) return;
+      if (t_next == pc.t1) {
+        more = take(piece++, pc, 73) && pc.t0 < pc.t1;
+        t_next = pc.t0;
+        if (!more) return;
+        q.tok0 = pc.tok0, q.ntok = pc.ntok;
+      }
+      q.n = min(4, pc.t1 - t_next);
+      const int g0 = (pc.beg + t_next * kSharedTile) / 16, g = g0 + lane;
+      q.last = (pc.end + 15) / 16 - g0;
+      q.head = pc.head;
+      q.page = q.rows8 = 0;
+      t_next += q.n;
+      if (lane < 8 * q.n && lane < q.last) {
+        const int blk = (int)((unsigned)(g * 16) / (unsigned)p.page_size);
+        q.rows8 = 2 * g - blk * (p.page_size / 8);
+        q.page = p.block_table[(size_t)pc.row * p.max_blocks + blk];
+      }
+    };
+    int place = warp == 0 ? 0 : 2, qt = 0;  // ring places, as k_place and v_place count; tiles of Q so far
     Batch now, then;
     fetch(now);
     fetch(then);
     while (ok && now.n > 0) {
-      if (now.on && (now.page < 0 || now.page >= p.num_pages)) {  // report, and read a valid page instead
+      if (now.page < 0 || now.page >= p.num_pages) {  // report, and read a valid page instead
         atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
         now.page = 0;
       }
-      if (now.first) announce(now.pc);
-      const uint32_t on = __ballot_sync(0xffffffffu, now.on);
-      for (int i = 0; i < now.n && ok; ++i, ++it) {
-        const int boxes = (__popc(on >> (8 * i) & 0xffu) + bpb - 1) / bpb;
-        const bool issue = (lane >> 3) == i && now.on && (lane & (bpb - 1)) == 0;
-        const uint32_t dst = (uint32_t)(lane & 7) * 16u * 128u;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int u = 2 * it + v, slot = u % NS;
-          if (u >= NS) ok = mbar_wait(BAR(KV_EMPTY + slot), (u / NS - 1) & 1, w, 71);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          if (lane == 0) mbar_arrive_expect_tx(BAR(KV_FULL + slot), (uint32_t)(boxes * p.box_rows * D * 2));
-          __syncwarp();
-          if (issue) {
+      if (warp == 3) {  // Q, before the first values (which are needed later)
+        for (int x = 0; x < now.ntok && ok; x += p.tile_tokens, ++qt) {
+          const int slot = qt & 1;
+          if (qt >= 2) ok = __all_sync(0xffffffffu, mbar_wait(BAR(Q_EMPTY + slot), (qt / 2 - 1) & 1, w, 72));
+          if (ok && elect_one()) {
+            mbar_arrive_expect_tx(BAR(Q_FULL + slot), (uint32_t)(p.tile_tokens * p.heads * D * 2));
 #pragma unroll
             for (int c = 0; c < CH; ++c)
-              tma_load_4d(kv_s + slot * TILE + c * CHUNK + dst, v ? &tm_v : &tm_k, BAR(KV_FULL + slot), c * 64, now.head,
-                          now.off, now.page);
+              tma_load_3d(q_s + slot * TILE + c * CHUNK, &tm_q, BAR(Q_FULL + slot), c * 64, now.head * p.heads, now.tok0 + x);
           }
           __syncwarp();
         }
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok && i == 0 && now.first) {  // Q behind the first keys, which need no room that the last unit's Q holds
-          const int tiles = now.pc.ntok > p.tile_tokens ? 2 : 1;
-          for (int x = 0; x < tiles && ok; ++x, ++qt) {
-            const int slot = qt & 1;
-            if (qt >= 2) ok = __all_sync(0xffffffffu, mbar_wait(BAR(Q_EMPTY + slot), (qt / 2 - 1) & 1, w, 72));
-            if (ok && lane == 0) {
-              mbar_arrive_expect_tx(BAR(Q_FULL + slot), (uint32_t)(p.tile_tokens * p.heads * D * 2));
-#pragma unroll
-              for (int c = 0; c < CH; ++c)
-                tma_load_3d(q_s + slot * TILE + c * CHUNK, &tm_q, BAR(Q_FULL + slot), c * 64, now.head * p.heads,
-                            now.pc.tok0 + x * p.tile_tokens);
-            }
-            __syncwarp();
-          }
+        if (!ok) break;
+      }
+      const int at8 = now.page * (p.page_size / 8) + now.rows8;
+      for (int i = 0; i < now.n; ++i) {
+        const int slot = place % NS, here = min(boxes, (max(now.last - 8 * i, 0) + (1 << shift) - 1) >> shift);
+        if (place >= NS) ok = __all_sync(0xffffffffu, mbar_wait(BAR(KV_EMPTY + slot), (place / NS - 1) & 1, w, 74));
+        if (!ok) break;
+        if (elect_one()) mbar_arrive_expect_tx(BAR(KV_FULL + slot), (uint32_t)(here * p.box_rows * D * 2));
+        __syncwarp();
+        const uint32_t dst = kv_s + slot * TILE, bar = BAR(KV_FULL + slot);
+        for (int x = 0; x < here; ++x) {  // (one lane issues, with the same operands in all)
+          const int row8 = __shfl_sync(0xffffffffu, at8, 8 * i + (x << shift));
+          if (elect_one()) tma_load_5d(dst + x * p.box_rows * D * 2, map, bar, 0, 0, 0, row8, now.head);
         }
+        place += place == 0 ? 1 : 2;
       }
       now = then;
       fetch(then);
     }
-    if (ok) announce(pc);  // the end
     if (!ok) {  // let copies already in flight land before the CTA's shared memory goes away
       const uint64_t t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 200000ull) {
@@ -427,61 +567,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ============================================================ products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // Job n is a tile of rows times a tile of keys; jobs take S, P and O of tile n & 1.
     // S of job n is issued before the product of job n - 1's P, which waits for its softmax.
     constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false), IDESC_O = idesc_bf16(128, D, false, true);
     struct Job {
-      int vslot, vphase;
+      uint32_t vslot, vphase;
       bool on, first, last, frees;  // first, last of its tile's run in the piece; the last to read its values
     } before{};
-    int n = 0, it = 0, qt = 0, runs[2] = {0, 0}, ps[2] = {0, 0};
-    bool ok = true;
-    auto product = [&](const Job& j, int t) {  // O_t (+)= P V
-      bool good = mbar_wait(BAR(KV_FULL + j.vslot), j.vphase, w, 73);
-      if (__all_sync(0xffffffffu, good)) good = mbar_wait(BAR(P_FULL + t), ps[t] & 1, w, 74);
-      if (__all_sync(0xffffffffu, good) && j.first && runs[t] > 0)  // the run before has been read
-        good = mbar_wait(BAR(O_EMPTY + t), (runs[t] - 1) & 1, w, 75);
-      if (!__all_sync(0xffffffffu, good)) return false;
+    uint32_t n = 0, qt = 0, runs[2] = {0, 0}, ps[2] = {0, 0};
+    uint32_t sk = 0, pk = 0, sv = 2, pv = 0;  // ring slots and phases of the tile's K and V
+    bool ok = true, start = true;
+    auto advance = [](uint32_t& slot, uint32_t& phase, uint32_t by) {
+      slot += by;
+      if (slot >= (uint32_t)NS) slot -= NS, phase ^= 1u;
+    };
+    auto there = [&](uint32_t bar, uint32_t phase) { return (bool)__all_sync(0xffffffffu, mbar_test(bar, phase)); };
+    auto wait = [&](uint32_t bar, uint32_t phase, unsigned site) {
+      return there(bar, phase) || __all_sync(0xffffffffu, mbar_wait(bar, phase, w, site));
+    };
+    auto product = [&](const Job& j, uint32_t t) {  // O_t (+)= P V
+      if (!wait(BAR(KV_FULL) + 8 * j.vslot, j.vphase, 75)) return false;
+      if (j.first && runs[t] > 0 && !wait(BAR(O_EMPTY) + 8 * t, (runs[t] - 1) & 1, 76)) return false;  // the run before has been read
+      if (!wait(BAR(P_FULL) + 16 * t, ps[t] & 1, 77)) return false;
+      tc_fence_after();
+      const uint64_t vd = smem_desc_sw128(kv_s + j.vslot * TILE, 1024, CH * 1024);
+      const uint32_t dst = tmem + 256u + (t ? (uint32_t)D : 0u), pa = tmem + (t ? 128u : 0u);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_ts_w(dst, pa + kk * 8, desc_add(vd, kk * CH * 2048), IDESC_O, (!j.first || kk > 0) ? 1u : 0u);
+      if (!wait(BAR(P_FULL) + 16 * t + 8, ps[t] & 1, 78)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 4; kk < 8; ++kk) mma_ts_w(dst, pa + kk * 8, desc_add(vd, kk * CH * 2048), IDESC_O, 1u);
       ++ps[t];
       if (j.first) ++runs[t];
-      tc_fence_after();
-      const uint32_t va = kv_s + j.vslot * TILE, dst = tmem + 256u + (t ? (uint32_t)D : 0u), pa = tmem + (t ? 128u : 0u);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ts_w(dst, pa + kk * 8, smem_desc_sw128(va + kk * 2048, CHUNK, 1024), IDESC_O, (!j.first || kk > 0) ? 1u : 0u);
-      if (j.frees) mma_commit_w(BAR(KV_EMPTY + j.vslot));
-      if (j.last) mma_commit_w(BAR(O_FINAL + t));
+      if (j.frees) mma_commit_w(BAR(KV_EMPTY) + 8 * j.vslot);
+      if (j.last) mma_commit_w(BAR(O_FINAL) + 8 * t);
       return true;
     };
-    for (int piece = 0; ok; ++piece) {
-      const int pslot = piece % kPieces;
-      ok = __all_sync(0xffffffffu, mbar_wait(BAR(PC_FULL + pslot), piece / kPieces & 1, w, 76));
-      if (!ok) break;
-      const int tiles = s_piece[pslot].t1 - s_piece[pslot].t0, subs = s_piece[pslot].ntok > p.tile_tokens ? 2 : 1;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(PC_EMPTY + pslot));
-      if (tiles == 0) break;
-      for (int x = 0; x < tiles && ok; ++x, ++it) {
-        const int uk = 2 * it, sk = uk % NS, uv = uk + 1;
-        for (int sub = 0; sub < subs && ok; ++sub, ++n) {
-          const int t = n & 1, qs = (qt + sub) & 1;
-          if (x == 0) ok = __all_sync(0xffffffffu, mbar_wait(BAR(Q_FULL + qs), (qt + sub) / 2 & 1, w, 77));
-          if (ok && sub == 0) ok = __all_sync(0xffffffffu, mbar_wait(BAR(KV_FULL + sk), uk / NS & 1, w, 78));
-          if (!ok) break;
+    Piece s;
+    for (int piece = 0; ok && take(piece, s, 79) && s.t0 < s.t1; ++piece) {
+      const int tiles = s.t1 - s.t0, subs = s.ntok > p.tile_tokens ? 2 : 1;
+      const int alone = 3 - subs;  // jobs between a tile's jobs on the same S: key tiles in turn, or every one
+      for (int x = 0; x < tiles && ok; ++x) {
+        bool here = there(BAR(KV_FULL) + 8 * sk, pk);
+        for (int sub = 0; sub < subs; ++sub, ++n) {
+          const uint32_t t = n & 1, q = qt + sub, qs = q & 1;
+          if (x == 0 && here) here = there(BAR(Q_FULL) + 8 * qs, q >> 1 & 1);
+          if (!here) {
+            // inputs that have not come yet: the last job's product need not wait for them
+            if (before.on && !(ok = product(before, t ^ 1))) break;
+            before.on = false;
+            ok = wait(BAR(KV_FULL) + 8 * sk, pk, 81);
+            if (ok && x == 0) ok = wait(BAR(Q_FULL) + 8 * qs, q >> 1 & 1, 80);
+            if (!ok) break;
+            here = true;
+          }
           tc_fence_after();
-          const uint32_t qa = q_s + qs * TILE, ka = kv_s + sk * TILE, dst = tmem + (t ? 128u : 0u);
+          const uint64_t qd = smem_desc_sw128(q_s + qs * TILE, 16, 1024), kd = smem_desc_sw128(kv_s + sk * TILE, 16, CH * 1024);
+          const uint32_t dst = tmem + (t ? 128u : 0u);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = (kk / 4) * CHUNK + (kk % 4) * 32;
-            mma_ss_w(dst, smem_desc_sw128(qa + o, 16, 1024), smem_desc_sw128(ka + o, 16, 1024), IDESC_S, kk > 0);
+            const uint32_t o = (kk % 4) * 32;
+            mma_ss_w(dst, desc_add(qd, (kk / 4) * CHUNK + o), desc_add(kd, (kk / 4) * 1024 + o), IDESC_S, kk > 0);
           }
-          mma_commit_w(BAR(S_FULL + t));
-          if (x == tiles - 1) mma_commit_w(BAR(Q_EMPTY + qs));
-          if (sub == subs - 1) mma_commit_w(BAR(KV_EMPTY + sk));
-          if (before.on) ok = product(before, t ^ 1);
-          const int alone = 3 - subs;  // jobs between a tile's jobs on the same S: key tiles in turn, or every one
-          before = {uv % NS, uv / NS & 1, true, x < alone, x >= tiles - alone, sub == subs - 1};
+          mma_commit_w(BAR(S_FULL) + 8 * t);
+          if (x == tiles - 1) mma_commit_w(BAR(Q_EMPTY) + 8 * qs);
+          if (sub == subs - 1) mma_commit_w(BAR(KV_EMPTY) + 8 * sk);
+          if (before.on && !(ok = product(before, t ^ 1))) break;
+          before = {sv, pv, true, x < alone, x >= tiles - alone, sub == subs - 1};
         }
+        advance(sk, pk, start ? 1u : 2u);  // (as k_place and v_place count)
+        advance(sv, pv, 2u);
+        start = false;
       }
       qt += subs;
     }
@@ -494,6 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ============================================================ softmax
+    // (registers go where a row's 128 scores are held: 88 + 2 x 208 is what 3 x 168 was)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + (t ? 128u : 0u), tO = tmem + lane_off + 256u + (t ? (uint32_t)D : 0u);
@@ -504,15 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int n0 = 0, it0 = 0, phase = 0, runs = 0;  // jobs and key tiles before the piece; S phases and runs of this tile
     uint32_t xg = 0, xb = 0, flip = 0;
-    for (int piece = 0; ok; ++piece) {
-      const int pslot = piece % kPieces;
-      ok = __all_sync(0xffffffffu, mbar_wait(BAR(PC_FULL + pslot), piece / kPieces & 1, w, 79));
-      if (!ok) break;
-      const Piece s = s_piece[pslot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(PC_EMPTY + pslot));
+    Piece s;
+    for (int piece = 0; ok && take(piece, s, 82) && s.t0 < s.t1; ++piece) {
       const int tiles = s.t1 - s.t0;
-      if (tiles == 0) break;
       const bool pair = s.ntok > p.tile_tokens;
       const int side = (t ^ n0) & 1;  // pair: tile of rows; else: which of the two runs of key tiles
       const int tok = s.tok0 + (pair ? side * p.tile_tokens : 0) + my_tok;
@@ -521,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int key_lo = 0, key_hi = 0;
       if (valid) {
         const int b = p.Nq == 1 ? tok : (int)((unsigned)tok / (unsigned)p.Nq);
-        const int len = min(max(p.seq_lens[b], 0), p.max_len), pos = len - p.Nq + tok - b * p.Nq;
+        const int len = s.kind == 1 ? s.end : min(max(p.seq_lens[b], 0), p.max_len), pos = len - p.Nq + tok - b * p.Nq;
         key_lo = p.win_left >= 0 ? max(s.lo, pos - p.win_left) : s.lo;
         key_hi = min(s.end, pos + 1);
       }
@@ -530,33 +685,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool poison = false;
       const int x_step = pair ? 1 : 2, x_first = pair ? 0 : side;
       for (int x = x_first; x < tiles; x += x_step, ++phase) {
-        const int uv = 2 * (it0 + x) + 1, vslot = uv % NS;
         const int j0 = s.beg + (s.t0 + x) * kSharedTile;
-        ok = mbar_wait(BAR(S_FULL + t), phase & 1, w, 80);
+        ok = mbar_wait(BAR(S_FULL + t), phase & 1, w, 83);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (j0 < s.all_lo || j0 + kSharedTile > s.all_hi) {
+        const bool inside = j0 >= s.all_lo && j0 + kSharedTile <= s.all_hi;  // every row sees every key
+        if (!inside) {
           // Some rows do not see some keys of the tile, and 0 times a NaN or an infinity
           // is not 0.  What no row sees (it may be anything) counts as zero; a value row
           // that some see, and that holds one, counts as zero too, and its rows get a NaN.
-          ok = mbar_wait(BAR(KV_FULL + vslot), uv / NS & 1, w, 81);
+          const int uv = v_place(it0 + x), vslot = uv % NS;
+          ok = mbar_wait(BAR(KV_FULL + vslot), uv / NS & 1, w, 84);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
           const int key = j0 + r;
           const bool out = key < s.lo || key >= s.end;
-          uint4* row = reinterpret_cast<uint4*>(sb + L::kKVOff + vslot * TILE + r * 128);
+          uint4* row = reinterpret_cast<uint4*>(sb + L::kKVOff + vslot * TILE + (r >> 3) * CH * 1024 + (r & 7) * 128);
           bool odd = false;
           if (max(j0, s.lo) < s.all_lo || min(j0 + kSharedTile, s.end) > s.all_hi) {
             if (!out && (key < s.all_lo || key >= s.all_hi)) {
               uint32_t bad = 0;
 #pragma unroll 1
               for (int i = 0; i < 8 * CH; ++i) {
-                const uint4 v = row[(i >> 3) * (CHUNK / 16) + (i + lane & 7)];  // (other banks for each lane)
+                const uint4 v = row[(i >> 3) * 64 + (i + lane & 7)];  // (other banks for each lane)
                 bad |= __vcmpeq2(v.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(v.y & 0x7f807f80u, 0x7f807f80u) |
                        __vcmpeq2(v.z & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(v.w & 0x7f807f80u, 0x7f807f80u);
               }
@@ -569,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive(pair ? BAR(XB + 2) : BAR(XB + t));
             }
             // (pairs: both tiles' warps have read the values before either clears them)
-            ok = pair ? mbar_wait(BAR(XB + 2), xb++ & 1, w, 82) : mbar_wait(BAR(XB + t), xg++ & 1, w, 83);
+            ok = pair ? mbar_wait(BAR(XB + 2), xb++ & 1, w, 85) : mbar_wait(BAR(XB + t), xg++ & 1, w, 86);
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
               break;
@@ -584,89 +740,101 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (side == 0 || !pair) {  // (the other tile's product comes behind this one's)
             if (out || odd) {
 #pragma unroll
-              for (int i = 0; i < 8 * CH; ++i) row[(i >> 3) * (CHUNK / 16) + (i + lane & 7)] = make_uint4(0u, 0u, 0u, 0u);
+              for (int i = 0; i < 8 * CH; ++i) row[(i >> 3) * 64 + (i + lane & 7)] = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
           }
         }
         if (live) {
-          uint32_t sr[4][32];
-          float mq[4];  // each load's maximum over its 32 columns
+          uint32_t sr[4][32], none = 0;  // bit c: no row of the warp sees any of the c-th 32 keys
+          float mq[4];                   // each load's maximum over its 32 columns
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32 * c, sr[c], mq[c]);
           tmem_ld_wait();
-          float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-          float v[128];
+          if (!inside) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(sr[i / 32][i % 32]);
-          if (j0 < key_lo || j0 + kSharedTile > key_hi) {  // a tile the row sees only in part, or not at all
+            for (int c = 0; c < 4; ++c) {
+              const int a = min(max(key_lo - j0 - 32 * c, 0), 32), z = min(max(key_hi - j0 - 32 * c, 0), 32);
+              const uint32_t sees = z > a ? (0xffffffffu >> (32 - (z - a))) << a : 0u;
+              if (__any_sync(0xffffffffu, ~sees)) {
+                float m = -INFINITY;
+                none |= __any_sync(0xffffffffu, sees) ? 0u : 1u << c;
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (j0 + i < key_lo || j0 + i >= key_hi) v[i] = -INFINITY;
-            float mg[8];
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              float m = fmaxf(v[16 * g], v[16 * g + 1]);
-#pragma unroll
-              for (int i = 2; i < 16; i += 2) m = max3f(m, v[16 * g + i], v[16 * g + i + 1]);
-              mg[g] = m;
+                for (int i = 0; i < 32; i += 2) {
+                  if (!(sees >> i & 1)) sr[c][i] = 0xff800000u;
+                  if (!(sees >> (i + 1) & 1)) sr[c][i + 1] = 0xff800000u;
+                  m = max3f(m, __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
+                }
+                mq[c] = m;
+              }
             }
-            mx = max3f(max3f(mg[0], mg[1], mg[2]), max3f(mg[3], mg[4], mg[5]), fmaxf(mg[6], mg[7]));
           }
-          const float m_new = mx * sl2;
+          const float m_new = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
           float alpha = 1.f;
           const bool moves = m_new > m_ref + p.tau;
           if (moves) {
             alpha = ex2_sfu(m_ref - m_new);
             m_ref = m_new;
           }
-          const float mb = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t nmb2 = f2_pack(-mb, -mb);
-          uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-          uint32_t pk[2][32];
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            float y0, y1;
-            f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), sl2x2, nmb2), y0, y1);
-            const float p0 = ex2_sfu(y0), p1 = ex2_sfu(y1);
-            acc[i & 3] = f2_add(acc[i & 3], f2_pack(p0, p1));
-            pk[i / 32][i % 32] = pack_bf16x2(p0, p1);
-            if (i == 31) tmem_st32(tS, pk[0]);  // the first half out early: frees registers
-          }
-          const uint64_t sum = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
-          float s0, s1;
-          f2_unpack(sum, s0, s1);
-          l = fmaf(l, alpha, s0 + s1);
           if (x != x_first && __any_sync(0xffffffffu, moves)) {
             // rows whose reference moved: O *= alpha (alpha = 1 for the others)
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t ov[32];
-              tmem_ld32(tO + 32 * c, ov);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 8) {
+              uint32_t ov[8];
+              tmem_ld8(tO + c, ov);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-              tmem_st32(tO + 32 * c, ov);
+              for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+              tmem_st8(tO + c, ov);
             }
           }
-          tmem_st32(tS + 32, pk[1]);
-          tmem_st_wait();
+          const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t nmb2 = f2_pack(-mb, -mb);
+          uint64_t acc[2] = {0ull, 0ull};
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (!(none >> c & 1)) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float y0, y1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])), sl2x2, nmb2), y0, y1);
+                const float p0 = ex2_sfu(y0), p1 = ex2_sfu(y1);
+                acc[i & 1] = f2_add(acc[i & 1], f2_pack(p0, p1));
+                pk[16 * (c & 1) + i] = pack_bf16x2(p0, p1);
+              }
+            } else {  // keys that no row of the warp sees
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[16 * (c & 1) + i] = 0u;
+            }
+            if (c & 1) {  // 64 keys: their product may begin
+              tmem_st32(tS + 16 * (c - 1), pk);
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(BAR(P_FULL + 2 * t + (c >> 1)));
+            }
+          }
+          float s0, s1;
+          f2_unpack(f2_add(acc[0], acc[1]), s0, s1);
+          l = fmaf(l, alpha, s0 + s1);
+        } else {
+          tc_fence_before();
+          mbar_arrive(BAR(P_FULL + 2 * t));
+          mbar_arrive(BAR(P_FULL + 2 * t + 1));
         }
-        tc_fence_before();
-        mbar_arrive(BAR(P_FULL + t));
       }
       if (!ok) break;
       n0 += pair ? 2 * tiles : tiles;
       it0 += tiles;
       // ---------------------------------------------------------- results of the run
       const int h = s.head * p.heads + my_head;
-      const long long place = s.whole ? (long long)(2 * s.kind + (pair ? 0 : side)) * rows + (long long)tok * p.Hq + h
-                                      : 4 * rows + ((long long)s.slot * 2 + side) * 128 + r;
+      const long long place = s.side == 0 ? s.place + (pair ? 0 : side) * rows + (long long)tok * p.Hq + h
+                                          : s.place + side * s.side + r;
       if (x_first >= tiles) {  // one tile of keys: the other run has none
         if (valid) p.part_lse[place] = -INFINITY;
         continue;
       }
-      ok = mbar_wait(BAR(O_FINAL + t), runs & 1, w, 84);
+      ok = mbar_wait(BAR(O_FINAL + t), runs & 1, w, 87);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
@@ -708,62 +876,103 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- merge
 
 // A warp per query row: the results of the group's shared keys and of the
-// request's own.  A part without mass has lse = -inf, and its O is not read.
+// request's own.  Lane i looks at part i; a part without mass has lse = -inf, and
+// its O is not read.
 template <int D>
 __global__ void __launch_bounds__(256) fa_decode_shared_merge_kernel(const __grid_constant__ SharedParams p) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const long long rows = (long long)p.B * p.Nq * p.Hq, x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done
   if (x >= rows) return;
   const long long token = div_ll(x, p.Hq);
   const int tok = (int)token, h = (int)(x - token * p.Hq), head = h / p.heads, b = tok / p.Nq;
-  const long long total = *p.plan.total, each = div_ll(total, p.shares), more = total - each * p.shares;
-  auto share_of = [&](long long s) {
-    return (int)(s < more * (each + 1) ? div_ll(s, each + 1) : more + div_ll(s - more * (each + 1), each));
-  };
+  // (the plan, which the main kernel's CTAs have all waited for; read past L1)
+  const int2 entries = __ldcg(p.plan.of_request + b);
+  // parts of each kind: n of them, `runs` in each of the shares from `first` on
+  int n[2] = {0, 0}, runs[2] = {1, 1}, first[2] = {0, 0};
+  long long base[2] = {0, 0}, begin[2] = {0, 0};  // place of the first part, or of the row in a slot; the unit's begin
+  bool cut[2] = {false, false};
+  const longlong2 h0 = __ldcg(reinterpret_cast<const longlong2*>(p.plan.head)),
+                  h1 = __ldcg(reinterpret_cast<const longlong2*>(p.plan.head) + 1);
+  SharedHead totals;
+  totals.total[0] = h0.x, totals.total[1] = h0.y, totals.total[2] = h1.x;
+  totals.shares[0] = (int)h1.y, totals.shares[1] = (int)(h1.y >> 32), totals.shares[2] = __ldcg(&p.plan.head->shares[2]);
+  const Deal deals[2] = {deal_of(totals, 0), deal_of(totals, 1)};
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    const int e = kind == 0 ? entries.x : entries.y;
+    if (e < 0) continue;
+    const SharedList& list = kind ? p.plan.own : p.plan.shared;
+    const SharedEntry* at = list.entry + e;
+    const int tok0 = __ldcg(&at->tok0), ntok = __ldcg(&at->ntok), tiles = __ldcg(&at->tiles);
+    const long long cum = __ldcg(list.cum + e);
+    const Weight wt = weight_of(p, ntok);
+    const int weight = wt.lead + wt.tile * tiles, chunks = chunks_of(p, ntok);
+    const int c = (tok - tok0) / (2 * p.tile_tokens), in = tok - tok0 - c * 2 * p.tile_tokens;
+    const bool pair = ntok - c * 2 * p.tile_tokens > p.tile_tokens;
+    begin[kind] = cum + (long long)weight * ((long long)head * chunks + c);
+    first[kind] = deals[kind].of(begin[kind] + wt.lead);
+    const int last = deals[kind].of(begin[kind] + weight - wt.tile);  // where the last tile begins
+    cut[kind] = first[kind] != last;
+    runs[kind] = pair ? 1 : 2;
+    n[kind] = (last - first[kind] + 1) * runs[kind];
+    const int side = in / p.tile_tokens;
+    base[kind] = cut[kind] ? 4 * rows + (kind ? 512ll * p.shares : 0) + side * (kind ? p.own_side : kSharedTile) +
+                                 (in - side * p.tile_tokens) * p.heads + h - head * p.heads
+                           : 2 * kind * rows + x;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done
   float acc[E], mass = 0.f, m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < E; ++i) acc[i] = 0.f;
-  auto add = [&](long long place) {
-    const float lc = p.part_lse[place];
-    if (lc == -INFINITY) return;
-    const float* src = p.part_o + place * D + lane * E;
-    float v[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = src[i];
-    const float mn = fmaxf(m, lc), ref = mn == -INFINITY ? 0.f : mn;  // (lc may be NaN)
-    const float al = ex2_sfu(m - ref), f = ex2_sfu(lc - ref);
-    m = mn;
-    mass = fmaf(mass, al, f);
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = fmaf(acc[i], al, f * v[i]);
-  };
-  const int g = p.plan.group[b];
-#pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    const int e = kind == 0 ? (g >= 0 ? p.plan.of_group[g] : -1) : p.plan.of_request[b];
-    if (e < 0) continue;
-    const SharedEntry ent = p.plan.entry[e];
-    const int weight = ent.tiles + p.lead, chunks = chunks_of(p, ent.ntok);
-    const int c = (tok - ent.tok0) / (2 * p.tile_tokens), in = tok - ent.tok0 - c * 2 * p.tile_tokens;
-    const bool pair = ent.ntok - c * 2 * p.tile_tokens > p.tile_tokens;
-    const long long u0 = p.plan.cum[e] + (long long)weight * ((long long)head * chunks + c);
-    const int first = share_of(u0 + p.lead), last = share_of(u0 + weight - 1);
-    if (first == last) {
-      add((2 * kind) * rows + x);
-      if (!pair) add((2 * kind + 1) * rows + x);
-      continue;
+  for (int i0 = 0; i0 < n[0] + n[1]; i0 += 32) {
+    float lc = -INFINITY;
+    long long place = 0;
+    if (i0 + lane < n[0] + n[1]) {
+      const bool own_part = i0 + lane >= n[0];
+      const int i = i0 + lane - (own_part ? n[0] : 0);
+      const bool two = (own_part ? runs[1] : runs[0]) == 2;
+      const int run = two ? i & 1 : 0, k = (own_part ? first[1] : first[0]) + (two ? i >> 1 : i);
+      // a cut unit's: of the share's last piece, if it begins before the unit, or its first
+      const long long slot = 2 * (long long)k + (own_part ? deals[1].begin(k) < begin[1] : deals[0].begin(k) < begin[0]);
+      const int side = own_part ? p.own_side : kSharedTile;
+      place = (own_part ? base[1] : base[0]) + ((own_part ? cut[1] : cut[0]) ? slot * 2 * side + run * side : run * rows);
+      lc = p.part_lse[place];
     }
-    const int side = in / p.tile_tokens, r = (in - side * p.tile_tokens) * p.heads + h - head * p.heads;
-    for (int k = first; k <= last; ++k) {
-      // the share's last piece, if it begins before the unit, or its first
-      const long long slot = 2 * (long long)k + (each * k + (k < more ? k : more) < u0 ? 1 : 0);
-      if (pair) {
-        add(4 * rows + (slot * 2 + side) * 128 + r);
-      } else {
-        add(4 * rows + slot * 256 + r);
-        add(4 * rows + slot * 256 + 128 + r);
+    float top = lc;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));  // (a NaN is left out)
+    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn, al = ex2_sfu(m - ref);
+    m = mn;
+    mass *= al;
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] *= al;
+    const float f = ex2_sfu(lc - ref);
+    unsigned todo = __ballot_sync(0xffffffffu, lc != -INFINITY);
+    while (todo) {
+      constexpr int U = 4;  // loads at a time
+      float v[U][E], fu[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int from = todo ? __ffs(todo) - 1 : 0;
+        const long long at = __shfl_sync(0xffffffffu, place, from);
+        const float w = __shfl_sync(0xffffffffu, f, from);
+        fu[u] = todo ? w : 0.f;
+        if (todo) {
+          const float* src = p.part_o + at * D + lane * E;
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[u][i] = src[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[u][i] = 0.f;
+        }
+        todo &= todo - 1;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        mass += fu[u];
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = fmaf(fu[u], v[u][i], acc[i]);
       }
     }
   }
@@ -789,19 +998,24 @@ static size_t plan_layout(SharedPlan* plan, void* at, int B, int G, int shares) 
     return here;
   };
   SharedPlan pl;
-  const size_t n = (size_t)B + G;
-  pl.total = reinterpret_cast<long long*>(take(8));
-  pl.count = reinterpret_cast<int*>(take(4));
-  pl.entry = reinterpret_cast<SharedEntry*>(take(sizeof(SharedEntry) * (n + G)));  // (and the groups', before they have a place)
-  pl.cum = reinterpret_cast<long long*>(take(8 * (n + 1)));
-  pl.of_group = reinterpret_cast<int*>(take(4 * (size_t)G));
-  pl.of_request = reinterpret_cast<int*>(take(4 * (size_t)B));
-  pl.group = reinterpret_cast<int*>(take(4 * (size_t)B));
+  pl.head = reinterpret_cast<SharedHead*>(take(sizeof(SharedHead)));
+  auto list = [&](SharedList& l, size_t entries, size_t starts) {
+    l.entry = reinterpret_cast<SharedEntry*>(take(sizeof(SharedEntry) * entries));
+    l.cum = reinterpret_cast<long long*>(take(8 * entries));
+    l.start = reinterpret_cast<SharedStart*>(take(sizeof(SharedStart) * starts));
+  };
+  list(pl.shared, G, shares);
+  list(pl.own, B, (size_t)kOwnShares * shares);
+  pl.of_request = reinterpret_cast<int2*>(take(8 * (size_t)B));
   pl.g_shared = reinterpret_cast<int*>(take(4 * (size_t)G));
-  pl.start_entry = reinterpret_cast<int*>(take(4 * (size_t)shares));
-  pl.start_off = reinterpret_cast<long long*>(take(8 * (size_t)shares));
+  pl.g_least = reinterpret_cast<int*>(take(4 * (size_t)G));
+  pl.g_most = reinterpret_cast<unsigned long long*>(take(8 * (size_t)G));
   if (plan != nullptr) *plan = pl;
   return off;
+}
+int shared_own_side(int Nq, int heads) { return Nq * heads < kSharedTile ? Nq * heads : kSharedTile; }
+size_t shared_part_rows(int B, int Nq, int Hq, int heads, int shares) {
+  return 4 * (size_t)B * Nq * Hq + 512 * (size_t)shares + 4 * (size_t)shared_own_side(Nq, heads) * kOwnShares * shares;
 }
 size_t shared_plan_bytes(int B, int G, int shares) { return plan_layout(nullptr, nullptr, B, G, shares); }
 void shared_plan_at(SharedPlan& plan, void* at, int B, int G, int shares) { plan_layout(&plan, at, B, G, shares); }

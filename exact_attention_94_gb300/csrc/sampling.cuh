@@ -43,20 +43,32 @@ struct SharedEntry {
   int lo, end;         // keys
   int all_lo, all_hi;  // the keys that every query token (of a request with keys) sees, if any
   int tiles;           // of 128 keys from lo rounded down to a TMA box
-  int kind;            // 0: a group's shared keys, 1: a request's own
+};
+// A share of a list of entries: where it begins, and how much it weighs.
+struct SharedStart {
+  long long begin, size, off;  // off: within its first entry
+  int e, count;                // that entry's number; entries of the list
+  SharedEntry entry;
+};
+struct SharedList {
+  SharedEntry* entry;  // those that have keys
+  long long* cum;      // weight before each
+  SharedStart* start;  // of each share
+};
+struct SharedHead {
+  long long total[3];  // weight of shared keys, of own keys dealt early, and late
+  int shares[3];       // they are dealt to
+  int queue;           // shares of own keys that CTAs have taken
 };
 // What a call's first kernel leaves for the others, in the workspace.
 struct SharedPlan {
-  int* count;          // [1] entries that have keys
-  long long* total;    // [1] weight of all
-  SharedEntry* entry;  // [G + B]
-  long long* cum;      // [G + B + 1] weight before each entry
-  int* of_group;       // [G] entry of its shared keys, -1: none
-  int* of_request;     // [B] entry of its own keys
-  int* group;          // [B] its group
-  int* g_shared;       // [G] keys that the group shares (as used)
-  int* start_entry;    // [shares] where each share begins
-  long long* start_off;
+  SharedHead* head;
+  SharedList shared;   // [G], shares: one for each CTA at most
+  SharedList own;      // [B]
+  int2* of_request;    // [B] entries of its group's shared keys and of its own, -1: none
+  int* g_shared;       // [G] keys that the group shares, its shortest request's (with keys), its longest's: where
+  int* g_least;        //   groups are too many for the first kernel's shared memory
+  unsigned long long* g_most;
 };
 struct SharedParams {
   const int* block_table;    // [B, max_blocks]
@@ -65,24 +77,49 @@ struct SharedParams {
   const int* shared_lens;    // [G]
   void* o;                   // [B, Nq, Hq, d] bf16
   float* lse;                // [B, Hq, Nq]
-  float* part_o;             // results of units inside one share, [4][rows][d] (shared / own keys, two runs each), then of
-  float* part_lse;           //   the pieces that a share's borders cut, [2 * shares][2][128][d]: each normalised; log2 of its mass
+  float* part_o;             // results of units inside one share, [4][rows][d] (shared / own keys, two runs each), then of the
+  float* part_lse;           //   pieces that shares' borders cut, two a share, [2][128][d] of shared keys, [2][own_side][d] of
+                             //   own: each normalised; log2 of its mass
   SharedPlan plan;
   int B, Nq, Hq, Hkv, heads; // heads: query heads of a K/V head
   int G, tile_tokens;        // groups; query tokens of a tile of rows
   int page_size, num_pages, max_blocks, max_len;
   int win_left;              // -1: no window
   int box_rows;              // keys per TMA box: 16 .. 128, divides the page and the tile
-  int shares, lead;          // tiles that a unit counts for its start and end
+  int shares;                // CTAs
+  int own_side;              // rows of a cut piece's run of own keys
   float scale_log2, tau;
   unsigned* err;
   unsigned long long timeout_ns;
 };
+int shared_own_side(int Nq, int heads);
+size_t shared_part_rows(int B, int Nq, int Hq, int heads, int shares);
 size_t shared_plan_bytes(int B, int G, int shares);
 void shared_plan_at(SharedPlan& plan, void* at, int B, int G, int shares);
 bool make_tmap_queries(CUtensorMap* m, const void* ptr, int D, int Hq, long long tokens, int heads, int tile_tokens);
 bool make_tmap_pages(CUtensorMap* m, const void* ptr, int D, int Hkv, int page_size, int num_pages, int box_rows);
 cudaError_t launch_decode_shared(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p,
                                  int D, cudaStream_t stream);
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, int c3,
+                                            int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
+      "[%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+// Whether the phase with the given parity has completed (mbar_try_wait may wait a while for it).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 }  // namespace fa
