@@ -1077,7 +1077,7 @@ size_t fa_decode_shared_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, i
   if (num_shares == 0) num_shares = shared_auto_shares();
   const size_t rows = shared_part_rows(B, Nq, Hq, Hq / Hkv, num_shares);
   return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float)) +
-         align256(shared_plan_bytes(B, num_groups, num_shares));
+         align256(shared_plan_bytes(B, num_groups));
 }
 
 // What the calls over either cache have in common: sizes, pointers, the parameters.
@@ -1103,13 +1103,14 @@ static fa_status shared_common(SharedParams& p, CUtensorMap& tq, const void* q, 
   p.seq_lens = seq_lens;
   p.starts = group_starts;
   p.shared_lens = shared_lens;
+  p.q = q;
   p.o = o;
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws);
   ws += align256(rows * d * sizeof(float));
   p.part_lse = reinterpret_cast<float*>(ws);
   ws += align256(rows * sizeof(float));
-  shared_plan_at(p.plan, ws, B, num_groups, num_shares);
+  shared_plan_at(p.plan, ws, B, num_groups);
   p.B = B, p.Nq = Nq, p.Hq = Hq, p.Hkv = Hkv, p.heads = Hq / Hkv;
   p.G = num_groups;
   p.tile_tokens = kSharedTile / p.heads;
@@ -1118,7 +1119,7 @@ static fa_status shared_common(SharedParams& p, CUtensorMap& tq, const void* q, 
   p.box_rows = 16;
   while (p.box_rows < kSharedTile && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
   p.shares = num_shares;
-  p.own_side = shared_own_side(Nq, p.heads);
+  p.few = shared_few(Nq, p.heads);
   p.scale_log2 = scale * kLog2e;
   p.tau = g_opt.tau;
   p.err = g_err_ptr;
@@ -1134,15 +1135,15 @@ fa_status fa_decode_paged_shared(const void* q, const void* k_pages, const void*
   if (!k_pages || !v_pages || (long long)num_pages * (page_size / 8) > 0x7fffffffll) return FA_ERR_INVALID_ARG;
   if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_MISALIGNED;
   SharedParams p{};
-  CUtensorMap tq, tk, tv;
-  const fa_status st = shared_common(p, tq, q, block_table, seq_lens, group_starts, shared_lens, o, lse, B, Nq, Hq, Hkv, d,
+  CUtensorMap maps[5];
+  const fa_status st = shared_common(p, maps[0], q, block_table, seq_lens, group_starts, shared_lens, o, lse, B, Nq, Hq, Hkv, d,
                                      page_size, num_pages, max_blocks, max_seq_len, num_groups, window_left, num_shares,
                                      workspace, scale);
   if (st != FA_OK) return st;
-  if (!make_tmap_pages(&tk, k_pages, d, Hkv, page_size, num_pages, p.box_rows) ||
-      !make_tmap_pages(&tv, v_pages, d, Hkv, page_size, num_pages, p.box_rows))
-    return FA_ERR_INVALID_ARG;
-  return launch_decode_shared(tq, tk, tv, p, d, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  for (int i = 0; i < 4; ++i)
+    if (!make_tmap_pages(&maps[1 + i], i & 1 ? v_pages : k_pages, d, Hkv, page_size, num_pages, i < 2 ? p.box_rows : 16))
+      return FA_ERR_INVALID_ARG;
+  return launch_decode_shared(maps, p, d, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -41,13 +41,18 @@ namespace fa {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-// What units of one and of two tiles of rows weigh (half microseconds, about).
-constexpr int kLeadOne = 5, kTileOne = 2, kLeadTwo = 12, kTileTwo = 3;
-constexpr int kLateShares = 4, kOwnShares = 1 + kLateShares;  // of own keys, for each CTA at most: late ones, all
-constexpr int kLate = 8;           // one in kLate of all work is own keys that are dealt late
-constexpr int kLateShare = 12;     //   in shares that weigh so much at least
-constexpr int kPlanSmem = 1024;  // groups, entries in the plan's shared memory
-constexpr int kPieces = 6;  // announced ahead
+// What units weigh.  Of many rows, in half microseconds about: of one and of two tiles of
+// rows, and each of their tiles of keys.  Of few rows: their start and end, in 16 keys.
+constexpr int kLeadOne = 5, kTileOne = 2, kLeadTwo = 12, kTileTwo = 3, kLeadFew = 6;
+constexpr float kFew = 0.17f;                  // of a CTA's half microseconds 16 keys of few rows take, d = 128
+constexpr int kWarps = 8;                      // of a CTA, that attend for few rows
+constexpr int kFewEarly = 8, kFewLate = 16;    // shares of few rows for each CTA at most, that warps begin with and that they take
+constexpr int kFewLateOf = 2;                  // one in so many of few rows' weight is dealt late,
+constexpr int kFewLateFrom = 64;               //   where a warp's share is this much at least
+constexpr int kFewLeast = 8, kFewLateLeast = 24;  // weight of those shares at least
+constexpr int kPlanSmem = 1024;                // groups, entries in the plan's shared memory
+constexpr int kMergeRows = 8;                  // of a warp of the merge
+constexpr int kPieces = 6;                     // announced ahead
 
 template <int D>
 struct SharedLayout {
@@ -57,8 +62,14 @@ struct SharedLayout {
   static constexpr uint32_t kQOff = 0;              // two tiles of Q
   static constexpr uint32_t kKVOff = 2 * kTile;
   static constexpr uint32_t kMiscOff = kKVOff + kStages * kTile;
-  static constexpr uint32_t kBytes = kMiscOff + 1024 + 1024;  // pieces, barriers; alignment slack
+  static constexpr uint32_t kMisc = D == 64 ? 3072 : 2048;   // barriers, pieces
+  static constexpr uint32_t kBytes = kMiscOff + kMisc + 1024;  // alignment slack
+  // Warps that attend for few rows, once the tiles are done with: of each a ring of 16 keys
+  // and values, and queries.
+  static constexpr uint32_t kWarpBytes = kMiscOff / kWarps / 1024 * 1024;
+  static constexpr uint32_t kFewTile = 16u * D * 2u;
 };
+static_assert(SharedLayout<128>::kBytes <= 227 * 1024 && SharedLayout<64>::kBytes <= 227 * 1024, "shared memory");
 constexpr int kThreads = 384;
 
 // Tiles t0 .. t1 - 1 of a unit, as the walk announces them; t0 = t1 marks the end.
@@ -73,19 +84,16 @@ struct Piece {
   int t0, t1, pad;
 };
 
-__device__ __forceinline__ int chunks_of(const SharedParams& p, int ntok) {  // of 256 rows
-  return (ntok + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
-}
-__device__ __forceinline__ long long units_of(const SharedParams& p, int ntok) {
-  return (long long)p.Hkv * chunks_of(p, ntok);
+__device__ __forceinline__ int chunks_of(const SharedParams& p, bool few, int ntok) {  // of 256 rows
+  return few ? 1 : (ntok + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
 }
 // What a unit weighs: its start and end, and each of its tiles of keys.  Slot
 // lead + tile * t of its weight is where tile t begins.
 struct Weight {
   int lead, tile;
 };
-__device__ __forceinline__ Weight weight_of(const SharedParams& p, int ntok) {
-  return ntok > p.tile_tokens ? Weight{kLeadTwo, kTileTwo} : Weight{kLeadOne, kTileOne};
+__device__ __forceinline__ Weight weight_of(const SharedParams& p, bool few, int ntok) {
+  return few ? Weight{kLeadFew, 1} : ntok > p.tile_tokens ? Weight{kLeadTwo, kTileTwo} : Weight{kLeadOne, kTileOne};
 }
 
 // a / b for a >= 0, b > 0, in 32 bits where both fit
@@ -113,9 +121,61 @@ struct Deal {
     return slot < early.total ? early.of(slot) : early.n + late.of(slot - early.total);
   }
 };
-__device__ __forceinline__ Deal deal_of(const SharedHead& h, int kind) {
-  return kind ? Deal{Equal(h.total[1], h.shares[1]), Equal(h.total[2], h.shares[2])}
-              : Deal{Equal(h.total[0], h.shares[0]), Equal(0, 0)};
+__device__ __forceinline__ Deal deal_of(const SharedHead& h, bool few) {
+  return few ? Deal{Equal(h.total[1], h.shares[1]), Equal(h.total[2], h.shares[2])}
+             : Deal{Equal(h.total[0], h.shares[0]), Equal(0, 0)};
+}
+
+// The units' pieces of a share, one after the other.
+struct Walk {
+  const SharedEntry* entries;
+  SharedEntry ent, ahead;
+  long long begin, at, to, off;
+  int e, count;
+  // Share k of a list of n entries; called by whole warps.
+  __device__ __forceinline__ void start(const SharedList& list, int n, const Deal& deal, int k) {
+    begin = at = deal.begin(k), to = deal.begin(k + 1);
+    int lo = 0, hi = n;  // the last entry that begins at or before it: 32 at a time
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, i = lo + lane_id() * step;
+      const unsigned votes = __ballot_sync(0xffffffffu, i < hi && list.cum[i] <= at);
+      lo += (__popc(votes) - 1) * step;
+      hi = min(hi, lo + step);
+    }
+    entries = list.entry;
+    e = lo, count = n;
+    ent = entries[e];
+    off = at - list.cum[e];
+    if (e + 1 < count) ahead = entries[e + 1];
+  }
+  // Tiles t0 .. t1 - 1 of unit u of `ent`; later: the unit begins behind the share's first slot.  False: the share is over.
+  __device__ __forceinline__ bool next(const SharedParams& p, bool few, int& u, int& t0, int& t1, bool& later) {
+    while (at < to) {
+      const Weight wt = weight_of(p, few, ent.ntok);
+      const int weight = wt.lead + wt.tile * ent.tiles, chunks = chunks_of(p, few, ent.ntok);
+      if (off >= (long long)weight * p.Hkv * chunks) {
+        off = 0;
+        ++e;
+        ent = ahead;
+        if (e + 1 < count) ahead = entries[e + 1];
+        continue;
+      }
+      u = (int)div_ll(off, weight);
+      const int w0 = (int)(off - (long long)u * weight), w1 = (int)(to - at < weight - w0 ? w0 + (to - at) : weight);
+      later = w0 == 0 && at > begin;
+      off += w1 - w0;
+      at += w1 - w0;
+      t0 = w0 <= wt.lead ? 0 : (w0 - wt.lead + wt.tile - 1) / wt.tile;
+      t1 = w1 <= wt.lead ? 0 : (w1 - wt.lead + wt.tile - 1) / wt.tile;
+      if (t0 < t1) return true;
+    }
+    return false;
+  }
+};
+// Place of the results of a share's cut pieces (two: it begins inside a unit, or it ends inside one).
+__device__ __forceinline__ long long cut_place(const SharedParams& p, bool few, int k, bool later) {
+  const long long rows = (long long)p.B * p.Nq * p.Hq, slot = 2 * (long long)k + (later ? 1 : 0);
+  return 4 * rows + (few ? 512ll * p.shares + slot * p.few : slot * 2 * kSharedTile);
 }
 
 }  // namespace
@@ -123,11 +183,11 @@ __device__ __forceinline__ Deal deal_of(const SharedHead& h, int kind) {
 // ---------------------------------------------------------------- plan
 
 __global__ void __launch_bounds__(kPlanThreads, 1) fa_shared_plan_kernel(const __grid_constant__ SharedParams p) {
-  __shared__ long long s_w[32];
-  __shared__ int s_n[32];
+  __shared__ long long s_w[2][32];
+  __shared__ int s_n[2][32];
   __shared__ int s_starts[kPlanSmem + 1], s_shared[kPlanSmem], s_least[kPlanSmem];
+  __shared__ int s_of[kPlanSmem];
   __shared__ unsigned long long s_most[kPlanSmem];
-  __shared__ long long s_cum[2][kPlanSmem];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const SharedPlan& pl = p.plan;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -135,8 +195,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fa_shared_plan_kernel(const _
   const int* starts = small ? s_starts : p.starts;
   int *least = small ? s_least : pl.g_least, *shared = small ? s_shared : pl.g_shared;
   unsigned long long* most = small ? s_most : pl.g_most;  // longest length, and the first request that has it
-  int* of_group = small ? s_shared : pl.g_shared;         // (in the shared lengths' places, at the end)
-  const int len0 = tid < p.B ? p.seq_lens[tid] : 0;       // (asked for early)
+  int* of_group = small ? s_of : pl.g_of;                 // its entry of shared keys
+  const int len0 = tid < p.B ? p.seq_lens[tid] : 0;       // (asked for early; of the thread's first entry too)
+  const int len1 = tid >= p.G && tid - p.G < p.B ? p.seq_lens[tid - p.G] : 0;
   // groups that do not cut the batch into runs are reported, and nothing counts as shared
   bool bad = false;
   for (int g = tid; g <= p.G; g += kPlanThreads) {
@@ -163,7 +224,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fa_shared_plan_kernel(const _
     }
     return g;
   };
-  auto length = [&](int b) { return min(max(b < kPlanThreads ? len0 : p.seq_lens[b], 0), p.max_len); };
   // each group's longest request and shortest with keys
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -193,156 +253,124 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fa_shared_plan_kernel(const _
     }
   }
   __syncthreads();
-  auto tile_count = [&](int lo, int end) {
-    return lo < end ? (end - lo / p.box_rows * p.box_rows + kSharedTile - 1) / kSharedTile : 0;
-  };
   // keys that group g shares, as used: none for a request alone, whose keys are all its own
   auto shares_of = [&](int g) {
     const int n = starts[g + 1] - starts[g] < 2 ? 0 : shared[g];
     return min(n, (int)(most[g] >> 32));
   };
-  // A list of entries, a block's threads at a time: those that have keys get the next places.
-  long long total = 0;
-  int count = 0;
-  auto place = [&](const SharedList& list, long long* cum, const SharedEntry& e) {
-    const bool on = e.tiles > 0;
-    const Weight u = weight_of(p, e.ntok);
-    const long long w = on ? (u.lead + (long long)u.tile * e.tiles) * units_of(p, e.ntok) : 0;
-    long long sum = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += x;
-    }
-    const unsigned votes = __ballot_sync(0xffffffffu, on);
-    __syncthreads();  // (the last call's have been read)
-    if (lane == 31) s_w[warp] = sum, s_n[warp] = __popc(votes);
-    __syncthreads();
-    long long ws = s_w[lane];
-    int ns = s_n[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, ws, o);
-      const int y = __shfl_up_sync(0xffffffffu, ns, o);
-      if (lane >= o) ws += x, ns += y;
-    }
-    const long long ahead_w = __shfl_sync(0xffffffffu, ws, (warp + 31) & 31);
-    const int ahead_n = __shfl_sync(0xffffffffu, ns, (warp + 31) & 31);
-    const int at = count + (warp > 0 ? ahead_n : 0) + __popc(votes & ((1u << lane) - 1u));
-    const long long before = total + (warp > 0 ? ahead_w : 0) + sum - w;
-    if (on) {
-      list.entry[at] = e;
-      list.cum[at] = before;
-      if (at < kPlanSmem) cum[at] = before;
-    }
-    total += __shfl_sync(0xffffffffu, ws, 31);
-    count += __shfl_sync(0xffffffffu, ns, 31);
-    return on ? at : -1;
-  };
-  // groups' shared keys
-  for (int g0 = 0; g0 < p.G; g0 += kPlanThreads) {
-    const int g = g0 + tid;
+  // Entries: groups' shared keys, then requests' own, a block's threads at a time.  Those that
+  // have keys get the next places of their list.
+  long long total[2] = {0, 0};
+  int count[2] = {0, 0};
+  for (int i0 = 0; i0 < p.G + p.B; i0 += kPlanThreads) {
+    const int g = i0 + tid, b = g - p.G;
     SharedEntry e{};
-    int n = 0;
-    if (g < p.G && grouped) {
-      n = shares_of(g);
+    int n = 0, of = -1;  // n: keys that the group shares; of: a request's group
+    if (b < 0) {
+      n = grouped ? shares_of(g) : 0;
       if (n > 0) {
         const int b0 = starts[g], top = (int)(most[g] >> 32), low = least[g];
-        e = {b0 * p.Nq, (starts[g + 1] - b0) * p.Nq, 0x7fffffff - (int)(unsigned)most[g], 0, n, 0, 0, 0};
+        e = {b0 * p.Nq, (starts[g + 1] - b0) * p.Nq, 0x7fffffff - (int)(unsigned)most[g], 0, n, 0, 0, 0, 0};
         if (p.win_left >= 0) {
           e.lo = max(0, low - p.Nq - p.win_left);
           e.all_lo = top - 1 - p.win_left;
         }
         e.all_lo = max(e.all_lo, e.lo);
         e.all_hi = min(n, low - p.Nq + 1);
-        e.tiles = tile_count(e.lo, n);
       }
-    }
-    const int at = place(pl.shared, s_cum[0], e);
-    if (g < p.G) {
-      least[g] = n;     // from here on: keys that the group shares,
-      of_group[g] = at; //   and its entry
-    }
-  }
-  const long long total_shared = total;
-  const int count_shared = count;
-  total = 0, count = 0;
-  __syncthreads();
-  // requests' own
-  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    SharedEntry e{};
-    int common = -1;
-    if (b < p.B) {
-      const int n = length(b), g = grouped ? group_of(b) : -1;
-      e = {b * p.Nq, p.Nq, b, 0, n, 0, 0, 0};
-      if (g >= 0) {
-        e.lo = min(least[g], n);
-        common = of_group[g];
-      }
+    } else if (b < p.B) {
+      const int len = min(max(i0 == 0 ? len1 : p.seq_lens[b], 0), p.max_len);
+      if (grouped) of = group_of(b);
+      e = {b * p.Nq, p.Nq, b, of >= 0 ? min(shares_of(of), len) : 0, len, 0, 0, 0, 1};
       if (p.win_left >= 0) {
-        e.lo = max(e.lo, n - p.Nq - p.win_left);
-        e.all_lo = n - 1 - p.win_left;
+        e.lo = max(e.lo, len - p.Nq - p.win_left);
+        e.all_lo = len - 1 - p.win_left;
       }
       e.all_lo = max(e.all_lo, e.lo);
-      e.all_hi = n - p.Nq + 1;
-      e.tiles = tile_count(e.lo, n);
+      e.all_hi = len - p.Nq + 1;
+      if (len == 0) of = -1;  // (all_lo, all_hi of the shared keys leave it out)
     }
-    const int at = place(pl.own, s_cum[1], e);
-    if (b < p.B) pl.of_request[b] = make_int2(common, at);
-  }
-  // Shares, no shorter than a tile each (or a unit's piece could be empty).  Shared
-  // keys and most of the own go to CTAs in proportion to what they weigh; the rest of
-  // the own to many small shares, which CTAs take as they come to an end.
-  SharedHead head{};
-  head.total[0] = total_shared;
-  head.total[2] = min(total, (total_shared + total) / kLate);
-  head.total[1] = total - head.total[2];
-  const float part = (float)total_shared / (float)max(total_shared + head.total[1], 1ll);
-  auto shares_in = [&](long long most, long long weight, int least) { return (int)min(most, weight / least); };
-  head.shares[0] = shares_in(min((long long)p.shares, (long long)(part * (float)p.shares + 0.999f)), total_shared, kTileTwo);
-  head.shares[1] = shares_in(head.total[1] > 0 ? max(p.shares - head.shares[0], 1) : 0, head.total[1], kTileTwo);
-  if (head.shares[1] == 0) head.total[2] += head.total[1], head.total[1] = 0;
-  head.shares[2] = shares_in((long long)kLateShares * p.shares, head.total[2], kLateShare);
-  if (head.total[2] > 0 && head.shares[2] == 0) {
-    if (head.shares[1] > 0) head.total[1] += head.total[2], head.total[2] = 0;
-    else head.shares[2] = 1;
-  }
-  head.queue = p.shares - head.shares[0];  // (shares of own keys that CTAs begin with)
-  if (tid == 0) *pl.head = head;
-  __syncthreads();
-  // where they begin
-#pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    const SharedList& list = kind ? pl.own : pl.shared;
-    const int n = kind ? count : count_shared, shares = kind ? head.shares[1] + head.shares[2] : head.shares[0];
-    const long long* cum = n <= kPlanSmem ? s_cum[kind] : list.cum;
-    const Deal deal = deal_of(head, kind);
-    for (int k = tid; k < shares; k += kPlanThreads) {
-      const long long at = deal.begin(k);
-      int a = 0, z = n;  // the last entry that begins at or before it
-      while (z - a > 1) {
-        const int m = (a + z) / 2;
-        if (cum[m] <= at) a = m; else z = m;
+    const bool few = (long long)e.ntok * p.heads <= p.few;
+    if (e.lo < e.end) e.tiles = few ? (e.end - e.lo / 16 * 16 + 15) / 16 : (e.end - e.lo / p.box_rows * p.box_rows + kSharedTile - 1) / kSharedTile;
+    const Weight u = weight_of(p, few, e.ntok);
+    const long long w = e.tiles > 0 ? (u.lead + (long long)u.tile * e.tiles) * p.Hkv * chunks_of(p, few, e.ntok) : 0;
+    int at = -1;
+    long long sum[2];
+    unsigned votes[2];
+#pragma unroll
+    for (int l = 0; l < 2; ++l) {
+      sum[l] = few == (l == 1) ? w : 0;
+      votes[l] = __ballot_sync(0xffffffffu, sum[l] > 0);
+      if (votes[l] != 0) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, sum[l], o);
+          if (lane >= o) sum[l] += x;
+        }
       }
-      SharedStart start{};
-      start.begin = at;
-      start.size = deal.begin(k + 1) - at;
-      start.off = at - cum[a];
-      start.e = a;
-      start.count = n;
-      start.entry = list.entry[a];
-      list.start[k] = start;
+      if (lane == 31) s_w[l][warp] = sum[l], s_n[l][warp] = __popc(votes[l]);
     }
+    __syncthreads();
+#pragma unroll
+    for (int l = 0; l < 2; ++l) {
+      long long ws = s_w[l][lane], before = total[l];
+      int ns = s_n[l][lane], place = count[l];
+      if (__any_sync(0xffffffffu, ns > 0)) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, ws, o);
+          const int y = __shfl_up_sync(0xffffffffu, ns, o);
+          if (lane >= o) ws += x, ns += y;
+        }
+        const long long ahead_w = __shfl_sync(0xffffffffu, ws, (warp + 31) & 31);
+        const int ahead_n = __shfl_sync(0xffffffffu, ns, (warp + 31) & 31);
+        if (warp > 0) before += ahead_w, place += ahead_n;
+        total[l] += __shfl_sync(0xffffffffu, ws, 31);
+        count[l] += __shfl_sync(0xffffffffu, ns, 31);
+      }
+      if (w > 0 && few == (l == 1)) {
+        place += __popc(votes[l] & ((1u << lane) - 1u));
+        pl.list[l].entry[place] = e;
+        pl.list[l].cum[place] = before + sum[l] - w;
+        at = 2 * place + l;
+      }
+    }
+    if (b < 0) of_group[g] = at;
+    __syncthreads();  // (groups come before requests, and every warp has read the sums)
+    if (b >= 0 && b < p.B) pl.of_request[b] = make_int2(of >= 0 ? of_group[of] : -1, at);
   }
+  // Shares.  Of many rows one for each of so many CTAs as their part of all work is, no
+  // shorter than a tile (or a unit's piece could be empty).  Of few rows one for each warp of
+  // the others, and the rest in smaller ones, which warps take as they come to an end.
+  SharedHead head{};
+  auto shares_in = [&](long long most, long long weight, int least) { return (int)min(most, weight / least); };
+  const float few_time = (float)total[1] * p.few_cost;
+  const float part = (float)total[0] / fmaxf((float)total[0] + few_time, 1.f);
+  head.total[0] = total[0];
+  head.shares[0] = shares_in(min((long long)p.shares, (long long)(part * (float)p.shares + 1.f)), total[0], kTileTwo);
+  if (total[1] > 0) {
+    const int others = p.shares - head.shares[0];
+    const bool late = total[1] >= (long long)kFewLateFrom * kWarps * others;
+    head.total[2] = late ? total[1] / (others > 0 ? kFewLateOf : 1) : 0;
+    head.shares[2] = shares_in((long long)kFewLate * p.shares, head.total[2], kFewLateLeast);
+    if (late && head.shares[2] == 0) head.shares[2] = 1;
+    head.total[1] = total[1] - head.total[2];
+    head.shares[1] = head.total[1] > 0 ? max(shares_in((long long)kWarps * others, head.total[1], kFewLeast), 1) : 0;
+  }
+  head.count[0] = count[0], head.count[1] = count[1];
+  head.queue = head.shares[1];
+  if (tid == 0) *pl.head = head;
 }
 
 // ---------------------------------------------------------------- main
 
-template <int D>
+#include "decode_few.cuh"
+
+template <int D, int NR>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_decode_shared_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ SharedParams p) {
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k16,
+                            const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ SharedParams p) {
   using L = SharedLayout<D>;
   constexpr int NS = L::kStages, CH = D / 64;
   constexpr uint32_t TILE = L::kTile, CHUNK = L::kChunk;
@@ -353,21 +381,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sb = smem_raw + (base - raw);
   const uint32_t q_s = base + L::kQOff, kv_s = base + L::kKVOff;
 
-  Piece* s_piece = reinterpret_cast<Piece*>(sb + L::kMiscOff);                         // [kPieces]
-  uint32_t* s_bad = reinterpret_cast<uint32_t*>(sb + L::kMiscOff + 64 * kPieces);      // [2 groups][2][4]
-  static_assert(sizeof(Piece) == 64, "pieces");
-  const uint32_t bar0 = base + L::kMiscOff + 64 * kPieces + 64;
   // Rings: K/V tiles, pieces.  Q[s]: a tile of Q has landed; its last S product is
   // done.  Per tile t in turn: S ready, P's first and second 64 keys ready, the last
   // product of a run of key tiles done (O), and O read.  X: the softmax warps of a
-  // tile, and of both, have come this far.
+  // tile, and of both, have come this far.  FEW: of each warp that attends for few rows,
+  // 16 keys and values have landed.
   enum { KV_FULL = 0, KV_EMPTY = NS, PC_FULL = 2 * NS, PC_EMPTY = PC_FULL + kPieces, Q_FULL = PC_EMPTY + kPieces,
          Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 2, O_FINAL = P_FULL + 4, O_EMPTY = O_FINAL + 2,
-         XB = O_EMPTY + 2, DRAIN = XB + 3, NBARS = DRAIN + 1 };
-  static_assert(64 * kPieces + 64 + 8 * NBARS + 16 <= 1024, "misc area");
+         XB = O_EMPTY + 2, DRAIN = XB + 3, FEW = DRAIN + 1, NBARS = FEW + kWarps * kFewStages };
+  const uint32_t bar0 = base + L::kMiscOff;
   auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sb + L::kMiscOff + 64 * kPieces + 64 + 8 * NBARS);
+  constexpr uint32_t SLOT = L::kMiscOff + 8 * NBARS, PIECES = SLOT + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sb + SLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Piece* s_piece = reinterpret_cast<Piece*>(sb + PIECES);                              // [kPieces]
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(sb + PIECES + 64 * kPieces);           // [2 groups][2][4]
+  FewPiece* s_few = reinterpret_cast<FewPiece*>(sb + PIECES);                          // [kWarps][kFewPieces], once those are done with
+  static_assert(sizeof(Piece) == 64 && PIECES % 8 == 0, "pieces");
+  static_assert(PIECES + 64 * kPieces + 64 <= L::kMiscOff + L::kMisc, "misc area");
+  static_assert(PIECES + kWarps * kFewPieces * sizeof(FewPiece) <= L::kMiscOff + L::kMisc, "misc area");
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBARS; ++i) {
@@ -407,69 +439,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto k_place = [](int it) { return it == 0 ? 0 : 2 * it - 1; };
   auto v_place = [](int it) { return 2 * it + 2; };
 
-  if (warp == 2) {
-    // ============================================================ walk over the shares
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    const SharedHead* head = p.plan.head;
-    const int n_shared = head->shares[0], n_own = head->shares[1] + head->shares[2];
-    const long long rows = (long long)p.B * p.Nq * p.Hq;
-    int kind = (int)blockIdx.x < n_shared ? 0 : 1, k = (int)blockIdx.x - (kind ? n_shared : 0);
-    SharedStart st = {};
-    SharedEntry ent = {}, ahead = {};
-    long long at = 0, to = 0, off = 0;
-    auto begin = [&]() {  // share k of the list
-      const SharedList& list = kind ? p.plan.own : p.plan.shared;
-      st = list.start[k];
-      at = st.begin, to = at + st.size, off = st.off;
-      ent = st.entry;
-      if (st.e + 1 < st.count) ahead = list.entry[st.e + 1];
-    };
-    if (k < (kind ? n_own : n_shared)) begin();
-    for (int pieces = 0;; ++pieces) {
+  // CTAs begin with a share of the entries with many rows, or with shares of few rows for their warps
+  const int n_many = p.plan.head->shares[0];
+  const bool many = (int)blockIdx.x < n_many;
+  const bool few = NR > 0 && (!many || p.plan.head->shares[2] > 0);  // (behind the tiles there are the late shares alone)
+  // (registers go where a row's 128 scores are held: 56 x 4 warps + 224 x 8 is what 168 x 12 was)
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (!many) {
+  } else if (warp == 2) {
+    // ============================================================ walk over the share
+    Walk walk;
+    walk.start(p.plan.list[0], p.plan.head->count[0], deal_of(*p.plan.head, false), (int)blockIdx.x);
+    bool left = true;
+    for (int pieces = 0; left; ++pieces) {
       Piece s = {};
-      for (;;) {  // the next piece; t0 = t1: none is left
-        if (at == to) {
-          if (kind == 1 && k >= n_own) break;
-          kind = 1;
-          if (lane == 0) k = atomicAdd(&p.plan.head->queue, 1);
-          k = __shfl_sync(0xffffffffu, k, 0);
-          if (k >= n_own) break;
-          begin();
-        }
-        const Weight wt = weight_of(p, ent.ntok);
-        const int weight = wt.lead + wt.tile * ent.tiles, chunks = chunks_of(p, ent.ntok);
-        if (off >= (long long)weight * p.Hkv * chunks) {
-          off = 0;
-          ++st.e;
-          ent = ahead;
-          if (st.e + 1 < st.count) ahead = (kind ? p.plan.own : p.plan.shared).entry[st.e + 1];
-          continue;
-        }
-        const int u = (int)div_ll(off, weight), w0 = (int)(off - (long long)u * weight);
-        const int w1 = (int)(to - at < weight - w0 ? w0 + (to - at) : weight);
-        const bool later = w0 == 0 && at > st.begin;  // the unit begins behind the share's first slot
-        off += w1 - w0;
-        at += w1 - w0;
-        s.t0 = w0 <= wt.lead ? 0 : (w0 - wt.lead + wt.tile - 1) / wt.tile;
-        s.t1 = w1 <= wt.lead ? 0 : (w1 - wt.lead + wt.tile - 1) / wt.tile;
-        if (s.t0 == s.t1) continue;
+      int u;
+      bool later;
+      left = walk.next(p, false, u, s.t0, s.t1, later);
+      if (left) {  // (else t0 = t1: the end)
+        const SharedEntry& ent = walk.ent;
+        const int chunks = chunks_of(p, false, ent.ntok);
         s.head = (int)((unsigned)u / (unsigned)chunks);
         const int c = u - s.head * chunks;
         s.tok0 = ent.tok0 + c * 2 * p.tile_tokens;
         s.ntok = min(2 * p.tile_tokens, ent.ntok - c * 2 * p.tile_tokens);
         s.lo = ent.lo, s.end = ent.end, s.all_lo = ent.all_lo, s.all_hi = ent.all_hi;
         s.beg = ent.lo / p.box_rows * p.box_rows;
-        s.kind = kind;
+        s.kind = ent.kind;
         s.row = ent.row;
-        const long long slot = 2 * (long long)k + (later ? 1 : 0);
-        if (s.t0 == 0 && s.t1 == ent.tiles) {
-          s.side = 0;
-          s.place = 2 * kind * rows;
-        } else {
-          s.side = kind ? p.own_side : kSharedTile;
-          s.place = 4 * rows + (kind ? 512ll * p.shares : 0) + slot * 2 * s.side;
-        }
-        break;
+        s.side = s.t0 == 0 && s.t1 == ent.tiles ? 0 : kSharedTile;
+        s.place = s.side == 0 ? 2 * (long long)ent.kind * p.B * p.Nq * p.Hq : cut_place(p, false, (int)blockIdx.x, later);
       }
       const int slot = pieces % kPieces;
       if (pieces >= kPieces &&
@@ -480,11 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(BAR(PC_FULL + slot));
       }
       __syncwarp();
-      if (s.t0 == s.t1) break;
     }
   } else if (warp == 0 || warp == 3) {
     // ============================================================ loads of K, and of Q and V
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     const CUtensorMap* map = warp == 0 ? &tm_k : &tm_v;
     if (lane == 0) {
       tma_prefetch_desc(map);
@@ -567,7 +565,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ============================================================ products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // Job n is a tile of rows times a tile of keys; jobs take S, P and O of tile n & 1.
     // S of job n is issued before the product of job n - 1's P, which waits for its softmax.
     constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false), IDESC_O = idesc_bf16(128, D, false, true);
@@ -651,10 +648,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(BAR(DRAIN), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
     }
-  } else if (warp >= 4) {
-    // ============================================================ softmax
-    // (registers go where a row's 128 scores are held: 88 + 2 x 208 is what 3 x 168 was)
+  }
+  __syncwarp();
+  if (few && many) __syncthreads();  // shared memory changes hands
+  } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if (many) {
+    // ============================================================ softmax
     const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + (t ? 128u : 0u), tO = tmem + lane_off + 256u + (t ? (uint32_t)D : 0u);
@@ -853,8 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * inv);
           if (valid && l != 0.f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4*>(dst + 32 * c)[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+            for (int i = 0; i < 32; i += 8) st_global_v8(dst + 32 * c + i, ov + i);
           }
         }
         // l = 0: the row sees none of these keys (a NaN passes through)
@@ -862,6 +861,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
       }
       mbar_arrive(BAR(O_EMPTY + t));
+    }
+  }
+    __syncwarp();
+    if constexpr (NR > 0) {
+      if (few && many) {
+        fence_proxy_async_smem();
+        __syncthreads();
+      }
+      const int x = warp - 4, others = (int)gridDim.x - n_many;
+      if (few) attend_few<D, NR>(p, tm_k16, tm_v16, w, many ? -1 : x * others + (int)blockIdx.x - n_many, base + x * L::kWarpBytes,
+                        sb + x * L::kWarpBytes, BAR(FEW + x * kFewStages), s_few + x * kFewPieces);
     }
   }
   __syncwarp();
@@ -875,113 +885,142 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- merge
 
-// A warp per query row: the results of the group's shared keys and of the
-// request's own.  Lane i looks at part i; a part without mass has lse = -inf, and
-// its O is not read.
-template <int D>
-__global__ void __launch_bounds__(256) fa_decode_shared_merge_kernel(const __grid_constant__ SharedParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+// A warp for R query rows of a token and K/V head, one where all are on the GPU at once: the
+// results of the group's shared keys and of the request's own.  Lane i looks at part i; a
+// part without mass has lse = -inf, and its O is not read.
+template <int D, int R>
+__global__ void __launch_bounds__(256, R == 1 ? 4 : 2) fa_decode_shared_merge_kernel(const __grid_constant__ SharedParams p) {
+  constexpr int E = D / 32, U = R == 1 ? 8 : 1;  // U: parts read at a time
+  const int lane = threadIdx.x & 31, fours = (p.heads + R - 1) / R;
   const long long rows = (long long)p.B * p.Nq * p.Hq, x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (x >= rows) return;
-  const long long token = div_ll(x, p.Hq);
-  const int tok = (int)token, h = (int)(x - token * p.Hq), head = h / p.heads, b = tok / p.Nq;
+  if (x >= (long long)p.B * p.Nq * p.Hkv * fours) return;
+  const long long of_four = div_ll(x, fours);
+  const int h0 = (int)(x - of_four * fours) * R, tok = (int)div_ll(of_four, p.Hkv), head = (int)(of_four - (long long)tok * p.Hkv);
+  const int b = tok / p.Nq, nr = min(R, p.heads - h0);
+  const long long row = (long long)tok * p.Hq + head * p.heads + h0;
   // (the plan, which the main kernel's CTAs have all waited for; read past L1)
   const int2 entries = __ldcg(p.plan.of_request + b);
   // parts of each kind: n of them, `runs` in each of the shares from `first` on
   int n[2] = {0, 0}, runs[2] = {1, 1}, first[2] = {0, 0};
   long long base[2] = {0, 0}, begin[2] = {0, 0};  // place of the first part, or of the row in a slot; the unit's begin
-  bool cut[2] = {false, false};
-  const longlong2 h0 = __ldcg(reinterpret_cast<const longlong2*>(p.plan.head)),
-                  h1 = __ldcg(reinterpret_cast<const longlong2*>(p.plan.head) + 1);
+  bool cut[2] = {false, false}, few[2] = {false, false};
   SharedHead totals;
-  totals.total[0] = h0.x, totals.total[1] = h0.y, totals.total[2] = h1.x;
-  totals.shares[0] = (int)h1.y, totals.shares[1] = (int)(h1.y >> 32), totals.shares[2] = __ldcg(&p.plan.head->shares[2]);
-  const Deal deals[2] = {deal_of(totals, 0), deal_of(totals, 1)};
+  const longlong2 t0 = __ldcg(reinterpret_cast<const longlong2*>(p.plan.head)),
+                  t1 = __ldcg(reinterpret_cast<const longlong2*>(p.plan.head) + 1);
+  totals.total[0] = t0.x, totals.total[1] = t0.y, totals.total[2] = t1.x;
+  totals.shares[0] = (int)t1.y, totals.shares[1] = (int)(t1.y >> 32), totals.shares[2] = __ldcg(&p.plan.head->shares[2]);
+  const Deal deals[2] = {deal_of(totals, false), deal_of(totals, true)};
 #pragma unroll
   for (int kind = 0; kind < 2; ++kind) {
-    const int e = kind == 0 ? entries.x : entries.y;
-    if (e < 0) continue;
-    const SharedList& list = kind ? p.plan.own : p.plan.shared;
-    const SharedEntry* at = list.entry + e;
+    const int of = kind == 0 ? entries.x : entries.y;
+    if (of < 0) continue;
+    few[kind] = of & 1;
+    const SharedList& list = p.plan.list[of & 1];
+    const Deal& deal = (of & 1) ? deals[1] : deals[0];
+    const SharedEntry* at = list.entry + (of >> 1);
     const int tok0 = __ldcg(&at->tok0), ntok = __ldcg(&at->ntok), tiles = __ldcg(&at->tiles);
-    const long long cum = __ldcg(list.cum + e);
-    const Weight wt = weight_of(p, ntok);
-    const int weight = wt.lead + wt.tile * tiles, chunks = chunks_of(p, ntok);
-    const int c = (tok - tok0) / (2 * p.tile_tokens), in = tok - tok0 - c * 2 * p.tile_tokens;
-    const bool pair = ntok - c * 2 * p.tile_tokens > p.tile_tokens;
+    const long long cum = __ldcg(list.cum + (of >> 1));
+    const Weight wt = weight_of(p, few[kind], ntok);
+    const int weight = wt.lead + wt.tile * tiles, chunks = chunks_of(p, few[kind], ntok);
+    const int c = few[kind] ? 0 : (tok - tok0) / (2 * p.tile_tokens), in = tok - tok0 - c * 2 * p.tile_tokens;
+    const bool pair = few[kind] || ntok - c * 2 * p.tile_tokens > p.tile_tokens;
     begin[kind] = cum + (long long)weight * ((long long)head * chunks + c);
-    first[kind] = deals[kind].of(begin[kind] + wt.lead);
-    const int last = deals[kind].of(begin[kind] + weight - wt.tile);  // where the last tile begins
+    first[kind] = deal.of(begin[kind] + wt.lead);
+    const int last = deal.of(begin[kind] + weight - wt.tile);  // where the last tile begins
     cut[kind] = first[kind] != last;
     runs[kind] = pair ? 1 : 2;
     n[kind] = (last - first[kind] + 1) * runs[kind];
-    const int side = in / p.tile_tokens;
-    base[kind] = cut[kind] ? 4 * rows + (kind ? 512ll * p.shares : 0) + side * (kind ? p.own_side : kSharedTile) +
-                                 (in - side * p.tile_tokens) * p.heads + h - head * p.heads
-                           : 2 * kind * rows + x;
+    const int side = few[kind] ? 0 : in / p.tile_tokens;
+    base[kind] = cut[kind] ? side * kSharedTile + (in - side * p.tile_tokens) * p.heads + h0 : 2 * kind * rows + row;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done
-  float acc[E], mass = 0.f, m = -INFINITY;
+  float acc[R][E], mass[R], m[R];
 #pragma unroll
-  for (int i = 0; i < E; ++i) acc[i] = 0.f;
+  for (int r = 0; r < R; ++r) {
+    mass[r] = 0.f, m[r] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[r][i] = 0.f;
+  }
   for (int i0 = 0; i0 < n[0] + n[1]; i0 += 32) {
-    float lc = -INFINITY;
+    float lc[R], f[R];
     long long place = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) lc[r] = -INFINITY;
     if (i0 + lane < n[0] + n[1]) {
       const bool own_part = i0 + lane >= n[0];
       const int i = i0 + lane - (own_part ? n[0] : 0);
       const bool two = (own_part ? runs[1] : runs[0]) == 2;
       const int run = two ? i & 1 : 0, k = (own_part ? first[1] : first[0]) + (two ? i >> 1 : i);
       // a cut unit's: of the share's last piece, if it begins before the unit, or its first
-      const long long slot = 2 * (long long)k + (own_part ? deals[1].begin(k) < begin[1] : deals[0].begin(k) < begin[0]);
-      const int side = own_part ? p.own_side : kSharedTile;
-      place = (own_part ? base[1] : base[0]) + ((own_part ? cut[1] : cut[0]) ? slot * 2 * side + run * side : run * rows);
-      lc = p.part_lse[place];
+      const bool in_few = own_part ? few[1] : few[0], later = (in_few ? deals[1] : deals[0]).begin(k) < (own_part ? begin[1] : begin[0]);
+      place = own_part ? base[1] : base[0];
+      place += (own_part ? cut[1] : cut[0]) ? cut_place(p, in_few, k, later) + run * kSharedTile : run * rows;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < nr) lc[r] = p.part_lse[place + r];
     }
-    float top = lc;
+    unsigned todo = 0, has[R];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));  // (a NaN is left out)
-    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn, al = ex2_sfu(m - ref);
-    m = mn;
-    mass *= al;
+    for (int r = 0; r < R; ++r) {
+      float top = lc[r];
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] *= al;
-    const float f = ex2_sfu(lc - ref);
-    unsigned todo = __ballot_sync(0xffffffffu, lc != -INFINITY);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));  // (a NaN is left out)
+      const float mn = fmaxf(m[r], top), ref = mn == -INFINITY ? 0.f : mn, al = ex2_sfu(m[r] - ref);
+      m[r] = mn;
+      mass[r] *= al;
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[r][i] *= al;
+      f[r] = ex2_sfu(lc[r] - ref);
+      has[r] = __ballot_sync(0xffffffffu, lc[r] != -INFINITY);
+      todo |= has[r];
+    }
     while (todo) {
-      constexpr int U = 4;  // loads at a time
-      float v[U][E], fu[U];
+      float v[U][R][E], fu[U][R];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int from = todo ? __ffs(todo) - 1 : 0;
         const long long at = __shfl_sync(0xffffffffu, place, from);
-        const float w = __shfl_sync(0xffffffffu, f, from);
-        fu[u] = todo ? w : 0.f;
-        if (todo) {
-          const float* src = p.part_o + at * D + lane * E;
 #pragma unroll
-          for (int i = 0; i < E; ++i) v[u][i] = src[i];
-        } else {
+        for (int r = 0; r < R; ++r) {
+          const float weight = __shfl_sync(0xffffffffu, f[r], from);
+          const bool on = todo != 0 && (has[r] >> from & 1);
+          fu[u][r] = on ? weight : 0.f;
+          const float* src = p.part_o + (at + r) * D + lane * E;
 #pragma unroll
-          for (int i = 0; i < E; ++i) v[u][i] = 0.f;
+          for (int i = 0; i < E; ++i) v[u][r][i] = 0.f;
+          if (on) {
+            if constexpr (E == 4) {
+              const float4 y = *reinterpret_cast<const float4*>(src);
+              v[u][r][0] = y.x, v[u][r][1] = y.y, v[u][r][2] = y.z, v[u][r][3] = y.w;
+            } else {
+              const float2 y = *reinterpret_cast<const float2*>(src);
+              v[u][r][0] = y.x, v[u][r][1] = y.y;
+            }
+          }
         }
         todo &= todo - 1;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        mass += fu[u];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = fmaf(fu[u], v[u][i], acc[i]);
-      }
+        for (int r = 0; r < R; ++r) {
+          mass[r] += fu[u][r];
+#pragma unroll
+          for (int i = 0; i < E; ++i) acc[r][i] = fmaf(fu[u][r], v[u][r][i], acc[r][i]);
+        }
     }
   }
-  const float inv = mass == 0.f ? 0.f : 1.f / mass;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + x * D + lane * E);
 #pragma unroll
-  for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-  if (lane == 0)
-    p.lse[((long long)b * p.Hq + h) * p.Nq + tok - b * p.Nq] = mass == 0.f ? -INFINITY : (m + __log2f(mass)) * 0.69314718055994531f;
+  for (int r = 0; r < R; ++r) {
+    if (r >= nr) break;
+    const float inv = mass[r] == 0.f ? 0.f : 1.f / mass[r];
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + (row + r) * D + lane * E);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf16x2(acc[r][i] * inv, acc[r][i + 1] * inv);
+    if (lane == 0)
+      p.lse[((long long)b * p.Hq + head * p.heads + h0 + r) * p.Nq + tok - b * p.Nq] =
+          mass[r] == 0.f ? -INFINITY : (m[r] + __log2f(mass[r])) * 0.69314718055994531f;
+  }
 }
 
 // ---------------------------------------------------------------- host
@@ -989,7 +1028,7 @@ __global__ void __launch_bounds__(256) fa_decode_shared_merge_kernel(const __gri
 static size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 // The plan's arrays one after the other from `at` (or their bytes alone).
-static size_t plan_layout(SharedPlan* plan, void* at, int B, int G, int shares) {
+static size_t plan_layout(SharedPlan* plan, void* at, int B, int G) {
   uint8_t* base = static_cast<uint8_t*>(at);
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -999,31 +1038,31 @@ static size_t plan_layout(SharedPlan* plan, void* at, int B, int G, int shares) 
   };
   SharedPlan pl;
   pl.head = reinterpret_cast<SharedHead*>(take(sizeof(SharedHead)));
-  auto list = [&](SharedList& l, size_t entries, size_t starts) {
-    l.entry = reinterpret_cast<SharedEntry*>(take(sizeof(SharedEntry) * entries));
-    l.cum = reinterpret_cast<long long*>(take(8 * entries));
-    l.start = reinterpret_cast<SharedStart*>(take(sizeof(SharedStart) * starts));
-  };
-  list(pl.shared, G, shares);
-  list(pl.own, B, (size_t)kOwnShares * shares);
+  for (SharedList& l : pl.list) {
+    l.entry = reinterpret_cast<SharedEntry*>(take(sizeof(SharedEntry) * ((size_t)G + B)));
+    l.cum = reinterpret_cast<long long*>(take(8 * ((size_t)G + B)));
+  }
   pl.of_request = reinterpret_cast<int2*>(take(8 * (size_t)B));
   pl.g_shared = reinterpret_cast<int*>(take(4 * (size_t)G));
+  pl.g_of = reinterpret_cast<int*>(take(4 * (size_t)G));
   pl.g_least = reinterpret_cast<int*>(take(4 * (size_t)G));
   pl.g_most = reinterpret_cast<unsigned long long*>(take(8 * (size_t)G));
   if (plan != nullptr) *plan = pl;
   return off;
 }
-int shared_own_side(int Nq, int heads) { return Nq * heads < kSharedTile ? Nq * heads : kSharedTile; }
-size_t shared_part_rows(int B, int Nq, int Hq, int heads, int shares) {
-  return 4 * (size_t)B * Nq * Hq + 512 * (size_t)shares + 4 * (size_t)shared_own_side(Nq, heads) * kOwnShares * shares;
+int shared_few(int Nq, int heads) {
+  const int rows = Nq * heads;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
 }
-size_t shared_plan_bytes(int B, int G, int shares) { return plan_layout(nullptr, nullptr, B, G, shares); }
-void shared_plan_at(SharedPlan& plan, void* at, int B, int G, int shares) { plan_layout(&plan, at, B, G, shares); }
+size_t shared_part_rows(int B, int Nq, int Hq, int heads, int shares) {
+  return 4 * (size_t)B * Nq * Hq + 512 * (size_t)shares + 2 * (size_t)shared_few(Nq, heads) * (kFewEarly + kFewLate) * shares;
+}
+size_t shared_plan_bytes(int B, int G) { return plan_layout(nullptr, nullptr, B, G); }
+void shared_plan_at(SharedPlan& plan, void* at, int B, int G) { plan_layout(&plan, at, B, G); }
 
-template <int D>
-static cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p,
-                            cudaStream_t stream) {
-  auto kern = fa_decode_shared_kernel<D>;
+template <int D, int NR>
+static cudaError_t launch_t(const CUtensorMap (&maps)[5], const SharedParams& p, cudaStream_t stream) {
+  auto kern = fa_decode_shared_kernel<D, NR>;
   constexpr uint32_t smem = SharedLayout<D>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -1039,18 +1078,31 @@ static cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const 
   cfg.stream = stream;
   cfg.attrs = &a;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p)) != cudaSuccess) return e;
-  const long long rows = (long long)p.B * p.Nq * p.Hq;
-  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+  if ((e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], maps[4], p)) != cudaSuccess) return e;
+  const long long tokens = (long long)p.B * p.Nq * p.Hkv;
+  const bool one = tokens * p.heads <= 32ll * kSms;
+  const long long warps = tokens * (one ? p.heads : (p.heads + kMergeRows - 1) / kMergeRows);
+  cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, fa_decode_shared_merge_kernel<D>, p);
+  return one ? cudaLaunchKernelEx(&cfg, fa_decode_shared_merge_kernel<D, 1>, p)
+             : cudaLaunchKernelEx(&cfg, fa_decode_shared_merge_kernel<D, kMergeRows>, p);
 }
 
-cudaError_t launch_decode_shared(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p,
-                                 int D, cudaStream_t stream) {
-  if (D == 64) return launch_t<64>(tq, tk, tv, p, stream);
-  if (D == 128) return launch_t<128>(tq, tk, tv, p, stream);
+template <int D>
+static cudaError_t launch_d(const CUtensorMap (&maps)[5], SharedParams p, cudaStream_t stream) {
+  p.few_cost = kFew * D / 128;
+  switch (p.few) {
+    case 8: return launch_t<D, 1>(maps, p, stream);
+    case 16: return launch_t<D, 2>(maps, p, stream);
+    case 32: return launch_t<D, 4>(maps, p, stream);
+    default: return launch_t<D, 0>(maps, p, stream);
+  }
+}
+
+cudaError_t launch_decode_shared(const CUtensorMap (&maps)[5], const SharedParams& p, int D, cudaStream_t stream) {
+  if (D == 64) return launch_d<64>(maps, p, stream);
+  if (D == 128) return launch_d<128>(maps, p, stream);
   return cudaErrorInvalidValue;
 }
 

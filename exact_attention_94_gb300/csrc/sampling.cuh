@@ -42,32 +42,27 @@ struct SharedEntry {
   int row;             // of the block table
   int lo, end;         // keys
   int all_lo, all_hi;  // the keys that every query token (of a request with keys) sees, if any
-  int tiles;           // of 128 keys from lo rounded down to a TMA box
-};
-// A share of a list of entries: where it begins, and how much it weighs.
-struct SharedStart {
-  long long begin, size, off;  // off: within its first entry
-  int e, count;                // that entry's number; entries of the list
-  SharedEntry entry;
+  int tiles;           // of 128 keys from lo rounded down to a TMA box; few rows: of 16 keys
+  int kind;            // 0: a group's shared keys, 1: a request's own
 };
 struct SharedList {
   SharedEntry* entry;  // those that have keys
   long long* cum;      // weight before each
-  SharedStart* start;  // of each share
 };
 struct SharedHead {
-  long long total[3];  // weight of shared keys, of own keys dealt early, and late
-  int shares[3];       // they are dealt to
-  int queue;           // shares of own keys that CTAs have taken
+  long long total[3];  // weight of the entries with many rows, of those with few dealt early, and late
+  int shares[3];       // they are dealt to: CTAs, warps
+  int count[2];        // entries of the lists
+  int queue;           // shares of few rows that warps have taken
 };
 // What a call's first kernel leaves for the others, in the workspace.
 struct SharedPlan {
   SharedHead* head;
-  SharedList shared;   // [G], shares: one for each CTA at most
-  SharedList own;      // [B]
-  int2* of_request;    // [B] entries of its group's shared keys and of its own, -1: none
-  int* g_shared;       // [G] keys that the group shares, its shortest request's (with keys), its longest's: where
-  int* g_least;        //   groups are too many for the first kernel's shared memory
+  SharedList list[2];  // [G + B] entries with many rows, with few
+  int2* of_request;    // [B] entries of its group's shared keys and of its own: 2 number + list, -1: none
+  int* g_shared;       // [G] keys that the group shares, its entry of them, the keys of its shortest request (that has
+  int* g_of;           //   some), of its longest: where groups are too many for the first kernel's shared memory
+  int* g_least;
   unsigned long long* g_most;
 };
 struct SharedParams {
@@ -75,11 +70,12 @@ struct SharedParams {
   const int* seq_lens;       // [B]
   const int* starts;         // [G + 1]
   const int* shared_lens;    // [G]
-  void* o;                   // [B, Nq, Hq, d] bf16
+  const void* q;             // [B, Nq, Hq, d] bf16
+  void* o;                   // the same
   float* lse;                // [B, Hq, Nq]
   float* part_o;             // results of units inside one share, [4][rows][d] (shared / own keys, two runs each), then of the
-  float* part_lse;           //   pieces that shares' borders cut, two a share, [2][128][d] of shared keys, [2][own_side][d] of
-                             //   own: each normalised; log2 of its mass
+  float* part_lse;           //   pieces that shares' borders cut, two a share, [2][128][d] of many rows, [few][d] of few: each
+                             //   normalised; log2 of its mass
   SharedPlan plan;
   int B, Nq, Hq, Hkv, heads; // heads: query heads of a K/V head
   int G, tile_tokens;        // groups; query tokens of a tile of rows
@@ -87,19 +83,19 @@ struct SharedParams {
   int win_left;              // -1: no window
   int box_rows;              // keys per TMA box: 16 .. 128, divides the page and the tile
   int shares;                // CTAs
-  int own_side;              // rows of a cut piece's run of own keys
+  int few;                   // most rows of an entry that a warp attends for: 0, 8, 16 or 32
+  float few_cost;            // of a CTA's time a slot of few rows' weight takes
   float scale_log2, tau;
   unsigned* err;
   unsigned long long timeout_ns;
 };
-int shared_own_side(int Nq, int heads);
+int shared_few(int Nq, int heads);
 size_t shared_part_rows(int B, int Nq, int Hq, int heads, int shares);
-size_t shared_plan_bytes(int B, int G, int shares);
-void shared_plan_at(SharedPlan& plan, void* at, int B, int G, int shares);
+size_t shared_plan_bytes(int B, int G);
+void shared_plan_at(SharedPlan& plan, void* at, int B, int G);
 bool make_tmap_queries(CUtensorMap* m, const void* ptr, int D, int Hq, long long tokens, int heads, int tile_tokens);
 bool make_tmap_pages(CUtensorMap* m, const void* ptr, int D, int Hkv, int page_size, int num_pages, int box_rows);
-cudaError_t launch_decode_shared(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p,
-                                 int D, cudaStream_t stream);
+cudaError_t launch_decode_shared(const CUtensorMap (&maps)[5], const SharedParams& p, int D, cudaStream_t stream);  // q; k, v; k, v by 16 keys
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, int c3,
                                             int c4) {

@@ -114,6 +114,14 @@ def test_many_rows(heads, n):
         check(call(m, num_shares=shares), ref)
 
 
+@pytest.mark.parametrize("heads", [1, 8, 40])
+def test_requests_without_keys_share_nothing(heads):
+    """Whole tiles that every request with keys sees: one without sees none of them."""
+    m = make([(520, [530, 0, 700, 0]), (300, [0, 300])], 1, heads, 1, 64, 16, seed=heads, fill=float("nan"))
+    for shares in (0, 1):
+        check(call(m, num_shares=shares), want(m))
+
+
 @pytest.mark.parametrize("window", [0, 1, 40, 127, 300])
 @pytest.mark.parametrize("Nq", [1, 4])
 def test_windows(window, Nq):
