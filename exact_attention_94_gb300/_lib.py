@@ -72,6 +72,7 @@ SIGNATURES = {
     "fa_qk_norm_rope_bwd": (_I, [_P] * 11 + [ctypes.POINTER(RopePlanStruct)] + [_I] * 4 + [_L] * 6 + [_I, _F, _P, _P]),
     "fa_decode_shared_workspace_bytes": (_S, [_I] * 7),
     "fa_decode_paged_shared": (_I, [_P] * 9 + [_I] * 12 + [_P, _F, _P]),
+    "fa_decode_kv8_shared": (_I, [_P] * 11 + [_I] * 12 + [_P, _F, _P]),
     "fa_device_error": (_I, [ctypes.POINTER(ctypes.c_uint)]),
     "fa_selftest_wait_timeout": (_I, [ctypes.c_double, _P]),
     "fa_selftest_exp2": (_I, [_P, _P, _I, _I, _P]),

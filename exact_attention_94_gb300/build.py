@@ -17,8 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa.so")
 SOURCES = ["api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_fp8.cu", "fa_plan.cu", "fa_rope.cu", "fa_kv8.cu",
-           "fa_decode_kv8.cu", "fa_norm.cu", "fa_decode_shared.cu",
-           "page_pool.cpp"]
+           "fa_decode_kv8.cu", "fa_norm.cu", "fa_decode_shared.cu", "fa_decode_shared8.cu", "page_pool.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(HERE, "..", "include")]
 

@@ -1143,7 +1143,27 @@ fa_status fa_decode_paged_shared(const void* q, const void* k_pages, const void*
   for (int i = 0; i < 4; ++i)
     if (!make_tmap_pages(&maps[1 + i], i & 1 ? v_pages : k_pages, d, Hkv, page_size, num_pages, i < 2 ? p.box_rows : 16))
       return FA_ERR_INVALID_ARG;
-  return launch_decode_shared(maps, p, d, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  return launch_decode_shared(maps, p, d, false, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+fa_status fa_decode_kv8_shared(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                               const float* v_scale, const int* block_table, const int* seq_lens, const int* group_starts,
+                               const int* shared_lens, void* o, float* lse, int B, int Nq, int Hq, int Hkv, int d,
+                               int page_size, int num_pages, int max_blocks, int max_seq_len, int num_groups, int window_left,
+                               int num_shares, void* workspace, float scale, fa_stream_t stream) {
+  if (!k_codes || !v_codes || !k_scale || !v_scale) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned4(k_scale) || !aligned4(v_scale)) return FA_ERR_MISALIGNED;
+  SharedParams p{};
+  CUtensorMap maps[5];
+  const fa_status st = shared_common(p, maps[0], q, block_table, seq_lens, group_starts, shared_lens, o, lse, B, Nq, Hq, Hkv, d,
+                                     page_size, num_pages, max_blocks, max_seq_len, num_groups, window_left, num_shares,
+                                     workspace, scale);
+  if (st != FA_OK) return st;
+  p.k_scale = k_scale, p.v_scale = v_scale;
+  for (int i = 0; i < 4; ++i)
+    if (!make_tmap_codes(&maps[1 + i], i & 1 ? v_codes : k_codes, d, page_size, (long long)num_pages * Hkv, i < 2 ? p.box_rows : 16))
+      return FA_ERR_INVALID_ARG;
+  return launch_decode_shared(maps, p, d, true, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -11,7 +11,7 @@
 // 8 x 8 blocks between lanes, and O^T stays in registers.  A warp has its own ring of
 // steps in shared memory, filled by TMA across units' borders, and meets no other warp
 // until its results are merged.
-constexpr int kFewStages = 6;  // of a warp's ring, at most
+constexpr int kFewStages = 5;  // of a warp's ring, at most
 constexpr int kFewPieces = 4;  // a warp knows of: one it works on, those it loads
 
 struct FewPiece {
@@ -21,7 +21,11 @@ struct FewPiece {
   int lo, end, all_lo, all_hi;
   int t0, t1;
 };
-static_assert(sizeof(FewPiece) == 40, "");
+// What a warp keeps in shared memory beside its rings.
+struct FewState {
+  FewPiece ring[kFewPieces];
+  unsigned long long bars[kFewStages];  // a step has landed
+};
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -41,21 +45,29 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Of a row of queries (at `row`, as copied), the second product operand for step x of 16 elements of d
+// against codes: a lane's four codes are d .. d + 3, the even ones first.
+__device__ __forceinline__ void few_queries(uint32_t& b0, uint32_t& b1, const uint8_t* row, int x, int q, int r) {
+  const int c = 8 * (x >> 2) + 2 * q + (x >> 1 & 1);
+  const uint2 v = *reinterpret_cast<const uint2*>(row + ((c ^ r) << 4) + 8 * (x & 1));
+  b0 = __byte_perm(v.x, v.y, 0x5410), b1 = __byte_perm(v.x, v.y, 0x7632);
+}
 // 16 bytes to shared memory, or zeros
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
-// k: the warp's first share, -1: none; at, mem: its shared memory; bars: kFewStages
-// barriers; ring: kFewPieces pieces.
-template <int D, int NR>
+// k: the warp's first share, -1: none; at, mem: its shared memory, of BYTES.
+template <int D, int NR, bool KV8, uint32_t BYTES>
 __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const WaitCtx& w,
-                                           int k, uint32_t at, uint8_t* mem, uint32_t bars, FewPiece* ring) {
-  using L = SharedLayout<D>;
-  constexpr int ROWS = 8 * NR, CH = D / 64, C16 = D / 8;  // C16: 16-byte chunks of a row
-  constexpr uint32_t TILE = L::kFewTile, QBYTES = ROWS * D * 2u;
-  constexpr int FIT = (int)((L::kWarpBytes - (QBYTES + 1023) / 1024 * 1024) / (2 * TILE)), NST = FIT < kFewStages ? FIT : kFewStages;
+                                           int k, uint32_t at, uint8_t* mem, FewState* state) {
+  constexpr int ROWS = 8 * NR, CH = D / 64, C16 = D / 8;  // C16: 16-byte chunks of a row of bf16
+  constexpr uint32_t TILE = 16u * D * (KV8 ? 1 : 2), QBYTES = ROWS * D * 2u, SCALES = KV8 ? 8 * kFewStages : 0;
+  constexpr int FIT = (int)((BYTES - QBYTES - SCALES) / (2 * TILE)), NST = FIT < kFewStages ? FIT : kFewStages;
   static_assert(NST >= 2, "ring");
+  FewPiece* ring = state->ring;
+  const uint32_t bars = smem_u32(state->bars);
+  float2* s_scale = reinterpret_cast<float2*>(mem + NST * 2 * TILE + QBYTES);  // KV8: of a step's keys, values
   constexpr bool QREG = NR <= 2;  // queries stay in registers
   constexpr uint32_t QAT = NST * 2 * TILE;
   const int lane = lane_id(), quad = lane >> 2, q2 = 2 * (lane & 3);
@@ -63,6 +75,12 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
   const Deal deal = deal_of(*p.plan.head, true);
   const int early = deal.early.n, all = early + deal.late.n, entries = p.plan.head->count[1];
   const float sl2 = p.scale_log2;
+  if (lane == 0) {
+    for (int i = 0; i < NST; ++i) mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  __syncwarp();
   // ------------------------------------------------------------ loads: shares, their pieces, batches of 32 steps
   Walk walk;
   walk.at = walk.to = 0;
@@ -113,7 +131,8 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
   };
   Batch now, then;
   now.n = then.n = 0;
-  int i_now = 0, at8 = 0, issued = 0, done = 0, st_in = 0;
+  int i_now = 0, row_at = 0, plane = 0, issued = 0, done = 0, st_in = 0;
+  float k_scale = 0.f, v_scale = 0.f;
   // ------------------------------------------------------------ the piece in work
   float o[D / 16][NR][4], m_ref[NR][2], l[NR][2];
   uint32_t qf[QREG ? NR : 1][QREG ? D / 8 : 1];
@@ -138,15 +157,25 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
           atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
           now.page = 0;
         }
-        at8 = now.page * (p.page_size / 8) + now.rows8;
+        row_at = KV8 ? now.rows8 * 8 : now.page * (p.page_size / 8) + now.rows8;  // row of the page, or eight of all pages'
+        plane = now.page * p.Hkv + now.head;
+        if constexpr (KV8) {
+          if (lane < now.n) k_scale = p.k_scale[plane], v_scale = p.v_scale[plane];
+        }
         then.n = 0;
       }
-      const int row8 = __shfl_sync(0xffffffffu, at8, i_now);
+      const int row = __shfl_sync(0xffffffffu, row_at, i_now), pl = KV8 ? __shfl_sync(0xffffffffu, plane, i_now) : 0;
       const uint32_t bar = bars + 8 * st_in, dst = at + st_in * 2 * TILE;
+      if (KV8 && lane == i_now) s_scale[st_in] = make_float2(k_scale, v_scale);
       if (elect_one()) {
         mbar_arrive_expect_tx(bar, 2 * TILE);
-        tma_load_5d(dst, &tm_k, bar, 0, 0, 0, row8, now.head);
-        tma_load_5d(dst + TILE, &tm_v, bar, 0, 0, 0, row8, now.head);
+        if constexpr (KV8) {
+          tma_load_3d(dst, &tm_k, bar, 0, row, pl);
+          tma_load_3d(dst + TILE, &tm_v, bar, 0, row, pl);
+        } else {
+          tma_load_5d(dst, &tm_k, bar, 0, 0, 0, row, now.head);
+          tma_load_5d(dst + TILE, &tm_v, bar, 0, 0, 0, row, now.head);
+        }
       }
       __syncwarp();
       if (++st_in == NST) st_in = 0;
@@ -176,7 +205,12 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
 #pragma unroll
           for (int c = 0; c < C16; c += 4) {
             uint32_t r[4];
-            ldsm4(r, at + QAT + (8 * nr + x7) * (D * 2) + (((c + (lane >> 3)) ^ x7) << 4));
+            if constexpr (KV8) {  // two steps of 16 elements of d
+#pragma unroll
+              for (int i = 0; i < 2; ++i) few_queries(r[2 * i], r[2 * i + 1], mem + QAT + (8 * nr + quad) * (D * 2), c / 2 + i, lane & 3, quad);
+            } else {
+              ldsm4(r, at + QAT + (8 * nr + x7) * (D * 2) + (((c + (lane >> 3)) ^ x7) << 4));
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) qf[nr][c + i] = r[i];
           }
@@ -212,7 +246,7 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
     ok = mbar_wait(bars + 8 * st, phase, w, 90);
     if (!__all_sync(0xffffffffu, ok)) break;
     const bool inside = j0 >= pc.all_lo && j0 + 16 <= pc.all_hi;  // every row sees every key
-    if (!inside) {
+    if (!KV8 && !inside) {
       // 0 times a NaN or an infinity is not 0: what no row sees (it may be anything) counts as
       // zero; a value row that some see, and that holds one, counts as zero too, and its
       // rows get a NaN.
@@ -257,10 +291,35 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
       for (int j = 0; j < 4 * CHAINS; ++j) s[nr][j / 4][j % 4] = 0.f;
+    uint4 kc[KV8 ? 2 : 1][KV8 ? CH : 1];  // codes: a key's chunks lane & 3 and, d = 128, 4 behind it
+    float mul = sl2, v_mul = 1.f;
+    uint32_t nan_k = 0, odd = 0;  // keys quad, quad + 8 with a NaN; 16 keys with values to poison who sees them
+    if constexpr (KV8) {
+      const float2 sc = s_scale[st];
+      mul = sl2 * sc.x, v_mul = sc.y;
+      if (!(fabsf(v_mul) < INFINITY)) v_mul = 0.f, odd = 0xffffu;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          const int key = quad + 8 * h, c = (lane & 3) + 4 * j;
+          const uint4 x = *reinterpret_cast<const uint4*>(mem + st * 2 * TILE + key * D + ((c ^ (D == 128 ? key & 7 : key >> 1 & 3)) << 4));
+          kc[h][j] = x;
+          if ((code_nans(x.x) | code_nans(x.y) | code_nans(x.z) | code_nans(x.w)) & 0x80808080u) nan_k |= 1u << h;
+        }
+    }
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
       uint32_t a[4];
-      ldsm4(a, ks + k_row + (x >> 2) * 1024 + (((2 * (x & 3) + (lane >> 4)) ^ x7) << 4));
+      if constexpr (KV8) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4& c = kc[h][x >> 2];
+          const uint32_t word = (x & 3) == 0 ? c.x : (x & 3) == 1 ? c.y : (x & 3) == 2 ? c.z : c.w;
+          a[h] = codes2_bf16(word << 8), a[2 + h] = codes2_bf16(word);
+        }
+      } else
+        ldsm4(a, ks + k_row + (x >> 2) * 1024 + (((2 * (x & 3) + (lane >> 4)) ^ x7) << 4));
       if constexpr (QREG) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) mma16816(s[nr][x % CHAINS], a, qf[nr][2 * x], qf[nr][2 * x + 1]);
@@ -268,17 +327,32 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
 #pragma unroll
         for (int nr = 0; nr < NR; nr += 2) {  // two tiles of rows, two chunks
           uint32_t b[4];
-          ldsm4(b, at + QAT + (8 * nr + (lane >> 4) * 8 + x7) * (D * 2) + (((2 * x + (lane >> 3 & 1)) ^ x7) << 4));
+          if constexpr (KV8) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) few_queries(b[2 * i], b[2 * i + 1], mem + QAT + (8 * (nr + i) + quad) * (D * 2), x, lane & 3, quad);
+          } else
+            ldsm4(b, at + QAT + (8 * nr + (lane >> 4) * 8 + x7) * (D * 2) + (((2 * x + (lane >> 3 & 1)) ^ x7) << 4));
           mma16816(s[nr][x % CHAINS], a, b[0], b[1]);
           mma16816(s[nr + 1][x % CHAINS], a, b[2], b[3]);
         }
       }
+    }
+    if (KV8 && __any_sync(0xffffffffu, nan_k != 0)) {
+      nan_k |= __shfl_xor_sync(0xffffffffu, nan_k, 1);
+      nan_k |= __shfl_xor_sync(0xffffffffu, nan_k, 2);
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (nan_k >> (j >> 1) & 1) s[nr][0][j] = __uint_as_float(0x7fffffffu);
     }
     bool moves = false;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
       for (int j = 0; j < 4 * (CHAINS - 1); ++j) s[nr][0][j] += s[nr][1 % CHAINS][j];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[nr][0][j] *= mul;
       if (!inside) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -287,7 +361,7 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
         }
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) moves |= fmaxf(s[nr][0][j], s[nr][0][j + 2]) * sl2 > m_ref[nr][j] + p.tau;
+      for (int j = 0; j < 2; ++j) moves |= fmaxf(s[nr][0][j], s[nr][0][j + 2]) > m_ref[nr][j] + p.tau;
     }
     if (__any_sync(0xffffffffu, moves)) {  // some row's reference moves: O, l *= alpha
 #pragma unroll
@@ -297,7 +371,6 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
           float m = fmaxf(s[nr][0][j], s[nr][0][j + 2]);
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-          m *= sl2;
           if (m > m_ref[nr][j] + p.tau) {
             const float alpha = ex2_sfu(m_ref[nr][j] - m);
             m_ref[nr][j] = m;
@@ -314,19 +387,52 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float m = m_ref[nr][j & 1] == -INFINITY ? 0.f : m_ref[nr][j & 1];
-        e[j] = ex2_sfu(fmaf(s[nr][0][j], sl2, -m));
+        e[j] = ex2_sfu(s[nr][0][j] - m);
       }
       l[nr][0] += e[0] + e[2];
       l[nr][1] += e[1] + e[3];
+      if constexpr (KV8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] *= v_mul;
+      }
       pb[nr][0] = transpose8(pack_bf16x2(e[0], e[1]));
       pb[nr][1] = transpose8(pack_bf16x2(e[2], e[3]));
     }
+    uint32_t vc[4], nan_v[2] = {0, 0};
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
       uint32_t a[4];
-      ldsm4t(a, vs + v_row + (x >> 2) * 1024 + (((2 * (x & 3) + (lane >> 3 & 1)) ^ x7) << 4));
+      if constexpr (KV8) {
+        // pairs of codes, transposed by two chunks: of a chunk, d = 2 quad is row quad of O^T's
+        // tile, d = 2 quad + 1 row quad + 8
+        if (x % 2 == 0) {
+          const int key = (lane >> 3 & 1) * 8 + (lane & 7), c = x + (lane >> 4);
+          ldsm4t(vc, vs + key * D + ((c ^ (D == 128 ? key & 7 : key >> 1 & 3)) << 4));
+          nan_v[0] |= code_nans(vc[0]) | code_nans(vc[2]);
+          nan_v[1] |= code_nans(vc[1]) | code_nans(vc[3]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a[2 * h] = codes2_bf16(vc[2 * (x % 2) + h] << 8), a[2 * h + 1] = codes2_bf16(vc[2 * (x % 2) + h]);
+      } else
+        ldsm4t(a, vs + v_row + (x >> 2) * 1024 + (((2 * (x & 3) + (lane >> 3 & 1)) ^ x7) << 4));
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) mma16816(o[x][nr], a, pb[nr][0], pb[nr][1]);
+    }
+    if (KV8 && (odd != 0 || __any_sync(0xffffffffu, ((nan_v[0] | nan_v[1]) & 0x80808080u) != 0))) {
+      // a NaN among the values (or their scale) is one in all elements of the rows that see its
+      // key: no code is a NaN as it is converted, so nothing of it reaches the others
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        odd |= ((nan_v[h] & 0x8080u ? 1u : 0u) | (nan_v[h] & 0x80800000u ? 2u : 0u)) << (8 * h + q2);
+      odd = __reduce_or_sync(0xffffffffu, odd);
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int a = min(max(key_lo[nr][j] - j0, 0), 16), z = min(max(key_hi[nr][j] - j0, 0), 16);
+          const uint32_t sees = z > a ? (0xffffu >> (16 - (z - a))) << a : 0u;
+          if (odd & sees) poison |= 1u << (2 * nr + j);
+        }
     }
     __syncwarp();  // every lane has read the step
     ++done;
@@ -351,9 +457,13 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
         if (quad == 0) p.part_lse[place] = sum == 0.f ? -INFINITY : m_ref[nr][j] + __log2f(sum);
         if (sum == 0.f) continue;
         const float inv = poison >> (2 * nr + j) & 1 ? __uint_as_float(0x7fffffffu) : 1.f / sum;
-        float* dst = p.part_o + place * D + quad;
+        float* dst = p.part_o + place * D;
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) dst[16 * x] = o[x][nr][j] * inv, dst[16 * x + 8] = o[x][nr][j + 2] * inv;
+        for (int x = 0; x < D / 16; ++x) {
+          const float a = o[x][nr][j] * inv, b = o[x][nr][j + 2] * inv;
+          if constexpr (KV8) *reinterpret_cast<float2*>(dst + 16 * x + 2 * quad) = make_float2(a, b);
+          else dst[16 * x + quad] = a, dst[16 * x + quad + 8] = b;
+        }
       }
   }
   if (!ok) {  // let copies already in flight land before the CTA's shared memory goes away

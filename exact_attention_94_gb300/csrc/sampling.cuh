@@ -70,6 +70,8 @@ struct SharedParams {
   const int* seq_lens;       // [B]
   const int* starts;         // [G + 1]
   const int* shared_lens;    // [G]
+  const float* k_scale;      // [num_pages, Hkv], of 8-bit pages
+  const float* v_scale;
   const void* q;             // [B, Nq, Hq, d] bf16
   void* o;                   // the same
   float* lse;                // [B, Hq, Nq]
@@ -83,6 +85,7 @@ struct SharedParams {
   int win_left;              // -1: no window
   int box_rows;              // keys per TMA box: 16 .. 128, divides the page and the tile
   int shares;                // CTAs
+  int warps;                 // of a CTA, that attend for few rows
   int few;                   // most rows of an entry that a warp attends for: 0, 8, 16 or 32
   float few_cost;            // of a CTA's time a slot of few rows' weight takes
   float scale_log2, tau;
@@ -95,7 +98,7 @@ size_t shared_plan_bytes(int B, int G);
 void shared_plan_at(SharedPlan& plan, void* at, int B, int G);
 bool make_tmap_queries(CUtensorMap* m, const void* ptr, int D, int Hq, long long tokens, int heads, int tile_tokens);
 bool make_tmap_pages(CUtensorMap* m, const void* ptr, int D, int Hkv, int page_size, int num_pages, int box_rows);
-cudaError_t launch_decode_shared(const CUtensorMap (&maps)[5], const SharedParams& p, int D, cudaStream_t stream);  // q; k, v; k, v by 16 keys
+cudaError_t launch_decode_shared(const CUtensorMap (&maps)[5], SharedParams& p, int D, bool kv8, cudaStream_t stream);  // q; k, v; k, v by 16 keys
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, int c3,
                                             int c4) {

@@ -1063,3 +1063,22 @@ def decode_paged_shared(q, k_pages, v_pages, block_table, seq_lens, group_starts
     if st:
         _lib.check(st, "fa_decode_paged_shared")
     return o, lse
+
+
+@_on_call_stream
+def decode_kv8_shared(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, group_starts, shared_lens,
+                      max_seq_len: int, window_left: int = -1, num_shares: int = 0, scale: Optional[float] = None,
+                      workspace=None, *, dev, raw):
+    """decode_paged_shared over the 8-bit paged cache (codes and scales as in
+    decode_kv8).  Returns (o [B, Nq, Hq, d], lse [B, Hq, Nq])."""
+    num_pages, Hkv, P, d = _check_kv8(k_codes, v_codes, k_scale, v_scale, dev)
+    B, Nq, Hq, blocks, groups, L, wl, shares, workspace, o, lse = _shared_args(
+        q, d, Hkv, block_table, seq_lens, group_starts, shared_lens, max_seq_len, window_left, num_shares, workspace, dev)
+    st = lib().fa_decode_kv8_shared(q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
+                                    v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), group_starts.data_ptr(),
+                                    shared_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Nq, Hq, Hkv, d, P, num_pages,
+                                    blocks, L, groups, wl, shares, workspace.data_ptr(),
+                                    1.0 / math.sqrt(d) if scale is None else float(scale), raw)
+    if st:
+        _lib.check(st, "fa_decode_kv8_shared")
+    return o, lse

@@ -690,7 +690,24 @@ fa_status fa_decode_paged_shared(const void* q, const void* k_pages, const void*
                                  int max_seq_len, int num_groups, int window_left, int num_shares, void* workspace,
                                  float scale, fa_stream_t stream);
 
-/* Bytes of workspace for a call with these arguments; 0 for sizes that the call refuses. */
+/*
+ * fa_decode_paged_shared over the 8-bit paged cache: codes and scales as
+ * fa_kv8_append writes them (k_codes, v_codes, k_scale, v_scale as in
+ * fa_decode_kv8).  A group's shared keys are read with the scales of the pages in
+ * its longest request's table row.  A value, times its scale, or a code that is a
+ * NaN reaches the queries that see its key, in its own or all d elements of
+ * their O, and no others; a value scale that is NaN or infinite makes every
+ * value of its page a NaN.  A probability times its value scale is rounded to
+ * bf16 before it meets the codes; value scales lie within 2^-80 .. 2^80 (or are
+ * 0), no key scale is negative.
+ */
+fa_status fa_decode_kv8_shared(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                               const float* v_scale, const int* block_table, const int* seq_lens, const int* group_starts,
+                               const int* shared_lens, void* o, float* lse, int B, int Nq, int Hq, int Hkv, int d,
+                               int page_size, int num_pages, int max_blocks, int max_seq_len, int num_groups, int window_left,
+                               int num_shares, void* workspace, float scale, fa_stream_t stream);
+
+/* Bytes of workspace for a call of either with these arguments; 0 for sizes that the calls refuse. */
 size_t fa_decode_shared_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int num_groups, int num_shares);
 
 /*
