@@ -40,17 +40,23 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // Of a row of queries (at `row`, as copied), the second product operand for step x of 16 elements of d
-// against codes: a lane's four codes are d .. d + 3, the even ones first.
+// against codes: a lane's four codes are d .. d + 3.
 __device__ __forceinline__ void few_queries(uint32_t& b0, uint32_t& b1, const uint8_t* row, int x, int q, int r) {
   const int c = 8 * (x >> 2) + 2 * q + (x >> 1 & 1);
   const uint2 v = *reinterpret_cast<const uint2*>(row + ((c ^ r) << 4) + 8 * (x & 1));
-  b0 = __byte_perm(v.x, v.y, 0x5410), b1 = __byte_perm(v.x, v.y, 0x7632);
+  b0 = v.x, b1 = v.y;
 }
 // 16 bytes to shared memory, or zeros
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
@@ -74,7 +80,7 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
   const SharedList& list = p.plan.list[1];
   const Deal deal = deal_of(*p.plan.head, true);
   const int early = deal.early.n, all = early + deal.late.n, entries = p.plan.head->count[1];
-  const float sl2 = p.scale_log2;
+  const float sl2 = p.scale_log2, tau = KV8 ? fminf(p.tau, kMaxTau) : p.tau;
   if (lane == 0) {
     for (int i = 0; i < NST; ++i) mbar_init(bars + 8 * i, 1);
     fence_mbar_init();
@@ -136,6 +142,7 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
   // ------------------------------------------------------------ the piece in work
   float o[D / 16][NR][4], m_ref[NR][2], l[NR][2];
   uint32_t qf[QREG ? NR : 1][QREG ? D / 8 : 1];
+  float q_back[KV8 ? NR : 1][2];  // what undoes the rows' scales
   int key_lo[NR][2], key_hi[NR][2];
   uint32_t poison = 0;
   FewPiece pc = {};
@@ -199,6 +206,27 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
       t = pc.t0;
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
+      if constexpr (KV8) {  // queries to f16, a row times its own scale: four lanes a row
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          uint8_t* q_row = mem + QAT + (8 * nr + quad) * (D * 2);
+          uint32_t most = 0;
+#pragma unroll
+          for (int c = lane & 3; c < C16; c += 4) most = largest_bf16(most, *reinterpret_cast<const uint4*>(q_row + ((c ^ quad) << 4)));
+          most = max(most >> 16, most & 0xffffu);
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          const RowScale rs(most);
+#pragma unroll
+          for (int c = lane & 3; c < C16; c += 4) {
+            uint4* x = reinterpret_cast<uint4*>(q_row + ((c ^ quad) << 4));
+            *x = bf16_f16(*x, rs.to);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) q_back[nr][j] = __shfl_sync(0xffffffffu, rs.back, 4 * (q2 + j));
+        }
+        __syncwarp();
+      }
       if constexpr (QREG) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
@@ -292,20 +320,19 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
 #pragma unroll
       for (int j = 0; j < 4 * CHAINS; ++j) s[nr][j / 4][j % 4] = 0.f;
     uint4 kc[KV8 ? 2 : 1][KV8 ? CH : 1];  // codes: a key's chunks lane & 3 and, d = 128, 4 behind it
-    float mul = sl2, v_mul = 1.f;
-    uint32_t nan_k = 0, odd = 0;  // keys quad, quad + 8 with a NaN; 16 keys with values to poison who sees them
+    float mul = sl2, v_mul = 1.f, lv = 0.f;  // lv: of the value scale, less the reference's own
+    uint32_t odd = 0;  // 16 keys with values to poison who sees them
     if constexpr (KV8) {
       const float2 sc = s_scale[st];
       mul = sl2 * sc.x, v_mul = sc.y;
+      lv = scale_log2(v_mul) - kAtRefLog2;
       if (!(fabsf(v_mul) < INFINITY)) v_mul = 0.f, odd = 0xffffu;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
           const int key = quad + 8 * h, c = (lane & 3) + 4 * j;
-          const uint4 x = *reinterpret_cast<const uint4*>(mem + st * 2 * TILE + key * D + ((c ^ (D == 128 ? key & 7 : key >> 1 & 3)) << 4));
-          kc[h][j] = x;
-          if ((code_nans(x.x) | code_nans(x.y) | code_nans(x.z) | code_nans(x.w)) & 0x80808080u) nan_k |= 1u << h;
+          kc[h][j] = *reinterpret_cast<const uint4*>(mem + st * 2 * TILE + key * D + ((c ^ (D == 128 ? key & 7 : key >> 1 & 3)) << 4));
         }
     }
 #pragma unroll
@@ -316,13 +343,13 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
         for (int h = 0; h < 2; ++h) {
           const uint4& c = kc[h][x >> 2];
           const uint32_t word = (x & 3) == 0 ? c.x : (x & 3) == 1 ? c.y : (x & 3) == 2 ? c.z : c.w;
-          a[h] = codes2_bf16(word << 8), a[2 + h] = codes2_bf16(word);
+          codes_f16(word, a[h], a[2 + h]);
         }
       } else
         ldsm4(a, ks + k_row + (x >> 2) * 1024 + (((2 * (x & 3) + (lane >> 4)) ^ x7) << 4));
       if constexpr (QREG) {
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) mma16816(s[nr][x % CHAINS], a, qf[nr][2 * x], qf[nr][2 * x + 1]);
+        for (int nr = 0; nr < NR; ++nr) mma16816<KV8>(s[nr][x % CHAINS], a, qf[nr][2 * x], qf[nr][2 * x + 1]);
       } else {
 #pragma unroll
         for (int nr = 0; nr < NR; nr += 2) {  // two tiles of rows, two chunks
@@ -332,19 +359,10 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
             for (int i = 0; i < 2; ++i) few_queries(b[2 * i], b[2 * i + 1], mem + QAT + (8 * (nr + i) + quad) * (D * 2), x, lane & 3, quad);
           } else
             ldsm4(b, at + QAT + (8 * nr + (lane >> 4) * 8 + x7) * (D * 2) + (((2 * x + (lane >> 3 & 1)) ^ x7) << 4));
-          mma16816(s[nr][x % CHAINS], a, b[0], b[1]);
-          mma16816(s[nr + 1][x % CHAINS], a, b[2], b[3]);
+          mma16816<KV8>(s[nr][x % CHAINS], a, b[0], b[1]);
+          mma16816<KV8>(s[nr + 1][x % CHAINS], a, b[2], b[3]);
         }
       }
-    }
-    if (KV8 && __any_sync(0xffffffffu, nan_k != 0)) {
-      nan_k |= __shfl_xor_sync(0xffffffffu, nan_k, 1);
-      nan_k |= __shfl_xor_sync(0xffffffffu, nan_k, 2);
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (nan_k >> (j >> 1) & 1) s[nr][0][j] = __uint_as_float(0x7fffffffu);
     }
     bool moves = false;
 #pragma unroll
@@ -352,7 +370,7 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
 #pragma unroll
       for (int j = 0; j < 4 * (CHAINS - 1); ++j) s[nr][0][j] += s[nr][1 % CHAINS][j];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[nr][0][j] *= mul;
+      for (int j = 0; j < 4; ++j) s[nr][0][j] *= KV8 ? mul * q_back[nr][j & 1] : mul;
       if (!inside) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -361,7 +379,7 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
         }
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) moves |= fmaxf(s[nr][0][j], s[nr][0][j + 2]) > m_ref[nr][j] + p.tau;
+      for (int j = 0; j < 2; ++j) moves |= fmaxf(s[nr][0][j], s[nr][0][j + 2]) + lv > m_ref[nr][j] + tau;
     }
     if (__any_sync(0xffffffffu, moves)) {  // some row's reference moves: O, l *= alpha
 #pragma unroll
@@ -371,7 +389,8 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
           float m = fmaxf(s[nr][0][j], s[nr][0][j + 2]);
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-          if (m > m_ref[nr][j] + p.tau) {
+          m += lv;
+          if (m > m_ref[nr][j] + tau) {
             const float alpha = ex2_sfu(m_ref[nr][j] - m);
             m_ref[nr][j] = m;
             l[nr][j] *= alpha;
@@ -395,8 +414,8 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
 #pragma unroll
         for (int j = 0; j < 4; ++j) e[j] *= v_mul;
       }
-      pb[nr][0] = transpose8(pack_bf16x2(e[0], e[1]));
-      pb[nr][1] = transpose8(pack_bf16x2(e[2], e[3]));
+      pb[nr][0] = transpose8(KV8 ? pack_f16x2(e[0], e[1]) : pack_bf16x2(e[0], e[1]));
+      pb[nr][1] = transpose8(KV8 ? pack_f16x2(e[2], e[3]) : pack_bf16x2(e[2], e[3]));
     }
     uint32_t vc[4], nan_v[2] = {0, 0};
 #pragma unroll
@@ -408,22 +427,28 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
         if (x % 2 == 0) {
           const int key = (lane >> 3 & 1) * 8 + (lane & 7), c = x + (lane >> 4);
           ldsm4t(vc, vs + key * D + ((c ^ (D == 128 ? key & 7 : key >> 1 & 3)) << 4));
-          nan_v[0] |= code_nans(vc[0]) | code_nans(vc[2]);
-          nan_v[1] |= code_nans(vc[1]) | code_nans(vc[3]);
+          if (!inside) {  // (0 times a NaN is not 0)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const uint32_t nan = __vcmpeq4(vc[h] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              vc[h] &= ~nan;
+              nan_v[h & 1] |= nan;
+            }
+          }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) a[2 * h] = codes2_bf16(vc[2 * (x % 2) + h] << 8), a[2 * h + 1] = codes2_bf16(vc[2 * (x % 2) + h]);
+        for (int h = 0; h < 2; ++h) codes_f16(__byte_perm(vc[2 * (x % 2) + h], 0u, 0x3120), a[2 * h], a[2 * h + 1]);
       } else
         ldsm4t(a, vs + v_row + (x >> 2) * 1024 + (((2 * (x & 3) + (lane >> 3 & 1)) ^ x7) << 4));
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr) mma16816(o[x][nr], a, pb[nr][0], pb[nr][1]);
+      for (int nr = 0; nr < NR; ++nr) mma16816<KV8>(o[x][nr], a, pb[nr][0], pb[nr][1]);
     }
-    if (KV8 && (odd != 0 || __any_sync(0xffffffffu, ((nan_v[0] | nan_v[1]) & 0x80808080u) != 0))) {
-      // a NaN among the values (or their scale) is one in all elements of the rows that see its
-      // key: no code is a NaN as it is converted, so nothing of it reaches the others
+    if (KV8 && (odd != 0 || (!inside && __any_sync(0xffffffffu, (nan_v[0] | nan_v[1]) != 0)))) {
+      // a NaN among values that not all rows see, or a value scale that is no number, is a NaN
+      // in all elements of the rows that see it
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        odd |= ((nan_v[h] & 0x8080u ? 1u : 0u) | (nan_v[h] & 0x80800000u ? 2u : 0u)) << (8 * h + q2);
+        odd |= ((nan_v[h] & 0xffffu ? 1u : 0u) | (nan_v[h] >> 16 ? 2u : 0u)) << (8 * h + q2);
       odd = __reduce_or_sync(0xffffffffu, odd);
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)

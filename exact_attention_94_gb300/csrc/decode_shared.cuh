@@ -191,26 +191,30 @@ __device__ __forceinline__ long long cut_place(const SharedParams& p, bool few, 
 
 // ---------------------------------------------------------------- main
 
-// Two e4m3 codes in the high bytes of halves, as bf16, of finite codes: their bits moved to
-// bf16's places are the values times 2^-120, subnormal ones too.
-__device__ __forceinline__ uint32_t codes2_bf16(uint32_t t) {
-  const uint32_t r = (t >> 4 & 0x07f007f0u) | (t & 0x80008000u);
-  const uint32_t up = 0x7b807b80u;  // 2^120
-  uint32_t y;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(r), "r"(up));
-  return y;
+// 8-bit pages: codes are exact in f16, so K and V tiles become f16, and what they meet:
+//  - a row of queries times a power of two of its own, exact for what is within 2^28 of its largest;
+//  - probabilities times value scales, against a reference per row at which that is kAtRef: rounded by
+//    2^-11 of themselves, or by 2^-32 of the row's largest.  (The row sums share the reference.)
+constexpr float kAtRefLog2 = 7.f, kMaxTau = 8.f;
+constexpr float kLeastScale = -80.f;  // log2 of a value scale, from below
+__device__ __forceinline__ float scale_log2(float v) { return v > 0.f && v < INFINITY ? fmaxf(__log2f(v), kLeastScale) : kLeastScale; }
+// The factor that takes a row with this largest |bf16| to 2^14 .. 2^15, and what undoes it.
+struct RowScale {
+  float to, back;
+  __device__ __forceinline__ explicit RowScale(uint32_t largest) {
+    const uint32_t e = max(largest >> 7, 15u);
+    to = __uint_as_float((268u - e) << 23), back = __uint_as_float((e - 14u) << 23);
+  }
+};
+__device__ __forceinline__ uint32_t bf16_f16(uint32_t x, float scale) {
+  return pack_f16x2(__uint_as_float(x << 16) * scale, __uint_as_float(x & 0xffff0000u) * scale);
 }
-// Four codes in their order.
-__device__ __forceinline__ void codes_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
-  lo = codes2_bf16(__byte_perm(x, 0u, 0x1404));
-  hi = codes2_bf16(__byte_perm(x, 0u, 0x3424));
+__device__ __forceinline__ uint4 bf16_f16(uint4 x, float scale) {
+  return make_uint4(bf16_f16(x.x, scale), bf16_f16(x.y, scale), bf16_f16(x.z, scale), bf16_f16(x.w, scale));
 }
-// Bit 7 of each byte: the code is a NaN (other bits are anything).
-__device__ __forceinline__ uint32_t code_nans(uint32_t x) { return (x & 0x7f7f7f7fu) + 0x01010101u; }
-// Puts NaNs where codes are.
-__device__ __forceinline__ void nans_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
-  lo |= __vcmpeq2(__byte_perm(x, 0u, 0x1404) & 0x7f007f00u, 0x7f007f00u) & 0x7fff7fffu;
-  hi |= __vcmpeq2(__byte_perm(x, 0u, 0x3424) & 0x7f007f00u, 0x7f007f00u) & 0x7fff7fffu;
+__device__ __forceinline__ uint32_t largest_bf16(uint32_t m, uint4 x) {  // two maxima
+  const uint32_t a = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(m, x.x & a), __vmaxu2(__vmaxu2(x.y & a, x.z & a), x.w & a));
 }
 
 #include "decode_few.cuh"
@@ -233,10 +237,11 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   // Rings: K/V tiles, pieces, codes.  Q[s]: a tile of Q has landed; its last S product is
   // done.  Per tile t in turn: S ready, P's first and second 64 keys ready, the last
   // product of a run of key tiles done (O), and O read.  X: the softmax warps of a
-  // tile, and of both, have come this far.
+  // tile, and of both, have come this far.  Q_READY: a tile of Q is f16.
   enum { KV_FULL = 0, KV_EMPTY = NS, PC_FULL = 2 * NS, PC_EMPTY = PC_FULL + kPieces, Q_FULL = PC_EMPTY + kPieces,
          Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 2, O_FINAL = P_FULL + 4, O_EMPTY = O_FINAL + 2,
-         XB = O_EMPTY + 2, DRAIN = XB + 3, RAW_FULL = DRAIN + 1, RAW_EMPTY = RAW_FULL + RAW, NBARS = RAW_EMPTY + RAW };
+         XB = O_EMPTY + 2, DRAIN = XB + 3, RAW_FULL = DRAIN + 1, RAW_EMPTY = RAW_FULL + RAW,
+         Q_READY = RAW_EMPTY + RAW, NBARS = Q_READY + (KV8 ? 2 : 0) };
   const uint32_t bar0 = base + L::kMiscOff;
   auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
   constexpr uint32_t SLOT = L::kMiscOff + 8 * NBARS, PIECES = SLOT + 16;
@@ -244,9 +249,9 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Piece* s_piece = reinterpret_cast<Piece*>(sb + PIECES);                              // [kPieces]
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(sb + PIECES + 64 * kPieces);           // [2 groups][2][4]
-  float* s_scale = reinterpret_cast<float*>(sb + PIECES + 64 * kPieces + 64);          // KV8: [kScales][8 of keys, 8 of values]
+  float* s_scale = reinterpret_cast<float*>(sb + PIECES + 64 * kPieces + 64);          // KV8: [kScales][8 of keys, 8 of values, 8 logarithms of these]
   static_assert(sizeof(Piece) == 64 && PIECES % 8 == 0, "pieces");
-  static_assert(PIECES + 64 * kPieces + 64 + (KV8 ? kScales * 64 : 0) <= L::kMiscOff + L::kMisc, "misc area");
+  static_assert(PIECES + 64 * kPieces + 64 + (KV8 ? kScales * 96 : 0) <= L::kMiscOff + L::kMisc, "misc area");
   // Few rows, once the tiles are done with: a warp's region, and what it keeps beside its rings.
   constexpr int FEW = few_warps(D, NR, KV8);
   constexpr uint32_t FEW_BYTES = L::kMiscOff / FEW / 1024 * 1024, FEW_OWN = KV8 ? FEW_BYTES - 256 : FEW_BYTES;
@@ -257,6 +262,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
     for (int i = 0; i < NBARS; ++i) {
       int n = 1;
       if (KV8 && (i < NS || i >= RAW_EMPTY)) n = 4;          // the warps that convert
+      if (i >= Q_READY) n = 8;
       if (i >= PC_EMPTY && i < PC_EMPTY + kPieces) n = KV8 ? 15 : 11;  // who loads, converts, multiplies, eight warps of softmax
       if ((i >= P_FULL && i < P_FULL + 4) || i == O_EMPTY || i == O_EMPTY + 1) n = 128;
       if (i == XB || i == XB + 1) n = 4;
@@ -410,8 +416,8 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
         if (!ok) break;
         if (KV8 && warp == 3) {  // scales, which the softmax warps read behind this tile's values
           if (lane >> 3 == i) {
-            float* sc = s_scale + ((place / 2 - 1) % kScales) * 16 + (lane & 7);
-            sc[0] = k_scale, sc[8] = v_scale;
+            float* sc = s_scale + ((place / 2 - 1) % kScales) * 24 + (lane & 7);
+            sc[0] = k_scale, sc[8] = v_scale, sc[16] = scale_log2(v_scale);
           }
           __syncwarp();
         }
@@ -441,7 +447,9 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
     // ============================================================ products
     // Job n is a tile of rows times a tile of keys; jobs take S, P and O of tile n & 1.
     // S of job n is issued before the product of job n - 1's P, which waits for its softmax.
-    constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false), IDESC_O = idesc_bf16(128, D, false, true);
+    constexpr uint32_t IDESC_S = KV8 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
+    constexpr uint32_t IDESC_O = KV8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
+    constexpr int QUERIES = KV8 ? (int)Q_READY : (int)Q_FULL;
     struct Job {
       uint32_t vslot, vphase;
       bool on, first, last, frees;  // first, last of its tile's run in the piece; the last to read its values
@@ -485,13 +493,16 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
         bool here = there(BAR(KV_FULL) + 8 * sk, pk);
         for (int sub = 0; sub < subs; ++sub, ++n) {
           const uint32_t t = n & 1, q = qt + sub, qs = q & 1;
-          if (x == 0 && here) here = there(BAR(Q_FULL) + 8 * qs, q >> 1 & 1);
+          if (x == 0 && here) here = there(BAR(QUERIES) + 8 * qs, q >> 1 & 1);
           if (!here) {
-            // inputs that have not come yet: the last job's product need not wait for them
-            if (before.on && !(ok = product(before, t ^ 1))) break;
-            before.on = false;
+            // Inputs that have not come yet: the last job's product need not wait for them.  (Not
+            // for the second tile of rows: its values' place in the ring may be these keys'.)
+            if (sub == 0) {
+              if (before.on && !(ok = product(before, t ^ 1))) break;
+              before.on = false;
+            }
             ok = wait(BAR(KV_FULL) + 8 * sk, pk, 81);
-            if (ok && x == 0) ok = wait(BAR(Q_FULL) + 8 * qs, q >> 1 & 1, 80);
+            if (ok && x == 0) ok = wait(BAR(QUERIES) + 8 * qs, q >> 1 & 1, 80);
             if (!ok) break;
             here = true;
           }
@@ -539,9 +550,9 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
       if constexpr (KV8) {
         if (many || FEW != 12) {
           asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    // ============================================================ codes to bf16
+    // ============================================================ codes to f16
     // A tile of codes as TMA lays it, 16-byte chunks swizzled over the banks, becomes one of
-    // bf16 as the products take it.  Tiles come in the order of the ring's places.
+    // f16 as the products take it.  Tiles come in the order of the ring's places.
     const int me = threadIdx.x & 127;
     auto convert = [&](int place) {
       const int from = place % RAW, to = place % NS;
@@ -554,14 +565,9 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
       for (int i = 0; i < D / 16; ++i) {
         const int at = i * 128 + me, key = at / (D / 16), c = (at % (D / 16)) ^ (D == 128 ? key & 7 : key >> 1 & 3);
         const uint4 x = raw[at];
-        const uint32_t nan = code_nans(x.x) | code_nans(x.y) | code_nans(x.z) | code_nans(x.w);
         uint4 y[2];
-        codes_bf16(x.x, y[0].x, y[0].y), codes_bf16(x.y, y[0].z, y[0].w);
-        codes_bf16(x.z, y[1].x, y[1].y), codes_bf16(x.w, y[1].z, y[1].w);
-        if (nan & 0x80808080u) {
-          nans_bf16(x.x, y[0].x, y[0].y), nans_bf16(x.y, y[0].z, y[0].w);
-          nans_bf16(x.z, y[1].x, y[1].y), nans_bf16(x.w, y[1].z, y[1].w);
-        }
+        codes_f16(x.x, y[0].x, y[0].y), codes_f16(x.y, y[0].z, y[0].w);
+        codes_f16(x.z, y[1].x, y[1].y), codes_f16(x.w, y[1].z, y[1].w);
         uint8_t* row = tile + (key >> 3) * CH * 1024 + (c >> 2) * 1024 + (key & 7) * 128;
         const int odd = c >> 2 & 1;  // (d = 128: half the lanes store their second half first, to other banks)
         *reinterpret_cast<uint4*>(row + ((((2 * c + odd) & 7) ^ (key & 7)) << 4)) = odd ? y[1] : y[0];
@@ -594,7 +600,9 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
     const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + (t ? 128u : 0u), tO = tmem + lane_off + 256u + (t ? (uint32_t)D : 0u);
-    const float sl2 = p.scale_log2;
+    float sl2 = p.scale_log2;
+    const float tau = KV8 ? fminf(p.tau, kMaxTau) : p.tau;
+    int qt = 0;  // tiles of Q so far
     const int my_tok = r / p.heads, my_head = r - my_tok * p.heads;
     const long long rows = (long long)p.B * p.Nq * p.Hq;
     bool ok = true;
@@ -616,6 +624,42 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
         key_hi = min(s.end, pos + 1);
       }
       const bool live = __any_sync(0xffffffffu, valid);  // some row of the warp is there
+      if constexpr (KV8) {  // queries to f16, a row times its own scale
+        const int q = qt + (pair ? side : 0), slot = q & 1;
+        ok = mbar_wait(BAR(Q_FULL + slot), q >> 1 & 1, w, 95);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        uint8_t* row = sb + L::kQOff + slot * TILE + r * 128;
+        uint32_t most = 0;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          most = largest_bf16(most, *reinterpret_cast<const uint4*>(row + (c >> 3) * CHUNK + (((c & 7) ^ (r & 7)) << 4)));
+        const RowScale rs(max(most >> 16, most & 0xffffu));
+        sl2 = p.scale_log2 * rs.back;
+        if (!pair) {  // each group converts half, when both have seen it
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(XB + 2));
+          ok = mbar_wait(BAR(XB + 2), xb++ & 1, w, 96);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4* at = reinterpret_cast<uint4*>(row + (c >> 3) * CHUNK + (((c & 7) ^ (r & 7)) << 4));
+          if (pair || c / (D / 16) == side) *at = bf16_f16(*at, rs.to);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(BAR(Q_READY + slot));
+          if (pair) mbar_arrive(BAR(Q_READY + slot));
+        }
+        qt += pair ? 2 : 1;
+      }
       float m_ref = -INFINITY, l = 0.f;
       bool poison = false;
       const int x_step = pair ? 1 : 2, x_first = pair ? 0 : side;
@@ -627,7 +671,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
           break;
         }
         tc_fence_after();
-        const float* sc = s_scale + ((it0 + x) % kScales) * 16;
+        const float* sc = s_scale + ((it0 + x) % kScales) * 24;
         if constexpr (KV8) {  // the tile's scales came with its values
           const int uv = v_place(it0 + x);
           ok = mbar_wait(BAR(KV_FULL + uv % NS), uv / NS & 1, w, 94);
@@ -658,8 +702,8 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
 #pragma unroll 1
               for (int i = 0; i < 8 * CH; ++i) {
                 const uint4 v = row[(i >> 3) * 64 + (i + lane & 7)];  // (other banks for each lane)
-                bad |= __vcmpeq2(v.x & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(v.y & 0x7f807f80u, 0x7f807f80u) |
-                       __vcmpeq2(v.z & 0x7f807f80u, 0x7f807f80u) | __vcmpeq2(v.w & 0x7f807f80u, 0x7f807f80u);
+                constexpr uint32_t E = KV8 ? 0x7c007c00u : 0x7f807f80u;
+                bad |= __vcmpeq2(v.x & E, E) | __vcmpeq2(v.y & E, E) | __vcmpeq2(v.z & E, E) | __vcmpeq2(v.w & E, E);
               }
               odd |= bad != 0;
             }
@@ -735,12 +779,13 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
           float m_new = -INFINITY;
           if constexpr (KV8) {
 #pragma unroll
-            for (int g = 0; g < 8; g += 2) m_new = max3f(m_new, mq[g] * mul[g], mq[g + 1] * mul[g + 1]);
+            for (int g = 0; g < 8; g += 2) m_new = max3f(m_new, fmaf(mq[g], mul[g], sc[16 + g]), fmaf(mq[g + 1], mul[g + 1], sc[17 + g]));
+            m_new -= kAtRefLog2;
           } else {
             m_new = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
           }
           float alpha = 1.f;
-          const bool moves = m_new > m_ref + p.tau;
+          const bool moves = m_new > m_ref + tau;
           if (moves) {
             alpha = ex2_sfu(m_ref - m_new);
             m_ref = m_new;
@@ -774,10 +819,12 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
                 acc[i & 1] = f2_add(acc[i & 1], f2_pack(p0, p1));
                 if constexpr (KV8) {
                   float v = sc[8 + g];
-                  if (!inside && !(fabsf(v) < INFINITY)) v = 0.f;  // (who sees such a page has a NaN by `poison`)
+                  if (!(fabsf(v) < INFINITY)) v = inside ? __uint_as_float(0x7fffffffu) : 0.f;  // (who sees such a page has a NaN by `poison`)
                   f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(v, v)), p0, p1);
+                  pk[16 * (c & 1) + i] = pack_f16x2(p0, p1);
+                } else {
+                  pk[16 * (c & 1) + i] = pack_bf16x2(p0, p1);
                 }
-                pk[16 * (c & 1) + i] = pack_bf16x2(p0, p1);
               }
             } else {  // keys that no row of the warp sees
 #pragma unroll
