@@ -56,7 +56,6 @@ constexpr int kFewLeast = 8, kFewLateLeast = 24;  // weight of those shares at l
 constexpr int kPlanSmem = 1024;                // groups, entries in the plan's shared memory
 constexpr int kMergeRows = 8;                  // of a warp of the merge
 constexpr int kPieces = 6;                     // announced ahead
-constexpr int kScales = 8;                     // key tiles whose scales are kept
 
 // The main kernel over bf16 pages, and over pages of 8-bit codes (KV8), whose tiles four more
 // warps convert.
@@ -68,15 +67,14 @@ template <int D, bool KV8>
 struct SharedLayout {
   static constexpr int kThreads = KV8 ? 512 : 384;
   static constexpr uint32_t kTile = 128u * D * 2u;  // a tile of Q, K or V
-  static constexpr uint32_t kRawTile = 128u * D;    // of codes
+  static constexpr uint32_t kRawTile = 128u * D;    // of codes, which land in their slot's second half
   static constexpr uint32_t kChunk = 128u * 128u;   // of Q: 128 rows x 128 bytes (one 128-byte swizzle column)
-  static constexpr int kStages = (KV8 ? 3 : 5) * 128 / D;  // K/V ring slots
-  static constexpr int kRaw = KV8 ? 512 / D : 0;           // slots of the codes' ring
+  static constexpr int kStages = 640 / D;                  // K/V ring slots
+  static constexpr int kScales = KV8 ? 1024 / D : 0;       // key tiles whose scales are kept
   static constexpr uint32_t kQOff = 0;                     // two tiles of Q
   static constexpr uint32_t kKVOff = 2 * kTile;
-  static constexpr uint32_t kRawOff = kKVOff + kStages * kTile;
-  static constexpr uint32_t kMiscOff = kRawOff + kRaw * kRawTile;
-  static constexpr uint32_t kMisc = 2048;                  // barriers, pieces
+  static constexpr uint32_t kMiscOff = kKVOff + kStages * kTile;
+  static constexpr uint32_t kMisc = KV8 && D == 64 ? 3072 : 2048;  // barriers, pieces
   static constexpr uint32_t kBytes = kMiscOff + kMisc + 1024;  // alignment slack
 };
 static_assert(SharedLayout<128, false>::kBytes <= 227 * 1024 && SharedLayout<128, true>::kBytes <= 227 * 1024, "shared memory");
@@ -225,7 +223,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
                             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k16,
                             const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ SharedParams p) {
   using L = SharedLayout<D, KV8>;
-  constexpr int NS = L::kStages, RAW = L::kRaw, CH = D / 64;
+  constexpr int NS = L::kStages, RAW = KV8 ? NS : 0, SCALES = L::kScales, CH = D / 64;
   constexpr uint32_t TILE = L::kTile, CHUNK = L::kChunk;
   const int warp = warp_id(), lane = lane_id();
 
@@ -234,14 +232,15 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   uint8_t* sb = smem_raw + (base - raw);
   const uint32_t q_s = base + L::kQOff, kv_s = base + L::kKVOff;
 
-  // Rings: K/V tiles, pieces, codes.  Q[s]: a tile of Q has landed; its last S product is
+  // Rings: K/V tiles, pieces.  RAW_FULL: a tile's codes have landed.  Q[s]: a tile of Q has landed; its last S product is
   // done.  Per tile t in turn: S ready, P's first and second 64 keys ready, the last
   // product of a run of key tiles done (O), and O read.  X: the softmax warps of a
-  // tile, and of both, have come this far.  Q_READY: a tile of Q is f16.
+  // tile, and of both, have come this far.  Q_READY: a tile of Q is f16.  SC_FULL: a
+  // key tile's scales are there.
   enum { KV_FULL = 0, KV_EMPTY = NS, PC_FULL = 2 * NS, PC_EMPTY = PC_FULL + kPieces, Q_FULL = PC_EMPTY + kPieces,
          Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 2, O_FINAL = P_FULL + 4, O_EMPTY = O_FINAL + 2,
-         XB = O_EMPTY + 2, DRAIN = XB + 3, RAW_FULL = DRAIN + 1, RAW_EMPTY = RAW_FULL + RAW,
-         Q_READY = RAW_EMPTY + RAW, NBARS = Q_READY + (KV8 ? 2 : 0) };
+         XB = O_EMPTY + 2, DRAIN = XB + 3, RAW_FULL = DRAIN + 1, Q_READY = RAW_FULL + RAW,
+         SC_FULL = Q_READY + (KV8 ? 2 : 0), NBARS = SC_FULL + SCALES };
   const uint32_t bar0 = base + L::kMiscOff;
   auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
   constexpr uint32_t SLOT = L::kMiscOff + 8 * NBARS, PIECES = SLOT + 16;
@@ -249,9 +248,9 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Piece* s_piece = reinterpret_cast<Piece*>(sb + PIECES);                              // [kPieces]
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(sb + PIECES + 64 * kPieces);           // [2 groups][2][4]
-  float* s_scale = reinterpret_cast<float*>(sb + PIECES + 64 * kPieces + 64);          // KV8: [kScales][8 of keys, 8 of values, 8 logarithms of these]
+  float* s_scale = reinterpret_cast<float*>(sb + PIECES + 64 * kPieces + 64);          // KV8: [SCALES][8 of keys, 8 of values, 8 logarithms of these]
   static_assert(sizeof(Piece) == 64 && PIECES % 8 == 0, "pieces");
-  static_assert(PIECES + 64 * kPieces + 64 + (KV8 ? kScales * 96 : 0) <= L::kMiscOff + L::kMisc, "misc area");
+  static_assert(PIECES + 64 * kPieces + 64 + SCALES * 96 <= L::kMiscOff + L::kMisc, "misc area");
   // Few rows, once the tiles are done with: a warp's region, and what it keeps beside its rings.
   constexpr int FEW = few_warps(D, NR, KV8);
   constexpr uint32_t FEW_BYTES = L::kMiscOff / FEW / 1024 * 1024, FEW_OWN = KV8 ? FEW_BYTES - 256 : FEW_BYTES;
@@ -261,8 +260,8 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBARS; ++i) {
       int n = 1;
-      if (KV8 && (i < NS || i >= RAW_EMPTY)) n = 4;          // the warps that convert
-      if (i >= Q_READY) n = 8;
+      if (KV8 && i < NS) n = 4;  // the warps that convert
+      if (i >= Q_READY) n = i < SC_FULL ? 8 : 1;
       if (i >= PC_EMPTY && i < PC_EMPTY + kPieces) n = KV8 ? 15 : 11;  // who loads, converts, multiplies, eight warps of softmax
       if ((i >= P_FULL && i < P_FULL + 4) || i == O_EMPTY || i == O_EMPTY + 1) n = 128;
       if (i == XB || i == XB + 1) n = 4;
@@ -407,23 +406,25 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
       const int plane = now.page * p.Hkv + now.head;
       float k_scale = 0.f, v_scale = 0.f;
       if constexpr (KV8) {
-        if (warp == 3 && lane < 8 * now.n && lane < now.last) k_scale = p.k_scale[plane], v_scale = p.v_scale[plane];
+        if (warp == 0 && lane < 8 * now.n && lane < now.last) k_scale = p.k_scale[plane], v_scale = p.v_scale[plane];
       }
-      constexpr int RING = KV8 ? RAW : NS, FULL = KV8 ? (int)RAW_FULL : (int)KV_FULL, EMPTY = KV8 ? (int)RAW_EMPTY : (int)KV_EMPTY;
+      constexpr int FULL = KV8 ? (int)RAW_FULL : (int)KV_FULL;
       for (int i = 0; i < now.n; ++i) {
-        const int slot = place % RING, here = min(boxes, (max(now.last - 8 * i, 0) + (1 << shift) - 1) >> shift);
-        if (place >= RING) ok = __all_sync(0xffffffffu, mbar_wait(BAR(EMPTY + slot), (place / RING - 1) & 1, w, 74));
+        const int slot = place % NS, here = min(boxes, (max(now.last - 8 * i, 0) + (1 << shift) - 1) >> shift);
+        if (place >= NS) ok = __all_sync(0xffffffffu, mbar_wait(BAR(KV_EMPTY + slot), (place / NS - 1) & 1, w, 74));
         if (!ok) break;
-        if (KV8 && warp == 3) {  // scales, which the softmax warps read behind this tile's values
+        if (KV8 && warp == 0) {  // scales
+          const int sc_slot = (place + 1) / 2 % (SCALES + !SCALES);
           if (lane >> 3 == i) {
-            float* sc = s_scale + ((place / 2 - 1) % kScales) * 24 + (lane & 7);
+            float* sc = s_scale + sc_slot * 24 + (lane & 7);
             sc[0] = k_scale, sc[8] = v_scale, sc[16] = scale_log2(v_scale);
           }
           __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(SC_FULL + sc_slot));
         }
         if (elect_one()) mbar_arrive_expect_tx(BAR(FULL + slot), (uint32_t)(here * p.box_rows * D * (KV8 ? 1 : 2)));
         __syncwarp();
-        const uint32_t dst = KV8 ? base + L::kRawOff + slot * L::kRawTile : kv_s + slot * TILE, bar = BAR(FULL + slot);
+        const uint32_t dst = kv_s + slot * TILE + (KV8 ? L::kRawTile : 0), bar = BAR(FULL + slot);
         for (int x = 0; x < here; ++x) {  // (one lane issues, with the same operands in all)
           const int row = __shfl_sync(0xffffffffu, at8, 8 * i + (x << shift));
           if constexpr (KV8) {
@@ -552,33 +553,39 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
           asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // ============================================================ codes to f16
     // A tile of codes as TMA lays it, 16-byte chunks swizzled over the banks, becomes one of
-    // f16 as the products take it.  Tiles come in the order of the ring's places.
+    // f16 as the products take it, in its place: the codes are its second half, and those
+    // of the last 64 keys wait in registers until all have been read.  (With the codes in a ring
+    // of their own there was room for three tiles, and products waited 1000 cycles each.)
     const int me = threadIdx.x & 127;
     auto convert = [&](int place) {
-      const int from = place % RAW, to = place % NS;
-      bool ok = mbar_wait(BAR(RAW_FULL + from), place / RAW & 1, w, 91);
-      if (ok && place >= NS) ok = mbar_wait(BAR(KV_EMPTY + to), (place / NS - 1) & 1, w, 92);
-      if (!__all_sync(0xffffffffu, ok)) return false;
-      const uint4* raw = reinterpret_cast<const uint4*>(sb + L::kRawOff + from * L::kRawTile);
-      uint8_t* tile = sb + L::kKVOff + to * TILE;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const int at = i * 128 + me, key = at / (D / 16), c = (at % (D / 16)) ^ (D == 128 ? key & 7 : key >> 1 & 3);
-        const uint4 x = raw[at];
+      const int slot = place % NS;
+      if (!__all_sync(0xffffffffu, mbar_wait(BAR(RAW_FULL + slot), place / NS & 1, w, 91))) return false;
+      uint8_t* tile = sb + L::kKVOff + slot * TILE;
+      const uint4* raw = reinterpret_cast<const uint4*>(tile + L::kRawTile);
+      constexpr int N = D / 32;  // chunks of a thread in half a tile
+      uint4 x[N], late[N];
+      auto put = [&](const uint4& codes, int at) {
+        const int key = at / (D / 16), c = (at % (D / 16)) ^ (D == 128 ? key & 7 : key >> 1 & 3);
         uint4 y[2];
-        codes_f16(x.x, y[0].x, y[0].y), codes_f16(x.y, y[0].z, y[0].w);
-        codes_f16(x.z, y[1].x, y[1].y), codes_f16(x.w, y[1].z, y[1].w);
+        codes_f16(codes.x, y[0].x, y[0].y), codes_f16(codes.y, y[0].z, y[0].w);
+        codes_f16(codes.z, y[1].x, y[1].y), codes_f16(codes.w, y[1].z, y[1].w);
         uint8_t* row = tile + (key >> 3) * CH * 1024 + (c >> 2) * 1024 + (key & 7) * 128;
         const int odd = c >> 2 & 1;  // (d = 128: half the lanes store their second half first, to other banks)
         *reinterpret_cast<uint4*>(row + ((((2 * c + odd) & 7) ^ (key & 7)) << 4)) = odd ? y[1] : y[0];
         *reinterpret_cast<uint4*>(row + ((((2 * c + 1 - odd) & 7) ^ (key & 7)) << 4)) = odd ? y[0] : y[1];
-      }
+      };
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = raw[i * 128 + me];
+#pragma unroll
+      for (int i = 0; i < N; ++i) late[i] = raw[(N + i) * 128 + me];
+#pragma unroll
+      for (int i = 0; i < N; ++i) put(x[i], i * 128 + me);
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < N; ++i) put(late[i], (N + i) * 128 + me);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(BAR(RAW_EMPTY + from));
-        mbar_arrive(BAR(KV_FULL + to));
-      }
+      if (lane == 0) mbar_arrive(BAR(KV_FULL + slot));
       return true;
     };
     bool ok = many;
@@ -671,10 +678,10 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
           break;
         }
         tc_fence_after();
-        const float* sc = s_scale + ((it0 + x) % kScales) * 24;
-        if constexpr (KV8) {  // the tile's scales came with its values
-          const int uv = v_place(it0 + x);
-          ok = mbar_wait(BAR(KV_FULL + uv % NS), uv / NS & 1, w, 94);
+        const int sc_slot = (it0 + x) % (SCALES + !SCALES);
+        const float* sc = s_scale + sc_slot * 24;
+        if constexpr (KV8) {
+          ok = mbar_wait(BAR(SC_FULL + sc_slot), (it0 + x) / SCALES & 1, w, 94);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
