@@ -196,6 +196,11 @@ __device__ __forceinline__ long long cut_place(const SharedParams& p, bool few, 
 constexpr float kAtRefLog2 = 7.f, kMaxTau = 8.f;
 constexpr float kLeastScale = -80.f;  // log2 of a value scale, from below
 __device__ __forceinline__ float scale_log2(float v) { return v > 0.f && v < INFINITY ? fmaxf(__log2f(v), kLeastScale) : kLeastScale; }
+__device__ __forceinline__ void load_8(const float* at, float (&x)[8]) {  // of shared memory
+  const uint32_t a = smem_u32(at);
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(a) : "memory");
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]) : "r"(a + 16) : "memory");
+}
 // The factor that takes a row with this largest |bf16| to 2^14 .. 2^15, and what undoes it.
 struct RowScale {
   float to, back;
@@ -235,21 +240,20 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   // Rings: K/V tiles, pieces.  RAW_FULL: a tile's codes have landed.  Q[s]: a tile of Q has landed; its last S product is
   // done.  Per tile t in turn: S ready, P's first and second 64 keys ready, the last
   // product of a run of key tiles done (O), and O read.  X: the softmax warps of a
-  // tile, and of both, have come this far.  Q_READY: a tile of Q is f16.  SC_FULL: a
-  // key tile's scales are there.
+  // tile, and of both, have come this far.  Q_READY: a tile of Q is f16.
   enum { KV_FULL = 0, KV_EMPTY = NS, PC_FULL = 2 * NS, PC_EMPTY = PC_FULL + kPieces, Q_FULL = PC_EMPTY + kPieces,
          Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 2, O_FINAL = P_FULL + 4, O_EMPTY = O_FINAL + 2,
          XB = O_EMPTY + 2, DRAIN = XB + 3, RAW_FULL = DRAIN + 1, Q_READY = RAW_FULL + RAW,
-         SC_FULL = Q_READY + (KV8 ? 2 : 0), NBARS = SC_FULL + SCALES };
+         NBARS = Q_READY + (KV8 ? 2 : 0) };
   const uint32_t bar0 = base + L::kMiscOff;
   auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
-  constexpr uint32_t SLOT = L::kMiscOff + 8 * NBARS, PIECES = SLOT + 16;
+  constexpr uint32_t SLOT = L::kMiscOff + (8 * NBARS + 15) / 16 * 16, PIECES = SLOT + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sb + SLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Piece* s_piece = reinterpret_cast<Piece*>(sb + PIECES);                              // [kPieces]
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(sb + PIECES + 64 * kPieces);           // [2 groups][2][4]
   float* s_scale = reinterpret_cast<float*>(sb + PIECES + 64 * kPieces + 64);          // KV8: [SCALES][8 of keys, 8 of values, 8 logarithms of these]
-  static_assert(sizeof(Piece) == 64 && PIECES % 8 == 0, "pieces");
+  static_assert(sizeof(Piece) == 64 && PIECES % 16 == 0, "pieces; scales are read 16 bytes at a time");
   static_assert(PIECES + 64 * kPieces + 64 + SCALES * 96 <= L::kMiscOff + L::kMisc, "misc area");
   // Few rows, once the tiles are done with: a warp's region, and what it keeps beside its rings.
   constexpr int FEW = few_warps(D, NR, KV8);
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
     for (int i = 0; i < NBARS; ++i) {
       int n = 1;
       if (KV8 && i < NS) n = 4;  // the warps that convert
-      if (i >= Q_READY) n = i < SC_FULL ? 8 : 1;
+      if (i >= Q_READY) n = 8;
       if (i >= PC_EMPTY && i < PC_EMPTY + kPieces) n = KV8 ? 15 : 11;  // who loads, converts, multiplies, eight warps of softmax
       if ((i >= P_FULL && i < P_FULL + 4) || i == O_EMPTY || i == O_EMPTY + 1) n = 128;
       if (i == XB || i == XB + 1) n = 4;
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   const bool many = (int)blockIdx.x < n_many;
   const bool few = NR > 0 && (!many || p.plan.head->shares[2] > 0);  // (behind the tiles there are the late shares alone)
   // Registers go where a row's 128 scores are held: 56 x 4 warps + 224 x 8 is what 168 x 12 was,
-  // (56 + 56) x 4 + 200 x 8, and then 56 x 4 + 152 x 12, what 128 x 16 was.  A CTA without tiles
+  // (56 + 72) x 4 + 192 x 8, and then 56 x 4 + 152 x 12, what 128 x 16 was.  A CTA without tiles
   // goes to the latter at once, one with tiles behind a barrier: where the warps that convert
   // could grow before the softmax warps have, they would take what those wait for forever.
   if (warp < 4) {
@@ -413,14 +417,14 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
         const int slot = place % NS, here = min(boxes, (max(now.last - 8 * i, 0) + (1 << shift) - 1) >> shift);
         if (place >= NS) ok = __all_sync(0xffffffffu, mbar_wait(BAR(KV_EMPTY + slot), (place / NS - 1) & 1, w, 74));
         if (!ok) break;
-        if (KV8 && warp == 0) {  // scales
+        if (KV8 && warp == 0) {  // scales, which the softmax warps read when the keys' scores are there
           const int sc_slot = (place + 1) / 2 % (SCALES + !SCALES);
           if (lane >> 3 == i) {
             float* sc = s_scale + sc_slot * 24 + (lane & 7);
-            sc[0] = k_scale, sc[8] = v_scale, sc[16] = scale_log2(v_scale);
+            // (a value scale that is no number is a NaN)
+            sc[0] = k_scale, sc[8] = fabsf(v_scale) < INFINITY ? v_scale : __uint_as_float(0x7fffffffu), sc[16] = scale_log2(v_scale);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(SC_FULL + sc_slot));
         }
         if (elect_one()) mbar_arrive_expect_tx(BAR(FULL + slot), (uint32_t)(here * p.box_rows * D * (KV8 ? 1 : 2)));
         __syncwarp();
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
     if (KV8 && warp >= 12) {
       if constexpr (KV8) {
         if (many || FEW != 12) {
-          asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+          asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ============================================================ codes to f16
     // A tile of codes as TMA lays it, 16-byte chunks swizzled over the banks, becomes one of
     // f16 as the products take it, in its place: the codes are its second half, and those
@@ -577,9 +581,9 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = raw[i * 128 + me];
 #pragma unroll
-      for (int i = 0; i < N; ++i) late[i] = raw[(N + i) * 128 + me];
-#pragma unroll
       for (int i = 0; i < N; ++i) put(x[i], i * 128 + me);
+#pragma unroll
+      for (int i = 0; i < N; ++i) late[i] = raw[(N + i) * 128 + me];
       asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
       for (int i = 0; i < N; ++i) put(late[i], (N + i) * 128 + me);
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
       if (FEW == 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     } else {
     if (!KV8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    else if (many || FEW != 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else if (many || FEW != 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     if (many) {
     // ============================================================ softmax
     const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
@@ -678,15 +682,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
           break;
         }
         tc_fence_after();
-        const int sc_slot = (it0 + x) % (SCALES + !SCALES);
-        const float* sc = s_scale + sc_slot * 24;
-        if constexpr (KV8) {
-          ok = mbar_wait(BAR(SC_FULL + sc_slot), (it0 + x) / SCALES & 1, w, 94);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-        }
+        const float* sc = s_scale + (it0 + x) % (SCALES + !SCALES) * 24;
         const bool inside = j0 >= s.all_lo && j0 + kSharedTile <= s.all_hi;  // every row sees every key
         if (!inside) {
           // Some rows do not see some keys of the tile, and 0 times a NaN or an infinity
@@ -745,11 +741,19 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
           uint32_t sr[4][32], none = 0;  // bit c: no row of the warp sees any of the c-th 32 keys
           constexpr int G = KV8 ? 8 : 4;  // loads, each with its maximum
           float mq[G], mul[KV8 ? 8 : 1];  // what scores of each load's keys are multiplied by
+          float v_mul[KV8 ? 8 : 1], v_log[KV8 ? 8 : 1];
           if constexpr (KV8) {
+            // (the scales are asked for here, in whole vectors: read where they are used, each was
+            // waited for, 1000 cycles a tile)
+            load_8(sc, mul), load_8(sc + 16, v_log), load_8(sc + 8, v_mul);
 #pragma unroll
             for (int g = 0; g < 8; ++g) tmem_ld16_max(tS + 16 * g, &sr[g >> 1][16 * (g & 1)], mq[g]);
 #pragma unroll
-            for (int g = 0; g < 8; ++g) mul[g] = sc[g] * sl2;
+            for (int g = 0; g < 8; ++g) mul[g] *= sl2;
+            if (!inside) {  // (who sees values whose scale is no number has a NaN by `poison`)
+#pragma unroll
+              for (int g = 0; g < 8; ++g) v_mul[g] = v_mul[g] == v_mul[g] ? v_mul[g] : 0.f;
+            }
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32 * c, sr[c], mq[c]);
@@ -786,7 +790,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
           float m_new = -INFINITY;
           if constexpr (KV8) {
 #pragma unroll
-            for (int g = 0; g < 8; g += 2) m_new = max3f(m_new, fmaf(mq[g], mul[g], sc[16 + g]), fmaf(mq[g + 1], mul[g + 1], sc[17 + g]));
+            for (int g = 0; g < 8; g += 2) m_new = max3f(m_new, fmaf(mq[g], mul[g], v_log[g]), fmaf(mq[g + 1], mul[g + 1], v_log[g + 1]));
             m_new -= kAtRefLog2;
           } else {
             m_new = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
@@ -825,9 +829,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
                 float p0 = ex2_sfu(y0), p1 = ex2_sfu(y1);
                 acc[i & 1] = f2_add(acc[i & 1], f2_pack(p0, p1));
                 if constexpr (KV8) {
-                  float v = sc[8 + g];
-                  if (!(fabsf(v) < INFINITY)) v = inside ? __uint_as_float(0x7fffffffu) : 0.f;  // (who sees such a page has a NaN by `poison`)
-                  f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(v, v)), p0, p1);
+                  f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(v_mul[g], v_mul[g])), p0, p1);
                   pk[16 * (c & 1) + i] = pack_f16x2(p0, p1);
                 } else {
                   pk[16 * (c & 1) + i] = pack_bf16x2(p0, p1);
