@@ -1119,7 +1119,6 @@ static fa_status shared_common(SharedParams& p, CUtensorMap& tq, const void* q, 
   p.box_rows = 16;
   while (p.box_rows < kSharedTile && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
   p.shares = num_shares;
-  p.few = shared_few(Nq, p.heads);
   p.scale_log2 = scale * kLog2e;
   p.tau = g_opt.tau;
   p.err = g_err_ptr;

@@ -1,4 +1,4 @@
-// Attention for entries of few rows (32 query rows at most), a warp by itself for each
+// Attention for entries of few rows (16 query rows at most), a warp by itself for each
 // piece of a unit, beside or behind the tiles of many rows: included by
 // fa_decode_shared.cu, within its namespace.
 //
@@ -74,7 +74,6 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
   FewPiece* ring = state->ring;
   const uint32_t bars = smem_u32(state->bars);
   float2* s_scale = reinterpret_cast<float2*>(mem + NST * 2 * TILE + QBYTES);  // KV8: of a step's keys, values
-  constexpr bool QREG = NR <= 2;  // queries stay in registers
   constexpr uint32_t QAT = NST * 2 * TILE;
   const int lane = lane_id(), quad = lane >> 2, q2 = 2 * (lane & 3);
   const SharedList& list = p.plan.list[1];
@@ -92,7 +91,7 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
   walk.at = walk.to = 0;
   bool more = all > 0;
   if (k >= 0 && k < early) walk.start(list, entries, deal, k);
-  int taken = 0, started = 0, finished = 0, queried = 0;  // pieces: known, worked on, done with, whose queries were asked for
+  int taken = 0, started = 0, queried = 0;  // pieces: known, worked on, whose queries were asked for
   int t_next = 0, t_end = 0, beg = 0, row = 0, head = 0;
   struct Batch {
     int n, page, rows8, head;  // lane i: step i's page and its place in there, in eights of keys
@@ -141,7 +140,7 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
   float k_scale = 0.f, v_scale = 0.f;
   // ------------------------------------------------------------ the piece in work
   float o[D / 16][NR][4], m_ref[NR][2], l[NR][2];
-  uint32_t qf[QREG ? NR : 1][QREG ? D / 8 : 1];
+  uint32_t qf[NR][D / 8];
   float q_back[KV8 ? NR : 1][2];  // what undoes the rows' scales
   int key_lo[NR][2], key_hi[NR][2];
   uint32_t poison = 0;
@@ -189,7 +188,7 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
       ++i_now;
       ++issued;
     }
-    if (queried < taken && queried <= (QREG ? started : finished)) {
+    if (queried < taken && queried <= started) {
       const FewPiece& f = ring[queried % kFewPieces];
       const int n = f.ntok * p.heads, h0 = (f.head_kind >> 1) * p.heads;
       for (int i = lane; i < ROWS * C16; i += 32) {
@@ -227,23 +226,22 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
         }
         __syncwarp();
       }
-      if constexpr (QREG) {
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+      for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-          for (int c = 0; c < C16; c += 4) {
+        for (int c = 0; c < C16; c += 4) {
+          if constexpr (KV8) {  // two steps of 16 elements of d
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              few_queries(qf[nr][c + 2 * i], qf[nr][c + 2 * i + 1], mem + QAT + (8 * nr + quad) * (D * 2), c / 2 + i, lane & 3, quad);
+          } else {
             uint32_t r[4];
-            if constexpr (KV8) {  // two steps of 16 elements of d
-#pragma unroll
-              for (int i = 0; i < 2; ++i) few_queries(r[2 * i], r[2 * i + 1], mem + QAT + (8 * nr + quad) * (D * 2), c / 2 + i, lane & 3, quad);
-            } else {
-              ldsm4(r, at + QAT + (8 * nr + x7) * (D * 2) + (((c + (lane >> 3)) ^ x7) << 4));
-            }
+            ldsm4(r, at + QAT + (8 * nr + x7) * (D * 2) + (((c + (lane >> 3)) ^ x7) << 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i) qf[nr][c + i] = r[i];
           }
-        __syncwarp();
-      }
+        }
+      __syncwarp();
       ++started;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
@@ -313,12 +311,11 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
       fence_proxy_async_smem();  // (the copy that fills the place next comes behind these writes)
       __syncwarp();
     }
-    constexpr int CHAINS = NR <= 2 ? 2 : 1;  // of dependent products
-    float s[NR][CHAINS][4];
+    float s[NR][2][4];  // two chains of dependent products
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-      for (int j = 0; j < 4 * CHAINS; ++j) s[nr][j / 4][j % 4] = 0.f;
+      for (int j = 0; j < 4; ++j) s[nr][0][j] = s[nr][1][j] = 0.f;
     uint4 kc[KV8 ? 2 : 1][KV8 ? CH : 1];  // codes: a key's chunks lane & 3 and, d = 128, 4 behind it
     float mul = sl2, v_mul = 1.f, lv = 0.f;  // lv: of the value scale, less the reference's own
     uint32_t odd = 0;  // 16 keys with values to poison who sees them
@@ -347,30 +344,14 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
         }
       } else
         ldsm4(a, ks + k_row + (x >> 2) * 1024 + (((2 * (x & 3) + (lane >> 4)) ^ x7) << 4));
-      if constexpr (QREG) {
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) mma16816<KV8>(s[nr][x % CHAINS], a, qf[nr][2 * x], qf[nr][2 * x + 1]);
-      } else {
-#pragma unroll
-        for (int nr = 0; nr < NR; nr += 2) {  // two tiles of rows, two chunks
-          uint32_t b[4];
-          if constexpr (KV8) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) few_queries(b[2 * i], b[2 * i + 1], mem + QAT + (8 * (nr + i) + quad) * (D * 2), x, lane & 3, quad);
-          } else
-            ldsm4(b, at + QAT + (8 * nr + (lane >> 4) * 8 + x7) * (D * 2) + (((2 * x + (lane >> 3 & 1)) ^ x7) << 4));
-          mma16816<KV8>(s[nr][x % CHAINS], a, b[0], b[1]);
-          mma16816<KV8>(s[nr + 1][x % CHAINS], a, b[2], b[3]);
-        }
-      }
+      for (int nr = 0; nr < NR; ++nr) mma16816<KV8>(s[nr][x % 2], a, qf[nr][2 * x], qf[nr][2 * x + 1]);
     }
     bool moves = false;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-      for (int j = 0; j < 4 * (CHAINS - 1); ++j) s[nr][0][j] += s[nr][1 % CHAINS][j];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[nr][0][j] *= KV8 ? mul * q_back[nr][j & 1] : mul;
+      for (int j = 0; j < 4; ++j) s[nr][0][j] = (s[nr][0][j] + s[nr][1][j]) * (KV8 ? mul * q_back[nr][j & 1] : mul);
       if (!inside) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -464,7 +445,6 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
     if (++st == NST) st = 0, phase ^= 1u;
     if (++t < pc.t1) continue;
     // ---- results of the piece
-    ++finished;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll

@@ -47,8 +47,7 @@ constexpr int kPlanThreads = 1024;
 // rows, and each of their tiles of keys.  Of few rows: their start and end, in 16 keys.
 constexpr int kLeadOne = 5, kTileOne = 2, kLeadTwo = 12, kTileTwo = 3, kLeadFew = 6;
 constexpr float kFew = 0.17f;                  // of a CTA's half microseconds 16 keys of few rows take, d = 128
-constexpr int kFewEarly = 12;                  // shares of few rows for each CTA at most, that warps begin with,
-__host__ __device__ constexpr int few_late(int few) { return few == 32 ? 8 : 16; }  // and that they take
+constexpr int kFewEarly = 12, kFewLate = 16;   // shares of few rows for each CTA at most, that warps begin with and that they take
 constexpr float kFew8 = 1.f;                   // what 16 keys of 8 bits take of that
 constexpr int kFewLateOf = 2;                  // one in so many of few rows' weight is dealt late,
 constexpr int kFewLateFrom = 64;               //   where a warp's share is this much at least
@@ -59,9 +58,7 @@ constexpr int kPieces = 6;                     // announced ahead
 
 // The main kernel over bf16 pages, and over pages of 8-bit codes (KV8), whose tiles four more
 // warps convert.
-// Warps of a CTA that attend for few rows: of 8-bit pages more, whose registers have O of 32
-// rows and d = 128 left out.
-__host__ __device__ constexpr int few_warps(int D, int NR, bool kv8) { return !kv8 || (NR == 4 && D == 128) ? 8 : 12; }
+__host__ __device__ constexpr int few_warps(bool kv8) { return kv8 ? 12 : 8; }  // of a CTA, that attend for few rows
 
 template <int D, bool KV8>
 struct SharedLayout {
@@ -103,10 +100,6 @@ __device__ __forceinline__ Weight weight_of(const SharedParams& p, bool few, int
   return few ? Weight{kLeadFew, 1} : ntok > p.tile_tokens ? Weight{kLeadTwo, kTileTwo} : Weight{kLeadOne, kTileOne};
 }
 
-// a / b for a >= 0, b > 0, in 32 bits where both fit
-__device__ __forceinline__ long long div_ll(long long a, long long b) {
-  return (((unsigned long long)a | (unsigned long long)b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
-}
 // `total` slots of weight in n equal shares: the first `more` have each + 1.
 struct Equal {
   long long total, each, more;
@@ -256,7 +249,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   static_assert(sizeof(Piece) == 64 && PIECES % 16 == 0, "pieces; scales are read 16 bytes at a time");
   static_assert(PIECES + 64 * kPieces + 64 + SCALES * 96 <= L::kMiscOff + L::kMisc, "misc area");
   // Few rows, once the tiles are done with: a warp's region, and what it keeps beside its rings.
-  constexpr int FEW = few_warps(D, NR, KV8);
+  constexpr int FEW = few_warps(KV8);
   constexpr uint32_t FEW_BYTES = L::kMiscOff / FEW / 1024 * 1024, FEW_OWN = KV8 ? FEW_BYTES - 256 : FEW_BYTES;
   static_assert(KV8 || PIECES + FEW * sizeof(FewState) <= L::kMiscOff + L::kMisc, "misc area");
   static_assert(sizeof(FewState) <= 256, "misc area");
@@ -553,7 +546,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
     };
     if (KV8 && warp >= 12) {
       if constexpr (KV8) {
-        if (many || FEW != 12) {
+        if (many) {
           asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ============================================================ codes to f16
     // A tile of codes as TMA lays it, 16-byte chunks swizzled over the banks, becomes one of
@@ -592,7 +585,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
       if (lane == 0) mbar_arrive(BAR(KV_FULL + slot));
       return true;
     };
-    bool ok = many;
+    bool ok = true;
     int it = 0;
     Piece s;
     for (int piece = 0; ok && take(piece, s, 93) && s.t0 < s.t1; ++piece)
@@ -602,10 +595,10 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
       }
       __syncwarp();
       if (many) __syncthreads();
-      if (FEW == 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     } else {
     if (!KV8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    else if (many || FEW != 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    else if (many) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     if (many) {
     // ============================================================ softmax
     const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
@@ -900,14 +893,14 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
       fence_proxy_async_smem();
       __syncthreads();
     }
-    if (KV8 && FEW == 12) {
+    if (KV8) {
       if (many) asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
       else asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     } else {
       few_rows();
     }
     }
-    if (KV8 && FEW == 12) few_rows();
+    if (KV8) few_rows();
   }
   __syncwarp();
   tc_fence_before();
@@ -935,7 +928,6 @@ static cudaError_t launch_shared_main(const CUtensorMap (&maps)[5], const Shared
   switch (p.few) {
     case 8: return launch_shared_t<D, 1, KV8>(maps, p, cfg);
     case 16: return launch_shared_t<D, 2, KV8>(maps, p, cfg);
-    case 32: return launch_shared_t<D, 4, KV8>(maps, p, cfg);
     default: return launch_shared_t<D, 0, KV8>(maps, p, cfg);
   }
 }

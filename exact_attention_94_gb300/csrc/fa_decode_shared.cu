@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fa_shared_plan_kernel(const _
     const int others = p.shares - head.shares[0];
     const bool late = total[1] >= (long long)kFewLateFrom * p.warps * others;
     head.total[2] = late ? total[1] / (others > 0 ? kFewLateOf : 1) : 0;
-    head.shares[2] = shares_in((long long)few_late(p.few) * p.shares, head.total[2], kFewLateLeast);
+    head.shares[2] = shares_in((long long)kFewLate * p.shares, head.total[2], kFewLateLeast);
     if (late && head.shares[2] == 0) head.shares[2] = 1;
     head.total[1] = total[1] - head.total[2];
     head.shares[1] = head.total[1] > 0 ? max(shares_in((long long)p.warps * others, head.total[1], kFewLeast), 1) : 0;
@@ -354,12 +354,16 @@ static size_t plan_layout(SharedPlan* plan, void* at, int B, int G) {
   if (plan != nullptr) *plan = pl;
   return off;
 }
-int shared_few(int Nq, int heads) {
+// The most rows of an entry that a warp attends for, if a request's own keys meet no more;
+// 0: tiles for all.  (64 requests of 4096 tokens, 64 heads over 8, d = 128: 16 rows 223 us by
+// warps and 193 by tiles, but 4 drafts of 4 heads behind shared prompts 38 and 41; 32 rows 367
+// and 198.  8-bit pages, whose conversions take registers: 16 rows 386 and 255, of d = 64 98 and 146.)
+int shared_few(int Nq, int heads, int D, bool kv8) {
   const int rows = Nq * heads;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+  return rows <= 8 ? 8 : rows <= 16 && !(kv8 && D == 128) ? 16 : 0;
 }
 size_t shared_part_rows(int B, int Nq, int Hq, int heads, int shares) {
-  return 4 * (size_t)B * Nq * Hq + 512 * (size_t)shares + 2 * (size_t)shared_few(Nq, heads) * (kFewEarly + few_late(shared_few(Nq, heads))) * shares;
+  return 4 * (size_t)B * Nq * Hq + 512 * (size_t)shares + 2 * (size_t)shared_few(Nq, heads, 64, false) * (kFewEarly + kFewLate) * shares;
 }
 size_t shared_plan_bytes(int B, int G) { return plan_layout(nullptr, nullptr, B, G); }
 void shared_plan_at(SharedPlan& plan, void* at, int B, int G) { plan_layout(&plan, at, B, G); }
@@ -379,7 +383,8 @@ static cudaError_t launch_merge(const SharedParams& p, cudaLaunchConfig_t& cfg) 
 cudaError_t launch_decode_shared(const CUtensorMap (&maps)[5], SharedParams& p, int D, bool kv8, cudaStream_t stream) {
   if (D != 64 && D != 128) return cudaErrorInvalidValue;
   p.few_cost = kFew * D / 128 * (kv8 ? kFew8 : 1.f);
-  p.warps = few_warps(D, p.few / 8, kv8);
+  p.few = shared_few(p.Nq, p.heads, D, kv8);
+  p.warps = few_warps(kv8);
   fa_shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;

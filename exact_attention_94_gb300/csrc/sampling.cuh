@@ -6,6 +6,11 @@
 
 namespace fa {
 
+// a / b for a >= 0, b > 0, in 32 bits where both fit
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  return (((unsigned long long)a | (unsigned long long)b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // Norms of heads with the rotation (see fa_qk_norm_rope in fa.h).
 struct NormRopeParams {
   const void* q;             // inputs of the forward
@@ -86,13 +91,13 @@ struct SharedParams {
   int box_rows;              // keys per TMA box: 16 .. 128, divides the page and the tile
   int shares;                // CTAs
   int warps;                 // of a CTA, that attend for few rows
-  int few;                   // most rows of an entry that a warp attends for: 0, 8, 16 or 32
+  int few;                   // most rows of an entry that a warp attends for: 0, 8 or 16
   float few_cost;            // of a CTA's time a slot of few rows' weight takes
   float scale_log2, tau;
   unsigned* err;
   unsigned long long timeout_ns;
 };
-int shared_few(int Nq, int heads);
+int shared_few(int Nq, int heads, int D, bool kv8);
 size_t shared_part_rows(int B, int Nq, int Hq, int heads, int shares);
 size_t shared_plan_bytes(int B, int G);
 void shared_plan_at(SharedPlan& plan, void* at, int B, int G);
