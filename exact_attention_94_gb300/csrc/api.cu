@@ -1139,9 +1139,11 @@ fa_status fa_decode_paged_shared(const void* q, const void* k_pages, const void*
                                      page_size, num_pages, max_blocks, max_seq_len, num_groups, window_left, num_shares,
                                      workspace, scale);
   if (st != FA_OK) return st;
-  for (int i = 0; i < 4; ++i)
-    if (!make_tmap_pages(&maps[1 + i], i & 1 ? v_pages : k_pages, d, Hkv, page_size, num_pages, i < 2 ? p.box_rows : 16))
+  for (int i = 0; i < 4; ++i) {
+    if (i >= 2 && p.box_rows == 16) maps[1 + i] = maps[i - 1];
+    else if (!make_tmap_pages(&maps[1 + i], i & 1 ? v_pages : k_pages, d, Hkv, page_size, num_pages, i < 2 ? p.box_rows : 16))
       return FA_ERR_INVALID_ARG;
+  }
   return launch_decode_shared(maps, p, d, false, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -1159,9 +1161,11 @@ fa_status fa_decode_kv8_shared(const void* q, const void* k_codes, const void* v
                                      workspace, scale);
   if (st != FA_OK) return st;
   p.k_scale = k_scale, p.v_scale = v_scale;
-  for (int i = 0; i < 4; ++i)
-    if (!make_tmap_codes(&maps[1 + i], i & 1 ? v_codes : k_codes, d, page_size, (long long)num_pages * Hkv, i < 2 ? p.box_rows : 16))
+  for (int i = 0; i < 4; ++i) {
+    if (i >= 2 && p.box_rows == 16) maps[1 + i] = maps[i - 1];
+    else if (!make_tmap_codes(&maps[1 + i], i & 1 ? v_codes : k_codes, d, page_size, (long long)num_pages * Hkv, i < 2 ? p.box_rows : 16))
       return FA_ERR_INVALID_ARG;
+  }
   return launch_decode_shared(maps, p, d, true, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 

@@ -11,6 +11,10 @@
 // 8 x 8 blocks between lanes, and O^T stays in registers.  A warp has its own ring of
 // steps in shared memory, filled by TMA across units' borders, and meets no other warp
 // until its results are merged.
+//
+// A warp alone takes some 1300 to 1570 cycles a step, dependent instructions and
+// instruction fetches, so an SM's eight take 80 GB/s of d = 128 and 48 of d = 64 (HBM's
+// share of an SM is 45); beside 130 CTAs of tiles 45.
 constexpr int kFewStages = 5;  // of a warp's ring, at most
 constexpr int kFewPieces = 4;  // a warp knows of: one it works on, those it loads
 

@@ -9,33 +9,53 @@
 //
 // Three kernels, the launch of each overlapping the one before:
 //  - the plan, one CTA: an entry for each group's shared keys and each request's
-//    own (query tokens, keys, table row), and where each CTA's share of the work
-//    begins.  The work is one list of tiles of 128 keys, of all (entry, K/V head,
-//    256 rows) units, dealt in equal shares; a unit counts `lead` tiles more, for
-//    its start and end.
-//  - the main kernel, one CTA per SM.  Rows take the M side of both tcgen05
-//    products: S [128 x 128 keys] = Q K^T, O [128 x d] += P V with P in TMEM over
-//    S, two tiles in turn, so one's products run while the other's softmax does.
-//    Units of more than 128 rows are two tiles of rows that meet the same keys;
-//    units of up to 128 are one tile of rows, whose key tiles the two take in
-//    turn, and both results are merged at the end.
-//  - the merge, a warp per query row: results of whole units (at their rows) or of
-//    the pieces that shares' borders cut.
+//    own (query tokens, keys, table row), in two lists: entries of many rows, whose
+//    (entry, K/V head, 256 rows) units are tiles of 128 keys, and of few (8 or 16),
+//    whose (entry, K/V head) units are steps of 16 keys.  Each list is cut in shares
+//    of equal weight, a unit weighing more for its start and end.
+//  - the main kernel, one CTA per SM.  A CTA of the first has a share of tiles; the
+//    warps of the others begin with a share of few rows each, and all warps take the
+//    rest of those from a queue as they come to an end.  So products that tensor cores
+//    bound run beside keys that HBM bounds.  (Own keys as tiles too, an eighth of their
+//    128 rows used: 64 requests with 16385 shared and 100 to 2000 own tokens 101 us
+//    and not 85, 256 with 32768 and 1 to 512 376 and not 257.)
+//    Tiles: rows take the M side of both tcgen05 products: S [128 x 128 keys] = Q K^T,
+//    O [128 x d] += P V with P in TMEM over S, two tiles in turn, so one's products run
+//    while the other's softmax does.  Units of more than 128 rows are two tiles of rows
+//    that meet the same keys; units of up to 128 are one tile of rows, whose key tiles
+//    the two take in turn, and both results are merged at the end.
+//    Few rows: decode_few.cuh.
+//  - the merge, a warp for up to 8 query rows: results of whole units (at their rows) or
+//    of the pieces that shares' borders cut.
 //
 // Rows of a tile are query tokens times the query heads of one K/V head, as they
 // lie in Q: a TMA box of [tokens][heads][64 elements].
 //
-// Main kernel's warps: 2 walks over the shares and announces their pieces; 0 loads
-// K and 3 loads Q and V (K and V into one ring, across units); 1 issues the products;
-// 4-7 and 8-11 are the softmax of the two tiles, a thread per row.
+// Main kernel's warps, of tiles: 2 walks over the share and announces its pieces; 0
+// loads K and 3 loads Q and V (K and V into one ring, across units); 1 issues the
+// products; 4-7 and 8-11 are the softmax of the two tiles, a thread per row; 12-15
+// convert 8-bit tiles.
 //
 // A TMA box is a page's keys (128 at most) of one head, all d of them: a tile of K or
 // V lies in shared memory as [8 keys][64 elements of d][8 x 128 bytes], so that one
 // box fills whole eights of keys.
+//
+// Measured, 64 heads over 8, d = 128, replayed graphs (bf16 pages / 8-bit):
+//   64 requests, 16385 shared, 100 to 2000 own            85 / 101 us
+//   256 requests, 32768 shared, 1 to 512 own              257 / 390 us
+//   256 requests, 32768 shared, one own                   226 / 312 us, 1.2 / 0.88 PFLOP/s
+//   32 requests, 131072 shared (256 rows)                 138 / 170 us
+//   64 requests, 8192 own                                 350 us, 6.1 TB/s / 271 us, 4.0 TB/s
+//   4 requests, 777 shared, 32 heads over 8               19 / 21 us
+// bf16 tiles are bound by the products (1570 cycles a job of two 128 x 128 x 128 products
+// that take 1280).  8-bit ones are bound by the softmax warps, with which the
+// converting ones share issue slots and registers: 2400 cycles a job.  The smallest
+// calls are the three kernels' latencies one after the other: plan 5 us, main 11, merge 3.
 #pragma once
 
 #include "sampling.cuh"
 
+#include <atomic>
 #include <cmath>
 
 namespace fa {
@@ -189,6 +209,19 @@ __device__ __forceinline__ long long cut_place(const SharedParams& p, bool few, 
 constexpr float kAtRefLog2 = 7.f, kMaxTau = 8.f;
 constexpr float kLeastScale = -80.f;  // log2 of a value scale, from below
 __device__ __forceinline__ float scale_log2(float v) { return v > 0.f && v < INFINITY ? fmaxf(__log2f(v), kLeastScale) : kLeastScale; }
+// Barrier `id` of 128 threads, and whether `ok` holds in all of them.
+__device__ __forceinline__ bool all_of_128(int id, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %2, 0;\n\t"
+      "bar.red.and.pred p, %1, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
 __device__ __forceinline__ void load_8(const float* at, float (&x)[8]) {  // of shared memory
   const uint32_t a = smem_u32(at);
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(a) : "memory");
@@ -556,7 +589,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
     const int me = threadIdx.x & 127;
     auto convert = [&](int place) {
       const int slot = place % NS;
-      if (!__all_sync(0xffffffffu, mbar_wait(BAR(RAW_FULL + slot), place / NS & 1, w, 91))) return false;
+      const bool ok = mbar_wait(BAR(RAW_FULL + slot), place / NS & 1, w, 91);
       uint8_t* tile = sb + L::kKVOff + slot * TILE;
       const uint4* raw = reinterpret_cast<const uint4*>(tile + L::kRawTile);
       constexpr int N = D / 32;  // chunks of a thread in half a tile
@@ -577,7 +610,8 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
       for (int i = 0; i < N; ++i) put(x[i], i * 128 + me);
 #pragma unroll
       for (int i = 0; i < N; ++i) late[i] = raw[(N + i) * 128 + me];
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      // (where a warp's wait has run out all four stop here: none waits for it again)
+      if (!all_of_128(1, ok)) return false;
 #pragma unroll
       for (int i = 0; i < N; ++i) put(late[i], (N + i) * 128 + me);
       fence_proxy_async_smem();
@@ -916,8 +950,16 @@ template <int D, int NR, bool KV8>
 static cudaError_t launch_shared_t(const CUtensorMap (&maps)[5], const SharedParams& p, cudaLaunchConfig_t& cfg) {
   auto kern = fa_decode_shared_kernel<D, NR, KV8>;
   constexpr uint32_t smem = SharedLayout<D, KV8>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (once for each of the first 64 devices: 1 us of the host's time a call)
+  static std::atomic<unsigned long long> set{0};
+  int dev = 64;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(set.load(std::memory_order_relaxed) & bit)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   cfg.gridDim = dim3((unsigned)p.shares);
   cfg.blockDim = dim3(SharedLayout<D, KV8>::kThreads);
   cfg.dynamicSmemBytes = smem;

@@ -697,9 +697,13 @@ fa_status fa_decode_paged_shared(const void* q, const void* k_pages, const void*
  * its longest request's table row.  A value, times its scale, or a code that is a
  * NaN reaches the queries that see its key, in its own or all d elements of
  * their O, and no others; a value scale that is NaN or infinite makes every
- * value of its page a NaN.  A probability times its value scale is rounded to
- * bf16 before it meets the codes; value scales lie within 2^-80 .. 2^80 (or are
- * 0), no key scale is negative.
+ * value of its page a NaN.  Queries are exact for elements within 2^28 of their
+ * row's largest; a probability times its value scale is rounded by 2^-11 of
+ * itself, or by 2^-32 of the row's largest, before it meets the codes.  No scale
+ * is negative; value scales lie within 2^-80 .. 2^80 (or are 0).  Where a page
+ * that requests share is only partly shared, and each has a copy of it
+ * (fa_kv8_append's copy_src), the copies' scales may differ: what the group
+ * shares is then read from the longest request's.
  */
 fa_status fa_decode_kv8_shared(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
                                const float* v_scale, const int* block_table, const int* seq_lens, const int* group_starts,
