@@ -78,7 +78,9 @@ constexpr int kPieces = 6;                     // announced ahead
 
 // The main kernel over bf16 pages, and over pages of 8-bit codes (KV8), whose tiles four more
 // warps convert.
-__host__ __device__ constexpr int few_warps(bool kv8) { return kv8 ? 12 : 8; }  // of a CTA, that attend for few rows
+// Warps of a CTA that attend for few rows: the softmax warps, and of 8-bit pages those that
+// convert, of d = 64 all of them (of d = 128 their rings have no room).
+__host__ __device__ constexpr int few_warps(int D, bool kv8) { return kv8 || D == 64 ? 12 : 8; }
 
 template <int D, bool KV8>
 struct SharedLayout {
@@ -91,7 +93,7 @@ struct SharedLayout {
   static constexpr uint32_t kQOff = 0;                     // two tiles of Q
   static constexpr uint32_t kKVOff = 2 * kTile;
   static constexpr uint32_t kMiscOff = kKVOff + kStages * kTile;
-  static constexpr uint32_t kMisc = KV8 && D == 64 ? 3072 : 2048;  // barriers, pieces
+  static constexpr uint32_t kMisc = D == 64 ? 4096 : 2048;  // barriers, pieces
   static constexpr uint32_t kBytes = kMiscOff + kMisc + 1024;  // alignment slack
 };
 static_assert(SharedLayout<128, false>::kBytes <= 227 * 1024 && SharedLayout<128, true>::kBytes <= 227 * 1024, "shared memory");
@@ -282,7 +284,8 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   static_assert(sizeof(Piece) == 64 && PIECES % 16 == 0, "pieces; scales are read 16 bytes at a time");
   static_assert(PIECES + 64 * kPieces + 64 + SCALES * 96 <= L::kMiscOff + L::kMisc, "misc area");
   // Few rows, once the tiles are done with: a warp's region, and what it keeps beside its rings.
-  constexpr int FEW = few_warps(KV8);
+  constexpr int FEW = few_warps(D, KV8);
+  constexpr bool ALL = !KV8 && FEW == 12;  // the warps that load and multiply are among them
   constexpr uint32_t FEW_BYTES = L::kMiscOff / FEW / 1024 * 1024, FEW_OWN = KV8 ? FEW_BYTES - 256 : FEW_BYTES;
   static_assert(KV8 || PIECES + FEW * sizeof(FewState) <= L::kMiscOff + L::kMisc, "misc area");
   static_assert(sizeof(FewState) <= 256, "misc area");
@@ -335,8 +338,17 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   // (56 + 72) x 4 + 192 x 8, and then 56 x 4 + 152 x 12, what 128 x 16 was.  A CTA without tiles
   // goes to the latter at once, one with tiles behind a barrier: where the warps that convert
   // could grow before the softmax warps have, they would take what those wait for forever.
+  auto few_rows = [&]() {
+    if constexpr (NR > 0) {
+      const int x = ALL ? warp : warp - 4, others = (int)gridDim.x - n_many;
+      if (few)
+        attend_few<D, NR, KV8, FEW_OWN>(p, tm_k16, tm_v16, w, many ? -1 : x * others + (int)blockIdx.x - n_many, base + x * FEW_BYTES,
+                                        sb + x * FEW_BYTES,
+                                        reinterpret_cast<FewState*>(KV8 ? sb + x * FEW_BYTES + FEW_OWN : sb + PIECES + x * sizeof(FewState)));
+    }
+  };
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (!ALL || many) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (!many) {
   } else if (warp == 2) {
     // ============================================================ walk over the share
@@ -567,16 +579,8 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   }
   __syncwarp();
   if (many) __syncthreads();  // shared memory changes hands, and registers
+  if (ALL) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
   } else {
-    auto few_rows = [&]() {
-      if constexpr (NR > 0) {
-        const int x = warp - 4, others = (int)gridDim.x - n_many;
-        if (few)
-          attend_few<D, NR, KV8, FEW_OWN>(p, tm_k16, tm_v16, w, many ? -1 : x * others + (int)blockIdx.x - n_many, base + x * FEW_BYTES,
-                                          sb + x * FEW_BYTES,
-                                          reinterpret_cast<FewState*>(KV8 ? sb + x * FEW_BYTES + FEW_OWN : sb + PIECES + x * sizeof(FewState)));
-      }
-    };
     if (KV8 && warp >= 12) {
       if constexpr (KV8) {
         if (many) {
@@ -631,8 +635,8 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
       if (many) __syncthreads();
       asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     } else {
-    if (!KV8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    else if (many) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if (!KV8 && (!ALL || many)) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    else if (KV8 && many) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     if (many) {
     // ============================================================ softmax
     const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
@@ -930,12 +934,16 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
     if (KV8) {
       if (many) asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
       else asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    } else if (ALL) {
+      if (many) asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+      else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     } else {
       few_rows();
     }
     }
     if (KV8) few_rows();
   }
+  if (ALL) few_rows();
   __syncwarp();
   tc_fence_before();
   __syncthreads();

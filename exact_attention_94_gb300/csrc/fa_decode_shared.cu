@@ -384,7 +384,7 @@ cudaError_t launch_decode_shared(const CUtensorMap (&maps)[5], SharedParams& p, 
   if (D != 64 && D != 128) return cudaErrorInvalidValue;
   p.few_cost = kFew * D / 128 * (kv8 ? kFew8 : 1.f);
   p.few = shared_few(p.Nq, p.heads, D, kv8);
-  p.warps = few_warps(kv8);
+  p.warps = few_warps(D, kv8);
   fa_shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
