@@ -640,7 +640,7 @@ def _on_call_stream(fn):
                 raise ValueError("stream must be on the device of the tensors")
             with torch.cuda.stream(stream):
                 return fn(*args, dev=dev, raw=stream.cuda_stream, **kwargs)
-        if dev == torch.cuda.current_device():
+        if dev == torch._C._cuda_getDevice():  # (a tensor is there, so CUDA is set up)
             return fn(*args, dev=dev, raw=torch._C._cuda_getCurrentRawStream(dev), **kwargs)
         with torch.cuda.device(dev):
             return fn(*args, dev=dev, raw=torch._C._cuda_getCurrentRawStream(dev), **kwargs)
@@ -670,11 +670,13 @@ def _check(name, t, dtype, dev, shape):
 
 def _check_dims(name, t, dtype, dev, dims, what):
     """As _check for a tensor that sets the call's sizes: its dimensions."""
-    if isinstance(t, torch.Tensor) and t.dim() != dims:
-        raise ValueError(f"{name} must be {what}")
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
-        _refuse(name, t, dtype, dev, None)
-    return t.shape
+    if isinstance(t, torch.Tensor):
+        size = t.shape
+        if len(size) != dims:
+            raise ValueError(f"{name} must be {what}")
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return size
+    _refuse(name, t, dtype, dev, None)
 
 
 def _check_int(name, n):

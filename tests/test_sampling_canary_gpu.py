@@ -76,3 +76,44 @@ def test_many_requests_in_many_groups():
     assert torch.allclose(lse[..., 0], pl, atol=2.0 ** -11, rtol=0)
     # both round O and the probabilities to bf16: 2^-8 of the largest |v| (below 8) four times
     assert (o.float() - po.float()).abs().max() <= 4 * 2.0 ** -8 * 8
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_two_calls_at_once(kv8):
+    """On two streams, each with workspace and outputs of its own."""
+    many = [(300, [301 + i for i in range(40)])]
+    one, two = ((make8 if kv8 else make)(g, 1, 16, 2, d, 16, seed=3) for g, d in ((many, 64), ([(0, [4000, 17, 900])] * 9, 128)))
+    call = ops.decode_kv8_shared if kv8 else ops.decode_paged_shared
+    sides = ("q", "k", "v") + (("k_scale", "v_scale") if kv8 else ())
+    args = [[m[x].cuda() for x in sides] + [i32(m[x]) for x in ("table", "lens", "starts", "shared")] + [max(m["lens"])] for m in (one, two)]
+    plain = [call(*a) for a in args]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(10):
+        for i in range(2):
+            got[i].append(call(*args[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, plain[i][0]) and torch.equal(lse, plain[i][1])
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_pages_beyond_32_bits(kv8):
+    """The same pages at the far end of a pool of more than 4 GB a side give the same bits."""
+    m = (make8 if kv8 else make)([(150, [200, 151, 700]), (40, [60] * 20)], 1, 8, 1, 128, 64, seed=4, **({} if kv8 else dict(fill=0.0)))
+    call = ops.decode_kv8_shared if kv8 else ops.decode_paged_shared
+    sides = ("k", "v") + (("k_scale", "v_scale") if kv8 else ())
+    tail = [i32(m[x]) for x in ("lens", "starts", "shared")] + [700]
+    near = [m[x].cuda() for x in sides]
+    plain = call(m["q"].cuda(), *near, i32(m["table"]), *tail)
+    n = near[0].shape[0]
+    pool = (1 << 32) // (64 * 128) // near[0].element_size() * 2 + n
+    far = []
+    for x in near:
+        y = torch.empty((pool, *x.shape[1:]), dtype=x.dtype, device="cuda")
+        y[-n:] = x
+        far.append(y)
+    got = call(m["q"].cuda(), *far, i32(m["table"] + pool - n), *tail)
+    assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+    assert ops.device_error() == 0
