@@ -55,7 +55,6 @@
 
 #include "sampling.cuh"
 
-#include <atomic>
 #include <cmath>
 
 namespace fa {
@@ -334,7 +333,8 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   const int n_many = p.plan.head->shares[0];
   const bool many = (int)blockIdx.x < n_many;
   const bool few = NR > 0 && (!many || p.plan.head->shares[2] > 0);  // (behind the tiles there are the late shares alone)
-  // Registers go where a row's 128 scores are held: 56 x 4 warps + 224 x 8 is what 168 x 12 was,
+  // Registers go where a row's 128 scores are held: 56 x 4 warps + 224 x 8 is what 168 x 12 was
+  // (and is again, where all twelve attend for few rows); of 8-bit pages
   // (56 + 72) x 4 + 192 x 8, and then 56 x 4 + 152 x 12, what 128 x 16 was.  A CTA without tiles
   // goes to the latter at once, one with tiles behind a barrier: where the warps that convert
   // could grow before the softmax warps have, they would take what those wait for forever.
@@ -348,598 +348,598 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
     }
   };
   if (warp < 4) {
-  if (!ALL || many) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  if (!many) {
-  } else if (warp == 2) {
-    // ============================================================ walk over the share
-    Walk walk;
-    walk.start(p.plan.list[0], p.plan.head->count[0], deal_of(*p.plan.head, false), (int)blockIdx.x);
-    bool left = true;
-    for (int pieces = 0; left; ++pieces) {
-      Piece s = {};
-      int u;
-      bool later;
-      left = walk.next(p, false, u, s.t0, s.t1, later);
-      if (left) {  // (else t0 = t1: the end)
-        const SharedEntry& ent = walk.ent;
-        const int chunks = chunks_of(p, false, ent.ntok);
-        s.head = (int)((unsigned)u / (unsigned)chunks);
-        const int c = u - s.head * chunks;
-        s.tok0 = ent.tok0 + c * 2 * p.tile_tokens;
-        s.ntok = min(2 * p.tile_tokens, ent.ntok - c * 2 * p.tile_tokens);
-        s.lo = ent.lo, s.end = ent.end, s.all_lo = ent.all_lo, s.all_hi = ent.all_hi;
-        s.beg = ent.lo / p.box_rows * p.box_rows;
-        s.kind = ent.kind;
-        s.row = ent.row;
-        s.side = s.t0 == 0 && s.t1 == ent.tiles ? 0 : kSharedTile;
-        s.place = s.side == 0 ? 2 * (long long)ent.kind * p.B * p.Nq * p.Hq : cut_place(p, false, (int)blockIdx.x, later);
-      }
-      const int slot = pieces % kPieces;
-      if (pieces >= kPieces &&
-          !__all_sync(0xffffffffu, mbar_wait(BAR(PC_EMPTY + slot), (pieces / kPieces - 1) & 1, w, 70)))
-        break;
-      if (lane == 0) {
-        s_piece[slot] = s;
-        mbar_arrive(BAR(PC_FULL + slot));
-      }
-      __syncwarp();
-    }
-  } else if (warp == 0 || warp == 3) {
-    // ============================================================ loads of K, and of Q and V
-    const CUtensorMap* map = warp == 0 ? &tm_k : &tm_v;
-    if (lane == 0) {
-      tma_prefetch_desc(map);
-      if (warp == 3) tma_prefetch_desc(&tm_q);
-    }
-    const int boxes = kSharedTile / p.box_rows, shift = __ffs(p.box_rows) - 5;  // TMA boxes of a tile; 16-key groups of one, log2
-    bool ok = true, more = true;
-    Piece pc;
-    pc.t0 = pc.t1 = 0;
-    int t_next = 0, piece = 0;
-    struct Batch {  // up to four tiles of a piece, lane i owning 16 keys; their pages are read two batches ahead
-      int n, rows8, page, head, last;  // rows8: of the cache, in eights, less the page's; last: 16-key groups there are
-      int tok0, ntok;                  // a piece's first batch: its query tokens; else 0
-    };
-    auto fetch = [&](Batch& q) {
-      q.n = q.ntok = 0;
-      if (!more) return;
-      if (t_next == pc.t1) {
-        more = take(piece++, pc, 73) && pc.t0 < pc.t1;
-        t_next = pc.t0;
-        if (!more) return;
-        q.tok0 = pc.tok0, q.ntok = pc.ntok;
-      }
-      q.n = min(4, pc.t1 - t_next);
-      const int g0 = (pc.beg + t_next * kSharedTile) / 16, g = g0 + lane;
-      q.last = (pc.end + 15) / 16 - g0;
-      q.head = pc.head;
-      q.page = q.rows8 = 0;
-      t_next += q.n;
-      if (lane < 8 * q.n && lane < q.last) {
-        const int blk = (int)((unsigned)(g * 16) / (unsigned)p.page_size);
-        q.rows8 = 2 * g - blk * (p.page_size / 8);
-        q.page = p.block_table[(size_t)pc.row * p.max_blocks + blk];
-      }
-    };
-    int place = warp == 0 ? 0 : 2, qt = 0;  // ring places, as k_place and v_place count; tiles of Q so far
-    Batch now, then;
-    fetch(now);
-    fetch(then);
-    while (ok && now.n > 0) {
-      if (now.page < 0 || now.page >= p.num_pages) {  // report, and read a valid page instead
-        atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
-        now.page = 0;
-      }
-      if (warp == 3) {  // Q, before the first values (which are needed later)
-        for (int x = 0; x < now.ntok && ok; x += p.tile_tokens, ++qt) {
-          const int slot = qt & 1;
-          if (qt >= 2) ok = __all_sync(0xffffffffu, mbar_wait(BAR(Q_EMPTY + slot), (qt / 2 - 1) & 1, w, 72));
-          if (ok && elect_one()) {
-            mbar_arrive_expect_tx(BAR(Q_FULL + slot), (uint32_t)(p.tile_tokens * p.heads * D * 2));
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-              tma_load_3d(q_s + slot * TILE + c * CHUNK, &tm_q, BAR(Q_FULL + slot), c * 64, now.head * p.heads, now.tok0 + x);
-          }
-          __syncwarp();
+    if (!ALL || many) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (!many) {
+    } else if (warp == 2) {
+      // ============================================================ walk over the share
+      Walk walk;
+      walk.start(p.plan.list[0], p.plan.head->count[0], deal_of(*p.plan.head, false), (int)blockIdx.x);
+      bool left = true;
+      for (int pieces = 0; left; ++pieces) {
+        Piece s = {};
+        int u;
+        bool later;
+        left = walk.next(p, false, u, s.t0, s.t1, later);
+        if (left) {  // (else t0 = t1: the end)
+          const SharedEntry& ent = walk.ent;
+          const int chunks = chunks_of(p, false, ent.ntok);
+          s.head = (int)((unsigned)u / (unsigned)chunks);
+          const int c = u - s.head * chunks;
+          s.tok0 = ent.tok0 + c * 2 * p.tile_tokens;
+          s.ntok = min(2 * p.tile_tokens, ent.ntok - c * 2 * p.tile_tokens);
+          s.lo = ent.lo, s.end = ent.end, s.all_lo = ent.all_lo, s.all_hi = ent.all_hi;
+          s.beg = ent.lo / p.box_rows * p.box_rows;
+          s.kind = ent.kind;
+          s.row = ent.row;
+          s.side = s.t0 == 0 && s.t1 == ent.tiles ? 0 : kSharedTile;
+          s.place = s.side == 0 ? 2 * (long long)ent.kind * p.B * p.Nq * p.Hq : cut_place(p, false, (int)blockIdx.x, later);
         }
-        if (!ok) break;
-      }
-      const int at8 = KV8 ? now.rows8 * 8 : now.page * (p.page_size / 8) + now.rows8;  // row of the page, or eight of all pages'
-      const int plane = now.page * p.Hkv + now.head;
-      float k_scale = 0.f, v_scale = 0.f;
-      if constexpr (KV8) {
-        if (warp == 0 && lane < 8 * now.n && lane < now.last) k_scale = p.k_scale[plane], v_scale = p.v_scale[plane];
-      }
-      constexpr int FULL = KV8 ? (int)RAW_FULL : (int)KV_FULL;
-      for (int i = 0; i < now.n; ++i) {
-        const int slot = place % NS, here = min(boxes, (max(now.last - 8 * i, 0) + (1 << shift) - 1) >> shift);
-        if (place >= NS) ok = __all_sync(0xffffffffu, mbar_wait(BAR(KV_EMPTY + slot), (place / NS - 1) & 1, w, 74));
-        if (!ok) break;
-        if (KV8 && warp == 0) {  // scales, which the softmax warps read when the keys' scores are there
-          const int sc_slot = (place + 1) / 2 % (SCALES + !SCALES);
-          if (lane >> 3 == i) {
-            float* sc = s_scale + sc_slot * 24 + (lane & 7);
-            // (a value scale that is no number is a NaN)
-            sc[0] = k_scale, sc[8] = fabsf(v_scale) < INFINITY ? v_scale : __uint_as_float(0x7fffffffu), sc[16] = scale_log2(v_scale);
-          }
-          __syncwarp();
+        const int slot = pieces % kPieces;
+        if (pieces >= kPieces &&
+            !__all_sync(0xffffffffu, mbar_wait(BAR(PC_EMPTY + slot), (pieces / kPieces - 1) & 1, w, 70)))
+          break;
+        if (lane == 0) {
+          s_piece[slot] = s;
+          mbar_arrive(BAR(PC_FULL + slot));
         }
-        if (elect_one()) mbar_arrive_expect_tx(BAR(FULL + slot), (uint32_t)(here * p.box_rows * D * (KV8 ? 1 : 2)));
         __syncwarp();
-        const uint32_t dst = kv_s + slot * TILE + (KV8 ? L::kRawTile : 0), bar = BAR(FULL + slot);
-        for (int x = 0; x < here; ++x) {  // (one lane issues, with the same operands in all)
-          const int row = __shfl_sync(0xffffffffu, at8, 8 * i + (x << shift));
-          if constexpr (KV8) {
-            const int pl = __shfl_sync(0xffffffffu, plane, 8 * i + (x << shift));
-            if (elect_one()) tma_load_3d(dst + x * p.box_rows * D, map, bar, 0, row, pl);
-          } else {
-            if (elect_one()) tma_load_5d(dst + x * p.box_rows * D * 2, map, bar, 0, 0, 0, row, now.head);
-          }
-        }
-        place += place == 0 ? 1 : 2;
       }
-      now = then;
+    } else if (warp == 0 || warp == 3) {
+      // ============================================================ loads of K, and of Q and V
+      const CUtensorMap* map = warp == 0 ? &tm_k : &tm_v;
+      if (lane == 0) {
+        tma_prefetch_desc(map);
+        if (warp == 3) tma_prefetch_desc(&tm_q);
+      }
+      const int boxes = kSharedTile / p.box_rows, shift = __ffs(p.box_rows) - 5;  // TMA boxes of a tile; 16-key groups of one, log2
+      bool ok = true, more = true;
+      Piece pc;
+      pc.t0 = pc.t1 = 0;
+      int t_next = 0, piece = 0;
+      struct Batch {  // up to four tiles of a piece, lane i owning 16 keys; their pages are read two batches ahead
+        int n, rows8, page, head, last;  // rows8: of the cache, in eights, less the page's; last: 16-key groups there are
+        int tok0, ntok;                  // a piece's first batch: its query tokens; else 0
+      };
+      auto fetch = [&](Batch& q) {
+        q.n = q.ntok = 0;
+        if (!more) return;
+        if (t_next == pc.t1) {
+          more = take(piece++, pc, 73) && pc.t0 < pc.t1;
+          t_next = pc.t0;
+          if (!more) return;
+          q.tok0 = pc.tok0, q.ntok = pc.ntok;
+        }
+        q.n = min(4, pc.t1 - t_next);
+        const int g0 = (pc.beg + t_next * kSharedTile) / 16, g = g0 + lane;
+        q.last = (pc.end + 15) / 16 - g0;
+        q.head = pc.head;
+        q.page = q.rows8 = 0;
+        t_next += q.n;
+        if (lane < 8 * q.n && lane < q.last) {
+          const int blk = (int)((unsigned)(g * 16) / (unsigned)p.page_size);
+          q.rows8 = 2 * g - blk * (p.page_size / 8);
+          q.page = p.block_table[(size_t)pc.row * p.max_blocks + blk];
+        }
+      };
+      int place = warp == 0 ? 0 : 2, qt = 0;  // ring places, as k_place and v_place count; tiles of Q so far
+      Batch now, then;
+      fetch(now);
       fetch(then);
-    }
-    if (!ok) {  // let copies already in flight land before the CTA's shared memory goes away
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 200000ull) {
-      }
-    }
-  } else if (warp == 1) {
-    // ============================================================ products
-    // Job n is a tile of rows times a tile of keys; jobs take S, P and O of tile n & 1.
-    // S of job n is issued before the product of job n - 1's P, which waits for its softmax.
-    constexpr uint32_t IDESC_S = KV8 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
-    constexpr uint32_t IDESC_O = KV8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
-    constexpr int QUERIES = KV8 ? (int)Q_READY : (int)Q_FULL;
-    struct Job {
-      uint32_t vslot, vphase;
-      bool on, first, last, frees;  // first, last of its tile's run in the piece; the last to read its values
-    } before{};
-    uint32_t n = 0, qt = 0, runs[2] = {0, 0}, ps[2] = {0, 0};
-    uint32_t sk = 0, pk = 0, sv = 2, pv = 0;  // ring slots and phases of the tile's K and V
-    bool ok = true, start = true;
-    auto advance = [](uint32_t& slot, uint32_t& phase, uint32_t by) {
-      slot += by;
-      if (slot >= (uint32_t)NS) slot -= NS, phase ^= 1u;
-    };
-    auto there = [&](uint32_t bar, uint32_t phase) { return (bool)__all_sync(0xffffffffu, mbar_test(bar, phase)); };
-    auto wait = [&](uint32_t bar, uint32_t phase, unsigned site) {
-      return there(bar, phase) || __all_sync(0xffffffffu, mbar_wait(bar, phase, w, site));
-    };
-    auto product = [&](const Job& j, uint32_t t) {  // O_t (+)= P V
-      if (!wait(BAR(KV_FULL) + 8 * j.vslot, j.vphase, 75)) return false;
-      if (j.first && runs[t] > 0 && !wait(BAR(O_EMPTY) + 8 * t, (runs[t] - 1) & 1, 76)) return false;  // the run before has been read
-      if (!wait(BAR(P_FULL) + 16 * t, ps[t] & 1, 77)) return false;
-      tc_fence_after();
-      const uint64_t vd = smem_desc_sw128(kv_s + j.vslot * TILE, 1024, CH * 1024);
-      const uint32_t dst = tmem + 256u + (t ? (uint32_t)D : 0u), pa = tmem + (t ? 128u : 0u);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_ts_w(dst, pa + kk * 8, desc_add(vd, kk * CH * 2048), IDESC_O, (!j.first || kk > 0) ? 1u : 0u);
-      if (!wait(BAR(P_FULL) + 16 * t + 8, ps[t] & 1, 78)) return false;
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 4; kk < 8; ++kk) mma_ts_w(dst, pa + kk * 8, desc_add(vd, kk * CH * 2048), IDESC_O, 1u);
-      ++ps[t];
-      if (j.first) ++runs[t];
-      if (j.frees) mma_commit_w(BAR(KV_EMPTY) + 8 * j.vslot);
-      if (j.last) mma_commit_w(BAR(O_FINAL) + 8 * t);
-      return true;
-    };
-    Piece s;
-    for (int piece = 0; ok && take(piece, s, 79) && s.t0 < s.t1; ++piece) {
-      const int tiles = s.t1 - s.t0, subs = s.ntok > p.tile_tokens ? 2 : 1;
-      const int alone = 3 - subs;  // jobs between a tile's jobs on the same S: key tiles in turn, or every one
-      for (int x = 0; x < tiles && ok; ++x) {
-        bool here = there(BAR(KV_FULL) + 8 * sk, pk);
-        for (int sub = 0; sub < subs; ++sub, ++n) {
-          const uint32_t t = n & 1, q = qt + sub, qs = q & 1;
-          if (x == 0 && here) here = there(BAR(QUERIES) + 8 * qs, q >> 1 & 1);
-          if (!here) {
-            // Inputs that have not come yet: the last job's product need not wait for them.  (Not
-            // for the second tile of rows: its values' place in the ring may be these keys'.)
-            if (sub == 0) {
-              if (before.on && !(ok = product(before, t ^ 1))) break;
-              before.on = false;
-            }
-            ok = wait(BAR(KV_FULL) + 8 * sk, pk, 81);
-            if (ok && x == 0) ok = wait(BAR(QUERIES) + 8 * qs, q >> 1 & 1, 80);
-            if (!ok) break;
-            here = true;
-          }
-          tc_fence_after();
-          const uint64_t qd = smem_desc_sw128(q_s + qs * TILE, 16, 1024), kd = smem_desc_sw128(kv_s + sk * TILE, 16, CH * 1024);
-          const uint32_t dst = tmem + (t ? 128u : 0u);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = (kk % 4) * 32;
-            mma_ss_w(dst, desc_add(qd, (kk / 4) * CHUNK + o), desc_add(kd, (kk / 4) * 1024 + o), IDESC_S, kk > 0);
-          }
-          mma_commit_w(BAR(S_FULL) + 8 * t);
-          if (x == tiles - 1) mma_commit_w(BAR(Q_EMPTY) + 8 * qs);
-          if (sub == subs - 1) mma_commit_w(BAR(KV_EMPTY) + 8 * sk);
-          if (before.on && !(ok = product(before, t ^ 1))) break;
-          before = {sv, pv, true, x < alone, x >= tiles - alone, sub == subs - 1};
+      while (ok && now.n > 0) {
+        if (now.page < 0 || now.page >= p.num_pages) {  // report, and read a valid page instead
+          atomicCAS(p.err, 0u, FA_DEVERR_BAD_PAGE);
+          now.page = 0;
         }
-        advance(sk, pk, start ? 1u : 2u);  // (as k_place and v_place count)
-        advance(sv, pv, 2u);
-        start = false;
+        if (warp == 3) {  // Q, before the first values (which are needed later)
+          for (int x = 0; x < now.ntok && ok; x += p.tile_tokens, ++qt) {
+            const int slot = qt & 1;
+            if (qt >= 2) ok = __all_sync(0xffffffffu, mbar_wait(BAR(Q_EMPTY + slot), (qt / 2 - 1) & 1, w, 72));
+            if (ok && elect_one()) {
+              mbar_arrive_expect_tx(BAR(Q_FULL + slot), (uint32_t)(p.tile_tokens * p.heads * D * 2));
+#pragma unroll
+              for (int c = 0; c < CH; ++c)
+                tma_load_3d(q_s + slot * TILE + c * CHUNK, &tm_q, BAR(Q_FULL + slot), c * 64, now.head * p.heads, now.tok0 + x);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
+        const int at8 = KV8 ? now.rows8 * 8 : now.page * (p.page_size / 8) + now.rows8;  // row of the page, or eight of all pages'
+        const int plane = now.page * p.Hkv + now.head;
+        float k_scale = 0.f, v_scale = 0.f;
+        if constexpr (KV8) {
+          if (warp == 0 && lane < 8 * now.n && lane < now.last) k_scale = p.k_scale[plane], v_scale = p.v_scale[plane];
+        }
+        constexpr int FULL = KV8 ? (int)RAW_FULL : (int)KV_FULL;
+        for (int i = 0; i < now.n; ++i) {
+          const int slot = place % NS, here = min(boxes, (max(now.last - 8 * i, 0) + (1 << shift) - 1) >> shift);
+          if (place >= NS) ok = __all_sync(0xffffffffu, mbar_wait(BAR(KV_EMPTY + slot), (place / NS - 1) & 1, w, 74));
+          if (!ok) break;
+          if (KV8 && warp == 0) {  // scales, which the softmax warps read when the keys' scores are there
+            const int sc_slot = (place + 1) / 2 % (SCALES + !SCALES);
+            if (lane >> 3 == i) {
+              float* sc = s_scale + sc_slot * 24 + (lane & 7);
+              // (a value scale that is no number is a NaN)
+              sc[0] = k_scale, sc[8] = fabsf(v_scale) < INFINITY ? v_scale : __uint_as_float(0x7fffffffu), sc[16] = scale_log2(v_scale);
+            }
+            __syncwarp();
+          }
+          if (elect_one()) mbar_arrive_expect_tx(BAR(FULL + slot), (uint32_t)(here * p.box_rows * D * (KV8 ? 1 : 2)));
+          __syncwarp();
+          const uint32_t dst = kv_s + slot * TILE + (KV8 ? L::kRawTile : 0), bar = BAR(FULL + slot);
+          for (int x = 0; x < here; ++x) {  // (one lane issues, with the same operands in all)
+            const int row = __shfl_sync(0xffffffffu, at8, 8 * i + (x << shift));
+            if constexpr (KV8) {
+              const int pl = __shfl_sync(0xffffffffu, plane, 8 * i + (x << shift));
+              if (elect_one()) tma_load_3d(dst + x * p.box_rows * D, map, bar, 0, row, pl);
+            } else {
+              if (elect_one()) tma_load_5d(dst + x * p.box_rows * D * 2, map, bar, 0, 0, 0, row, now.head);
+            }
+          }
+          place += place == 0 ? 1 : 2;
+        }
+        now = then;
+        fetch(then);
       }
-      qt += subs;
+      if (!ok) {  // let copies already in flight land before the CTA's shared memory goes away
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    } else if (warp == 1) {
+      // ============================================================ products
+      // Job n is a tile of rows times a tile of keys; jobs take S, P and O of tile n & 1.
+      // S of job n is issued before the product of job n - 1's P, which waits for its softmax.
+      constexpr uint32_t IDESC_S = KV8 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
+      constexpr uint32_t IDESC_O = KV8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
+      constexpr int QUERIES = KV8 ? (int)Q_READY : (int)Q_FULL;
+      struct Job {
+        uint32_t vslot, vphase;
+        bool on, first, last, frees;  // first, last of its tile's run in the piece; the last to read its values
+      } before{};
+      uint32_t n = 0, qt = 0, runs[2] = {0, 0}, ps[2] = {0, 0};
+      uint32_t sk = 0, pk = 0, sv = 2, pv = 0;  // ring slots and phases of the tile's K and V
+      bool ok = true, start = true;
+      auto advance = [](uint32_t& slot, uint32_t& phase, uint32_t by) {
+        slot += by;
+        if (slot >= (uint32_t)NS) slot -= NS, phase ^= 1u;
+      };
+      auto there = [&](uint32_t bar, uint32_t phase) { return (bool)__all_sync(0xffffffffu, mbar_test(bar, phase)); };
+      auto wait = [&](uint32_t bar, uint32_t phase, unsigned site) {
+        return there(bar, phase) || __all_sync(0xffffffffu, mbar_wait(bar, phase, w, site));
+      };
+      auto product = [&](const Job& j, uint32_t t) {  // O_t (+)= P V
+        if (!wait(BAR(KV_FULL) + 8 * j.vslot, j.vphase, 75)) return false;
+        if (j.first && runs[t] > 0 && !wait(BAR(O_EMPTY) + 8 * t, (runs[t] - 1) & 1, 76)) return false;  // the run before has been read
+        if (!wait(BAR(P_FULL) + 16 * t, ps[t] & 1, 77)) return false;
+        tc_fence_after();
+        const uint64_t vd = smem_desc_sw128(kv_s + j.vslot * TILE, 1024, CH * 1024);
+        const uint32_t dst = tmem + 256u + (t ? (uint32_t)D : 0u), pa = tmem + (t ? 128u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_w(dst, pa + kk * 8, desc_add(vd, kk * CH * 2048), IDESC_O, (!j.first || kk > 0) ? 1u : 0u);
+        if (!wait(BAR(P_FULL) + 16 * t + 8, ps[t] & 1, 78)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 4; kk < 8; ++kk) mma_ts_w(dst, pa + kk * 8, desc_add(vd, kk * CH * 2048), IDESC_O, 1u);
+        ++ps[t];
+        if (j.first) ++runs[t];
+        if (j.frees) mma_commit_w(BAR(KV_EMPTY) + 8 * j.vslot);
+        if (j.last) mma_commit_w(BAR(O_FINAL) + 8 * t);
+        return true;
+      };
+      Piece s;
+      for (int piece = 0; ok && take(piece, s, 79) && s.t0 < s.t1; ++piece) {
+        const int tiles = s.t1 - s.t0, subs = s.ntok > p.tile_tokens ? 2 : 1;
+        const int alone = 3 - subs;  // jobs between a tile's jobs on the same S: key tiles in turn, or every one
+        for (int x = 0; x < tiles && ok; ++x) {
+          bool here = there(BAR(KV_FULL) + 8 * sk, pk);
+          for (int sub = 0; sub < subs; ++sub, ++n) {
+            const uint32_t t = n & 1, q = qt + sub, qs = q & 1;
+            if (x == 0 && here) here = there(BAR(QUERIES) + 8 * qs, q >> 1 & 1);
+            if (!here) {
+              // Inputs that have not come yet: the last job's product need not wait for them.  (Not
+              // for the second tile of rows: its values' place in the ring may be these keys'.)
+              if (sub == 0) {
+                if (before.on && !(ok = product(before, t ^ 1))) break;
+                before.on = false;
+              }
+              ok = wait(BAR(KV_FULL) + 8 * sk, pk, 81);
+              if (ok && x == 0) ok = wait(BAR(QUERIES) + 8 * qs, q >> 1 & 1, 80);
+              if (!ok) break;
+              here = true;
+            }
+            tc_fence_after();
+            const uint64_t qd = smem_desc_sw128(q_s + qs * TILE, 16, 1024), kd = smem_desc_sw128(kv_s + sk * TILE, 16, CH * 1024);
+            const uint32_t dst = tmem + (t ? 128u : 0u);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = (kk % 4) * 32;
+              mma_ss_w(dst, desc_add(qd, (kk / 4) * CHUNK + o), desc_add(kd, (kk / 4) * 1024 + o), IDESC_S, kk > 0);
+            }
+            mma_commit_w(BAR(S_FULL) + 8 * t);
+            if (x == tiles - 1) mma_commit_w(BAR(Q_EMPTY) + 8 * qs);
+            if (sub == subs - 1) mma_commit_w(BAR(KV_EMPTY) + 8 * sk);
+            if (before.on && !(ok = product(before, t ^ 1))) break;
+            before = {sv, pv, true, x < alone, x >= tiles - alone, sub == subs - 1};
+          }
+          advance(sk, pk, start ? 1u : 2u);  // (as k_place and v_place count)
+          advance(sv, pv, 2u);
+          start = false;
+        }
+        qt += subs;
+      }
+      if (ok && before.on) ok = product(before, (n - 1) & 1);
+      // Drain: every product and every earlier commit's arrival has landed
+      // before TMEM is released and the CTA's shared memory goes away.
+      mma_commit_w(BAR(DRAIN));
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(BAR(DRAIN), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
+      }
     }
-    if (ok && before.on) ok = product(before, (n - 1) & 1);
-    // Drain: every product and every earlier commit's arrival has landed
-    // before TMEM is released and the CTA's shared memory goes away.
-    mma_commit_w(BAR(DRAIN));
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(BAR(DRAIN), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
-    }
-  }
-  __syncwarp();
-  if (many) __syncthreads();  // shared memory changes hands, and registers
-  if (ALL) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    __syncwarp();
+    if (many) __syncthreads();  // shared memory changes hands, and registers
+    if (ALL) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
   } else {
     if (KV8 && warp >= 12) {
       if constexpr (KV8) {
         if (many) {
           asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    // ============================================================ codes to f16
-    // A tile of codes as TMA lays it, 16-byte chunks swizzled over the banks, becomes one of
-    // f16 as the products take it, in its place: the codes are its second half, and those
-    // of the last 64 keys wait in registers until all have been read.  (With the codes in a ring
-    // of their own there was room for three tiles, and products waited 1000 cycles each.)
-    const int me = threadIdx.x & 127;
-    auto convert = [&](int place) {
-      const int slot = place % NS;
-      const bool ok = mbar_wait(BAR(RAW_FULL + slot), place / NS & 1, w, 91);
-      uint8_t* tile = sb + L::kKVOff + slot * TILE;
-      const uint4* raw = reinterpret_cast<const uint4*>(tile + L::kRawTile);
-      constexpr int N = D / 32;  // chunks of a thread in half a tile
-      uint4 x[N], late[N];
-      auto put = [&](const uint4& codes, int at) {
-        const int key = at / (D / 16), c = (at % (D / 16)) ^ (D == 128 ? key & 7 : key >> 1 & 3);
-        uint4 y[2];
-        codes_f16(codes.x, y[0].x, y[0].y), codes_f16(codes.y, y[0].z, y[0].w);
-        codes_f16(codes.z, y[1].x, y[1].y), codes_f16(codes.w, y[1].z, y[1].w);
-        uint8_t* row = tile + (key >> 3) * CH * 1024 + (c >> 2) * 1024 + (key & 7) * 128;
-        const int odd = c >> 2 & 1;  // (d = 128: half the lanes store their second half first, to other banks)
-        *reinterpret_cast<uint4*>(row + ((((2 * c + odd) & 7) ^ (key & 7)) << 4)) = odd ? y[1] : y[0];
-        *reinterpret_cast<uint4*>(row + ((((2 * c + 1 - odd) & 7) ^ (key & 7)) << 4)) = odd ? y[0] : y[1];
-      };
+          // ============================================================ codes to f16
+          // A tile of codes as TMA lays it, 16-byte chunks swizzled over the banks, becomes one of
+          // f16 as the products take it, in its place: the codes are its second half, and those
+          // of the last 64 keys wait in registers until all have been read.  (With the codes in a ring
+          // of their own there was room for three tiles, and products waited 1000 cycles each.)
+          const int me = threadIdx.x & 127;
+          auto convert = [&](int place) {
+            const int slot = place % NS;
+            const bool ok = mbar_wait(BAR(RAW_FULL + slot), place / NS & 1, w, 91);
+            uint8_t* tile = sb + L::kKVOff + slot * TILE;
+            const uint4* raw = reinterpret_cast<const uint4*>(tile + L::kRawTile);
+            constexpr int N = D / 32;  // chunks of a thread in half a tile
+            uint4 x[N], late[N];
+            auto put = [&](const uint4& codes, int at) {
+              const int key = at / (D / 16), c = (at % (D / 16)) ^ (D == 128 ? key & 7 : key >> 1 & 3);
+              uint4 y[2];
+              codes_f16(codes.x, y[0].x, y[0].y), codes_f16(codes.y, y[0].z, y[0].w);
+              codes_f16(codes.z, y[1].x, y[1].y), codes_f16(codes.w, y[1].z, y[1].w);
+              uint8_t* row = tile + (key >> 3) * CH * 1024 + (c >> 2) * 1024 + (key & 7) * 128;
+              const int odd = c >> 2 & 1;  // (d = 128: half the lanes store their second half first, to other banks)
+              *reinterpret_cast<uint4*>(row + ((((2 * c + odd) & 7) ^ (key & 7)) << 4)) = odd ? y[1] : y[0];
+              *reinterpret_cast<uint4*>(row + ((((2 * c + 1 - odd) & 7) ^ (key & 7)) << 4)) = odd ? y[0] : y[1];
+            };
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = raw[i * 128 + me];
+            for (int i = 0; i < N; ++i) x[i] = raw[i * 128 + me];
 #pragma unroll
-      for (int i = 0; i < N; ++i) put(x[i], i * 128 + me);
+            for (int i = 0; i < N; ++i) put(x[i], i * 128 + me);
 #pragma unroll
-      for (int i = 0; i < N; ++i) late[i] = raw[(N + i) * 128 + me];
-      // (where a warp's wait has run out all four stop here: none waits for it again)
-      if (!all_of_128(1, ok)) return false;
+            for (int i = 0; i < N; ++i) late[i] = raw[(N + i) * 128 + me];
+            // (where a warp's wait has run out all four stop here: none waits for it again)
+            if (!all_of_128(1, ok)) return false;
 #pragma unroll
-      for (int i = 0; i < N; ++i) put(late[i], (N + i) * 128 + me);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(KV_FULL + slot));
-      return true;
-    };
-    bool ok = true;
-    int it = 0;
-    Piece s;
-    for (int piece = 0; ok && take(piece, s, 93) && s.t0 < s.t1; ++piece)
-      for (int x = s.t0; x < s.t1 && ok; ++x, ++it) ok = convert(k_place(it)) && (it == 0 || convert(v_place(it - 1)));
-    if (ok && it > 0) convert(v_place(it - 1));
+            for (int i = 0; i < N; ++i) put(late[i], (N + i) * 128 + me);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(KV_FULL + slot));
+            return true;
+          };
+          bool ok = true;
+          int it = 0;
+          Piece s;
+          for (int piece = 0; ok && take(piece, s, 93) && s.t0 < s.t1; ++piece)
+            for (int x = s.t0; x < s.t1 && ok; ++x, ++it) ok = convert(k_place(it)) && (it == 0 || convert(v_place(it - 1)));
+          if (ok && it > 0) convert(v_place(it - 1));
         }
       }
       __syncwarp();
       if (many) __syncthreads();
       asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     } else {
-    if (!KV8 && (!ALL || many)) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    else if (KV8 && many) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    if (many) {
-    // ============================================================ softmax
-    const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + lane_off + (t ? 128u : 0u), tO = tmem + lane_off + 256u + (t ? (uint32_t)D : 0u);
-    float sl2 = p.scale_log2;
-    const float tau = KV8 ? fminf(p.tau, kMaxTau) : p.tau;
-    int qt = 0;  // tiles of Q so far
-    const int my_tok = r / p.heads, my_head = r - my_tok * p.heads;
-    const long long rows = (long long)p.B * p.Nq * p.Hq;
-    bool ok = true;
-    int n0 = 0, it0 = 0, phase = 0, runs = 0;  // jobs and key tiles before the piece; S phases and runs of this tile
-    uint32_t xg = 0, xb = 0, flip = 0;
-    Piece s;
-    for (int piece = 0; ok && take(piece, s, 82) && s.t0 < s.t1; ++piece) {
-      const int tiles = s.t1 - s.t0;
-      const bool pair = s.ntok > p.tile_tokens;
-      const int side = (t ^ n0) & 1;  // pair: tile of rows; else: which of the two runs of key tiles
-      const int tok = s.tok0 + (pair ? side * p.tile_tokens : 0) + my_tok;
-      const bool valid = my_tok < p.tile_tokens && tok < s.tok0 + s.ntok;
-      // the keys this row sees: [key_lo, key_hi)
-      int key_lo = 0, key_hi = 0;
-      if (valid) {
-        const int b = p.Nq == 1 ? tok : (int)((unsigned)tok / (unsigned)p.Nq);
-        const int len = s.kind == 1 ? s.end : min(max(p.seq_lens[b], 0), p.max_len), pos = len - p.Nq + tok - b * p.Nq;
-        key_lo = p.win_left >= 0 ? max(s.lo, pos - p.win_left) : s.lo;
-        key_hi = min(s.end, pos + 1);
-      }
-      const bool live = __any_sync(0xffffffffu, valid);  // some row of the warp is there
-      if constexpr (KV8) {  // queries to f16, a row times its own scale
-        const int q = qt + (pair ? side : 0), slot = q & 1;
-        ok = mbar_wait(BAR(Q_FULL + slot), q >> 1 & 1, w, 95);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        uint8_t* row = sb + L::kQOff + slot * TILE + r * 128;
-        uint32_t most = 0;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          most = largest_bf16(most, *reinterpret_cast<const uint4*>(row + (c >> 3) * CHUNK + (((c & 7) ^ (r & 7)) << 4)));
-        const RowScale rs(max(most >> 16, most & 0xffffu));
-        sl2 = p.scale_log2 * rs.back;
-        if (!pair) {  // each group converts half, when both have seen it
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(XB + 2));
-          ok = mbar_wait(BAR(XB + 2), xb++ & 1, w, 96);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
+      if (!KV8 && (!ALL || many)) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+      else if (KV8 && many) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+      if (many) {
+        // ============================================================ softmax
+        const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + lane_off + (t ? 128u : 0u), tO = tmem + lane_off + 256u + (t ? (uint32_t)D : 0u);
+        float sl2 = p.scale_log2;
+        const float tau = KV8 ? fminf(p.tau, kMaxTau) : p.tau;
+        int qt = 0;  // tiles of Q so far
+        const int my_tok = r / p.heads, my_head = r - my_tok * p.heads;
+        const long long rows = (long long)p.B * p.Nq * p.Hq;
+        bool ok = true;
+        int n0 = 0, it0 = 0, phase = 0, runs = 0;  // jobs and key tiles before the piece; S phases and runs of this tile
+        uint32_t xg = 0, xb = 0, flip = 0;
+        Piece s;
+        for (int piece = 0; ok && take(piece, s, 82) && s.t0 < s.t1; ++piece) {
+          const int tiles = s.t1 - s.t0;
+          const bool pair = s.ntok > p.tile_tokens;
+          const int side = (t ^ n0) & 1;  // pair: tile of rows; else: which of the two runs of key tiles
+          const int tok = s.tok0 + (pair ? side * p.tile_tokens : 0) + my_tok;
+          const bool valid = my_tok < p.tile_tokens && tok < s.tok0 + s.ntok;
+          // the keys this row sees: [key_lo, key_hi)
+          int key_lo = 0, key_hi = 0;
+          if (valid) {
+            const int b = p.Nq == 1 ? tok : (int)((unsigned)tok / (unsigned)p.Nq);
+            const int len = s.kind == 1 ? s.end : min(max(p.seq_lens[b], 0), p.max_len), pos = len - p.Nq + tok - b * p.Nq;
+            key_lo = p.win_left >= 0 ? max(s.lo, pos - p.win_left) : s.lo;
+            key_hi = min(s.end, pos + 1);
           }
-        }
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4* at = reinterpret_cast<uint4*>(row + (c >> 3) * CHUNK + (((c & 7) ^ (r & 7)) << 4));
-          if (pair || c / (D / 16) == side) *at = bf16_f16(*at, rs.to);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(BAR(Q_READY + slot));
-          if (pair) mbar_arrive(BAR(Q_READY + slot));
-        }
-        qt += pair ? 2 : 1;
-      }
-      float m_ref = -INFINITY, l = 0.f;
-      bool poison = false;
-      const int x_step = pair ? 1 : 2, x_first = pair ? 0 : side;
-      for (int x = x_first; x < tiles; x += x_step, ++phase) {
-        const int j0 = s.beg + (s.t0 + x) * kSharedTile;
-        ok = mbar_wait(BAR(S_FULL + t), phase & 1, w, 83);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float* sc = s_scale + (it0 + x) % (SCALES + !SCALES) * 24;
-        const bool inside = j0 >= s.all_lo && j0 + kSharedTile <= s.all_hi;  // every row sees every key
-        if (!inside) {
-          // Some rows do not see some keys of the tile, and 0 times a NaN or an infinity
-          // is not 0.  What no row sees (it may be anything) counts as zero; a value row
-          // that some see, and that holds one, counts as zero too, and its rows get a NaN.
-          const int uv = v_place(it0 + x), vslot = uv % NS;
-          ok = mbar_wait(BAR(KV_FULL + vslot), uv / NS & 1, w, 84);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          const int key = j0 + r;
-          const bool out = key < s.lo || key >= s.end;
-          uint4* row = reinterpret_cast<uint4*>(sb + L::kKVOff + vslot * TILE + (r >> 3) * CH * 1024 + (r & 7) * 128);
-          // (a value scale that is no number makes all its page's values such)
-          bool odd = KV8 && !out && !(fabsf(sc[8 + (r >> 4)]) < INFINITY);
-          if (KV8 || max(j0, s.lo) < s.all_lo || min(j0 + kSharedTile, s.end) > s.all_hi) {
-            if (!out && (key < s.all_lo || key >= s.all_hi)) {
-              uint32_t bad = 0;
-#pragma unroll 1
-              for (int i = 0; i < 8 * CH; ++i) {
-                const uint4 v = row[(i >> 3) * 64 + (i + lane & 7)];  // (other banks for each lane)
-                constexpr uint32_t E = KV8 ? 0x7c007c00u : 0x7f807f80u;
-                bad |= __vcmpeq2(v.x & E, E) | __vcmpeq2(v.y & E, E) | __vcmpeq2(v.z & E, E) | __vcmpeq2(v.w & E, E);
-              }
-              odd |= bad != 0;
-            }
-            const uint32_t votes = __ballot_sync(0xffffffffu, odd);
-            uint32_t* slot = s_bad + 8 * t + 4 * (flip++ & 1);
-            if (lane == 0) {
-              slot[quarter] = votes;
-              mbar_arrive(pair ? BAR(XB + 2) : BAR(XB + t));
-            }
-            // (pairs: both tiles' warps have read the values before either clears them)
-            ok = pair ? mbar_wait(BAR(XB + 2), xb++ & 1, w, 85) : mbar_wait(BAR(XB + t), xg++ & 1, w, 86);
+          const bool live = __any_sync(0xffffffffu, valid);  // some row of the warp is there
+          if constexpr (KV8) {  // queries to f16, a row times its own scale
+            const int q = qt + (pair ? side : 0), slot = q & 1;
+            ok = mbar_wait(BAR(Q_FULL + slot), q >> 1 & 1, w, 95);
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
               break;
             }
+            uint8_t* row = sb + L::kQOff + slot * TILE + r * 128;
+            uint32_t most = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int a = min(max(key_lo - j0 - 32 * i, 0), 32), z = min(max(key_hi - j0 - 32 * i, 0), 32);
-              const uint32_t sees = z > a ? (0xffffffffu >> (32 - (z - a))) << a : 0u;
-              poison |= (slot[i] & sees) != 0;
+            for (int c = 0; c < D / 8; ++c)
+              most = largest_bf16(most, *reinterpret_cast<const uint4*>(row + (c >> 3) * CHUNK + (((c & 7) ^ (r & 7)) << 4)));
+            const RowScale rs(max(most >> 16, most & 0xffffu));
+            sl2 = p.scale_log2 * rs.back;
+            if (!pair) {  // each group converts half, when both have seen it
+              __syncwarp();
+              if (lane == 0) mbar_arrive(BAR(XB + 2));
+              ok = mbar_wait(BAR(XB + 2), xb++ & 1, w, 96);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
             }
-          }
-          if (side == 0 || !pair) {  // (the other tile's product comes behind this one's)
-            if (out || odd) {
 #pragma unroll
-              for (int i = 0; i < 8 * CH; ++i) row[(i >> 3) * 64 + (i + lane & 7)] = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < D / 8; ++c) {
+              uint4* at = reinterpret_cast<uint4*>(row + (c >> 3) * CHUNK + (((c & 7) ^ (r & 7)) << 4));
+              if (pair || c / (D / 16) == side) *at = bf16_f16(*at, rs.to);
             }
             fence_proxy_async_smem();
-          }
-        }
-        if (live) {
-          uint32_t sr[4][32], none = 0;  // bit c: no row of the warp sees any of the c-th 32 keys
-          constexpr int G = KV8 ? 8 : 4;  // loads, each with its maximum
-          float mq[G], mul[KV8 ? 8 : 1];  // what scores of each load's keys are multiplied by
-          float v_mul[KV8 ? 8 : 1], v_log[KV8 ? 8 : 1];
-          if constexpr (KV8) {
-            // (the scales are asked for here, in whole vectors: read where they are used, each was
-            // waited for, 1000 cycles a tile)
-            load_8(sc, mul), load_8(sc + 16, v_log), load_8(sc + 8, v_mul);
-#pragma unroll
-            for (int g = 0; g < 8; ++g) tmem_ld16_max(tS + 16 * g, &sr[g >> 1][16 * (g & 1)], mq[g]);
-#pragma unroll
-            for (int g = 0; g < 8; ++g) mul[g] *= sl2;
-            if (!inside) {  // (who sees values whose scale is no number has a NaN by `poison`)
-#pragma unroll
-              for (int g = 0; g < 8; ++g) v_mul[g] = v_mul[g] == v_mul[g] ? v_mul[g] : 0.f;
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(BAR(Q_READY + slot));
+              if (pair) mbar_arrive(BAR(Q_READY + slot));
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32 * c, sr[c], mq[c]);
-            mul[0] = sl2;
+            qt += pair ? 2 : 1;
           }
-          tmem_ld_wait();
-          if (!inside) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int a = min(max(key_lo - j0 - 32 * c, 0), 32), z = min(max(key_hi - j0 - 32 * c, 0), 32);
-              const uint32_t sees = z > a ? (0xffffffffu >> (32 - (z - a))) << a : 0u;
-              if (__any_sync(0xffffffffu, ~sees)) {
-                none |= __any_sync(0xffffffffu, sees) ? 0u : 1u << c;
-#pragma unroll
-                for (int h = 0; h < G / 4; ++h) {
-                  float m = -INFINITY;
-#pragma unroll
-                  for (int i = h * (128 / G); i < (h + 1) * (128 / G); i += 2) {
-                    // (times its scale first: -inf times 0 is no number)
-                    if constexpr (KV8) {
-                      sr[c][i] = __float_as_uint(__uint_as_float(sr[c][i]) * mul[2 * c + h]);
-                      sr[c][i + 1] = __float_as_uint(__uint_as_float(sr[c][i + 1]) * mul[2 * c + h]);
-                    }
-                    if (!(sees >> i & 1)) sr[c][i] = 0xff800000u;
-                    if (!(sees >> (i + 1) & 1)) sr[c][i + 1] = 0xff800000u;
-                    m = max3f(m, __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
+          float m_ref = -INFINITY, l = 0.f;
+          bool poison = false;
+          const int x_step = pair ? 1 : 2, x_first = pair ? 0 : side;
+          for (int x = x_first; x < tiles; x += x_step, ++phase) {
+            const int j0 = s.beg + (s.t0 + x) * kSharedTile;
+            ok = mbar_wait(BAR(S_FULL + t), phase & 1, w, 83);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float* sc = s_scale + (it0 + x) % (SCALES + !SCALES) * 24;
+            const bool inside = j0 >= s.all_lo && j0 + kSharedTile <= s.all_hi;  // every row sees every key
+            if (!inside) {
+              // Some rows do not see some keys of the tile, and 0 times a NaN or an infinity
+              // is not 0.  What no row sees (it may be anything) counts as zero; a value row
+              // that some see, and that holds one, counts as zero too, and its rows get a NaN.
+              const int uv = v_place(it0 + x), vslot = uv % NS;
+              ok = mbar_wait(BAR(KV_FULL + vslot), uv / NS & 1, w, 84);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              const int key = j0 + r;
+              const bool out = key < s.lo || key >= s.end;
+              uint4* row = reinterpret_cast<uint4*>(sb + L::kKVOff + vslot * TILE + (r >> 3) * CH * 1024 + (r & 7) * 128);
+              // (a value scale that is no number makes all its page's values such)
+              bool odd = KV8 && !out && !(fabsf(sc[8 + (r >> 4)]) < INFINITY);
+              if (KV8 || max(j0, s.lo) < s.all_lo || min(j0 + kSharedTile, s.end) > s.all_hi) {
+                if (!out && (key < s.all_lo || key >= s.all_hi)) {
+                  uint32_t bad = 0;
+#pragma unroll 1
+                  for (int i = 0; i < 8 * CH; ++i) {
+                    const uint4 v = row[(i >> 3) * 64 + (i + lane & 7)];  // (other banks for each lane)
+                    constexpr uint32_t E = KV8 ? 0x7c007c00u : 0x7f807f80u;
+                    bad |= __vcmpeq2(v.x & E, E) | __vcmpeq2(v.y & E, E) | __vcmpeq2(v.z & E, E) | __vcmpeq2(v.w & E, E);
                   }
-                  mq[c * (G / 4) + h] = m;
-                  if constexpr (KV8) mul[2 * c + h] = 1.f;
+                  odd |= bad != 0;
+                }
+                const uint32_t votes = __ballot_sync(0xffffffffu, odd);
+                uint32_t* slot = s_bad + 8 * t + 4 * (flip++ & 1);
+                if (lane == 0) {
+                  slot[quarter] = votes;
+                  mbar_arrive(pair ? BAR(XB + 2) : BAR(XB + t));
+                }
+                // (pairs: both tiles' warps have read the values before either clears them)
+                ok = pair ? mbar_wait(BAR(XB + 2), xb++ & 1, w, 85) : mbar_wait(BAR(XB + t), xg++ & 1, w, 86);
+                if (!__all_sync(0xffffffffu, ok)) {
+                  ok = false;
+                  break;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int a = min(max(key_lo - j0 - 32 * i, 0), 32), z = min(max(key_hi - j0 - 32 * i, 0), 32);
+                  const uint32_t sees = z > a ? (0xffffffffu >> (32 - (z - a))) << a : 0u;
+                  poison |= (slot[i] & sees) != 0;
                 }
               }
+              if (side == 0 || !pair) {  // (the other tile's product comes behind this one's)
+                if (out || odd) {
+#pragma unroll
+                  for (int i = 0; i < 8 * CH; ++i) row[(i >> 3) * 64 + (i + lane & 7)] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+              }
+            }
+            if (live) {
+              uint32_t sr[4][32], none = 0;  // bit c: no row of the warp sees any of the c-th 32 keys
+              constexpr int G = KV8 ? 8 : 4;  // loads, each with its maximum
+              float mq[G], mul[KV8 ? 8 : 1];  // what scores of each load's keys are multiplied by
+              float v_mul[KV8 ? 8 : 1], v_log[KV8 ? 8 : 1];
+              if constexpr (KV8) {
+                // (the scales are asked for here, in whole vectors: read where they are used, each was
+                // waited for, 1000 cycles a tile)
+                load_8(sc, mul), load_8(sc + 16, v_log), load_8(sc + 8, v_mul);
+#pragma unroll
+                for (int g = 0; g < 8; ++g) tmem_ld16_max(tS + 16 * g, &sr[g >> 1][16 * (g & 1)], mq[g]);
+#pragma unroll
+                for (int g = 0; g < 8; ++g) mul[g] *= sl2;
+                if (!inside) {  // (who sees values whose scale is no number has a NaN by `poison`)
+#pragma unroll
+                  for (int g = 0; g < 8; ++g) v_mul[g] = v_mul[g] == v_mul[g] ? v_mul[g] : 0.f;
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32 * c, sr[c], mq[c]);
+                mul[0] = sl2;
+              }
+              tmem_ld_wait();
+              if (!inside) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const int a = min(max(key_lo - j0 - 32 * c, 0), 32), z = min(max(key_hi - j0 - 32 * c, 0), 32);
+                  const uint32_t sees = z > a ? (0xffffffffu >> (32 - (z - a))) << a : 0u;
+                  if (__any_sync(0xffffffffu, ~sees)) {
+                    none |= __any_sync(0xffffffffu, sees) ? 0u : 1u << c;
+#pragma unroll
+                    for (int h = 0; h < G / 4; ++h) {
+                      float m = -INFINITY;
+#pragma unroll
+                      for (int i = h * (128 / G); i < (h + 1) * (128 / G); i += 2) {
+                        // (times its scale first: -inf times 0 is no number)
+                        if constexpr (KV8) {
+                          sr[c][i] = __float_as_uint(__uint_as_float(sr[c][i]) * mul[2 * c + h]);
+                          sr[c][i + 1] = __float_as_uint(__uint_as_float(sr[c][i + 1]) * mul[2 * c + h]);
+                        }
+                        if (!(sees >> i & 1)) sr[c][i] = 0xff800000u;
+                        if (!(sees >> (i + 1) & 1)) sr[c][i + 1] = 0xff800000u;
+                        m = max3f(m, __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
+                      }
+                      mq[c * (G / 4) + h] = m;
+                      if constexpr (KV8) mul[2 * c + h] = 1.f;
+                    }
+                  }
+                }
+              }
+              float m_new = -INFINITY;
+              if constexpr (KV8) {
+#pragma unroll
+                for (int g = 0; g < 8; g += 2) m_new = max3f(m_new, fmaf(mq[g], mul[g], v_log[g]), fmaf(mq[g + 1], mul[g + 1], v_log[g + 1]));
+                m_new -= kAtRefLog2;
+              } else {
+                m_new = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
+              }
+              float alpha = 1.f;
+              const bool moves = m_new > m_ref + tau;
+              if (moves) {
+                alpha = ex2_sfu(m_ref - m_new);
+                m_ref = m_new;
+              }
+              if (x != x_first && __any_sync(0xffffffffu, moves)) {
+                // rows whose reference moved: O *= alpha (alpha = 1 for the others)
+#pragma unroll 1
+                for (int c = 0; c < D; c += 8) {
+                  uint32_t ov[8];
+                  tmem_ld8(tO + c, ov);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                  tmem_st8(tO + c, ov);
+                }
+              }
+              const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+              const uint64_t nmb2 = f2_pack(-mb, -mb);
+              uint64_t acc[2] = {0ull, 0ull};
+              uint32_t pk[32];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                if (!(none >> c & 1)) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    const int g = KV8 ? 2 * c + (i >> 3) : 0;
+                    float y0, y1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])),
+                                     f2_pack(mul[g], mul[g]), nmb2), y0, y1);
+                    float p0 = ex2_sfu(y0), p1 = ex2_sfu(y1);
+                    acc[i & 1] = f2_add(acc[i & 1], f2_pack(p0, p1));
+                    if constexpr (KV8) {
+                      f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(v_mul[g], v_mul[g])), p0, p1);
+                      pk[16 * (c & 1) + i] = pack_f16x2(p0, p1);
+                    } else {
+                      pk[16 * (c & 1) + i] = pack_bf16x2(p0, p1);
+                    }
+                  }
+                } else {  // keys that no row of the warp sees
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) pk[16 * (c & 1) + i] = 0u;
+                }
+                if (c & 1) {  // 64 keys: their product may begin
+                  tmem_st32(tS + 16 * (c - 1), pk);
+                  tmem_st_wait();
+                  tc_fence_before();
+                  mbar_arrive(BAR(P_FULL + 2 * t + (c >> 1)));
+                }
+              }
+              float s0, s1;
+              f2_unpack(f2_add(acc[0], acc[1]), s0, s1);
+              l = fmaf(l, alpha, s0 + s1);
+            } else {
+              tc_fence_before();
+              mbar_arrive(BAR(P_FULL + 2 * t));
+              mbar_arrive(BAR(P_FULL + 2 * t + 1));
             }
           }
-          float m_new = -INFINITY;
-          if constexpr (KV8) {
+          if (!ok) break;
+          n0 += pair ? 2 * tiles : tiles;
+          it0 += tiles;
+          // ---------------------------------------------------------- results of the run
+          const int h = s.head * p.heads + my_head;
+          const long long place = s.side == 0 ? s.place + (pair ? 0 : side) * rows + (long long)tok * p.Hq + h
+                                              : s.place + side * s.side + r;
+          if (x_first >= tiles) {  // one tile of keys: the other run has none
+            if (valid) p.part_lse[place] = -INFINITY;
+            continue;
+          }
+          ok = mbar_wait(BAR(O_FINAL + t), runs & 1, w, 87);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          ++runs;
+          if (live) {
+            tc_fence_after();
+            const float inv = poison ? __uint_as_float(0x7fffffffu) : 1.f / l;
+            float* dst = p.part_o + place * D;
 #pragma unroll
-            for (int g = 0; g < 8; g += 2) m_new = max3f(m_new, fmaf(mq[g], mul[g], v_log[g]), fmaf(mq[g + 1], mul[g + 1], v_log[g + 1]));
-            m_new -= kAtRefLog2;
-          } else {
-            m_new = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
-          }
-          float alpha = 1.f;
-          const bool moves = m_new > m_ref + tau;
-          if (moves) {
-            alpha = ex2_sfu(m_ref - m_new);
-            m_ref = m_new;
-          }
-          if (x != x_first && __any_sync(0xffffffffu, moves)) {
-            // rows whose reference moved: O *= alpha (alpha = 1 for the others)
-#pragma unroll 1
-            for (int c = 0; c < D; c += 8) {
-              uint32_t ov[8];
-              tmem_ld8(tO + c, ov);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ov[32];
+              tmem_ld32(tO + 32 * c, ov);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-              tmem_st8(tO + c, ov);
-            }
-          }
-          const float mb = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t nmb2 = f2_pack(-mb, -mb);
-          uint64_t acc[2] = {0ull, 0ull};
-          uint32_t pk[32];
+              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * inv);
+              if (valid && l != 0.f) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (!(none >> c & 1)) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int g = KV8 ? 2 * c + (i >> 3) : 0;
-                float y0, y1;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])),
-                                 f2_pack(mul[g], mul[g]), nmb2), y0, y1);
-                float p0 = ex2_sfu(y0), p1 = ex2_sfu(y1);
-                acc[i & 1] = f2_add(acc[i & 1], f2_pack(p0, p1));
-                if constexpr (KV8) {
-                  f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(v_mul[g], v_mul[g])), p0, p1);
-                  pk[16 * (c & 1) + i] = pack_f16x2(p0, p1);
-                } else {
-                  pk[16 * (c & 1) + i] = pack_bf16x2(p0, p1);
-                }
+                for (int i = 0; i < 32; i += 8) st_global_v8(dst + 32 * c + i, ov + i);
               }
-            } else {  // keys that no row of the warp sees
-#pragma unroll
-              for (int i = 0; i < 16; ++i) pk[16 * (c & 1) + i] = 0u;
             }
-            if (c & 1) {  // 64 keys: their product may begin
-              tmem_st32(tS + 16 * (c - 1), pk);
-              tmem_st_wait();
-              tc_fence_before();
-              mbar_arrive(BAR(P_FULL + 2 * t + (c >> 1)));
-            }
+            // l = 0: the row sees none of these keys (a NaN passes through)
+            if (valid) p.part_lse[place] = l == 0.f ? -INFINITY : m_ref + __log2f(l);
+            tc_fence_before();
           }
-          float s0, s1;
-          f2_unpack(f2_add(acc[0], acc[1]), s0, s1);
-          l = fmaf(l, alpha, s0 + s1);
-        } else {
-          tc_fence_before();
-          mbar_arrive(BAR(P_FULL + 2 * t));
-          mbar_arrive(BAR(P_FULL + 2 * t + 1));
+          mbar_arrive(BAR(O_EMPTY + t));
         }
       }
-      if (!ok) break;
-      n0 += pair ? 2 * tiles : tiles;
-      it0 += tiles;
-      // ---------------------------------------------------------- results of the run
-      const int h = s.head * p.heads + my_head;
-      const long long place = s.side == 0 ? s.place + (pair ? 0 : side) * rows + (long long)tok * p.Hq + h
-                                          : s.place + side * s.side + r;
-      if (x_first >= tiles) {  // one tile of keys: the other run has none
-        if (valid) p.part_lse[place] = -INFINITY;
-        continue;
+      __syncwarp();
+      if (many) {
+        fence_proxy_async_smem();
+        __syncthreads();
       }
-      ok = mbar_wait(BAR(O_FINAL + t), runs & 1, w, 87);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
+      if (KV8) {
+        if (many) asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+      } else if (ALL) {
+        if (many) asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+      } else {
+        few_rows();
       }
-      ++runs;
-      if (live) {
-        tc_fence_after();
-        const float inv = poison ? __uint_as_float(0x7fffffffu) : 1.f / l;
-        float* dst = p.part_o + place * D;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          tmem_ld32(tO + 32 * c, ov);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * inv);
-          if (valid && l != 0.f) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) st_global_v8(dst + 32 * c + i, ov + i);
-          }
-        }
-        // l = 0: the row sees none of these keys (a NaN passes through)
-        if (valid) p.part_lse[place] = l == 0.f ? -INFINITY : m_ref + __log2f(l);
-        tc_fence_before();
-      }
-      mbar_arrive(BAR(O_EMPTY + t));
-    }
-  }
-    __syncwarp();
-    if (many) {
-      fence_proxy_async_smem();
-      __syncthreads();
-    }
-    if (KV8) {
-      if (many) asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
-      else asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    } else if (ALL) {
-      if (many) asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
-      else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-    } else {
-      few_rows();
-    }
     }
     if (KV8) few_rows();
   }
@@ -958,16 +958,8 @@ template <int D, int NR, bool KV8>
 static cudaError_t launch_shared_t(const CUtensorMap (&maps)[5], const SharedParams& p, cudaLaunchConfig_t& cfg) {
   auto kern = fa_decode_shared_kernel<D, NR, KV8>;
   constexpr uint32_t smem = SharedLayout<D, KV8>::kBytes;
-  // (once for each of the first 64 devices: 1 us of the host's time a call)
-  static std::atomic<unsigned long long> set{0};
-  int dev = 64;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(set.load(std::memory_order_relaxed) & bit)) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-    set.fetch_or(bit, std::memory_order_relaxed);
-  }
   cfg.gridDim = dim3((unsigned)p.shares);
   cfg.blockDim = dim3(SharedLayout<D, KV8>::kThreads);
   cfg.dynamicSmemBytes = smem;
