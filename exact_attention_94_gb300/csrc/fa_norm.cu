@@ -422,7 +422,7 @@ void set_chunks(NormRopeParams& p, int D) {
   // more heads a thread share its sines and weights, as long as enough threads are left
   const long long one = (long long)p.T * (p.Hq + p.Hkv) * (D / 16);
   const long long heads = (one + kNormFull - 1) / kNormFull;
-  p.heads_per_thread = (int)(heads < kNormHeads ? heads : kNormHeads);
+  p.heads_per_thread = heads < 1 ? 1 : (int)(heads < kNormHeads ? heads : kNormHeads);  // (no tokens: 1, it divides)
   p.q_chunks = (p.Hq + p.heads_per_thread - 1) / p.heads_per_thread;
   p.k_chunks = (p.Hkv + p.heads_per_thread - 1) / p.heads_per_thread;
 }
