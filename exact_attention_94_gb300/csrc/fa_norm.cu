@@ -154,10 +154,11 @@ __device__ __forceinline__ float squares(const float (&x)[16]) {
   f2_unpack(f2_add(a, b), lo, hi);
   return lo + hi;
 }
-// Sums of squares outside these are taken again of x 2^-64 or x 2^64: values beyond
+// Sums of squares outside these are taken again of x 2^-68 or x 2^64: values beyond
 // 2^64 would square to infinity, and those below 2^-50 count where eps is as small.
+// (128 squares of what is below 2^60 add up to less than 2^127.)
 __device__ __forceinline__ float other_scale(float sum, float eps) {
-  if (!(sum < 1e37f)) return 0x1p-64f;
+  if (!(sum < 1e37f)) return 0x1p-68f;
   return sum < 1e-30f && eps < 1e-24f ? 0x1p64f : 1.f;
 }
 
