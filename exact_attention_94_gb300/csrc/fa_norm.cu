@@ -350,13 +350,25 @@ __global__ void __launch_bounds__(kNormThreads) fa_norm_rope_bwd_kernel(const __
         float s, m;
         sums(s, m);
         const float f = other_scale(s, p.eps);
-        if (f != 1.f) {
+        // The products u x may leave fp32 where u n does not (at its lower end too, if eps lets r be beyond 2^14):
+        // then n comes first.
+        const bool far = f != 1.f || !(fabsf(m) < 1e37f) || (fabsf(m) < 1e-30f && p.eps < 1e-8f);
+        if (far) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) x2[i] = f2_mul(x2[i], f2_pack(f, f));
           sums(s, m);
         }
         const float r = rsqrtf(fmaf(s, 1.f / D, p.eps * f * f));
-        m *= r * (1.f / D);  // mean(u n)
+        if (far) {
+          uint64_t c = 0ull;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) c = f2_fma(u2[i], f2_mul(x2[i], f2_pack(r * (1.f / D), r * (1.f / D))), c);
+          float lo, hi;
+          f2_unpack(c, lo, hi);
+          m = head_sum<TPT>(lo + hi, mask);
+        } else {
+          m *= r * (1.f / D);  // mean(u n)
+        }
         const uint64_t r2 = f2_pack(r, r), m2 = f2_pack(-m, -m), rf2 = f2_pack(r * f, r * f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {

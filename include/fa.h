@@ -631,6 +631,8 @@ size_t fa_qk_norm_rope_bwd_workspace_bytes(int T, int Hq, int Hkv, int d);
  * Gradients of fa_qk_norm_rope from those of its outputs.  With g = Rot^T dy
  * and u = w g:
  *     dx = r (u - n mean(u n)),   dw = sum over tokens and heads of g n.
+ * worked out in fp32; where the products u x leave its range, the mean is taken
+ * of u n.
  *   dyq, dyk : gradients of q_out and k_out;  q, k : the call's inputs
  *   dq, dk   : written, bf16; may be dyq / q (dyk / k) with the same stride
  *   dwq, dwk : fp32 [d], written (zeros for T = 0); NULL for an absent side.  The

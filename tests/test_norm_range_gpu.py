@@ -1,5 +1,5 @@
 """fa_qk_norm_rope and its gradient over the whole range of bf16: heads whose
-squares leave fp32.
+squares, and gradients whose products with them, leave fp32.
 
 Tolerances as in test_norm_rope_gpu.py: what is taken at another scale is taken
 at a power of two, which rounds nothing; a root times that scale below 2^-126
@@ -56,3 +56,10 @@ def test_the_largest_values(d):
     x[4, 1, 9] = top
     x[5, 2] = 2.0 ** 127
     both(x, scaled(bf((6, 3, d), 2), 40), d, 1e-6)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("x_log2,dy_log2,eps", [(59, 70, 1e-6), (40, 100, 0.0), (20, 120, 1e-6), (100, 90, 1e-6),
+                                                (-40, -110, 0.0), (-30, -115, 1e-20), (-8, -115, 1e-6), (-100, -20, 0.0)])
+def test_gradients_whose_products_leave_fp32(d, x_log2, dy_log2, eps):
+    both(scaled(bf((6, 3, d), 1), x_log2), scaled(bf((6, 3, d), 2), dy_log2), d, eps)
