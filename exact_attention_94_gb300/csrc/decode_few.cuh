@@ -377,9 +377,10 @@ __device__ __forceinline__ void attend_few(const SharedParams& p, const CUtensor
           for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
           m += lv;
           if (m > m_ref[nr][j] + tau) {
-            const float alpha = ex2_sfu(m_ref[nr][j] - m);
+            const float half = KV8 ? ex2_sfu(0.5f * (m_ref[nr][j] - m)) : 1.f;  // (as for tiles)
+            const float alpha = KV8 ? half * half : ex2_sfu(m_ref[nr][j] - m);
             m_ref[nr][j] = m;
-            l[nr][j] *= alpha;
+            l[nr][j] = KV8 ? l[nr][j] * half * half : l[nr][j] * alpha;
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) o[x][nr][j] *= alpha, o[x][nr][j + 2] *= alpha;
           }

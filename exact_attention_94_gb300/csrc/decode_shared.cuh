@@ -206,7 +206,9 @@ __device__ __forceinline__ long long cut_place(const SharedParams& p, bool few, 
 // 8-bit pages: codes are exact in f16, so K and V tiles become f16, and what they meet:
 //  - a row of queries times a power of two of its own, exact for what is within 2^28 of its largest;
 //  - probabilities times value scales, against a reference per row at which that is kAtRef: rounded by
-//    2^-11 of themselves, or by 2^-32 of the row's largest.  (The row sums share the reference.)
+//    2^-11 of themselves, or by 2^-32 of the row's largest.  The row sums share the reference.  They
+//    are of the probabilities alone, of which none that counts is below 2^-110 or above 2^95 of it;
+//    it may move by more than 2^126 from one page to the next, so they go along in two halves.
 constexpr float kAtRefLog2 = 7.f, kMaxTau = 8.f;
 constexpr float kLeastScale = -80.f;  // log2 of a value scale, from below
 __device__ __forceinline__ float scale_log2(float v) { return v > 0.f && v < INFINITY ? fmaxf(__log2f(v), kLeastScale) : kLeastScale; }
@@ -826,10 +828,11 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
               } else {
                 m_new = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sl2;
               }
-              float alpha = 1.f;
+              float alpha = 1.f, half = 1.f;  // KV8: alpha = half^2
               const bool moves = m_new > m_ref + tau;
               if (moves) {
-                alpha = ex2_sfu(m_ref - m_new);
+                if constexpr (KV8) half = ex2_sfu(0.5f * (m_ref - m_new)), alpha = half * half;
+                else alpha = ex2_sfu(m_ref - m_new);
                 m_ref = m_new;
               }
               if (x != x_first && __any_sync(0xffffffffu, moves)) {
@@ -879,7 +882,8 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
               }
               float s0, s1;
               f2_unpack(f2_add(acc[0], acc[1]), s0, s1);
-              l = fmaf(l, alpha, s0 + s1);
+              // (value scales move the reference by up to 2^160, which half leaves in range; l stays there)
+              l = KV8 ? fmaf(l * half, half, s0 + s1) : fmaf(l, alpha, s0 + s1);
             } else {
               tc_fence_before();
               mbar_arrive(BAR(P_FULL + 2 * t));
