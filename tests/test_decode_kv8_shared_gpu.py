@@ -1,10 +1,11 @@
 """Attention of requests that share prefixes, over pages of 8-bit codes, against
 the reference in 64 bits on the values that the codes stand for.
 
-Tolerances as for bf16 pages: half a bf16 step of O, 2^-8 |o|; a probability
-times its value scale is rounded to bf16 (2^-8 of itself at most), a code is
-exact in bf16; scores are fp32 sums of exact products, times a scale:
-2^-8 |o| + (2^-8 + 2^-11) a, a = sum_j P_j |v_j|; lse 2^-12.
+Tolerances as for bf16 pages: half a bf16 step of O, 2^-8 |o|; scores are fp32
+sums of exact products, times a scale: 2^-11 a, a = sum_j P_j |v_j|; and 2^-8 a,
+what probabilities rounded to bf16 would take, where these are f16: 2^-8 |o| +
+(2^-8 + 2^-11) a; lse 2^-12.  test_decode_kv8_shared_rounding.py has the tolerance
+that f16 leaves.
 """
 import numpy as np
 import pytest
