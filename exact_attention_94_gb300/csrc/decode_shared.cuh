@@ -315,7 +315,7 @@ __global__ void __launch_bounds__((SharedLayout<D, KV8>::kThreads), 1)
   const uint32_t tmem = *tmem_slot;
   const WaitCtx w{abort_flag, p.timeout_ns, p.err};
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is there
-  asm volatile("griddepcontrol.launch_dependents;");  // the merge may be set up from the plan; it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge may be set up; it waits for this grid's end
 
   // the next piece announced, read by every lane of a warp
   auto take = [&](int piece, Piece& s, unsigned site) {

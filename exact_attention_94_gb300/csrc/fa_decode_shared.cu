@@ -189,6 +189,65 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fa_shared_plan_kernel(const _
 
 // ---------------------------------------------------------------- merge
 
+// What the merge reads of the plan: EARLY, while its writes need not be visible yet, past L1; else through it, for all
+// warps of an SM read the same (past it 4096 rows took 8 us more).
+template <bool EARLY, class T>
+__device__ __forceinline__ T seen(const T* at) {
+  if constexpr (sizeof(T) == 16) {
+    longlong2 x;
+    if constexpr (EARLY) asm volatile("ld.relaxed.gpu.global.v2.s64 {%0, %1}, [%2];" : "=l"(x.x), "=l"(x.y) : "l"(at) : "memory");
+    else asm volatile("ld.global.v2.s64 {%0, %1}, [%2];" : "=l"(x.x), "=l"(x.y) : "l"(at) : "memory");
+    return x;
+  } else if constexpr (sizeof(T) == 8) {
+    long long x;
+    if constexpr (EARLY) asm volatile("ld.relaxed.gpu.global.s64 %0, [%1];" : "=l"(x) : "l"(at) : "memory");
+    else asm volatile("ld.global.s64 %0, [%1];" : "=l"(x) : "l"(at) : "memory");
+    return x;
+  } else {
+    int x;
+    if constexpr (EARLY) asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(at) : "memory");
+    else asm volatile("ld.global.s32 %0, [%1];" : "=r"(x) : "l"(at) : "memory");
+    return x;
+  }
+}
+struct SeenPlan {
+  int entry[2];                   // of_request
+  int tok0[2], ntok[2], tiles[2];
+  long long cum[2];
+  longlong2 head[2];              // totals, shares of the first two lists
+  int last;                       // shares of the third
+  // What is at the places `of` of the lists, and the head.
+  template <bool EARLY>
+  __device__ __forceinline__ void read(const SharedParams& p, const int (&of)[2]) {
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      tok0[kind] = ntok[kind] = tiles[kind] = 0, cum[kind] = 0;
+      if (of[kind] < 0) continue;
+      const SharedList& list = p.plan.list[of[kind] & 1];
+      const int i = min(of[kind] >> 1, p.G + p.B - 1);  // (an entry there is, whatever has been read)
+      const SharedEntry* e = list.entry + i;
+      tok0[kind] = seen<EARLY>(&e->tok0), ntok[kind] = seen<EARLY>(&e->ntok), tiles[kind] = seen<EARLY>(&e->tiles);
+      cum[kind] = seen<EARLY>(list.cum + i);
+    }
+    const longlong2* h = reinterpret_cast<const longlong2*>(p.plan.head);
+    head[0] = seen<EARLY>(h), head[1] = seen<EARLY>(h + 1), last = seen<EARLY>(&p.plan.head->shares[2]);
+  }
+  template <bool EARLY>
+  __device__ __forceinline__ void read_entries(const SharedParams& p, int b) {
+    const long long x = seen<EARLY>(reinterpret_cast<const long long*>(p.plan.of_request + b));
+    entry[0] = (int)x, entry[1] = (int)(x >> 32);
+  }
+  __device__ __forceinline__ bool operator==(const SeenPlan& o) const {
+    bool same = head[0].x == o.head[0].x && head[0].y == o.head[0].y && head[1].x == o.head[1].x && head[1].y == o.head[1].y &&
+                last == o.last;
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind)
+      same = same && entry[kind] == o.entry[kind] && tok0[kind] == o.tok0[kind] && ntok[kind] == o.ntok[kind] &&
+             tiles[kind] == o.tiles[kind] && cum[kind] == o.cum[kind];
+    return same;
+  }
+};
+
 // A warp for R query rows of a token and K/V head, one where all are on the GPU at once: the
 // results of the group's shared keys and of the request's own.  Lane i looks at part i; a
 // part without mass has lse = -inf, and its O is not read.
@@ -202,42 +261,49 @@ __global__ void __launch_bounds__(256, R == 1 ? 4 : 2) fa_decode_shared_merge_ke
   const int h0 = (int)(x - of_four * fours) * R, tok = (int)div_ll(of_four, p.Hkv), head = (int)(of_four - (long long)tok * p.Hkv);
   const int b = tok / p.Nq, nr = min(R, p.heads - h0);
   const long long row = (long long)tok * p.Hq + head * p.heads + h0;
-  // (the plan, which the main kernel's CTAs have all waited for; read past L1)
-  const int2 entries = __ldcg(p.plan.of_request + b);
   // parts of each kind: n of them, `runs` in each of the shares from `first` on
-  int n[2] = {0, 0}, runs[2] = {1, 1}, first[2] = {0, 0};
-  long long base[2] = {0, 0}, begin[2] = {0, 0};  // place of the first part, or of the row in a slot; the unit's begin
-  bool cut[2] = {false, false}, few[2] = {false, false};
-  SharedHead totals;
-  const longlong2 t0 = __ldcg(reinterpret_cast<const longlong2*>(p.plan.head)),
-                  t1 = __ldcg(reinterpret_cast<const longlong2*>(p.plan.head) + 1);
-  totals.total[0] = t0.x, totals.total[1] = t0.y, totals.total[2] = t1.x;
-  totals.shares[0] = (int)t1.y, totals.shares[1] = (int)(t1.y >> 32), totals.shares[2] = __ldcg(&p.plan.head->shares[2]);
-  const Deal deals[2] = {deal_of(totals, false), deal_of(totals, true)};
+  int n[2], runs[2], first[2];
+  long long base[2], begin[2];  // place of the first part, or of the row in a slot; the unit's begin
+  bool cut[2], few[2];
+  Deal deals[2] = {{{0, 0}, {0, 0}}, {{0, 0}, {0, 0}}};
+  // The plan's writes are sure to be visible behind the wait alone, but until then the main kernel works: they are
+  // read and worked on before it, and read behind it once more, all at once, to compare.  (1 us of a call; 4 to 8
+  // where all of this begins behind the wait.)
+  SeenPlan plan;
+  for (bool early = true;; early = false) {
+    plan.read_entries<true>(p, b);
+    plan.read<true>(p, plan.entry);
+    SharedHead totals;
+    totals.total[0] = plan.head[0].x, totals.total[1] = plan.head[0].y, totals.total[2] = plan.head[1].x;
+    totals.shares[0] = (int)plan.head[1].y, totals.shares[1] = (int)(plan.head[1].y >> 32), totals.shares[2] = plan.last;
+    deals[0] = deal_of(totals, false), deals[1] = deal_of(totals, true);
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    const int of = kind == 0 ? entries.x : entries.y;
-    if (of < 0) continue;
-    few[kind] = of & 1;
-    const SharedList& list = p.plan.list[of & 1];
-    const Deal& deal = (of & 1) ? deals[1] : deals[0];
-    const SharedEntry* at = list.entry + (of >> 1);
-    const int tok0 = __ldcg(&at->tok0), ntok = __ldcg(&at->ntok), tiles = __ldcg(&at->tiles);
-    const long long cum = __ldcg(list.cum + (of >> 1));
-    const Weight wt = weight_of(p, few[kind], ntok);
-    const int weight = wt.lead + wt.tile * tiles, chunks = chunks_of(p, few[kind], ntok);
-    const int c = few[kind] ? 0 : (tok - tok0) / (2 * p.tile_tokens), in = tok - tok0 - c * 2 * p.tile_tokens;
-    const bool pair = few[kind] || ntok - c * 2 * p.tile_tokens > p.tile_tokens;
-    begin[kind] = cum + (long long)weight * ((long long)head * chunks + c);
-    first[kind] = deal.of(begin[kind] + wt.lead);
-    const int last = deal.of(begin[kind] + weight - wt.tile);  // where the last tile begins
-    cut[kind] = first[kind] != last;
-    runs[kind] = pair ? 1 : 2;
-    n[kind] = (last - first[kind] + 1) * runs[kind];
-    const int side = few[kind] ? 0 : in / p.tile_tokens;
-    base[kind] = cut[kind] ? side * kSharedTile + (in - side * p.tile_tokens) * p.heads + h0 : 2 * kind * rows + row;
+    for (int kind = 0; kind < 2; ++kind) {
+      n[kind] = 0, runs[kind] = 1, first[kind] = 0, base[kind] = begin[kind] = 0, cut[kind] = few[kind] = false;
+      const int of = plan.entry[kind];
+      if (of < 0) continue;
+      few[kind] = of & 1;
+      const Deal& deal = (of & 1) ? deals[1] : deals[0];
+      const Weight wt = weight_of(p, few[kind], plan.ntok[kind]);
+      const int weight = wt.lead + wt.tile * plan.tiles[kind], chunks = chunks_of(p, few[kind], plan.ntok[kind]);
+      const int c = few[kind] ? 0 : (tok - plan.tok0[kind]) / (2 * p.tile_tokens), in = tok - plan.tok0[kind] - c * 2 * p.tile_tokens;
+      const bool pair = few[kind] || plan.ntok[kind] - c * 2 * p.tile_tokens > p.tile_tokens;
+      begin[kind] = plan.cum[kind] + (long long)weight * ((long long)head * chunks + c);
+      first[kind] = deal.of(begin[kind] + wt.lead);
+      const int last = deal.of(begin[kind] + weight - wt.tile);  // where the last tile begins
+      cut[kind] = first[kind] != last;
+      runs[kind] = pair ? 1 : 2;
+      n[kind] = (last - first[kind] + 1) * runs[kind];
+      const int side = few[kind] ? 0 : in / p.tile_tokens;
+      base[kind] = cut[kind] ? side * kSharedTile + (in - side * p.tile_tokens) * p.heads + h0 : 2 * kind * rows + row;
+    }
+    if (!early) break;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done, and the plan before it
+    SeenPlan now;
+    now.read_entries<false>(p, b);
+    now.read<false>(p, plan.entry);
+    if (__all_sync(0xffffffffu, now == plan)) break;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's grid is done
   float acc[R][E], mass[R], m[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
