@@ -973,7 +973,9 @@ template <int D, bool KV8>
 static cudaError_t launch_shared_main(const CUtensorMap (&maps)[5], const SharedParams& p, cudaLaunchConfig_t& cfg) {
   switch (p.few) {
     case 8: return launch_shared_t<D, 1, KV8>(maps, p, cfg);
-    case 16: return launch_shared_t<D, 2, KV8>(maps, p, cfg);
+    case 16:
+      if constexpr (!(KV8 && D == 128)) return launch_shared_t<D, 2, KV8>(maps, p, cfg);
+      else return cudaErrorInvalidValue;  // (shared_few gives these to tiles)
     default: return launch_shared_t<D, 0, KV8>(maps, p, cfg);
   }
 }
