@@ -948,7 +948,7 @@ def _norm_side(name, plan, dev, w, tensors, out):
     H, d = size[-2], size[-1]
     if d != plan.d:
         raise ValueError(f"{name} has head dim {d}, the plan {plan.d}")
-    strides += [_check_rows(f"d{name}", t, dev, size) for t in tensors[1:]]
+    strides += [_check_rows(f"dy{name}", t, dev, size) for t in tensors[1:]]
     wide = isinstance(w, torch.Tensor) and w.dtype is torch.float32
     _check(f"w{name}", w, torch.float32 if wide else torch.bfloat16, dev, (d,))
     if out is None:
