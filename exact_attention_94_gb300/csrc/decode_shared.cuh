@@ -41,16 +41,18 @@
 // box fills whole eights of keys.
 //
 // Measured, 64 heads over 8, d = 128, replayed graphs (bf16 pages / 8-bit):
-//   64 requests, 16385 shared, 100 to 2000 own            85 / 101 us
-//   256 requests, 32768 shared, 1 to 512 own              257 / 390 us
-//   256 requests, 32768 shared, one own                   226 / 312 us, 1.2 / 0.88 PFLOP/s
-//   32 requests, 131072 shared (256 rows)                 138 / 170 us
-//   64 requests, 8192 own                                 350 us, 6.1 TB/s / 271 us, 4.0 TB/s
-//   4 requests, 777 shared, 32 heads over 8               19 / 21 us
+//   64 requests, 16385 shared, 100 to 2000 own            85 / 104 us
+//   256 requests, 32768 shared, 1 to 512 own              257 / 393 us
+//   256 requests, 32768 shared, one own                   226 / 318 us, 1.2 / 0.86 PFLOP/s
+//   32 requests, 131072 shared (256 rows)                 140 / 172 us
+//   64 requests, 8192 own                                 354 us, 6.1 TB/s / 272 us, 4.0 TB/s
+//   4 requests, 777 shared, 32 heads over 8               20 / 22 us
+// (at 2070 MHz; over bf16 pages the power cap holds 256 requests at 1980 to 2040).
 // bf16 tiles are bound by the products (1570 cycles a job of two 128 x 128 x 128 products
-// that take 1280).  8-bit ones are bound by the softmax warps, with which the
+// that take 1280: 171 us of 226 for 216 jobs an SM; start and merge are some 25 more, and
+// 30 are not accounted for).  8-bit ones are bound by the softmax warps, with which the
 // converting ones share issue slots and registers: 2400 cycles a job.  The smallest
-// calls are the three kernels' latencies one after the other: plan 5 us, main 11, merge 3.
+// calls are the three kernels' latencies one after the other: plan 5 us, main 11, merge 4.
 #pragma once
 
 #include "sampling.cuh"

@@ -421,9 +421,10 @@ static size_t plan_layout(SharedPlan* plan, void* at, int B, int G) {
   return off;
 }
 // The most rows of an entry that a warp attends for, if a request's own keys meet no more;
-// 0: tiles for all.  (64 requests of 4096 tokens, 64 heads over 8, d = 128: 16 rows 223 us by
+// 0: tiles for all.  (64 requests of 4096 tokens, 64 heads over 8, d = 128: 16 rows 224 us by
 // warps and 193 by tiles, but 4 drafts of 4 heads behind shared prompts 38 and 41; 32 rows 367
-// and 198.  8-bit pages, whose conversions take registers: 16 rows 386 and 255, of d = 64 98 and 146.)
+// and 197.  8-bit pages, whose conversions take registers: 16 rows 386 and 267, of d = 64 98 and 146.
+// Rows alone decide: where 16 rows of bf16 meet long own keys, tiles would be the better choice.)
 int shared_few(int Nq, int heads, int D, bool kv8) {
   const int rows = Nq * heads;
   return rows <= 8 ? 8 : rows <= 16 && !(kv8 && D == 128) ? 16 : 0;
