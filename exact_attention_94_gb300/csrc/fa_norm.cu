@@ -463,7 +463,7 @@ cudaError_t launch_norm_rope(NormRopeParams& p, int D, bool neighbours, cudaStre
 
 // Blocks in proportion to the heads of each side, one at least for a side that has heads, no more than there is work for.
 int norm_rope_bwd_blocks(int T, int Hq, int Hkv, int D, int* q_blocks) {
-  constexpr int kMost = kSms * 6;
+  constexpr int kMost = kSms * 6;  // twice what stands on the SMs at once (three blocks of 148 registers a thread each)
   const int heads = kNormThreads / (D / 16);
   auto most = [&](int H) { return ((long long)T * H + heads - 1) / heads; };
   long long nq = Hq > 0 ? (long long)kMost * Hq / (Hq + Hkv) : 0;
